@@ -52,10 +52,11 @@
 extern "C" {
 #endif
 
-/* Logit element types. */
+/* Element types. SV_E4M3 is a type of the key/value cache only. */
 enum {
   SV_BF16 = 0, /* bfloat16 */
-  SV_F32 = 1   /* IEEE fp32 */
+  SV_F32 = 1,  /* IEEE fp32 */
+  SV_E4M3 = 2  /* 8-bit float, 4 exponent and 3 mantissa bits, largest value 448 */
 };
 
 /* Host-side return codes (no work is enqueued when one of these is returned). */
@@ -82,7 +83,11 @@ enum {
   SV_DEV_NONFINITE = 32,     /* a logit row holds NaN or +inf */
   SV_DEV_EMPTY_ROW = 64,     /* a logit row is entirely -inf */
   SV_DEV_UNIFORM_RANGE = 128,/* a uniform is NaN or outside [0, 1] */
-  SV_DEV_TIMEOUT = 256       /* a bounded wait in the fused kernel ran out (results invalid) */
+  SV_DEV_TIMEOUT = 256,      /* a bounded wait in a kernel ran out (results invalid) */
+  SV_DEV_SLOT_RANGE = 512,   /* a cache slot outside the cache, other than -1 */
+  SV_DEV_PAGE_RANGE = 1024,  /* a needed page outside the cache, or a context outside its page table */
+  SV_DEV_TREE = 2048         /* a malformed tree: a parent that is not an earlier node, or a node
+                                with children whose draft row lies outside the draft logits */
 };
 
 /* Bytes of device workspace spec_verify needs for this problem size; 0 for an
@@ -401,6 +406,145 @@ size_t sv_lmhead_workspace_size(int N, int D, int V);
 int sv_lmhead_stats(const void* hidden, const void* weight, const int32_t* tokens, int N, int D,
                     int V, float temperature, double* row_max, double* lse, float* at,
                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------- a tree of drafted tokens
+ *
+ * One step of decoding with a tree of drafted tokens: queries and keys are
+ * normalised and rotated (sv_qk_norm_rope), keys and values go into the paged
+ * cache (sv_cache_write), the tree attends the cache (sv_tree_attention), and
+ * the scored tree is verified (spec_verify_tree). The keys and values of the
+ * accepted nodes then go to consecutive positions with a second sv_cache_write,
+ * in which the rejected nodes' slots are -1.
+ *
+ * A tree of T nodes (1 <= T <= 128) is an array of T parents: parents[i] is an
+ * earlier node (0 <= parents[i] < i), -1 for a node under the context, or -2 for
+ * padding, which is no node; a padding node has no children.
+ *
+ * Norms per head and rotation by position, in one pass. For every row x of D
+ * values (a head of a token): y = x / sqrt(mean(x^2) + eps) * weight, then the
+ * first R values rotate in pairs, (i, i + R/2), or (2i, 2i + 1) when interleaved,
+ * by the angle positions[n] * inv_freq[i]:
+ *   (y0, y1) -> (y0 cos - y1 sin, y1 cos + y0 sin).
+ *   q, k          device, [N, Hq, D] and [N, Hkv, D], dtype, values of a row
+ *                 consecutive, token and head strides in elements; Hq or Hkv may
+ *                 be 0 (its pointers may then be NULL), not both
+ *   q_weight, k_weight  device, [D] dtype, or NULL for ones
+ *   inv_freq      device, [R/2] fp32
+ *   positions     device, [N] int32
+ *   D, R          1 <= D <= 1024, 0 <= R <= D, R even
+ *   q_out, k_out  device, written; strides as above; may be q and k themselves
+ *                 (same pointer and strides), must not overlap them otherwise
+ * Computed in fp32 (the angle's reduction to a fraction of a turn in 64-bit
+ * integers, so that far positions lose nothing) and rounded once. 16-byte
+ * aligned rows with D and R multiples of 16 (fp32: 8), D <= 512 (fp32: 256),
+ * take the vector path. No workspace. Returns SV_OK once enqueued; N == 0 returns SV_OK at once. */
+int sv_qk_norm_rope(const void* q, int64_t q_stride_n, int64_t q_stride_h, const void* k,
+                    int64_t k_stride_n, int64_t k_stride_h, const void* q_weight,
+                    const void* k_weight, const float* inv_freq, const int32_t* positions, int N,
+                    int Hq, int Hkv, int D, int R, int dtype, float eps, int interleaved, void* q_out,
+                    int64_t qo_stride_n, int64_t qo_stride_h, void* k_out, int64_t ko_stride_n,
+                    int64_t ko_stride_h, void* stream);
+
+/* The paged cache: k_cache and v_cache are [num_pages, Hkv, page_size, D] of
+ * cache_dtype (SV_BF16 or SV_E4M3); with SV_E4M3, k_scale and v_scale are
+ * [num_pages, Hkv, page_size] fp32 (else NULL). The token in slot s lies in page
+ * s / page_size at offset s % page_size.
+ *
+ * Writes N tokens' keys and values into their slots:
+ *   k, v     device, [N, Hkv, D], dtype (SV_BF16 or SV_F32), strides in elements
+ *   slots    device, [N] int64; -1 writes nothing. No slot may occur twice.
+ *   status   device word, may be NULL: SV_DEV_SLOT_RANGE is OR-ed into it when a
+ *            slot lies outside the cache (that token is not written). The
+ *            call does not clear it.
+ * SV_BF16 rounds to nearest even. SV_E4M3 stores a row of D values as
+ * code = e4m3(x * (448 / a)) with the scale a / 448, a = max(max |x|, 1e-30), both
+ * quotients rounded to fp32 and the code to nearest even; a row that holds NaN
+ * or infinity gets a NaN scale and codes of 0, so that it reads back as NaN.
+ * 1 <= D <= 1024. Returns SV_OK once enqueued; N == 0 returns SV_OK at once. */
+int sv_cache_write(const void* k, int64_t k_stride_n, int64_t k_stride_h, const void* v,
+                   int64_t v_stride_n, int64_t v_stride_h, const int64_t* slots, int N, int Hkv,
+                   int D, int dtype, void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                   int64_t num_pages, int page_size, int cache_dtype, uint32_t* status, void* stream);
+
+/* Reads N tokens back: k_out and v_out (device, [N, Hkv, D], dtype, strides in
+ * elements) get the stored values, code * scale rounded once. A slot of -1
+ * gives zeros; any other slot outside the cache does too, and sets
+ * SV_DEV_SLOT_RANGE in `status` as above. */
+int sv_cache_read(const void* k_cache, const void* v_cache, const float* k_scale,
+                  const float* v_scale, int64_t num_pages, int page_size, int cache_dtype,
+                  const int64_t* slots, int N, int Hkv, int D, int dtype, void* k_out,
+                  int64_t ko_stride_n, int64_t ko_stride_h, void* v_out, int64_t vo_stride_n,
+                  int64_t vo_stride_h, uint32_t* status, void* stream);
+
+/* Bytes of device workspace sv_tree_attention needs; 0 for invalid sizes.
+ * Pure host function. */
+size_t sv_tree_attention_workspace_size(int B, int T, int Hq, int Hkv, int D, int max_pages,
+                                        int page_size);
+
+/* Attention of B trees of T nodes over the paged cache. Sequence b has
+ * ctx_lens[b] context tokens at positions 0 .. ctx_lens[b] - 1, and node i's key
+ * and value lie at position ctx_lens[b] + i; position t is in page
+ * page_table[b, t / page_size]. Node i attends the context, its ancestors and
+ * itself: out = softmax(scale q k) v over those, query head h with key/value head
+ * h / (Hq / Hkv).
+ *   q           device, [B, T, Hq, D] bf16, strides in elements
+ *   k_cache, v_cache, k_scale, v_scale, num_pages, page_size, cache_dtype  the cache
+ *   page_table  device, [B, max_pages] int32; entries past a sequence's last node
+ *               are not read
+ *   ctx_lens    device, [B] int32, 0 or more
+ *   parents     device, [B, T] int32, or NULL for chains (node i's parent is i - 1)
+ *   out         device, [B, T, Hq, D] bf16, contiguous (written); 0 for padding
+ *   workspace   device, sv_tree_attention_workspace_size() bytes, 256-byte aligned;
+ *               its first 4 bytes are the device status word
+ * T = 1 is the ordinary decoding step. Sums, maxima and the running output are
+ * fp32; the weights are rounded to bf16 for their product with the values. A
+ * sequence with a malformed tree (SV_DEV_TREE), or whose context or
+ * needed pages lie outside the table or the cache (SV_DEV_PAGE_RANGE), gets NaN
+ * outputs; the others are unaffected. What masked positions hold, NaN included,
+ * does not matter. D a multiple of 16 up to 256, page sizes of 16, 32, 64 or 128 and
+ * 16-byte aligned rows take the tensor-core kernel, other shapes (D up to
+ * 1024) a plain one. Returns SV_OK once enqueued; B == 0 returns SV_OK at once. */
+int sv_tree_attention(const void* q, int64_t q_stride_b, int64_t q_stride_t, int64_t q_stride_h,
+                      const void* k_cache, const void* v_cache, const float* k_scale,
+                      const float* v_scale, int64_t num_pages, int page_size, int cache_dtype,
+                      const int32_t* page_table, const int32_t* ctx_lens, const int32_t* parents,
+                      int B, int T, int Hq, int Hkv, int D, int max_pages, float scale, void* out,
+                      void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of device workspace spec_verify_tree needs; 0 for invalid sizes (B < 0,
+ * T outside [1, 128], V outside [1, 2^30]). Pure host function. */
+size_t sv_tree_workspace_size(int B, int T, int V, int dtype);
+
+/* Verification of B trees of T nodes: the modified rejection sampling of the
+ * card's §4.2 with several candidates at a node. Node 0 is the root, the last
+ * emitted token (parents[b, 0] is -1; every other node has a parent or is padding).
+ * At the current node, the root at first, with q its target row's and p its
+ * draft row's softmax(l / T), the children are tried in index order against the residual
+ * r, q at first: child c of token x is accepted while u < min(1, r(x)/p(x)), and
+ * becomes the current node; a rejection turns r into max(0, r - p) over its sum (a
+ * sum below 2^-40, which is r = p but for rounding, leaves r). When no child is left, one token is drawn
+ * from r. With each node's children drawn independently from p, the emitted
+ * tokens follow the target's distribution. A chain gives spec_verify's results.
+ *   target_logits  device, [B, T, V] dtype: row i is the target's at node i
+ *   draft_logits   device, [R, V] dtype: the draft's rows
+ *   draft_index    device, [B, T] int32: node i's row of draft_logits; read for
+ *                  nodes with children only
+ *   tokens         device, [B, T] int32: the nodes' tokens (the root's is not read)
+ *   parents        device, [B, T] int32
+ *   uniforms       device, [B, T] fp32: node i's test; the root's is the draw's
+ *   out_tokens     device, [B, T] int32 (written): accepted tokens, the drawn
+ *                  token, then -1
+ *   out_nodes      device, [B, T] int32 (written): accepted nodes, then -1
+ *   n_accepted     device, [B] int32 (written)
+ * Rows of nodes that are not visited are not read. A sequence fails (all -1,
+ * status bit) on a malformed tree, a token outside [0, V) or a uniform outside
+ * [0, 1] of any node, and on NaN, +inf or an empty row among the visited
+ * rows. Conventions and workspace as for spec_verify. */
+int spec_verify_tree(const void* target_logits, const void* draft_logits, const int32_t* draft_index,
+                     const int32_t* tokens, const int32_t* parents, const float* uniforms, int B, int T,
+                     int V, int R, int dtype, float temperature, int32_t* out_tokens,
+                     int32_t* out_nodes, int32_t* n_accepted, void* workspace, size_t workspace_bytes,
+                     void* stream);
 
 #ifdef __cplusplus
 }

@@ -30,14 +30,18 @@ __all__ = [
     "sv_greedy_workspace_size", "spec_verify_greedy", "verify_greedy", "sv_force_path",
     "sv_test_withhold_plans", "sv_topk_workspace_size", "spec_verify_topk", "verify_topk",
     "sv_topp_workspace_size", "spec_verify_topp", "verify_topp", "spec_verify_host_async",
-    "sv_lmhead_workspace_size", "sv_lmhead_stats", "lmhead_stats", "EXPORTED_SYMBOLS",
+    "sv_lmhead_workspace_size", "sv_lmhead_stats", "lmhead_stats",
+    "SV_E4M3", "PagedCache", "new_cache", "sv_qk_norm_rope", "qk_norm_rope", "sv_cache_write", "cache_write",
+    "sv_cache_read", "cache_read", "sv_tree_attention_workspace_size", "sv_tree_attention",
+    "tree_attention", "sv_tree_workspace_size", "spec_verify_tree", "verify_tree", "EXPORTED_SYMBOLS",
 ]
 
 SV_BF16 = 0
 SV_F32 = 1
+SV_E4M3 = 2
 SV_OK = 0
 DEVICE_BITS = {16: "token_range", 32: "nonfinite", 64: "empty_row", 128: "uniform_range",
-               256: "timeout"}
+               256: "timeout", 512: "slot_range", 1024: "page_range", 2048: "tree"}
 
 EXPORTED_SYMBOLS = (
     "sv_workspace_size", "spec_verify", "spec_verify_debug", "spec_verify_profiled",
@@ -47,7 +51,9 @@ EXPORTED_SYMBOLS = (
     "sv_greedy_workspace_size", "spec_verify_greedy", "sv_force_path", "sv_test_withhold_plans",
     "sv_topk_workspace_size", "spec_verify_topk", "sv_topp_workspace_size", "spec_verify_topp",
     "spec_verify_host_async", "sv_lmhead_workspace_size", "sv_lmhead_stats",
-    "sv_topp_kernels_per_call",
+    "sv_topp_kernels_per_call", "sv_qk_norm_rope", "sv_cache_write", "sv_cache_read",
+    "sv_tree_attention_workspace_size", "sv_tree_attention", "sv_tree_workspace_size",
+    "spec_verify_tree",
 )
 
 _lib = None
@@ -122,6 +128,26 @@ def load_library(path: str | None = None, build: bool = False) -> ctypes.CDLL:
     lib.sv_lmhead_workspace_size.restype = sz
     lib.sv_lmhead_stats.argtypes = [vp, vp, vp, i32, i32, i32, f32, dp, dp, vp, vp, sz, vp]
     lib.sv_lmhead_stats.restype = i32
+    i64 = ctypes.c_int64
+    lib.sv_qk_norm_rope.argtypes = [vp, i64, i64, vp, i64, i64, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32,
+                                    f32, i32, vp, i64, i64, vp, i64, i64, vp]
+    lib.sv_qk_norm_rope.restype = i32
+    lib.sv_cache_write.argtypes = [vp, i64, i64, vp, i64, i64, vp, i32, i32, i32, i32, vp, vp, vp, vp, i64,
+                                   i32, i32, vp, vp]
+    lib.sv_cache_write.restype = i32
+    lib.sv_cache_read.argtypes = [vp, vp, vp, vp, i64, i32, i32, vp, i32, i32, i32, i32, vp, i64, i64, vp,
+                                  i64, i64, vp, vp]
+    lib.sv_cache_read.restype = i32
+    lib.sv_tree_attention_workspace_size.argtypes = [i32] * 7
+    lib.sv_tree_attention_workspace_size.restype = sz
+    lib.sv_tree_attention.argtypes = [vp, i64, i64, i64, vp, vp, vp, vp, i64, i32, i32, vp, vp, vp, i32, i32,
+                                      i32, i32, i32, i32, f32, vp, vp, sz, vp]
+    lib.sv_tree_attention.restype = i32
+    lib.sv_tree_workspace_size.argtypes = [i32, i32, i32, i32]
+    lib.sv_tree_workspace_size.restype = sz
+    lib.spec_verify_tree.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, f32, vp, vp, vp, vp, sz,
+                                     vp]
+    lib.spec_verify_tree.restype = i32
     if path is None:
         _lib = lib
     return lib
@@ -526,3 +552,275 @@ def lmhead_stats(hidden, weight, tokens, temperature, *, workspace=None, stream=
     if rc != SV_OK:
         raise StatusError(rc, "sv_lmhead_stats")
     return row_max, lse, at
+
+
+# ---------------------------------------------------------------- a tree of drafted tokens
+
+class PagedCache:
+    """A paged key/value cache: k and v [num_pages, Hkv, page_size, D], bfloat16
+    or float8_e4m3fn, the latter with fp32 scales [num_pages, Hkv, page_size].
+    Holds the tensors it is given; checks them once."""
+
+    __slots__ = ("k", "v", "k_scale", "v_scale", "num_pages", "heads", "page_size", "head_dim", "code",
+                 "device")
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype:
+            raise ValueError("k and v must be [num_pages, Hkv, page_size, D] of one type")
+        if k.dtype == torch.bfloat16:
+            self.code = SV_BF16
+            if k_scale is not None or v_scale is not None:
+                raise ValueError("a bfloat16 cache has no scales")
+        elif k.dtype == torch.float8_e4m3fn:
+            self.code = SV_E4M3
+            for t in (k_scale, v_scale):
+                if t is None or t.shape != k.shape[:3] or t.dtype != torch.float32:
+                    raise ValueError("a float8_e4m3fn cache needs fp32 scales [num_pages, Hkv, page_size]")
+        else:
+            raise TypeError(f"a cache is bfloat16 or float8_e4m3fn, got {k.dtype}")
+        for t in (k, v, k_scale, v_scale):
+            if t is None:
+                continue
+            if not t.is_cuda or t.device != k.device:
+                raise ValueError("a cache's tensors must be on one CUDA device")
+            if not t.is_contiguous():
+                raise ValueError("a cache's tensors must be contiguous")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.num_pages, self.heads, self.page_size, self.head_dim = k.shape
+        self.device = k.device
+
+
+def new_cache(num_pages, heads, page_size, head_dim, dtype=torch.bfloat16, device="cuda") -> PagedCache:
+    """An empty (zeroed) cache of `dtype` (torch.bfloat16 or torch.float8_e4m3fn)."""
+    shape = (num_pages, heads, page_size, head_dim)
+    if dtype == torch.float8_e4m3fn:
+        k, v = (torch.zeros(shape, dtype=torch.uint8, device=device).view(dtype) for _ in range(2))
+        ks, vs = (torch.zeros(shape[:3], dtype=torch.float32, device=device) for _ in range(2))
+        return PagedCache(k, v, ks, vs)
+    return PagedCache(*(torch.zeros(shape, dtype=dtype, device=device) for _ in range(2)))
+
+
+def _address(t):
+    return t.data_ptr() if t is not None else None
+
+
+def _raw_stream(device, stream):
+    return (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
+
+
+def _rows(name, t, shape, dtype=None):
+    """Checks a [N, H, D] operand on the GPU whose rows are consecutive."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}'s last axis must be contiguous")
+
+
+def _vector(name, t, shape, dtype):
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    if tuple(t.shape) != shape or t.dtype != dtype:
+        raise ValueError(f"{name} must be {list(shape)} {dtype}")
+
+
+def sv_qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved, q_out, k_out,
+                    stream=None) -> int:
+    """Direct binding of the norm and rotation: q and q_out [N, Hq, D], k and
+    k_out [N, Hkv, D] bf16 or f32 (any token and head strides), weights [D] or
+    None, inv_freq [R/2] f32, positions [N] int32; returns the host status code."""
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q must be [N, Hq, D] and k [N, Hkv, D]")
+    N, Hq, D = q.shape
+    Hkv = k.shape[1]
+    _rows("q", q, (N, Hq, D))
+    _rows("k", k, (N, Hkv, D), q.dtype)
+    _rows("q_out", q_out, (N, Hq, D), q.dtype)
+    _rows("k_out", k_out, (N, Hkv, D), q.dtype)
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _vector(name, w, (D,), q.dtype)
+    if inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be [R/2]")
+    _vector("inv_freq", inv_freq, tuple(inv_freq.shape), torch.float32)
+    _vector("positions", positions, (N,), torch.int32)
+    return load_library().sv_qk_norm_rope(
+        q.data_ptr(), q.stride(0), q.stride(1), k.data_ptr(), k.stride(0), k.stride(1), _address(q_weight),
+        _address(k_weight), inv_freq.data_ptr(), positions.data_ptr(), N, Hq, Hkv, D,
+        2 * inv_freq.shape[0], _dtype_code(q), eps, 1 if interleaved else 0, q_out.data_ptr(),
+        q_out.stride(0), q_out.stride(1), k_out.data_ptr(), k_out.stride(0), k_out.stride(1),
+        _raw_stream(q.device, stream))
+
+
+def qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions, *, eps=1e-6, interleaved=False, q_out=None,
+                 k_out=None, stream=None):
+    """Norms per head and rotation by position in one pass; allocates the
+    outputs that are not given (pass q and k themselves to work in place) and
+    returns (q_out, k_out)."""
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if k_out is None:
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    rc = sv_qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved, q_out, k_out,
+                         stream=stream)
+    if rc != SV_OK:
+        raise StatusError(rc, "sv_qk_norm_rope")
+    return q_out, k_out
+
+
+def sv_cache_write(k, v, slots, cache, status=None, stream=None) -> int:
+    """Direct binding of the cache write: k, v [N, Hkv, D] bf16 or f32 (any
+    token and head strides), slots [N] int64 (-1 writes nothing), `status` an
+    int32 tensor whose first word collects device status bits, or None;
+    returns the host status code."""
+    N = slots.shape[0]
+    shape = (N, cache.heads, cache.head_dim)
+    _rows("k", k, shape)
+    _rows("v", v, shape, k.dtype)
+    _vector("slots", slots, (N,), torch.int64)
+    return load_library().sv_cache_write(
+        k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0), v.stride(1), slots.data_ptr(), N,
+        cache.heads, cache.head_dim, _dtype_code(k), cache.k.data_ptr(), cache.v.data_ptr(),
+        _address(cache.k_scale), _address(cache.v_scale), cache.num_pages, cache.page_size, cache.code,
+        _address(status), _raw_stream(k.device, stream))
+
+
+def cache_write(k, v, slots, cache, *, status=None, stream=None):
+    """Writes (and quantises, for a float8_e4m3fn cache) keys and values into
+    their slots; returns the cache."""
+    rc = sv_cache_write(k, v, slots, cache, status, stream=stream)
+    if rc != SV_OK:
+        raise StatusError(rc, "sv_cache_write")
+    return cache
+
+
+def sv_cache_read(cache, slots, k_out, v_out, status=None, stream=None) -> int:
+    """Direct binding of the cache read into k_out, v_out [N, Hkv, D] bf16 or
+    f32 (any token and head strides); returns the host status code."""
+    N = slots.shape[0]
+    shape = (N, cache.heads, cache.head_dim)
+    _rows("k_out", k_out, shape)
+    _rows("v_out", v_out, shape, k_out.dtype)
+    _vector("slots", slots, (N,), torch.int64)
+    return load_library().sv_cache_read(
+        cache.k.data_ptr(), cache.v.data_ptr(), _address(cache.k_scale), _address(cache.v_scale),
+        cache.num_pages, cache.page_size, cache.code, slots.data_ptr(), N, cache.heads, cache.head_dim,
+        _dtype_code(k_out), k_out.data_ptr(), k_out.stride(0), k_out.stride(1), v_out.data_ptr(),
+        v_out.stride(0), v_out.stride(1), _address(status), _raw_stream(k_out.device, stream))
+
+
+def cache_read(cache, slots, *, dtype=torch.bfloat16, k_out=None, v_out=None, status=None, stream=None):
+    """The keys and values in `slots` (zeros for -1), as `dtype` where the
+    outputs are not given; returns (k_out, v_out)."""
+    shape = (slots.shape[0], cache.heads, cache.head_dim)
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=dtype if v_out is None else v_out.dtype, device=cache.device)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=k_out.dtype, device=cache.device)
+    rc = sv_cache_read(cache, slots, k_out, v_out, status, stream=stream)
+    if rc != SV_OK:
+        raise StatusError(rc, "sv_cache_read")
+    return k_out, v_out
+
+
+def sv_tree_attention_workspace_size(B: int, T: int, Hq: int, Hkv: int, D: int, max_pages: int,
+                                     page_size: int) -> int:
+    return int(load_library().sv_tree_attention_workspace_size(B, T, Hq, Hkv, D, max_pages, page_size))
+
+
+def sv_tree_attention(q, cache, page_table, ctx_lens, parents, scale, out, workspace, stream=None) -> int:
+    """Direct binding of the tree attention: q [B, T, Hq, D] bf16 (any strides
+    but the last), page_table [B, max_pages], ctx_lens [B] and parents [B, T]
+    (or None for chains) int32, out [B, T, Hq, D] bf16 contiguous; returns the
+    host status code."""
+    if q.dim() != 4:
+        raise ValueError("q must be [B, T, Hq, D]")
+    B, T, Hq, D = q.shape
+    _rows("q", q, (B, T, Hq, cache.head_dim), torch.bfloat16)
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, max_pages]")
+    _vector("page_table", page_table, (B, page_table.shape[1]), torch.int32)
+    _vector("ctx_lens", ctx_lens, (B,), torch.int32)
+    if parents is not None:
+        _vector("parents", parents, (B, T), torch.int32)
+    _vector("out", out, (B, T, Hq, D), torch.bfloat16)
+    return load_library().sv_tree_attention(
+        q.data_ptr(), q.stride(0), q.stride(1), q.stride(2), cache.k.data_ptr(), cache.v.data_ptr(),
+        _address(cache.k_scale), _address(cache.v_scale), cache.num_pages, cache.page_size, cache.code,
+        page_table.data_ptr(), ctx_lens.data_ptr(), _address(parents), B, T, Hq, cache.heads, D,
+        page_table.shape[1], scale, out.data_ptr(), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _raw_stream(q.device, stream))
+
+
+def tree_attention(q, cache, page_table, ctx_lens, parents=None, *, scale=None, out=None, workspace=None,
+                   stream=None):
+    """Attention of trees of drafted tokens over the paged cache (`scale`
+    defaults to D ** -0.5); allocates the output and a workspace if none is
+    given, and returns out [B, T, Hq, D] bf16."""
+    if q.dim() != 4:
+        raise ValueError("q must be [B, T, Hq, D]")
+    B, T, Hq, D = q.shape
+    if out is None:
+        out = torch.empty((B, T, Hq, D), dtype=torch.bfloat16, device=q.device)
+    if workspace is None:
+        n = sv_tree_attention_workspace_size(B, T, Hq, cache.heads, D, page_table.shape[-1], cache.page_size)
+        workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=q.device)
+    rc = sv_tree_attention(q, cache, page_table, ctx_lens, parents, D ** -0.5 if scale is None else scale, out,
+                           workspace, stream=stream)
+    if rc != SV_OK:
+        raise StatusError(rc, "sv_tree_attention")
+    return out
+
+
+def sv_tree_workspace_size(B: int, T: int, V: int, dtype: int) -> int:
+    return int(load_library().sv_tree_workspace_size(B, T, V, dtype))
+
+
+def spec_verify_tree(target, draft, draft_index, tokens, parents, uniforms, temperature, out_tokens, out_nodes,
+                     n_accepted, workspace, stream=None) -> int:
+    """Direct binding of tree verification: target [B, T, V] and draft [R, V]
+    bf16/f32, draft_index, tokens, parents [B, T] int32, uniforms [B, T] f32;
+    returns the host status code."""
+    if target.dim() != 3 or draft.dim() != 2 or draft.shape[1] != target.shape[2]:
+        raise ValueError("target must be [B, T, V] and draft [R, V]")
+    B, T, V = target.shape
+    if draft.dtype != target.dtype:
+        raise TypeError("draft must have the target's dtype")
+    for name, t in (("target", target), ("draft", draft)):
+        if not t.is_cuda or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    for name, t in (("draft_index", draft_index), ("tokens", tokens), ("parents", parents),
+                    ("out_tokens", out_tokens), ("out_nodes", out_nodes)):
+        _vector(name, t, (B, T), torch.int32)
+    _vector("uniforms", uniforms, (B, T), torch.float32)
+    _vector("n_accepted", n_accepted, (B,), torch.int32)
+    return load_library().spec_verify_tree(
+        target.data_ptr(), draft.data_ptr(), draft_index.data_ptr(), tokens.data_ptr(), parents.data_ptr(),
+        uniforms.data_ptr(), B, T, V, draft.shape[0], _dtype_code(target), temperature, out_tokens.data_ptr(),
+        out_nodes.data_ptr(), n_accepted.data_ptr(), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _raw_stream(target.device, stream))
+
+
+def verify_tree(target, draft, draft_index, tokens, parents, uniforms, temperature, *, workspace=None, outs=None,
+                stream=None):
+    """Verification of trees of drafted tokens; allocates the outputs (unless
+    `outs` holds the three) and a workspace if none is given, and returns
+    (out_tokens [B, T], out_nodes [B, T], n_accepted [B]), all int32."""
+    if target.dim() != 3:
+        raise ValueError("target must be [B, T, V]")
+    B, T, V = target.shape
+    dev = target.device
+    if outs is None:
+        outs = (torch.empty(B, T, dtype=torch.int32, device=dev), torch.empty(B, T, dtype=torch.int32, device=dev),
+                torch.empty(B, dtype=torch.int32, device=dev))
+    if workspace is None:
+        n = sv_tree_workspace_size(B, T, V, _dtype_code(target))
+        workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
+    rc = spec_verify_tree(target, draft, draft_index, tokens, parents, uniforms, temperature, *outs, workspace,
+                          stream=stream)
+    if rc != SV_OK:
+        raise StatusError(rc, "spec_verify_tree")
+    return tuple(outs)

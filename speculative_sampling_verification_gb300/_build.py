@@ -16,7 +16,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libspecverify.so")
-SOURCES = ["sv_kernels.cu", "sv_api.cu", "sv_static_scratch.cu", "sv_lmhead.cu"]
+SOURCES = ["sv_kernels.cu", "sv_api.cu", "sv_static_scratch.cu", "sv_lmhead.cu",
+           "sv_tree_io.cu", "sv_tree_attn.cu", "sv_tree_verify.cu"]
 # Translation units: (source, extra nvcc flags, object). sv_kernels.cu is
 # compiled three times, each unit holding one group of its kernels (SV_TU).
 UNITS = [("sv_kernels.cu", ["-DSV_TU=1"], "sv_kernels_verify.o"),
@@ -24,7 +25,10 @@ UNITS = [("sv_kernels.cu", ["-DSV_TU=1"], "sv_kernels_verify.o"),
          ("sv_kernels.cu", ["-DSV_TU=3"], "sv_kernels_topp.o"),
          ("sv_api.cu", [], "sv_api.o"),
          ("sv_static_scratch.cu", [], "sv_static_scratch.o"),
-         ("sv_lmhead.cu", [], "sv_lmhead.o")]
+         ("sv_lmhead.cu", [], "sv_lmhead.o"),
+         ("sv_tree_io.cu", [], "sv_tree_io.o"),
+         ("sv_tree_attn.cu", [], "sv_tree_attn.o"),
+         ("sv_tree_verify.cu", [], "sv_tree_verify.o")]
 HEADERS = ["sv_device.cuh", "sv_internal.h", "sv_exp_table.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2", "-diag-suppress=177",

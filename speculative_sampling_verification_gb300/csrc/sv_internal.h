@@ -26,6 +26,7 @@ constexpr int kSubPerChunk = 8;
 constexpr long long kMinDrawCtas = 2 * 152;
 
 constexpr int kMaxK = 64;
+constexpr int kHeadDimMax = 1024;  // values of a head: norms, cache, attention
 
 enum : int { kModeResidual = 0, kModeBonus = 1, kModeFailed = -1 };
 

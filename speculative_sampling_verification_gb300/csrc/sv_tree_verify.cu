@@ -1,0 +1,664 @@
+// Verification of a tree of drafted tokens (spec_verify_tree): the modified
+// rejection sampling of "Accelerating Large Language Model Decoding with
+// Speculative Sampling" (wikillm.com paper card, §4.2) with several candidates
+// at a node, tried in turn.
+//
+// At the current node, with target row q and draft row p (softmax at
+// temperature T), the children are tried in index order against the residual
+// r, which is q at first. Child c of token x is accepted when
+// u_c < min(1, r(x)/p(x)); a rejection turns r into max(0, r - p)/sum. The children
+// are drawn from the same p, so after any number of rejections
+//     r = max(0, A q - B p)
+// with two scalars: max(0, max(0, A q - B p) - p) = max(0, A q - (B + 1) p),
+// because where the inner maximum is 0 the outer one is too. So a rejection
+// costs one pass over two rows for Z = sum max(0, A q - (B + 1) p), then
+// (A, B) <- (A, B + 1) / Z, and no residual is ever stored. A sum below 2^-40 (r
+// equals p but for rounding: such a rejection has that probability) leaves r
+// as it was.
+//
+// One thread-block cluster a sequence; the vocabulary is cut into one region
+// per warp of the cluster. Only the rows of visited nodes are read: from HBM
+// once, then from L2. A pass ends with the warps' sums joined in a fixed order:
+// within a CTA through shared memory, across the cluster by pushing each CTA's
+// figures to every other, so that each CTA comes to the same decision by itself.
+// The draw needs no pass of its own: the sums of the pass that made the
+// residual lead to one warp's region, which that warp scans.
+#include <cfloat>
+#include <cmath>
+#include <cstdint>
+#include <algorithm>
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "../../include/spec_verify.h"
+#include "sv_device.cuh"
+#include "sv_internal.h"
+
+namespace sv {
+namespace tvf {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxCluster = 8;  // the portable cluster size
+constexpr int kTreeMax = 128;
+constexpr double kResidualMin = 9.094947017729282e-13;  // 2^-40
+constexpr int kStep = 256;      // elements a warp takes at once: eight a lane
+
+struct Args {
+  const void *target, *draft;
+  const int32_t *draft_index, *tokens, *parents;
+  const float* uniforms;
+  int32_t *out_tokens, *out_nodes, *n_acc;
+  unsigned* status;
+  int B, T, V, R, region;  // region: elements of a warp, a multiple of 8
+  float ih, il;            // 1/T as a float-float
+  int unit_t;
+};
+
+struct Exchange {
+  double sum[2][kMaxCluster];  // per CTA: of q and p, or of the residual
+  float top[2][kMaxCluster];   // per CTA: row maxima
+};
+
+struct Shared {
+  float2 tab[256];
+  Exchange x[2];
+  double wsum[2][2][kWarps];  // [buffer][q or p][warp]: sums of the warps' regions
+  float wtop[2][kWarps];
+  double cta_sum[2][kMaxCluster];  // [buffer]: the CTAs' sums of the current residual
+  double ratio[kTreeMax];  // q(x)/p(x) of the children's tokens
+  int parents[kTreeMax], tokens[kTreeMax], drow[kTreeMax];
+  float u[kTreeMax];
+  int path[kTreeMax];
+  float m[2];
+  double S[2];
+  double Z;
+};
+
+template <int DT>
+SV_DEVINL float load_one(const void* row, long long i) {
+  return DT == SV_BF16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(row)[i])
+                       : static_cast<const float*>(row)[i];
+}
+
+// Eight elements from e on (e a multiple of 8); -inf from `end` on. VEC: rows
+// are 16-byte aligned.
+template <int DT, bool VEC>
+SV_DEVINL void load8(const void* row, int e, int end, float2 (&v)[4]) {
+  if (VEC && e + 8 <= end) {
+    if constexpr (DT == SV_BF16) {
+      const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(row) + e);
+      v[0] = make_float2(bf16_lo(w.x), bf16_hi(w.x));
+      v[1] = make_float2(bf16_lo(w.y), bf16_hi(w.y));
+      v[2] = make_float2(bf16_lo(w.z), bf16_hi(w.z));
+      v[3] = make_float2(bf16_lo(w.w), bf16_hi(w.w));
+    } else {
+      const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(row) + e);
+      const float4 a = p[0], b = p[1];
+      v[0] = make_float2(a.x, a.y);
+      v[1] = make_float2(a.z, a.w);
+      v[2] = make_float2(b.x, b.y);
+      v[3] = make_float2(b.z, b.w);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i].x = e + 2 * i < end ? load_one<DT>(row, e + 2 * i) : neg_inf();
+      v[i].y = e + 2 * i + 1 < end ? load_one<DT>(row, e + 2 * i + 1) : neg_inf();
+    }
+  }
+}
+
+// exp((l - m)/T) of a pair as float-floats, to about 1e-12.
+SV_DEVINL ff2 weight2(float2 l, float nm, const Args& a, const float2* tab) {
+  const ff2 x = scaled_diff2(l, f2(nm), a.ih, a.il, a.unit_t != 0);
+  return exp_ff2(x.hi, x.lo, tab);
+}
+
+SV_DEVINL double weight(float l, float m, const Args& a, const float2* tab) {
+  const ff x = scaled_diff(l, m, a.ih, a.il, a.unit_t != 0);
+  return ff_to_double(exp_ff(x.hi, x.lo, tab));
+}
+
+// A pass's weights: w(x) = e_q max(0, a - b e^d) with e_q = exp((lq - mq)/T) and
+// d = ((lp - mp) - (lq - mq))/T, or e_q alone (`plain`). With a = A and
+// b = B S_q/S_p this is S_q max(0, A q - B p), q's factor taken out: where A q and
+// B p nearly cancel, the error is then that of the ratio p/q alone, and tokens of
+// one logit difference keep their exact proportions. d is formed as
+// (lp - lq) + (mq - mp) for the same reason.
+struct Mix {
+  const void *q, *p;
+  float nmq;     // -mq
+  ff c;          // mq - mp
+  ff a, b;
+  bool plain;
+};
+
+// Ratios above e^80 count as e^80: their weight is 0 unless b < a e^-80.
+constexpr float kRatioTop = 80.0f;
+
+SV_DEVINL ff2 mix2(float2 lq, float2 lp, const Mix& x, const Args& a, const float2* tab) {
+  const ff2 e = weight2(lq, x.nmq, a, tab);
+  const ff2 d0 = two_sum2(lp, f2_mul(lq, f2(-1.0f)));
+  const ff2 d1 = two_sum2(d0.hi, f2(x.c.hi));
+  ff2 d = {d1.hi, f2_add(d1.lo, f2_add(d0.lo, f2(x.c.lo)))};
+  if (a.unit_t == 0) {
+    const float2 h = f2_mul(d.hi, f2(a.ih));
+    const float2 r = f2_fma(d.hi, f2(a.ih), f2_mul(h, f2(-1.0f)));
+    d.lo = f2_fma(d.hi, f2(a.il), f2_fma(d.lo, f2(a.ih), r));
+    d.hi = h;
+  }
+  if (d.hi.x > kRatioTop) d.hi.x = kRatioTop, d.lo.x = 0.0f;
+  if (d.hi.y > kRatioTop) d.hi.y = kRatioTop, d.lo.y = 0.0f;
+  const ff2 r = exp_ff2(d.hi, d.lo, tab);
+  // t = a - b r
+  const float2 ph = f2_mul(r.hi, f2(-x.b.hi));
+  const float2 pe = f2_fma(r.hi, f2(-x.b.hi), f2_mul(ph, f2(-1.0f)));
+  const float2 pl = f2_sub(pe, f2_fma(r.hi, f2(x.b.lo), f2_mul(r.lo, f2(x.b.hi))));
+  const ff2 t0 = two_sum2(f2(x.a.hi), ph);
+  const float2 tl = f2_add(t0.lo, f2_add(f2(x.a.lo), pl));
+  // w = e t, 0 where t is not positive or the target has no such token
+  const float2 wh = f2_mul(e.hi, t0.hi);
+  const float2 we = f2_fma(e.hi, t0.hi, f2_mul(wh, f2(-1.0f)));
+  const float2 wl = f2_add(we, f2_fma(e.hi, tl, f2_mul(e.lo, t0.hi)));
+  const float2 s = f2_add(t0.hi, tl);
+  const bool kx = e.hi.x > 0.0f && s.x > 0.0f, ky = e.hi.y > 0.0f && s.y > 0.0f;
+  return {make_float2(kx ? wh.x : 0.0f, ky ? wh.y : 0.0f),
+          make_float2(kx ? wl.x : 0.0f, ky ? wl.y : 0.0f)};
+}
+
+template <int DT, bool VEC>
+SV_DEVINL void mix8(const Mix& x, int e, int end, const Args& a, const float2* tab, ff2 (&w)[4]) {
+  float2 q[4];
+  load8<DT, VEC>(x.q, e, end, q);
+  if (x.plain) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = weight2(q[i], x.nmq, a, tab);
+    return;
+  }
+  float2 p[4];
+  load8<DT, VEC>(x.p, e, end, p);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = mix2(q[i], p[i], x, a, tab);
+}
+
+SV_DEVINL double warp_sum(double v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+SV_DEVINL double ff2_total(const ff2& s) {
+  return ((double)s.hi.x + (double)s.hi.y) + ((double)s.lo.x + (double)s.lo.y);
+}
+
+// Maximum and sum of exp((l - max)/T) over a warp's region of one row. NaN and
+// +inf end in a NaN sum; a region of -inf has the maximum -inf and the sum 0.
+template <int DT, bool VEC>
+SV_DEVINL void region_stats(const void* row, int begin, int end, int lane, const Args& a,
+                            const float2* tab, float* top, double* sum) {
+  float m = neg_inf();
+#pragma unroll 4
+  for (int e = begin + lane * 8; e < end; e += kStep) {
+    float2 v[4];
+    load8<DT, VEC>(row, e, end, v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = fmaxf(m, fmaxf(v[i].x, v[i].y));
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float nm = m == neg_inf() ? 0.0f : -m;
+  ff2 acc = {f2(1.0f), f2(0.0f)};
+#pragma unroll 2
+  for (int e = begin + lane * 8; e < end; e += kStep) {
+    float2 v[4];
+    load8<DT, VEC>(row, e, end, v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ff_accumulate_biased2(acc, weight2(v[i], nm, a, tab));
+  }
+  acc.hi = f2_add(acc.hi, f2(-1.0f));
+  *top = m;
+  *sum = warp_sum(ff2_total(acc));
+}
+
+// Sum of the residual's weights over a warp's region.
+template <int DT, bool VEC>
+SV_DEVINL double region_mix(const Mix& x, int begin, int end, int lane, const Args& a, const float2* tab) {
+  ff2 acc = {f2(0.0f), f2(0.0f)};
+  for (int e = begin + lane * 8; e < end; e += kStep) {
+    ff2 w[4];
+    mix8<DT, VEC>(x, e, end, a, tab, w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const ff2 s = two_sum2(acc.hi, w[i].hi);
+      acc.hi = s.hi;
+      acc.lo = f2_add(acc.lo, f2_add(s.lo, w[i].lo));
+    }
+  }
+  return warp_sum(ff2_total(acc));
+}
+
+// exp((part - whole)/T) of two maxima; 0 for a part without an entry.
+SV_DEVINL double rescale(float part, float whole, const Args& a, const float2* tab) {
+  return part == neg_inf() ? 0.0 : weight(part, whole, a, tab);
+}
+
+// exp(((lq - mq) - (lp - mp))/T), c = mq - mp: from the difference of the logits, so
+// that it holds where both probabilities are too small for fp32. Beyond e^80 it
+// is infinite, below e^-87 a positive 1e-40; 0 where the target has no such token.
+SV_DEVINL double token_ratio(float lq, float lp, ff c, const Args& a, const float2* tab) {
+  if (lq == neg_inf()) return 0.0;
+  if (lp == neg_inf()) return INFINITY;
+  const ff d0 = two_sum(lq, -lp);
+  const ff d1 = two_sum(d0.hi, -c.hi);
+  const float dl = __fadd_rn(d1.lo, __fsub_rn(d0.lo, c.lo));
+  const ff h = two_prod(d1.hi, a.ih);
+  const float hl = __fmaf_rn(d1.hi, a.il, __fmaf_rn(dl, a.ih, h.lo));
+  if (h.hi > kRatioTop) return INFINITY;
+  if (h.hi < -87.0f) return 1e-40;
+  return ff_to_double(exp_ff(h.hi, hl, tab));
+}
+
+// The token at which the running sum of the region's weights passes `target`,
+// or the region's last token of positive weight.
+template <int DT, bool VEC>
+SV_DEVINL int region_draw(const Mix& x, int begin, int end, double target, int lane, const Args& a,
+                          const float2* tab) {
+  double before = 0.0;
+  int last = -1;
+  for (int e0 = begin; e0 < end; e0 += kStep) {
+    const int e = e0 + lane * 8;
+    ff2 w[4];
+    mix8<DT, VEC>(x, e, end, a, tab, w);
+    double v[8], mine = 0.0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = (double)w[i].hi.x + (double)w[i].lo.x;
+      v[2 * i + 1] = (double)w[i].hi.y + (double)w[i].lo.y;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      mine += v[i];
+      if (v[i] > 0.0) last = e + i;
+    }
+    double incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const double t = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += t;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, before + incl > target);
+    if (hit) {
+      const int owner = __ffs(hit) - 1;
+      int token = e;
+      if (lane == owner) {
+        double run = before + (incl - mine);
+        token = -1;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          run += v[i];
+          if (token < 0 && v[i] > 0.0 && run > target) token = e + i;
+        }
+        if (token < 0) token = last;  // the sums' rounding hid the step
+      }
+      return __shfl_sync(0xffffffffu, token, owner);
+    }
+    before += __shfl_sync(0xffffffffu, incl, 31);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) last = max(last, __shfl_xor_sync(0xffffffffu, last, o));
+  return last;
+}
+
+template <int DT, bool VEC>
+__global__ void __launch_bounds__(kThreads) tree_verify_kernel(Args a, int nc) {
+  __shared__ Shared sh;
+  constexpr int kEs = DT == SV_BF16 ? 2 : 4;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const unsigned rank = cluster_ctarank();
+  const long long b = blockIdx.x / nc;
+  const int T = a.T;
+  sh.tab[tid] = kSvExp2Table[tid];
+
+  // ---- the tree, checked by every CTA alike
+  unsigned bad = 0;
+  if (tid < T) {
+    const long long at = b * T + tid;
+    const int p = a.parents[at];
+    sh.parents[tid] = p;
+    sh.tokens[tid] = a.tokens[at];
+    sh.u[tid] = a.uniforms[at];
+    sh.drow[tid] = a.draft_index[at];
+  }
+  __syncthreads();
+  if (tid < T) {
+    const int p = sh.parents[tid];
+    if (tid == 0 ? p != -1 : (p != -2 && (p < 0 || p >= tid || sh.parents[p] == -2))) bad |= SV_DEV_TREE;
+    if (p != -2) {
+      if (!(sh.u[tid] >= 0.0f && sh.u[tid] <= 1.0f)) bad |= SV_DEV_UNIFORM_RANGE;
+      if (tid > 0 && (sh.tokens[tid] < 0 || sh.tokens[tid] >= a.V)) bad |= SV_DEV_TOKEN_RANGE;
+      if (tid > 0 && p >= 0 && p < tid && (sh.drow[p] < 0 || sh.drow[p] >= a.R)) bad |= SV_DEV_TREE;
+    }
+  }
+  if (bad && rank == 0) atomicOr(a.status, bad);
+  const bool failed_args = __syncthreads_or(bad != 0);
+  int32_t* out = a.out_tokens + b * T;
+  int32_t* nodes = a.out_nodes + b * T;
+  if (failed_args) {  // every CTA of the cluster comes here
+    if (rank == 0) {
+      for (int i = tid; i < T; i += kThreads) out[i] = nodes[i] = -1;
+      if (tid == 0) a.n_acc[b] = -1;
+    }
+    return;
+  }
+  cluster_sync();  // every CTA has started: its shared memory may be written
+
+  const int region0 = (int)(rank * kWarps + warp);
+  const int begin = (int)min((long long)a.V, (long long)region0 * a.region);
+  const int end = (int)min((long long)a.V, (long long)begin + a.region);
+  unsigned phase = 0;
+  int cur = 0, count = 0, buf = 0;
+  unsigned failure = 0;
+  Mix x{};
+  for (;;) {  // one round a visited node
+    bool kids = false;
+    for (int i = cur + 1 + tid; i < T; i += kThreads) kids |= sh.parents[i] == cur;
+    kids = __syncthreads_or(kids);
+    const void* q = static_cast<const unsigned char*>(a.target) + ((b * T + cur) * a.V) * kEs;
+    const void* p = kids ? static_cast<const unsigned char*>(a.draft) + (long long)sh.drow[cur] * a.V * kEs
+                         : nullptr;
+    // ---- maxima and sums of the node's rows
+    buf = 0;
+    {
+      float top;
+      double sum;
+      region_stats<DT, VEC>(q, begin, end, lane, a, sh.tab, &top, &sum);
+      if (lane == 0) {
+        sh.wtop[0][warp] = top;
+        sh.wsum[0][0][warp] = sum;
+      }
+      if (kids) {
+        region_stats<DT, VEC>(p, begin, end, lane, a, sh.tab, &top, &sum);
+        if (lane == 0) {
+          sh.wtop[1][warp] = top;
+          sh.wsum[0][1][warp] = sum;
+        }
+      }
+    }
+    __syncthreads();
+    Exchange& ex = sh.x[phase & 1];
+    ++phase;
+    if (warp < (kids ? 2 : 1)) {  // warp 0 joins q's regions, warp 1 p's
+      const int r = warp;
+      const float t = lane < kWarps ? sh.wtop[r][lane] : neg_inf();
+      float m = t;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      // A region's sum may be NaN although its maximum is -inf: it counts.
+      double s = 0.0;
+      if (lane < kWarps) {
+        const double own = sh.wsum[0][r][lane];
+        s = own == 0.0 ? 0.0 : own * (t == neg_inf() ? 1.0 : weight(t, m, a, sh.tab));
+        sh.wsum[0][r][lane] = s;  // now relative to the CTA's maximum
+      }
+      s = warp_sum(s);
+      if (lane < nc) {
+        const unsigned dst = dsmem_map(smem_u32(&ex.sum[r][rank]), lane);
+        dsmem_st_u64(dst, (unsigned long long)__double_as_longlong(s));
+        dsmem_st_f32(dsmem_map(smem_u32(&ex.top[r][rank]), lane), m);
+      }
+    }
+    cluster_sync();
+    if (warp < (kids ? 2 : 1)) {
+      const int r = warp;
+      const float t = lane < nc ? ex.top[r][lane] : neg_inf();
+      float m = t;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      double s = 0.0;
+      if (lane < nc) {
+        const double own = ex.sum[r][lane];
+        s = own == 0.0 ? 0.0 : own * (t == neg_inf() ? 1.0 : weight(t, m, a, sh.tab));
+        if (r == 0) sh.cta_sum[0][lane] = s;
+      }
+      const double cta_scale = rescale(__shfl_sync(0xffffffffu, t, rank), m, a, sh.tab);
+      if (r == 0 && lane < kWarps) sh.wsum[0][0][lane] *= cta_scale;
+      s = warp_sum(s);
+      if (lane == 0) {
+        sh.m[r] = m;
+        sh.S[r] = s;
+      }
+    }
+    __syncthreads();
+    for (int r = 0; r < (kids ? 2 : 1); ++r) {
+      if (!(sh.S[r] < INFINITY) || sh.m[r] == INFINITY) failure |= SV_DEV_NONFINITE;
+      else if (sh.m[r] == neg_inf()) failure |= SV_DEV_EMPTY_ROW;
+    }
+    if (failure) break;
+    x = Mix{};
+    x.q = q;
+    x.p = p;
+    x.nmq = -sh.m[0];
+    x.plain = true;
+    if (!kids) break;
+    x.c = two_sum(sh.m[0], -sh.m[1]);
+    const double Sq = sh.S[0], Sp = sh.S[1];
+    for (int i = cur + 1 + tid; i < T; i += kThreads) {
+      if (sh.parents[i] != cur) continue;
+      sh.ratio[i] = token_ratio(load_one<DT>(q, sh.tokens[i]), load_one<DT>(p, sh.tokens[i]), x.c, a, sh.tab) *
+                    (Sp / Sq);
+    }
+    __syncthreads();
+
+    // ---- the children in turn
+    double A = 1.0, Bp = 0.0;
+    int next = -1;
+    for (int i = cur + 1; i < T && next < 0; ++i) {
+      if (sh.parents[i] != cur) continue;
+      // r(x)/p(x) = A q/p - B
+      if ((double)sh.u[i] < fmin(1.0, A * sh.ratio[i] - Bp)) {
+        next = i;
+        break;
+      }
+      // Scaled by a power of two so that the larger scalar lies in [1, 2).
+      const double s = exp2(-(double)ilogb(fmax(A, Bp + 1.0)));
+      const double fa = A * s, fb = (Bp + 1.0) * s * (Sq / Sp);
+      Mix y = x;
+      y.plain = false;
+      y.a = {(float)fa, (float)(fa - (double)(float)fa)};
+      y.b = {(float)fb, (float)(fb - (double)(float)fb)};
+      const int nb = buf ^ 1;
+      const double sum = region_mix<DT, VEC>(y, begin, end, lane, a, sh.tab);
+      if (lane == 0) sh.wsum[nb][0][warp] = sum;
+      __syncthreads();
+      Exchange& ez = sh.x[phase & 1];
+      ++phase;
+      if (warp == 0) {
+        const double c = warp_sum(lane < kWarps ? sh.wsum[nb][0][lane] : 0.0);
+        if (lane < nc)
+          dsmem_st_u64(dsmem_map(smem_u32(&ez.sum[0][rank]), lane),
+                       (unsigned long long)__double_as_longlong(c));
+      }
+      cluster_sync();
+      if (warp == 0) {
+        const double c = lane < nc ? ez.sum[0][lane] : 0.0;
+        if (lane < nc) sh.cta_sum[nb][lane] = c;
+        const double z = warp_sum(c);
+        if (lane == 0) sh.Z = z;
+      }
+      __syncthreads();
+      const double Z = sh.Z / (Sq * s);
+      if (Z >= kResidualMin) {
+        A = A / Z;
+        Bp = (Bp + 1.0) / Z;
+        x = y;
+        buf = nb;
+      }
+      __syncthreads();  // sh.Z and the other buffer are free again
+    }
+    if (next < 0) break;
+    if (tid == 0) sh.path[count] = next;
+    ++count;
+    cur = next;
+    __syncthreads();
+  }
+
+  if (failure) {
+    if (rank == 0) {
+      if (tid == 0) {
+        atomicOr(a.status, failure);
+        a.n_acc[b] = -1;
+      }
+      for (int i = tid; i < T; i += kThreads) out[i] = nodes[i] = -1;
+    }
+    return;
+  }
+
+  // ---- the draw: the CTA, then the warp whose region holds u * total
+  if (rank == 0) {
+    for (int i = tid; i < T; i += kThreads) {
+      const int node = i < count ? sh.path[i] : -1;
+      nodes[i] = node;
+      if (i != count) out[i] = node < 0 ? -1 : sh.tokens[node];
+    }
+    if (tid == 0) a.n_acc[b] = count;
+  }
+  double total = 0.0;
+  for (int c = 0; c < nc; ++c) total += sh.cta_sum[buf][c];
+  const double goal = (double)sh.u[0] * total;
+  double before = 0.0, at = 0.0;
+  int owner = -1, last = 0;
+  for (int c = 0; c < nc; ++c) {
+    const double s = sh.cta_sum[buf][c];
+    if (s > 0.0) {
+      last = c;
+      if (owner < 0 && before + s > goal) {
+        owner = c;
+        at = before;
+      }
+    }
+    before += s;
+  }
+  const bool past = owner < 0;  // u = 1: the last token of positive weight
+  if (past) owner = last;
+  if (owner != (int)rank) return;
+  before = at;
+  int w = -1;
+  last = 0;
+  for (int i = 0; i < kWarps; ++i) {
+    const double s = sh.wsum[buf][0][i];
+    if (s > 0.0) {
+      last = i;
+      if (w < 0 && !past && before + s > goal) {
+        w = i;
+        at = before;
+      }
+    }
+    before += s;
+  }
+  const bool beyond = w < 0;
+  if (beyond) w = last;
+  if (w != warp) return;
+  const int token = region_draw<DT, VEC>(x, begin, end, beyond ? INFINITY : goal - at, lane, a, sh.tab);
+  if (lane == 0) out[count] = token;
+}
+
+// ---------------------------------------------------------------- host side
+
+bool misaligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
+
+bool sizes_ok(int B, int T, int V, int dtype) {
+  if (dtype != SV_BF16 && dtype != SV_F32) return false;
+  if (B < 0 || T < 1 || T > kTreeMax || V < 1 || V > (1 << 30)) return false;
+  return (long long)B * T * V <= (1ll << 45) && B <= (1 << 27);
+}
+
+// CTAs a sequence: each warp gets a step of 256 elements at least, up to the
+// portable cluster size.
+int cluster_size(int V) {
+  int nc = 1;
+  while (nc < kMaxCluster && (long long)nc * kWarps * kStep < V) nc <<= 1;
+  return nc;
+}
+
+template <int DT, bool VEC>
+cudaError_t launch(const Args& a, cudaStream_t st) {
+  const int nc = cluster_size(a.V);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)a.B * (unsigned)nc);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)nc;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, tree_verify_kernel<DT, VEC>, a, nc);
+}
+
+}  // namespace tvf
+}  // namespace sv
+
+using namespace sv::tvf;
+
+extern "C" {
+
+size_t sv_tree_workspace_size(int B, int T, int V, int dtype) {
+  return sizes_ok(B, T, V, dtype) ? 256 : 0;
+}
+
+int spec_verify_tree(const void* target_logits, const void* draft_logits, const int32_t* draft_index,
+                     const int32_t* tokens, const int32_t* parents, const float* uniforms, int B, int T,
+                     int V, int R, int dtype, float temperature, int32_t* out_tokens,
+                     int32_t* out_nodes, int32_t* n_accepted, void* workspace, size_t workspace_bytes,
+                     void* stream) {
+  if (dtype != SV_BF16 && dtype != SV_F32) return SV_ERR_DTYPE;
+  if (!sizes_ok(B, T, V, dtype) || R < 0) return SV_ERR_SHAPE;
+  if (!std::isfinite(temperature) || !(temperature > 0.0f)) return SV_ERR_TEMPERATURE;
+  if (B == 0) return SV_OK;
+  if (!target_logits || (R > 0 && !draft_logits) || !draft_index || !tokens || !parents || !uniforms ||
+      !out_tokens || !out_nodes || !n_accepted || !workspace)
+    return SV_ERR_NULL;
+  const size_t es = dtype == SV_BF16 ? 2 : 4;
+  if (misaligned(target_logits, es) || misaligned(draft_logits, es) || misaligned(draft_index, 4) ||
+      misaligned(tokens, 4) || misaligned(parents, 4) || misaligned(uniforms, 4) ||
+      misaligned(out_tokens, 4) || misaligned(out_nodes, 4) || misaligned(n_accepted, 4) ||
+      misaligned(workspace, 256))
+    return SV_ERR_ALIGN;
+  if (workspace_bytes < sv_tree_workspace_size(B, T, V, dtype)) return SV_ERR_WORKSPACE;
+  Args a{};
+  a.target = target_logits;
+  a.draft = draft_logits;
+  a.draft_index = draft_index;
+  a.tokens = tokens;
+  a.parents = parents;
+  a.uniforms = uniforms;
+  a.out_tokens = out_tokens;
+  a.out_nodes = out_nodes;
+  a.n_acc = n_accepted;
+  a.status = static_cast<unsigned*>(workspace);
+  a.B = B;
+  a.T = T;
+  a.V = V;
+  a.R = R;
+  const long long regions = (long long)cluster_size(V) * kWarps;
+  a.region = (int)(((V + regions - 1) / regions + 7) / 8 * 8);
+  const double inv = 1.0 / (double)temperature;
+  a.ih = (float)inv;
+  a.il = (float)(inv - (double)a.ih);
+  a.unit_t = temperature == 1.0f;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (cudaMemsetAsync(workspace, 0, 4, st) != cudaSuccess) return SV_ERR_CUDA;
+  const bool vec = !misaligned(target_logits, 16) && !misaligned(draft_logits, 16) && (size_t)V * es % 16 == 0;
+  cudaError_t e;
+  if (dtype == SV_BF16)
+    e = vec ? launch<SV_BF16, true>(a, st) : launch<SV_BF16, false>(a, st);
+  else
+    e = vec ? launch<SV_F32, true>(a, st) : launch<SV_F32, false>(a, st);
+  return e == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+}
+
+}  // extern "C"
