@@ -5,7 +5,10 @@
 #include <cmath>
 #include <cstdint>
 #include <algorithm>
+#include <mutex>
 
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -31,6 +34,959 @@ struct Args {
   int B, T, Hq, Hkv, D, P, max_pages;
   float scale;
 };
+
+// ---------------------------------------------------------------- tensor cores
+//
+// Rows are (node, query head of the group) pairs that share a key/value head: a
+// Q tile is up to 128 of them, the M of one tcgen05.mma. Keys come in tiles of
+// KT positions. For a tile: S = Q K^T into tensor memory; one thread a row turns
+// S into P = 2^(S c - m c) (c = scale log2 e) with its running maximum m and sum,
+// and writes P as bf16 over S; O += P V with P as the tensor-memory operand.
+// O is rescaled in tensor memory only when the maximum grows by more than 2^8
+// in P (P stays below 2^8, and the result does not depend on the reference). P is
+// rounded to bf16 (half a step, 2^-8) because the tensor cores take it so; the
+// sums are those of the unrounded values.
+//
+// Two streams, each with its S, O and a warpgroup for the softmax, keep the
+// tensor cores busy while a softmax runs. With at most 128 rows a key/value
+// head (SHARED = false) the streams take alternate tiles of the same rows, and
+// their results are joined at the end; with more rows (SHARED) each stream has a Q
+// tile of its own and both use every tile. Head sizes above 128 have room for
+// one stream only.
+//
+// Work: the tiles of all (sequence, key/value head) items form one line, cut into
+// equal ranges, one for each group of CTAs (the CTAs of a group take the item's
+// Q tiles, in step, so that a tile is read from HBM once). The cuts follow the
+// lengths on the device, so ragged batches and few long sequences balance
+// alike. An item that lies in one range is written at once; the parts of a cut
+// one go to the workspace as (O, m, sum), and the last CTA to arrive joins them in
+// the order of the ranges, so that results do not depend on the timing.
+//
+// Warps: 0-7 softmax (warp w reads lanes 32 (w % 4) ..), 8 producer (TMA, one box a
+// page), 9 MMA issuer and owner of the tensor memory, 10-17 (e4m3 cache) convert
+// codes to bf16 between a staging ring and the operand ring; the scales of
+// keys enter S, those of values enter P, in fp32.
+
+constexpr int kConvWarps = 8;
+constexpr int kSoftWarps = 8;
+constexpr int kProducer = 8, kIssuer = 9;
+constexpr int kMaxCtas = 152;
+constexpr int kScaleSlots = 8;
+constexpr float kLazy = 8.0f;   // growth of the maximum (powers of two) before O is rescaled
+
+struct TcArgs {
+  Args a;
+  int rows, rpt;        // rows a key/value head (T G); rows of a Q tile
+  int parts_per_item;   // CTAs of a group: Q tiles (or pairs of them) of an item
+  int groups;           // ranges of the line of tiles
+  int box;              // keys of one TMA box: min(page, KT)
+  float c;              // |scale| log2 e, or 1 for a scale of 0
+  unsigned qflip;       // sign bits to flip in Q (a negative scale)
+  int qzero;            // a scale of 0: Q counts as 0
+  unsigned* counters;   // [groups parts_per_item]: parts that have arrived
+  float* part_o;        // [groups parts_per_item 2][rows of a CTA][D]
+  float2* part_ml;      // [groups parts_per_item 2][rows of a CTA]
+};
+
+template <int DP, bool F8, bool SHARED>
+struct Cfg {
+  static constexpr int KT = DP == 256 ? 64 : 128;
+  static constexpr int NS = DP == 256 ? 1 : 2;
+  static constexpr int NQ = SHARED ? 2 : 1;
+  static constexpr int kQBytes = 128 * DP * 2;
+  static constexpr int kSlot = KT * DP * 2;
+  static constexpr int kStage = KT * DP;
+  static constexpr int kBudget = 219 * 1024;
+  static constexpr int kStages = F8 ? 4 : 0;
+  static constexpr int kFit = (kBudget - NQ * kQBytes - kStages * kStage - (F8 ? kScaleSlots * 2 * KT * 4 : 0)) / kSlot;
+  static constexpr int kSlots = kFit < 8 ? kFit : 8;
+  static constexpr bool kAlternate = NS == 2 && !SHARED;
+  static constexpr int kThreads = 32 * (10 + (F8 ? kConvWarps : 0));
+  static constexpr unsigned kS0 = 0, kS1 = 128, kO0 = NS == 2 ? 256 : 128, kO1 = 256 + DP;
+};
+
+struct TcTail {
+  unsigned long long full[8], empty[8];
+  unsigned long long sfull[4], sempty[4];
+  unsigned long long scale[kScaleSlots];
+  unsigned long long q_ready, s_ready[2], p_ready[2], pv_done[2];
+  unsigned long long wg_sync[2], all_sync;  // barriers of a warpgroup, and of all softmax warps
+  unsigned tmem_base, abort, bad[2], badv[2], last;
+  int b0;
+  long long lo, hi, base0, total;
+  int groups;
+  int par[2][2][kTreeMax];
+  float2 ml[2][128];
+};
+
+template <int DP, bool F8, bool SHARED>
+constexpr int tc_smem() {
+  using C = Cfg<DP, F8, SHARED>;
+  return 1024 + C::NQ * C::kQBytes + C::kSlots * C::kSlot + C::kStages * C::kStage +
+         (F8 ? kScaleSlots * 2 * C::KT * 4 : 0) + (int)sizeof(TcTail);
+}
+
+SV_DEVINL void bar_arrive(unsigned bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+SV_DEVINL bool bar_wait(unsigned bar, unsigned parity, volatile unsigned* abort, unsigned* status) {
+  if (mbar_test_parity(bar, parity)) return true;
+  const uint64_t t0 = global_ns();
+  for (unsigned i = 1;; ++i) {
+    if (mbar_test_parity(bar, parity)) return true;
+    if ((i & 255) == 0) {
+      if (*abort) return false;
+      if (global_ns() - t0 > kWaitLimitNs) {
+        atomicOr(status, (unsigned)SV_DEV_TIMEOUT);
+        *abort = 1;
+        return false;
+      }
+    }
+  }
+}
+
+SV_DEVINL void tma_4d(unsigned dst, const CUtensorMap* map, int x, int y, int z, int w, unsigned bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
+
+// Descriptors of shared-memory operands in 128-byte swizzle atoms (8 rows of 128
+// bytes): rows of 64 values along K (Q and K), or rows of 64 values along N (V,
+// whose rows are the K of its product; `lead` bytes to the next 64 of N).
+SV_DEVINL uint64_t desc_k(unsigned addr) {
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+SV_DEVINL uint64_t desc_n(unsigned addr, unsigned lead) {
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)((lead >> 4) & 0x3FFFu) << 16) |
+         ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+// kind::f16, fp32 accumulator, bf16 operands, M = 128; B along N when `nmajor`.
+SV_DEVINL uint32_t idesc(int n, bool nmajor) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((nmajor ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
+         (8u << 24);
+}
+
+SV_DEVINL void mma_ss(unsigned d, uint64_t a, uint64_t b, uint32_t id, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"((unsigned)acc)
+      : "memory");
+}
+SV_DEVINL void mma_ts(unsigned d, unsigned a, uint64_t b, uint32_t id, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(id), "r"((unsigned)acc)
+      : "memory");
+}
+SV_DEVINL void commit(unsigned bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+               : "memory");
+}
+SV_DEVINL void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+SV_DEVINL void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+SV_DEVINL void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+SV_DEVINL void tmem_ld32(unsigned t, float (&v)[32]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+      "%30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(t));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+SV_DEVINL void tmem_ld8(unsigned t, float (&v)[8]) {
+  uint32_t r[8];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+                 "=r"(r[7])
+               : "r"(t));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+SV_DEVINL void tmem_st16(unsigned t, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16};" ::"r"(t),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+SV_DEVINL void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Barrier of some warps on an mbarrier (one arrival a warp), bounded like every
+// wait: a warp that gave up must not leave the others waiting.
+SV_DEVINL bool warps_sync(unsigned bar, unsigned& phase, int lane, volatile unsigned* abort, unsigned* status) {
+  __syncwarp();
+  if (lane == 0) bar_arrive(bar);
+  const bool ok = __all_sync(0xffffffffu, bar_wait(bar, phase & 1, abort, status));
+  ++phase;
+  return ok;
+}
+
+// Tiles of a sequence; a context outside its page table counts as one tile.
+SV_DEVINL bool ctx_ok(const Args& a, int ctx) { return ctx >= 0 && (long long)ctx <= (long long)a.max_pages * a.P; }
+template <int KT>
+SV_DEVINL int tiles_of(const Args& a, int ctx) {
+  return ctx_ok(a, ctx) ? (int)(((long long)ctx + a.T + KT - 1) / KT) : 1;
+}
+
+// A CTA's way along its range: the item (b, hk), its tile count, context and the
+// tiles [t0, t1) of it that lie in the range.
+template <int KT>
+struct Walk {
+  int b, hk, n, ctx, t0, t1;
+  long long base, pos, hi;  // the line's index of the item's first tile, of t0, of the range's end
+  SV_DEVINL void start(const Args& a, const TcTail& t) {
+    b = t.b0;
+    pos = t.lo;
+    hi = t.hi;
+    if (pos >= hi) return;
+    ctx = a.ctx_lens[b];
+    n = tiles_of<KT>(a, ctx);
+    const long long rem = pos - t.base0;
+    hk = (int)(rem / n);
+    t0 = (int)(rem - (long long)hk * n);
+    base = pos - t0;
+    clip();
+  }
+  SV_DEVINL void clip() { t1 = (int)((long long)n < t0 + (hi - pos) ? (long long)n : t0 + (hi - pos)); }
+  SV_DEVINL bool more() const { return pos < hi; }
+  SV_DEVINL void next(const Args& a) {
+    pos += t1 - t0;
+    if (pos >= hi) return;
+    if (++hk == a.Hkv) {
+      hk = 0;
+      ctx = a.ctx_lens[++b];
+      n = tiles_of<KT>(a, ctx);
+    }
+    t0 = 0;
+    base = pos;
+    clip();
+  }
+};
+
+// Place of tile i's keys and values in the order of the operand ring.
+template <bool ALT>
+SV_DEVINL unsigned k_entry(int i) { return ALT ? (i == 0 ? 0u : 2u * i - 1u) : 2u * i; }
+template <bool ALT>
+SV_DEVINL unsigned v_entry(int i, int n) { return ALT ? (i == n - 1 ? 2u * n - 1u : 2u * i + 2u) : 2u * i + 1u; }
+
+// Two e4m3 codes in the high bytes of the halves of x -> bf16 pair: the code's
+// exponent and mantissa moved into bf16's place are its value times 2^-120
+// (subnormals too), which the product undoes exactly. (0x7f, NaN, reads as 480:
+// rows with NaN carry it in their scale.)
+SV_DEVINL uint32_t e4m3_to_bf16(uint32_t x) {
+  const uint32_t y = ((x >> 4) & 0x07f007f0u) | (x & 0x80008000u);
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(y), "r"(0x7b807b80u));
+  return r;
+}
+
+template <int DP, bool F8, bool SHARED>
+__global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
+    tree_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                     const __grid_constant__ TcArgs x) {
+  using C = Cfg<DP, F8, SHARED>;
+  constexpr int KT = C::KT, NS = C::NS;
+  constexpr bool ALT = C::kAlternate;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                         ~static_cast<uintptr_t>(1023));
+  unsigned char* ring = smem + C::NQ * C::kQBytes;
+  unsigned char* stage = ring + C::kSlots * C::kSlot;
+  float* scales = reinterpret_cast<float*>(stage + C::kStages * C::kStage);  // [kScaleSlots][2][KT]
+  TcTail& t = *reinterpret_cast<TcTail*>(reinterpret_cast<unsigned char*>(scales) +
+                                         (F8 ? kScaleSlots * 2 * KT * 4 : 0));
+  const Args& a = x.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int group = blockIdx.x / x.parts_per_item, part = blockIdx.x % x.parts_per_item;
+  constexpr int kSoft = NS * 4;  // softmax warps at work
+
+  if (warp == 0) {  // this CTA's range, from the lengths
+    long long total = 0;
+    for (int b = lane; b < a.B; b += 32) total += (long long)tiles_of<KT>(a, a.ctx_lens[b]) * a.Hkv;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    const int groups = (int)min((long long)x.groups, total);
+    const long long lo = group < groups ? (long long)group * total / groups : 0;
+    const long long hi = group < groups ? (long long)(group + 1) * total / groups : 0;
+    long long before = 0;
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+      const long long n = b0 + lane < a.B ? (long long)tiles_of<KT>(a, a.ctx_lens[b0 + lane]) * a.Hkv : 0;
+      long long incl = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      const bool mine = lo >= before + incl - n && lo < before + incl;
+      if (mine) {
+        t.b0 = b0 + lane;
+        t.base0 = before + incl - n;
+      }
+      if (__any_sync(0xffffffffu, mine)) break;
+      before += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) {
+      t.lo = lo;
+      t.hi = hi;
+      t.total = total;
+      t.groups = groups;
+    }
+  } else if (warp == kProducer && lane == 0) {
+    for (int i = 0; i < C::kSlots; ++i) {
+      mbar_init(smem_u32(&t.full[i]), F8 ? kConvWarps : 1);
+      mbar_init(smem_u32(&t.empty[i]), 1);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(smem_u32(&t.sfull[i]), 1);
+      mbar_init(smem_u32(&t.sempty[i]), kConvWarps);
+    }
+    for (int i = 0; i < kScaleSlots; ++i) mbar_init(smem_u32(&t.scale[i]), 1);
+    mbar_init(smem_u32(&t.q_ready), kSoft);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&t.s_ready[i]), 1);
+      mbar_init(smem_u32(&t.p_ready[i]), 4);
+      mbar_init(smem_u32(&t.pv_done[i]), 1);
+      mbar_init(smem_u32(&t.wg_sync[i]), 4);
+    }
+    mbar_init(smem_u32(&t.all_sync), kSoft);
+    t.abort = 0;
+    t.bad[0] = t.bad[1] = t.badv[0] = t.badv[1] = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  } else if (warp == kIssuer) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(&t.tmem_base)),
+                 "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const unsigned tmem = t.tmem_base;
+  volatile unsigned* abort = &t.abort;
+  Walk<KT> w;
+  w.start(a, t);
+
+  if (warp == kProducer) {
+    // ---- TMA: entry by entry, a lane a page
+    unsigned entry = 0, tile_no = 0;
+    bool ok = true;
+    for (; w.more() && ok; w.next(a)) {
+      const int n = w.t1 - w.t0;
+      int live = a.T;  // nodes up to the last that is not padding
+      if (a.parents && (long long)w.t1 * KT > w.ctx) {
+        live = 0;
+        for (int i = lane; i < a.T; i += 32)
+          if (a.parents[(long long)w.b * a.T + i] != -2) live = i + 1;
+        live = __reduce_max_sync(0xffffffffu, live);
+      }
+      const bool seq_ok = ctx_ok(a, w.ctx);
+      for (int e = 0; e < 2 * n && ok; ++e, ++entry) {
+        bool isv;
+        int i;
+        if (ALT) {
+          isv = e == 2 * n - 1 || (e >= 2 && (e & 1) == 0);
+          i = isv ? (e == 2 * n - 1 ? n - 1 : e / 2 - 1) : (e + 1) / 2;
+        } else {
+          isv = e & 1;
+          i = e >> 1;
+        }
+        const int tile = w.t0 + i;
+        const int boxes = KT / x.box;
+        const int pos = tile * KT + lane * x.box;
+        int page = -1;
+        if (seq_ok && lane < boxes && pos < w.ctx + live && pos / a.P < a.max_pages)
+          page = a.page_table[(long long)w.b * a.max_pages + pos / a.P];
+        if (page < 0 || page >= a.num_pages) page = -1;
+        const unsigned hit = __ballot_sync(0xffffffffu, page >= 0);
+        const int y = pos % a.P;
+        unsigned bar;
+        unsigned char* dst;
+        unsigned limit_ok;
+        if (F8) {
+          const int s = (int)(entry % 4);
+          limit_ok = entry < 4 || bar_wait(smem_u32(&t.sempty[s]), ((entry / 4) & 1) ^ 1, abort, a.status);
+          bar = smem_u32(&t.sfull[s]);
+          dst = stage + s * C::kStage;
+        } else {
+          const int s = (int)(entry % C::kSlots);
+          limit_ok = entry < (unsigned)C::kSlots ||
+                     bar_wait(smem_u32(&t.empty[s]), ((entry / C::kSlots) & 1) ^ 1, abort, a.status);
+          bar = smem_u32(&t.full[s]);
+          dst = ring + s * C::kSlot;
+        }
+        ok = __all_sync(0xffffffffu, limit_ok);
+        if (!ok) break;
+        const unsigned sbar = smem_u32(&t.scale[tile_no % kScaleSlots]);
+        if (lane == 0) {
+          // The TMA box counts whole: columns past D arrive as zeros.
+          mbar_arrive_expect_tx(bar, (unsigned)__popc(hit) * x.box * DP * (F8 ? 1 : 2));
+          if (F8 && !isv) mbar_arrive_expect_tx(sbar, (unsigned)__popc(hit) * x.box * 4 * 2);
+        }
+        __syncwarp();
+        if (page >= 0) {
+          const CUtensorMap* map = isv ? &map_v : &map_k;
+          if (F8) {
+            tma_4d(smem_u32(dst) + lane * x.box * DP, map, 0, y, w.hk, page, bar);
+            if (!isv) {
+              float* sc = scales + (tile_no % kScaleSlots) * 2 * KT + lane * x.box;
+              const long long r = ((long long)page * a.Hkv + w.hk) * a.P + y;
+              bulk_copy_g2s(smem_u32(sc), a.ks + r, x.box * 4, sbar);
+              bulk_copy_g2s(smem_u32(sc + KT), a.vs + r, x.box * 4, sbar);
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < DP / 64; ++k)
+              tma_4d(smem_u32(dst) + k * KT * 128 + lane * x.box * 128, map, k * 64, y, w.hk, page, bar);
+          }
+        }
+        if (!isv) ++tile_no;
+      }
+    }
+    if (*abort) {  // copies in flight must land before the shared memory goes
+      for (int i = 0; i < (F8 ? 4 : C::kSlots); ++i) {
+        const unsigned held = F8 ? 4u : (unsigned)C::kSlots;
+        if (entry < (unsigned)i + 1) break;
+        const unsigned e = entry - 1 - i;
+        const unsigned bar = F8 ? smem_u32(&t.sfull[e % held]) : smem_u32(&t.full[e % held]);
+        const uint64_t t0 = global_ns();
+        while (!mbar_test_parity(bar, (e / held) & 1) && global_ns() - t0 < 1000000) {
+        }
+      }
+    }
+  } else if (warp == kIssuer) {
+    // ---- MMA
+    if (lane == 0) {
+      const uint32_t id_qk = idesc(KT, false), id_pv = idesc(a.D, true);
+      const int ksteps = a.D / 16;
+      unsigned entry0 = 0, item = 0;
+      unsigned pcount[2] = {0, 0};   // P's awaited, by stream
+      bool ok = true;
+      auto full = [&](unsigned e) {
+        ok = ok && bar_wait(smem_u32(&t.full[e % C::kSlots]), (e / C::kSlots) & 1, abort, a.status);
+        if (ok) fence_after();
+        return ok;
+      };
+      auto qk = [&](int s, unsigned e) {
+        // S of this stream holds the last P until its product is complete.
+        if (pcount[s] > 0)
+          ok = ok && bar_wait(smem_u32(&t.pv_done[s]), (pcount[s] - 1) & 1, abort, a.status);
+        if (!ok) return;
+        fence_after();
+        const unsigned q = smem_u32(smem + (SHARED ? s * C::kQBytes : 0));
+        const unsigned k = smem_u32(ring + (e % C::kSlots) * C::kSlot);
+        const unsigned d = tmem + (s ? C::kS1 : C::kS0);
+        for (int i = 0; i < ksteps; ++i)
+          mma_ss(d, desc_k(q + (i >> 2) * 128 * 128 + (i & 3) * 32),
+                 desc_k(k + (i >> 2) * KT * 128 + (i & 3) * 32), id_qk, i > 0);
+      };
+      auto pv = [&](int s, unsigned e, bool acc) {
+        const unsigned v = smem_u32(ring + (e % C::kSlots) * C::kSlot);
+        const unsigned p = tmem + (s ? C::kS1 : C::kS0), d = tmem + (s ? C::kO1 : C::kO0);
+#pragma unroll
+        for (int i = 0; i < KT / 16; ++i)
+          mma_ts(d, p + i * 8, desc_n(v + i * 2048, KT * 128), id_pv, acc || i > 0);
+      };
+      auto p_wait = [&](int s) {
+        ok = ok && bar_wait(smem_u32(&t.p_ready[s]), pcount[s] & 1, abort, a.status);
+        if (ok) fence_after();
+        ++pcount[s];
+        return ok;
+      };
+      auto release = [&](unsigned e) { commit(smem_u32(&t.empty[e % C::kSlots])); };
+      for (; w.more() && ok; w.next(a), ++item) {
+        const int n = w.t1 - w.t0;
+        ok = ok && bar_wait(smem_u32(&t.q_ready), item & 1, abort, a.status);
+        if (!ok) break;
+        fence_after();
+        if (ALT) {
+          for (int i = 0; i < 2 && i < n; ++i) {
+            const unsigned e = entry0 + k_entry<true>(i);
+            if (!full(e)) break;
+            qk(i, e);
+            if (!ok) break;
+            release(e);
+            commit(smem_u32(&t.s_ready[i]));
+          }
+          for (int i = 0; i < n && ok; ++i) {
+            const int s = i & 1;
+            const unsigned ev = entry0 + v_entry<true>(i, n);
+            if (!full(ev) || !p_wait(s)) break;
+            pv(s, ev, i >= 2);
+            release(ev);
+            commit(smem_u32(&t.pv_done[s]));
+            if (i + 2 < n) {
+              const unsigned e = entry0 + k_entry<true>(i + 2);
+              if (!full(e)) break;
+              qk(s, e);
+              if (!ok) break;
+              release(e);
+              commit(smem_u32(&t.s_ready[s]));
+            }
+          }
+        } else {
+          for (int i = -1; i < n && ok; ++i) {
+            for (int s = 0; s < NS && ok; ++s) {
+              if (i >= 0) {
+                const unsigned ev = entry0 + 2u * i + 1u;
+                if (!full(ev) || !p_wait(s)) break;
+                pv(s, ev, i > 0);
+                if (s == NS - 1) release(ev);
+                commit(smem_u32(&t.pv_done[s]));
+              }
+              if (i + 1 < n) {
+                const unsigned e = entry0 + 2u * (i + 1);
+                if (!full(e)) break;
+                qk(s, e);
+                if (!ok) break;
+                if (s == NS - 1) release(e);
+                commit(smem_u32(&t.s_ready[s]));
+              }
+            }
+          }
+        }
+        entry0 += 2u * n;
+      }
+    }
+  } else if (warp < kSoft) {
+    // ---- softmax, one thread a row
+    const int s = warp >> 2;           // stream
+    const int wt = threadIdx.x & 127;  // thread of the warpgroup: its row, and a key row of V
+    const int q = warp & 3;
+    const unsigned lanes = (unsigned)(q * 32) << 16;
+    const unsigned sbase = tmem + (s ? C::kS1 : C::kS0) + lanes;
+    const unsigned obase = tmem + (s ? C::kO1 : C::kO0) + lanes;
+    const int G = a.Hq / a.Hkv;
+    const int tile_rows = x.rpt;
+    const int row0 = (SHARED ? part * 2 + s : part) * tile_rows;  // first row of this thread's Q tile
+    const int nrows = max(0, min(tile_rows, x.rows - row0));
+    const int row = row0 + wt;
+    const bool have = wt < nrows;
+    const bool busy = q * 32 < nrows;  // the warp has rows
+    const int node = have ? row / G : 0;
+    const float c = x.c, grow = kLazy / c;
+    unsigned item = 0, tile_no = 0, scount = 0, entry0 = 0, wg_phase = 0, all_phase = 0;
+    bool ok = true;
+    for (; w.more() && ok; w.next(a), ++item) {
+      const int n = w.t1 - w.t0;
+      const bool seq_ok = ctx_ok(a, w.ctx);
+      const bool tail = seq_ok && (long long)w.t1 * KT > w.ctx;
+      // Q into shared memory, 16 bytes a thread and step.
+      {
+        const int units = a.D / 8;
+        constexpr int kLoaders = SHARED ? 128 : NS * 128;
+        const int first = SHARED ? wt : threadIdx.x;
+        unsigned char* qs = smem + (SHARED ? s * C::kQBytes : 0);
+        for (int i = first; i < 128 * units; i += kLoaders) {
+          const int r = i / units, u = i - r * units;
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (r < nrows && !x.qzero) {
+            const int qr = row0 + r;
+            v = *reinterpret_cast<const uint4*>(a.q + w.b * a.q_sb + (long long)(qr / G) * a.q_st +
+                                                (long long)(w.hk * G + qr % G) * a.q_sh + u * 8);
+            v.x ^= x.qflip;
+            v.y ^= x.qflip;
+            v.z ^= x.qflip;
+            v.w ^= x.qflip;
+          }
+          *reinterpret_cast<uint4*>(qs + (u >> 3) * 16384 + r * 128 + (((u & 7) ^ (r & 7)) << 4)) = v;
+        }
+        fence_async();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(smem_u32(&t.q_ready));
+      }
+      // The tree and the pages, while the first keys are on their way.
+      unsigned anc[4] = {};
+      int* par = t.par[item & 1][s];
+      {
+        unsigned bad = seq_ok ? 0u : (unsigned)SV_DEV_PAGE_RANGE;
+        if (tail) {
+          if (wt < a.T) par[wt] = a.parents ? a.parents[(long long)w.b * a.T + wt] : wt - 1;
+          ok = warps_sync(smem_u32(&t.wg_sync[s]), wg_phase, lane, abort, a.status);
+          if (!ok) break;
+          if (wt < a.T) {
+            const int p = par[wt];
+            if (p < -2 || p >= wt || (p >= 0 && par[p] == -2)) bad |= SV_DEV_TREE;
+          }
+          if (have) {
+            for (int j = node, left = a.T; j >= 0 && left > 0; --left) {
+              const int p = par[j];
+              if (p == -2) break;
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (k == j >> 5) anc[k] |= 1u << (j & 31);
+              j = p < j ? p : -1;
+            }
+          }
+        }
+        if (seq_ok && s == 0) {
+          const int p0 = (int)((long long)w.t0 * KT / a.P);
+          const int p1 = (int)min(((long long)w.t1 * KT + a.P - 1) / a.P, ((long long)w.ctx + a.T + a.P - 1) / a.P);
+          for (int p = p0 + wt; p < p1; p += 128) {
+            bool used = (long long)p * a.P < w.ctx;
+            if (!used) {
+              const int j1 = min((long long)a.T, (long long)(p + 1) * a.P - w.ctx);
+              for (int j = max(0, p * a.P - w.ctx); j < j1 && !used; ++j) used = par[j] != -2;
+            }
+            if (!used) continue;
+            const int id = p < a.max_pages ? a.page_table[(long long)w.b * a.max_pages + p] : -1;
+            if (id < 0 || id >= a.num_pages) bad |= SV_DEV_PAGE_RANGE;
+          }
+        }
+        if (bad) {
+          atomicOr(&t.bad[item & 1], 1u);
+          atomicOr(a.status, bad);
+        }
+      }
+
+      float m = -INFINITY, sum = 0.0f;
+      bool any = false;  // this stream has tiles of the item
+      for (int i = ALT ? s : 0; i < n; i += ALT ? 2 : 1) {
+        const int tile = w.t0 + i;
+        const bool edge = (long long)(tile + 1) * KT > w.ctx || !seq_ok;
+        ok = __all_sync(0xffffffffu, bar_wait(smem_u32(&t.s_ready[s]), scount & 1, abort, a.status));
+        const float* ksc = scales + ((tile_no + i) % kScaleSlots) * 2 * KT;
+        if (F8)
+          ok = __all_sync(0xffffffffu,
+                          ok && bar_wait(smem_u32(&t.scale[(tile_no + i) % kScaleSlots]),
+                                         ((tile_no + i) / kScaleSlots) & 1, abort, a.status));
+        if (!ok) break;
+        fence_after();
+        if (busy) {
+          // Which of 32 columns from `col` on the row attends: context, then
+          // ancestors; nothing in a sequence at fault.
+          auto seen = [&](int col) -> unsigned {
+            if (!seq_ok) return 0u;
+            const long long n0 = (long long)tile * KT + col - w.ctx;
+            if (n0 <= -32) return 0xffffffffu;
+            if (n0 >= kTreeMax) return 0u;
+            const int k = (int)(n0 >> 5), sh = (int)(n0 & 31);
+            const unsigned lo = k < 0 ? 0xffffffffu : k == 0 ? anc[0] : k == 1 ? anc[1] : k == 2 ? anc[2] : anc[3];
+            const unsigned hi = k < 0 ? anc[0] : k == 0 ? anc[1] : k == 1 ? anc[2] : k == 2 ? anc[3] : 0u;
+            return __funnelshift_r(lo, hi, sh);
+          };
+          float top = -INFINITY;
+#pragma unroll 1
+          for (int col = 0; col < KT; col += 32) {
+            float v[32];
+            tmem_ld32(sbase + col, v);
+            if (F8) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] *= ksc[col + j];
+            }
+            if (edge) {
+              const unsigned see = seen(col);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = see >> j & 1u ? v[j] : -INFINITY;
+            }
+#pragma unroll
+            for (int j = 0; j < 32; ++j) top = fmaxf(top, v[j]);
+          }
+          const bool raise = top > m + grow || (m == -INFINITY && top > m);
+          if (__any_sync(0xffffffffu, raise)) {
+            const float nm = raise ? top : m;
+            const float f = raise ? (m == -INFINITY ? 0.0f : ex2_fast((m - nm) * c)) : 1.0f;
+            if (any) {
+              ok = __all_sync(0xffffffffu,
+                              bar_wait(smem_u32(&t.pv_done[s]), (scount - 1) & 1, abort, a.status));
+              if (!ok) break;
+              fence_after();
+#pragma unroll 1
+              for (int col = 0; col < a.D; col += 16) {
+                float v0[8], v1[8];
+                uint32_t r[16];
+                tmem_ld8(obase + col, v0);
+                tmem_ld8(obase + col + 8, v1);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                  r[j] = __float_as_uint(v0[j] * f);
+                  r[j + 8] = __float_as_uint(v1[j] * f);
+                }
+                tmem_st16(obase + col, r);
+              }
+            }
+            sum *= f;
+            m = nm;
+          }
+          const float mc = m == -INFINITY ? 0.0f : m * c;
+          float part_sum = 0.0f;
+#pragma unroll 1
+          for (int col = 0; col < KT; col += 32) {
+            float v[32];
+            tmem_ld32(sbase + col, v);
+            const unsigned see = edge ? seen(col) : 0xffffffffu;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              float y = v[j];
+              if (F8) y *= ksc[col + j];
+              y = ex2_fast(__fmaf_rn(y, c, -mc));
+              if (edge) y = see >> j & 1u ? y : 0.0f;
+              part_sum += y;
+              if (F8) {
+                y *= ksc[KT + col + j];
+                if (edge) y = see >> j & 1u ? y : 0.0f;
+              }
+              v[j] = y;
+            }
+            uint32_t r[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+              r[j] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+            tmem_st16(sbase + col / 2, r);
+          }
+          sum += part_sum;
+          tmem_wait_st();
+        }
+        // Values that no row, or not every row, may use: 0 times what lies there
+        // must be 0. Dead rows are zeroed; a node's NaN or infinity is taken out
+        // and given to its descendants at the end.
+        if (!F8 && edge && (!SHARED || s == 0)) {
+          const unsigned ev = entry0 + v_entry<ALT>(i, n);
+          ok = __all_sync(0xffffffffu, bar_wait(smem_u32(&t.full[ev % C::kSlots]), (ev / C::kSlots) & 1, abort,
+                                                a.status));
+          if (!ok) break;
+          const long long nd = (long long)tile * KT + wt - w.ctx;
+          if (wt < KT && (nd >= 0 || !seq_ok)) {
+            unsigned char* vrow = ring + (ev % C::kSlots) * C::kSlot + wt * 128;
+            const bool dead = !seq_ok || nd >= a.T || par[nd] == -2;
+            for (int u = 0; u < DP / 8; ++u) {
+              uint4* at = reinterpret_cast<uint4*>(vrow + (u >> 3) * KT * 128 + (((u & 7) ^ (wt & 7)) << 4));
+              uint4 v = dead ? make_uint4(0, 0, 0, 0) : *at;
+              uint32_t z[4] = {v.x, v.y, v.z, v.w};
+              bool found = dead;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                if ((z[j] & 0x7f80u) == 0x7f80u) z[j] &= 0xffff0000u, found = true, t.badv[item & 1] = 1;
+                if ((z[j] & 0x7f800000u) == 0x7f800000u) z[j] &= 0x0000ffffu, found = true, t.badv[item & 1] = 1;
+              }
+              if (found) *at = make_uint4(z[0], z[1], z[2], z[3]);
+            }
+          }
+          fence_async();
+        }
+        any = true;
+        ++scount;
+        fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(smem_u32(&t.p_ready[s]));
+      }
+      if (!ok) break;
+      tile_no += n;
+      entry0 += 2u * n;
+
+      // ---- the item's end: the streams' results joined, written or stored as a part
+      if (any) {
+        ok = __all_sync(0xffffffffu, bar_wait(smem_u32(&t.pv_done[s]), (scount - 1) & 1, abort, a.status));
+        if (!ok) break;
+      }
+      t.ml[s][wt] = make_float2(any ? m : -INFINITY, any ? sum : 0.0f);
+      fence_before();
+      ok = warps_sync(smem_u32(&t.all_sync), all_phase, lane, abort, a.status);
+      if (!ok) break;
+      fence_after();
+      const bool bad = t.bad[item & 1] != 0;
+      const bool badv = t.badv[item & 1] != 0;
+      if (threadIdx.x == 0) t.bad[(item + 1) & 1] = t.badv[(item + 1) & 1] = 0;
+      float f0 = 1.0f, f1 = 0.0f;
+      if (ALT) {
+        const float2 p0 = t.ml[0][wt], p1 = t.ml[1][wt];
+        m = fmaxf(p0.x, p1.x);
+        f0 = p0.x == -INFINITY ? 0.0f : ex2_fast((p0.x - m) * c);
+        f1 = p1.x == -INFINITY ? 0.0f : ex2_fast((p1.x - m) * c);
+        sum = p0.y * f0 + p1.y * f1;
+      }
+      if (bad) m = __int_as_float(0x7fc00000);
+      const bool whole = w.t0 == 0 && w.t1 == w.n;
+      const int cols = ALT ? a.D / 2 : a.D, col0 = ALT ? s * cols : 0;
+      const int cta_rows = SHARED ? 2 * tile_rows : tile_rows;
+      const int prow = SHARED ? s * tile_rows + wt : wt;
+      const long long slot = ((long long)(group * x.parts_per_item + part) * 2 + (w.t0 == 0 ? 1 : 0));
+      float* po = x.part_o + (slot * cta_rows + prow) * a.D;
+      const bool dead = have && a.parents && a.parents[(long long)w.b * a.T + node] == -2;
+      const float inv = bad ? m : sum == 0.0f || dead ? 0.0f : 1.0f / sum;
+      __nv_bfloat16* out = a.out + (((long long)w.b * a.T + node) * a.Hq + w.hk * G + row % G) * a.D;
+      if (busy) {
+        for (int col = col0; col < col0 + cols; col += 8) {
+          float v[8];
+          tmem_ld8(tmem + lanes + C::kO0 + (SHARED && s ? DP : 0) + col, v);
+          if (ALT) {
+            float u[8];
+            tmem_ld8(tmem + lanes + C::kO1 + col, u);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              v[j] = (f0 > 0.0f || isnan(f0) ? v[j] * f0 : 0.0f) + (f1 > 0.0f || isnan(f1) ? u[j] * f1 : 0.0f);
+          }
+          if (badv && have) {  // NaN and infinities of the nodes this row attends
+            for (int nd = 0; nd < a.T; ++nd) {
+              const long long pos = (long long)w.ctx + nd;
+              if (pos < (long long)w.t0 * KT || pos >= (long long)w.t1 * KT) continue;
+              unsigned word = anc[0];
+#pragma unroll
+              for (int k = 1; k < 4; ++k)
+                if (k == nd >> 5) word = anc[k];
+              if (!(word >> (nd & 31) & 1u) || pos / a.P >= a.max_pages) continue;
+              const int id = a.page_table[(long long)w.b * a.max_pages + pos / a.P];
+              if (id < 0 || id >= a.num_pages) continue;
+              const __nv_bfloat16* vr = static_cast<const __nv_bfloat16*>(a.vc) +
+                                        (((long long)id * a.Hkv + w.hk) * a.P + pos % a.P) * a.D + col;
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const float y = __bfloat162float(vr[j]);
+                if (!isfinite(y)) v[j] += y;
+              }
+            }
+          }
+          if (!have) continue;
+          if (whole) {
+            uint4 o;
+            uint32_t r[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const __nv_bfloat162 h = __floats2bfloat162_rn(inv == 0.0f ? 0.0f : v[2 * j] * inv,
+                                                             inv == 0.0f ? 0.0f : v[2 * j + 1] * inv);
+              r[j] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+            o = make_uint4(r[0], r[1], r[2], r[3]);
+            *reinterpret_cast<uint4*>(out + col) = o;
+          } else {
+            *reinterpret_cast<float4*>(po + col) = make_float4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<float4*>(po + col + 4) = make_float4(v[4], v[5], v[6], v[7]);
+          }
+        }
+        if (!whole && have && (!ALT || s == 0)) x.part_ml[slot * cta_rows + prow] = make_float2(m, sum);
+      }
+      if (!whole) {
+        // The last part to arrive joins them all, in the order of the ranges.
+        const long long total = t.total;
+        const int ng = t.groups;
+        const int gs = (int)(((w.base + 1) * ng - 1) / total), ge = (int)(((w.base + w.n) * ng - 1) / total);
+        __threadfence();
+        ok = warps_sync(smem_u32(&t.all_sync), all_phase, lane, abort, a.status);
+        if (!ok) break;
+        if (threadIdx.x == 0)
+          t.last = atomicAdd(&x.counters[gs * x.parts_per_item + part], 1u) == (unsigned)(ge - gs);
+        ok = warps_sync(smem_u32(&t.all_sync), all_phase, lane, abort, a.status);
+        if (!ok) break;
+        if (t.last) {
+          __threadfence();
+          const int units = a.D / 4;
+          const int rows_here = SHARED ? cta_rows : nrows;
+          for (int i = threadIdx.x; i < rows_here * units; i += NS * 128) {
+            const int r = i / units, u = i - r * units;
+            const int gr = part * cta_rows + r;
+            if (gr >= x.rows) continue;
+            float top = -INFINITY;
+            bool poison = false;
+            for (int g = gs; g <= ge; ++g) {
+              const long long sl = (long long)(g * x.parts_per_item + part) * 2 + (g == gs ? 1 : 0);
+              const float pm = __ldcg(&x.part_ml[sl * cta_rows + r]).x;
+              poison = poison || isnan(pm);
+              top = fmaxf(top, pm);
+            }
+            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            float l = 0.0f;
+            for (int g = gs; g <= ge; ++g) {
+              const long long sl = (long long)(g * x.parts_per_item + part) * 2 + (g == gs ? 1 : 0);
+              const float2 ml = __ldcg(&x.part_ml[sl * cta_rows + r]);
+              if (ml.x == -INFINITY) continue;
+              const float f = ex2_fast((ml.x - top) * c);
+              const float4 o = __ldcg(reinterpret_cast<const float4*>(x.part_o + (sl * cta_rows + r) * a.D) + u);
+              l = fmaf(ml.y, f, l);
+              acc.x = fmaf(o.x, f, acc.x);
+              acc.y = fmaf(o.y, f, acc.y);
+              acc.z = fmaf(o.z, f, acc.z);
+              acc.w = fmaf(o.w, f, acc.w);
+            }
+            const int nd = gr / G;
+            const bool gone = a.parents && a.parents[(long long)w.b * a.T + nd] == -2;
+            float inv_l = l == 0.0f || gone ? 0.0f : 1.0f / l;
+            if (poison) inv_l = __int_as_float(0x7fc00000);
+            if (inv_l == 0.0f) acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            const __nv_bfloat162 h0 = __floats2bfloat162_rn(acc.x * inv_l, acc.y * inv_l);
+            const __nv_bfloat162 h1 = __floats2bfloat162_rn(acc.z * inv_l, acc.w * inv_l);
+            uint2 o;
+            o.x = *reinterpret_cast<const uint32_t*>(&h0);
+            o.y = *reinterpret_cast<const uint32_t*>(&h1);
+            *reinterpret_cast<uint2*>(a.out + (((long long)w.b * a.T + nd) * a.Hq + w.hk * G + gr % G) * a.D +
+                                      u * 4) = o;
+          }
+        }
+      }
+    }
+  } else if (F8 && warp >= kIssuer + 1) {
+    // ---- codes to bf16: 16 of a row a thread and step
+    const int ct = threadIdx.x - 32 * (kIssuer + 1);
+    unsigned entry = 0;
+    bool ok = true;
+    for (; w.more() && ok; w.next(a)) {
+      const int n = w.t1 - w.t0;
+      for (int e = 0; e < 2 * n && ok; ++e, ++entry) {
+        const int st = (int)(entry % 4), sl = (int)(entry % C::kSlots);
+        ok = bar_wait(smem_u32(&t.sfull[st]), (entry / 4) & 1, abort, a.status);
+        if (ok && entry >= (unsigned)C::kSlots)
+          ok = bar_wait(smem_u32(&t.empty[sl]), ((entry / C::kSlots) & 1) ^ 1, abort, a.status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const unsigned char* src = stage + st * C::kStage;
+        unsigned char* dst = ring + sl * C::kSlot;
+        constexpr int kUnits = DP / 16;
+#pragma unroll 4
+        for (int i = ct; i < KT * kUnits; i += 32 * kConvWarps) {
+          const int r = i / kUnits, u = i % kUnits;
+          const uint4 v = *reinterpret_cast<const uint4*>(src + i * 16);
+          const uint32_t z[4] = {v.x, v.y, v.z, v.w};
+          uint32_t o[8];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            o[2 * j] = e4m3_to_bf16(__byte_perm(z[j], 0, 0x1404));
+            o[2 * j + 1] = e4m3_to_bf16(__byte_perm(z[j], 0, 0x3424));
+          }
+          unsigned char* base = dst + (u >> 2) * KT * 128 + r * 128;
+          const int u0 = (u & 3) * 2;
+          const bool odd = (u >> 2) & 1;  // odd blocks write their halves the other way round: no bank conflicts
+          const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
+          *reinterpret_cast<uint4*>(base + (((u0 + odd) ^ (r & 7)) << 4)) = odd ? hi : lo;
+          *reinterpret_cast<uint4*>(base + (((u0 + !odd) ^ (r & 7)) << 4)) = odd ? lo : hi;
+        }
+        fence_async();
+        __syncwarp();
+        if (lane == 0) {
+          bar_arrive(smem_u32(&t.full[sl]));
+          bar_arrive(smem_u32(&t.sempty[st]));
+        }
+      }
+    }
+  }
+  fence_before();
+  __syncthreads();
+  if (warp == kIssuer) {
+    __syncwarp();
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+  }
+}
 
 // ---------------------------------------------------------------- any shape
 //
@@ -167,8 +1123,110 @@ bool sizes_ok(int B, int T, int Hq, int Hkv, int D, int max_pages, int page_size
       D > kHeadDimMax || max_pages < 1 || page_size < 1)
     return false;
   // Positions are 32-bit, and so are the rows of a call.
-  return (long long)max_pages * page_size < (1ll << 31) - kTreeMax && (long long)B * T * Hq < (1ll << 31) &&
-         (long long)B * max_pages < (1ll << 40);
+  return (long long)max_pages * page_size < (1ll << 31) - 2 * kTreeMax &&
+         (long long)B * T * Hq < (1ll << 31) && (long long)B * max_pages < (1ll << 40);
+}
+
+// Shapes that the tensor-core kernel takes.
+bool tc_shape(int D, int page_size) {
+  return D % 16 == 0 && D <= 256 && (page_size == 16 || page_size == 32 || page_size == 64 || page_size == 128);
+}
+
+// How the rows of an item are cut: up to 128 in one Q tile; more in pairs of equal
+// tiles (D above 128: single tiles), a CTA each.
+struct Plan {
+  int rows, rpt, parts, groups, cta_rows, pad;
+  bool shared;
+  size_t off_counters, off_ml, off_o, total;
+};
+
+Plan make_plan(int T, int Hq, int Hkv, int D) {
+  Plan p{};
+  p.rows = T * (Hq / Hkv);
+  p.shared = D <= 128 && p.rows > 128;
+  if (p.shared) {
+    p.parts = (p.rows + 255) / 256;
+    p.rpt = (p.rows + 2 * p.parts - 1) / (2 * p.parts);
+    p.cta_rows = 2 * p.rpt;
+  } else {
+    p.parts = (p.rows + 127) / 128;
+    p.rpt = (p.rows + p.parts - 1) / p.parts;
+    p.cta_rows = p.rpt;
+  }
+  p.groups = std::max(1, kMaxCtas / p.parts);
+  const size_t slots = (size_t)p.groups * p.parts * 2;
+  size_t off = 256;
+  p.off_counters = off;
+  off = align_up(off + (size_t)p.groups * p.parts * 4, 256);
+  p.off_ml = off;
+  off = align_up(off + slots * p.cta_rows * sizeof(float2), 256);
+  p.off_o = off;
+  off = align_up(off + slots * p.cta_rows * (size_t)D * 4, 256);
+  p.total = off;
+  return p;
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  });
+  return fn;
+}
+
+// The cache as boxes of `box` tokens of one page and head: bf16 in columns of 64
+// with the 128-byte swizzle, codes in whole rows of DP.
+bool make_map(CUtensorMap* m, const void* base, const Args& a, bool f8, int dp, int box) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const size_t es = f8 ? 1 : 2;
+  const cuuint64_t dims[4] = {(cuuint64_t)a.D, (cuuint64_t)a.P, (cuuint64_t)a.Hkv, (cuuint64_t)a.num_pages};
+  const cuuint64_t strides[3] = {a.D * es, (cuuint64_t)a.P * a.D * es, (cuuint64_t)a.Hkv * a.P * a.D * es};
+  const cuuint32_t boxes[4] = {(cuuint32_t)(f8 ? dp : 64), (cuuint32_t)box, 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(m, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+            const_cast<void*>(base), dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            f8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int DP, bool F8, bool SHARED>
+int launch_tc(const TcArgs& x, cudaStream_t st) {
+  constexpr int kSmem = tc_smem<DP, F8, SHARED>();
+  static std::mutex mu;
+  static bool set[64] = {};
+  int device = 0;
+  if (cudaGetDevice(&device) != cudaSuccess || device < 0 || device >= 64) return SV_ERR_CUDA;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!set[device]) {
+      if (cudaFuncSetAttribute(tree_attn_kernel<DP, F8, SHARED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               kSmem) != cudaSuccess)
+        return SV_ERR_CUDA;
+      set[device] = true;
+    }
+  }
+  CUtensorMap mk, mv;
+  if (!make_map(&mk, x.a.kc, x.a, F8, DP, x.box) || !make_map(&mv, x.a.vc, x.a, F8, DP, x.box))
+    return SV_ERR_CUDA;
+  tree_attn_kernel<DP, F8, SHARED><<<(unsigned)(x.groups * x.parts_per_item), Cfg<DP, F8, SHARED>::kThreads, kSmem,
+                                     st>>>(mk, mv, x);
+  return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+}
+
+template <bool F8>
+int launch_tc_any(TcArgs& x, const Plan& p, cudaStream_t st) {
+  const int D = x.a.D;
+  x.box = std::min(x.a.P, D > 128 ? 64 : 128);
+  if (D > 128) return launch_tc<256, F8, false>(x, st);
+  if (D > 64) return p.shared ? launch_tc<128, F8, true>(x, st) : launch_tc<128, F8, false>(x, st);
+  return p.shared ? launch_tc<64, F8, true>(x, st) : launch_tc<64, F8, false>(x, st);
 }
 
 }  // namespace tat
@@ -181,7 +1239,7 @@ extern "C" {
 size_t sv_tree_attention_workspace_size(int B, int T, int Hq, int Hkv, int D, int max_pages,
                                         int page_size) {
   if (!sizes_ok(B, T, Hq, Hkv, D, max_pages, page_size)) return 0;
-  return 256;
+  return tc_shape(D, page_size) ? make_plan(T, Hq, Hkv, D).total : 256;
 }
 
 int sv_tree_attention(const void* q, int64_t q_stride_b, int64_t q_stride_t, int64_t q_stride_h,
@@ -229,6 +1287,28 @@ int sv_tree_attention(const void* q, int64_t q_stride_b, int64_t q_stride_t, int
   a.max_pages = max_pages;
   a.scale = scale;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  // 16-byte aligned rows for the tensor-core kernel; scales are copied in 16 bytes too.
+  const bool tc = tc_shape(D, page_size) && !misaligned(q, 16) && !misaligned(out, 16) &&
+                  !misaligned(k_cache, 16) && !misaligned(v_cache, 16) && !misaligned(k_scale, 16) &&
+                  !misaligned(v_scale, 16) && q_stride_b % 8 == 0 && q_stride_t % 8 == 0 && q_stride_h % 8 == 0;
+  if (tc) {
+    const Plan p = make_plan(T, Hq, Hkv, D);
+    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    TcArgs x{};
+    x.a = a;
+    x.rows = p.rows;
+    x.rpt = p.rpt;
+    x.parts_per_item = p.parts;
+    x.groups = p.groups;
+    x.c = scale == 0.0f ? 1.0f : std::fabs(scale) * 1.4426950408889634f;
+    x.qflip = scale < 0.0f ? 0x80008000u : 0u;
+    x.qzero = scale == 0.0f;
+    x.counters = reinterpret_cast<unsigned*>(ws + p.off_counters);
+    x.part_ml = reinterpret_cast<float2*>(ws + p.off_ml);
+    x.part_o = reinterpret_cast<float*>(ws + p.off_o);
+    if (cudaMemsetAsync(workspace, 0, p.off_ml, st) != cudaSuccess) return SV_ERR_CUDA;
+    return cache_dtype == SV_E4M3 ? launch_tc_any<true>(x, p, st) : launch_tc_any<false>(x, p, st);
+  }
   if (cudaMemsetAsync(workspace, 0, 4, st) != cudaSuccess) return SV_ERR_CUDA;
   const long long rows = (long long)B * T * Hq;
   const unsigned grid = (unsigned)((rows + kAnyThreads / 32 - 1) / (kAnyThreads / 32));
