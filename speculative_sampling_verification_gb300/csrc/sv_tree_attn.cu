@@ -10,6 +10,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
@@ -63,15 +64,17 @@ struct Args {
 // the order of the ranges, so that results do not depend on the timing.
 //
 // Warps: 0-7 softmax (warp w reads lanes 32 (w % 4) ..), 8 producer (TMA, one box a
-// page), 9 MMA issuer and owner of the tensor memory, 10-17 (e4m3 cache) convert
+// page), 9 MMA issuer and owner of the tensor memory, 12-15 (e4m3 cache) convert
 // codes to bf16 between a staging ring and the operand ring; the scales of
 // keys enter S, those of values enter P, in fp32.
 
-constexpr int kConvWarps = 8;
+constexpr int kConvWarps = 4;
 constexpr int kSoftWarps = 8;
 constexpr int kProducer = 8, kIssuer = 9;
 constexpr int kMaxCtas = 152;
 constexpr int kScaleSlots = 8;
+constexpr int kMaxSlots = 10;
+constexpr int kFewRows = 40;    // rows up to which keys, not rows, are the M of the products
 constexpr float kLazy = 8.0f;   // growth of the maximum (powers of two) before O is rescaled
 
 struct TcArgs {
@@ -81,6 +84,7 @@ struct TcArgs {
   int groups;           // ranges of the line of tiles
   int box;              // keys of one TMA box: min(page, KT)
   float c;              // |scale| log2 e, or 1 for a scale of 0
+  float join_c;         // powers of two in a unit of the parts' m
   unsigned qflip;       // sign bits to flip in Q (a negative scale)
   int qzero;            // a scale of 0: Q counts as 0
   unsigned* counters;   // [groups parts_per_item]: parts that have arrived
@@ -101,12 +105,12 @@ struct Cfg {
   static constexpr int kFit = (kBudget - NQ * kQBytes - kStages * kStage - (F8 ? kScaleSlots * 2 * KT * 4 : 0)) / kSlot;
   static constexpr int kSlots = kFit < 8 ? kFit : 8;
   static constexpr bool kAlternate = NS == 2 && !SHARED;
-  static constexpr int kThreads = 32 * (10 + (F8 ? kConvWarps : 0));
+  static constexpr int kThreads = 32 * (12 + (F8 ? kConvWarps : 0));
   static constexpr unsigned kS0 = 0, kS1 = 128, kO0 = NS == 2 ? 256 : 128, kO1 = 256 + DP;
 };
 
 struct TcTail {
-  unsigned long long full[8], empty[8];
+  unsigned long long full[kMaxSlots], empty[kMaxSlots];
   unsigned long long sfull[4], sempty[4];
   unsigned long long scale[kScaleSlots];
   unsigned long long q_ready, s_ready[2], p_ready[2], pv_done[2];
@@ -194,29 +198,66 @@ SV_DEVINL void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;
 SV_DEVINL void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 SV_DEVINL void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-SV_DEVINL void tmem_ld32(unsigned t, float (&v)[32]) {
+// 64 columns of this thread's lane.
+SV_DEVINL void tmem_ld64(unsigned t, float* v) {
+  uint32_t r[64];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, "
+      "%18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, "
+      "%34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, "
+      "%50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63"
+      "}, [%64];\n\ttcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]),
+        "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]),
+        "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]),
+        "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]),
+        "=r"(r[63])
+      : "r"(t));
+#pragma unroll
+  for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
+}
+SV_DEVINL void tmem_ld16(unsigned t, float* v) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15"
+      "}, [%16];\n\ttcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(t));
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+SV_DEVINL void tmem_ld32(unsigned t, float* v) {
   uint32_t r[32];
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
-      "%30, %31}, [%32];"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, "
+      "%18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31"
+      "}, [%32];\n\ttcgen05.wait::ld.sync.aligned;"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
         "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
         "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
         "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
         "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(t));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 SV_DEVINL void tmem_ld8(unsigned t, float (&v)[8]) {
   uint32_t r[8];
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+               "tcgen05.wait::ld.sync.aligned;"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
                  "=r"(r[7])
                : "r"(t));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
 }
@@ -227,6 +268,15 @@ SV_DEVINL void tmem_st16(unsigned t, const uint32_t (&r)[16]) {
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
       "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
+}
+SV_DEVINL void tmem_st8(unsigned t, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(t),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+SV_DEVINL uint32_t pack_bf16(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 SV_DEVINL void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -282,6 +332,102 @@ struct Walk {
   }
 };
 
+// One warp: the range of tiles that is group `group`'s, from the lengths.
+template <int KT>
+SV_DEVINL void find_range(const TcArgs& x, TcTail& t, int group, int lane) {
+  const Args& a = x.a;
+  long long total = 0;
+  for (int b = lane; b < a.B; b += 32) total += (long long)tiles_of<KT>(a, a.ctx_lens[b]) * a.Hkv;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  const int groups = (int)min((long long)x.groups, total);
+  const long long lo = group < groups ? (long long)group * total / groups : 0;
+  const long long hi = group < groups ? (long long)(group + 1) * total / groups : 0;
+  long long before = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    const long long n = b0 + lane < a.B ? (long long)tiles_of<KT>(a, a.ctx_lens[b0 + lane]) * a.Hkv : 0;
+    long long incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    const bool mine = lo >= before + incl - n && lo < before + incl;
+    if (mine) {
+      t.b0 = b0 + lane;
+      t.base0 = before + incl - n;
+    }
+    if (__any_sync(0xffffffffu, mine)) break;
+    before += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  if (lane == 0) {
+    t.lo = lo;
+    t.hi = hi;
+    t.total = total;
+    t.groups = groups;
+  }
+}
+
+// Called by `threads` threads once their part of an item that is cut is written:
+// the last part to arrive joins them all, in the order of the ranges. `sum` and O of
+// a part are relative to its m (in units of 1/join_c powers of two); NaN marks a sequence at fault.
+template <int KT>
+SV_DEVINL bool join_parts(const TcArgs& x, TcTail& t, const Walk<KT>& w, int group, int part, int cta_rows,
+                          int rows_here, int threads, unsigned& phase, int lane, volatile unsigned* abort) {
+  const Args& a = x.a;
+  const long long total = t.total;
+  const int ng = t.groups, G = a.Hq / a.Hkv;
+  const int gs = (int)(((w.base + 1) * ng - 1) / total), ge = (int)(((w.base + w.n) * ng - 1) / total);
+  __threadfence();
+  if (!warps_sync(smem_u32(&t.all_sync), phase, lane, abort, a.status)) return false;
+  if (threadIdx.x == 0)
+    t.last = atomicAdd(&x.counters[gs * x.parts_per_item + part], 1u) == (unsigned)(ge - gs);
+  if (!warps_sync(smem_u32(&t.all_sync), phase, lane, abort, a.status)) return false;
+  if (!t.last) return true;
+  __threadfence();
+  const int units = a.D / 4;
+  for (int i = threadIdx.x; i < rows_here * units; i += threads) {
+    const int r = i / units, u = i - r * units;
+    const int gr = part * cta_rows + r;
+    if (gr >= x.rows) continue;
+    float top = -INFINITY;
+    bool poison = false;
+    for (int g = gs; g <= ge; ++g) {
+      const long long sl = (long long)(g * x.parts_per_item + part) * 2 + (g == gs ? 1 : 0);
+      const float pm = __ldcg(&x.part_ml[sl * cta_rows + r]).x;
+      poison = poison || isnan(pm);
+      top = fmaxf(top, pm);
+    }
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float l = 0.0f;
+#pragma unroll 4
+    for (int g = gs; g <= ge; ++g) {
+      const long long sl = (long long)(g * x.parts_per_item + part) * 2 + (g == gs ? 1 : 0);
+      const float2 ml = __ldcg(&x.part_ml[sl * cta_rows + r]);
+      const float4 o = __ldcg(reinterpret_cast<const float4*>(x.part_o + (sl * cta_rows + r) * a.D) + u);
+      if (ml.x == -INFINITY) continue;
+      const float f = ex2_fast((ml.x - top) * x.join_c);
+      l = fmaf(ml.y, f, l);
+      acc.x = fmaf(o.x, f, acc.x);
+      acc.y = fmaf(o.y, f, acc.y);
+      acc.z = fmaf(o.z, f, acc.z);
+      acc.w = fmaf(o.w, f, acc.w);
+    }
+    const int nd = gr / G;
+    const bool gone = a.parents && a.parents[(long long)w.b * a.T + nd] == -2;
+    float inv_l = l == 0.0f || gone ? 0.0f : 1.0f / l;
+    if (poison) inv_l = __int_as_float(0x7fc00000);
+    if (inv_l == 0.0f) acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const __nv_bfloat162 h0 = __floats2bfloat162_rn(acc.x * inv_l, acc.y * inv_l);
+    const __nv_bfloat162 h1 = __floats2bfloat162_rn(acc.z * inv_l, acc.w * inv_l);
+    uint2 o;
+    o.x = *reinterpret_cast<const uint32_t*>(&h0);
+    o.y = *reinterpret_cast<const uint32_t*>(&h1);
+    *reinterpret_cast<uint2*>(a.out + (((long long)w.b * a.T + nd) * a.Hq + w.hk * G + gr % G) * a.D + u * 4) = o;
+  }
+  return true;
+}
+
 // Place of tile i's keys and values in the order of the operand ring.
 template <bool ALT>
 SV_DEVINL unsigned k_entry(int i) { return ALT ? (i == 0 ? 0u : 2u * i - 1u) : 2u * i; }
@@ -319,37 +465,8 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
   const int group = blockIdx.x / x.parts_per_item, part = blockIdx.x % x.parts_per_item;
   constexpr int kSoft = NS * 4;  // softmax warps at work
 
-  if (warp == 0) {  // this CTA's range, from the lengths
-    long long total = 0;
-    for (int b = lane; b < a.B; b += 32) total += (long long)tiles_of<KT>(a, a.ctx_lens[b]) * a.Hkv;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    const int groups = (int)min((long long)x.groups, total);
-    const long long lo = group < groups ? (long long)group * total / groups : 0;
-    const long long hi = group < groups ? (long long)(group + 1) * total / groups : 0;
-    long long before = 0;
-    for (int b0 = 0; b0 < a.B; b0 += 32) {
-      const long long n = b0 + lane < a.B ? (long long)tiles_of<KT>(a, a.ctx_lens[b0 + lane]) * a.Hkv : 0;
-      long long incl = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
-      }
-      const bool mine = lo >= before + incl - n && lo < before + incl;
-      if (mine) {
-        t.b0 = b0 + lane;
-        t.base0 = before + incl - n;
-      }
-      if (__any_sync(0xffffffffu, mine)) break;
-      before += __shfl_sync(0xffffffffu, incl, 31);
-    }
-    if (lane == 0) {
-      t.lo = lo;
-      t.hi = hi;
-      t.total = total;
-      t.groups = groups;
-    }
+  if (warp == 0) {
+    find_range<KT>(x, t, group, lane);
   } else if (warp == kProducer && lane == 0) {
     for (int i = 0; i < C::kSlots; ++i) {
       mbar_init(smem_u32(&t.full[i]), F8 ? kConvWarps : 1);
@@ -685,23 +802,40 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
             const unsigned hi = k < 0 ? anc[0] : k == 0 ? anc[1] : k == 1 ? anc[2] : k == 2 ? anc[3] : 0u;
             return __funnelshift_r(lo, hi, sh);
           };
-          float top = -INFINITY;
-#pragma unroll 1
-          for (int col = 0; col < KT; col += 32) {
-            float v[32];
-            tmem_ld32(sbase + col, v);
+          // S, 64 columns at a time, with the keys' scales and the mask. 128 columns do
+          // not fit the registers: they are read a second time.
+          float v[64];
+          auto load = [&](int col) {
+            tmem_ld64(sbase + col, v);
             if (F8) {
 #pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] *= ksc[col + j];
+              for (int j = 0; j < 64; j += 4) {
+                const float4 f = *reinterpret_cast<const float4*>(ksc + col + j);
+                const float2 z0 = f2_mul(make_float2(v[j], v[j + 1]), make_float2(f.x, f.y));
+                const float2 z1 = f2_mul(make_float2(v[j + 2], v[j + 3]), make_float2(f.z, f.w));
+                v[j] = z0.x;
+                v[j + 1] = z0.y;
+                v[j + 2] = z1.x;
+                v[j + 3] = z1.y;
+              }
             }
             if (edge) {
-              const unsigned see = seen(col);
 #pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = see >> j & 1u ? v[j] : -INFINITY;
+              for (int h = 0; h < 64; h += 32) {
+                const unsigned see = seen(col + h);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[h + j] = see >> j & 1u ? v[h + j] : -INFINITY;
+              }
             }
+          };
+          float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int j = 0; j < 32; ++j) top = fmaxf(top, v[j]);
+          for (int col = 0; col < KT; col += 64) {
+            load(col);
+#pragma unroll
+            for (int j = 0; j < 64; ++j) top4[j & 3] = fmaxf(top4[j & 3], v[j]);
           }
+          const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
           const bool raise = top > m + grow || (m == -INFINITY && top > m);
           if (__any_sync(0xffffffffu, raise)) {
             const float nm = raise ? top : m;
@@ -728,34 +862,37 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
             sum *= f;
             m = nm;
           }
-          const float mc = m == -INFINITY ? 0.0f : m * c;
-          float part_sum = 0.0f;
-#pragma unroll 1
-          for (int col = 0; col < KT; col += 32) {
-            float v[32];
-            tmem_ld32(sbase + col, v);
-            const unsigned see = edge ? seen(col) : 0xffffffffu;
+          // A masked score is -inf, so its weight comes out as 0 (the values' scales
+          // may be NaN there, hence the select after them).
+          const float2 c2 = f2(c), mc2 = f2(m == -INFINITY ? 0.0f : -m * c);
+          float2 sum2[2] = {f2(0.0f), f2(0.0f)};
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              float y = v[j];
-              if (F8) y *= ksc[col + j];
-              y = ex2_fast(__fmaf_rn(y, c, -mc));
-              if (edge) y = see >> j & 1u ? y : 0.0f;
-              part_sum += y;
-              if (F8) {
-                y *= ksc[KT + col + j];
-                if (edge) y = see >> j & 1u ? y : 0.0f;
+          for (int col = 0; col < KT; col += 64) {
+            if (KT > 64) load(col);
+#pragma unroll
+            for (int h = 0; h < 64; h += 32) {
+              uint32_t r[16];
+              const unsigned see = F8 && edge ? seen(col + h) : 0xffffffffu;
+#pragma unroll
+              for (int j = 0; j < 32; j += 2) {
+                const float2 y = f2_fma(make_float2(v[h + j], v[h + j + 1]), c2, mc2);
+                float2 p = make_float2(ex2_fast(y.x), ex2_fast(y.y));
+                sum2[(j >> 1) & 1] = f2_add(sum2[(j >> 1) & 1], p);
+                if (F8) {
+                  p = f2_mul(p, *reinterpret_cast<const float2*>(ksc + KT + col + h + j));
+                  if (edge) {
+                    p.x = see >> j & 1u ? p.x : 0.0f;
+                    p.y = see >> (j + 1) & 1u ? p.y : 0.0f;
+                  }
+                }
+                const __nv_bfloat162 b = __floats2bfloat162_rn(p.x, p.y);
+                r[j >> 1] = *reinterpret_cast<const uint32_t*>(&b);
               }
-              v[j] = y;
+              tmem_st16(sbase + (col + h) / 2, r);
             }
-            uint32_t r[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
-              r[j] = *reinterpret_cast<const uint32_t*>(&h);
-            }
-            tmem_st16(sbase + col / 2, r);
           }
+          const float2 sum1 = f2_add(sum2[0], sum2[1]);
+          const float part_sum = sum1.x + sum1.y;
           sum += part_sum;
           tmem_wait_st();
         }
@@ -829,6 +966,7 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
       __nv_bfloat16* out = a.out + (((long long)w.b * a.T + node) * a.Hq + w.hk * G + row % G) * a.D;
       if (busy) {
         for (int col = col0; col < col0 + cols; col += 8) {
+          __syncwarp();  // tensor memory is read by whole warps
           float v[8];
           tmem_ld8(tmem + lanes + C::kO0 + (SHARED && s ? DP : 0) + col, v);
           if (ALT) {
@@ -878,66 +1016,14 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
         if (!whole && have && (!ALT || s == 0)) x.part_ml[slot * cta_rows + prow] = make_float2(m, sum);
       }
       if (!whole) {
-        // The last part to arrive joins them all, in the order of the ranges.
-        const long long total = t.total;
-        const int ng = t.groups;
-        const int gs = (int)(((w.base + 1) * ng - 1) / total), ge = (int)(((w.base + w.n) * ng - 1) / total);
-        __threadfence();
-        ok = warps_sync(smem_u32(&t.all_sync), all_phase, lane, abort, a.status);
+        const int rows_here = SHARED ? cta_rows : nrows;
+        ok = join_parts(x, t, w, group, part, cta_rows, rows_here, NS * 128, all_phase, lane, abort);
         if (!ok) break;
-        if (threadIdx.x == 0)
-          t.last = atomicAdd(&x.counters[gs * x.parts_per_item + part], 1u) == (unsigned)(ge - gs);
-        ok = warps_sync(smem_u32(&t.all_sync), all_phase, lane, abort, a.status);
-        if (!ok) break;
-        if (t.last) {
-          __threadfence();
-          const int units = a.D / 4;
-          const int rows_here = SHARED ? cta_rows : nrows;
-          for (int i = threadIdx.x; i < rows_here * units; i += NS * 128) {
-            const int r = i / units, u = i - r * units;
-            const int gr = part * cta_rows + r;
-            if (gr >= x.rows) continue;
-            float top = -INFINITY;
-            bool poison = false;
-            for (int g = gs; g <= ge; ++g) {
-              const long long sl = (long long)(g * x.parts_per_item + part) * 2 + (g == gs ? 1 : 0);
-              const float pm = __ldcg(&x.part_ml[sl * cta_rows + r]).x;
-              poison = poison || isnan(pm);
-              top = fmaxf(top, pm);
-            }
-            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            float l = 0.0f;
-            for (int g = gs; g <= ge; ++g) {
-              const long long sl = (long long)(g * x.parts_per_item + part) * 2 + (g == gs ? 1 : 0);
-              const float2 ml = __ldcg(&x.part_ml[sl * cta_rows + r]);
-              if (ml.x == -INFINITY) continue;
-              const float f = ex2_fast((ml.x - top) * c);
-              const float4 o = __ldcg(reinterpret_cast<const float4*>(x.part_o + (sl * cta_rows + r) * a.D) + u);
-              l = fmaf(ml.y, f, l);
-              acc.x = fmaf(o.x, f, acc.x);
-              acc.y = fmaf(o.y, f, acc.y);
-              acc.z = fmaf(o.z, f, acc.z);
-              acc.w = fmaf(o.w, f, acc.w);
-            }
-            const int nd = gr / G;
-            const bool gone = a.parents && a.parents[(long long)w.b * a.T + nd] == -2;
-            float inv_l = l == 0.0f || gone ? 0.0f : 1.0f / l;
-            if (poison) inv_l = __int_as_float(0x7fc00000);
-            if (inv_l == 0.0f) acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            const __nv_bfloat162 h0 = __floats2bfloat162_rn(acc.x * inv_l, acc.y * inv_l);
-            const __nv_bfloat162 h1 = __floats2bfloat162_rn(acc.z * inv_l, acc.w * inv_l);
-            uint2 o;
-            o.x = *reinterpret_cast<const uint32_t*>(&h0);
-            o.y = *reinterpret_cast<const uint32_t*>(&h1);
-            *reinterpret_cast<uint2*>(a.out + (((long long)w.b * a.T + nd) * a.Hq + w.hk * G + gr % G) * a.D +
-                                      u * 4) = o;
-          }
-        }
       }
     }
-  } else if (F8 && warp >= kIssuer + 1) {
+  } else if (F8 && warp >= 12) {
     // ---- codes to bf16: 16 of a row a thread and step
-    const int ct = threadIdx.x - 32 * (kIssuer + 1);
+    const int ct = threadIdx.x - 32 * 12;
     unsigned entry = 0;
     bool ok = true;
     for (; w.more() && ok; w.next(a)) {
@@ -977,6 +1063,732 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
           bar_arrive(smem_u32(&t.sempty[st]));
         }
       }
+    }
+  }
+  fence_before();
+  __syncthreads();
+  if (warp == kIssuer) {
+    __syncwarp();
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+  }
+}
+
+// ---------------------------------------------------------------- tensor cores, few rows
+//
+// Up to 40 rows a key/value head (ordinary decoding, small trees): the operands
+// change places. S^T = K Q^T has the tile's 128 keys as the M of the product and the
+// rows as its N, so the tensor cores and the softmax work on the rows that exist.
+// One thread a key holds that key's scores of all rows, its scales and its
+// mask; the maximum of a row is not needed, only a reference m that no score
+// exceeds by more than 2^8: a vote of the warpgroup finds the rare tile that does, and only
+// then are maxima taken across the threads and O rescaled. P^T goes to shared
+// memory as the other operand of O^T = V^T P^T (M = 128 channels of the head).
+// A row's sum is kept by each thread for its keys and joined at the item's end.
+//
+// An e4m3 cache feeds the tensor cores as it is (kind::f8f6f4), with no pass to
+// convert it: Q and P enter as sums of e4m3 pieces, each piece with columns of
+// its own. Q scaled by a power of two to at most 448 is hi + lo/16, exact but for
+// elements below 2^-15 of the row's largest, which are off by up to 2^-22 of that. P
+// times the value's scale (over a power of two not below any scale) is p1 + p2/16 + p3/256,
+// off by at most 2^-12 of itself or 2^-18 against a largest weight of 1 to 2^8.
+// A bf16 cache uses bf16 operands, P rounded once (2^-8).
+//
+// Streams, ranges and parts are those of the kernel above; the next tile's
+// S^T is issued before this tile's O^T, so neither waits for the other.
+
+template <int RP, bool F8>
+struct FewCfg {
+  static constexpr int KT = 128;
+  static constexpr int N1 = F8 ? 2 * RP : (RP + 15) / 16 * 16;         // columns of S^T
+  static constexpr int N2 = F8 ? (3 * RP + 15) / 16 * 16 : N1;         // columns of O^T
+  static constexpr int kQBytes = N1 * 128 * (F8 ? 1 : 2);
+  static constexpr int kPBytes = KT * 128;
+  static constexpr int kSlot = KT * (F8 ? 128 : 256);
+  static constexpr int kTailBytes = 12 * 1024;
+  static constexpr int kFit = (226 * 1024 - kTailBytes - kQBytes - 2 * kPBytes) / kSlot;
+  static constexpr int kSlots = kFit < kMaxSlots ? kFit : kMaxSlots;
+  static constexpr int kThreads = 320;
+  static constexpr unsigned kS = 0, kO = 256;  // tensor memory: two of each, 128 columns apart
+};
+
+template <int RP>
+struct FewTail {
+  TcTail t;
+  unsigned long long anc[2][2][64];  // [item parity][stream][node]: ancestors and itself
+  // Arrays that are read four values at a time lie on 16-byte boundaries.
+  alignas(16) float mref[2][RP];     // [stream] references, powers of two
+  alignas(16) float fac[2][RP];      // [stream] factors of a rescaling
+  float wmax[2][4][RP], wsum[2][4][RP], wvs[2][4];
+  float vref[2];
+  alignas(16) float qc[2][RP];       // [item parity] c over the row's scale of Q
+  float4 fin[RP];
+  unsigned vote[2][2];               // [stream][tile parity]
+};
+
+template <int RP, bool F8>
+constexpr int few_smem() {
+  using C = FewCfg<RP, F8>;
+  static_assert(sizeof(FewTail<RP>) <= C::kTailBytes, "tail");
+  static_assert(RP % 8 == 0 && C::kQBytes % 1024 == 0, "rows of four values, blocks of 1024 bytes");
+  return 1024 + C::kQBytes + 2 * C::kPBytes + C::kSlots * C::kSlot + (int)sizeof(FewTail<RP>);
+}
+
+SV_DEVINL void mma_f8(unsigned d, uint64_t a, uint64_t b, uint32_t id, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"((unsigned)acc)
+      : "memory");
+}
+
+SV_DEVINL float redux_max(float v) {
+  // Order-preserving integers: the warp's integer maximum.
+  const int b = __float_as_int(v);
+  const int m = __reduce_max_sync(0xffffffffu, b ^ ((b >> 31) & 0x7fffffff));
+  return __int_as_float(m ^ ((m >> 31) & 0x7fffffff));
+}
+
+SV_DEVINL uint32_t half2_bits(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
+
+// Two e4m3 codes of a half pair, and the pair they stand for.
+SV_DEVINL uint32_t half2_to_e4m3(__half2 h) {
+  unsigned short r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(half2_bits(h)));
+  return r;
+}
+SV_DEVINL __half2 e4m3_to_half2(uint32_t c) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((unsigned short)c));
+  return *reinterpret_cast<const __half2*>(&r);
+}
+
+template <int N>
+SV_DEVINL void tmem_ld_cols(unsigned t, float* v) {
+  if constexpr (N >= 64) {
+    tmem_ld64(t, v);
+    if constexpr (N > 64) tmem_ld_cols<N - 64>(t + 64, v + 64);
+  } else if constexpr (N >= 32) {
+    tmem_ld32(t, v);
+    if constexpr (N > 32) tmem_ld_cols<N - 32>(t + 32, v + 32);
+  } else if constexpr (N >= 16) {
+    tmem_ld16(t, v);
+    if constexpr (N > 16) tmem_ld_cols<N - 16>(t + 16, v + 16);
+  } else {
+    float u[8];
+    tmem_ld8(t, u);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = u[i];
+  }
+}
+
+// Place in the operand ring: K0 K1 K2 V0 K3 V1 ... (S^T of tile i + 2 before O^T of tile i).
+SV_DEVINL unsigned few_k(int i) { return i < 2 ? (unsigned)i : 2u * i - 2u; }
+SV_DEVINL unsigned few_v(int i, int n) { return (unsigned)min(2 * i + 3, n + i); }
+
+template <int RP, bool F8>
+__global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
+    tree_attn_few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                         const __grid_constant__ TcArgs x) {
+  using C = FewCfg<RP, F8>;
+  constexpr int KT = 128;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                         ~static_cast<uintptr_t>(1023));
+  unsigned char* pbuf = smem;                          // [2][128 keys][128 bytes]
+  unsigned char* ring = pbuf + 2 * C::kPBytes;
+  unsigned char* qbuf = ring + C::kSlots * C::kSlot;   // [blocks of 128 bytes][N1 rows]
+  FewTail<RP>& f = *reinterpret_cast<FewTail<RP>*>(qbuf + C::kQBytes);
+  TcTail& t = f.t;
+  const Args& a = x.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int group = blockIdx.x, part = 0;
+  constexpr int kSoft = 8;
+
+  if (warp == 0) {
+    find_range<KT>(x, t, group, lane);
+  } else if (warp == kProducer && lane == 0) {
+    for (int i = 0; i < C::kSlots; ++i) {
+      mbar_init(smem_u32(&t.full[i]), 1);
+      mbar_init(smem_u32(&t.empty[i]), 1);
+    }
+    mbar_init(smem_u32(&t.q_ready), kSoft);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&t.s_ready[i]), 1);
+      mbar_init(smem_u32(&t.p_ready[i]), 4);
+      mbar_init(smem_u32(&t.pv_done[i]), 1);
+      mbar_init(smem_u32(&t.wg_sync[i]), 4);
+      f.vote[i][0] = f.vote[i][1] = 0;
+    }
+    mbar_init(smem_u32(&t.all_sync), kSoft);
+    t.abort = 0;
+    t.bad[0] = t.bad[1] = t.badv[0] = t.badv[1] = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  } else if (warp == kIssuer) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(&t.tmem_base)),
+                 "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const unsigned tmem = t.tmem_base;
+  volatile unsigned* abort = &t.abort;
+  Walk<KT> w;
+  w.start(a, t);
+
+  if (warp == kProducer) {
+    unsigned entry = 0;
+    bool ok = true;
+    for (; w.more() && ok; w.next(a)) {
+      const int n = w.t1 - w.t0;
+      int live = a.T;
+      if (a.parents && (long long)w.t1 * KT > w.ctx) {
+        live = 0;
+        for (int i = lane; i < a.T; i += 32)
+          if (a.parents[(long long)w.b * a.T + i] != -2) live = i + 1;
+        live = __reduce_max_sync(0xffffffffu, live);
+      }
+      const bool seq_ok = ctx_ok(a, w.ctx);
+      int nk = 0, nv = 0;  // keys and values issued
+      for (int e = 0; e < 2 * n && ok; ++e, ++entry) {
+        const bool isv = !(nk < n && nk < nv + 3);
+        const int tile = w.t0 + (isv ? nv++ : nk++);
+        const int pos = tile * KT + lane * x.box;
+        int page = -1;
+        if (seq_ok && lane < KT / x.box && pos < w.ctx + live && pos / a.P < a.max_pages)
+          page = a.page_table[(long long)w.b * a.max_pages + pos / a.P];
+        if (page < 0 || page >= a.num_pages) page = -1;
+        const unsigned hit = __ballot_sync(0xffffffffu, page >= 0);
+        const int s = (int)(entry % C::kSlots);
+        ok = __all_sync(0xffffffffu, entry < (unsigned)C::kSlots ||
+                                         bar_wait(smem_u32(&t.empty[s]), ((entry / C::kSlots) & 1) ^ 1, abort,
+                                                  a.status));
+        if (!ok) break;
+        const unsigned bar = smem_u32(&t.full[s]);
+        const unsigned dst = smem_u32(ring + s * C::kSlot) + lane * x.box * 128;
+        if (lane == 0) mbar_arrive_expect_tx(bar, (unsigned)__popc(hit) * x.box * (C::kSlot / KT));
+        __syncwarp();
+        if (page >= 0) {
+          const CUtensorMap* map = isv ? &map_v : &map_k;
+          tma_4d(dst, map, 0, 0, w.hk, page, bar);
+          if (!F8) tma_4d(dst + KT * 128, map, 64, 0, w.hk, page, bar);
+        }
+      }
+    }
+    if (*abort) {
+      for (int i = 0; i < C::kSlots && entry >= (unsigned)i + 1; ++i) {
+        const unsigned e = entry - 1 - i;
+        const uint64_t t0 = global_ns();
+        while (!mbar_test_parity(smem_u32(&t.full[e % C::kSlots]), (e / C::kSlots) & 1) &&
+               global_ns() - t0 < 1000000) {
+        }
+      }
+    }
+  } else if (warp == kIssuer) {
+    if (lane == 0) {
+      // fp32 accumulator, M = 128; A and B bf16 or e4m3 (code 0).
+      constexpr uint32_t kTypes = F8 ? 0u : (1u << 7) | (1u << 10);
+      constexpr uint32_t id_qk = (1u << 4) | kTypes | ((uint32_t)(C::N1 >> 3) << 17) | (8u << 24);
+      constexpr uint32_t id_pv =
+          (1u << 4) | kTypes | (1u << 15) | (1u << 16) | ((uint32_t)(C::N2 >> 3) << 17) | (8u << 24);
+      const int ksteps = F8 ? (a.D + 31) / 32 : a.D / 16;
+      unsigned entry0 = 0, item = 0, pcount[2] = {0, 0};
+      bool ok = true;
+      auto full = [&](unsigned e) {
+        ok = ok && bar_wait(smem_u32(&t.full[e % C::kSlots]), (e / C::kSlots) & 1, abort, a.status);
+        if (ok) fence_after();
+        return ok;
+      };
+      auto qk = [&](int i) {
+        const unsigned e = entry0 + few_k(i);
+        if (!full(e)) return;
+        const unsigned k = smem_u32(ring + (e % C::kSlots) * C::kSlot), q = smem_u32(qbuf);
+        const unsigned d = tmem + C::kS + 128 * (i & 1);
+        for (int j = 0; j < ksteps; ++j) {
+          const unsigned off = (j & 3) * 32;
+          if (F8)
+            mma_f8(d, desc_k(k + off), desc_k(q + off), id_qk, j > 0);
+          else
+            mma_ss(d, desc_k(k + (j >> 2) * KT * 128 + off), desc_k(q + (j >> 2) * C::N1 * 128 + off), id_qk,
+                   j > 0);
+        }
+        commit(smem_u32(&t.empty[e % C::kSlots]));
+        commit(smem_u32(&t.s_ready[i & 1]));
+      };
+      for (; w.more() && ok; w.next(a), ++item) {
+        const int n = w.t1 - w.t0;
+        ok = ok && bar_wait(smem_u32(&t.q_ready), item & 1, abort, a.status);
+        if (!ok) break;
+        fence_after();
+        qk(0);
+        if (n > 1 && ok) qk(1);
+        for (int i = 0; i < n && ok; ++i) {
+          const int s = i & 1;
+          ok = ok && bar_wait(smem_u32(&t.p_ready[s]), pcount[s] & 1, abort, a.status);
+          if (!ok) break;
+          fence_after();
+          ++pcount[s];
+          if (i + 2 < n) qk(i + 2);
+          const unsigned e = entry0 + few_v(i, n);
+          if (!ok || !full(e)) break;
+          const unsigned v = smem_u32(ring + (e % C::kSlots) * C::kSlot), p = smem_u32(pbuf + s * C::kPBytes);
+          const unsigned d = tmem + C::kO + 128 * s;
+#pragma unroll
+          for (int j = 0; j < (F8 ? 4 : 8); ++j) {
+            const unsigned off = j * (F8 ? 4096 : 2048);
+            if (F8)
+              mma_f8(d, desc_n(v + off, KT * 128), desc_n(p + off, KT * 128), id_pv, i > 1 || j > 0);
+            else
+              mma_ss(d, desc_n(v + off, KT * 128), desc_n(p + off, KT * 128), id_pv, i > 1 || j > 0);
+          }
+          commit(smem_u32(&t.empty[e % C::kSlots]));
+          commit(smem_u32(&t.pv_done[s]));
+        }
+        entry0 += 2u * n;
+      }
+    }
+  } else if (warp < kSoft) {
+    const int s = warp >> 2, q = warp & 3;
+    const int wt = threadIdx.x & 127;  // key of the tile, and channel of the head
+    const unsigned lanes = (unsigned)(q * 32) << 16;
+    const unsigned sbase = tmem + lanes + C::kS + 128 * s;
+    const unsigned obase = tmem + lanes + C::kO + 128 * s;
+    const int G = a.Hq / a.Hkv, nrows = x.rows;
+    unsigned item = 0, scount = 0, entry0 = 0, wg_phase = 0, all_phase = 0;
+    bool ok = true;
+
+    // Q of an item into shared memory (e4m3: as two pieces): a warp a row.
+    auto load_q = [&](const Walk<KT>& it, unsigned parity) {
+      for (int r = warp; r < RP; r += kSoft) {
+        const bool on = r < nrows && !x.qzero;
+        uint2 v = make_uint2(0, 0);  // four elements a lane
+        if (on && lane * 4 < a.D)
+          v = *reinterpret_cast<const uint2*>(a.q + it.b * a.q_sb + (long long)(r / G) * a.q_st +
+                                              (long long)(it.hk * G + r % G) * a.q_sh + lane * 4);
+        v.x ^= x.qflip;
+        v.y ^= x.qflip;
+        if (!on) v = make_uint2(0, 0);
+        if (F8) {
+          float e[4] = {bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y)};
+          float top = fmaxf(fmaxf(fabsf(e[0]), fabsf(e[1])), fmaxf(fabsf(e[2]), fabsf(e[3])));
+          top = redux_max(top);
+          // 2^k with top 2^k in [128, 256); rows of zeros, infinities or NaN as they are.
+          int k = 134 - (int)(__float_as_uint(top) >> 23);
+          if (!(top > 0.0f) || !(top < INFINITY)) k = 0;
+          k = max(-126, min(126, k));
+          const float up = __int_as_float((k + 127) << 23), down = __int_as_float((127 - k) << 23);
+          uint32_t hi = 0, lo = 0;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float y = e[j] * up;
+            const uint32_t h = __nv_cvt_float_to_fp8(y, __NV_SATFINITE, __NV_E4M3);
+            const float back = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)h, __NV_E4M3)));
+            const uint32_t l = __nv_cvt_float_to_fp8((y - back) * 16.0f, __NV_SATFINITE, __NV_E4M3);
+            // e4m3 has no infinity: one in Q counts as NaN.
+            hi |= (isinf(y) ? 0x7fu : h) << (8 * j);
+            lo |= (isfinite(y) ? l : 0x7fu) << (8 * j);
+          }
+          const int u = lane >> 2;
+          *reinterpret_cast<uint32_t*>(qbuf + r * 128 + ((u ^ (r & 7)) << 4) + (lane & 3) * 4) = hi;
+          const int r2 = r + RP;
+          *reinterpret_cast<uint32_t*>(qbuf + r2 * 128 + ((u ^ (r2 & 7)) << 4) + (lane & 3) * 4) = lo;
+          if (lane == 0) f.qc[parity][r] = x.c * down;
+        } else {
+          const int u = lane >> 1;  // 16-byte unit of the row
+          *reinterpret_cast<uint2*>(qbuf + (u >> 3) * C::N1 * 128 + r * 128 + (((u & 7) ^ (r & 7)) << 4) +
+                                    (lane & 1) * 8) = v;
+          if (lane == 0) f.qc[parity][r] = x.c;
+        }
+      }
+      if (!F8) {  // rows that pad the columns to a multiple of 16
+        for (int r = RP + warp; r < C::N1; r += kSoft) {
+          const int u = lane >> 1;
+          *reinterpret_cast<uint2*>(qbuf + (u >> 3) * C::N1 * 128 + r * 128 + (((u & 7) ^ (r & 7)) << 4) +
+                                    (lane & 1) * 8) = make_uint2(0, 0);
+        }
+      }
+      fence_async();
+      fence_before();
+      __syncwarp();
+      if (lane == 0) bar_arrive(smem_u32(&t.q_ready));
+    };
+    if (w.more()) load_q(w, 0);
+
+    for (; w.more() && ok; ++item) {
+      const int n = w.t1 - w.t0;
+      const bool seq_ok = ctx_ok(a, w.ctx);
+      const bool tail = seq_ok && (long long)w.t1 * KT > w.ctx;
+      int* par = t.par[item & 1][s];
+      unsigned long long* anc = f.anc[item & 1][s];
+      const float* qc = f.qc[item & 1];
+      if (wt < RP) f.mref[s][wt] = wt < nrows ? -INFINITY : 0.0f;
+      if (wt == 0) f.vref[s] = 0.0f;
+      {
+        unsigned bad = seq_ok ? 0u : (unsigned)SV_DEV_PAGE_RANGE;
+        if (tail && wt < a.T) par[wt] = a.parents ? a.parents[(long long)w.b * a.T + wt] : wt - 1;
+        ok = warps_sync(smem_u32(&t.wg_sync[s]), wg_phase, lane, abort, a.status);
+        if (!ok) break;
+        if (tail) {
+          if (wt < a.T) {
+            const int p = par[wt];
+            if (p < -2 || p >= wt || (p >= 0 && par[p] == -2)) bad |= SV_DEV_TREE;
+            unsigned long long set = 0;
+            for (int j = wt, left = a.T; j >= 0 && left > 0; --left) {
+              const int pj = par[j];
+              if (pj == -2) break;
+              set |= 1ull << j;
+              j = pj < j ? pj : -1;
+            }
+            anc[wt] = set;
+          }
+          ok = warps_sync(smem_u32(&t.wg_sync[s]), wg_phase, lane, abort, a.status);
+          if (!ok) break;
+        }
+        if (seq_ok && s == 0) {
+          const int p0 = (int)((long long)w.t0 * KT / a.P);
+          const int p1 = (int)min(((long long)w.t1 * KT + a.P - 1) / a.P, ((long long)w.ctx + a.T + a.P - 1) / a.P);
+          for (int p = p0 + wt; p < p1; p += 128) {
+            bool used = (long long)p * a.P < w.ctx;
+            if (!used) {
+              const int j1 = min((long long)a.T, (long long)(p + 1) * a.P - w.ctx);
+              for (int j = max(0, p * a.P - w.ctx); j < j1 && !used; ++j) used = par[j] != -2;
+            }
+            if (!used) continue;
+            const int id = p < a.max_pages ? a.page_table[(long long)w.b * a.max_pages + p] : -1;
+            if (id < 0 || id >= a.num_pages) bad |= SV_DEV_PAGE_RANGE;
+          }
+        }
+        if (bad) {
+          atomicOr(&t.bad[item & 1], 1u);
+          atomicOr(a.status, bad);
+        }
+      }
+
+      float l[RP];
+#pragma unroll
+      for (int r = 0; r < RP; ++r) l[r] = 0.0f;
+      bool any = false;
+      // Scales of this thread's key, one of the stream's tiles ahead.
+      float ksc = 1.0f, vsc = 1.0f;
+      auto fetch_scales = [&](int i) {
+        ksc = vsc = 0.0f;
+        const long long pos = (long long)(w.t0 + i) * KT + wt;
+        if (!seq_ok || i >= n || pos >= (long long)w.ctx + a.T || pos / a.P >= a.max_pages) return;
+        const int id = a.page_table[(long long)w.b * a.max_pages + pos / a.P];
+        if (id < 0 || id >= a.num_pages) return;
+        const long long at = ((long long)id * a.Hkv + w.hk) * a.P + pos % a.P;
+        ksc = __ldg(a.ks + at);
+        vsc = __ldg(a.vs + at);
+      };
+      if (F8) fetch_scales(s);
+      for (int i = s; i < n; i += 2) {
+        const int tile = w.t0 + i;
+        const bool edge = (long long)(tile + 1) * KT > w.ctx || !seq_ok;
+        // Rows that attend this thread's key.
+        unsigned long long see = ~0ull;
+        if (edge) {
+          const long long nd = (long long)tile * KT + wt - w.ctx;
+          if (!seq_ok || nd >= a.T) {
+            see = 0;
+          } else if (nd >= 0) {
+            see = 0;
+            for (int r = 0; r < nrows; ++r)
+              if (anc[r / G] >> nd & 1ull) see |= 1ull << r;
+          }
+        }
+        ok = __all_sync(0xffffffffu, bar_wait(smem_u32(&t.s_ready[s]), scount & 1, abort, a.status));
+        if (!ok) break;
+        fence_after();
+        // Scores in powers of two, S^T times the scales, and how far they exceed m.
+        float y[RP];
+        {
+          tmem_ld_cols<RP>(sbase, y);
+          if (F8) {
+            float z[RP];
+            tmem_ld_cols<RP>(sbase + RP, z);
+#pragma unroll
+            for (int r = 0; r < RP; ++r) y[r] = __fmaf_rn(z[r], 0.0625f, y[r]) * ksc;
+          }
+          float over = -INFINITY;
+#pragma unroll
+          for (int r = 0; r < RP; r += 4) {
+            const float4 c4 = *reinterpret_cast<const float4*>(qc + r);
+            const float4 m4 = *reinterpret_cast<const float4*>(&f.mref[s][r]);
+            const float cc[4] = {c4.x, c4.y, c4.z, c4.w}, mm[4] = {m4.x, m4.y, m4.z, m4.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              float v = y[r + j] * cc[j];
+              if (edge) v = see >> (r + j) & 1ull ? v : -INFINITY;
+              y[r + j] = v;
+              over = fmaxf(over, v - mm[j]);
+            }
+          }
+          bool raise = over > kLazy;
+          if (F8) raise = raise || (see != 0 && vsc > f.vref[s]);
+          if (__any_sync(0xffffffffu, raise) && lane == 0) f.vote[s][(scount & 1)] = 1;
+        }
+        const float vs_now = see != 0 ? vsc : 0.0f;  // masked places may hold anything
+        if (F8) fetch_scales(i + 2);
+        ok = warps_sync(smem_u32(&t.wg_sync[s]), wg_phase, lane, abort, a.status);
+        if (!ok) break;
+        const bool raise = f.vote[s][scount & 1] != 0;
+        if (any) {  // O and the P buffer of this stream: its last product must be complete
+          ok = __all_sync(0xffffffffu, bar_wait(smem_u32(&t.pv_done[s]), (scount - 1) & 1, abort, a.status));
+          if (!ok) break;
+          fence_after();
+        }
+        if (raise) {
+          // New references: the warpgroup's maxima; then O and the sums to match.
+#pragma unroll
+          for (int r = 0; r < RP; ++r) {
+            const float v = redux_max(y[r]);
+            if (lane == 0) f.wmax[s][q][r] = v;
+          }
+          if (F8) {
+            const float v = redux_max(vs_now > 0.0f ? vs_now : 0.0f);
+            if (lane == 0) f.wvs[s][q] = v;
+          }
+          ok = warps_sync(smem_u32(&t.wg_sync[s]), wg_phase, lane, abort, a.status);
+          if (!ok) break;
+          float g = 1.0f, vnew = 0.0f;
+          if (F8) {
+            const float vold = f.vref[s];
+            const float vtop = fmaxf(fmaxf(f.wvs[s][0], f.wvs[s][1]), fmaxf(f.wvs[s][2], f.wvs[s][3]));
+            const unsigned up = (__float_as_uint(vtop) + 0x7fffffu) >> 23;  // power of two not below it
+            vnew = fmaxf(vold, vtop > 0.0f ? __int_as_float(max(1u, min(253u, up)) << 23) : 0.0f);
+            if (vnew > vold) g = vold / vnew;
+          }
+          if (wt < RP) {
+            const float top = fmaxf(fmaxf(f.wmax[s][0][wt], f.wmax[s][1][wt]),
+                                    fmaxf(f.wmax[s][2][wt], f.wmax[s][3][wt]));
+            const float old = f.mref[s][wt];
+            float fr = 1.0f;
+            if (wt < nrows && top > old + kLazy) {
+              f.mref[s][wt] = top;
+              fr = old == -INFINITY ? 0.0f : ex2_fast(old - top);
+            }
+            f.fac[s][wt] = fr;
+          }
+          ok = warps_sync(smem_u32(&t.wg_sync[s]), wg_phase, lane, abort, a.status);
+          if (!ok) break;
+          if (wt == 0) {
+            f.vote[s][scount & 1] = 0;
+            if (F8) f.vref[s] = vnew;
+          }
+#pragma unroll
+          for (int r = 0; r < RP; ++r) l[r] *= f.fac[s][r];
+          if (any) {
+#pragma unroll 1
+            for (int pc = 0; pc < (F8 ? 3 : 1); ++pc) {
+#pragma unroll 1
+              for (int r = 0; r < RP; r += 8) {
+                float v[8];
+                uint32_t o[8];
+                tmem_ld8(obase + pc * RP + r, v);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) o[j] = __float_as_uint(v[j] * (f.fac[s][r + j] * g));
+                tmem_st8(obase + pc * RP + r, o);
+              }
+            }
+            tmem_wait_st();
+          }
+          // f.vref and f.fac are read by all before the next change
+          ok = warps_sync(smem_u32(&t.wg_sync[s]), wg_phase, lane, abort, a.status);
+          if (!ok) break;
+        }
+        // Weights, their sums, and P^T: this key's 128 bytes, rows one after another.
+        float vs = 1.0f;
+        if (F8) {
+          const float vr = f.vref[s];
+          vs = vr > 0.0f ? vs_now * __fdividef(1.0f, vr) : 0.0f;
+          if (isnan(vs_now)) vs = vs_now;
+        }
+        uint32_t words[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) words[k] = 0;
+#pragma unroll
+        for (int r = 0; r < RP; r += 4) {
+          const float4 m4 = *reinterpret_cast<const float4*>(&f.mref[s][r]);
+          const float mm[4] = {m4.x, m4.y, m4.z, m4.w};
+          float p[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            // A row that has seen nothing yet has m = -inf: all its scores are -inf.
+            p[j] = ex2_fast(y[r + j] - (mm[j] == -INFINITY ? 0.0f : mm[j]));
+            l[r + j] += p[j];
+            if (F8) p[j] *= vs;
+            if (edge) p[j] = see >> (r + j) & 1ull ? p[j] : 0.0f;
+          }
+          if (F8) {
+            uint32_t c1 = 0, c2 = 0, c3 = 0;
+#pragma unroll
+            for (int j = 0; j < 4; j += 2) {
+              const __half2 h = __floats2half2_rn(p[j], p[j + 1]);
+              const uint32_t e1 = half2_to_e4m3(h);
+              const __half2 r1 = __hmul2(__hsub2(h, e4m3_to_half2(e1)), __half2half2(__ushort_as_half(0x4c00)));
+              const uint32_t e2 = half2_to_e4m3(r1);
+              const __half2 r2 = __hmul2(__hsub2(r1, e4m3_to_half2(e2)), __half2half2(__ushort_as_half(0x4c00)));
+              const uint32_t e3 = half2_to_e4m3(r2);
+              c1 |= e1 << (8 * j);
+              c2 |= e2 << (8 * j);
+              c3 |= e3 << (8 * j);
+            }
+            words[r / 4] = c1;
+            words[(RP + r) / 4] = c2;
+            if ((2 * RP + r) / 4 < 32) words[(2 * RP + r) / 4] = c3;
+          } else {
+            words[r / 2] = pack_bf16(p[0], p[1]);
+            words[r / 2 + 1] = pack_bf16(p[2], p[3]);
+          }
+        }
+        constexpr int kUnits = (F8 ? C::N2 : 2 * C::N2) / 16;
+        unsigned char* prow = pbuf + s * C::kPBytes + wt * 128;
+#pragma unroll
+        for (int k = 0; k < kUnits; ++k)
+          *reinterpret_cast<uint4*>(prow + ((k ^ (wt & 7)) << 4)) =
+              make_uint4(words[4 * k], words[4 * k + 1], words[4 * k + 2], words[4 * k + 3]);
+        if (edge) {
+          // 0 times what lies at masked positions must be 0: rows past the tree are zeroed, a
+          // node's NaN (or infinity) is taken out and given to its descendants at the end.
+          const unsigned ev = entry0 + few_v(i, n);
+          ok = __all_sync(0xffffffffu, bar_wait(smem_u32(&t.full[ev % C::kSlots]), (ev / C::kSlots) & 1, abort,
+                                                a.status));
+          if (!ok) break;
+          const long long nd = (long long)tile * KT + wt - w.ctx;
+          if (nd >= 0 || !seq_ok) {
+            unsigned char* vrow = ring + (ev % C::kSlots) * C::kSlot + wt * 128;
+            const bool dead = !seq_ok || nd >= a.T || par[nd] == -2;
+            for (int u = 0; u < (F8 ? 8 : 16); ++u) {
+              uint4* at = reinterpret_cast<uint4*>(vrow + (u >> 3) * KT * 128 + (((u & 7) ^ (wt & 7)) << 4));
+              uint4 v = dead ? make_uint4(0, 0, 0, 0) : *at;
+              uint32_t z[4] = {v.x, v.y, v.z, v.w};
+              bool found = dead;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                if (F8) {
+#pragma unroll
+                  for (int b = 0; b < 32; b += 8)
+                    if ((z[j] >> b & 0x7fu) == 0x7fu) z[j] &= ~(0xffu << b), found = true, t.badv[item & 1] = 1;
+                } else {
+                  if ((z[j] & 0x7f80u) == 0x7f80u) z[j] &= 0xffff0000u, found = true, t.badv[item & 1] = 1;
+                  if ((z[j] & 0x7f800000u) == 0x7f800000u) z[j] &= 0x0000ffffu, found = true, t.badv[item & 1] = 1;
+                }
+              }
+              if (found) *at = make_uint4(z[0], z[1], z[2], z[3]);
+            }
+          }
+        }
+        fence_async();
+        any = true;
+        ++scount;
+        fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(smem_u32(&t.p_ready[s]));
+      }
+      if (!ok) break;
+      entry0 += 2u * n;
+
+      // ---- the item's end
+#pragma unroll
+      for (int r = 0; r < RP; ++r) {
+        float v = l[r];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        if (lane == 0) f.wsum[s][q][r] = v;
+      }
+      ok = warps_sync(smem_u32(&t.all_sync), all_phase, lane, abort, a.status);
+      if (!ok) break;
+      // Both streams have read their last S: the next item's Q may go in.
+      Walk<KT> nx = w;
+      nx.next(a);
+      if (nx.more()) load_q(nx, (item + 1) & 1);
+      const bool bad = t.bad[item & 1] != 0, badv = t.badv[item & 1] != 0;
+      if (threadIdx.x < RP) {
+        const int r = threadIdx.x;
+        const float m0 = f.mref[0][r], m1 = n > 1 ? f.mref[1][r] : -INFINITY;
+        const float m = fmaxf(m0, m1);
+        const float g0 = m0 == -INFINITY ? 0.0f : ex2_fast(m0 - m), g1 = m1 == -INFINITY ? 0.0f : ex2_fast(m1 - m);
+        const float l0 = (f.wsum[0][0][r] + f.wsum[0][1][r]) + (f.wsum[0][2][r] + f.wsum[0][3][r]);
+        const float l1 = (f.wsum[1][0][r] + f.wsum[1][1][r]) + (f.wsum[1][2][r] + f.wsum[1][3][r]);
+        f.fin[r] = make_float4(F8 ? g0 * f.vref[0] : g0, F8 ? g1 * f.vref[1] : g1, m, l0 * g0 + l1 * g1);
+      }
+      if (any) {
+        ok = __all_sync(0xffffffffu, bar_wait(smem_u32(&t.pv_done[s]), (scount - 1) & 1, abort, a.status));
+        if (!ok) break;
+      }
+      fence_before();
+      ok = warps_sync(smem_u32(&t.all_sync), all_phase, lane, abort, a.status);
+      if (!ok) break;
+      fence_after();
+      if (threadIdx.x == 0) t.bad[(item + 1) & 1] = t.badv[(item + 1) & 1] = 0;
+      const bool whole = w.t0 == 0 && w.t1 == w.n;
+      const long long slot = (long long)group * 2 + (w.t0 == 0 ? 1 : 0);
+      for (int r0 = 8 * s; r0 < RP && r0 < nrows; r0 += 16) {
+        __syncwarp();  // tensor memory is read by whole warps
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+#pragma unroll
+        for (int st = 0; st < 2; ++st) {
+          if (st == 1 && n < 2) break;
+          float u[8];
+          tmem_ld8(tmem + lanes + C::kO + 128 * st + r0, u);
+          if (F8) {
+            float u2[8], u3[8];
+            tmem_ld8(tmem + lanes + C::kO + 128 * st + RP + r0, u2);
+            tmem_ld8(tmem + lanes + C::kO + 128 * st + 2 * RP + r0, u3);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) u[j] = __fmaf_rn(__fmaf_rn(u3[j], 0.0625f, u2[j]), 0.0625f, u[j]);
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float g = st ? f.fin[r0 + j].y : f.fin[r0 + j].x;
+            v[j] = g == 0.0f ? v[j] : __fmaf_rn(u[j], g, v[j]);
+          }
+        }
+        if (wt >= a.D) continue;
+        if (badv) {  // NaN and infinities of the nodes a row attends
+          for (int nd = 0; nd < a.T; ++nd) {
+            const long long pos = (long long)w.ctx + nd;
+            if (pos < (long long)w.t0 * KT || pos >= (long long)w.t1 * KT || pos / a.P >= a.max_pages) continue;
+            const int id = a.page_table[(long long)w.b * a.max_pages + pos / a.P];
+            if (id < 0 || id >= a.num_pages) continue;
+            const long long at = (((long long)id * a.Hkv + w.hk) * a.P + pos % a.P) * a.D + wt;
+            const float z = F8 ? ((static_cast<const unsigned char*>(a.vc)[at] & 0x7f) == 0x7f
+                                      ? __int_as_float(0x7fc00000)
+                                      : 0.0f)
+                               : __bfloat162float(static_cast<const __nv_bfloat16*>(a.vc)[at]);
+            if (isfinite(z)) continue;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (r0 + j < nrows && (anc[(r0 + j) / G] >> nd & 1ull)) v[j] += z;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int r = r0 + j;
+          if (r >= nrows) break;
+          const float4 fin = f.fin[r];
+          if (whole) {
+            const int node = r / G;
+            const bool dead = a.parents && a.parents[(long long)w.b * a.T + node] == -2;
+            const float o = bad ? __int_as_float(0x7fc00000)
+                                : (dead || fin.w == 0.0f ? 0.0f : v[j] * (1.0f / fin.w));
+            a.out[(((long long)w.b * a.T + node) * a.Hq + w.hk * G + r % G) * a.D + wt] = __float2bfloat16_rn(o);
+          } else {
+            x.part_o[(slot * nrows + r) * a.D + wt] = v[j];
+            if (wt == 0) x.part_ml[slot * nrows + r] = make_float2(bad ? __int_as_float(0x7fc00000) : fin.z, fin.w);
+          }
+        }
+      }
+      if (!whole) {
+        ok = join_parts(x, t, w, group, part, nrows, nrows, 256, all_phase, lane, abort);
+        if (!ok) break;
+      }
+      w = nx;
     }
   }
   fence_before();
@@ -1136,13 +1948,14 @@ bool tc_shape(int D, int page_size) {
 // tiles (D above 128: single tiles), a CTA each.
 struct Plan {
   int rows, rpt, parts, groups, cta_rows, pad;
-  bool shared;
+  bool shared, few;
   size_t off_counters, off_ml, off_o, total;
 };
 
 Plan make_plan(int T, int Hq, int Hkv, int D) {
   Plan p{};
   p.rows = T * (Hq / Hkv);
+  p.few = D <= 128 && p.rows <= kFewRows;
   p.shared = D <= 128 && p.rows > 128;
   if (p.shared) {
     p.parts = (p.rows + 255) / 256;
@@ -1182,7 +1995,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 
 // The cache as boxes of `box` tokens of one page and head: bf16 in columns of 64
 // with the 128-byte swizzle, codes in whole rows of DP.
-bool make_map(CUtensorMap* m, const void* base, const Args& a, bool f8, int dp, int box) {
+bool make_map(CUtensorMap* m, const void* base, const Args& a, bool f8, int dp, int box, bool swizzle) {
   auto fn = encode_fn();
   if (!fn) return false;
   const size_t es = f8 ? 1 : 2;
@@ -1192,7 +2005,7 @@ bool make_map(CUtensorMap* m, const void* base, const Args& a, bool f8, int dp, 
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   return fn(m, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
             const_cast<void*>(base), dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            f8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1213,10 +2026,34 @@ int launch_tc(const TcArgs& x, cudaStream_t st) {
     }
   }
   CUtensorMap mk, mv;
-  if (!make_map(&mk, x.a.kc, x.a, F8, DP, x.box) || !make_map(&mv, x.a.vc, x.a, F8, DP, x.box))
+  if (!make_map(&mk, x.a.kc, x.a, F8, DP, x.box, !F8) || !make_map(&mv, x.a.vc, x.a, F8, DP, x.box, !F8))
     return SV_ERR_CUDA;
   tree_attn_kernel<DP, F8, SHARED><<<(unsigned)(x.groups * x.parts_per_item), Cfg<DP, F8, SHARED>::kThreads, kSmem,
                                      st>>>(mk, mv, x);
+  return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+}
+
+template <int RP, bool F8>
+int launch_few(const TcArgs& x, cudaStream_t st) {
+  constexpr int kSmem = few_smem<RP, F8>();
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+  static std::mutex mu;
+  static bool set[64] = {};
+  int device = 0;
+  if (cudaGetDevice(&device) != cudaSuccess || device < 0 || device >= 64) return SV_ERR_CUDA;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!set[device]) {
+      if (cudaFuncSetAttribute(tree_attn_few_kernel<RP, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               kSmem) != cudaSuccess)
+        return SV_ERR_CUDA;
+      set[device] = true;
+    }
+  }
+  CUtensorMap mk, mv;
+  if (!make_map(&mk, x.a.kc, x.a, F8, 128, x.box, true) || !make_map(&mv, x.a.vc, x.a, F8, 128, x.box, true))
+    return SV_ERR_CUDA;
+  tree_attn_few_kernel<RP, F8><<<(unsigned)x.groups, FewCfg<RP, F8>::kThreads, kSmem, st>>>(mk, mv, x);
   return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 
@@ -1224,6 +2061,7 @@ template <bool F8>
 int launch_tc_any(TcArgs& x, const Plan& p, cudaStream_t st) {
   const int D = x.a.D;
   x.box = std::min(x.a.P, D > 128 ? 64 : 128);
+  if (p.few) return p.rows <= 16 ? launch_few<16, F8>(x, st) : launch_few<kFewRows, F8>(x, st);
   if (D > 128) return launch_tc<256, F8, false>(x, st);
   if (D > 64) return p.shared ? launch_tc<128, F8, true>(x, st) : launch_tc<128, F8, false>(x, st);
   return p.shared ? launch_tc<64, F8, true>(x, st) : launch_tc<64, F8, false>(x, st);
@@ -1301,6 +2139,7 @@ int sv_tree_attention(const void* q, int64_t q_stride_b, int64_t q_stride_t, int
     x.parts_per_item = p.parts;
     x.groups = p.groups;
     x.c = scale == 0.0f ? 1.0f : std::fabs(scale) * 1.4426950408889634f;
+    x.join_c = p.few ? 1.0f : x.c;
     x.qflip = scale < 0.0f ? 0x80008000u : 0u;
     x.qzero = scale == 0.0f;
     x.counters = reinterpret_cast<unsigned*>(ws + p.off_counters);
