@@ -137,9 +137,9 @@ SV_DEVINL void bar_arrive(unsigned bar) {
 SV_DEVINL bool bar_wait(unsigned bar, unsigned parity, volatile unsigned* abort, unsigned* status) {
   if (mbar_test_parity(bar, parity)) return true;
   const uint64_t t0 = global_ns();
-  for (unsigned i = 1;; ++i) {
+  for (unsigned i = 0;; ++i) {
     if (mbar_test_parity(bar, parity)) return true;
-    if ((i & 255) == 0) {
+    if ((i & 63) == 0) {
       if (*abort) return false;
       if (global_ns() - t0 > kWaitLimitNs) {
         atomicOr(status, (unsigned)SV_DEV_TIMEOUT);
@@ -148,6 +148,11 @@ SV_DEVINL bool bar_wait(unsigned bar, unsigned parity, volatile unsigned* abort,
       }
     }
   }
+}
+
+// The same by a whole warp, with one answer.
+SV_DEVINL bool warp_wait(unsigned bar, unsigned parity, volatile unsigned* abort, unsigned* status) {
+  return __all_sync(0xffffffffu, bar_wait(bar, parity, abort, status));
 }
 
 SV_DEVINL void tma_4d(unsigned dst, const CUtensorMap* map, int x, int y, int z, int w, unsigned bar) {
@@ -176,23 +181,44 @@ SV_DEVINL uint32_t idesc(int n, bool nmajor) {
          (8u << 24);
 }
 
-SV_DEVINL void mma_ss(unsigned d, uint64_t a, uint64_t b, uint32_t id, bool acc) {
+// The whole issuing warp runs these; `lead` is nonzero in the one lane that issues.
+// The operands are the same in every lane, and kept so for the compiler (uni), so
+// that they stay in uniform registers: issued from a branch of one lane, each
+// instruction took about 130 cycles.
+SV_DEVINL unsigned elect_lane() {
+  unsigned r;
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(id), "r"((unsigned)acc)
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r;
+}
+SV_DEVINL unsigned uni(unsigned v) { return __shfl_sync(0xffffffffu, v, 0); }
+SV_DEVINL void mma_ss(unsigned lead, unsigned d, uint64_t a, uint64_t b, uint32_t id, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"((unsigned)acc), "r"(lead)
       : "memory");
 }
-SV_DEVINL void mma_ts(unsigned d, unsigned a, uint64_t b, uint32_t id, bool acc) {
+SV_DEVINL void mma_ts(unsigned lead, unsigned d, unsigned a, uint64_t b, uint32_t id, bool acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(id), "r"((unsigned)acc)
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(id), "r"((unsigned)acc), "r"(lead)
       : "memory");
 }
-SV_DEVINL void commit(unsigned bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-               : "memory");
+SV_DEVINL void mma_f8(unsigned lead, unsigned d, uint64_t a, uint64_t b, uint32_t id, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"((unsigned)acc), "r"(lead)
+      : "memory");
+}
+SV_DEVINL void commit(unsigned lead, unsigned bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(lead)
+      : "memory");
 }
 SV_DEVINL void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 SV_DEVINL void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -371,18 +397,18 @@ SV_DEVINL void find_range(const TcArgs& x, TcTail& t, int group, int lane) {
 // Called by `threads` threads once their part of an item that is cut is written:
 // the last part to arrive joins them all, in the order of the ranges. `sum` and O of
 // a part are relative to its m (in units of 1/join_c powers of two); NaN marks a sequence at fault.
-template <int KT>
-SV_DEVINL bool join_parts(const TcArgs& x, TcTail& t, const Walk<KT>& w, int group, int part, int cta_rows,
-                          int rows_here, int threads, unsigned& phase, int lane, volatile unsigned* abort) {
+template <int KT, typename Sync>
+SV_DEVINL bool join_parts(const TcArgs& x, TcTail& t, const Walk<KT>& w, int part, int cta_rows, int rows_here,
+                          int threads, const Sync& sync) {
   const Args& a = x.a;
   const long long total = t.total;
   const int ng = t.groups, G = a.Hq / a.Hkv;
   const int gs = (int)(((w.base + 1) * ng - 1) / total), ge = (int)(((w.base + w.n) * ng - 1) / total);
   __threadfence();
-  if (!warps_sync(smem_u32(&t.all_sync), phase, lane, abort, a.status)) return false;
+  if (!sync()) return false;
   if (threadIdx.x == 0)
     t.last = atomicAdd(&x.counters[gs * x.parts_per_item + part], 1u) == (unsigned)(ge - gs);
-  if (!warps_sync(smem_u32(&t.all_sync), phase, lane, abort, a.status)) return false;
+  if (!sync()) return false;
   if (!t.last) return true;
   __threadfence();
   const int units = a.D / 4;
@@ -461,7 +487,7 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
   TcTail& t = *reinterpret_cast<TcTail*>(reinterpret_cast<unsigned char*>(scales) +
                                          (F8 ? kScaleSlots * 2 * KT * 4 : 0));
   const Args& a = x.a;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int group = blockIdx.x / x.parts_per_item, part = blockIdx.x % x.parts_per_item;
   constexpr int kSoft = NS * 4;  // softmax warps at work
 
@@ -592,47 +618,50 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
     }
   } else if (warp == kIssuer) {
     // ---- MMA
-    if (lane == 0) {
+    {
+      const unsigned lead = elect_lane();
       const uint32_t id_qk = idesc(KT, false), id_pv = idesc(a.D, true);
       const int ksteps = a.D / 16;
       unsigned entry0 = 0, item = 0;
       unsigned pcount[2] = {0, 0};   // P's awaited, by stream
       bool ok = true;
       auto full = [&](unsigned e) {
-        ok = ok && bar_wait(smem_u32(&t.full[e % C::kSlots]), (e / C::kSlots) & 1, abort, a.status);
+        ok = ok && warp_wait(smem_u32(&t.full[e % C::kSlots]), (e / C::kSlots) & 1, abort, a.status);
         if (ok) fence_after();
         return ok;
       };
       auto qk = [&](int s, unsigned e) {
         // S of this stream holds the last P until its product is complete.
         if (pcount[s] > 0)
-          ok = ok && bar_wait(smem_u32(&t.pv_done[s]), (pcount[s] - 1) & 1, abort, a.status);
+          ok = ok && warp_wait(smem_u32(&t.pv_done[s]), (pcount[s] - 1) & 1, abort, a.status);
         if (!ok) return;
         fence_after();
-        const unsigned q = smem_u32(smem + (SHARED ? s * C::kQBytes : 0));
-        const unsigned k = smem_u32(ring + (e % C::kSlots) * C::kSlot);
-        const unsigned d = tmem + (s ? C::kS1 : C::kS0);
-        for (int i = 0; i < ksteps; ++i)
-          mma_ss(d, desc_k(q + (i >> 2) * 128 * 128 + (i & 3) * 32),
-                 desc_k(k + (i >> 2) * KT * 128 + (i & 3) * 32), id_qk, i > 0);
+        const uint64_t q = desc_k(uni(smem_u32(smem + (SHARED ? s * C::kQBytes : 0))));
+        const uint64_t k = desc_k(uni(smem_u32(ring + (e % C::kSlots) * C::kSlot)));
+        const unsigned d = uni(tmem + (s ? C::kS1 : C::kS0));
+#pragma unroll
+        for (int i = 0; i < DP / 16; ++i)
+          if (i < ksteps)
+            mma_ss(lead, d, q + (((i >> 2) * 128 * 128 + (i & 3) * 32) >> 4),
+                   k + (((i >> 2) * KT * 128 + (i & 3) * 32) >> 4), id_qk, i > 0);
       };
       auto pv = [&](int s, unsigned e, bool acc) {
-        const unsigned v = smem_u32(ring + (e % C::kSlots) * C::kSlot);
-        const unsigned p = tmem + (s ? C::kS1 : C::kS0), d = tmem + (s ? C::kO1 : C::kO0);
+        const uint64_t v = desc_n(uni(smem_u32(ring + (e % C::kSlots) * C::kSlot)), KT * 128);
+        const unsigned p = uni(tmem + (s ? C::kS1 : C::kS0)), d = uni(tmem + (s ? C::kO1 : C::kO0));
 #pragma unroll
         for (int i = 0; i < KT / 16; ++i)
-          mma_ts(d, p + i * 8, desc_n(v + i * 2048, KT * 128), id_pv, acc || i > 0);
+          mma_ts(lead, d, p + i * 8, v + ((i * 2048) >> 4), id_pv, acc || i > 0);
       };
       auto p_wait = [&](int s) {
-        ok = ok && bar_wait(smem_u32(&t.p_ready[s]), pcount[s] & 1, abort, a.status);
+        ok = ok && warp_wait(smem_u32(&t.p_ready[s]), pcount[s] & 1, abort, a.status);
         if (ok) fence_after();
         ++pcount[s];
         return ok;
       };
-      auto release = [&](unsigned e) { commit(smem_u32(&t.empty[e % C::kSlots])); };
+      auto release = [&](unsigned e) { commit(lead, smem_u32(&t.empty[e % C::kSlots])); };
       for (; w.more() && ok; w.next(a), ++item) {
         const int n = w.t1 - w.t0;
-        ok = ok && bar_wait(smem_u32(&t.q_ready), item & 1, abort, a.status);
+        ok = ok && warp_wait(smem_u32(&t.q_ready), item & 1, abort, a.status);
         if (!ok) break;
         fence_after();
         if (ALT) {
@@ -642,7 +671,7 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
             qk(i, e);
             if (!ok) break;
             release(e);
-            commit(smem_u32(&t.s_ready[i]));
+            commit(lead, smem_u32(&t.s_ready[i]));
           }
           for (int i = 0; i < n && ok; ++i) {
             const int s = i & 1;
@@ -650,14 +679,14 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
             if (!full(ev) || !p_wait(s)) break;
             pv(s, ev, i >= 2);
             release(ev);
-            commit(smem_u32(&t.pv_done[s]));
+            commit(lead, smem_u32(&t.pv_done[s]));
             if (i + 2 < n) {
               const unsigned e = entry0 + k_entry<true>(i + 2);
               if (!full(e)) break;
               qk(s, e);
               if (!ok) break;
               release(e);
-              commit(smem_u32(&t.s_ready[s]));
+              commit(lead, smem_u32(&t.s_ready[s]));
             }
           }
         } else {
@@ -668,7 +697,7 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
                 if (!full(ev) || !p_wait(s)) break;
                 pv(s, ev, i > 0);
                 if (s == NS - 1) release(ev);
-                commit(smem_u32(&t.pv_done[s]));
+                commit(lead, smem_u32(&t.pv_done[s]));
               }
               if (i + 1 < n) {
                 const unsigned e = entry0 + 2u * (i + 1);
@@ -676,7 +705,7 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
                 qk(s, e);
                 if (!ok) break;
                 if (s == NS - 1) release(e);
-                commit(smem_u32(&t.s_ready[s]));
+                commit(lead, smem_u32(&t.s_ready[s]));
               }
             }
           }
@@ -1017,7 +1046,9 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
       }
       if (!whole) {
         const int rows_here = SHARED ? cta_rows : nrows;
-        ok = join_parts(x, t, w, group, part, cta_rows, rows_here, NS * 128, all_phase, lane, abort);
+        ok = join_parts(x, t, w, part, cta_rows, rows_here, NS * 128, [&] {
+          return warps_sync(smem_u32(&t.all_sync), all_phase, lane, abort, a.status);
+        });
         if (!ok) break;
       }
     }
@@ -1081,28 +1112,30 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
 // rows as its N, so the tensor cores and the softmax work on the rows that exist.
 // One thread a key holds that key's scores of all rows, its scales and its
 // mask; the maximum of a row is not needed, only a reference m that no score
-// exceeds by more than 2^8: a vote of the warpgroup finds the rare tile that does, and only
-// then are maxima taken across the threads and O rescaled. P^T goes to shared
-// memory as the other operand of O^T = V^T P^T (M = 128 channels of the head).
-// A row's sum is kept by each thread for its keys and joined at the item's end.
+// exceeds by more than 2^8 (e4m3: 2^2): a vote of the warpgroup finds the rare tile that
+// does, and only then are maxima taken across the threads and O rescaled. P^T goes to
+// shared memory as the other operand of O^T = V^T P^T (M = 128 channels of the
+// head). A row's sum is kept by each thread for its keys and joined at the item's end.
 //
 // An e4m3 cache feeds the tensor cores as it is (kind::f8f6f4), with no pass to
-// convert it: Q and P enter as sums of e4m3 pieces, each piece with columns of
-// its own. Q scaled by a power of two to at most 448 is hi + lo/16, exact but for
-// elements below 2^-15 of the row's largest, which are off by up to 2^-22 of that. P
-// times the value's scale (over a power of two not below any scale) is p1 + p2/16 + p3/256,
-// off by at most 2^-12 of itself or 2^-18 against a largest weight of 1 to 2^8.
-// A bf16 cache uses bf16 operands, P rounded once (2^-8).
+// convert it: Q and P enter as sums of e4m3 pieces. Q, scaled by a power of two to
+// (224, 448], is hi + lo, exact for elements above 2^-10 of the row's largest and off by
+// 2^-19 of that at most below; both multiply into the same columns. P, times 2^6 and the value's
+// scale over a power of two not below any scale seen, is p1 + p2/16 + p3/256 with columns of
+// O for each piece: off by at most 2^-12 of itself or, for small weights, 2^-24 of the
+// reference weight. A bf16 cache uses bf16 operands, P rounded once (2^-8).
 //
 // Streams, ranges and parts are those of the kernel above; the next tile's
-// S^T is issued before this tile's O^T, so neither waits for the other.
+// S^T is issued before this tile's O^T, so neither waits for the other. The softmax
+// warps meet at hardware barriers, so none of them leaves early: once a wait
+// has run out they only count their tiles down.
 
 template <int RP, bool F8>
 struct FewCfg {
   static constexpr int KT = 128;
-  static constexpr int N1 = F8 ? 2 * RP : (RP + 15) / 16 * 16;         // columns of S^T
-  static constexpr int N2 = F8 ? (3 * RP + 15) / 16 * 16 : N1;         // columns of O^T
-  static constexpr int kQBytes = N1 * 128 * (F8 ? 1 : 2);
+  static constexpr int N1 = (RP + 15) / 16 * 16;                // columns of S^T
+  static constexpr int N2 = F8 ? (3 * RP + 15) / 16 * 16 : N1;  // columns of O^T
+  static constexpr int kQBytes = N1 * 128 * 2;                  // two blocks: channels (bf16) or pieces
   static constexpr int kPBytes = KT * 128;
   static constexpr int kSlot = KT * (F8 ? 128 : 256);
   static constexpr int kTailBytes = 12 * 1024;
@@ -1110,7 +1143,11 @@ struct FewCfg {
   static constexpr int kSlots = kFit < kMaxSlots ? kFit : kMaxSlots;
   static constexpr int kThreads = 320;
   static constexpr unsigned kS = 0, kO = 256;  // tensor memory: two of each, 128 columns apart
+  static constexpr float kGrow = F8 ? 2.0f : 8.0f;
+  static constexpr float kLift = F8 ? 64.0f : 1.0f;
 };
+
+constexpr float kNoScore = -1e30f;  // reference of a row that has seen no key
 
 template <int RP>
 struct FewTail {
@@ -1119,27 +1156,33 @@ struct FewTail {
   // Arrays that are read four values at a time lie on 16-byte boundaries.
   alignas(16) float mref[2][RP];     // [stream] references, powers of two
   alignas(16) float fac[2][RP];      // [stream] factors of a rescaling
-  float wmax[2][4][RP], wsum[2][4][RP], wvs[2][4];
-  float vref[2];
   alignas(16) float qc[2][RP];       // [item parity] c over the row's scale of Q
   float4 fin[RP];
-  unsigned vote[2][2];               // [stream][tile parity]
+  float wmax[2][4][RP], wsum[2][4][RP], wvs[2][4];
+  float vref[2];
 };
 
 template <int RP, bool F8>
 constexpr int few_smem() {
   using C = FewCfg<RP, F8>;
   static_assert(sizeof(FewTail<RP>) <= C::kTailBytes, "tail");
-  static_assert(RP % 8 == 0 && C::kQBytes % 1024 == 0, "rows of four values, blocks of 1024 bytes");
+  static_assert(RP % 8 == 0 && C::kQBytes % 2048 == 0, "rows of four values, blocks of 1024 bytes");
   return 1024 + C::kQBytes + 2 * C::kPBytes + C::kSlots * C::kSlot + (int)sizeof(FewTail<RP>);
 }
 
-SV_DEVINL void mma_f8(unsigned d, uint64_t a, uint64_t b, uint32_t id, bool acc) {
+// Hardware barrier of `threads` threads, and the OR of their predicates.
+SV_DEVINL void named_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+SV_DEVINL bool named_any(int id, int threads, bool v) {
+  unsigned r;
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(id), "r"((unsigned)acc)
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, %2, %3, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((unsigned)v), "r"(id), "r"(threads)
       : "memory");
+  return r != 0;
 }
 
 SV_DEVINL float redux_max(float v) {
@@ -1165,10 +1208,7 @@ SV_DEVINL __half2 e4m3_to_half2(uint32_t c) {
 
 template <int N>
 SV_DEVINL void tmem_ld_cols(unsigned t, float* v) {
-  if constexpr (N >= 64) {
-    tmem_ld64(t, v);
-    if constexpr (N > 64) tmem_ld_cols<N - 64>(t + 64, v + 64);
-  } else if constexpr (N >= 32) {
+  if constexpr (N >= 32) {
     tmem_ld32(t, v);
     if constexpr (N > 32) tmem_ld_cols<N - 32>(t + 32, v + 32);
   } else if constexpr (N >= 16) {
@@ -1197,12 +1237,12 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
                                                          ~static_cast<uintptr_t>(1023));
   unsigned char* pbuf = smem;                          // [2][128 keys][128 bytes]
   unsigned char* ring = pbuf + 2 * C::kPBytes;
-  unsigned char* qbuf = ring + C::kSlots * C::kSlot;   // [blocks of 128 bytes][N1 rows]
+  unsigned char* qbuf = ring + C::kSlots * C::kSlot;   // [2 blocks][N1 rows][128 bytes]
   FewTail<RP>& f = *reinterpret_cast<FewTail<RP>*>(qbuf + C::kQBytes);
   TcTail& t = f.t;
   const Args& a = x.a;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int group = blockIdx.x, part = 0;
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  const int group = blockIdx.x;
   constexpr int kSoft = 8;
 
   if (warp == 0) {
@@ -1217,10 +1257,7 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
       mbar_init(smem_u32(&t.s_ready[i]), 1);
       mbar_init(smem_u32(&t.p_ready[i]), 4);
       mbar_init(smem_u32(&t.pv_done[i]), 1);
-      mbar_init(smem_u32(&t.wg_sync[i]), 4);
-      f.vote[i][0] = f.vote[i][1] = 0;
     }
-    mbar_init(smem_u32(&t.all_sync), kSoft);
     t.abort = 0;
     t.bad[0] = t.bad[1] = t.badv[0] = t.badv[1] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -1263,9 +1300,8 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
         if (page < 0 || page >= a.num_pages) page = -1;
         const unsigned hit = __ballot_sync(0xffffffffu, page >= 0);
         const int s = (int)(entry % C::kSlots);
-        ok = __all_sync(0xffffffffu, entry < (unsigned)C::kSlots ||
-                                         bar_wait(smem_u32(&t.empty[s]), ((entry / C::kSlots) & 1) ^ 1, abort,
-                                                  a.status));
+        ok = entry < (unsigned)C::kSlots ||
+             warp_wait(smem_u32(&t.empty[s]), ((entry / C::kSlots) & 1) ^ 1, abort, a.status);
         if (!ok) break;
         const unsigned bar = smem_u32(&t.full[s]);
         const unsigned dst = smem_u32(ring + s * C::kSlot) + lane * x.box * 128;
@@ -1278,7 +1314,7 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
         }
       }
     }
-    if (*abort) {
+    if (*abort) {  // copies in flight must land before the shared memory goes
       for (int i = 0; i < C::kSlots && entry >= (unsigned)i + 1; ++i) {
         const unsigned e = entry - 1 - i;
         const uint64_t t0 = global_ns();
@@ -1288,67 +1324,71 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
       }
     }
   } else if (warp == kIssuer) {
-    if (lane == 0) {
-      // fp32 accumulator, M = 128; A and B bf16 or e4m3 (code 0).
-      constexpr uint32_t kTypes = F8 ? 0u : (1u << 7) | (1u << 10);
-      constexpr uint32_t id_qk = (1u << 4) | kTypes | ((uint32_t)(C::N1 >> 3) << 17) | (8u << 24);
-      constexpr uint32_t id_pv =
-          (1u << 4) | kTypes | (1u << 15) | (1u << 16) | ((uint32_t)(C::N2 >> 3) << 17) | (8u << 24);
-      const int ksteps = F8 ? (a.D + 31) / 32 : a.D / 16;
-      unsigned entry0 = 0, item = 0, pcount[2] = {0, 0};
-      bool ok = true;
-      auto full = [&](unsigned e) {
-        ok = ok && bar_wait(smem_u32(&t.full[e % C::kSlots]), (e / C::kSlots) & 1, abort, a.status);
-        if (ok) fence_after();
-        return ok;
-      };
-      auto qk = [&](int i) {
-        const unsigned e = entry0 + few_k(i);
-        if (!full(e)) return;
-        const unsigned k = smem_u32(ring + (e % C::kSlots) * C::kSlot), q = smem_u32(qbuf);
-        const unsigned d = tmem + C::kS + 128 * (i & 1);
-        for (int j = 0; j < ksteps; ++j) {
-          const unsigned off = (j & 3) * 32;
-          if (F8)
-            mma_f8(d, desc_k(k + off), desc_k(q + off), id_qk, j > 0);
-          else
-            mma_ss(d, desc_k(k + (j >> 2) * KT * 128 + off), desc_k(q + (j >> 2) * C::N1 * 128 + off), id_qk,
+    const unsigned lead = elect_lane();
+    // fp32 accumulator, M = 128; A and B bf16 or e4m3 (code 0).
+    constexpr uint32_t kTypes = F8 ? 0u : (1u << 7) | (1u << 10);
+    constexpr uint32_t id_qk = (1u << 4) | kTypes | ((uint32_t)(C::N1 >> 3) << 17) | (8u << 24);
+    constexpr uint32_t id_pv = (1u << 4) | kTypes | (1u << 15) | (1u << 16) | ((uint32_t)(C::N2 >> 3) << 17) | (8u << 24);
+    const int ksteps = F8 ? (a.D + 31) / 32 : a.D / 16;
+    const uint64_t q = desc_k(uni(smem_u32(qbuf)));
+    unsigned entry0 = 0, item = 0, pcount[2] = {0, 0};
+    bool ok = true;
+    auto full = [&](unsigned e) {
+      ok = ok && warp_wait(smem_u32(&t.full[e % C::kSlots]), (e / C::kSlots) & 1, abort, a.status);
+      if (ok) fence_after();
+      return ok;
+    };
+    auto qk = [&](int i) {
+      const unsigned e = entry0 + few_k(i);
+      if (!full(e)) return;
+      const uint64_t k = desc_k(uni(smem_u32(ring + (e % C::kSlots) * C::kSlot)));
+      const unsigned d = uni(tmem + C::kS + 128 * (i & 1));
+      if (F8) {  // the pieces of Q one after the other
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if ((j & 3) < ksteps)
+            mma_f8(lead, d, k + (j & 3) * 2, q + (j >> 2) * (C::N1 * 8) + (j & 3) * 2, id_qk, j > 0);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j < ksteps)
+            mma_ss(lead, d, k + (j >> 2) * (KT * 8) + (j & 3) * 2, q + (j >> 2) * (C::N1 * 8) + (j & 3) * 2, id_qk,
                    j > 0);
-        }
-        commit(smem_u32(&t.empty[e % C::kSlots]));
-        commit(smem_u32(&t.s_ready[i & 1]));
-      };
-      for (; w.more() && ok; w.next(a), ++item) {
-        const int n = w.t1 - w.t0;
-        ok = ok && bar_wait(smem_u32(&t.q_ready), item & 1, abort, a.status);
+      }
+      commit(lead, smem_u32(&t.s_ready[i & 1]));
+      commit(lead, smem_u32(&t.empty[e % C::kSlots]));
+    };
+    for (; w.more() && ok; w.next(a), ++item) {
+      const int n = w.t1 - w.t0;
+      ok = ok && warp_wait(smem_u32(&t.q_ready), item & 1, abort, a.status);
+      if (!ok) break;
+      fence_after();
+      qk(0);
+      if (n > 1 && ok) qk(1);
+      for (int i = 0; i < n && ok; ++i) {
+        const int s = i & 1;
+        ok = ok && warp_wait(smem_u32(&t.p_ready[s]), pcount[s] & 1, abort, a.status);
         if (!ok) break;
         fence_after();
-        qk(0);
-        if (n > 1 && ok) qk(1);
-        for (int i = 0; i < n && ok; ++i) {
-          const int s = i & 1;
-          ok = ok && bar_wait(smem_u32(&t.p_ready[s]), pcount[s] & 1, abort, a.status);
-          if (!ok) break;
-          fence_after();
-          ++pcount[s];
-          if (i + 2 < n) qk(i + 2);
-          const unsigned e = entry0 + few_v(i, n);
-          if (!ok || !full(e)) break;
-          const unsigned v = smem_u32(ring + (e % C::kSlots) * C::kSlot), p = smem_u32(pbuf + s * C::kPBytes);
-          const unsigned d = tmem + C::kO + 128 * s;
+        ++pcount[s];
+        if (i + 2 < n) qk(i + 2);
+        const unsigned e = entry0 + few_v(i, n);
+        if (!ok || !full(e)) break;
+        const uint64_t v = desc_n(uni(smem_u32(ring + (e % C::kSlots) * C::kSlot)), KT * 128);
+        const uint64_t p = desc_n(uni(smem_u32(pbuf + s * C::kPBytes)), KT * 128);
+        const unsigned d = uni(tmem + C::kO + 128 * s);
 #pragma unroll
-          for (int j = 0; j < (F8 ? 4 : 8); ++j) {
-            const unsigned off = j * (F8 ? 4096 : 2048);
-            if (F8)
-              mma_f8(d, desc_n(v + off, KT * 128), desc_n(p + off, KT * 128), id_pv, i > 1 || j > 0);
-            else
-              mma_ss(d, desc_n(v + off, KT * 128), desc_n(p + off, KT * 128), id_pv, i > 1 || j > 0);
-          }
-          commit(smem_u32(&t.empty[e % C::kSlots]));
-          commit(smem_u32(&t.pv_done[s]));
+        for (int j = 0; j < (F8 ? 4 : 8); ++j) {
+          const unsigned off = j * (F8 ? 4096 : 2048) >> 4;
+          if (F8)
+            mma_f8(lead, d, v + off, p + off, id_pv, i > 1 || j > 0);
+          else
+            mma_ss(lead, d, v + off, p + off, id_pv, i > 1 || j > 0);
         }
-        entry0 += 2u * n;
+        commit(lead, smem_u32(&t.pv_done[s]));
+        commit(lead, smem_u32(&t.empty[e % C::kSlots]));
       }
+      entry0 += 2u * n;
     }
   } else if (warp < kSoft) {
     const int s = warp >> 2, q = warp & 3;
@@ -1357,140 +1397,149 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
     const unsigned sbase = tmem + lanes + C::kS + 128 * s;
     const unsigned obase = tmem + lanes + C::kO + 128 * s;
     const int G = a.Hq / a.Hkv, nrows = x.rows;
-    unsigned item = 0, scount = 0, entry0 = 0, wg_phase = 0, all_phase = 0;
-    bool ok = true;
+    unsigned item = 0, scount = 0, entry0 = 0;
+    auto wait = [&](unsigned long long* bar, unsigned parity) { bar_wait(smem_u32(bar), parity, abort, a.status); };
 
-    // Q of an item into shared memory (e4m3: as two pieces): a warp a row.
-    auto load_q = [&](const Walk<KT>& it, unsigned parity) {
-      for (int r = warp; r < RP; r += kSoft) {
-        const bool on = r < nrows && !x.qzero;
-        uint2 v = make_uint2(0, 0);  // four elements a lane
-        if (on && lane * 4 < a.D)
-          v = *reinterpret_cast<const uint2*>(a.q + it.b * a.q_sb + (long long)(r / G) * a.q_st +
-                                              (long long)(it.hk * G + r % G) * a.q_sh + lane * 4);
-        v.x ^= x.qflip;
-        v.y ^= x.qflip;
-        if (!on) v = make_uint2(0, 0);
-        if (F8) {
-          float e[4] = {bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y)};
-          float top = fmaxf(fmaxf(fabsf(e[0]), fabsf(e[1])), fmaxf(fabsf(e[2]), fabsf(e[3])));
-          top = redux_max(top);
-          // 2^k with top 2^k in [128, 256); rows of zeros, infinities or NaN as they are.
-          int k = 134 - (int)(__float_as_uint(top) >> 23);
-          if (!(top > 0.0f) || !(top < INFINITY)) k = 0;
-          k = max(-126, min(126, k));
-          const float up = __int_as_float((k + 127) << 23), down = __int_as_float((127 - k) << 23);
-          uint32_t hi = 0, lo = 0;
+    // Q of an item: eight lanes a row, 16 values each; fetched early, stored when the
+    // products with the last Q are done.
+    constexpr int kQPasses = (C::N1 + 31) / 32;
+    uint4 qv[kQPasses][2];
+    auto fetch_q = [&](const Walk<KT>& it) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float y = e[j] * up;
-            const uint32_t h = __nv_cvt_float_to_fp8(y, __NV_SATFINITE, __NV_E4M3);
-            const float back = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)h, __NV_E4M3)));
-            const uint32_t l = __nv_cvt_float_to_fp8((y - back) * 16.0f, __NV_SATFINITE, __NV_E4M3);
-            // e4m3 has no infinity: one in Q counts as NaN.
-            hi |= (isinf(y) ? 0x7fu : h) << (8 * j);
-            lo |= (isfinite(y) ? l : 0x7fu) << (8 * j);
-          }
-          const int u = lane >> 2;
-          *reinterpret_cast<uint32_t*>(qbuf + r * 128 + ((u ^ (r & 7)) << 4) + (lane & 3) * 4) = hi;
-          const int r2 = r + RP;
-          *reinterpret_cast<uint32_t*>(qbuf + r2 * 128 + ((u ^ (r2 & 7)) << 4) + (lane & 3) * 4) = lo;
-          if (lane == 0) f.qc[parity][r] = x.c * down;
-        } else {
-          const int u = lane >> 1;  // 16-byte unit of the row
-          *reinterpret_cast<uint2*>(qbuf + (u >> 3) * C::N1 * 128 + r * 128 + (((u & 7) ^ (r & 7)) << 4) +
-                                    (lane & 1) * 8) = v;
-          if (lane == 0) f.qc[parity][r] = x.c;
+      for (int k = 0; k < kQPasses; ++k) {
+        const int r = (threadIdx.x >> 3) + 32 * k, u = threadIdx.x & 7;
+        qv[k][0] = qv[k][1] = make_uint4(0, 0, 0, 0);
+        if (r < nrows && !x.qzero && u * 16 < a.D) {
+          const uint4* at = reinterpret_cast<const uint4*>(a.q + it.b * a.q_sb + (long long)(r / G) * a.q_st +
+                                                           (long long)(it.hk * G + r % G) * a.q_sh + u * 16);
+          qv[k][0] = at[0];
+          qv[k][1] = at[1];
         }
       }
-      if (!F8) {  // rows that pad the columns to a multiple of 16
-        for (int r = RP + warp; r < C::N1; r += kSoft) {
-          const int u = lane >> 1;
-          *reinterpret_cast<uint2*>(qbuf + (u >> 3) * C::N1 * 128 + r * 128 + (((u & 7) ^ (r & 7)) << 4) +
-                                    (lane & 1) * 8) = make_uint2(0, 0);
+    };
+    auto put_q = [&](unsigned parity) {
+#pragma unroll
+      for (int k = 0; k < kQPasses; ++k) {
+        const int r = (threadIdx.x >> 3) + 32 * k, u = threadIdx.x & 7;
+        uint32_t z[8] = {qv[k][0].x, qv[k][0].y, qv[k][0].z, qv[k][0].w,
+                         qv[k][1].x, qv[k][1].y, qv[k][1].z, qv[k][1].w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) z[j] ^= x.qflip;
+        float down = 1.0f;
+        if (F8) {
+          float top = 0.0f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) top = fmaxf(top, fmaxf(fabsf(bf16_lo(z[j])), fabsf(bf16_hi(z[j]))));
+#pragma unroll
+          for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          // 2^e with top 2^e in (224, 448]; rows of zeros or with infinities as they are.
+          const unsigned bits = __float_as_uint(top);
+          int e = ((bits & 0x7fffffu) > 0x600000u ? 134 : 135) - (int)(bits >> 23);
+          if (!(top > 0.0f) || !(top < INFINITY)) e = 0;
+          e = max(-126, min(126, e));
+          const float up = __int_as_float((e + 127) << 23);
+          down = __int_as_float((127 - e) << 23);
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float y0 = bf16_lo(z[j]) * up, y1 = bf16_hi(z[j]) * up;
+            const uint32_t h = __nv_cvt_float2_to_fp8x2(make_float2(y0, y1), __NV_SATFINITE, __NV_E4M3);
+            const float2 back = __half22float2(e4m3_to_half2(h));
+            const uint32_t l =
+                __nv_cvt_float2_to_fp8x2(make_float2(y0 - back.x, y1 - back.y), __NV_SATFINITE, __NV_E4M3);
+            // e4m3 has no infinity: an infinite element counts as NaN.
+            const uint32_t nan = (isfinite(y0) ? 0u : 0x7fu) | (isfinite(y1) ? 0u : 0x7f00u);
+            if (j & 1) {
+              hi[j >> 1] |= (h | nan) << 16;
+              lo[j >> 1] |= (l | nan) << 16;
+            } else {
+              hi[j >> 1] = h | nan;
+              lo[j >> 1] = l | nan;
+            }
+          }
+          if (r < C::N1) {
+            unsigned char* at = qbuf + r * 128 + ((u ^ (r & 7)) << 4);
+            *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(at + C::N1 * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          }
+        } else if (r < C::N1) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int c = 2 * u + h;
+            *reinterpret_cast<uint4*>(qbuf + (c >> 3) * C::N1 * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
+                make_uint4(z[4 * h], z[4 * h + 1], z[4 * h + 2], z[4 * h + 3]);
+          }
         }
+        if (u == 0 && r < RP) f.qc[parity][r] = x.c * down;
       }
       fence_async();
       fence_before();
       __syncwarp();
       if (lane == 0) bar_arrive(smem_u32(&t.q_ready));
     };
-    if (w.more()) load_q(w, 0);
+    if (w.more()) {
+      fetch_q(w);
+      put_q(0);
+    }
 
-    for (; w.more() && ok; ++item) {
+    for (; w.more(); ++item) {
       const int n = w.t1 - w.t0;
       const bool seq_ok = ctx_ok(a, w.ctx);
       const bool tail = seq_ok && (long long)w.t1 * KT > w.ctx;
       int* par = t.par[item & 1][s];
       unsigned long long* anc = f.anc[item & 1][s];
       const float* qc = f.qc[item & 1];
-      if (wt < RP) f.mref[s][wt] = wt < nrows ? -INFINITY : 0.0f;
+      const float* mref = f.mref[s];
+      if (wt < RP) f.mref[s][wt] = wt < nrows ? kNoScore : 0.0f;
       if (wt == 0) f.vref[s] = 0.0f;
-      {
-        unsigned bad = seq_ok ? 0u : (unsigned)SV_DEV_PAGE_RANGE;
-        if (tail && wt < a.T) par[wt] = a.parents ? a.parents[(long long)w.b * a.T + wt] : wt - 1;
-        ok = warps_sync(smem_u32(&t.wg_sync[s]), wg_phase, lane, abort, a.status);
-        if (!ok) break;
-        if (tail) {
-          if (wt < a.T) {
-            const int p = par[wt];
-            if (p < -2 || p >= wt || (p >= 0 && par[p] == -2)) bad |= SV_DEV_TREE;
-            unsigned long long set = 0;
-            for (int j = wt, left = a.T; j >= 0 && left > 0; --left) {
-              const int pj = par[j];
-              if (pj == -2) break;
-              set |= 1ull << j;
-              j = pj < j ? pj : -1;
-            }
-            anc[wt] = set;
+      unsigned bad = seq_ok ? 0u : (unsigned)SV_DEV_PAGE_RANGE;
+      // Page of this thread's key in tile i of the item, -1 for none.
+      auto page_of = [&](int i) -> int {
+        const long long pos = (long long)(w.t0 + i) * KT + wt;
+        if (!seq_ok || i >= n || pos >= (long long)w.ctx + a.T || pos / a.P >= a.max_pages) return -1;
+        return a.page_table[(long long)w.b * a.max_pages + pos / a.P];
+      };
+      // Its scales.
+      auto scales_of = [&](int i, int id, float* k, float* v) {
+        *k = *v = 0.0f;
+        if (!F8 || id < 0 || id >= a.num_pages) return;
+        const long long at =
+            ((long long)id * a.Hkv + w.hk) * a.P + (int)(((long long)(w.t0 + i) * KT + wt) % a.P);
+        *k = __ldg(a.ks + at);
+        *v = __ldg(a.vs + at);
+      };
+      int id = page_of(s), id_next = page_of(s + 2);
+      if (tail && wt < a.T) par[wt] = a.parents ? a.parents[(long long)w.b * a.T + wt] : wt - 1;
+      float ksc, vsc;
+      scales_of(s, id, &ksc, &vsc);
+      named_sync(1 + s, 128);
+      if (tail) {
+        if (wt < a.T) {
+          const int p = par[wt];
+          if (p < -2 || p >= wt || (p >= 0 && par[p] == -2)) bad |= SV_DEV_TREE;
+          unsigned long long set = 0;
+          for (int j = wt, left = a.T; j >= 0 && left > 0; --left) {
+            const int pj = par[j];
+            if (pj == -2) break;
+            set |= 1ull << j;
+            j = pj < j ? pj : -1;
           }
-          ok = warps_sync(smem_u32(&t.wg_sync[s]), wg_phase, lane, abort, a.status);
-          if (!ok) break;
+          anc[wt] = set;
         }
-        if (seq_ok && s == 0) {
-          const int p0 = (int)((long long)w.t0 * KT / a.P);
-          const int p1 = (int)min(((long long)w.t1 * KT + a.P - 1) / a.P, ((long long)w.ctx + a.T + a.P - 1) / a.P);
-          for (int p = p0 + wt; p < p1; p += 128) {
-            bool used = (long long)p * a.P < w.ctx;
-            if (!used) {
-              const int j1 = min((long long)a.T, (long long)(p + 1) * a.P - w.ctx);
-              for (int j = max(0, p * a.P - w.ctx); j < j1 && !used; ++j) used = par[j] != -2;
-            }
-            if (!used) continue;
-            const int id = p < a.max_pages ? a.page_table[(long long)w.b * a.max_pages + p] : -1;
-            if (id < 0 || id >= a.num_pages) bad |= SV_DEV_PAGE_RANGE;
-          }
-        }
-        if (bad) {
-          atomicOr(&t.bad[item & 1], 1u);
-          atomicOr(a.status, bad);
-        }
+        named_sync(1 + s, 128);
       }
 
       float l[RP];
 #pragma unroll
       for (int r = 0; r < RP; ++r) l[r] = 0.0f;
       bool any = false;
-      // Scales of this thread's key, one of the stream's tiles ahead.
-      float ksc = 1.0f, vsc = 1.0f;
-      auto fetch_scales = [&](int i) {
-        ksc = vsc = 0.0f;
-        const long long pos = (long long)(w.t0 + i) * KT + wt;
-        if (!seq_ok || i >= n || pos >= (long long)w.ctx + a.T || pos / a.P >= a.max_pages) return;
-        const int id = a.page_table[(long long)w.b * a.max_pages + pos / a.P];
-        if (id < 0 || id >= a.num_pages) return;
-        const long long at = ((long long)id * a.Hkv + w.hk) * a.P + pos % a.P;
-        ksc = __ldg(a.ks + at);
-        vsc = __ldg(a.vs + at);
-      };
-      if (F8) fetch_scales(s);
       for (int i = s; i < n; i += 2) {
         const int tile = w.t0 + i;
         const bool edge = (long long)(tile + 1) * KT > w.ctx || !seq_ok;
         // Rows that attend this thread's key.
         unsigned long long see = ~0ull;
+        const long long nd = (long long)tile * KT + wt - w.ctx;  // the key's node
         if (edge) {
-          const long long nd = (long long)tile * KT + wt - w.ctx;
           if (!seq_ok || nd >= a.T) {
             see = 0;
           } else if (nd >= 0) {
@@ -1499,49 +1548,55 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
               if (anc[r / G] >> nd & 1ull) see |= 1ull << r;
           }
         }
-        ok = __all_sync(0xffffffffu, bar_wait(smem_u32(&t.s_ready[s]), scount & 1, abort, a.status));
-        if (!ok) break;
+        // A needed page outside the cache or the table; the next tile's page and scales.
+        if (seq_ok && (nd < 0 || (nd < a.T && par[nd] != -2)) && (id < 0 || id >= a.num_pages))
+          bad |= SV_DEV_PAGE_RANGE;
+        const float kc = F8 ? ksc : 1.0f;
+        const float vs_now = see != 0 ? vsc : 0.0f;  // masked places may hold anything
+        scales_of(i + 2, id_next, &ksc, &vsc);
+        id = id_next;
+        id_next = page_of(i + 4);
+
+        wait(&t.s_ready[s], scount & 1);
         fence_after();
-        // Scores in powers of two, S^T times the scales, and how far they exceed m.
+        // Scores less m, in powers of two; masked ones -inf.
         float y[RP];
-        {
+        auto scores = [&](bool less) {
           tmem_ld_cols<RP>(sbase, y);
-          if (F8) {
-            float z[RP];
-            tmem_ld_cols<RP>(sbase + RP, z);
-#pragma unroll
-            for (int r = 0; r < RP; ++r) y[r] = __fmaf_rn(z[r], 0.0625f, y[r]) * ksc;
-          }
-          float over = -INFINITY;
 #pragma unroll
           for (int r = 0; r < RP; r += 4) {
             const float4 c4 = *reinterpret_cast<const float4*>(qc + r);
-            const float4 m4 = *reinterpret_cast<const float4*>(&f.mref[s][r]);
-            const float cc[4] = {c4.x, c4.y, c4.z, c4.w}, mm[4] = {m4.x, m4.y, m4.z, m4.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              float v = y[r + j] * cc[j];
-              if (edge) v = see >> (r + j) & 1ull ? v : -INFINITY;
-              y[r + j] = v;
-              over = fmaxf(over, v - mm[j]);
+            const float cc[4] = {c4.x, c4.y, c4.z, c4.w};
+            float mm[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (less) {
+              const float4 m4 = *reinterpret_cast<const float4*>(mref + r);
+              mm[0] = m4.x;
+              mm[1] = m4.y;
+              mm[2] = m4.z;
+              mm[3] = m4.w;
             }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) y[r + j] = __fmaf_rn(y[r + j], F8 ? cc[j] * kc : cc[j], -mm[j]);
           }
-          bool raise = over > kLazy;
-          if (F8) raise = raise || (see != 0 && vsc > f.vref[s]);
-          if (__any_sync(0xffffffffu, raise) && lane == 0) f.vote[s][(scount & 1)] = 1;
-        }
-        const float vs_now = see != 0 ? vsc : 0.0f;  // masked places may hold anything
-        if (F8) fetch_scales(i + 2);
-        ok = warps_sync(smem_u32(&t.wg_sync[s]), wg_phase, lane, abort, a.status);
-        if (!ok) break;
-        const bool raise = f.vote[s][scount & 1] != 0;
+          if (edge) {
+#pragma unroll
+            for (int r = 0; r < RP; ++r) y[r] = see >> r & 1ull ? y[r] : -INFINITY;
+          }
+        };
+        scores(true);
+        float over[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int r = 0; r < RP; ++r) over[r & 3] = fmaxf(over[r & 3], y[r]);
+        bool up = fmaxf(fmaxf(over[0], over[1]), fmaxf(over[2], over[3])) > C::kGrow;
+        if (F8) up = up || vs_now > f.vref[s];
+        const bool raise = named_any(1 + s, 128, up);
         if (any) {  // O and the P buffer of this stream: its last product must be complete
-          ok = __all_sync(0xffffffffu, bar_wait(smem_u32(&t.pv_done[s]), (scount - 1) & 1, abort, a.status));
-          if (!ok) break;
+          wait(&t.pv_done[s], (scount - 1) & 1);
           fence_after();
         }
         if (raise) {
           // New references: the warpgroup's maxima; then O and the sums to match.
+          scores(false);
 #pragma unroll
           for (int r = 0; r < RP; ++r) {
             const float v = redux_max(y[r]);
@@ -1551,35 +1606,33 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
             const float v = redux_max(vs_now > 0.0f ? vs_now : 0.0f);
             if (lane == 0) f.wvs[s][q] = v;
           }
-          ok = warps_sync(smem_u32(&t.wg_sync[s]), wg_phase, lane, abort, a.status);
-          if (!ok) break;
+          named_sync(1 + s, 128);
           float g = 1.0f, vnew = 0.0f;
           if (F8) {
             const float vold = f.vref[s];
             const float vtop = fmaxf(fmaxf(f.wvs[s][0], f.wvs[s][1]), fmaxf(f.wvs[s][2], f.wvs[s][3]));
-            const unsigned up = (__float_as_uint(vtop) + 0x7fffffu) >> 23;  // power of two not below it
-            vnew = fmaxf(vold, vtop > 0.0f ? __int_as_float(max(1u, min(253u, up)) << 23) : 0.0f);
+            const unsigned ex = (__float_as_uint(vtop) + 0x7fffffu) >> 23;  // power of two not below it
+            vnew = fmaxf(vold, vtop > 0.0f ? __int_as_float(max(8u, min(250u, ex)) << 23) : 0.0f);
             if (vnew > vold) g = vold / vnew;
           }
           if (wt < RP) {
             const float top = fmaxf(fmaxf(f.wmax[s][0][wt], f.wmax[s][1][wt]),
                                     fmaxf(f.wmax[s][2][wt], f.wmax[s][3][wt]));
-            const float old = f.mref[s][wt];
+            const float old = mref[wt];
             float fr = 1.0f;
-            if (wt < nrows && top > old + kLazy) {
+            if (wt < nrows && top > old + C::kGrow) {
               f.mref[s][wt] = top;
-              fr = old == -INFINITY ? 0.0f : ex2_fast(old - top);
+              fr = ex2_fast(old - top);
             }
             f.fac[s][wt] = fr;
           }
-          ok = warps_sync(smem_u32(&t.wg_sync[s]), wg_phase, lane, abort, a.status);
-          if (!ok) break;
-          if (wt == 0) {
-            f.vote[s][scount & 1] = 0;
-            if (F8) f.vref[s] = vnew;
-          }
+          named_sync(1 + s, 128);
+          if (wt == 0 && F8) f.vref[s] = vnew;
 #pragma unroll
-          for (int r = 0; r < RP; ++r) l[r] *= f.fac[s][r];
+          for (int r = 0; r < RP; ++r) {
+            l[r] *= f.fac[s][r];
+            y[r] -= mref[r];
+          }
           if (any) {
 #pragma unroll 1
             for (int pc = 0; pc < (F8 ? 3 : 1); ++pc) {
@@ -1595,50 +1648,49 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
             }
             tmem_wait_st();
           }
-          // f.vref and f.fac are read by all before the next change
-          ok = warps_sync(smem_u32(&t.wg_sync[s]), wg_phase, lane, abort, a.status);
-          if (!ok) break;
+          named_sync(1 + s, 128);  // fac and vref have been read and written
         }
         // Weights, their sums, and P^T: this key's 128 bytes, rows one after another.
         float vs = 1.0f;
         if (F8) {
           const float vr = f.vref[s];
-          vs = vr > 0.0f ? vs_now * __fdividef(1.0f, vr) : 0.0f;
-          if (isnan(vs_now)) vs = vs_now;
+          vs = vr > 0.0f ? vs_now * (C::kLift * __fdividef(1.0f, vr)) : isnan(vs_now) ? vs_now : 0.0f;
         }
         uint32_t words[32];
 #pragma unroll
         for (int k = 0; k < 32; ++k) words[k] = 0;
 #pragma unroll
         for (int r = 0; r < RP; r += 4) {
-          const float4 m4 = *reinterpret_cast<const float4*>(&f.mref[s][r]);
-          const float mm[4] = {m4.x, m4.y, m4.z, m4.w};
           float p[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            // A row that has seen nothing yet has m = -inf: all its scores are -inf.
-            p[j] = ex2_fast(y[r + j] - (mm[j] == -INFINITY ? 0.0f : mm[j]));
+            p[j] = ex2_fast(y[r + j]);
             l[r + j] += p[j];
-            if (F8) p[j] *= vs;
-            if (edge) p[j] = see >> (r + j) & 1ull ? p[j] : 0.0f;
           }
           if (F8) {
-            uint32_t c1 = 0, c2 = 0, c3 = 0;
+            const float2 p0 = f2_mul(make_float2(p[0], p[1]), f2(vs)), p1 = f2_mul(make_float2(p[2], p[3]), f2(vs));
+            p[0] = p0.x;
+            p[1] = p0.y;
+            p[2] = p1.x;
+            p[3] = p1.y;
+            if (edge) {  // the scale may be NaN
 #pragma unroll
-            for (int j = 0; j < 4; j += 2) {
-              const __half2 h = __floats2half2_rn(p[j], p[j + 1]);
-              const uint32_t e1 = half2_to_e4m3(h);
-              const __half2 r1 = __hmul2(__hsub2(h, e4m3_to_half2(e1)), __half2half2(__ushort_as_half(0x4c00)));
-              const uint32_t e2 = half2_to_e4m3(r1);
-              const __half2 r2 = __hmul2(__hsub2(r1, e4m3_to_half2(e2)), __half2half2(__ushort_as_half(0x4c00)));
-              const uint32_t e3 = half2_to_e4m3(r2);
-              c1 |= e1 << (8 * j);
-              c2 |= e2 << (8 * j);
-              c3 |= e3 << (8 * j);
+              for (int j = 0; j < 4; ++j) p[j] = see >> (r + j) & 1ull ? p[j] : 0.0f;
             }
-            words[r / 4] = c1;
-            words[(RP + r) / 4] = c2;
-            if ((2 * RP + r) / 4 < 32) words[(2 * RP + r) / 4] = c3;
+            const __half2 sixteen = __half2half2(__ushort_as_half(0x4c00));
+            uint32_t c[3][2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const __half2 h = __floats2half2_rn(p[2 * j], p[2 * j + 1]);
+              c[0][j] = half2_to_e4m3(h);
+              const __half2 r1 = __hmul2(__hsub2(h, e4m3_to_half2(c[0][j])), sixteen);
+              c[1][j] = half2_to_e4m3(r1);
+              const __half2 r2 = __hmul2(__hsub2(r1, e4m3_to_half2(c[1][j])), sixteen);
+              c[2][j] = half2_to_e4m3(r2);
+            }
+            words[r / 4] = __byte_perm(c[0][0], c[0][1], 0x5410);
+            words[(RP + r) / 4] = __byte_perm(c[1][0], c[1][1], 0x5410);
+            words[(2 * RP + r) / 4] = __byte_perm(c[2][0], c[2][1], 0x5410);
           } else {
             words[r / 2] = pack_bf16(p[0], p[1]);
             words[r / 2 + 1] = pack_bf16(p[2], p[3]);
@@ -1654,30 +1706,24 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
           // 0 times what lies at masked positions must be 0: rows past the tree are zeroed, a
           // node's NaN (or infinity) is taken out and given to its descendants at the end.
           const unsigned ev = entry0 + few_v(i, n);
-          ok = __all_sync(0xffffffffu, bar_wait(smem_u32(&t.full[ev % C::kSlots]), (ev / C::kSlots) & 1, abort,
-                                                a.status));
-          if (!ok) break;
-          const long long nd = (long long)tile * KT + wt - w.ctx;
+          wait(&t.full[ev % C::kSlots], (ev / C::kSlots) & 1);
           if (nd >= 0 || !seq_ok) {
             unsigned char* vrow = ring + (ev % C::kSlots) * C::kSlot + wt * 128;
             const bool dead = !seq_ok || nd >= a.T || par[nd] == -2;
+#pragma unroll 4
             for (int u = 0; u < (F8 ? 8 : 16); ++u) {
               uint4* at = reinterpret_cast<uint4*>(vrow + (u >> 3) * KT * 128 + (((u & 7) ^ (wt & 7)) << 4));
               uint4 v = dead ? make_uint4(0, 0, 0, 0) : *at;
-              uint32_t z[4] = {v.x, v.y, v.z, v.w};
-              bool found = dead;
+              uint32_t z[4] = {v.x, v.y, v.z, v.w}, found = 0;
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                if (F8) {
-#pragma unroll
-                  for (int b = 0; b < 32; b += 8)
-                    if ((z[j] >> b & 0x7fu) == 0x7fu) z[j] &= ~(0xffu << b), found = true, t.badv[item & 1] = 1;
-                } else {
-                  if ((z[j] & 0x7f80u) == 0x7f80u) z[j] &= 0xffff0000u, found = true, t.badv[item & 1] = 1;
-                  if ((z[j] & 0x7f800000u) == 0x7f800000u) z[j] &= 0x0000ffffu, found = true, t.badv[item & 1] = 1;
-                }
+              for (int j = 0; j < 4; ++j) {  // full bytes or halves where the element is not finite
+                const uint32_t not_finite = F8 ? __vcmpeq4(z[j] & 0x7f7f7f7fu, 0x7f7f7f7fu)
+                                               : __vcmpeq2(z[j] & 0x7f807f80u, 0x7f807f80u);
+                z[j] &= ~not_finite;
+                found |= not_finite;
               }
-              if (found) *at = make_uint4(z[0], z[1], z[2], z[3]);
+              if (found) t.badv[item & 1] = 1;
+              if (found || dead) *at = make_uint4(z[0], z[1], z[2], z[3]);
             }
           }
         }
@@ -1688,10 +1734,16 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
         __syncwarp();
         if (lane == 0) bar_arrive(smem_u32(&t.p_ready[s]));
       }
-      if (!ok) break;
       entry0 += 2u * n;
 
       // ---- the item's end
+      Walk<KT> nx = w;
+      nx.next(a);
+      if (nx.more()) fetch_q(nx);
+      if (bad) {
+        atomicOr(&t.bad[item & 1], 1u);
+        atomicOr(a.status, bad);
+      }
 #pragma unroll
       for (int r = 0; r < RP; ++r) {
         float v = l[r];
@@ -1699,33 +1751,34 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
         for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
         if (lane == 0) f.wsum[s][q][r] = v;
       }
-      ok = warps_sync(smem_u32(&t.all_sync), all_phase, lane, abort, a.status);
-      if (!ok) break;
+      named_sync(3, 256);
       // Both streams have read their last S: the next item's Q may go in.
-      Walk<KT> nx = w;
-      nx.next(a);
-      if (nx.more()) load_q(nx, (item + 1) & 1);
-      const bool bad = t.bad[item & 1] != 0, badv = t.badv[item & 1] != 0;
+      if (nx.more()) put_q((item + 1) & 1);
+      const bool at_fault = t.bad[item & 1] != 0, badv = t.badv[item & 1] != 0;
       if (threadIdx.x < RP) {
         const int r = threadIdx.x;
-        const float m0 = f.mref[0][r], m1 = n > 1 ? f.mref[1][r] : -INFINITY;
+        const bool dead = r < nrows && a.parents && a.parents[(long long)w.b * a.T + r / G] == -2;
+        const float m0 = f.mref[0][r], m1 = n > 1 ? f.mref[1][r] : kNoScore;
         const float m = fmaxf(m0, m1);
-        const float g0 = m0 == -INFINITY ? 0.0f : ex2_fast(m0 - m), g1 = m1 == -INFINITY ? 0.0f : ex2_fast(m1 - m);
+        const float g0 = ex2_fast(m0 - m), g1 = n > 1 ? ex2_fast(m1 - m) : 0.0f;
         const float l0 = (f.wsum[0][0][r] + f.wsum[0][1][r]) + (f.wsum[0][2][r] + f.wsum[0][3][r]);
         const float l1 = (f.wsum[1][0][r] + f.wsum[1][1][r]) + (f.wsum[1][2][r] + f.wsum[1][3][r]);
-        f.fin[r] = make_float4(F8 ? g0 * f.vref[0] : g0, F8 ? g1 * f.vref[1] : g1, m, l0 * g0 + l1 * g1);
+        const float sum = dead ? 0.0f : l0 * g0 + (n > 1 ? l1 * g1 : 0.0f);
+        const bool whole = w.t0 == 0 && w.t1 == w.n;
+        // Factors of the streams' O: for a whole item with the division by the sum.
+        float inv = 1.0f;
+        if (whole) inv = at_fault ? __int_as_float(0x7fc00000) : sum == 0.0f ? 0.0f : 1.0f / sum;
+        f.fin[r] = make_float4((F8 ? g0 * (f.vref[0] / C::kLift) : g0), (F8 ? g1 * (f.vref[1] / C::kLift) : g1),
+                               whole ? inv : at_fault ? __int_as_float(0x7fc00000) : m, sum);
       }
-      if (any) {
-        ok = __all_sync(0xffffffffu, bar_wait(smem_u32(&t.pv_done[s]), (scount - 1) & 1, abort, a.status));
-        if (!ok) break;
-      }
+      if (any) wait(&t.pv_done[s], (scount - 1) & 1);
       fence_before();
-      ok = warps_sync(smem_u32(&t.all_sync), all_phase, lane, abort, a.status);
-      if (!ok) break;
+      named_sync(3, 256);
       fence_after();
       if (threadIdx.x == 0) t.bad[(item + 1) & 1] = t.badv[(item + 1) & 1] = 0;
       const bool whole = w.t0 == 0 && w.t1 == w.n;
       const long long slot = (long long)group * 2 + (w.t0 == 0 ? 1 : 0);
+#pragma unroll 1
       for (int r0 = 8 * s; r0 < RP && r0 < nrows; r0 += 16) {
         __syncwarp();  // tensor memory is read by whole warps
         float v[8];
@@ -1751,12 +1804,12 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
         }
         if (wt >= a.D) continue;
         if (badv) {  // NaN and infinities of the nodes a row attends
-          for (int nd = 0; nd < a.T; ++nd) {
-            const long long pos = (long long)w.ctx + nd;
+          for (int k = 0; k < a.T; ++k) {
+            const long long pos = (long long)w.ctx + k;
             if (pos < (long long)w.t0 * KT || pos >= (long long)w.t1 * KT || pos / a.P >= a.max_pages) continue;
-            const int id = a.page_table[(long long)w.b * a.max_pages + pos / a.P];
-            if (id < 0 || id >= a.num_pages) continue;
-            const long long at = (((long long)id * a.Hkv + w.hk) * a.P + pos % a.P) * a.D + wt;
+            const int pg = a.page_table[(long long)w.b * a.max_pages + pos / a.P];
+            if (pg < 0 || pg >= a.num_pages) continue;
+            const long long at = (((long long)pg * a.Hkv + w.hk) * a.P + pos % a.P) * a.D + wt;
             const float z = F8 ? ((static_cast<const unsigned char*>(a.vc)[at] & 0x7f) == 0x7f
                                       ? __int_as_float(0x7fc00000)
                                       : 0.0f)
@@ -1764,7 +1817,7 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
             if (isfinite(z)) continue;
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-              if (r0 + j < nrows && (anc[(r0 + j) / G] >> nd & 1ull)) v[j] += z;
+              if (r0 + j < nrows && (anc[(r0 + j) / G] >> k & 1ull)) v[j] += z;
           }
         }
 #pragma unroll
@@ -1773,21 +1826,19 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
           if (r >= nrows) break;
           const float4 fin = f.fin[r];
           if (whole) {
-            const int node = r / G;
-            const bool dead = a.parents && a.parents[(long long)w.b * a.T + node] == -2;
-            const float o = bad ? __int_as_float(0x7fc00000)
-                                : (dead || fin.w == 0.0f ? 0.0f : v[j] * (1.0f / fin.w));
-            a.out[(((long long)w.b * a.T + node) * a.Hq + w.hk * G + r % G) * a.D + wt] = __float2bfloat16_rn(o);
+            const float o = fin.z == 0.0f ? 0.0f : v[j] * fin.z;
+            a.out[(((long long)w.b * a.T + r / G) * a.Hq + w.hk * G + r % G) * a.D + wt] = __float2bfloat16_rn(o);
           } else {
             x.part_o[(slot * nrows + r) * a.D + wt] = v[j];
-            if (wt == 0) x.part_ml[slot * nrows + r] = make_float2(bad ? __int_as_float(0x7fc00000) : fin.z, fin.w);
+            if (wt == 0) x.part_ml[slot * nrows + r] = make_float2(fin.z, fin.w);
           }
         }
       }
-      if (!whole) {
-        ok = join_parts(x, t, w, group, part, nrows, nrows, 256, all_phase, lane, abort);
-        if (!ok) break;
-      }
+      if (!whole)
+        join_parts(x, t, w, 0, nrows, nrows, 256, [&] {
+          named_sync(3, 256);
+          return true;
+        });
       w = nx;
     }
   }
