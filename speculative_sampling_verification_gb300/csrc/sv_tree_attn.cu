@@ -83,6 +83,7 @@ struct TcArgs {
   int parts_per_item;   // CTAs of a group: Q tiles (or pairs of them) of an item
   int groups;           // ranges of the line of tiles
   int box;              // keys of one TMA box: min(page, KT)
+  int lp;               // log2 of the page size (a power of two here)
   float c;              // |scale| log2 e, or 1 for a scale of 0
   float join_c;         // powers of two in a unit of the parts' m
   unsigned qflip;       // sign bits to flip in Q (a negative scale)
@@ -137,6 +138,7 @@ SV_DEVINL void bar_arrive(unsigned bar) {
 SV_DEVINL bool bar_wait(unsigned bar, unsigned parity, volatile unsigned* abort, unsigned* status) {
   if (mbar_test_parity(bar, parity)) return true;
   const uint64_t t0 = global_ns();
+#pragma unroll 1
   for (unsigned i = 0;; ++i) {
     if (mbar_test_parity(bar, parity)) return true;
     if ((i & 63) == 0) {
@@ -316,6 +318,21 @@ SV_DEVINL bool warps_sync(unsigned bar, unsigned& phase, int lane, volatile unsi
   return ok;
 }
 
+// Hardware barrier of `threads` threads, and the OR of their predicates.
+SV_DEVINL void named_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+SV_DEVINL bool named_any(int id, int threads, bool v) {
+  unsigned r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, %2, %3, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((unsigned)v), "r"(id), "r"(threads)
+      : "memory");
+  return r != 0;
+}
+
 // Tiles of a sequence; a context outside its page table counts as one tile.
 SV_DEVINL bool ctx_ok(const Args& a, int ctx) { return ctx >= 0 && (long long)ctx <= (long long)a.max_pages * a.P; }
 template <int KT>
@@ -363,6 +380,7 @@ template <int KT>
 SV_DEVINL void find_range(const TcArgs& x, TcTail& t, int group, int lane) {
   const Args& a = x.a;
   long long total = 0;
+#pragma unroll 1
   for (int b = lane; b < a.B; b += 32) total += (long long)tiles_of<KT>(a, a.ctx_lens[b]) * a.Hkv;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
@@ -370,6 +388,7 @@ SV_DEVINL void find_range(const TcArgs& x, TcTail& t, int group, int lane) {
   const long long lo = group < groups ? (long long)group * total / groups : 0;
   const long long hi = group < groups ? (long long)(group + 1) * total / groups : 0;
   long long before = 0;
+#pragma unroll 1
   for (int b0 = 0; b0 < a.B; b0 += 32) {
     const long long n = b0 + lane < a.B ? (long long)tiles_of<KT>(a, a.ctx_lens[b0 + lane]) * a.Hkv : 0;
     long long incl = n;
@@ -397,9 +416,17 @@ SV_DEVINL void find_range(const TcArgs& x, TcTail& t, int group, int lane) {
 // Called by `threads` threads once their part of an item that is cut is written:
 // the last part to arrive joins them all, in the order of the ranges. `sum` and O of
 // a part are relative to its m (in units of 1/join_c powers of two); NaN marks a sequence at fault.
-template <int KT, typename Sync>
-SV_DEVINL bool join_parts(const TcArgs& x, TcTail& t, const Walk<KT>& w, int part, int cta_rows, int rows_here,
-                          int threads, const Sync& sync) {
+// Out of line: it runs once an item, and the kernels' code is long as it is. `phase`: of
+// the softmax warps' mbarrier, or null where they meet at a hardware barrier.
+template <int KT>
+__device__ __noinline__ bool join_parts(const TcArgs& x, TcTail& t, const Walk<KT>& w, int part, int cta_rows,
+                                        int rows_here, int threads, unsigned* phase) {
+  const int lane = threadIdx.x & 31;
+  auto sync = [&]() -> bool {
+    if (phase) return warps_sync(smem_u32(&t.all_sync), *phase, lane, &t.abort, x.a.status);
+    named_sync(3, threads);
+    return true;
+  };
   const Args& a = x.a;
   const long long total = t.total;
   const int ng = t.groups, G = a.Hq / a.Hkv;
@@ -412,6 +439,7 @@ SV_DEVINL bool join_parts(const TcArgs& x, TcTail& t, const Walk<KT>& w, int par
   if (!t.last) return true;
   __threadfence();
   const int units = a.D / 4;
+#pragma unroll 1
   for (int i = threadIdx.x; i < rows_here * units; i += threads) {
     const int r = i / units, u = i - r * units;
     const int gr = part * cta_rows + r;
@@ -533,6 +561,7 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
     // ---- TMA: entry by entry, a lane a page
     unsigned entry = 0, tile_no = 0;
     bool ok = true;
+#pragma unroll 1
     for (; w.more() && ok; w.next(a)) {
       const int n = w.t1 - w.t0;
       int live = a.T;  // nodes up to the last that is not padding
@@ -543,6 +572,7 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
         live = __reduce_max_sync(0xffffffffu, live);
       }
       const bool seq_ok = ctx_ok(a, w.ctx);
+#pragma unroll 1
       for (int e = 0; e < 2 * n && ok; ++e, ++entry) {
         bool isv;
         int i;
@@ -557,11 +587,11 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
         const int boxes = KT / x.box;
         const int pos = tile * KT + lane * x.box;
         int page = -1;
-        if (seq_ok && lane < boxes && pos < w.ctx + live && pos / a.P < a.max_pages)
-          page = a.page_table[(long long)w.b * a.max_pages + pos / a.P];
+        if (seq_ok && lane < boxes && pos < w.ctx + live && (pos >> x.lp) < a.max_pages)
+          page = a.page_table[(long long)w.b * a.max_pages + (pos >> x.lp)];
         if (page < 0 || page >= a.num_pages) page = -1;
         const unsigned hit = __ballot_sync(0xffffffffu, page >= 0);
-        const int y = pos % a.P;
+        const int y = pos & (a.P - 1);
         unsigned bar;
         unsigned char* dst;
         unsigned limit_ok;
@@ -659,12 +689,14 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
         return ok;
       };
       auto release = [&](unsigned e) { commit(lead, smem_u32(&t.empty[e % C::kSlots])); };
+#pragma unroll 1
       for (; w.more() && ok; w.next(a), ++item) {
         const int n = w.t1 - w.t0;
         ok = ok && warp_wait(smem_u32(&t.q_ready), item & 1, abort, a.status);
         if (!ok) break;
         fence_after();
         if (ALT) {
+#pragma unroll 1
           for (int i = 0; i < 2 && i < n; ++i) {
             const unsigned e = entry0 + k_entry<true>(i);
             if (!full(e)) break;
@@ -673,6 +705,7 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
             release(e);
             commit(lead, smem_u32(&t.s_ready[i]));
           }
+#pragma unroll 1
           for (int i = 0; i < n && ok; ++i) {
             const int s = i & 1;
             const unsigned ev = entry0 + v_entry<true>(i, n);
@@ -690,7 +723,9 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
             }
           }
         } else {
+#pragma unroll 1
           for (int i = -1; i < n && ok; ++i) {
+#pragma unroll 1
             for (int s = 0; s < NS && ok; ++s) {
               if (i >= 0) {
                 const unsigned ev = entry0 + 2u * i + 1u;
@@ -732,6 +767,7 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
     const float c = x.c, grow = kLazy / c;
     unsigned item = 0, tile_no = 0, scount = 0, entry0 = 0, wg_phase = 0, all_phase = 0;
     bool ok = true;
+#pragma unroll 1
     for (; w.more() && ok; w.next(a), ++item) {
       const int n = w.t1 - w.t0;
       const bool seq_ok = ctx_ok(a, w.ctx);
@@ -742,6 +778,7 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
         constexpr int kLoaders = SHARED ? 128 : NS * 128;
         const int first = SHARED ? wt : threadIdx.x;
         unsigned char* qs = smem + (SHARED ? s * C::kQBytes : 0);
+#pragma unroll 1
         for (int i = first; i < 128 * units; i += kLoaders) {
           const int r = i / units, u = i - r * units;
           uint4 v = make_uint4(0, 0, 0, 0);
@@ -775,6 +812,7 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
             if (p < -2 || p >= wt || (p >= 0 && par[p] == -2)) bad |= SV_DEV_TREE;
           }
           if (have) {
+#pragma unroll 1
             for (int j = node, left = a.T; j >= 0 && left > 0; --left) {
               const int p = par[j];
               if (p == -2) break;
@@ -786,12 +824,14 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
           }
         }
         if (seq_ok && s == 0) {
-          const int p0 = (int)((long long)w.t0 * KT / a.P);
-          const int p1 = (int)min(((long long)w.t1 * KT + a.P - 1) / a.P, ((long long)w.ctx + a.T + a.P - 1) / a.P);
+          const int p0 = (int)(((long long)w.t0 * KT) >> x.lp);
+          const int p1 = (int)min(((long long)w.t1 * KT + a.P - 1) >> x.lp, ((long long)w.ctx + a.T + a.P - 1) >> x.lp);
+#pragma unroll 1
           for (int p = p0 + wt; p < p1; p += 128) {
             bool used = (long long)p * a.P < w.ctx;
             if (!used) {
               const int j1 = min((long long)a.T, (long long)(p + 1) * a.P - w.ctx);
+#pragma unroll 1
               for (int j = max(0, p * a.P - w.ctx); j < j1 && !used; ++j) used = par[j] != -2;
             }
             if (!used) continue;
@@ -807,6 +847,7 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
 
       float m = -INFINITY, sum = 0.0f;
       bool any = false;  // this stream has tiles of the item
+#pragma unroll 1
       for (int i = ALT ? s : 0; i < n; i += ALT ? 2 : 1) {
         const int tile = w.t0 + i;
         const bool edge = (long long)(tile + 1) * KT > w.ctx || !seq_ok;
@@ -937,6 +978,7 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
           if (wt < KT && (nd >= 0 || !seq_ok)) {
             unsigned char* vrow = ring + (ev % C::kSlots) * C::kSlot + wt * 128;
             const bool dead = !seq_ok || nd >= a.T || par[nd] == -2;
+#pragma unroll 1
             for (int u = 0; u < DP / 8; ++u) {
               uint4* at = reinterpret_cast<uint4*>(vrow + (u >> 3) * KT * 128 + (((u & 7) ^ (wt & 7)) << 4));
               uint4 v = dead ? make_uint4(0, 0, 0, 0) : *at;
@@ -994,6 +1036,7 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
       const float inv = bad ? m : sum == 0.0f || dead ? 0.0f : 1.0f / sum;
       __nv_bfloat16* out = a.out + (((long long)w.b * a.T + node) * a.Hq + w.hk * G + row % G) * a.D;
       if (busy) {
+#pragma unroll 1
         for (int col = col0; col < col0 + cols; col += 8) {
           __syncwarp();  // tensor memory is read by whole warps
           float v[8];
@@ -1006,6 +1049,7 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
               v[j] = (f0 > 0.0f || isnan(f0) ? v[j] * f0 : 0.0f) + (f1 > 0.0f || isnan(f1) ? u[j] * f1 : 0.0f);
           }
           if (badv && have) {  // NaN and infinities of the nodes this row attends
+#pragma unroll 1
             for (int nd = 0; nd < a.T; ++nd) {
               const long long pos = (long long)w.ctx + nd;
               if (pos < (long long)w.t0 * KT || pos >= (long long)w.t1 * KT) continue;
@@ -1013,11 +1057,11 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
 #pragma unroll
               for (int k = 1; k < 4; ++k)
                 if (k == nd >> 5) word = anc[k];
-              if (!(word >> (nd & 31) & 1u) || pos / a.P >= a.max_pages) continue;
-              const int id = a.page_table[(long long)w.b * a.max_pages + pos / a.P];
+              if (!(word >> (nd & 31) & 1u) || (pos >> x.lp) >= a.max_pages) continue;
+              const int id = a.page_table[(long long)w.b * a.max_pages + (pos >> x.lp)];
               if (id < 0 || id >= a.num_pages) continue;
               const __nv_bfloat16* vr = static_cast<const __nv_bfloat16*>(a.vc) +
-                                        (((long long)id * a.Hkv + w.hk) * a.P + pos % a.P) * a.D + col;
+                                        (((long long)id * a.Hkv + w.hk) * a.P + (pos & (a.P - 1))) * a.D + col;
 #pragma unroll
               for (int j = 0; j < 8; ++j) {
                 const float y = __bfloat162float(vr[j]);
@@ -1046,9 +1090,9 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
       }
       if (!whole) {
         const int rows_here = SHARED ? cta_rows : nrows;
-        ok = join_parts(x, t, w, part, cta_rows, rows_here, NS * 128, [&] {
-          return warps_sync(smem_u32(&t.all_sync), all_phase, lane, abort, a.status);
-        });
+        unsigned phase = all_phase;
+        ok = join_parts(x, t, w, part, cta_rows, rows_here, NS * 128, &phase);
+        all_phase = phase;
         if (!ok) break;
       }
     }
@@ -1057,8 +1101,10 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
     const int ct = threadIdx.x - 32 * 12;
     unsigned entry = 0;
     bool ok = true;
+#pragma unroll 1
     for (; w.more() && ok; w.next(a)) {
       const int n = w.t1 - w.t0;
+#pragma unroll 1
       for (int e = 0; e < 2 * n && ok; ++e, ++entry) {
         const int st = (int)(entry % 4), sl = (int)(entry % C::kSlots);
         ok = bar_wait(smem_u32(&t.sfull[st]), (entry / 4) & 1, abort, a.status);
@@ -1112,7 +1158,7 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
 // rows as its N, so the tensor cores and the softmax work on the rows that exist.
 // One thread a key holds that key's scores of all rows, its scales and its
 // mask; the maximum of a row is not needed, only a reference m that no score
-// exceeds by more than 2^8 (e4m3: 2^2): a vote of the warpgroup finds the rare tile that
+// exceeds by more than 2^8 (e4m3: 2^4): a vote of the warpgroup finds the rare tile that
 // does, and only then are maxima taken across the threads and O rescaled. P^T goes to
 // shared memory as the other operand of O^T = V^T P^T (M = 128 channels of the
 // head). A row's sum is kept by each thread for its keys and joined at the item's end.
@@ -1120,9 +1166,9 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
 // An e4m3 cache feeds the tensor cores as it is (kind::f8f6f4), with no pass to
 // convert it: Q and P enter as sums of e4m3 pieces. Q, scaled by a power of two to
 // (224, 448], is hi + lo, exact for elements above 2^-10 of the row's largest and off by
-// 2^-19 of that at most below; both multiply into the same columns. P, times 2^6 and the value's
+// 2^-19 of that at most below; both multiply into the same columns. P, times 2^4 and the value's
 // scale over a power of two not below any scale seen, is p1 + p2/16 + p3/256 with columns of
-// O for each piece: off by at most 2^-12 of itself or, for small weights, 2^-24 of the
+// O for each piece: off by at most 2^-12 of itself or, for small weights, 2^-22 of the
 // reference weight. A bf16 cache uses bf16 operands, P rounded once (2^-8).
 //
 // Streams, ranges and parts are those of the kernel above; the next tile's
@@ -1143,8 +1189,8 @@ struct FewCfg {
   static constexpr int kSlots = kFit < kMaxSlots ? kFit : kMaxSlots;
   static constexpr int kThreads = 320;
   static constexpr unsigned kS = 0, kO = 256;  // tensor memory: two of each, 128 columns apart
-  static constexpr float kGrow = F8 ? 2.0f : 8.0f;
-  static constexpr float kLift = F8 ? 64.0f : 1.0f;
+  static constexpr float kGrow = F8 ? 4.0f : 8.0f;
+  static constexpr float kLift = F8 ? 16.0f : 1.0f;
 };
 
 constexpr float kNoScore = -1e30f;  // reference of a row that has seen no key
@@ -1160,6 +1206,7 @@ struct FewTail {
   float4 fin[RP];
   float wmax[2][4][RP], wsum[2][4][RP], wvs[2][4];
   float vref[2];
+  int row_out[RP];                   // a row's place in a token block of the output: node Hq + head of the group
 };
 
 template <int RP, bool F8>
@@ -1168,21 +1215,6 @@ constexpr int few_smem() {
   static_assert(sizeof(FewTail<RP>) <= C::kTailBytes, "tail");
   static_assert(RP % 8 == 0 && C::kQBytes % 2048 == 0, "rows of four values, blocks of 1024 bytes");
   return 1024 + C::kQBytes + 2 * C::kPBytes + C::kSlots * C::kSlot + (int)sizeof(FewTail<RP>);
-}
-
-// Hardware barrier of `threads` threads, and the OR of their predicates.
-SV_DEVINL void named_sync(int id, int threads) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-SV_DEVINL bool named_any(int id, int threads, bool v) {
-  unsigned r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, %2, %3, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"((unsigned)v), "r"(id), "r"(threads)
-      : "memory");
-  return r != 0;
 }
 
 SV_DEVINL float redux_max(float v) {
@@ -1220,6 +1252,31 @@ SV_DEVINL void tmem_ld_cols(unsigned t, float* v) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = u[i];
   }
+}
+
+// Sums of v[0 .. N) over a warp: each step halves the lanes that share a row and the
+// rows that a lane holds (N shuffles in all, not 5 N), in the same order every time.
+template <int N, int O>
+SV_DEVINL void halve(const float (&v)[N], int lane, int base, int count, float* out) {
+  if constexpr (O == 0) {
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (j < count) out[base + j] = v[j];
+  } else {
+    constexpr int H = (N + 1) / 2;
+    const bool up = lane & O;
+    float k[H];
+#pragma unroll
+    for (int j = 0; j < H; ++j) {
+      const float hi = j + H < N ? v[j + H] : 0.0f;
+      k[j] = (up ? hi : v[j]) + __shfl_xor_sync(0xffffffffu, up ? v[j] : hi, O);
+    }
+    halve<H, O / 2>(k, lane, up ? base + H : base, up ? count - H : min(count, H), out);
+  }
+}
+template <int N>
+SV_DEVINL void row_sums(const float (&v)[N], int lane, float* out) {
+  halve<N, 16>(v, lane, 0, N, out);
 }
 
 // Place in the operand ring: K0 K1 K2 V0 K3 V1 ... (S^T of tile i + 2 before O^T of tile i).
@@ -1279,6 +1336,7 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
   if (warp == kProducer) {
     unsigned entry = 0;
     bool ok = true;
+#pragma unroll 1
     for (; w.more() && ok; w.next(a)) {
       const int n = w.t1 - w.t0;
       int live = a.T;
@@ -1290,13 +1348,14 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
       }
       const bool seq_ok = ctx_ok(a, w.ctx);
       int nk = 0, nv = 0;  // keys and values issued
+#pragma unroll 1
       for (int e = 0; e < 2 * n && ok; ++e, ++entry) {
         const bool isv = !(nk < n && nk < nv + 3);
         const int tile = w.t0 + (isv ? nv++ : nk++);
         const int pos = tile * KT + lane * x.box;
         int page = -1;
-        if (seq_ok && lane < KT / x.box && pos < w.ctx + live && pos / a.P < a.max_pages)
-          page = a.page_table[(long long)w.b * a.max_pages + pos / a.P];
+        if (seq_ok && lane < KT / x.box && pos < w.ctx + live && (pos >> x.lp) < a.max_pages)
+          page = a.page_table[(long long)w.b * a.max_pages + (pos >> x.lp)];
         if (page < 0 || page >= a.num_pages) page = -1;
         const unsigned hit = __ballot_sync(0xffffffffu, page >= 0);
         const int s = (int)(entry % C::kSlots);
@@ -1358,6 +1417,7 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
       commit(lead, smem_u32(&t.s_ready[i & 1]));
       commit(lead, smem_u32(&t.empty[e % C::kSlots]));
     };
+#pragma unroll 1
     for (; w.more() && ok; w.next(a), ++item) {
       const int n = w.t1 - w.t0;
       ok = ok && warp_wait(smem_u32(&t.q_ready), item & 1, abort, a.status);
@@ -1365,6 +1425,7 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
       fence_after();
       qk(0);
       if (n > 1 && ok) qk(1);
+#pragma unroll 1
       for (int i = 0; i < n && ok; ++i) {
         const int s = i & 1;
         ok = ok && warp_wait(smem_u32(&t.p_ready[s]), pcount[s] & 1, abort, a.status);
@@ -1477,11 +1538,34 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
       __syncwarp();
       if (lane == 0) bar_arrive(smem_u32(&t.q_ready));
     };
+    // Page of this thread's key in tile i of an item, -1 for none, and the key's scales.
+    auto page_of = [&](const Walk<KT>& it, int i) -> int {
+      const long long pos = (long long)(it.t0 + i) * KT + wt;
+      if (!ctx_ok(a, it.ctx) || it.t0 + i >= it.t1 || pos >= (long long)it.ctx + a.T ||
+          (pos >> x.lp) >= a.max_pages)
+        return -1;
+      return a.page_table[(long long)it.b * a.max_pages + (pos >> x.lp)];
+    };
+    auto scales_of = [&](const Walk<KT>& it, int i, int id, float* k, float* v) {
+      *k = *v = 0.0f;
+      if (!F8 || id < 0 || id >= a.num_pages) return;
+      const long long at =
+          (((long long)id * a.Hkv + it.hk) << x.lp) + (((it.t0 + i) * KT + wt) & (a.P - 1));
+      *k = __ldg(a.ks + at);
+      *v = __ldg(a.vs + at);
+    };
+    int id = -1, id_next = -1;
+    float ksc = 0.0f, vsc = 0.0f;
+    if (threadIdx.x < RP) f.row_out[threadIdx.x] = threadIdx.x / G * a.Hq + threadIdx.x % G;
     if (w.more()) {
+      id = page_of(w, s);
+      id_next = page_of(w, s + 2);
       fetch_q(w);
+      scales_of(w, s, id, &ksc, &vsc);
       put_q(0);
     }
 
+#pragma unroll 1
     for (; w.more(); ++item) {
       const int n = w.t1 - w.t0;
       const bool seq_ok = ctx_ok(a, w.ctx);
@@ -1493,31 +1577,14 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
       if (wt < RP) f.mref[s][wt] = wt < nrows ? kNoScore : 0.0f;
       if (wt == 0) f.vref[s] = 0.0f;
       unsigned bad = seq_ok ? 0u : (unsigned)SV_DEV_PAGE_RANGE;
-      // Page of this thread's key in tile i of the item, -1 for none.
-      auto page_of = [&](int i) -> int {
-        const long long pos = (long long)(w.t0 + i) * KT + wt;
-        if (!seq_ok || i >= n || pos >= (long long)w.ctx + a.T || pos / a.P >= a.max_pages) return -1;
-        return a.page_table[(long long)w.b * a.max_pages + pos / a.P];
-      };
-      // Its scales.
-      auto scales_of = [&](int i, int id, float* k, float* v) {
-        *k = *v = 0.0f;
-        if (!F8 || id < 0 || id >= a.num_pages) return;
-        const long long at =
-            ((long long)id * a.Hkv + w.hk) * a.P + (int)(((long long)(w.t0 + i) * KT + wt) % a.P);
-        *k = __ldg(a.ks + at);
-        *v = __ldg(a.vs + at);
-      };
-      int id = page_of(s), id_next = page_of(s + 2);
       if (tail && wt < a.T) par[wt] = a.parents ? a.parents[(long long)w.b * a.T + wt] : wt - 1;
-      float ksc, vsc;
-      scales_of(s, id, &ksc, &vsc);
       named_sync(1 + s, 128);
       if (tail) {
         if (wt < a.T) {
           const int p = par[wt];
           if (p < -2 || p >= wt || (p >= 0 && par[p] == -2)) bad |= SV_DEV_TREE;
           unsigned long long set = 0;
+#pragma unroll 1
           for (int j = wt, left = a.T; j >= 0 && left > 0; --left) {
             const int pj = par[j];
             if (pj == -2) break;
@@ -1533,6 +1600,7 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
 #pragma unroll
       for (int r = 0; r < RP; ++r) l[r] = 0.0f;
       bool any = false;
+#pragma unroll 1
       for (int i = s; i < n; i += 2) {
         const int tile = w.t0 + i;
         const bool edge = (long long)(tile + 1) * KT > w.ctx || !seq_ok;
@@ -1544,8 +1612,9 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
             see = 0;
           } else if (nd >= 0) {
             see = 0;
-            for (int r = 0; r < nrows; ++r)
-              if (anc[r / G] >> nd & 1ull) see |= 1ull << r;
+#pragma unroll 1
+            for (int k = (int)nd; k < a.T; ++k)  // a node's descendants come after it
+              if (anc[k] >> nd & 1ull) see |= ((1ull << G) - 1) << (k * G);
           }
         }
         // A needed page outside the cache or the table; the next tile's page and scales.
@@ -1553,9 +1622,9 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
           bad |= SV_DEV_PAGE_RANGE;
         const float kc = F8 ? ksc : 1.0f;
         const float vs_now = see != 0 ? vsc : 0.0f;  // masked places may hold anything
-        scales_of(i + 2, id_next, &ksc, &vsc);
+        scales_of(w, i + 2, id_next, &ksc, &vsc);
         id = id_next;
-        id_next = page_of(i + 4);
+        id_next = page_of(w, i + 4);
 
         wait(&t.s_ready[s], scount & 1);
         fence_after();
@@ -1620,7 +1689,7 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
                                     fmaxf(f.wmax[s][2][wt], f.wmax[s][3][wt]));
             const float old = mref[wt];
             float fr = 1.0f;
-            if (wt < nrows && top > old + C::kGrow) {
+            if (wt < nrows && top > old) {  // every row that grew, so that the next raise is far
               f.mref[s][wt] = top;
               fr = ex2_fast(old - top);
             }
@@ -1710,17 +1779,20 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
           if (nd >= 0 || !seq_ok) {
             unsigned char* vrow = ring + (ev % C::kSlots) * C::kSlot + wt * 128;
             const bool dead = !seq_ok || nd >= a.T || par[nd] == -2;
-#pragma unroll 4
+#pragma unroll 2
             for (int u = 0; u < (F8 ? 8 : 16); ++u) {
               uint4* at = reinterpret_cast<uint4*>(vrow + (u >> 3) * KT * 128 + (((u & 7) ^ (wt & 7)) << 4));
               uint4 v = dead ? make_uint4(0, 0, 0, 0) : *at;
               uint32_t z[4] = {v.x, v.y, v.z, v.w}, found = 0;
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {  // full bytes or halves where the element is not finite
-                const uint32_t not_finite = F8 ? __vcmpeq4(z[j] & 0x7f7f7f7fu, 0x7f7f7f7fu)
-                                               : __vcmpeq2(z[j] & 0x7f807f80u, 0x7f807f80u);
-                z[j] &= ~not_finite;
-                found |= not_finite;
+              for (int j = 0; j < 4; ++j) {
+                // Top bits of the bytes or halves whose element is not finite: those whose
+                // exponent (and mantissa, of a code) are all ones, difference zero.
+                const uint32_t ones = F8 ? 0x7f7f7f7fu : 0x7f807f80u;
+                const uint32_t top = F8 ? 0x80808080u : 0x80008000u;
+                const uint32_t m = ~(((z[j] & ones) ^ ones) + (top - (F8 ? 0x01010101u : 0x00010001u))) & top;
+                z[j] &= ~(F8 ? (m >> 7) * 0xffu : (m >> 15) * 0xffffu);
+                found |= m;
               }
               if (found) t.badv[item & 1] = 1;
               if (found || dead) *at = make_uint4(z[0], z[1], z[2], z[3]);
@@ -1739,21 +1811,22 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
       // ---- the item's end
       Walk<KT> nx = w;
       nx.next(a);
-      if (nx.more()) fetch_q(nx);
+      if (nx.more()) {
+        fetch_q(nx);
+        id = page_of(nx, s);
+        id_next = page_of(nx, s + 2);
+      }
       if (bad) {
         atomicOr(&t.bad[item & 1], 1u);
         atomicOr(a.status, bad);
       }
-#pragma unroll
-      for (int r = 0; r < RP; ++r) {
-        float v = l[r];
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        if (lane == 0) f.wsum[s][q][r] = v;
-      }
+      row_sums<RP>(l, lane, f.wsum[s][q]);
       named_sync(3, 256);
       // Both streams have read their last S: the next item's Q may go in.
-      if (nx.more()) put_q((item + 1) & 1);
+      if (nx.more()) {
+        put_q((item + 1) & 1);
+        scales_of(nx, s, id, &ksc, &vsc);
+      }
       const bool at_fault = t.bad[item & 1] != 0, badv = t.badv[item & 1] != 0;
       if (threadIdx.x < RP) {
         const int r = threadIdx.x;
@@ -1804,12 +1877,13 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
         }
         if (wt >= a.D) continue;
         if (badv) {  // NaN and infinities of the nodes a row attends
+#pragma unroll 1
           for (int k = 0; k < a.T; ++k) {
             const long long pos = (long long)w.ctx + k;
-            if (pos < (long long)w.t0 * KT || pos >= (long long)w.t1 * KT || pos / a.P >= a.max_pages) continue;
-            const int pg = a.page_table[(long long)w.b * a.max_pages + pos / a.P];
+            if (pos < (long long)w.t0 * KT || pos >= (long long)w.t1 * KT || (pos >> x.lp) >= a.max_pages) continue;
+            const int pg = a.page_table[(long long)w.b * a.max_pages + (pos >> x.lp)];
             if (pg < 0 || pg >= a.num_pages) continue;
-            const long long at = (((long long)pg * a.Hkv + w.hk) * a.P + pos % a.P) * a.D + wt;
+            const long long at = (((long long)pg * a.Hkv + w.hk) * a.P + (pos & (a.P - 1))) * a.D + wt;
             const float z = F8 ? ((static_cast<const unsigned char*>(a.vc)[at] & 0x7f) == 0x7f
                                       ? __int_as_float(0x7fc00000)
                                       : 0.0f)
@@ -1827,7 +1901,7 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
           const float4 fin = f.fin[r];
           if (whole) {
             const float o = fin.z == 0.0f ? 0.0f : v[j] * fin.z;
-            a.out[(((long long)w.b * a.T + r / G) * a.Hq + w.hk * G + r % G) * a.D + wt] = __float2bfloat16_rn(o);
+            a.out[((long long)w.b * a.T * a.Hq + w.hk * G + f.row_out[r]) * a.D + wt] = __float2bfloat16_rn(o);
           } else {
             x.part_o[(slot * nrows + r) * a.D + wt] = v[j];
             if (wt == 0) x.part_ml[slot * nrows + r] = make_float2(fin.z, fin.w);
@@ -1835,10 +1909,7 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
         }
       }
       if (!whole)
-        join_parts(x, t, w, 0, nrows, nrows, 256, [&] {
-          named_sync(3, 256);
-          return true;
-        });
+        join_parts(x, t, w, 0, nrows, nrows, 256, nullptr);
       w = nx;
     }
   }
@@ -2112,6 +2183,7 @@ template <bool F8>
 int launch_tc_any(TcArgs& x, const Plan& p, cudaStream_t st) {
   const int D = x.a.D;
   x.box = std::min(x.a.P, D > 128 ? 64 : 128);
+  x.lp = x.a.P == 16 ? 4 : x.a.P == 32 ? 5 : x.a.P == 64 ? 6 : 7;
   if (p.few) return p.rows <= 16 ? launch_few<16, F8>(x, st) : launch_few<kFewRows, F8>(x, st);
   if (D > 128) return launch_tc<256, F8, false>(x, st);
   if (D > 64) return p.shared ? launch_tc<128, F8, true>(x, st) : launch_tc<128, F8, false>(x, st);
