@@ -55,8 +55,8 @@ struct Args {
 // tile of its own and both use every tile. Head sizes above 128 have room for
 // one stream only.
 //
-// Work: the tiles of all (sequence, key/value head) items form one line, cut into
-// equal ranges, one for each group of CTAs (the CTAs of a group take the item's
+// Work: the tiles of all (sequence, key/value head) items, with a few units for the item
+// itself before them, form one line, cut into equal ranges, one for each group of CTAs (the CTAs of a group take the item's
 // Q tiles, in step, so that a tile is read from HBM once). The cuts follow the
 // lengths on the device, so ragged batches and few long sequences balance
 // alike. An item that lies in one range is written at once; the parts of a cut
@@ -297,6 +297,44 @@ SV_DEVINL void tmem_st16(unsigned t, const uint32_t (&r)[16]) {
       "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
+SV_DEVINL void tmem_ld4(unsigned t, float (&v)[4]) {
+  uint32_t r[4];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];\n\ttcgen05.wait::ld.sync.aligned;"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(t));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(r[i]);
+}
+SV_DEVINL void tmem_st4(unsigned t, float a, float b, float c, float d) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(t), "f"(a), "f"(b), "f"(c),
+               "f"(d)
+               : "memory");
+}
+// Single columns: t and t + step; or three of each, `piece` apart.
+SV_DEVINL void tmem_ld_1x2(unsigned t, unsigned step, float* a, float* b) {
+  uint32_t r[2];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%2];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%1}, [%3];\n\ttcgen05.wait::ld.sync.aligned;"
+      : "=&r"(r[0]), "=&r"(r[1])
+      : "r"(t), "r"(t + step));
+  *a = __uint_as_float(r[0]);
+  *b = __uint_as_float(r[1]);
+}
+SV_DEVINL void tmem_ld_3x2(unsigned t, unsigned piece, unsigned step, float (&v)[6]) {
+  uint32_t r[6];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%6];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%1}, [%7];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%2}, [%8];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%3}, [%9];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%4}, [%10];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%5}, [%11];\n\ttcgen05.wait::ld.sync.aligned;"
+      : "=&r"(r[0]), "=&r"(r[1]), "=&r"(r[2]), "=&r"(r[3]), "=&r"(r[4]), "=&r"(r[5])
+      : "r"(t), "r"(t + piece), "r"(t + 2 * piece), "r"(t + step), "r"(t + step + piece), "r"(t + step + 2 * piece));
+#pragma unroll
+  for (int i = 0; i < 6; ++i) v[i] = __uint_as_float(r[i]);
+}
 SV_DEVINL void tmem_st8(unsigned t, const uint32_t (&r)[8]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(t),
                "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
@@ -340,38 +378,41 @@ SV_DEVINL int tiles_of(const Args& a, int ctx) {
   return ctx_ok(a, ctx) ? (int)(((long long)ctx + a.T + KT - 1) / KT) : 1;
 }
 
+// Units of an item on the line before its tiles: what an item costs a CTA beside
+// its tiles (Q, the first references, the output), in tiles.
+constexpr int kItemUnits = 5;
+
 // A CTA's way along its range: the item (b, hk), its tile count, context and the
 // tiles [t0, t1) of it that lie in the range.
 template <int KT>
 struct Walk {
   int b, hk, n, ctx, t0, t1;
-  long long base, pos, hi;  // the line's index of the item's first tile, of t0, of the range's end
+  long long base, hi;  // the line's index of the item's first unit, of the range's end
   SV_DEVINL void start(const Args& a, const TcTail& t) {
-    b = t.b0;
-    pos = t.lo;
+    t0 = t1 = 0;
     hi = t.hi;
-    if (pos >= hi) return;
+    if (t.lo >= hi) return;
+    b = t.b0;
     ctx = a.ctx_lens[b];
     n = tiles_of<KT>(a, ctx);
-    const long long rem = pos - t.base0;
-    hk = (int)(rem / n);
-    t0 = (int)(rem - (long long)hk * n);
-    base = pos - t0;
-    clip();
+    const unsigned long long rem = t.lo - t.base0;
+    hk = (int)(rem / (unsigned)(n + kItemUnits));
+    base = t.base0 + (long long)hk * (n + kItemUnits);
+    t0 = (int)max(0ll, t.lo - base - kItemUnits);
+    t1 = (int)min((long long)n, hi - base - kItemUnits);
+    if (t0 >= t1) next(a);  // only units before the item's tiles
   }
-  SV_DEVINL void clip() { t1 = (int)((long long)n < t0 + (hi - pos) ? (long long)n : t0 + (hi - pos)); }
-  SV_DEVINL bool more() const { return pos < hi; }
+  SV_DEVINL bool more() const { return t0 < t1; }
   SV_DEVINL void next(const Args& a) {
-    pos += t1 - t0;
-    if (pos >= hi) return;
+    base += n + kItemUnits;
+    t0 = t1 = 0;
+    if (base + kItemUnits >= hi) return;
     if (++hk == a.Hkv) {
       hk = 0;
       ctx = a.ctx_lens[++b];
       n = tiles_of<KT>(a, ctx);
     }
-    t0 = 0;
-    base = pos;
-    clip();
+    t1 = (int)min((long long)n, hi - base - kItemUnits);
   }
 };
 
@@ -381,7 +422,8 @@ SV_DEVINL void find_range(const TcArgs& x, TcTail& t, int group, int lane) {
   const Args& a = x.a;
   long long total = 0;
 #pragma unroll 1
-  for (int b = lane; b < a.B; b += 32) total += (long long)tiles_of<KT>(a, a.ctx_lens[b]) * a.Hkv;
+  for (int b = lane; b < a.B; b += 32)
+    total += (long long)(tiles_of<KT>(a, a.ctx_lens[b]) + kItemUnits) * a.Hkv;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   const int groups = (int)min((long long)x.groups, total);
@@ -390,7 +432,8 @@ SV_DEVINL void find_range(const TcArgs& x, TcTail& t, int group, int lane) {
   long long before = 0;
 #pragma unroll 1
   for (int b0 = 0; b0 < a.B; b0 += 32) {
-    const long long n = b0 + lane < a.B ? (long long)tiles_of<KT>(a, a.ctx_lens[b0 + lane]) * a.Hkv : 0;
+    const long long n =
+        b0 + lane < a.B ? (long long)(tiles_of<KT>(a, a.ctx_lens[b0 + lane]) + kItemUnits) * a.Hkv : 0;
     long long incl = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -430,7 +473,8 @@ __device__ __noinline__ bool join_parts(const TcArgs& x, TcTail& t, const Walk<K
   const Args& a = x.a;
   const long long total = t.total;
   const int ng = t.groups, G = a.Hq / a.Hkv;
-  const int gs = (int)(((w.base + 1) * ng - 1) / total), ge = (int)(((w.base + w.n) * ng - 1) / total);
+  const long long first = w.base + kItemUnits;  // the item's first tile on the line
+  const int gs = (int)(((first + 1) * ng - 1) / total), ge = (int)(((first + w.n) * ng - 1) / total);
   __threadfence();
   if (!sync()) return false;
   if (threadIdx.x == 0)
@@ -1176,18 +1220,22 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
 // warps meet at hardware barriers, so none of them leaves early: once a wait
 // has run out they only count their tiles down.
 
+// The rows of a tile are shared by two warps for each 32 keys, RP/2 each ("halves").
 template <int RP, bool F8>
 struct FewCfg {
   static constexpr int KT = 128;
-  static constexpr int N1 = (RP + 15) / 16 * 16;                // columns of S^T
-  static constexpr int N2 = F8 ? (3 * RP + 15) / 16 * 16 : N1;  // columns of O^T
-  static constexpr int kQBytes = N1 * 128 * 2;                  // two blocks: channels (bf16) or pieces
+  static constexpr int HR = RP / 2;                                // rows of a half
+  static constexpr int HS = (HR + 7) / 8 * 8;                      // its columns of S^T
+  static constexpr int HN = F8 ? (3 * HR + 15) / 16 * 16 : HS;     // its columns of O^T and P
+  static constexpr int N1 = 2 * HS, N2 = 2 * HN;
+  static constexpr int kQBytes = N1 * 128 * 2;                     // two blocks: channels (bf16) or pieces
   static constexpr int kPBytes = KT * 128;
   static constexpr int kSlot = KT * (F8 ? 128 : 256);
   static constexpr int kTailBytes = 12 * 1024;
   static constexpr int kFit = (226 * 1024 - kTailBytes - kQBytes - 2 * kPBytes) / kSlot;
   static constexpr int kSlots = kFit < kMaxSlots ? kFit : kMaxSlots;
-  static constexpr int kThreads = 320;
+  static constexpr int kSoft = 16;                                 // softmax warps
+  static constexpr int kThreads = 32 * (kSoft + 2);
   static constexpr unsigned kS = 0, kO = 256;  // tensor memory: two of each, 128 columns apart
   static constexpr float kGrow = F8 ? 4.0f : 8.0f;
   static constexpr float kLift = F8 ? 16.0f : 1.0f;
@@ -1204,7 +1252,7 @@ struct FewTail {
   alignas(16) float fac[2][RP];      // [stream] factors of a rescaling
   alignas(16) float qc[2][RP];       // [item parity] c over the row's scale of Q
   float4 fin[RP];
-  float wmax[2][4][RP], wsum[2][4][RP], wvs[2][4];
+  float wmax[2][4][RP], wsum[2][4][RP], wvs[2][2][4];
   float vref[2];
   int row_out[RP];                   // a row's place in a token block of the output: node Hq + head of the group
 };
@@ -1213,7 +1261,7 @@ template <int RP, bool F8>
 constexpr int few_smem() {
   using C = FewCfg<RP, F8>;
   static_assert(sizeof(FewTail<RP>) <= C::kTailBytes, "tail");
-  static_assert(RP % 8 == 0 && C::kQBytes % 2048 == 0, "rows of four values, blocks of 1024 bytes");
+  static_assert(C::HR % 4 == 0 && C::kQBytes % 2048 == 0, "rows of four values, blocks of 1024 bytes");
   return 1024 + C::kQBytes + 2 * C::kPBytes + C::kSlots * C::kSlot + (int)sizeof(FewTail<RP>);
 }
 
@@ -1288,7 +1336,8 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
     tree_attn_few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                          const __grid_constant__ TcArgs x) {
   using C = FewCfg<RP, F8>;
-  constexpr int KT = 128;
+  constexpr int KT = 128, HR = C::HR, kSoft = C::kSoft;
+  constexpr int kProducer = kSoft, kIssuer = kSoft + 1;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                          ~static_cast<uintptr_t>(1023));
@@ -1300,7 +1349,6 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
   const Args& a = x.a;
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int group = blockIdx.x;
-  constexpr int kSoft = 8;
 
   if (warp == 0) {
     find_range<KT>(x, t, group, lane);
@@ -1312,7 +1360,7 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
     mbar_init(smem_u32(&t.q_ready), kSoft);
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&t.s_ready[i]), 1);
-      mbar_init(smem_u32(&t.p_ready[i]), 4);
+      mbar_init(smem_u32(&t.p_ready[i]), kSoft / 2);
       mbar_init(smem_u32(&t.pv_done[i]), 1);
     }
     t.abort = 0;
@@ -1452,87 +1500,84 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
       entry0 += 2u * n;
     }
   } else if (warp < kSoft) {
-    const int s = warp >> 2, q = warp & 3;
-    const int wt = threadIdx.x & 127;  // key of the tile, and channel of the head
+    const int s = warp >> 3, h = warp >> 2 & 1, q = warp & 3;  // stream, half of the rows, 32 keys
+    const int wt = threadIdx.x & 127;                          // key of the tile, and channel of the head
+    const int st = threadIdx.x & 255;                          // thread of the stream
+    const int row0 = h * HR;
     const unsigned lanes = (unsigned)(q * 32) << 16;
-    const unsigned sbase = tmem + lanes + C::kS + 128 * s;
-    const unsigned obase = tmem + lanes + C::kO + 128 * s;
+    const unsigned sbase = tmem + lanes + C::kS + 128 * s + h * C::HS;
+    const unsigned obase = tmem + lanes + C::kO + 128 * s + h * C::HN;
     const int G = a.Hq / a.Hkv, nrows = x.rows;
     unsigned item = 0, scount = 0, entry0 = 0;
     auto wait = [&](unsigned long long* bar, unsigned parity) { bar_wait(smem_u32(bar), parity, abort, a.status); };
 
     // Q of an item: eight lanes a row, 16 values each; fetched early, stored when the
     // products with the last Q are done.
-    constexpr int kQPasses = (C::N1 + 31) / 32;
-    uint4 qv[kQPasses][2];
+    const int qpos = threadIdx.x >> 3, qu = threadIdx.x & 7;  // row of the operand, 16 of its values
+    const int qrow = qpos % C::HS < HR && qpos < C::N1 ? qpos / C::HS * HR + qpos % C::HS : RP;
+    const bool q_on = qrow < nrows && qu * 16 < a.D;
+    const long long q_at = q_on ? (long long)(qrow / G) * a.q_st + (long long)(qrow % G) * a.q_sh + qu * 16 : 0;
+    uint4 qv[2];
+    auto q_of = [&](const Walk<KT>& it) {
+      return reinterpret_cast<const uint4*>(a.q + it.b * a.q_sb + (long long)it.hk * G * a.q_sh + q_at);
+    };
     auto fetch_q = [&](const Walk<KT>& it) {
-#pragma unroll
-      for (int k = 0; k < kQPasses; ++k) {
-        const int r = (threadIdx.x >> 3) + 32 * k, u = threadIdx.x & 7;
-        qv[k][0] = qv[k][1] = make_uint4(0, 0, 0, 0);
-        if (r < nrows && !x.qzero && u * 16 < a.D) {
-          const uint4* at = reinterpret_cast<const uint4*>(a.q + it.b * a.q_sb + (long long)(r / G) * a.q_st +
-                                                           (long long)(it.hk * G + r % G) * a.q_sh + u * 16);
-          qv[k][0] = at[0];
-          qv[k][1] = at[1];
-        }
+      qv[0] = qv[1] = make_uint4(0, 0, 0, 0);
+      if (q_on && !x.qzero) {
+        qv[0] = q_of(it)[0];
+        qv[1] = q_of(it)[1];
       }
     };
     auto put_q = [&](unsigned parity) {
+      uint32_t z[8] = {qv[0].x, qv[0].y, qv[0].z, qv[0].w, qv[1].x, qv[1].y, qv[1].z, qv[1].w};
 #pragma unroll
-      for (int k = 0; k < kQPasses; ++k) {
-        const int r = (threadIdx.x >> 3) + 32 * k, u = threadIdx.x & 7;
-        uint32_t z[8] = {qv[k][0].x, qv[k][0].y, qv[k][0].z, qv[k][0].w,
-                         qv[k][1].x, qv[k][1].y, qv[k][1].z, qv[k][1].w};
+      for (int j = 0; j < 8; ++j) z[j] ^= x.qflip;
+      float down = 1.0f;
+      if (F8) {
+        float top = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) z[j] ^= x.qflip;
-        float down = 1.0f;
-        if (F8) {
-          float top = 0.0f;
+        for (int j = 0; j < 8; ++j) top = fmaxf(top, fmaxf(fabsf(bf16_lo(z[j])), fabsf(bf16_hi(z[j]))));
 #pragma unroll
-          for (int j = 0; j < 8; ++j) top = fmaxf(top, fmaxf(fabsf(bf16_lo(z[j])), fabsf(bf16_hi(z[j]))));
+        for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        // 2^e with top 2^e in (224, 448]; rows of zeros or with infinities as they are.
+        const unsigned bits = __float_as_uint(top);
+        int e = ((bits & 0x7fffffu) > 0x600000u ? 134 : 135) - (int)(bits >> 23);
+        if (!(top > 0.0f) || !(top < INFINITY)) e = 0;
+        e = max(-126, min(126, e));
+        const float up = __int_as_float((e + 127) << 23);
+        down = __int_as_float((127 - e) << 23);
+        uint32_t hi[4], lo[4];
 #pragma unroll
-          for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-          // 2^e with top 2^e in (224, 448]; rows of zeros or with infinities as they are.
-          const unsigned bits = __float_as_uint(top);
-          int e = ((bits & 0x7fffffu) > 0x600000u ? 134 : 135) - (int)(bits >> 23);
-          if (!(top > 0.0f) || !(top < INFINITY)) e = 0;
-          e = max(-126, min(126, e));
-          const float up = __int_as_float((e + 127) << 23);
-          down = __int_as_float((127 - e) << 23);
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float y0 = bf16_lo(z[j]) * up, y1 = bf16_hi(z[j]) * up;
-            const uint32_t h = __nv_cvt_float2_to_fp8x2(make_float2(y0, y1), __NV_SATFINITE, __NV_E4M3);
-            const float2 back = __half22float2(e4m3_to_half2(h));
-            const uint32_t l =
-                __nv_cvt_float2_to_fp8x2(make_float2(y0 - back.x, y1 - back.y), __NV_SATFINITE, __NV_E4M3);
-            // e4m3 has no infinity: an infinite element counts as NaN.
-            const uint32_t nan = (isfinite(y0) ? 0u : 0x7fu) | (isfinite(y1) ? 0u : 0x7f00u);
-            if (j & 1) {
-              hi[j >> 1] |= (h | nan) << 16;
-              lo[j >> 1] |= (l | nan) << 16;
-            } else {
-              hi[j >> 1] = h | nan;
-              lo[j >> 1] = l | nan;
-            }
-          }
-          if (r < C::N1) {
-            unsigned char* at = qbuf + r * 128 + ((u ^ (r & 7)) << 4);
-            *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(at + C::N1 * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          }
-        } else if (r < C::N1) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int c = 2 * u + h;
-            *reinterpret_cast<uint4*>(qbuf + (c >> 3) * C::N1 * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
-                make_uint4(z[4 * h], z[4 * h + 1], z[4 * h + 2], z[4 * h + 3]);
+        for (int j = 0; j < 8; ++j) {
+          const float y0 = bf16_lo(z[j]) * up, y1 = bf16_hi(z[j]) * up;
+          const uint32_t c = __nv_cvt_float2_to_fp8x2(make_float2(y0, y1), __NV_SATFINITE, __NV_E4M3);
+          const float2 back = __half22float2(e4m3_to_half2(c));
+          const uint32_t l =
+              __nv_cvt_float2_to_fp8x2(make_float2(y0 - back.x, y1 - back.y), __NV_SATFINITE, __NV_E4M3);
+          // e4m3 has no infinity: an infinite element counts as NaN.
+          const uint32_t nan = (isfinite(y0) ? 0u : 0x7fu) | (isfinite(y1) ? 0u : 0x7f00u);
+          if (j & 1) {
+            hi[j >> 1] |= (c | nan) << 16;
+            lo[j >> 1] |= (l | nan) << 16;
+          } else {
+            hi[j >> 1] = c | nan;
+            lo[j >> 1] = l | nan;
           }
         }
-        if (u == 0 && r < RP) f.qc[parity][r] = x.c * down;
+        if (qpos < C::N1) {
+          unsigned char* at = qbuf + qpos * 128 + ((qu ^ (qpos & 7)) << 4);
+          *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(at + C::N1 * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+      } else if (qpos < C::N1) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int c = 2 * qu + k;
+          *reinterpret_cast<uint4*>(qbuf + (c >> 3) * C::N1 * 128 + qpos * 128 + (((c & 7) ^ (qpos & 7)) << 4)) =
+              make_uint4(z[4 * k], z[4 * k + 1], z[4 * k + 2], z[4 * k + 3]);
+        }
       }
+      if (qu == 0 && qrow < RP) f.qc[parity][qrow] = x.c * down;
       fence_async();
       fence_before();
       __syncwarp();
@@ -1554,14 +1599,17 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
       *k = __ldg(a.ks + at);
       *v = __ldg(a.vs + at);
     };
-    int id = -1, id_next = -1;
-    float ksc = 0.0f, vsc = 0.0f;
+    // A tile's scales are fetched two of the stream's tiles ahead, its page three.
+    int id = -1, id1 = -1, id2 = -1;
+    float ksc = 0.0f, vsc = 0.0f, ksc1 = 0.0f, vsc1 = 0.0f;
     if (threadIdx.x < RP) f.row_out[threadIdx.x] = threadIdx.x / G * a.Hq + threadIdx.x % G;
     if (w.more()) {
       id = page_of(w, s);
-      id_next = page_of(w, s + 2);
+      id1 = page_of(w, s + 2);
+      id2 = page_of(w, s + 4);
       fetch_q(w);
       scales_of(w, s, id, &ksc, &vsc);
+      scales_of(w, s + 2, id1, &ksc1, &vsc1);
       put_q(0);
     }
 
@@ -1572,68 +1620,77 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
       const bool tail = seq_ok && (long long)w.t1 * KT > w.ctx;
       int* par = t.par[item & 1][s];
       unsigned long long* anc = f.anc[item & 1][s];
-      const float* qc = f.qc[item & 1];
-      const float* mref = f.mref[s];
-      if (wt < RP) f.mref[s][wt] = wt < nrows ? kNoScore : 0.0f;
-      if (wt == 0) f.vref[s] = 0.0f;
+      const float* qc = f.qc[item & 1] + row0;
+      const float* mref = f.mref[s] + row0;
+      if (st < RP) f.mref[s][st] = st < nrows ? kNoScore : 0.0f;
+      if (st == 0) f.vref[s] = 0.0f;
       unsigned bad = seq_ok ? 0u : (unsigned)SV_DEV_PAGE_RANGE;
-      if (tail && wt < a.T) par[wt] = a.parents ? a.parents[(long long)w.b * a.T + wt] : wt - 1;
-      named_sync(1 + s, 128);
+      if (tail && st < a.T) par[st] = a.parents ? a.parents[(long long)w.b * a.T + st] : st - 1;
+      // The next item's first needs on their way to L2 while this one is worked on.
+      Walk<KT> nx = w;
+      nx.next(a);
+      if (nx.more() && q_on) asm volatile("prefetch.global.L2 [%0];" ::"l"(q_of(nx)));
+      named_sync(1 + s, 256);
       if (tail) {
-        if (wt < a.T) {
-          const int p = par[wt];
-          if (p < -2 || p >= wt || (p >= 0 && par[p] == -2)) bad |= SV_DEV_TREE;
+        if (st < a.T) {
+          const int p = par[st];
+          if (p < -2 || p >= st || (p >= 0 && par[p] == -2)) bad |= SV_DEV_TREE;
           unsigned long long set = 0;
 #pragma unroll 1
-          for (int j = wt, left = a.T; j >= 0 && left > 0; --left) {
+          for (int j = st, left = a.T; j >= 0 && left > 0; --left) {
             const int pj = par[j];
             if (pj == -2) break;
             set |= 1ull << j;
             j = pj < j ? pj : -1;
           }
-          anc[wt] = set;
+          anc[st] = set;
         }
-        named_sync(1 + s, 128);
+        named_sync(1 + s, 256);
       }
 
-      float l[RP];
+      float l[HR];
 #pragma unroll
-      for (int r = 0; r < RP; ++r) l[r] = 0.0f;
+      for (int r = 0; r < HR; ++r) l[r] = 0.0f;
       bool any = false;
 #pragma unroll 1
       for (int i = s; i < n; i += 2) {
         const int tile = w.t0 + i;
         const bool edge = (long long)(tile + 1) * KT > w.ctx || !seq_ok;
-        // Rows that attend this thread's key.
-        unsigned long long see = ~0ull;
+        // Rows of the half that attend this thread's key.
+        unsigned see = ~0u;
         const long long nd = (long long)tile * KT + wt - w.ctx;  // the key's node
         if (edge) {
+          unsigned long long all = ~0ull;
           if (!seq_ok || nd >= a.T) {
-            see = 0;
+            all = 0;
           } else if (nd >= 0) {
-            see = 0;
+            all = 0;
 #pragma unroll 1
             for (int k = (int)nd; k < a.T; ++k)  // a node's descendants come after it
-              if (anc[k] >> nd & 1ull) see |= ((1ull << G) - 1) << (k * G);
+              if (anc[k] >> nd & 1ull) all |= ((1ull << G) - 1) << (k * G);
           }
+          see = (unsigned)(all >> row0);
         }
-        // A needed page outside the cache or the table; the next tile's page and scales.
+        // A needed page outside the cache or the table; then the next pages and scales.
         if (seq_ok && (nd < 0 || (nd < a.T && par[nd] != -2)) && (id < 0 || id >= a.num_pages))
           bad |= SV_DEV_PAGE_RANGE;
         const float kc = F8 ? ksc : 1.0f;
         const float vs_now = see != 0 ? vsc : 0.0f;  // masked places may hold anything
-        scales_of(w, i + 2, id_next, &ksc, &vsc);
-        id = id_next;
-        id_next = page_of(w, i + 4);
+        ksc = ksc1;
+        vsc = vsc1;
+        scales_of(w, i + 4, id2, &ksc1, &vsc1);
+        id = id1;
+        id1 = id2;
+        id2 = page_of(w, i + 6);
 
         wait(&t.s_ready[s], scount & 1);
         fence_after();
         // Scores less m, in powers of two; masked ones -inf.
-        float y[RP];
+        float y[C::HS];
         auto scores = [&](bool less) {
-          tmem_ld_cols<RP>(sbase, y);
+          tmem_ld_cols<C::HS>(sbase, y);
 #pragma unroll
-          for (int r = 0; r < RP; r += 4) {
+          for (int r = 0; r < HR; r += 4) {
             const float4 c4 = *reinterpret_cast<const float4*>(qc + r);
             const float cc[4] = {c4.x, c4.y, c4.z, c4.w};
             float mm[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -1649,87 +1706,90 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
           }
           if (edge) {
 #pragma unroll
-            for (int r = 0; r < RP; ++r) y[r] = see >> r & 1ull ? y[r] : -INFINITY;
+            for (int r = 0; r < HR; ++r) y[r] = see >> r & 1u ? y[r] : -INFINITY;
           }
         };
         scores(true);
         float over[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int r = 0; r < RP; ++r) over[r & 3] = fmaxf(over[r & 3], y[r]);
+        for (int r = 0; r < HR; ++r) over[r & 3] = fmaxf(over[r & 3], y[r]);
         bool up = fmaxf(fmaxf(over[0], over[1]), fmaxf(over[2], over[3])) > C::kGrow;
         if (F8) up = up || vs_now > f.vref[s];
-        const bool raise = named_any(1 + s, 128, up);
+        const bool raise = named_any(1 + s, 256, up);
         if (any) {  // O and the P buffer of this stream: its last product must be complete
           wait(&t.pv_done[s], (scount - 1) & 1);
           fence_after();
         }
         if (raise) {
-          // New references: the warpgroup's maxima; then O and the sums to match.
+          // New references: the stream's maxima; then O and the sums to match.
           scores(false);
 #pragma unroll
-          for (int r = 0; r < RP; ++r) {
+          for (int r = 0; r < HR; ++r) {
             const float v = redux_max(y[r]);
-            if (lane == 0) f.wmax[s][q][r] = v;
+            if (lane == 0) f.wmax[s][q][row0 + r] = v;
           }
-          if (F8) {
+          if (F8) {  // (both halves have the same scales but where a mask parts them)
             const float v = redux_max(vs_now > 0.0f ? vs_now : 0.0f);
-            if (lane == 0) f.wvs[s][q] = v;
+            if (lane == 0) f.wvs[s][h][q] = v;
           }
-          named_sync(1 + s, 128);
+          named_sync(1 + s, 256);
           float g = 1.0f, vnew = 0.0f;
           if (F8) {
             const float vold = f.vref[s];
-            const float vtop = fmaxf(fmaxf(f.wvs[s][0], f.wvs[s][1]), fmaxf(f.wvs[s][2], f.wvs[s][3]));
+            float vtop = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) vtop = fmaxf(vtop, fmaxf(f.wvs[s][0][k], f.wvs[s][1][k]));
             const unsigned ex = (__float_as_uint(vtop) + 0x7fffffu) >> 23;  // power of two not below it
             vnew = fmaxf(vold, vtop > 0.0f ? __int_as_float(max(8u, min(250u, ex)) << 23) : 0.0f);
             if (vnew > vold) g = vold / vnew;
           }
-          if (wt < RP) {
-            const float top = fmaxf(fmaxf(f.wmax[s][0][wt], f.wmax[s][1][wt]),
-                                    fmaxf(f.wmax[s][2][wt], f.wmax[s][3][wt]));
-            const float old = mref[wt];
+          if (st < RP) {
+            const float top = fmaxf(fmaxf(f.wmax[s][0][st], f.wmax[s][1][st]),
+                                    fmaxf(f.wmax[s][2][st], f.wmax[s][3][st]));
+            const float old = f.mref[s][st];
             float fr = 1.0f;
-            if (wt < nrows && top > old) {  // every row that grew, so that the next raise is far
-              f.mref[s][wt] = top;
+            if (st < nrows && top > old) {  // every row that grew, so that the next raise is far
+              f.mref[s][st] = top;
               fr = ex2_fast(old - top);
             }
-            f.fac[s][wt] = fr;
+            f.fac[s][st] = fr;
           }
-          named_sync(1 + s, 128);
-          if (wt == 0 && F8) f.vref[s] = vnew;
+          named_sync(1 + s, 256);
+          if (st == 0 && F8) f.vref[s] = vnew;
+          const float* fac = f.fac[s] + row0;
 #pragma unroll
-          for (int r = 0; r < RP; ++r) {
-            l[r] *= f.fac[s][r];
+          for (int r = 0; r < HR; ++r) {
+            l[r] *= fac[r];
             y[r] -= mref[r];
           }
           if (any) {
 #pragma unroll 1
-            for (int pc = 0; pc < (F8 ? 3 : 1); ++pc) {
-#pragma unroll 1
-              for (int r = 0; r < RP; r += 8) {
-                float v[8];
-                uint32_t o[8];
-                tmem_ld8(obase + pc * RP + r, v);
+            for (int r = 0; r < HR; r += 4) {
+              const float4 f4 = *reinterpret_cast<const float4*>(fac + r);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) o[j] = __float_as_uint(v[j] * (f.fac[s][r + j] * g));
-                tmem_st8(obase + pc * RP + r, o);
+              for (int pc = 0; pc < (F8 ? 3 : 1); ++pc) {
+                float v[4];
+                tmem_ld4(obase + pc * HR + r, v);
+                tmem_st4(obase + pc * HR + r, v[0] * (f4.x * g), v[1] * (f4.y * g), v[2] * (f4.z * g),
+                         v[3] * (f4.w * g));
               }
             }
             tmem_wait_st();
           }
-          named_sync(1 + s, 128);  // fac and vref have been read and written
+          named_sync(1 + s, 256);  // fac and vref have been read and written
         }
-        // Weights, their sums, and P^T: this key's 128 bytes, rows one after another.
+        // Weights, their sums, and P^T: the half's part of this key's 128 bytes.
         float vs = 1.0f;
         if (F8) {
           const float vr = f.vref[s];
           vs = vr > 0.0f ? vs_now * (C::kLift * __fdividef(1.0f, vr)) : isnan(vs_now) ? vs_now : 0.0f;
         }
-        uint32_t words[32];
+        constexpr int kWords = C::HN / (F8 ? 4 : 2);
+        uint32_t words[kWords];
 #pragma unroll
-        for (int k = 0; k < 32; ++k) words[k] = 0;
+        for (int k = 0; k < kWords; ++k) words[k] = 0;
 #pragma unroll
-        for (int r = 0; r < RP; r += 4) {
+        for (int r = 0; r < HR; r += 4) {
           float p[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -1744,32 +1804,32 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
             p[3] = p1.y;
             if (edge) {  // the scale may be NaN
 #pragma unroll
-              for (int j = 0; j < 4; ++j) p[j] = see >> (r + j) & 1ull ? p[j] : 0.0f;
+              for (int j = 0; j < 4; ++j) p[j] = see >> (r + j) & 1u ? p[j] : 0.0f;
             }
             const __half2 sixteen = __half2half2(__ushort_as_half(0x4c00));
             uint32_t c[3][2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              const __half2 h = __floats2half2_rn(p[2 * j], p[2 * j + 1]);
-              c[0][j] = half2_to_e4m3(h);
-              const __half2 r1 = __hmul2(__hsub2(h, e4m3_to_half2(c[0][j])), sixteen);
+              const __half2 w0 = __floats2half2_rn(p[2 * j], p[2 * j + 1]);
+              c[0][j] = half2_to_e4m3(w0);
+              const __half2 r1 = __hmul2(__hsub2(w0, e4m3_to_half2(c[0][j])), sixteen);
               c[1][j] = half2_to_e4m3(r1);
               const __half2 r2 = __hmul2(__hsub2(r1, e4m3_to_half2(c[1][j])), sixteen);
               c[2][j] = half2_to_e4m3(r2);
             }
             words[r / 4] = __byte_perm(c[0][0], c[0][1], 0x5410);
-            words[(RP + r) / 4] = __byte_perm(c[1][0], c[1][1], 0x5410);
-            words[(2 * RP + r) / 4] = __byte_perm(c[2][0], c[2][1], 0x5410);
+            words[(HR + r) / 4] = __byte_perm(c[1][0], c[1][1], 0x5410);
+            words[(2 * HR + r) / 4] = __byte_perm(c[2][0], c[2][1], 0x5410);
           } else {
             words[r / 2] = pack_bf16(p[0], p[1]);
             words[r / 2 + 1] = pack_bf16(p[2], p[3]);
           }
         }
-        constexpr int kUnits = (F8 ? C::N2 : 2 * C::N2) / 16;
         unsigned char* prow = pbuf + s * C::kPBytes + wt * 128;
+        const int unit0 = h * (kWords / 4);
 #pragma unroll
-        for (int k = 0; k < kUnits; ++k)
-          *reinterpret_cast<uint4*>(prow + ((k ^ (wt & 7)) << 4)) =
+        for (int k = 0; k < kWords / 4; ++k)
+          *reinterpret_cast<uint4*>(prow + (((unit0 + k) ^ (wt & 7)) << 4)) =
               make_uint4(words[4 * k], words[4 * k + 1], words[4 * k + 2], words[4 * k + 3]);
         if (edge) {
           // 0 times what lies at masked positions must be 0: rows past the tree are zeroed, a
@@ -1780,7 +1840,7 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
             unsigned char* vrow = ring + (ev % C::kSlots) * C::kSlot + wt * 128;
             const bool dead = !seq_ok || nd >= a.T || par[nd] == -2;
 #pragma unroll 2
-            for (int u = 0; u < (F8 ? 8 : 16); ++u) {
+            for (int u = h * (F8 ? 4 : 8); u < (h + 1) * (F8 ? 4 : 8); ++u) {
               uint4* at = reinterpret_cast<uint4*>(vrow + (u >> 3) * KT * 128 + (((u & 7) ^ (wt & 7)) << 4));
               uint4 v = dead ? make_uint4(0, 0, 0, 0) : *at;
               uint32_t z[4] = {v.x, v.y, v.z, v.w}, found = 0;
@@ -1809,23 +1869,23 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
       entry0 += 2u * n;
 
       // ---- the item's end
-      Walk<KT> nx = w;
-      nx.next(a);
       if (nx.more()) {
         fetch_q(nx);
         id = page_of(nx, s);
-        id_next = page_of(nx, s + 2);
+        id1 = page_of(nx, s + 2);
+        id2 = page_of(nx, s + 4);
       }
       if (bad) {
         atomicOr(&t.bad[item & 1], 1u);
         atomicOr(a.status, bad);
       }
-      row_sums<RP>(l, lane, f.wsum[s][q]);
-      named_sync(3, 256);
+      row_sums<HR>(l, lane, f.wsum[s][q] + row0);
+      named_sync(3, 32 * kSoft);
       // Both streams have read their last S: the next item's Q may go in.
       if (nx.more()) {
         put_q((item + 1) & 1);
         scales_of(nx, s, id, &ksc, &vsc);
+        scales_of(nx, s + 2, id1, &ksc1, &vsc1);
       }
       const bool at_fault = t.bad[item & 1] != 0, badv = t.badv[item & 1] != 0;
       if (threadIdx.x < RP) {
@@ -1846,70 +1906,54 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
       }
       if (any) wait(&t.pv_done[s], (scount - 1) & 1);
       fence_before();
-      named_sync(3, 256);
+      named_sync(3, 32 * kSoft);
       fence_after();
       if (threadIdx.x == 0) t.bad[(item + 1) & 1] = t.badv[(item + 1) & 1] = 0;
       const bool whole = w.t0 == 0 && w.t1 == w.n;
       const long long slot = (long long)group * 2 + (w.t0 == 0 ? 1 : 0);
+      // A row a group of four warps and step (a short loop: it runs once an item).
+      const long long out0 = ((long long)w.b * a.T * a.Hq + w.hk * G) * a.D + wt;
 #pragma unroll 1
-      for (int r0 = 8 * s; r0 < RP && r0 < nrows; r0 += 16) {
+      for (int r = 2 * s + h; r < nrows; r += 4) {
         __syncwarp();  // tensor memory is read by whole warps
-        float v[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-#pragma unroll
-        for (int st = 0; st < 2; ++st) {
-          if (st == 1 && n < 2) break;
-          float u[8];
-          tmem_ld8(tmem + lanes + C::kO + 128 * st + r0, u);
-          if (F8) {
-            float u2[8], u3[8];
-            tmem_ld8(tmem + lanes + C::kO + 128 * st + RP + r0, u2);
-            tmem_ld8(tmem + lanes + C::kO + 128 * st + 2 * RP + r0, u3);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) u[j] = __fmaf_rn(__fmaf_rn(u3[j], 0.0625f, u2[j]), 0.0625f, u[j]);
-          }
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float g = st ? f.fin[r0 + j].y : f.fin[r0 + j].x;
-            v[j] = g == 0.0f ? v[j] : __fmaf_rn(u[j], g, v[j]);
-          }
+        const float4 fin = f.fin[r];
+        const unsigned col = tmem + lanes + C::kO + (r >= HR ? C::HN + r - HR : r);
+        float o0, o1 = 0.0f;
+        if (F8) {
+          float u[6];
+          tmem_ld_3x2(col, HR, 128, u);
+          o0 = __fmaf_rn(__fmaf_rn(u[2], 0.0625f, u[1]), 0.0625f, u[0]);
+          o1 = __fmaf_rn(__fmaf_rn(u[5], 0.0625f, u[4]), 0.0625f, u[3]);
+        } else {
+          tmem_ld_1x2(col, 128, &o0, &o1);
         }
+        // A stream that had no tile, or a row that it gave nothing, has factor 0.
+        float v = fin.x == 0.0f ? 0.0f : o0 * fin.x;
+        if (fin.y != 0.0f) v = __fmaf_rn(o1, fin.y, v);
         if (wt >= a.D) continue;
-        if (badv) {  // NaN and infinities of the nodes a row attends
-#pragma unroll 1
+        if (badv) {  // NaN and infinities of the nodes the row attends
           for (int k = 0; k < a.T; ++k) {
             const long long pos = (long long)w.ctx + k;
             if (pos < (long long)w.t0 * KT || pos >= (long long)w.t1 * KT || (pos >> x.lp) >= a.max_pages) continue;
             const int pg = a.page_table[(long long)w.b * a.max_pages + (pos >> x.lp)];
-            if (pg < 0 || pg >= a.num_pages) continue;
+            if (pg < 0 || pg >= a.num_pages || !(anc[r / G] >> k & 1ull)) continue;
             const long long at = (((long long)pg * a.Hkv + w.hk) * a.P + (pos & (a.P - 1))) * a.D + wt;
             const float z = F8 ? ((static_cast<const unsigned char*>(a.vc)[at] & 0x7f) == 0x7f
                                       ? __int_as_float(0x7fc00000)
                                       : 0.0f)
                                : __bfloat162float(static_cast<const __nv_bfloat16*>(a.vc)[at]);
-            if (isfinite(z)) continue;
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if (r0 + j < nrows && (anc[(r0 + j) / G] >> k & 1ull)) v[j] += z;
+            if (!isfinite(z)) v += z;
           }
         }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int r = r0 + j;
-          if (r >= nrows) break;
-          const float4 fin = f.fin[r];
-          if (whole) {
-            const float o = fin.z == 0.0f ? 0.0f : v[j] * fin.z;
-            a.out[((long long)w.b * a.T * a.Hq + w.hk * G + f.row_out[r]) * a.D + wt] = __float2bfloat16_rn(o);
-          } else {
-            x.part_o[(slot * nrows + r) * a.D + wt] = v[j];
-            if (wt == 0) x.part_ml[slot * nrows + r] = make_float2(fin.z, fin.w);
-          }
+        if (whole) {
+          a.out[out0 + (long long)f.row_out[r] * a.D] = __float2bfloat16_rn(fin.z == 0.0f ? 0.0f : v * fin.z);
+        } else {
+          x.part_o[(slot * nrows + r) * a.D + wt] = v;
+          if (wt == 0) x.part_ml[slot * nrows + r] = make_float2(fin.z, fin.w);
         }
       }
       if (!whole)
-        join_parts(x, t, w, 0, nrows, nrows, 256, nullptr);
+        join_parts(x, t, w, 0, nrows, nrows, 32 * kSoft, nullptr);
       w = nx;
     }
   }
