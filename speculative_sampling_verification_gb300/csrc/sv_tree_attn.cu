@@ -357,6 +357,8 @@ SV_DEVINL bool warps_sync(unsigned bar, unsigned& phase, int lane, volatile unsi
 }
 
 // Hardware barrier of `threads` threads, and the OR of their predicates.
+// The kernel launched before this one (which cleared the counters) is complete.
+SV_DEVINL void wait_for_clear() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 SV_DEVINL void named_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
@@ -380,7 +382,7 @@ SV_DEVINL int tiles_of(const Args& a, int ctx) {
 
 // Units of an item on the line before its tiles: what an item costs a CTA beside
 // its tiles (Q, the first references, the output), in tiles.
-constexpr int kItemUnits = 5;
+constexpr int kItemUnits = 8;
 
 // A CTA's way along its range: the item (b, hk), its tile count, context and the
 // tiles [t0, t1) of it that lie in the range.
@@ -488,28 +490,42 @@ __device__ __noinline__ bool join_parts(const TcArgs& x, TcTail& t, const Walk<K
     const int r = i / units, u = i - r * units;
     const int gr = part * cta_rows + r;
     if (gr >= x.rows) continue;
-    float top = -INFINITY;
+    // Eight parts at a time, their loads together; a running reference over the batches.
+    float top = -INFINITY, l = 0.0f;
     bool poison = false;
-    for (int g = gs; g <= ge; ++g) {
-      const long long sl = (long long)(g * x.parts_per_item + part) * 2 + (g == gs ? 1 : 0);
-      const float pm = __ldcg(&x.part_ml[sl * cta_rows + r]).x;
-      poison = poison || isnan(pm);
-      top = fmaxf(top, pm);
-    }
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    float l = 0.0f;
-#pragma unroll 4
-    for (int g = gs; g <= ge; ++g) {
-      const long long sl = (long long)(g * x.parts_per_item + part) * 2 + (g == gs ? 1 : 0);
-      const float2 ml = __ldcg(&x.part_ml[sl * cta_rows + r]);
-      const float4 o = __ldcg(reinterpret_cast<const float4*>(x.part_o + (sl * cta_rows + r) * a.D) + u);
-      if (ml.x == -INFINITY) continue;
-      const float f = ex2_fast((ml.x - top) * x.join_c);
-      l = fmaf(ml.y, f, l);
-      acc.x = fmaf(o.x, f, acc.x);
-      acc.y = fmaf(o.y, f, acc.y);
-      acc.z = fmaf(o.z, f, acc.z);
-      acc.w = fmaf(o.w, f, acc.w);
+#pragma unroll 1
+    for (int g0 = gs; g0 <= ge; g0 += 8) {
+      float2 ml[8];
+      float4 o[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int g = min(g0 + k, ge);
+        const long long sl = (long long)(g * x.parts_per_item + part) * 2 + (g == gs ? 1 : 0);
+        ml[k] = __ldcg(&x.part_ml[sl * cta_rows + r]);
+        o[k] = __ldcg(reinterpret_cast<const float4*>(x.part_o + (sl * cta_rows + r) * a.D) + u);
+      }
+      float nt = top;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (g0 + k > ge) ml[k].x = -INFINITY;
+        poison = poison || isnan(ml[k].x);
+        nt = fmaxf(nt, ml[k].x);
+      }
+      const float keep = top == -INFINITY ? 0.0f : ex2_fast((top - nt) * x.join_c);
+      l *= keep;
+      acc = make_float4(acc.x * keep, acc.y * keep, acc.z * keep, acc.w * keep);
+      top = nt;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (ml[k].x == -INFINITY) continue;
+        const float f = ex2_fast((ml[k].x - top) * x.join_c);
+        l = fmaf(ml[k].y, f, l);
+        acc.x = fmaf(o[k].x, f, acc.x);
+        acc.y = fmaf(o[k].y, f, acc.y);
+        acc.z = fmaf(o[k].z, f, acc.z);
+        acc.w = fmaf(o[k].w, f, acc.w);
+      }
     }
     const int nd = gr / G;
     const bool gone = a.parents && a.parents[(long long)w.b * a.T + nd] == -2;
@@ -593,6 +609,7 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  wait_for_clear();
   fence_before();
   __syncthreads();
   fence_after();
@@ -1302,9 +1319,9 @@ SV_DEVINL void tmem_ld_cols(unsigned t, float* v) {
   }
 }
 
-// Sums of v[0 .. N) over a warp: each step halves the lanes that share a row and the
-// rows that a lane holds (N shuffles in all, not 5 N), in the same order every time.
-template <int N, int O>
+// Sums (or maxima) of v[0 .. N) over a warp: each step halves the lanes that share a row
+// and the rows that a lane holds (N shuffles in all, not 5 N), in the same order every time.
+template <bool MAX, int N, int O>
 SV_DEVINL void halve(const float (&v)[N], int lane, int base, int count, float* out) {
   if constexpr (O == 0) {
 #pragma unroll
@@ -1317,16 +1334,12 @@ SV_DEVINL void halve(const float (&v)[N], int lane, int base, int count, float* 
 #pragma unroll
     for (int j = 0; j < H; ++j) {
       const float hi = j + H < N ? v[j + H] : 0.0f;
-      k[j] = (up ? hi : v[j]) + __shfl_xor_sync(0xffffffffu, up ? v[j] : hi, O);
+      const float mine = up ? hi : v[j], other = __shfl_xor_sync(0xffffffffu, up ? v[j] : hi, O);
+      k[j] = MAX ? fmaxf(mine, other) : mine + other;
     }
-    halve<H, O / 2>(k, lane, up ? base + H : base, up ? count - H : min(count, H), out);
+    halve<MAX, H, O / 2>(k, lane, up ? base + H : base, up ? count - H : min(count, H), out);
   }
 }
-template <int N>
-SV_DEVINL void row_sums(const float (&v)[N], int lane, float* out) {
-  halve<N, 16>(v, lane, 0, N, out);
-}
-
 // Place in the operand ring: K0 K1 K2 V0 K3 V1 ... (S^T of tile i + 2 before O^T of tile i).
 SV_DEVINL unsigned few_k(int i) { return i < 2 ? (unsigned)i : 2u * i - 2u; }
 SV_DEVINL unsigned few_v(int i, int n) { return (unsigned)min(2 * i + 3, n + i); }
@@ -1373,6 +1386,7 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  wait_for_clear();
   fence_before();
   __syncthreads();
   fence_after();
@@ -1723,10 +1737,11 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
         if (raise) {
           // New references: the stream's maxima; then O and the sums to match.
           scores(false);
+          {
+            float v[HR];
 #pragma unroll
-          for (int r = 0; r < HR; ++r) {
-            const float v = redux_max(y[r]);
-            if (lane == 0) f.wmax[s][q][row0 + r] = v;
+            for (int r = 0; r < HR; ++r) v[r] = y[r];
+            halve<true, HR, 16>(v, lane, 0, HR, f.wmax[s][q] + row0);
           }
           if (F8) {  // (both halves have the same scales but where a mask parts them)
             const float v = redux_max(vs_now > 0.0f ? vs_now : 0.0f);
@@ -1879,7 +1894,7 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
         atomicOr(&t.bad[item & 1], 1u);
         atomicOr(a.status, bad);
       }
-      row_sums<HR>(l, lane, f.wsum[s][q] + row0);
+      halve<false, HR, 16>(l, lane, 0, HR, f.wsum[s][q] + row0);
       named_sync(3, 32 * kSoft);
       // Both streams have read their last S: the next item's Q may go in.
       if (nx.more()) {
@@ -1913,7 +1928,7 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
       const long long slot = (long long)group * 2 + (w.t0 == 0 ? 1 : 0);
       // A row a group of four warps and step (a short loop: it runs once an item).
       const long long out0 = ((long long)w.b * a.T * a.Hq + w.hk * G) * a.D + wt;
-#pragma unroll 1
+#pragma unroll 2
       for (int r = 2 * s + h; r < nrows; r += 4) {
         __syncwarp();  // tensor memory is read by whole warps
         const float4 fin = f.fin[r];
@@ -1964,6 +1979,14 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
     fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
   }
+}
+
+// Clears the status word and the counters of parts. The attention kernel starts while it
+// runs (what came before it in the stream has ended by then), and waits for its end
+// before any of them is touched.
+__global__ void clear_kernel(unsigned* p, int n) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  for (int i = threadIdx.x; i < n; i += blockDim.x) p[i] = 0;
 }
 
 // ---------------------------------------------------------------- any shape
@@ -2175,6 +2198,23 @@ bool make_map(CUtensorMap* m, const void* base, const Args& a, bool f8, int dp, 
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A launch that may begin before the kernel ahead of it has ended.
+template <typename Kernel>
+int launch_early(Kernel kernel, unsigned grid, int threads, int smem, cudaStream_t st, const CUtensorMap& mk,
+                 const CUtensorMap& mv, const TcArgs& x) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, mk, mv, x) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+}
+
 template <int DP, bool F8, bool SHARED>
 int launch_tc(const TcArgs& x, cudaStream_t st) {
   constexpr int kSmem = tc_smem<DP, F8, SHARED>();
@@ -2194,9 +2234,8 @@ int launch_tc(const TcArgs& x, cudaStream_t st) {
   CUtensorMap mk, mv;
   if (!make_map(&mk, x.a.kc, x.a, F8, DP, x.box, !F8) || !make_map(&mv, x.a.vc, x.a, F8, DP, x.box, !F8))
     return SV_ERR_CUDA;
-  tree_attn_kernel<DP, F8, SHARED><<<(unsigned)(x.groups * x.parts_per_item), Cfg<DP, F8, SHARED>::kThreads, kSmem,
-                                     st>>>(mk, mv, x);
-  return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+  return launch_early(tree_attn_kernel<DP, F8, SHARED>, (unsigned)(x.groups * x.parts_per_item),
+                      Cfg<DP, F8, SHARED>::kThreads, kSmem, st, mk, mv, x);
 }
 
 template <int RP, bool F8>
@@ -2219,8 +2258,8 @@ int launch_few(const TcArgs& x, cudaStream_t st) {
   CUtensorMap mk, mv;
   if (!make_map(&mk, x.a.kc, x.a, F8, 128, x.box, true) || !make_map(&mv, x.a.vc, x.a, F8, 128, x.box, true))
     return SV_ERR_CUDA;
-  tree_attn_few_kernel<RP, F8><<<(unsigned)x.groups, FewCfg<RP, F8>::kThreads, kSmem, st>>>(mk, mv, x);
-  return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+  return launch_early(tree_attn_few_kernel<RP, F8>, (unsigned)x.groups, FewCfg<RP, F8>::kThreads, kSmem, st, mk, mv,
+                      x);
 }
 
 template <bool F8>
@@ -2312,7 +2351,8 @@ int sv_tree_attention(const void* q, int64_t q_stride_b, int64_t q_stride_t, int
     x.counters = reinterpret_cast<unsigned*>(ws + p.off_counters);
     x.part_ml = reinterpret_cast<float2*>(ws + p.off_ml);
     x.part_o = reinterpret_cast<float*>(ws + p.off_o);
-    if (cudaMemsetAsync(workspace, 0, p.off_ml, st) != cudaSuccess) return SV_ERR_CUDA;
+    clear_kernel<<<1, 256, 0, st>>>(static_cast<unsigned*>(workspace), (int)(p.off_ml / 4));
+    if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
     return cache_dtype == SV_E4M3 ? launch_tc_any<true>(x, p, st) : launch_tc_any<false>(x, p, st);
   }
   if (cudaMemsetAsync(workspace, 0, 4, st) != cudaSuccess) return SV_ERR_CUDA;
