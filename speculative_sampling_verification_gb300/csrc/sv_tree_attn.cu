@@ -73,7 +73,7 @@ constexpr int kSoftWarps = 8;
 constexpr int kProducer = 8, kIssuer = 9;
 constexpr int kMaxCtas = 152;
 constexpr int kScaleSlots = 8;
-constexpr int kMaxSlots = 10;
+constexpr int kMaxSlots = 8;
 constexpr int kFewRows = 40;    // rows up to which keys, not rows, are the M of the products
 constexpr float kLazy = 8.0f;   // growth of the maximum (powers of two) before O is rescaled
 
@@ -250,35 +250,6 @@ SV_DEVINL void tmem_ld64(unsigned t, float* v) {
 #pragma unroll
   for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
 }
-SV_DEVINL void tmem_ld16(unsigned t, float* v) {
-  uint32_t r[16];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
-      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15"
-      "}, [%16];\n\ttcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(t));
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-}
-SV_DEVINL void tmem_ld32(unsigned t, float* v) {
-  uint32_t r[32];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
-      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, "
-      "%18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31"
-      "}, [%32];\n\ttcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
-        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
-        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(t));
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-}
 SV_DEVINL void tmem_ld8(unsigned t, float (&v)[8]) {
   uint32_t r[8];
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
@@ -296,6 +267,20 @@ SV_DEVINL void tmem_st16(unsigned t, const uint32_t (&r)[16]) {
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
       "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
+}
+SV_DEVINL void tmem_ld24(unsigned t, float* v) {
+  uint32_t r[24];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%24];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%16, %17, %18, %19, %20, %21, %22, %23}, [%25];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=&r"(r[0]), "=&r"(r[1]), "=&r"(r[2]), "=&r"(r[3]), "=&r"(r[4]), "=&r"(r[5]), "=&r"(r[6]),
+        "=&r"(r[7]), "=&r"(r[8]), "=&r"(r[9]), "=&r"(r[10]), "=&r"(r[11]), "=&r"(r[12]),
+        "=&r"(r[13]), "=&r"(r[14]), "=&r"(r[15]), "=&r"(r[16]), "=&r"(r[17]), "=&r"(r[18]),
+        "=&r"(r[19]), "=&r"(r[20]), "=&r"(r[21]), "=&r"(r[22]), "=&r"(r[23])
+      : "r"(t), "r"(t + 16));
+#pragma unroll
+  for (int i = 0; i < 24; ++i) v[i] = __uint_as_float(r[i]);
 }
 SV_DEVINL void tmem_ld4(unsigned t, float (&v)[4]) {
   uint32_t r[4];
@@ -382,7 +367,7 @@ SV_DEVINL int tiles_of(const Args& a, int ctx) {
 
 // Units of an item on the line before its tiles: what an item costs a CTA beside
 // its tiles (Q, the first references, the output), in tiles.
-constexpr int kItemUnits = 8;
+constexpr int kItemUnits = 10;
 
 // A CTA's way along its range: the item (b, hk), its tile count, context and the
 // tiles [t0, t1) of it that lie in the range.
@@ -1249,8 +1234,10 @@ struct FewCfg {
   static constexpr int kPBytes = KT * 128;
   static constexpr int kSlot = KT * (F8 ? 128 : 256);
   static constexpr int kTailBytes = 12 * 1024;
-  static constexpr int kFit = (226 * 1024 - kTailBytes - kQBytes - 2 * kPBytes) / kSlot;
-  static constexpr int kSlots = kFit < kMaxSlots ? kFit : kMaxSlots;
+  static constexpr int kFit = (226 * 1024 - kTailBytes - kQBytes - 4 * kPBytes) / kSlot;
+  // More than 96 KB in flight on each SM only lengthens the queue at the memory: an
+  // e4m3 cache's batch took 219 us with ten slots, 214 with seven, 210 with five.
+  static constexpr int kSlots = kFit < 6 ? kFit : 6;
   static constexpr int kSoft = 16;                                 // softmax warps
   static constexpr int kThreads = 32 * (kSoft + 2);
   static constexpr unsigned kS = 0, kO = 256;  // tensor memory: two of each, 128 columns apart
@@ -1279,7 +1266,7 @@ constexpr int few_smem() {
   using C = FewCfg<RP, F8>;
   static_assert(sizeof(FewTail<RP>) <= C::kTailBytes, "tail");
   static_assert(C::HR % 4 == 0 && C::kQBytes % 2048 == 0, "rows of four values, blocks of 1024 bytes");
-  return 1024 + C::kQBytes + 2 * C::kPBytes + C::kSlots * C::kSlot + (int)sizeof(FewTail<RP>);
+  return 1024 + C::kQBytes + 4 * C::kPBytes + C::kSlots * C::kSlot + (int)sizeof(FewTail<RP>);
 }
 
 SV_DEVINL float redux_max(float v) {
@@ -1305,12 +1292,9 @@ SV_DEVINL __half2 e4m3_to_half2(uint32_t c) {
 
 template <int N>
 SV_DEVINL void tmem_ld_cols(unsigned t, float* v) {
-  if constexpr (N >= 32) {
-    tmem_ld32(t, v);
-    if constexpr (N > 32) tmem_ld_cols<N - 32>(t + 32, v + 32);
-  } else if constexpr (N >= 16) {
-    tmem_ld16(t, v);
-    if constexpr (N > 16) tmem_ld_cols<N - 16>(t + 16, v + 16);
+  static_assert(N == 24 || N == 8, "columns of a half");
+  if constexpr (N == 24) {
+    tmem_ld24(t, v);
   } else {
     float u[8];
     tmem_ld8(t, u);
@@ -1354,8 +1338,8 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                          ~static_cast<uintptr_t>(1023));
-  unsigned char* pbuf = smem;                          // [2][128 keys][128 bytes]
-  unsigned char* ring = pbuf + 2 * C::kPBytes;
+  unsigned char* pbuf = smem;                          // [tile of four][128 keys][128 bytes]
+  unsigned char* ring = pbuf + 4 * C::kPBytes;
   unsigned char* qbuf = ring + C::kSlots * C::kSlot;   // [2 blocks][N1 rows][128 bytes]
   FewTail<RP>& f = *reinterpret_cast<FewTail<RP>*>(qbuf + C::kQBytes);
   TcTail& t = f.t;
@@ -1498,7 +1482,7 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
         const unsigned e = entry0 + few_v(i, n);
         if (!ok || !full(e)) break;
         const uint64_t v = desc_n(uni(smem_u32(ring + (e % C::kSlots) * C::kSlot)), KT * 128);
-        const uint64_t p = desc_n(uni(smem_u32(pbuf + s * C::kPBytes)), KT * 128);
+        const uint64_t p = desc_n(uni(smem_u32(pbuf + (i & 3) * C::kPBytes)), KT * 128);
         const unsigned d = uni(tmem + C::kO + 128 * s);
 #pragma unroll
         for (int j = 0; j < (F8 ? 4 : 8); ++j) {
@@ -1641,9 +1625,11 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
       unsigned bad = seq_ok ? 0u : (unsigned)SV_DEV_PAGE_RANGE;
       if (tail && st < a.T) par[st] = a.parents ? a.parents[(long long)w.b * a.T + st] : st - 1;
       // The next item's first needs on their way to L2 while this one is worked on.
-      Walk<KT> nx = w;
-      nx.next(a);
-      if (nx.more() && q_on) asm volatile("prefetch.global.L2 [%0];" ::"l"(q_of(nx)));
+      {
+        Walk<KT> nx = w;
+        nx.next(a);
+        if (nx.more() && q_on) asm volatile("prefetch.global.L2 [%0];" ::"l"(q_of(nx)));
+      }
       named_sync(1 + s, 256);
       if (tail) {
         if (st < a.T) {
@@ -1690,12 +1676,16 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
           bad |= SV_DEV_PAGE_RANGE;
         const float kc = F8 ? ksc : 1.0f;
         const float vs_now = see != 0 ? vsc : 0.0f;  // masked places may hold anything
-        ksc = ksc1;
-        vsc = vsc1;
-        scales_of(w, i + 4, id2, &ksc1, &vsc1);
         id = id1;
-        id1 = id2;
-        id2 = page_of(w, i + 6);
+        if (F8) {
+          ksc = ksc1;
+          vsc = vsc1;
+          scales_of(w, i + 4, id2, &ksc1, &vsc1);
+          id1 = id2;
+          id2 = page_of(w, i + 6);
+        } else {
+          id1 = page_of(w, i + 4);
+        }
 
         wait(&t.s_ready[s], scount & 1);
         fence_after();
@@ -1730,11 +1720,13 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
         bool up = fmaxf(fmaxf(over[0], over[1]), fmaxf(over[2], over[3])) > C::kGrow;
         if (F8) up = up || vs_now > f.vref[s];
         const bool raise = named_any(1 + s, 256, up);
-        if (any) {  // O and the P buffer of this stream: its last product must be complete
-          wait(&t.pv_done[s], (scount - 1) & 1);
-          fence_after();
-        }
+        // (This tile's P buffer is free: its S^T was issued, and announced, after the
+        // product that read the buffer four tiles ago.)
         if (raise) {
+          if (any) {  // O of this stream: its last product must be complete
+            wait(&t.pv_done[s], (scount - 1) & 1);
+            fence_after();
+          }
           // New references: the stream's maxima; then O and the sums to match.
           scores(false);
           {
@@ -1840,7 +1832,7 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
             words[r / 2 + 1] = pack_bf16(p[2], p[3]);
           }
         }
-        unsigned char* prow = pbuf + s * C::kPBytes + wt * 128;
+        unsigned char* prow = pbuf + (i & 3) * C::kPBytes + wt * 128;
         const int unit0 = h * (kWords / 4);
 #pragma unroll
         for (int k = 0; k < kWords / 4; ++k)
@@ -1884,6 +1876,8 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
       entry0 += 2u * n;
 
       // ---- the item's end
+      Walk<KT> nx = w;
+      nx.next(a);
       if (nx.more()) {
         fetch_q(nx);
         id = page_of(nx, s);
