@@ -57,24 +57,31 @@ struct Args {
 };
 
 struct Exchange {
-  double sum[2][kMaxCluster];  // per CTA: of q and p, or of the residual
+  alignas(8) ff sum[2][kMaxCluster];  // per CTA: of q and p, or of the residual
   float top[2][kMaxCluster];   // per CTA: row maxima
 };
 
 struct Shared {
   float2 tab[256];
   Exchange x[2];
-  double wsum[2][2][kWarps];  // [buffer][q or p][warp]: sums of the warps' regions
+  ff wsum[2][2][kWarps];      // [buffer][q or p][warp]: sums of the warps' regions
   float wtop[2][kWarps];
-  double cta_sum[2][kMaxCluster];  // [buffer]: the CTAs' sums of the current residual
+  ff cta_sum[2][kMaxCluster];  // [buffer]: the CTAs' sums of the current residual
   double ratio[kTreeMax];  // q(x)/p(x) of the children's tokens
   int parents[kTreeMax], tokens[kTreeMax], drow[kTreeMax];
   float u[kTreeMax];
   int path[kTreeMax];
   float m[2];
   double S[2];
-  double Z;
+  // The deciding warp's word to the others: the next node, kDraw, or kResidual (a pass for a
+  // new residual with these scalars; `keep` of the last one).
+  int next;
+  ff a, b;
+  int keep;
+  unsigned failure;
 };
+
+constexpr int kDraw = -1, kResidual = -2;
 
 template <int DT>
 SV_DEVINL float load_one(const void* row, long long i) {
@@ -116,9 +123,9 @@ SV_DEVINL ff2 weight2(float2 l, float nm, const Args& a, const float2* tab) {
   return exp_ff2(x.hi, x.lo, tab);
 }
 
-SV_DEVINL double weight(float l, float m, const Args& a, const float2* tab) {
+SV_DEVINL ff weight_ff(float l, float m, const Args& a, const float2* tab) {
   const ff x = scaled_diff(l, m, a.ih, a.il, a.unit_t != 0);
-  return ff_to_double(exp_ff(x.hi, x.lo, tab));
+  return exp_ff(x.hi, x.lo, tab);
 }
 
 // A pass's weights: w(x) = e_q max(0, a - b e^d) with e_q = exp((lq - mq)/T) and
@@ -157,13 +164,13 @@ SV_DEVINL ff2 mix2(float2 lq, float2 lp, const Mix& x, const Args& a, const floa
   const float2 pe = f2_fma(r.hi, f2(-x.b.hi), f2_mul(ph, f2(-1.0f)));
   const float2 pl = f2_sub(pe, f2_fma(r.hi, f2(x.b.lo), f2_mul(r.lo, f2(x.b.hi))));
   const ff2 t0 = two_sum2(f2(x.a.hi), ph);
-  const float2 tl = f2_add(t0.lo, f2_add(f2(x.a.lo), pl));
+  // (Normalised: where the heads cancel, the tails are all there is.)
+  const ff2 t = two_sum2(t0.hi, f2_add(t0.lo, f2_add(f2(x.a.lo), pl)));
   // w = e t, 0 where t is not positive or the target has no such token
-  const float2 wh = f2_mul(e.hi, t0.hi);
-  const float2 we = f2_fma(e.hi, t0.hi, f2_mul(wh, f2(-1.0f)));
-  const float2 wl = f2_add(we, f2_fma(e.hi, tl, f2_mul(e.lo, t0.hi)));
-  const float2 s = f2_add(t0.hi, tl);
-  const bool kx = e.hi.x > 0.0f && s.x > 0.0f, ky = e.hi.y > 0.0f && s.y > 0.0f;
+  const float2 wh = f2_mul(e.hi, t.hi);
+  const float2 we = f2_fma(e.hi, t.hi, f2_mul(wh, f2(-1.0f)));
+  const float2 wl = f2_add(we, f2_fma(e.hi, t.lo, f2_mul(e.lo, t.hi)));
+  const bool kx = e.hi.x > 0.0f && t.hi.x > 0.0f, ky = e.hi.y > 0.0f && t.hi.y > 0.0f;
   return {make_float2(kx ? wh.x : 0.0f, ky ? wh.y : 0.0f),
           make_float2(kx ? wl.x : 0.0f, ky ? wl.y : 0.0f)};
 }
@@ -183,21 +190,17 @@ SV_DEVINL void mix8(const Mix& x, int e, int end, const Args& a, const float2* t
   for (int i = 0; i < 4; ++i) w[i] = mix2(q[i], p[i], x, a, tab);
 }
 
-SV_DEVINL double warp_sum(double v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-
-SV_DEVINL double ff2_total(const ff2& s) {
-  return ((double)s.hi.x + (double)s.hi.y) + ((double)s.lo.x + (double)s.lo.y);
+// fp64 runs at a 64th of the fp32 rate here: it is left to one warp's decisions, and
+// sums are float-floats (about 2^-44).
+SV_DEVINL ff ff2_warp_sum(const ff2& s) {
+  return ff_warp_sum(ff_add({s.hi.x, s.lo.x}, {s.hi.y, s.lo.y}));
 }
 
 // Maximum and sum of exp((l - max)/T) over a warp's region of one row. NaN and
 // +inf end in a NaN sum; a region of -inf has the maximum -inf and the sum 0.
 template <int DT, bool VEC>
 SV_DEVINL void region_stats(const void* row, int begin, int end, int lane, const Args& a,
-                            const float2* tab, float* top, double* sum) {
+                            const float2* tab, float* top, ff* sum) {
   float m = neg_inf();
 #pragma unroll 4
   for (int e = begin + lane * 8; e < end; e += kStep) {
@@ -219,12 +222,12 @@ SV_DEVINL void region_stats(const void* row, int begin, int end, int lane, const
   }
   acc.hi = f2_add(acc.hi, f2(-1.0f));
   *top = m;
-  *sum = warp_sum(ff2_total(acc));
+  *sum = ff2_warp_sum(acc);
 }
 
 // Sum of the residual's weights over a warp's region.
 template <int DT, bool VEC>
-SV_DEVINL double region_mix(const Mix& x, int begin, int end, int lane, const Args& a, const float2* tab) {
+SV_DEVINL ff region_mix(const Mix& x, int begin, int end, int lane, const Args& a, const float2* tab) {
   ff2 acc = {f2(0.0f), f2(0.0f)};
   for (int e = begin + lane * 8; e < end; e += kStep) {
     ff2 w[4];
@@ -236,12 +239,7 @@ SV_DEVINL double region_mix(const Mix& x, int begin, int end, int lane, const Ar
       acc.lo = f2_add(acc.lo, f2_add(s.lo, w[i].lo));
     }
   }
-  return warp_sum(ff2_total(acc));
-}
-
-// exp((part - whole)/T) of two maxima; 0 for a part without an entry.
-SV_DEVINL double rescale(float part, float whole, const Args& a, const float2* tab) {
-  return part == neg_inf() ? 0.0 : weight(part, whole, a, tab);
+  return ff2_warp_sum(acc);
 }
 
 // exp(((lq - mq) - (lp - mp))/T), c = mq - mp: from the difference of the logits, so
@@ -263,48 +261,47 @@ SV_DEVINL double token_ratio(float lq, float lp, ff c, const Args& a, const floa
 // The token at which the running sum of the region's weights passes `target`,
 // or the region's last token of positive weight.
 template <int DT, bool VEC>
-SV_DEVINL int region_draw(const Mix& x, int begin, int end, double target, int lane, const Args& a,
+SV_DEVINL int region_draw(const Mix& x, int begin, int end, ff target, int lane, const Args& a,
                           const float2* tab) {
-  double before = 0.0;
+  ff before = {0.0f, 0.0f};
   int last = -1;
+#pragma unroll 1
   for (int e0 = begin; e0 < end; e0 += kStep) {
     const int e = e0 + lane * 8;
     ff2 w[4];
     mix8<DT, VEC>(x, e, end, a, tab, w);
-    double v[8], mine = 0.0;
+    ff mine = {0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      v[2 * i] = (double)w[i].hi.x + (double)w[i].lo.x;
-      v[2 * i + 1] = (double)w[i].hi.y + (double)w[i].lo.y;
+      mine = ff_add(mine, {w[i].hi.x, w[i].lo.x});
+      mine = ff_add(mine, {w[i].hi.y, w[i].lo.y});
+      if (w[i].hi.x > 0.0f) last = e + 2 * i;
+      if (w[i].hi.y > 0.0f) last = e + 2 * i + 1;
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      mine += v[i];
-      if (v[i] > 0.0) last = e + i;
-    }
-    double incl = mine;
+    ff incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const double t = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += t;
+      const ff t = ff_shfl_up(incl, o);
+      if (lane >= o) incl = ff_add(incl, t);
     }
-    const unsigned hit = __ballot_sync(0xffffffffu, before + incl > target);
+    const unsigned hit = __ballot_sync(0xffffffffu, ff_gt(ff_add(before, incl), target));
     if (hit) {
       const int owner = __ffs(hit) - 1;
       int token = e;
       if (lane == owner) {
-        double run = before + (incl - mine);
+        ff run = ff_add(before, ff_sub(incl, mine));
         token = -1;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          run += v[i];
-          if (token < 0 && v[i] > 0.0 && run > target) token = e + i;
+          const ff v = i & 1 ? ff{w[i >> 1].hi.y, w[i >> 1].lo.y} : ff{w[i >> 1].hi.x, w[i >> 1].lo.x};
+          run = ff_add(run, v);
+          if (token < 0 && v.hi > 0.0f && ff_gt(run, target)) token = e + i;
         }
         if (token < 0) token = last;  // the sums' rounding hid the step
       }
       return __shfl_sync(0xffffffffu, token, owner);
     }
-    before += __shfl_sync(0xffffffffu, incl, 31);
+    before = ff_add(before, {__shfl_sync(0xffffffffu, incl.hi, 31), __shfl_sync(0xffffffffu, incl.lo, 31)});
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) last = max(last, __shfl_xor_sync(0xffffffffu, last, o));
@@ -370,20 +367,14 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(Args a, int nc) {
                          : nullptr;
     // ---- maxima and sums of the node's rows
     buf = 0;
-    {
+#pragma unroll 1
+    for (int r = 0; r < (kids ? 2 : 1); ++r) {
       float top;
-      double sum;
-      region_stats<DT, VEC>(q, begin, end, lane, a, sh.tab, &top, &sum);
+      ff sum;
+      region_stats<DT, VEC>(r ? p : q, begin, end, lane, a, sh.tab, &top, &sum);
       if (lane == 0) {
-        sh.wtop[0][warp] = top;
-        sh.wsum[0][0][warp] = sum;
-      }
-      if (kids) {
-        region_stats<DT, VEC>(p, begin, end, lane, a, sh.tab, &top, &sum);
-        if (lane == 0) {
-          sh.wtop[1][warp] = top;
-          sh.wsum[0][1][warp] = sum;
-        }
+        sh.wtop[r][warp] = top;
+        sh.wsum[0][r][warp] = sum;
       }
     }
     __syncthreads();
@@ -396,16 +387,16 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(Args a, int nc) {
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
       // A region's sum may be NaN although its maximum is -inf: it counts.
-      double s = 0.0;
+      ff s = {0.0f, 0.0f};
       if (lane < kWarps) {
-        const double own = sh.wsum[0][r][lane];
-        s = own == 0.0 ? 0.0 : own * (t == neg_inf() ? 1.0 : weight(t, m, a, sh.tab));
+        s = sh.wsum[0][r][lane];
+        if (s.hi != 0.0f && t != neg_inf()) s = ff_mul(s, weight_ff(t, m, a, sh.tab));
         sh.wsum[0][r][lane] = s;  // now relative to the CTA's maximum
       }
-      s = warp_sum(s);
+      s = ff_warp_sum(s);
       if (lane < nc) {
         const unsigned dst = dsmem_map(smem_u32(&ex.sum[r][rank]), lane);
-        dsmem_st_u64(dst, (unsigned long long)__double_as_longlong(s));
+        dsmem_st_f32x2(dst, s.hi, s.lo);
         dsmem_st_f32(dsmem_map(smem_u32(&ex.top[r][rank]), lane), m);
       }
     }
@@ -416,92 +407,117 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(Args a, int nc) {
       float m = t;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      double s = 0.0;
+      ff s = {0.0f, 0.0f}, w = {1.0f, 0.0f};
+      if (t != neg_inf()) w = weight_ff(t, m, a, sh.tab);
       if (lane < nc) {
-        const double own = ex.sum[r][lane];
-        s = own == 0.0 ? 0.0 : own * (t == neg_inf() ? 1.0 : weight(t, m, a, sh.tab));
+        s = ex.sum[r][lane];
+        if (s.hi != 0.0f) s = ff_mul(s, w);
         if (r == 0) sh.cta_sum[0][lane] = s;
       }
-      const double cta_scale = rescale(__shfl_sync(0xffffffffu, t, rank), m, a, sh.tab);
-      if (r == 0 && lane < kWarps) sh.wsum[0][0][lane] *= cta_scale;
-      s = warp_sum(s);
+      // The regions' sums, relative to the row's maximum.
+      const ff cw = {__shfl_sync(0xffffffffu, w.hi, rank), __shfl_sync(0xffffffffu, w.lo, rank)};
+      if (r == 0 && lane < kWarps && sh.wsum[0][0][lane].hi != 0.0f)
+        sh.wsum[0][0][lane] = ff_mul(sh.wsum[0][0][lane], cw);
+      s = ff_warp_sum(s);
       if (lane == 0) {
         sh.m[r] = m;
-        sh.S[r] = s;
+        sh.S[r] = ff_to_double(s);
       }
     }
     __syncthreads();
-    for (int r = 0; r < (kids ? 2 : 1); ++r) {
-      if (!(sh.S[r] < INFINITY) || sh.m[r] == INFINITY) failure |= SV_DEV_NONFINITE;
-      else if (sh.m[r] == neg_inf()) failure |= SV_DEV_EMPTY_ROW;
-    }
-    if (failure) break;
     x = Mix{};
     x.q = q;
     x.p = p;
     x.nmq = -sh.m[0];
     x.plain = true;
-    if (!kids) break;
-    x.c = two_sum(sh.m[0], -sh.m[1]);
-    const double Sq = sh.S[0], Sp = sh.S[1];
-    for (int i = cur + 1 + tid; i < T; i += kThreads) {
-      if (sh.parents[i] != cur) continue;
-      sh.ratio[i] = token_ratio(load_one<DT>(q, sh.tokens[i]), load_one<DT>(p, sh.tokens[i]), x.c, a, sh.tab) *
-                    (Sp / Sq);
-    }
-    __syncthreads();
+    if (kids) x.c = two_sum(sh.m[0], -sh.m[1]);
 
-    // ---- the children in turn
-    double A = 1.0, Bp = 0.0;
-    int next = -1;
-    for (int i = cur + 1; i < T && next < 0; ++i) {
-      if (sh.parents[i] != cur) continue;
-      // r(x)/p(x) = A q/p - B
-      if ((double)sh.u[i] < fmin(1.0, A * sh.ratio[i] - Bp)) {
-        next = i;
-        break;
+    // ---- the children in turn, by warp 0 of each CTA alike; the others serve its passes
+    double A = 1.0, Bp = 0.0, scale = 1.0, q_over_p = 1.0, Sq = 1.0;
+    int i = cur + 1;
+    if (warp == 0) {
+      unsigned f = 0;
+      for (int r = 0; r < (kids ? 2 : 1); ++r) {
+        if (!(sh.S[r] < INFINITY) || sh.m[r] == INFINITY) f |= SV_DEV_NONFINITE;
+        else if (sh.m[r] == neg_inf()) f |= SV_DEV_EMPTY_ROW;
       }
-      // Scaled by a power of two so that the larger scalar lies in [1, 2).
-      const double s = exp2(-(double)ilogb(fmax(A, Bp + 1.0)));
-      const double fa = A * s, fb = (Bp + 1.0) * s * (Sq / Sp);
+      if (lane == 0) sh.failure = f;
+      if (kids && !f) {
+        Sq = sh.S[0];
+        q_over_p = Sq / sh.S[1];
+        const double p_over_q = sh.S[1] / Sq;
+        for (int k = cur + 1 + lane; k < T; k += 32)
+          if (sh.parents[k] == cur)
+            sh.ratio[k] = token_ratio(load_one<DT>(q, sh.tokens[k]), load_one<DT>(p, sh.tokens[k]), x.c, a, sh.tab) *
+                          p_over_q;
+      }
+      __syncwarp();
+    }
+    int next;
+    for (;;) {
+      if (warp == 0) {
+        int to = kDraw;
+        for (; i < T; ++i) {
+          if (sh.parents[i] != cur) continue;
+          // r(x)/p(x) = A q/p - B
+          to = (double)sh.u[i] < fmin(1.0, A * sh.ratio[i] - Bp) ? i : kResidual;
+          ++i;
+          break;
+        }
+        if (to == kResidual && sh.failure == 0) {
+          // Scaled by a power of two so that the larger scalar lies in [1, 2).
+          const int ex2 = ilogb(fmax(A, Bp + 1.0));
+          scale = ldexp(1.0, -ex2);
+          const double fa = A * scale, fb = (Bp + 1.0) * scale * q_over_p;
+          if (lane == 0) {
+            sh.a = {(float)fa, (float)(fa - (double)(float)fa)};
+            sh.b = {(float)fb, (float)(fb - (double)(float)fb)};
+          }
+        }
+        if (lane == 0) sh.next = to;
+      }
+      __syncthreads();
+      next = sh.next;
+      failure = sh.failure;
+      if (failure || next != kResidual) break;
       Mix y = x;
       y.plain = false;
-      y.a = {(float)fa, (float)(fa - (double)(float)fa)};
-      y.b = {(float)fb, (float)(fb - (double)(float)fb)};
+      y.a = sh.a;
+      y.b = sh.b;
       const int nb = buf ^ 1;
-      const double sum = region_mix<DT, VEC>(y, begin, end, lane, a, sh.tab);
+      const ff sum = region_mix<DT, VEC>(y, begin, end, lane, a, sh.tab);
       if (lane == 0) sh.wsum[nb][0][warp] = sum;
       __syncthreads();
       Exchange& ez = sh.x[phase & 1];
       ++phase;
       if (warp == 0) {
-        const double c = warp_sum(lane < kWarps ? sh.wsum[nb][0][lane] : 0.0);
-        if (lane < nc)
-          dsmem_st_u64(dsmem_map(smem_u32(&ez.sum[0][rank]), lane),
-                       (unsigned long long)__double_as_longlong(c));
+        const ff c = ff_warp_sum(lane < kWarps ? sh.wsum[nb][0][lane] : ff{0.0f, 0.0f});
+        if (lane < nc) dsmem_st_f32x2(dsmem_map(smem_u32(&ez.sum[0][rank]), lane), c.hi, c.lo);
       }
       cluster_sync();
       if (warp == 0) {
-        const double c = lane < nc ? ez.sum[0][lane] : 0.0;
+        const ff c = lane < nc ? ez.sum[0][lane] : ff{0.0f, 0.0f};
         if (lane < nc) sh.cta_sum[nb][lane] = c;
-        const double z = warp_sum(c);
-        if (lane == 0) sh.Z = z;
+        const double Z = ff_to_double(ff_warp_sum(c)) / (Sq * scale);
+        const bool keep = Z >= kResidualMin;
+        if (keep) {
+          const double inv = 1.0 / Z;
+          A *= inv;
+          Bp = (Bp + 1.0) * inv;
+        }
+        if (lane == 0) sh.keep = keep;
       }
       __syncthreads();
-      const double Z = sh.Z / (Sq * s);
-      if (Z >= kResidualMin) {
-        A = A / Z;
-        Bp = (Bp + 1.0) / Z;
+      if (sh.keep) {
         x = y;
         buf = nb;
       }
-      __syncthreads();  // sh.Z and the other buffer are free again
     }
-    if (next < 0) break;
+    __syncthreads();  // sh.next and sh.failure have been read
+    if (failure || next < 0) break;
     if (tid == 0) sh.path[count] = next;
     ++count;
     cur = next;
-    __syncthreads();
   }
 
   if (failure) {
@@ -524,21 +540,22 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(Args a, int nc) {
     }
     if (tid == 0) a.n_acc[b] = count;
   }
-  double total = 0.0;
-  for (int c = 0; c < nc; ++c) total += sh.cta_sum[buf][c];
-  const double goal = (double)sh.u[0] * total;
-  double before = 0.0, at = 0.0;
+  ff total = {0.0f, 0.0f};
+  for (int c = 0; c < nc; ++c) total = ff_add(total, sh.cta_sum[buf][c]);
+  const ff goal = ff_mul_f(total, sh.u[0]);
+  ff before = {0.0f, 0.0f}, at = {0.0f, 0.0f};
   int owner = -1, last = 0;
   for (int c = 0; c < nc; ++c) {
-    const double s = sh.cta_sum[buf][c];
-    if (s > 0.0) {
+    const ff s = sh.cta_sum[buf][c];
+    const ff upto = ff_add(before, s);
+    if (s.hi > 0.0f) {
       last = c;
-      if (owner < 0 && before + s > goal) {
+      if (owner < 0 && ff_gt(upto, goal)) {
         owner = c;
         at = before;
       }
     }
-    before += s;
+    before = upto;
   }
   const bool past = owner < 0;  // u = 1: the last token of positive weight
   if (past) owner = last;
@@ -547,20 +564,22 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(Args a, int nc) {
   int w = -1;
   last = 0;
   for (int i = 0; i < kWarps; ++i) {
-    const double s = sh.wsum[buf][0][i];
-    if (s > 0.0) {
+    const ff s = sh.wsum[buf][0][i];
+    const ff upto = ff_add(before, s);
+    if (s.hi > 0.0f) {
       last = i;
-      if (w < 0 && !past && before + s > goal) {
+      if (w < 0 && !past && ff_gt(upto, goal)) {
         w = i;
         at = before;
       }
     }
-    before += s;
+    before = upto;
   }
   const bool beyond = w < 0;
   if (beyond) w = last;
   if (w != warp) return;
-  const int token = region_draw<DT, VEC>(x, begin, end, beyond ? INFINITY : goal - at, lane, a, sh.tab);
+  const ff rest = beyond ? ff{INFINITY, 0.0f} : ff_sub(goal, at);
+  const int token = region_draw<DT, VEC>(x, begin, end, rest, lane, a, sh.tab);
   if (lane == 0) out[count] = token;
 }
 
