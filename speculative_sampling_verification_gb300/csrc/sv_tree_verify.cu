@@ -23,6 +23,13 @@
 // figures to every other, so that each CTA comes to the same decision by itself.
 // The draw needs no pass of its own: the sums of the pass that made the
 // residual lead to one warp's region, which that warp scans.
+//
+// Precision: an acceptance test goes wrong with the probability of its ratio's
+// error, so the rows' sums for the tests are taken in fp32 with hardware exponentials
+// (about 1e-7). A draw goes wrong when u falls between the two places of any of V
+// borders, so what a draw uses (the residual's two sums and its own weights, or
+// the last row's weights) is computed in float-floats with exponentials of 1e-12, in
+// a pass that is made only when a node has a rejection or a draw.
 #include <cfloat>
 #include <cmath>
 #include <cstdint>
@@ -53,6 +60,7 @@ struct Args {
   unsigned* status;
   int B, T, V, R, region;  // region: elements of a warp, a multiple of 8
   float ih, il;            // 1/T as a float-float
+  float c2;                // log2(e)/T
   int unit_t;
 };
 
@@ -65,6 +73,7 @@ struct Shared {
   float2 tab[256];
   Exchange x[2];
   ff wsum[2][2][kWarps];      // [buffer][q or p][warp]: sums of the warps' regions
+  float wfast[2][kWarps];     // the tests' sums
   float wtop[2][kWarps];
   ff cta_sum[2][kMaxCluster];  // [buffer]: the CTAs' sums of the current residual
   double ratio[kTreeMax];  // q(x)/p(x) of the children's tokens
@@ -121,11 +130,6 @@ SV_DEVINL void load8(const void* row, int e, int end, float2 (&v)[4]) {
 SV_DEVINL ff2 weight2(float2 l, float nm, const Args& a, const float2* tab) {
   const ff2 x = scaled_diff2(l, f2(nm), a.ih, a.il, a.unit_t != 0);
   return exp_ff2(x.hi, x.lo, tab);
-}
-
-SV_DEVINL ff weight_ff(float l, float m, const Args& a, const float2* tab) {
-  const ff x = scaled_diff(l, m, a.ih, a.il, a.unit_t != 0);
-  return exp_ff(x.hi, x.lo, tab);
 }
 
 // A pass's weights: w(x) = e_q max(0, a - b e^d) with e_q = exp((lq - mq)/T) and
@@ -196,11 +200,10 @@ SV_DEVINL ff ff2_warp_sum(const ff2& s) {
   return ff_warp_sum(ff_add({s.hi.x, s.lo.x}, {s.hi.y, s.lo.y}));
 }
 
-// Maximum and sum of exp((l - max)/T) over a warp's region of one row. NaN and
-// +inf end in a NaN sum; a region of -inf has the maximum -inf and the sum 0.
+// Maximum and sum of exp((l - max)/T), in fp32, over a warp's region of one row. NaN
+// and +inf end in a NaN sum; a region of -inf has the maximum -inf and the sum 0.
 template <int DT, bool VEC>
-SV_DEVINL void region_stats(const void* row, int begin, int end, int lane, const Args& a,
-                            const float2* tab, float* top, ff* sum) {
+SV_DEVINL void region_stats(const void* row, int begin, int end, int lane, const Args& a, float* top, float* sum) {
   float m = neg_inf();
 #pragma unroll 4
   for (int e = begin + lane * 8; e < end; e += kStep) {
@@ -211,9 +214,30 @@ SV_DEVINL void region_stats(const void* row, int begin, int end, int lane, const
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const float nm = m == neg_inf() ? 0.0f : -m;
-  ff2 acc = {f2(1.0f), f2(0.0f)};
+  const float2 nm = f2(m == neg_inf() ? 0.0f : -m), c = f2(a.c2);
+  float2 acc[2] = {f2(0.0f), f2(0.0f)};
 #pragma unroll 2
+  for (int e = begin + lane * 8; e < end; e += kStep) {
+    float2 v[4];
+    load8<DT, VEC>(row, e, end, v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 y = f2_mul(f2_add(v[i], nm), c);
+      acc[i & 1] = f2_add(acc[i & 1], make_float2(ex2_fast(y.x), ex2_fast(y.y)));
+    }
+  }
+  float t = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+  *top = m;
+  *sum = t;
+}
+
+// The same sum as a float-float, with the row's maximum -nm as the reference.
+template <int DT, bool VEC>
+SV_DEVINL ff region_sum(const void* row, float nm, int begin, int end, int lane, const Args& a, const float2* tab) {
+  ff2 acc = {f2(1.0f), f2(0.0f)};
+#pragma unroll 1
   for (int e = begin + lane * 8; e < end; e += kStep) {
     float2 v[4];
     load8<DT, VEC>(row, e, end, v);
@@ -221,14 +245,14 @@ SV_DEVINL void region_stats(const void* row, int begin, int end, int lane, const
     for (int i = 0; i < 4; ++i) ff_accumulate_biased2(acc, weight2(v[i], nm, a, tab));
   }
   acc.hi = f2_add(acc.hi, f2(-1.0f));
-  *top = m;
-  *sum = ff2_warp_sum(acc);
+  return ff2_warp_sum(acc);
 }
 
 // Sum of the residual's weights over a warp's region.
 template <int DT, bool VEC>
 SV_DEVINL ff region_mix(const Mix& x, int begin, int end, int lane, const Args& a, const float2* tab) {
   ff2 acc = {f2(0.0f), f2(0.0f)};
+#pragma unroll 1
   for (int e = begin + lane * 8; e < end; e += kStep) {
     ff2 w[4];
     mix8<DT, VEC>(x, e, end, a, tab, w);
@@ -309,7 +333,7 @@ SV_DEVINL int region_draw(const Mix& x, int begin, int end, ff target, int lane,
 }
 
 template <int DT, bool VEC>
-__global__ void __launch_bounds__(kThreads) tree_verify_kernel(Args a, int nc) {
+__global__ void __launch_bounds__(kThreads, 4) tree_verify_kernel(Args a, int nc) {
   __shared__ Shared sh;
   constexpr int kEs = DT == SV_BF16 ? 2 : 4;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -369,59 +393,45 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(Args a, int nc) {
     buf = 0;
 #pragma unroll 1
     for (int r = 0; r < (kids ? 2 : 1); ++r) {
-      float top;
-      ff sum;
-      region_stats<DT, VEC>(r ? p : q, begin, end, lane, a, sh.tab, &top, &sum);
+      float top, sum;
+      region_stats<DT, VEC>(r ? p : q, begin, end, lane, a, &top, &sum);
       if (lane == 0) {
         sh.wtop[r][warp] = top;
-        sh.wsum[0][r][warp] = sum;
+        sh.wfast[r][warp] = sum;
       }
     }
     __syncthreads();
     Exchange& ex = sh.x[phase & 1];
     ++phase;
-    if (warp < (kids ? 2 : 1)) {  // warp 0 joins q's regions, warp 1 p's
-      const int r = warp;
-      const float t = lane < kWarps ? sh.wtop[r][lane] : neg_inf();
-      float m = t;
+    // Warp 0 joins q's regions, warp 1 p's. (A region's sum may be NaN although
+    // its maximum is -inf: it counts.)
+    auto joined = [&](float t, float own, float* m) {
+      float top = t;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      // A region's sum may be NaN although its maximum is -inf: it counts.
-      ff s = {0.0f, 0.0f};
-      if (lane < kWarps) {
-        s = sh.wsum[0][r][lane];
-        if (s.hi != 0.0f && t != neg_inf()) s = ff_mul(s, weight_ff(t, m, a, sh.tab));
-        sh.wsum[0][r][lane] = s;  // now relative to the CTA's maximum
-      }
-      s = ff_warp_sum(s);
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      *m = top;
+      float sum = own == 0.0f ? 0.0f : t == neg_inf() ? own : own * ex2_fast((t - top) * a.c2);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      return sum;
+    };
+    if (warp < (kids ? 2 : 1)) {
+      const int r = warp;
+      float m;
+      const float sum = joined(lane < kWarps ? sh.wtop[r][lane] : neg_inf(), lane < kWarps ? sh.wfast[r][lane] : 0.0f, &m);
       if (lane < nc) {
-        const unsigned dst = dsmem_map(smem_u32(&ex.sum[r][rank]), lane);
-        dsmem_st_f32x2(dst, s.hi, s.lo);
+        dsmem_st_f32x2(dsmem_map(smem_u32(&ex.sum[r][rank]), lane), sum, 0.0f);
         dsmem_st_f32(dsmem_map(smem_u32(&ex.top[r][rank]), lane), m);
       }
     }
     cluster_sync();
     if (warp < (kids ? 2 : 1)) {
       const int r = warp;
-      const float t = lane < nc ? ex.top[r][lane] : neg_inf();
-      float m = t;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      ff s = {0.0f, 0.0f}, w = {1.0f, 0.0f};
-      if (t != neg_inf()) w = weight_ff(t, m, a, sh.tab);
-      if (lane < nc) {
-        s = ex.sum[r][lane];
-        if (s.hi != 0.0f) s = ff_mul(s, w);
-        if (r == 0) sh.cta_sum[0][lane] = s;
-      }
-      // The regions' sums, relative to the row's maximum.
-      const ff cw = {__shfl_sync(0xffffffffu, w.hi, rank), __shfl_sync(0xffffffffu, w.lo, rank)};
-      if (r == 0 && lane < kWarps && sh.wsum[0][0][lane].hi != 0.0f)
-        sh.wsum[0][0][lane] = ff_mul(sh.wsum[0][0][lane], cw);
-      s = ff_warp_sum(s);
+      float m;
+      const float sum = joined(lane < nc ? ex.top[r][lane] : neg_inf(), lane < nc ? ex.sum[r][lane].hi : 0.0f, &m);
       if (lane == 0) {
         sh.m[r] = m;
-        sh.S[r] = ff_to_double(s);
+        sh.S[r] = (double)sum;
       }
     }
     __syncthreads();
@@ -431,9 +441,10 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(Args a, int nc) {
     x.nmq = -sh.m[0];
     x.plain = true;
     if (kids) x.c = two_sum(sh.m[0], -sh.m[1]);
+    const float nmp = kids ? -sh.m[1] : 0.0f;
 
     // ---- the children in turn, by warp 0 of each CTA alike; the others serve its passes
-    double A = 1.0, Bp = 0.0, scale = 1.0, q_over_p = 1.0, Sq = 1.0;
+    double A = 1.0, Bp = 0.0, scale = 1.0, p_over_q = 1.0, Sq = 1.0;
     int i = cur + 1;
     if (warp == 0) {
       unsigned f = 0;
@@ -443,43 +454,67 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(Args a, int nc) {
       }
       if (lane == 0) sh.failure = f;
       if (kids && !f) {
-        Sq = sh.S[0];
-        q_over_p = Sq / sh.S[1];
-        const double p_over_q = sh.S[1] / Sq;
+        p_over_q = sh.S[1] / sh.S[0];
         for (int k = cur + 1 + lane; k < T; k += 32)
           if (sh.parents[k] == cur)
-            sh.ratio[k] = token_ratio(load_one<DT>(q, sh.tokens[k]), load_one<DT>(p, sh.tokens[k]), x.c, a, sh.tab) *
-                          p_over_q;
+            sh.ratio[k] = token_ratio(load_one<DT>(q, sh.tokens[k]), load_one<DT>(p, sh.tokens[k]), x.c, a, sh.tab);
       }
       __syncwarp();
     }
     int next;
+    bool precise = false;  // the sums in float-floats are at hand
     for (;;) {
       if (warp == 0) {
         int to = kDraw;
         for (; i < T; ++i) {
           if (sh.parents[i] != cur) continue;
           // r(x)/p(x) = A q/p - B
-          to = (double)sh.u[i] < fmin(1.0, A * sh.ratio[i] - Bp) ? i : kResidual;
+          to = (double)sh.u[i] < fmin(1.0, A * (sh.ratio[i] * p_over_q) - Bp) ? i : kResidual;
           ++i;
           break;
-        }
-        if (to == kResidual && sh.failure == 0) {
-          // Scaled by a power of two so that the larger scalar lies in [1, 2).
-          const int ex2 = ilogb(fmax(A, Bp + 1.0));
-          scale = ldexp(1.0, -ex2);
-          const double fa = A * scale, fb = (Bp + 1.0) * scale * q_over_p;
-          if (lane == 0) {
-            sh.a = {(float)fa, (float)(fa - (double)(float)fa)};
-            sh.b = {(float)fb, (float)(fb - (double)(float)fb)};
-          }
         }
         if (lane == 0) sh.next = to;
       }
       __syncthreads();
       next = sh.next;
       failure = sh.failure;
-      if (failure || next != kResidual) break;
+      if (failure || next >= 0) break;
+      if (!precise) {
+        precise = true;
+        const int rows = next == kResidual ? 2 : 1;
+#pragma unroll 1
+        for (int r = 0; r < rows; ++r) {
+          const ff sum = region_sum<DT, VEC>(r ? p : q, r ? nmp : x.nmq, begin, end, lane, a, sh.tab);
+          if (lane == 0) sh.wsum[0][r][warp] = sum;
+        }
+        __syncthreads();
+        Exchange& ep = sh.x[phase & 1];
+        ++phase;
+        if (warp < rows) {
+          const ff c = ff_warp_sum(lane < kWarps ? sh.wsum[0][warp][lane] : ff{0.0f, 0.0f});
+          if (lane < nc) dsmem_st_f32x2(dsmem_map(smem_u32(&ep.sum[warp][rank]), lane), c.hi, c.lo);
+        }
+        cluster_sync();
+        if (warp == 0) {
+          const ff c = lane < nc ? ep.sum[0][lane] : ff{0.0f, 0.0f};
+          if (lane < nc) sh.cta_sum[0][lane] = c;
+          Sq = ff_to_double(ff_warp_sum(c));
+          if (rows == 2) p_over_q = ff_to_double(ff_warp_sum(lane < nc ? ep.sum[1][lane] : ff{0.0f, 0.0f})) / Sq;
+        }
+        __syncthreads();
+      }
+      if (next == kDraw) break;
+      if (warp == 0) {
+        // Scaled by a power of two so that the larger scalar lies in [1, 2).
+        const int ex2 = ilogb(fmax(A, Bp + 1.0));
+        scale = ldexp(1.0, -ex2);
+        const double fa = A * scale, fb = (Bp + 1.0) * scale / p_over_q;
+        if (lane == 0) {
+          sh.a = {(float)fa, (float)(fa - (double)(float)fa)};
+          sh.b = {(float)fb, (float)(fb - (double)(float)fb)};
+        }
+      }
+      __syncthreads();
       Mix y = x;
       y.plain = false;
       y.a = sh.a;
@@ -669,6 +704,7 @@ int spec_verify_tree(const void* target_logits, const void* draft_logits, const 
   a.ih = (float)inv;
   a.il = (float)(inv - (double)a.ih);
   a.unit_t = temperature == 1.0f;
+  a.c2 = (float)(1.4426950408889634074 * inv);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (cudaMemsetAsync(workspace, 0, 4, st) != cudaSuccess) return SV_ERR_CUDA;
   const bool vec = !misaligned(target_logits, 16) && !misaligned(draft_logits, 16) && (size_t)V * es % 16 == 0;
