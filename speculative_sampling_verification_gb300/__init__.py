@@ -562,7 +562,7 @@ class PagedCache:
     Holds the tensors it is given; checks them once."""
 
     __slots__ = ("k", "v", "k_scale", "v_scale", "num_pages", "heads", "page_size", "head_dim", "code",
-                 "device")
+                 "device", "addresses")
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
         if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype:
@@ -588,6 +588,7 @@ class PagedCache:
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.num_pages, self.heads, self.page_size, self.head_dim = k.shape
         self.device = k.device
+        self.addresses = (k.data_ptr(), v.data_ptr(), _address(k_scale), _address(v_scale))
 
 
 def new_cache(num_pages, heads, page_size, head_dim, dtype=torch.bfloat16, device="cuda") -> PagedCache:
@@ -605,25 +606,29 @@ def _address(t):
 
 
 def _raw_stream(device, stream):
-    return (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index)  # 2 us less than through a Stream object
 
 
-def _rows(name, t, shape, dtype=None):
-    """Checks a [N, H, D] operand on the GPU whose rows are consecutive."""
+def _rows(name, t, shape, dtype):
+    """Checks an operand on the GPU whose rows are consecutive."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if dtype is not None and t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape[-1] > 1 and t.stride(-1) != 1:
+    strides = t.stride()
+    if strides[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name}'s last axis must be contiguous")
+    return strides
 
 
 def _vector(name, t, shape, dtype):
     if not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA tensor")
-    if tuple(t.shape) != shape or t.dtype != dtype:
+    if t.shape != shape or t.dtype is not dtype:
         raise ValueError(f"{name} must be {list(shape)} {dtype}")
 
 
@@ -635,24 +640,21 @@ def sv_qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions, eps, interlea
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q must be [N, Hq, D] and k [N, Hkv, D]")
     N, Hq, D = q.shape
-    Hkv = k.shape[1]
-    _rows("q", q, (N, Hq, D))
-    _rows("k", k, (N, Hkv, D), q.dtype)
-    _rows("q_out", q_out, (N, Hq, D), q.dtype)
-    _rows("k_out", k_out, (N, Hkv, D), q.dtype)
+    Hkv, dtype, code = k.shape[1], q.dtype, _dtype_code(q)
+    qs, qos = _rows("q", q, (N, Hq, D), dtype), _rows("q_out", q_out, (N, Hq, D), dtype)
+    ks, kos = _rows("k", k, (N, Hkv, D), dtype), _rows("k_out", k_out, (N, Hkv, D), dtype)
     for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
         if w is not None:
-            _vector(name, w, (D,), q.dtype)
+            _vector(name, w, (D,), dtype)
     if inv_freq.dim() != 1:
         raise ValueError("inv_freq must be [R/2]")
-    _vector("inv_freq", inv_freq, tuple(inv_freq.shape), torch.float32)
+    half = inv_freq.shape[0]
+    _vector("inv_freq", inv_freq, (half,), torch.float32)
     _vector("positions", positions, (N,), torch.int32)
     return load_library().sv_qk_norm_rope(
-        q.data_ptr(), q.stride(0), q.stride(1), k.data_ptr(), k.stride(0), k.stride(1), _address(q_weight),
-        _address(k_weight), inv_freq.data_ptr(), positions.data_ptr(), N, Hq, Hkv, D,
-        2 * inv_freq.shape[0], _dtype_code(q), eps, 1 if interleaved else 0, q_out.data_ptr(),
-        q_out.stride(0), q_out.stride(1), k_out.data_ptr(), k_out.stride(0), k_out.stride(1),
-        _raw_stream(q.device, stream))
+        q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1], _address(q_weight), _address(k_weight),
+        inv_freq.data_ptr(), positions.data_ptr(), N, Hq, Hkv, D, 2 * half, code, eps, 1 if interleaved else 0,
+        q_out.data_ptr(), qos[0], qos[1], k_out.data_ptr(), kos[0], kos[1], _raw_stream(q.device, stream))
 
 
 def qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions, *, eps=1e-6, interleaved=False, q_out=None,
@@ -678,14 +680,13 @@ def sv_cache_write(k, v, slots, cache, status=None, stream=None) -> int:
     returns the host status code."""
     N = slots.shape[0]
     shape = (N, cache.heads, cache.head_dim)
-    _rows("k", k, shape)
-    _rows("v", v, shape, k.dtype)
+    code = _dtype_code(k)
+    ks, vs = _rows("k", k, shape, k.dtype), _rows("v", v, shape, k.dtype)
     _vector("slots", slots, (N,), torch.int64)
     return load_library().sv_cache_write(
-        k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0), v.stride(1), slots.data_ptr(), N,
-        cache.heads, cache.head_dim, _dtype_code(k), cache.k.data_ptr(), cache.v.data_ptr(),
-        _address(cache.k_scale), _address(cache.v_scale), cache.num_pages, cache.page_size, cache.code,
-        _address(status), _raw_stream(k.device, stream))
+        k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], slots.data_ptr(), N, cache.heads, cache.head_dim,
+        code, *cache.addresses, cache.num_pages, cache.page_size, cache.code, _address(status),
+        _raw_stream(k.device, stream))
 
 
 def cache_write(k, v, slots, cache, *, status=None, stream=None):
@@ -702,14 +703,13 @@ def sv_cache_read(cache, slots, k_out, v_out, status=None, stream=None) -> int:
     f32 (any token and head strides); returns the host status code."""
     N = slots.shape[0]
     shape = (N, cache.heads, cache.head_dim)
-    _rows("k_out", k_out, shape)
-    _rows("v_out", v_out, shape, k_out.dtype)
+    code = _dtype_code(k_out)
+    ks, vs = _rows("k_out", k_out, shape, k_out.dtype), _rows("v_out", v_out, shape, k_out.dtype)
     _vector("slots", slots, (N,), torch.int64)
     return load_library().sv_cache_read(
-        cache.k.data_ptr(), cache.v.data_ptr(), _address(cache.k_scale), _address(cache.v_scale),
-        cache.num_pages, cache.page_size, cache.code, slots.data_ptr(), N, cache.heads, cache.head_dim,
-        _dtype_code(k_out), k_out.data_ptr(), k_out.stride(0), k_out.stride(1), v_out.data_ptr(),
-        v_out.stride(0), v_out.stride(1), _address(status), _raw_stream(k_out.device, stream))
+        *cache.addresses, cache.num_pages, cache.page_size, cache.code, slots.data_ptr(), N, cache.heads,
+        cache.head_dim, code, k_out.data_ptr(), ks[0], ks[1], v_out.data_ptr(), vs[0], vs[1], _address(status),
+        _raw_stream(k_out.device, stream))
 
 
 def cache_read(cache, slots, *, dtype=torch.bfloat16, k_out=None, v_out=None, status=None, stream=None):
@@ -739,19 +739,19 @@ def sv_tree_attention(q, cache, page_table, ctx_lens, parents, scale, out, works
     if q.dim() != 4:
         raise ValueError("q must be [B, T, Hq, D]")
     B, T, Hq, D = q.shape
-    _rows("q", q, (B, T, Hq, cache.head_dim), torch.bfloat16)
+    qs = _rows("q", q, (B, T, Hq, cache.head_dim), torch.bfloat16)
     if page_table.dim() != 2:
         raise ValueError("page_table must be [B, max_pages]")
-    _vector("page_table", page_table, (B, page_table.shape[1]), torch.int32)
+    width = page_table.shape[1]
+    _vector("page_table", page_table, (B, width), torch.int32)
     _vector("ctx_lens", ctx_lens, (B,), torch.int32)
     if parents is not None:
         _vector("parents", parents, (B, T), torch.int32)
     _vector("out", out, (B, T, Hq, D), torch.bfloat16)
     return load_library().sv_tree_attention(
-        q.data_ptr(), q.stride(0), q.stride(1), q.stride(2), cache.k.data_ptr(), cache.v.data_ptr(),
-        _address(cache.k_scale), _address(cache.v_scale), cache.num_pages, cache.page_size, cache.code,
-        page_table.data_ptr(), ctx_lens.data_ptr(), _address(parents), B, T, Hq, cache.heads, D,
-        page_table.shape[1], scale, out.data_ptr(), workspace.data_ptr(),
+        q.data_ptr(), qs[0], qs[1], qs[2], *cache.addresses, cache.num_pages, cache.page_size, cache.code,
+        page_table.data_ptr(), ctx_lens.data_ptr(), _address(parents), B, T, Hq, cache.heads, D, width, scale,
+        out.data_ptr(), workspace.data_ptr(),
         workspace.numel() * workspace.element_size(), _raw_stream(q.device, stream))
 
 

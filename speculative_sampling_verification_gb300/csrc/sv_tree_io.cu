@@ -20,7 +20,8 @@
 namespace sv {
 namespace tio {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
+constexpr int kSms = 152;
 
 // ---------------------------------------------------------------- element access
 
@@ -108,22 +109,42 @@ SV_DEVINL float2 turn_cos_sin(int position, unsigned long long F) {
   return make_float2(c, s);
 }
 
-// A thread group of L lanes takes `hpg` heads of one token. Its lanes hold 2 VEC
-// elements of a row each, as two 16-byte vectors: with halves, vector s and
-// its partner R/2 further (the pair that rotates together, so nothing crosses
-// lanes); interleaved, or past R, two vectors that each stand alone. The angles
-// are computed once and serve the group's heads.
+// 16 bytes as loaded (eight bf16 or four fp32 values).
+template <int DT, int VEC>
+SV_DEVINL void unpack(const uint4& w, float (&v)[VEC]) {
+  const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (DT == SV_BF16) {
+      v[2 * i] = bf16_lo(x[i]);
+      v[2 * i + 1] = bf16_hi(x[i]);
+    } else {
+      v[i] = __uint_as_float(x[i]);
+    }
+  }
+}
+template <int DT>
+SV_DEVINL uint4 raw_vec(const void* base, long long at) {
+  return *reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(base) + at * (DT == SV_BF16 ? 2 : 4));
+}
+
+// A thread group of L lanes takes `hpg` heads of one token, one after another with the
+// next one's loads under way. Its lanes hold 2 VEC elements of a row each, as two
+// 16-byte vectors: with halves, vector s and its partner R/2 further (the pair that
+// rotates together, so nothing crosses lanes); interleaved, or past R, two vectors that
+// each stand alone. The angles are computed once and serve the group's heads: with one
+// head a group their cosines and sines bound the kernel (137 us for 16383 tokens of
+// 40 heads of 128 in bf16); so it takes 67 us, 5.0 TB/s. Blocks of 128 threads: 77 us
+// with 256, whose last blocks are fewer and longer.
 template <int DT, int L, bool INTER>
 __global__ void __launch_bounds__(kThreads) norm_rope_kernel(NormRopeArgs a) {
   constexpr int VEC = DT == SV_BF16 ? 8 : 4;
-  constexpr int kAng = VEC;  // angles a lane needs (both layouts: VEC pairs in 2 VEC elements)
   extern __shared__ unsigned long long frac[];  // [R/2]
   for (int i = threadIdx.x; i < a.R / 2; i += kThreads) frac[i] = turn_fraction(a.inv_freq[i]);
   __syncthreads();
   const int lane = threadIdx.x % L;
   const int slots = a.D / (2 * VEC);       // lanes with work
   const int rot = a.R / (2 * VEC);         // of which the first `rot` rotate
-  const bool in = lane < slots;
   // Element offsets of the lane's two vectors.
   int e0, e1;
   if (INTER || lane >= rot) {
@@ -135,51 +156,53 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(NormRopeArgs a) {
   }
   const bool turns = lane < rot;
   const float inv_d = 1.0f / (float)a.D;
-  const long long total = (long long)a.N * a.groups;
-  const long long stride = (long long)gridDim.x * (kThreads / L);
+  const long long g = (long long)blockIdx.x * (kThreads / L) + threadIdx.x / L;
+  const bool live = lane < slots && g < (long long)a.N * a.groups;
   const int H = a.Hq + a.Hkv;
-  // All lanes of a warp stay in the loop (the sums are exchanged warp-wide).
-  const long long rounds = (total + stride - 1) / stride;
-  long long g = (long long)blockIdx.x * (kThreads / L) + threadIdx.x / L;
-  for (long long it = 0; it < rounds; ++it, g += stride) {
-    const bool live = in && g < total;
-    const int n = live ? (int)(g / a.groups) : 0;
-    const int h0 = live ? (int)(g % a.groups) * a.hpg : 0;
-    float cs[kAng], sn[kAng];
-    if (turns && live) {
-      const int pos = a.positions[n];
+  const int n = live ? (int)(g / a.groups) : 0;
+  const int h0 = live ? (int)(g % a.groups) * a.hpg : 0;
+  const int h1 = live ? min(H, h0 + a.hpg) : 0;
+  float cs[VEC], sn[VEC];
+  if (turns && live) {
+    const int pos = a.positions[n];
 #pragma unroll
-      for (int i = 0; i < kAng; ++i) {
-        const float2 c = turn_cos_sin(pos, frac[lane * VEC + i]);
-        cs[i] = c.x;
-        sn[i] = c.y;
-      }
+    for (int i = 0; i < VEC; ++i) {
+      const float2 c = turn_cos_sin(pos, frac[lane * VEC + i]);
+      cs[i] = c.x;
+      sn[i] = c.y;
     }
-    for (int j = 0; j < a.hpg; ++j) {
-      const int h = h0 + j;
-      const bool on = live && h < H;
-      const bool isq = h < a.Hq;
-      float x0[VEC], x1[VEC];
+  }
+  // All lanes of a warp stay in the loop (the sums are exchanged warp-wide).
+  uint4 raw[2], ahead[2];
+  auto fetch = [&](int h, uint4 (&to)[2]) {
+    to[0] = to[1] = make_uint4(0, 0, 0, 0);
+    if (h >= h1) return;
+    const bool isq = h < a.Hq;
+    const void* src = isq ? a.q : a.k;
+    const long long at = isq ? n * a.q_sn + h * a.q_sh : n * a.k_sn + (h - a.Hq) * a.k_sh;
+    to[0] = raw_vec<DT>(src, at + e0);
+    to[1] = raw_vec<DT>(src, at + e1);
+  };
+  fetch(h0, raw);
+#pragma unroll 1
+  for (int i = 0; i < a.hpg; ++i) {
+    const int h = h0 + i;
+    fetch(h + 1, ahead);  // the next head's row while this one is worked on
+    const bool on = h < h1, isq = h < a.Hq;
+    float x0[VEC], x1[VEC];
+    unpack<DT, VEC>(raw[0], x0);
+    unpack<DT, VEC>(raw[1], x1);
+    float ss = 0.0f;
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) x0[i] = x1[i] = 0.0f;
-      if (on) {
-        const void* src = isq ? a.q : a.k;
-        const long long at = isq ? n * a.q_sn + h * a.q_sh : n * a.k_sn + (h - a.Hq) * a.k_sh;
-        load_vec<DT, VEC>(src, at + e0, x0);
-        load_vec<DT, VEC>(src, at + e1, x1);
-      }
-      float ss = 0.0f;
+    for (int i = 0; i < VEC; ++i) ss = fmaf(x0[i], x0[i], fmaf(x1[i], x1[i], ss));
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) ss = fmaf(x0[i], x0[i], fmaf(x1[i], x1[i], ss));
-#pragma unroll
-      for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      if (!on) continue;
-      const float r = 1.0f / sqrtf(fmaf(ss, inv_d, a.eps));
-      const void* w = isq ? a.qw : a.kw;
-      if (w) {
+    for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    if (on) {
+      const float r = rsqrtf(fmaf(ss, inv_d, a.eps));
+      if (isq ? a.qw != nullptr : a.kw != nullptr) {
         float w0[VEC], w1[VEC];
-        load_vec<DT, VEC>(w, e0, w0);
-        load_vec<DT, VEC>(w, e1, w1);
+        load_vec<DT, VEC>(isq ? a.qw : a.kw, e0, w0);
+        load_vec<DT, VEC>(isq ? a.qw : a.kw, e1, w1);
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
           x0[i] *= r * w0[i];
@@ -216,6 +239,8 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(NormRopeArgs a) {
       store_vec<DT, VEC>(dst, to + e0, x0);
       store_vec<DT, VEC>(dst, to + e1, x1);
     }
+    raw[0] = ahead[0];
+    raw[1] = ahead[1];
   }
 }
 
@@ -317,128 +342,153 @@ SV_DEVINL bool slot_ok(const CacheArgs& a, long long slot) {
   return false;
 }
 
-// L lanes take one (token, head), its key and its value together, 16 elements
-// of each a lane. A row's scale is its largest magnitude over 448, the largest
-// e4m3 value, so that no code saturates but by rounding. A row with NaN or
-// infinity gets a NaN scale and codes of zero: it reads back as NaN everywhere.
-template <int DT, int CDT, int L>
+// L lanes take HB heads of one token, key and value together, 16 elements of each row a
+// lane: one slot leads to 2 HB rows whose loads are in flight together. A row's scale
+// is its largest magnitude over 448, the largest e4m3 value, so that no code saturates
+// but by rounding. A row with NaN or infinity gets a NaN scale and codes of zero: it
+// reads back as NaN everywhere.
+template <int DT, int CDT, int L, int HB>
 __global__ void __launch_bounds__(kThreads) cache_write_kernel(CacheArgs a) {
   constexpr int VEC = DT == SV_BF16 ? 8 : 4;
   constexpr int NV = 16 / VEC;
   const int lane = threadIdx.x % L;
+  const int quads = (a.H + HB - 1) / HB;
   const long long item = (long long)blockIdx.x * (kThreads / L) + threadIdx.x / L;
-  const bool row = item < (long long)a.N * a.H;
-  const int n = row ? (int)(item / a.H) : 0, h = row ? (int)(item % a.H) : 0;
+  const bool row = item < (long long)a.N * quads;
+  const int n = row ? (int)(item / quads) : 0, h0 = row ? (int)(item % quads) * HB : 0;
   const long long slot = row ? a.slots[n] : -1;
   const bool on = row && lane * 16 < a.D && slot_ok(a, slot);
-  float x[2][16];
-  float amax[2] = {0.0f, 0.0f};
+  uint4 raw[HB][2][NV];
 #pragma unroll
-  for (int w = 0; w < 2; ++w) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      float t[VEC];
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) t[j] = 0.0f;
-      if (on)
-        load_vec<DT, VEC>(w ? a.v : a.k,
-                          (w ? n * a.v_sn + h * a.v_sh : n * a.k_sn + h * a.k_sh) + lane * 16 + i * VEC, t);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) x[w][i * VEC + j] = t[j];
-    }
-  }
-  if constexpr (CDT == SV_E4M3) {
+  for (int j = 0; j < HB; ++j) {
+    const int h = h0 + j;
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) amax[w] = max_nan(amax[w], fabsf(x[w][i]));
-#pragma unroll
-      for (int o = L / 2; o > 0; o >>= 1)
-        amax[w] = max_nan(amax[w], __shfl_xor_sync(0xffffffffu, amax[w], o));
+      for (int i = 0; i < NV; ++i) {
+        raw[j][w][i] = make_uint4(0, 0, 0, 0);
+        if (on && h < a.H)
+          raw[j][w][i] = raw_vec<DT>(w ? a.v : a.k, (w ? n * a.v_sn + h * a.v_sh : n * a.k_sn + h * a.k_sh) +
+                                                        lane * 16 + i * VEC);
+      }
     }
   }
-  if (!on) return;
-  const long long r = cache_row(a, slot, h);
+  const long long r0 = on ? cache_row(a, slot, h0) : 0;
 #pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    void* c = w ? a.vc : a.kc;
-    if constexpr (CDT == SV_E4M3) {
-      const bool bad = !(amax[w] < INFINITY);
-      const float top = fmaxf(amax[w], kAmaxMin);
-      const float inv = bad ? 0.0f : __fdiv_rn(kE4m3Max, top);
-      uint32_t o[4];
+  for (int j = 0; j < HB; ++j) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float y[4];
+    for (int w = 0; w < 2; ++w) {
+      float x[16], amax = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) y[j] = bad ? 0.0f : x[w][4 * i + j] * inv;
-        o[i] = e4m3_pair(y[0], y[1]) | (e4m3_pair(y[2], y[3]) << 16);
+      for (int i = 0; i < NV; ++i) {
+        float t[VEC];
+        unpack<DT, VEC>(raw[j][w][i], t);
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) x[i * VEC + k] = t[k];
       }
-      *reinterpret_cast<uint4*>(static_cast<unsigned char*>(c) + r * a.D + lane * 16) =
-          make_uint4(o[0], o[1], o[2], o[3]);
-      if (lane == 0)
-        (w ? a.vs : a.ks)[r] = bad ? __int_as_float(0x7fc00000) : __fdiv_rn(top, kE4m3Max);
-    } else {
+      if constexpr (CDT == SV_E4M3) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float t[8];
+        for (int i = 0; i < 16; ++i) amax = max_nan(amax, fabsf(x[i]));
 #pragma unroll
-        for (int j = 0; j < 8; ++j) t[j] = x[w][8 * i + j];
-        store_vec<SV_BF16, 8>(c, r * a.D + lane * 16 + 8 * i, t);
+        for (int o = L / 2; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      }
+      if (!on || h0 + j >= a.H) continue;
+      const long long r = r0 + (long long)j * a.P;
+      void* c = w ? a.vc : a.kc;
+      if constexpr (CDT == SV_E4M3) {
+        const bool bad = !(amax < INFINITY);
+        const float top = fmaxf(amax, kAmaxMin);
+        const float inv = bad ? 0.0f : __fdiv_rn(kE4m3Max, top);
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float y[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) y[k] = bad ? 0.0f : x[4 * i + k] * inv;
+          o[i] = e4m3_pair(y[0], y[1]) | (e4m3_pair(y[2], y[3]) << 16);
+        }
+        *reinterpret_cast<uint4*>(static_cast<unsigned char*>(c) + r * a.D + lane * 16) =
+            make_uint4(o[0], o[1], o[2], o[3]);
+        if (lane == 0) (w ? a.vs : a.ks)[r] = bad ? __int_as_float(0x7fc00000) : __fdiv_rn(top, kE4m3Max);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float t[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) t[k] = x[8 * i + k];
+          store_vec<SV_BF16, 8>(c, r * a.D + lane * 16 + 8 * i, t);
+        }
       }
     }
   }
 }
 
-template <int DT, int CDT, int L>
+template <int DT, int CDT, int L, int HB>
 __global__ void __launch_bounds__(kThreads) cache_read_kernel(CacheArgs a) {
   constexpr int VEC = DT == SV_BF16 ? 8 : 4;
-  constexpr int NV = 16 / VEC;
+  constexpr int NV = 16 / VEC, CV = CDT == SV_E4M3 ? 1 : 2;  // 16-byte vectors of a lane's elements
   const int lane = threadIdx.x % L;
+  const int quads = (a.H + HB - 1) / HB;
   const long long item = (long long)blockIdx.x * (kThreads / L) + threadIdx.x / L;
-  if (item >= (long long)a.N * a.H || lane * 16 >= a.D) return;
-  const int n = (int)(item / a.H), h = (int)(item % a.H);
+  if (item >= (long long)a.N * quads || lane * 16 >= a.D) return;
+  const int n = (int)(item / quads), h0 = (int)(item % quads) * HB;
   const long long slot = a.slots[n];
   const bool ok = slot_ok(a, slot);
-  const long long r = ok ? cache_row(a, slot, h) : 0;
-  float x[2][16];
+  const long long r0 = ok ? cache_row(a, slot, h0) : 0;
+  uint4 raw[HB][2][CV];
+  float scale[HB][2];
 #pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    const void* c = w ? a.vc : a.kc;
-    if (!ok) {
+  for (int j = 0; j < HB; ++j) {
+    const long long r = r0 + (long long)j * a.P;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) x[w][i] = 0.0f;
-    } else if constexpr (CDT == SV_E4M3) {
-      const uint4 q = *reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(c) + r * a.D + lane * 16);
-      const float s = (w ? a.vs : a.ks)[r];
-      const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+    for (int w = 0; w < 2; ++w) {
+      const bool on = ok && h0 + j < a.H;
+      scale[j][w] = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 lo = e4m3_unpack(u[i]), hi = e4m3_unpack(u[i] >> 16);
-        x[w][4 * i] = lo.x * s;
-        x[w][4 * i + 1] = lo.y * s;
-        x[w][4 * i + 2] = hi.x * s;
-        x[w][4 * i + 3] = hi.y * s;
+      for (int i = 0; i < CV; ++i) {
+        raw[j][w][i] = make_uint4(0, 0, 0, 0);
+        if (on)
+          raw[j][w][i] = *reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(w ? a.vc : a.kc) +
+                                                         (r * a.D + lane * 16) * CV + 16 * i);
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float t[8];
-        load_vec<SV_BF16, 8>(c, r * a.D + lane * 16 + 8 * i, t);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[w][8 * i + j] = t[j];
-      }
+      if (CDT == SV_E4M3 && on) scale[j][w] = (w ? a.vs : a.ks)[r];
     }
   }
 #pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    const long long to = (w ? n * a.v_sn + h * a.v_sh : n * a.k_sn + h * a.k_sh) + lane * 16;
+  for (int j = 0; j < HB; ++j) {
+    const int h = h0 + j;
+    if (h >= a.H) break;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      float t[VEC];
+    for (int w = 0; w < 2; ++w) {
+      float x[16];
+      if constexpr (CDT == SV_E4M3) {
+        const float s = scale[j][w];
+        const uint32_t u[4] = {raw[j][w][0].x, raw[j][w][0].y, raw[j][w][0].z, raw[j][w][0].w};
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) t[j] = x[w][i * VEC + j];
-      store_vec<DT, VEC>(w ? a.vo : a.ko, to + i * VEC, t);
+        for (int i = 0; i < 4; ++i) {
+          const float2 lo = e4m3_unpack(u[i]), hi = e4m3_unpack(u[i] >> 16);
+          x[4 * i] = lo.x * s;
+          x[4 * i + 1] = lo.y * s;
+          x[4 * i + 2] = hi.x * s;
+          x[4 * i + 3] = hi.y * s;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < CV; ++i) {
+          float t[8];
+          unpack<SV_BF16, 8>(raw[j][w][i], t);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) x[8 * i + k] = t[k];
+        }
+      }
+      const long long to = (w ? n * a.v_sn + h * a.v_sh : n * a.k_sn + h * a.k_sh) + lane * 16;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        float t[VEC];
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) t[k] = x[i * VEC + k];
+        store_vec<DT, VEC>(w ? a.vo : a.ko, to + i * VEC, t);
+      }
     }
   }
 }
@@ -541,8 +591,13 @@ cudaError_t norm_rope(NormRopeArgs a, bool vec, cudaStream_t st) {
   }
   const int L = lanes_for(a.D / (2 * VEC));
   const int per_block = kThreads / L;
+  // Heads a group: one where the call is small and latency counts; else as many as leave
+  // eight blocks an SM, so that the angles are shared.
   a.hpg = 1;
-  a.groups = H;
+  for (int hpg = 4; hpg <= 16; hpg *= 2)
+    if (H >= hpg && (long long)a.N * ((H + hpg - 1) / hpg) >= 8ll * kSms * per_block) a.hpg = hpg;
+  a.groups = (H + a.hpg - 1) / a.hpg;
+  a.hpg = (H + a.groups - 1) / a.groups;  // evenly
   const unsigned grid = blocks_for((long long)a.N * a.groups, per_block);
   switch (L) {
     case 1: launch_norm_rope<DT, 1>(a, grid, st); break;
@@ -555,13 +610,23 @@ cudaError_t norm_rope(NormRopeArgs a, bool vec, cudaStream_t st) {
   return cudaGetLastError();
 }
 
+template <int DT, int CDT, bool READ, int L, int HB>
+void launch_cache_hb(const CacheArgs& a, cudaStream_t st) {
+  const unsigned grid = blocks_for((long long)a.N * ((a.H + HB - 1) / HB), kThreads / L);
+  if (READ)
+    cache_read_kernel<DT, CDT, L, HB><<<grid, kThreads, 0, st>>>(a);
+  else
+    cache_write_kernel<DT, CDT, L, HB><<<grid, kThreads, 0, st>>>(a);
+}
+
+// Two heads a group (four loads of 16 bytes and more in flight a lane) where that leaves eight
+// blocks an SM; one in small calls.
 template <int DT, int CDT, bool READ, int L>
 void launch_cache_l(const CacheArgs& a, cudaStream_t st) {
-  const unsigned grid = blocks_for((long long)a.N * a.H, kThreads / L);
-  if (READ)
-    cache_read_kernel<DT, CDT, L><<<grid, kThreads, 0, st>>>(a);
+  if (a.H >= 2 && (long long)a.N * ((a.H + 1) / 2) >= 8ll * kSms * (kThreads / L))
+    launch_cache_hb<DT, CDT, READ, L, 2>(a, st);
   else
-    cache_write_kernel<DT, CDT, L><<<grid, kThreads, 0, st>>>(a);
+    launch_cache_hb<DT, CDT, READ, L, 1>(a, st);
 }
 
 template <int DT, int CDT, bool READ>
