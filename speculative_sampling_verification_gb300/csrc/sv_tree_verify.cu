@@ -62,6 +62,12 @@ struct Args {
   float ih, il;            // 1/T as a float-float
   float c2;                // log2(e)/T
   int unit_t;
+  // The short exponentials (exp_draw2): its constants, the bound of a logit that they
+  // take, and whether the temperature allows them.
+  DrawConst dc;
+  float reach;
+  double inv_t;
+  int short_ok;
 };
 
 struct Exchange {
@@ -70,7 +76,7 @@ struct Exchange {
 };
 
 struct Shared {
-  float2 tab[256];
+  float2 tab[256], tab1k[1024];
   Exchange x[2];
   ff wsum[2][2][kWarps];      // [buffer][q or p][warp]: sums of the warps' regions
   float wfast[2][kWarps];     // the tests' sums
@@ -91,6 +97,14 @@ struct Shared {
 };
 
 constexpr int kDraw = -1, kResidual = -2;
+
+constexpr double kLn2 = 0.69314718055994530942;
+
+// exp(v) for |v| of a few, to about 1e-12.
+SV_DEVINL double power(double v, const float2* tab) {
+  const float hi = (float)v;
+  return ff_to_double(exp_ff(hi, (float)(v - (double)hi), tab));
+}
 
 template <int DT>
 SV_DEVINL float load_one(const void* row, long long i) {
@@ -144,10 +158,55 @@ struct Mix {
   ff c;          // mq - mp
   ff a, b;
   bool plain;
+  // With `shorter` (row maxima and their difference within 1500 T) the weights come from
+  // exp_draw2 on the logits as they are, to 5e-11: q's relative to 2^q0 (qb is 127 - q0), the
+  // ratio's times 2^n (rb is 127 + n, and b takes the rest of exp((mq - mp)/T)); top is the
+  // largest difference whose ratio stays in range.
+  bool shorter;
+  int qb, rb;
+  float top;
 };
 
 // Ratios above e^80 count as e^80: their weight is 0 unless b < a e^-80.
 constexpr float kRatioTop = 80.0f;
+
+// e_q of a pair of logits of q (or of p, with its own qb).
+SV_DEVINL ff2 short2(float2 l, int qb, const Args& a, const float2* tab1k) {
+  l = make_float2(fmaxf(l.x, -a.reach), fmaxf(l.y, -a.reach));
+  return exp_draw2(l, make_int2(qb, qb), a.dc, tab1k);
+}
+
+SV_DEVINL ff2 plain2(float2 l, const Mix& x, const Args& a, const float2* tab, const float2* tab1k) {
+  return x.shorter ? short2(l, x.qb, a, tab1k) : weight2(l, x.nmq, a, tab);
+}
+
+// a - b r, then times e; 0 where that is not positive.
+SV_DEVINL ff2 mixed(const ff2& e, const ff2& r, const Mix& x) {
+  const float2 ph = f2_mul(r.hi, f2(-x.b.hi));
+  const float2 pe = f2_fma(r.hi, f2(-x.b.hi), f2_mul(ph, f2(-1.0f)));
+  const float2 pl = f2_sub(pe, f2_fma(r.hi, f2(x.b.lo), f2_mul(r.lo, f2(x.b.hi))));
+  const ff2 t0 = two_sum2(f2(x.a.hi), ph);
+  // (Normalised: where the heads cancel, the tails are all there is.)
+  const ff2 t = two_sum2(t0.hi, f2_add(t0.lo, f2_add(f2(x.a.lo), pl)));
+  const float2 wh = f2_mul(e.hi, t.hi);
+  const float2 we = f2_fma(e.hi, t.hi, f2_mul(wh, f2(-1.0f)));
+  const float2 wl = f2_add(we, f2_fma(e.hi, t.lo, f2_mul(e.lo, t.hi)));
+  const bool kx = e.hi.x > 0.0f && t.hi.x > 0.0f, ky = e.hi.y > 0.0f && t.hi.y > 0.0f;
+  return {make_float2(kx ? wh.x : 0.0f, ky ? wh.y : 0.0f),
+          make_float2(kx ? wl.x : 0.0f, ky ? wl.y : 0.0f)};
+}
+
+SV_DEVINL ff2 mix2_short(float2 lq, float2 lp, const Mix& x, const Args& a, const float2* tab1k) {
+  const ff2 e = short2(lq, x.qb, a, tab1k);
+  ff2 d = two_sum2(lp, f2_mul(lq, f2(-1.0f)));
+  if (!(d.hi.x < x.top)) d.hi.x = x.top, d.lo.x = 0.0f;  // (also where the target has no such token)
+  if (!(d.hi.y < x.top)) d.hi.y = x.top, d.lo.y = 0.0f;
+  if (d.hi.x < -a.reach) d.hi.x = -a.reach, d.lo.x = 0.0f;
+  if (d.hi.y < -a.reach) d.hi.y = -a.reach, d.lo.y = 0.0f;
+  ff2 r = exp_draw2(d.hi, make_int2(x.rb, x.rb), a.dc, tab1k);
+  r.lo = f2_fma(r.hi, f2_mul(d.lo, f2(a.ih)), r.lo);
+  return mixed(e, r, x);
+}
 
 SV_DEVINL ff2 mix2(float2 lq, float2 lp, const Mix& x, const Args& a, const float2* tab) {
   const ff2 e = weight2(lq, x.nmq, a, tab);
@@ -163,35 +222,23 @@ SV_DEVINL ff2 mix2(float2 lq, float2 lp, const Mix& x, const Args& a, const floa
   if (d.hi.x > kRatioTop) d.hi.x = kRatioTop, d.lo.x = 0.0f;
   if (d.hi.y > kRatioTop) d.hi.y = kRatioTop, d.lo.y = 0.0f;
   const ff2 r = exp_ff2(d.hi, d.lo, tab);
-  // t = a - b r
-  const float2 ph = f2_mul(r.hi, f2(-x.b.hi));
-  const float2 pe = f2_fma(r.hi, f2(-x.b.hi), f2_mul(ph, f2(-1.0f)));
-  const float2 pl = f2_sub(pe, f2_fma(r.hi, f2(x.b.lo), f2_mul(r.lo, f2(x.b.hi))));
-  const ff2 t0 = two_sum2(f2(x.a.hi), ph);
-  // (Normalised: where the heads cancel, the tails are all there is.)
-  const ff2 t = two_sum2(t0.hi, f2_add(t0.lo, f2_add(f2(x.a.lo), pl)));
-  // w = e t, 0 where t is not positive or the target has no such token
-  const float2 wh = f2_mul(e.hi, t.hi);
-  const float2 we = f2_fma(e.hi, t.hi, f2_mul(wh, f2(-1.0f)));
-  const float2 wl = f2_add(we, f2_fma(e.hi, t.lo, f2_mul(e.lo, t.hi)));
-  const bool kx = e.hi.x > 0.0f && t.hi.x > 0.0f, ky = e.hi.y > 0.0f && t.hi.y > 0.0f;
-  return {make_float2(kx ? wh.x : 0.0f, ky ? wh.y : 0.0f),
-          make_float2(kx ? wl.x : 0.0f, ky ? wl.y : 0.0f)};
+  return mixed(e, r, x);
 }
 
 template <int DT, bool VEC>
-SV_DEVINL void mix8(const Mix& x, int e, int end, const Args& a, const float2* tab, ff2 (&w)[4]) {
+SV_DEVINL void mix8(const Mix& x, int e, int end, const Args& a, const float2* tab, const float2* tab1k,
+                    ff2 (&w)[4]) {
   float2 q[4];
   load8<DT, VEC>(x.q, e, end, q);
   if (x.plain) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = weight2(q[i], x.nmq, a, tab);
+    for (int i = 0; i < 4; ++i) w[i] = plain2(q[i], x, a, tab, tab1k);
     return;
   }
   float2 p[4];
   load8<DT, VEC>(x.p, e, end, p);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = mix2(q[i], p[i], x, a, tab);
+  for (int i = 0; i < 4; ++i) w[i] = x.shorter ? mix2_short(q[i], p[i], x, a, tab1k) : mix2(q[i], p[i], x, a, tab);
 }
 
 // fp64 runs at a 64th of the fp32 rate here: it is left to one warp's decisions, and
@@ -233,16 +280,17 @@ SV_DEVINL void region_stats(const void* row, int begin, int end, int lane, const
   *sum = t;
 }
 
-// The same sum as a float-float, with the row's maximum -nm as the reference.
+// The same sum as a float-float, of a row's weights as the draw takes them.
 template <int DT, bool VEC>
-SV_DEVINL ff region_sum(const void* row, float nm, int begin, int end, int lane, const Args& a, const float2* tab) {
+SV_DEVINL ff region_sum(const Mix& x, int begin, int end, int lane, const Args& a, const float2* tab,
+                        const float2* tab1k) {
   ff2 acc = {f2(1.0f), f2(0.0f)};
 #pragma unroll 1
   for (int e = begin + lane * 8; e < end; e += kStep) {
     float2 v[4];
-    load8<DT, VEC>(row, e, end, v);
+    load8<DT, VEC>(x.q, e, end, v);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) ff_accumulate_biased2(acc, weight2(v[i], nm, a, tab));
+    for (int i = 0; i < 4; ++i) ff_accumulate_biased2(acc, plain2(v[i], x, a, tab, tab1k));
   }
   acc.hi = f2_add(acc.hi, f2(-1.0f));
   return ff2_warp_sum(acc);
@@ -250,12 +298,13 @@ SV_DEVINL ff region_sum(const void* row, float nm, int begin, int end, int lane,
 
 // Sum of the residual's weights over a warp's region.
 template <int DT, bool VEC>
-SV_DEVINL ff region_mix(const Mix& x, int begin, int end, int lane, const Args& a, const float2* tab) {
+SV_DEVINL ff region_mix(const Mix& x, int begin, int end, int lane, const Args& a, const float2* tab,
+                        const float2* tab1k) {
   ff2 acc = {f2(0.0f), f2(0.0f)};
 #pragma unroll 1
   for (int e = begin + lane * 8; e < end; e += kStep) {
     ff2 w[4];
-    mix8<DT, VEC>(x, e, end, a, tab, w);
+    mix8<DT, VEC>(x, e, end, a, tab, tab1k, w);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const ff2 s = two_sum2(acc.hi, w[i].hi);
@@ -286,14 +335,14 @@ SV_DEVINL double token_ratio(float lq, float lp, ff c, const Args& a, const floa
 // or the region's last token of positive weight.
 template <int DT, bool VEC>
 SV_DEVINL int region_draw(const Mix& x, int begin, int end, ff target, int lane, const Args& a,
-                          const float2* tab) {
+                          const float2* tab, const float2* tab1k) {
   ff before = {0.0f, 0.0f};
   int last = -1;
 #pragma unroll 1
   for (int e0 = begin; e0 < end; e0 += kStep) {
     const int e = e0 + lane * 8;
     ff2 w[4];
-    mix8<DT, VEC>(x, e, end, a, tab, w);
+    mix8<DT, VEC>(x, e, end, a, tab, tab1k, w);
     ff mine = {0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -341,6 +390,8 @@ __global__ void __launch_bounds__(kThreads, 4) tree_verify_kernel(Args a, int nc
   const long long b = blockIdx.x / nc;
   const int T = a.T;
   sh.tab[tid] = kSvExp2Table[tid];
+#pragma unroll
+  for (int i = 0; i < 1024; i += kThreads) sh.tab1k[tid + i] = kSvExp2Table1024[tid + i];
 
   // ---- the tree, checked by every CTA alike
   unsigned bad = 0;
@@ -441,7 +492,21 @@ __global__ void __launch_bounds__(kThreads, 4) tree_verify_kernel(Args a, int nc
     x.nmq = -sh.m[0];
     x.plain = true;
     if (kids) x.c = two_sum(sh.m[0], -sh.m[1]);
-    const float nmp = kids ? -sh.m[1] : 0.0f;
+    const float mq = sh.m[0], mp = kids ? sh.m[1] : sh.m[0];
+    const float near = 0.75f * a.reach;
+    x.shorter = a.short_ok && fabsf(mq) < near && fabsf(mp) < near && fabsf(mq - mp) < near;
+    Mix xp = x;  // the draft row alone
+    xp.q = p;
+    xp.nmq = -mp;
+    int n2 = 0;
+    if (x.shorter) {
+      const int q0 = (int)floorf(mq * a.c2) + 1, p0 = (int)floorf(mp * a.c2) + 1;
+      n2 = (int)rintf((mq - mp) * a.c2);
+      x.qb = 127 - q0;
+      xp.qb = 127 - p0;
+      x.rb = 127 + n2;
+      x.top = fminf(a.reach, (float)(126 - n2) / a.c2);
+    }
 
     // ---- the children in turn, by warp 0 of each CTA alike; the others serve its passes
     double A = 1.0, Bp = 0.0, scale = 1.0, p_over_q = 1.0, Sq = 1.0;
@@ -484,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 4) tree_verify_kernel(Args a, int nc
         const int rows = next == kResidual ? 2 : 1;
 #pragma unroll 1
         for (int r = 0; r < rows; ++r) {
-          const ff sum = region_sum<DT, VEC>(r ? p : q, r ? nmp : x.nmq, begin, end, lane, a, sh.tab);
+          const ff sum = region_sum<DT, VEC>(r ? xp : x, begin, end, lane, a, sh.tab, sh.tab1k);
           if (lane == 0) sh.wsum[0][r][warp] = sum;
         }
         __syncthreads();
@@ -499,7 +564,12 @@ __global__ void __launch_bounds__(kThreads, 4) tree_verify_kernel(Args a, int nc
           const ff c = lane < nc ? ep.sum[0][lane] : ff{0.0f, 0.0f};
           if (lane < nc) sh.cta_sum[0][lane] = c;
           Sq = ff_to_double(ff_warp_sum(c));
-          if (rows == 2) p_over_q = ff_to_double(ff_warp_sum(lane < nc ? ep.sum[1][lane] : ff{0.0f, 0.0f})) / Sq;
+          if (rows == 2) {
+            p_over_q = ff_to_double(ff_warp_sum(lane < nc ? ep.sum[1][lane] : ff{0.0f, 0.0f})) / Sq;
+            // (The short weights' sums are relative to powers of two, not to the maxima.)
+            if (x.shorter)
+              p_over_q *= power((double)(x.qb - xp.qb) * kLn2 + ((double)mq - (double)mp) * a.inv_t, sh.tab);
+          }
         }
         __syncthreads();
       }
@@ -508,7 +578,9 @@ __global__ void __launch_bounds__(kThreads, 4) tree_verify_kernel(Args a, int nc
         // Scaled by a power of two so that the larger scalar lies in [1, 2).
         const int ex2 = ilogb(fmax(A, Bp + 1.0));
         scale = ldexp(1.0, -ex2);
-        const double fa = A * scale, fb = (Bp + 1.0) * scale / p_over_q;
+        const double fa = A * scale;
+        double fb = (Bp + 1.0) * scale / p_over_q;
+        if (x.shorter) fb *= power(((double)mq - (double)mp) * a.inv_t - (double)n2 * kLn2, sh.tab);
         if (lane == 0) {
           sh.a = {(float)fa, (float)(fa - (double)(float)fa)};
           sh.b = {(float)fb, (float)(fb - (double)(float)fb)};
@@ -520,7 +592,7 @@ __global__ void __launch_bounds__(kThreads, 4) tree_verify_kernel(Args a, int nc
       y.a = sh.a;
       y.b = sh.b;
       const int nb = buf ^ 1;
-      const ff sum = region_mix<DT, VEC>(y, begin, end, lane, a, sh.tab);
+      const ff sum = region_mix<DT, VEC>(y, begin, end, lane, a, sh.tab, sh.tab1k);
       if (lane == 0) sh.wsum[nb][0][warp] = sum;
       __syncthreads();
       Exchange& ez = sh.x[phase & 1];
@@ -614,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, 4) tree_verify_kernel(Args a, int nc
   if (beyond) w = last;
   if (w != warp) return;
   const ff rest = beyond ? ff{INFINITY, 0.0f} : ff_sub(goal, at);
-  const int token = region_draw<DT, VEC>(x, begin, end, rest, lane, a, sh.tab);
+  const int token = region_draw<DT, VEC>(x, begin, end, rest, lane, a, sh.tab, sh.tab1k);
   if (lane == 0) out[count] = token;
 }
 
@@ -705,6 +777,16 @@ int spec_verify_tree(const void* target_logits, const void* draft_logits, const 
   a.il = (float)(inv - (double)a.ih);
   a.unit_t = temperature == 1.0f;
   a.c2 = (float)(1.4426950408889634074 * inv);
+  a.inv_t = inv;
+  {
+    const double C = (double)temperature * 0.69314718055994530942 / 1024.0;
+    a.dc.ch = (float)C;
+    a.dc.cli = (float)((C - (double)a.dc.ch) * inv);
+    a.dc.inv = (float)(1.0 / C);
+    a.dc.ih = a.ih;
+  }
+  a.reach = 2000.0f * temperature;
+  a.short_ok = temperature >= 1e-3f && temperature <= 1e3f;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (cudaMemsetAsync(workspace, 0, 4, st) != cudaSuccess) return SV_ERR_CUDA;
   const bool vec = !misaligned(target_logits, 16) && !misaligned(draft_logits, 16) && (size_t)V * es % 16 == 0;
