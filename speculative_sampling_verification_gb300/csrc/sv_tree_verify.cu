@@ -247,37 +247,61 @@ SV_DEVINL ff ff2_warp_sum(const ff2& s) {
   return ff_warp_sum(ff_add({s.hi.x, s.lo.x}, {s.hi.y, s.lo.y}));
 }
 
-// Maximum and sum of exp((l - max)/T), in fp32, over a warp's region of one row. NaN
-// and +inf end in a NaN sum; a region of -inf has the maximum -inf and the sum 0.
-template <int DT, bool VEC>
-SV_DEVINL void region_stats(const void* row, int begin, int end, int lane, const Args& a, float* top, float* sum) {
-  float m = neg_inf();
-#pragma unroll 4
-  for (int e = begin + lane * 8; e < end; e += kStep) {
-    float2 v[4];
-    load8<DT, VEC>(row, e, end, v);
+// Maximum and sum of exp((l - max)/T), in fp32, over a warp's region of one or two
+// rows, in one pass: a lane's running maximum moves at most once for eight elements.
+// NaN and +inf end in a NaN sum; a region of -inf has the maximum -inf and the sum 0.
+struct Running {
+  float m, s;
+  SV_DEVINL void take(const float2 (&v)[4], float c2) {
+    float top = m;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) m = fmaxf(m, fmaxf(v[i].x, v[i].y));
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const float2 nm = f2(m == neg_inf() ? 0.0f : -m), c = f2(a.c2);
-  float2 acc[2] = {f2(0.0f), f2(0.0f)};
-#pragma unroll 2
-  for (int e = begin + lane * 8; e < end; e += kStep) {
-    float2 v[4];
-    load8<DT, VEC>(row, e, end, v);
+    for (int i = 0; i < 4; ++i) top = fmaxf(top, fmaxf(v[i].x, v[i].y));
+    const float ref = top == neg_inf() ? 0.0f : top;
+    float2 acc[2] = {f2(0.0f), f2(0.0f)};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float2 y = f2_mul(f2_add(v[i], nm), c);
+      const float2 y = f2_mul(f2_add(v[i], f2(-ref)), f2(c2));
       acc[i & 1] = f2_add(acc[i & 1], make_float2(ex2_fast(y.x), ex2_fast(y.y)));
     }
+    const float2 t = f2_add(acc[0], acc[1]);
+    const float keep = top > m ? ex2_fast((m - ref) * c2) : 1.0f;  // m = -inf: 0 (and s = 0)
+    s = fmaf(s, keep, t.x + t.y);
+    m = top;
   }
-  float t = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
+  SV_DEVINL void over_warp(float c2) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-  *top = m;
-  *sum = t;
+    for (int o = 16; o > 0; o >>= 1) {
+      const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
+      const float top = fmaxf(m, m2);
+      const float ref = top == neg_inf() ? 0.0f : top;
+      s = (m == neg_inf() ? s : s * ex2_fast((m - ref) * c2)) + (m2 == neg_inf() ? s2 : s2 * ex2_fast((m2 - ref) * c2));
+      m = top;
+    }
+  }
+};
+
+template <int DT, bool VEC>
+SV_DEVINL void region_stats(const void* q, const void* p, int begin, int end, int lane, const Args& a, Running (&r)[2]) {
+  r[0] = r[1] = {neg_inf(), 0.0f};
+  if (p) {
+#pragma unroll 2
+    for (int e = begin + lane * 8; e < end; e += kStep) {
+      float2 v[4], w[4];
+      load8<DT, VEC>(q, e, end, v);
+      load8<DT, VEC>(p, e, end, w);
+      r[0].take(v, a.c2);
+      r[1].take(w, a.c2);
+    }
+    r[1].over_warp(a.c2);
+  } else {
+#pragma unroll 2
+    for (int e = begin + lane * 8; e < end; e += kStep) {
+      float2 v[4];
+      load8<DT, VEC>(q, e, end, v);
+      r[0].take(v, a.c2);
+    }
+  }
+  r[0].over_warp(a.c2);
 }
 
 // The same sum as a float-float, of a row's weights as the draw takes them.
@@ -442,13 +466,15 @@ __global__ void __launch_bounds__(kThreads, 4) tree_verify_kernel(Args a, int nc
                          : nullptr;
     // ---- maxima and sums of the node's rows
     buf = 0;
-#pragma unroll 1
-    for (int r = 0; r < (kids ? 2 : 1); ++r) {
-      float top, sum;
-      region_stats<DT, VEC>(r ? p : q, begin, end, lane, a, &top, &sum);
+    {
+      Running r[2];
+      region_stats<DT, VEC>(q, p, begin, end, lane, a, r);
       if (lane == 0) {
-        sh.wtop[r][warp] = top;
-        sh.wfast[r][warp] = sum;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          sh.wtop[k][warp] = r[k].m;
+          sh.wfast[k][warp] = r[k].s;
+        }
       }
     }
     __syncthreads();
