@@ -40,7 +40,7 @@ struct Args {
 //
 // Rows are (node, query head of the group) pairs that share a key/value head: a
 // Q tile is up to 128 of them, the M of one tcgen05.mma. Keys come in tiles of
-// KT positions. For a tile: S = Q K^T into tensor memory; one thread a row turns
+// KT positions. For a tile: S = Q K^T into tensor memory; two threads a row turn
 // S into P = 2^(S c - m c) (c = scale log2 e) with its running maximum m and sum,
 // and writes P as bf16 over S; O += P V with P as the tensor-memory operand.
 // O is rescaled in tensor memory only when the maximum grows by more than 2^8
@@ -63,14 +63,15 @@ struct Args {
 // one go to the workspace as (O, m, sum), and the last CTA to arrive joins them in
 // the order of the ranges, so that results do not depend on the timing.
 //
-// Warps: 0-7 softmax (warp w reads lanes 32 (w % 4) ..), 8 producer (TMA, one box a
-// page), 9 MMA issuer and owner of the tensor memory, 12-15 (e4m3 cache) convert
-// codes to bf16 between a staging ring and the operand ring; the scales of
-// keys enter S, those of values enter P, in fp32.
+// Warps: 0-15 softmax (a stream has eight: four for the lanes of its 128 rows, for each
+// half of a tile's keys; one stream only: 0-7), 16 producer (TMA, one box a page), 17 MMA
+// issuer and owner of the tensor memory, 20-23 (e4m3 cache) convert codes to bf16 between
+// a staging ring and the operand ring; the scales of keys enter S, those of values
+// enter P, in fp32. The softmax warps meet at hardware barriers, so none of them
+// leaves early: once a wait has run out they only count their tiles down.
 
 constexpr int kConvWarps = 4;
-constexpr int kSoftWarps = 8;
-constexpr int kProducer = 8, kIssuer = 9;
+constexpr int kProducer = 16, kIssuer = 17, kConverter = 20;
 constexpr int kMaxCtas = 152;
 constexpr int kScaleSlots = 8;
 constexpr int kMaxSlots = 8;
@@ -101,12 +102,12 @@ struct Cfg {
   static constexpr int kQBytes = 128 * DP * 2;
   static constexpr int kSlot = KT * DP * 2;
   static constexpr int kStage = KT * DP;
-  static constexpr int kBudget = 219 * 1024;
+  static constexpr int kBudget = 214 * 1024;
   static constexpr int kStages = F8 ? 4 : 0;
   static constexpr int kFit = (kBudget - NQ * kQBytes - kStages * kStage - (F8 ? kScaleSlots * 2 * KT * 4 : 0)) / kSlot;
   static constexpr int kSlots = kFit < 8 ? kFit : 8;
   static constexpr bool kAlternate = NS == 2 && !SHARED;
-  static constexpr int kThreads = 32 * (12 + (F8 ? kConvWarps : 0));
+  static constexpr int kThreads = 32 * (F8 ? kConverter + kConvWarps : kIssuer + 1);
   static constexpr unsigned kS0 = 0, kS1 = 128, kO0 = NS == 2 ? 256 : 128, kO1 = 256 + DP;
 };
 
@@ -115,20 +116,24 @@ struct TcTail {
   unsigned long long sfull[4], sempty[4];
   unsigned long long scale[kScaleSlots];
   unsigned long long q_ready, s_ready[2], p_ready[2], pv_done[2];
-  unsigned long long wg_sync[2], all_sync;  // barriers of a warpgroup, and of all softmax warps
   unsigned tmem_base, abort, bad[2], badv[2], last;
   int b0;
   long long lo, hi, base0, total;
   int groups;
   int par[2][2][kTreeMax];
-  float2 ml[2][128];
+};
+
+struct WideTail {
+  TcTail t;
+  float2 ml[2][2][128];  // [stream][half of the keys][row]: maximum and sum
+  float rmax[2][2][128];
 };
 
 template <int DP, bool F8, bool SHARED>
 constexpr int tc_smem() {
   using C = Cfg<DP, F8, SHARED>;
   return 1024 + C::NQ * C::kQBytes + C::kSlots * C::kSlot + C::kStages * C::kStage +
-         (F8 ? kScaleSlots * 2 * C::KT * 4 : 0) + (int)sizeof(TcTail);
+         (F8 ? kScaleSlots * 2 * C::KT * 4 : 0) + (int)sizeof(WideTail);
 }
 
 SV_DEVINL void bar_arrive(unsigned bar) {
@@ -226,29 +231,22 @@ SV_DEVINL void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;
 SV_DEVINL void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 SV_DEVINL void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// 64 columns of this thread's lane.
-SV_DEVINL void tmem_ld64(unsigned t, float* v) {
-  uint32_t r[64];
+// 32 columns of this thread's lane.
+SV_DEVINL void tmem_ld32(unsigned t, float* v) {
+  uint32_t r[32];
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
       "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, "
-      "%18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, "
-      "%34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, "
-      "%50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63"
-      "}, [%64];\n\ttcgen05.wait::ld.sync.aligned;"
+      "%18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31"
+      "}, [%32];\n\ttcgen05.wait::ld.sync.aligned;"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
         "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
         "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
         "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
-        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]),
-        "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]),
-        "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]),
-        "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
-        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]),
-        "=r"(r[63])
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(t));
 #pragma unroll
-  for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 SV_DEVINL void tmem_ld8(unsigned t, float (&v)[8]) {
   uint32_t r[8];
@@ -330,16 +328,6 @@ SV_DEVINL uint32_t pack_bf16(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 SV_DEVINL void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// Barrier of some warps on an mbarrier (one arrival a warp), bounded like every
-// wait: a warp that gave up must not leave the others waiting.
-SV_DEVINL bool warps_sync(unsigned bar, unsigned& phase, int lane, volatile unsigned* abort, unsigned* status) {
-  __syncwarp();
-  if (lane == 0) bar_arrive(bar);
-  const bool ok = __all_sync(0xffffffffu, bar_wait(bar, phase & 1, abort, status));
-  ++phase;
-  return ok;
-}
 
 // Hardware barrier of `threads` threads, and the OR of their predicates.
 // The kernel launched before this one (which cleared the counters) is complete.
@@ -446,28 +434,21 @@ SV_DEVINL void find_range(const TcArgs& x, TcTail& t, int group, int lane) {
 // Called by `threads` threads once their part of an item that is cut is written:
 // the last part to arrive joins them all, in the order of the ranges. `sum` and O of
 // a part are relative to its m (in units of 1/join_c powers of two); NaN marks a sequence at fault.
-// Out of line: it runs once an item, and the kernels' code is long as it is. `phase`: of
-// the softmax warps' mbarrier, or null where they meet at a hardware barrier.
+// Out of line: it runs once an item, and the kernels' code is long as it is.
 template <int KT>
-__device__ __noinline__ bool join_parts(const TcArgs& x, TcTail& t, const Walk<KT>& w, int part, int cta_rows,
-                                        int rows_here, int threads, unsigned* phase) {
-  const int lane = threadIdx.x & 31;
-  auto sync = [&]() -> bool {
-    if (phase) return warps_sync(smem_u32(&t.all_sync), *phase, lane, &t.abort, x.a.status);
-    named_sync(3, threads);
-    return true;
-  };
+__device__ __noinline__ void join_parts(const TcArgs& x, TcTail& t, const Walk<KT>& w, int part, int cta_rows,
+                                        int rows_here, int threads) {
   const Args& a = x.a;
   const long long total = t.total;
   const int ng = t.groups, G = a.Hq / a.Hkv;
   const long long first = w.base + kItemUnits;  // the item's first tile on the line
   const int gs = (int)(((first + 1) * ng - 1) / total), ge = (int)(((first + w.n) * ng - 1) / total);
   __threadfence();
-  if (!sync()) return false;
+  named_sync(3, threads);
   if (threadIdx.x == 0)
     t.last = atomicAdd(&x.counters[gs * x.parts_per_item + part], 1u) == (unsigned)(ge - gs);
-  if (!sync()) return false;
-  if (!t.last) return true;
+  named_sync(3, threads);
+  if (!t.last) return;
   __threadfence();
   const int units = a.D / 4;
 #pragma unroll 1
@@ -524,7 +505,6 @@ __device__ __noinline__ bool join_parts(const TcArgs& x, TcTail& t, const Walk<K
     o.y = *reinterpret_cast<const uint32_t*>(&h1);
     *reinterpret_cast<uint2*>(a.out + (((long long)w.b * a.T + nd) * a.Hq + w.hk * G + gr % G) * a.D + u * 4) = o;
   }
-  return true;
 }
 
 // Place of tile i's keys and values in the order of the operand ring.
@@ -557,12 +537,13 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
   unsigned char* ring = smem + C::NQ * C::kQBytes;
   unsigned char* stage = ring + C::kSlots * C::kSlot;
   float* scales = reinterpret_cast<float*>(stage + C::kStages * C::kStage);  // [kScaleSlots][2][KT]
-  TcTail& t = *reinterpret_cast<TcTail*>(reinterpret_cast<unsigned char*>(scales) +
-                                         (F8 ? kScaleSlots * 2 * KT * 4 : 0));
+  WideTail& wide = *reinterpret_cast<WideTail*>(reinterpret_cast<unsigned char*>(scales) +
+                                                (F8 ? kScaleSlots * 2 * KT * 4 : 0));
+  TcTail& t = wide.t;
   const Args& a = x.a;
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int group = blockIdx.x / x.parts_per_item, part = blockIdx.x % x.parts_per_item;
-  constexpr int kSoft = NS * 4;  // softmax warps at work
+  constexpr int kSoft = NS * 8;  // softmax warps at work
 
   if (warp == 0) {
     find_range<KT>(x, t, group, lane);
@@ -579,11 +560,10 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
     mbar_init(smem_u32(&t.q_ready), kSoft);
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&t.s_ready[i]), 1);
-      mbar_init(smem_u32(&t.p_ready[i]), 4);
+      mbar_init(smem_u32(&t.p_ready[i]), 8);
       mbar_init(smem_u32(&t.pv_done[i]), 1);
-      mbar_init(smem_u32(&t.wg_sync[i]), 4);
     }
-    mbar_init(smem_u32(&t.all_sync), kSoft);
+
     t.abort = 0;
     t.bad[0] = t.bad[1] = t.badv[0] = t.badv[1] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -726,7 +706,8 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
         const unsigned p = uni(tmem + (s ? C::kS1 : C::kS0)), d = uni(tmem + (s ? C::kO1 : C::kO0));
 #pragma unroll
         for (int i = 0; i < KT / 16; ++i)
-          mma_ts(lead, d, p + i * 8, v + ((i * 2048) >> 4), id_pv, acc || i > 0);
+          // P lies over the first half of each half of S's columns.
+          mma_ts(lead, d, p + i / (KT / 32) * (KT / 2) + i % (KT / 32) * 8, v + ((i * 2048) >> 4), id_pv, acc || i > 0);
       };
       auto p_wait = [&](int s) {
         ok = ok && warp_wait(smem_u32(&t.p_ready[s]), pcount[s] & 1, abort, a.status);
@@ -795,12 +776,13 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
       }
     }
   } else if (warp < kSoft) {
-    // ---- softmax, one thread a row
-    const int s = warp >> 2;           // stream
-    const int wt = threadIdx.x & 127;  // thread of the warpgroup: its row, and a key row of V
-    const int q = warp & 3;
+    // ---- softmax, two threads a row: a half of the tile's keys each
+    const int s = warp >> 3, hf = warp >> 2 & 1, q = warp & 3;  // stream, half, 32 rows
+    const int wt = threadIdx.x & 127;  // row of the Q tile, and key row of V
+    const int st = threadIdx.x & 255;  // thread of the stream
+    constexpr int HC = KT / 2;         // keys of a half
     const unsigned lanes = (unsigned)(q * 32) << 16;
-    const unsigned sbase = tmem + (s ? C::kS1 : C::kS0) + lanes;
+    const unsigned sbase = tmem + (s ? C::kS1 : C::kS0) + lanes + hf * HC;
     const unsigned obase = tmem + (s ? C::kO1 : C::kO0) + lanes;
     const int G = a.Hq / a.Hkv;
     const int tile_rows = x.rpt;
@@ -811,21 +793,20 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
     const bool busy = q * 32 < nrows;  // the warp has rows
     const int node = have ? row / G : 0;
     const float c = x.c, grow = kLazy / c;
-    unsigned item = 0, tile_no = 0, scount = 0, entry0 = 0, wg_phase = 0, all_phase = 0;
-    bool ok = true;
+    unsigned item = 0, tile_no = 0, scount = 0, entry0 = 0;
+    auto wait = [&](unsigned long long* bar, unsigned parity) { bar_wait(smem_u32(bar), parity, abort, a.status); };
 #pragma unroll 1
-    for (; w.more() && ok; w.next(a), ++item) {
+    for (; w.more(); w.next(a), ++item) {
       const int n = w.t1 - w.t0;
       const bool seq_ok = ctx_ok(a, w.ctx);
       const bool tail = seq_ok && (long long)w.t1 * KT > w.ctx;
       // Q into shared memory, 16 bytes a thread and step.
       {
         const int units = a.D / 8;
-        constexpr int kLoaders = SHARED ? 128 : NS * 128;
-        const int first = SHARED ? wt : threadIdx.x;
+        constexpr int kLoaders = SHARED ? 256 : NS * 256;
         unsigned char* qs = smem + (SHARED ? s * C::kQBytes : 0);
 #pragma unroll 1
-        for (int i = first; i < 128 * units; i += kLoaders) {
+        for (int i = SHARED ? st : threadIdx.x; i < 128 * units; i += kLoaders) {
           const int r = i / units, u = i - r * units;
           uint4 v = make_uint4(0, 0, 0, 0);
           if (r < nrows && !x.qzero) {
@@ -850,12 +831,11 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
       {
         unsigned bad = seq_ok ? 0u : (unsigned)SV_DEV_PAGE_RANGE;
         if (tail) {
-          if (wt < a.T) par[wt] = a.parents ? a.parents[(long long)w.b * a.T + wt] : wt - 1;
-          ok = warps_sync(smem_u32(&t.wg_sync[s]), wg_phase, lane, abort, a.status);
-          if (!ok) break;
-          if (wt < a.T) {
-            const int p = par[wt];
-            if (p < -2 || p >= wt || (p >= 0 && par[p] == -2)) bad |= SV_DEV_TREE;
+          if (st < a.T) par[st] = a.parents ? a.parents[(long long)w.b * a.T + st] : st - 1;
+          named_sync(1 + s, 256);
+          if (st < a.T) {
+            const int p = par[st];
+            if (p < -2 || p >= st || (p >= 0 && par[p] == -2)) bad |= SV_DEV_TREE;
           }
           if (have) {
 #pragma unroll 1
@@ -873,7 +853,7 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
           const int p0 = (int)(((long long)w.t0 * KT) >> x.lp);
           const int p1 = (int)min(((long long)w.t1 * KT + a.P - 1) >> x.lp, ((long long)w.ctx + a.T + a.P - 1) >> x.lp);
 #pragma unroll 1
-          for (int p = p0 + wt; p < p1; p += 128) {
+          for (int p = p0 + st; p < p1; p += 256) {
             bool used = (long long)p * a.P < w.ctx;
             if (!used) {
               const int j1 = min((long long)a.T, (long long)(p + 1) * a.P - w.ctx);
@@ -897,119 +877,110 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
       for (int i = ALT ? s : 0; i < n; i += ALT ? 2 : 1) {
         const int tile = w.t0 + i;
         const bool edge = (long long)(tile + 1) * KT > w.ctx || !seq_ok;
-        ok = __all_sync(0xffffffffu, bar_wait(smem_u32(&t.s_ready[s]), scount & 1, abort, a.status));
-        const float* ksc = scales + ((tile_no + i) % kScaleSlots) * 2 * KT;
-        if (F8)
-          ok = __all_sync(0xffffffffu,
-                          ok && bar_wait(smem_u32(&t.scale[(tile_no + i) % kScaleSlots]),
-                                         ((tile_no + i) / kScaleSlots) & 1, abort, a.status));
-        if (!ok) break;
+        const float* ksc = scales + ((tile_no + i) % kScaleSlots) * 2 * KT + hf * HC;
+        wait(&t.s_ready[s], scount & 1);
+        if (F8) wait(&t.scale[(tile_no + i) % kScaleSlots], ((tile_no + i) / kScaleSlots) & 1);
         fence_after();
+        // Which of 32 of the half's columns from `col` on the row attends: context, then
+        // ancestors; nothing in a sequence at fault.
+        auto seen = [&](int col) -> unsigned {
+          if (!seq_ok) return 0u;
+          const long long n0 = (long long)tile * KT + hf * HC + col - w.ctx;
+          if (n0 <= -32) return 0xffffffffu;
+          if (n0 >= kTreeMax) return 0u;
+          const int k = (int)(n0 >> 5), sh = (int)(n0 & 31);
+          const unsigned lo = k < 0 ? 0xffffffffu : k == 0 ? anc[0] : k == 1 ? anc[1] : k == 2 ? anc[2] : anc[3];
+          const unsigned hi = k < 0 ? anc[0] : k == 0 ? anc[1] : k == 1 ? anc[2] : k == 2 ? anc[3] : 0u;
+          return __funnelshift_r(lo, hi, sh);
+        };
+        // S, 32 columns at a time, with the keys' scales and the mask.
+        float v[32];
+        auto load = [&](int col) {
+          tmem_ld32(sbase + col, v);
+          if (F8) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) {
+              const float4 f = *reinterpret_cast<const float4*>(ksc + col + j);
+              const float2 z0 = f2_mul(make_float2(v[j], v[j + 1]), make_float2(f.x, f.y));
+              const float2 z1 = f2_mul(make_float2(v[j + 2], v[j + 3]), make_float2(f.z, f.w));
+              v[j] = z0.x;
+              v[j + 1] = z0.y;
+              v[j + 2] = z1.x;
+              v[j + 3] = z1.y;
+            }
+          }
+          if (edge) {
+            const unsigned see = seen(col);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = see >> j & 1u ? v[j] : -INFINITY;
+          }
+        };
+        float top = -INFINITY;
         if (busy) {
-          // Which of 32 columns from `col` on the row attends: context, then
-          // ancestors; nothing in a sequence at fault.
-          auto seen = [&](int col) -> unsigned {
-            if (!seq_ok) return 0u;
-            const long long n0 = (long long)tile * KT + col - w.ctx;
-            if (n0 <= -32) return 0xffffffffu;
-            if (n0 >= kTreeMax) return 0u;
-            const int k = (int)(n0 >> 5), sh = (int)(n0 & 31);
-            const unsigned lo = k < 0 ? 0xffffffffu : k == 0 ? anc[0] : k == 1 ? anc[1] : k == 2 ? anc[2] : anc[3];
-            const unsigned hi = k < 0 ? anc[0] : k == 0 ? anc[1] : k == 1 ? anc[2] : k == 2 ? anc[3] : 0u;
-            return __funnelshift_r(lo, hi, sh);
-          };
-          // S, 64 columns at a time, with the keys' scales and the mask. 128 columns do
-          // not fit the registers: they are read a second time.
-          float v[64];
-          auto load = [&](int col) {
-            tmem_ld64(sbase + col, v);
-            if (F8) {
-#pragma unroll
-              for (int j = 0; j < 64; j += 4) {
-                const float4 f = *reinterpret_cast<const float4*>(ksc + col + j);
-                const float2 z0 = f2_mul(make_float2(v[j], v[j + 1]), make_float2(f.x, f.y));
-                const float2 z1 = f2_mul(make_float2(v[j + 2], v[j + 3]), make_float2(f.z, f.w));
-                v[j] = z0.x;
-                v[j + 1] = z0.y;
-                v[j + 2] = z1.x;
-                v[j + 3] = z1.y;
-              }
-            }
-            if (edge) {
-#pragma unroll
-              for (int h = 0; h < 64; h += 32) {
-                const unsigned see = seen(col + h);
-#pragma unroll
-                for (int j = 0; j < 32; ++j) v[h + j] = see >> j & 1u ? v[h + j] : -INFINITY;
-              }
-            }
-          };
           float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int col = 0; col < KT; col += 64) {
+          for (int col = 0; col < HC; col += 32) {
             load(col);
 #pragma unroll
-            for (int j = 0; j < 64; ++j) top4[j & 3] = fmaxf(top4[j & 3], v[j]);
+            for (int j = 0; j < 32; ++j) top4[j & 3] = fmaxf(top4[j & 3], v[j]);
           }
-          const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
-          const bool raise = top > m + grow || (m == -INFINITY && top > m);
-          if (__any_sync(0xffffffffu, raise)) {
-            const float nm = raise ? top : m;
-            const float f = raise ? (m == -INFINITY ? 0.0f : ex2_fast((m - nm) * c)) : 1.0f;
-            if (any) {
-              ok = __all_sync(0xffffffffu,
-                              bar_wait(smem_u32(&t.pv_done[s]), (scount - 1) & 1, abort, a.status));
-              if (!ok) break;
-              fence_after();
+          top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
+        }
+        // Both threads of a row hold the same reference m: where one of the stream's rows
+        // outgrows it, all take their maxima over both halves.
+        if (named_any(1 + s, 256, top > m + grow || (m == -INFINITY && top > m))) {
+          wide.rmax[s][hf][wt] = top;
+          named_sync(1 + s, 256);
+          const float nm = fmaxf(m, fmaxf(top, wide.rmax[s][hf ^ 1][wt]));
+          const float f = m == -INFINITY ? 0.0f : ex2_fast((m - nm) * c);  // (1 where the row did not grow)
+          if (any && busy) {
+            wait(&t.pv_done[s], (scount - 1) & 1);
+            fence_after();
 #pragma unroll 1
-              for (int col = 0; col < a.D; col += 16) {
-                float v0[8], v1[8];
-                uint32_t r[16];
-                tmem_ld8(obase + col, v0);
-                tmem_ld8(obase + col + 8, v1);
+            for (int col = 16 * hf; col < a.D; col += 32) {
+              float v0[8], v1[8];
+              uint32_t r[16];
+              tmem_ld8(obase + col, v0);
+              tmem_ld8(obase + col + 8, v1);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                  r[j] = __float_as_uint(v0[j] * f);
-                  r[j + 8] = __float_as_uint(v1[j] * f);
-                }
-                tmem_st16(obase + col, r);
+              for (int j = 0; j < 8; ++j) {
+                r[j] = __float_as_uint(v0[j] * f);
+                r[j + 8] = __float_as_uint(v1[j] * f);
               }
+              tmem_st16(obase + col, r);
             }
-            sum *= f;
-            m = nm;
           }
+          sum *= f;
+          m = nm;
+        }
+        if (busy) {
           // A masked score is -inf, so its weight comes out as 0 (the values' scales
           // may be NaN there, hence the select after them).
           const float2 c2 = f2(c), mc2 = f2(m == -INFINITY ? 0.0f : -m * c);
           float2 sum2[2] = {f2(0.0f), f2(0.0f)};
 #pragma unroll
-          for (int col = 0; col < KT; col += 64) {
-            if (KT > 64) load(col);
+          for (int col = 0; col < HC; col += 32) {
+            if (HC > 32) load(col);
+            uint32_t r[16];
+            const unsigned see = F8 && edge ? seen(col) : 0xffffffffu;
 #pragma unroll
-            for (int h = 0; h < 64; h += 32) {
-              uint32_t r[16];
-              const unsigned see = F8 && edge ? seen(col + h) : 0xffffffffu;
-#pragma unroll
-              for (int j = 0; j < 32; j += 2) {
-                const float2 y = f2_fma(make_float2(v[h + j], v[h + j + 1]), c2, mc2);
-                float2 p = make_float2(ex2_fast(y.x), ex2_fast(y.y));
-                sum2[(j >> 1) & 1] = f2_add(sum2[(j >> 1) & 1], p);
-                if (F8) {
-                  p = f2_mul(p, *reinterpret_cast<const float2*>(ksc + KT + col + h + j));
-                  if (edge) {
-                    p.x = see >> j & 1u ? p.x : 0.0f;
-                    p.y = see >> (j + 1) & 1u ? p.y : 0.0f;
-                  }
+            for (int j = 0; j < 32; j += 2) {
+              const float2 y = f2_fma(make_float2(v[j], v[j + 1]), c2, mc2);
+              float2 p = make_float2(ex2_fast(y.x), ex2_fast(y.y));
+              sum2[(j >> 1) & 1] = f2_add(sum2[(j >> 1) & 1], p);
+              if (F8) {
+                p = f2_mul(p, *reinterpret_cast<const float2*>(ksc + KT + col + j));
+                if (edge) {
+                  p.x = see >> j & 1u ? p.x : 0.0f;
+                  p.y = see >> (j + 1) & 1u ? p.y : 0.0f;
                 }
-                const __nv_bfloat162 b = __floats2bfloat162_rn(p.x, p.y);
-                r[j >> 1] = *reinterpret_cast<const uint32_t*>(&b);
               }
-              tmem_st16(sbase + (col + h) / 2, r);
+              r[j >> 1] = pack_bf16(p.x, p.y);
             }
+            tmem_st16(sbase + col / 2, r);
           }
           const float2 sum1 = f2_add(sum2[0], sum2[1]);
-          const float part_sum = sum1.x + sum1.y;
-          sum += part_sum;
+          sum += sum1.x + sum1.y;
           tmem_wait_st();
         }
         // Values that no row, or not every row, may use: 0 times what lies there
@@ -1017,15 +988,13 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
         // and given to its descendants at the end.
         if (!F8 && edge && (!SHARED || s == 0)) {
           const unsigned ev = entry0 + v_entry<ALT>(i, n);
-          ok = __all_sync(0xffffffffu, bar_wait(smem_u32(&t.full[ev % C::kSlots]), (ev / C::kSlots) & 1, abort,
-                                                a.status));
-          if (!ok) break;
+          wait(&t.full[ev % C::kSlots], (ev / C::kSlots) & 1);
           const long long nd = (long long)tile * KT + wt - w.ctx;
           if (wt < KT && (nd >= 0 || !seq_ok)) {
             unsigned char* vrow = ring + (ev % C::kSlots) * C::kSlot + wt * 128;
             const bool dead = !seq_ok || nd >= a.T || par[nd] == -2;
 #pragma unroll 1
-            for (int u = 0; u < DP / 8; ++u) {
+            for (int u = hf * (DP / 16); u < (hf + 1) * (DP / 16); ++u) {
               uint4* at = reinterpret_cast<uint4*>(vrow + (u >> 3) * KT * 128 + (((u & 7) ^ (wt & 7)) << 4));
               uint4 v = dead ? make_uint4(0, 0, 0, 0) : *at;
               uint32_t z[4] = {v.x, v.y, v.z, v.w};
@@ -1046,34 +1015,31 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
         __syncwarp();
         if (lane == 0) bar_arrive(smem_u32(&t.p_ready[s]));
       }
-      if (!ok) break;
       tile_no += n;
       entry0 += 2u * n;
 
       // ---- the item's end: the streams' results joined, written or stored as a part
-      if (any) {
-        ok = __all_sync(0xffffffffu, bar_wait(smem_u32(&t.pv_done[s]), (scount - 1) & 1, abort, a.status));
-        if (!ok) break;
-      }
-      t.ml[s][wt] = make_float2(any ? m : -INFINITY, any ? sum : 0.0f);
+      if (any) wait(&t.pv_done[s], (scount - 1) & 1);
+      wide.ml[s][hf][wt] = make_float2(any ? m : -INFINITY, any ? sum : 0.0f);
       fence_before();
-      ok = warps_sync(smem_u32(&t.all_sync), all_phase, lane, abort, a.status);
-      if (!ok) break;
+      named_sync(3, 32 * kSoft);
       fence_after();
       const bool bad = t.bad[item & 1] != 0;
       const bool badv = t.badv[item & 1] != 0;
       if (threadIdx.x == 0) t.bad[(item + 1) & 1] = t.badv[(item + 1) & 1] = 0;
       float f0 = 1.0f, f1 = 0.0f;
+      sum = wide.ml[s][0][wt].y + wide.ml[s][1][wt].y;
       if (ALT) {
-        const float2 p0 = t.ml[0][wt], p1 = t.ml[1][wt];
-        m = fmaxf(p0.x, p1.x);
-        f0 = p0.x == -INFINITY ? 0.0f : ex2_fast((p0.x - m) * c);
-        f1 = p1.x == -INFINITY ? 0.0f : ex2_fast((p1.x - m) * c);
-        sum = p0.y * f0 + p1.y * f1;
+        const float m0 = wide.ml[0][0][wt].x, m1 = wide.ml[1][0][wt].x;
+        m = fmaxf(m0, m1);
+        f0 = m0 == -INFINITY ? 0.0f : ex2_fast((m0 - m) * c);
+        f1 = m1 == -INFINITY ? 0.0f : ex2_fast((m1 - m) * c);
+        sum = (wide.ml[0][0][wt].y + wide.ml[0][1][wt].y) * f0 + (wide.ml[1][0][wt].y + wide.ml[1][1][wt].y) * f1;
       }
       if (bad) m = __int_as_float(0x7fc00000);
       const bool whole = w.t0 == 0 && w.t1 == w.n;
-      const int cols = ALT ? a.D / 2 : a.D, col0 = ALT ? s * cols : 0;
+      // Eight columns a step, the row's threads in turn.
+      const int col0 = 8 * (ALT ? 2 * s + hf : hf), step = ALT ? 32 : 16;
       const int cta_rows = SHARED ? 2 * tile_rows : tile_rows;
       const int prow = SHARED ? s * tile_rows + wt : wt;
       const long long slot = ((long long)(group * x.parts_per_item + part) * 2 + (w.t0 == 0 ? 1 : 0));
@@ -1083,7 +1049,7 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
       __nv_bfloat16* out = a.out + (((long long)w.b * a.T + node) * a.Hq + w.hk * G + row % G) * a.D;
       if (busy) {
 #pragma unroll 1
-        for (int col = col0; col < col0 + cols; col += 8) {
+        for (int col = col0; col < a.D; col += step) {
           __syncwarp();  // tensor memory is read by whole warps
           float v[8];
           tmem_ld8(tmem + lanes + C::kO0 + (SHARED && s ? DP : 0) + col, v);
@@ -1132,19 +1098,13 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
             *reinterpret_cast<float4*>(po + col + 4) = make_float4(v[4], v[5], v[6], v[7]);
           }
         }
-        if (!whole && have && (!ALT || s == 0)) x.part_ml[slot * cta_rows + prow] = make_float2(m, sum);
+        if (!whole && have && hf == 0 && (!ALT || s == 0)) x.part_ml[slot * cta_rows + prow] = make_float2(m, sum);
       }
-      if (!whole) {
-        const int rows_here = SHARED ? cta_rows : nrows;
-        unsigned phase = all_phase;
-        ok = join_parts(x, t, w, part, cta_rows, rows_here, NS * 128, &phase);
-        all_phase = phase;
-        if (!ok) break;
-      }
+      if (!whole) join_parts(x, t, w, part, cta_rows, SHARED ? cta_rows : nrows, 32 * kSoft);
     }
-  } else if (F8 && warp >= 12) {
+  } else if (F8 && warp >= kConverter) {
     // ---- codes to bf16: 16 of a row a thread and step
-    const int ct = threadIdx.x - 32 * 12;
+    const int ct = threadIdx.x - 32 * kConverter;
     unsigned entry = 0;
     bool ok = true;
 #pragma unroll 1
@@ -1962,7 +1922,7 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
         }
       }
       if (!whole)
-        join_parts(x, t, w, 0, nrows, nrows, 32 * kSoft, nullptr);
+        join_parts(x, t, w, 0, nrows, nrows, 32 * kSoft);
       w = nx;
     }
   }
