@@ -318,11 +318,7 @@ SV_DEVINL void tmem_ld_3x2(unsigned t, unsigned piece, unsigned step, float (&v)
 #pragma unroll
   for (int i = 0; i < 6; ++i) v[i] = __uint_as_float(r[i]);
 }
-SV_DEVINL void tmem_st8(unsigned t, const uint32_t (&r)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(t),
-               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
-}
+
 SV_DEVINL uint32_t pack_bf16(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -354,7 +350,8 @@ SV_DEVINL int tiles_of(const Args& a, int ctx) {
 }
 
 // Units of an item on the line before its tiles: what an item costs a CTA beside
-// its tiles (Q, the first references, the output), in tiles.
+// its tiles (Q, the first references, the output), in tiles. 64 sequences of 9 nodes,
+// ragged to 8192 (bf16 / e4m3 cache): 6 units 239 / 219 us, 10 units 222 / 206.
 constexpr int kItemUnits = 10;
 
 // A CTA's way along its range: the item (b, hk), its tile count, context and the
