@@ -75,7 +75,7 @@ constexpr int kProducer = 16, kIssuer = 17, kConverter = 20;
 constexpr int kMaxCtas = 152;
 constexpr int kScaleSlots = 8;
 constexpr int kMaxSlots = 8;
-constexpr int kFewRows = 40;    // rows up to which keys, not rows, are the M of the products
+constexpr int kFewRows = 40;    // most rows of the kernel whose products have keys as their M
 constexpr float kLazy = 8.0f;   // growth of the maximum (powers of two) before O is rescaled
 
 struct TcArgs {
@@ -351,7 +351,8 @@ SV_DEVINL int tiles_of(const Args& a, int ctx) {
 
 // Units of an item on the line before its tiles: what an item costs a CTA beside
 // its tiles (Q, the first references, the output), in tiles. 64 sequences of 9 nodes,
-// ragged to 8192 (bf16 / e4m3 cache): 6 units 239 / 219 us, 10 units 222 / 206.
+// ragged to 8192 (bf16 / e4m3 cache): 6 units 219 / 218 us, 10 units 208 / 206, 14 units
+// 211 / 210.
 constexpr int kItemUnits = 10;
 
 // A CTA's way along its range: the item (b, hk), its tile count, context and the
@@ -1156,8 +1157,8 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
 
 // ---------------------------------------------------------------- tensor cores, few rows
 //
-// Up to 40 rows a key/value head (ordinary decoding, small trees): the operands
-// change places. S^T = K Q^T has the tile's 128 keys as the M of the product and the
+// Few rows a key/value head (ordinary decoding, small trees; keys_as_m below has the
+// rule): the operands change places. S^T = K Q^T has the tile's 128 keys as the M of the product and the
 // rows as its N, so the tensor cores and the softmax work on the rows that exist.
 // One thread a key holds that key's scores of all rows, its scales and its
 // mask; the maximum of a row is not needed, only a reference m that no score
@@ -2088,14 +2089,13 @@ bool tc_shape(int D, int page_size) {
 // tiles (D above 128: single tiles), a CTA each.
 struct Plan {
   int rows, rpt, parts, groups, cta_rows, pad;
-  bool shared, few;
+  bool shared;
   size_t off_counters, off_ml, off_o, total;
 };
 
 Plan make_plan(int T, int Hq, int Hkv, int D) {
   Plan p{};
   p.rows = T * (Hq / Hkv);
-  p.few = D <= 128 && p.rows <= kFewRows;
   p.shared = D <= 128 && p.rows > 128;
   if (p.shared) {
     p.parts = (p.rows + 255) / 256;
@@ -2213,12 +2213,27 @@ int launch_few(const TcArgs& x, cudaStream_t st) {
                       x);
 }
 
+// Whether keys, not rows, are the M of the products. Measured, keys / rows as M in us:
+// e4m3, 64 sequences to 8192, D 128: 156 / 403 (4 rows), 206 / 409 (36), since only the
+// first takes the codes as they are; it loses only for contexts of a few tiles (53 / 48
+// at 300 keys, 36 rows, D 64). bf16, D 128: one sequence of 32768 39 / 42 (4 rows) and 52 / 54
+// (36); 64 to 8192 206 / 202 and 222 / 209; 160 to 1024 111 / 122 and 148 / 139. bf16, D 64,
+// one sequence of 32768 31 / 28 and 41 / 35; 64 to 8192 175 / 131 and 200 / 136.
+bool keys_as_m(int rows, int D, bool f8) {
+  return f8 ? D <= 128 && rows <= kFewRows : D > 64 && D <= 128 && rows <= 16;
+}
+
 template <bool F8>
 int launch_tc_any(TcArgs& x, const Plan& p, cudaStream_t st) {
   const int D = x.a.D;
   x.box = std::min(x.a.P, D > 128 ? 64 : 128);
   x.lp = x.a.P == 16 ? 4 : x.a.P == 32 ? 5 : x.a.P == 64 ? 6 : 7;
-  if (p.few) return p.rows <= 16 ? launch_few<16, F8>(x, st) : launch_few<kFewRows, F8>(x, st);
+  if (keys_as_m(p.rows, D, F8)) {
+    if constexpr (F8) {
+      if (p.rows > 16) return launch_few<kFewRows, true>(x, st);
+    }
+    return launch_few<16, F8>(x, st);
+  }
   if (D > 128) return launch_tc<256, F8, false>(x, st);
   if (D > 64) return p.shared ? launch_tc<128, F8, true>(x, st) : launch_tc<128, F8, false>(x, st);
   return p.shared ? launch_tc<64, F8, true>(x, st) : launch_tc<64, F8, false>(x, st);
@@ -2296,7 +2311,7 @@ int sv_tree_attention(const void* q, int64_t q_stride_b, int64_t q_stride_t, int
     x.parts_per_item = p.parts;
     x.groups = p.groups;
     x.c = scale == 0.0f ? 1.0f : std::fabs(scale) * 1.4426950408889634f;
-    x.join_c = p.few ? 1.0f : x.c;
+    x.join_c = keys_as_m(p.rows, D, cache_dtype == SV_E4M3) ? 1.0f : x.c;
     x.qflip = scale < 0.0f ? 0x80008000u : 0u;
     x.qzero = scale == 0.0f;
     x.counters = reinterpret_cast<unsigned*>(ws + p.off_counters);
