@@ -403,6 +403,9 @@ def time_sub_workload(sv, name: str, dev, stream, reps_min_s: float = 0.25, step
         if rc != 0:
             raise RuntimeError(f"spec_verify failed: {sv.sv_status_string(rc)}")
 
+    # The inputs and, through reused memory, the workspace have writes pending on the
+    # current stream, which `stream` does not wait for by itself.
+    torch.cuda.synchronize()
     with torch.cuda.stream(stream):
         call(0)
         for a, b in evs:
@@ -1433,6 +1436,7 @@ def run_lmhead(args, world, rank, local):
         if rc != 0:
             raise RuntimeError(f"sv_lmhead_stats: {sv.sv_status_string(rc)}")
 
+    torch.cuda.synchronize()  # the inputs, made on the current stream
     with torch.cuda.stream(stream):
         call()
     torch.cuda.synchronize()
