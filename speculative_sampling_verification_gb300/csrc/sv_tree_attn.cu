@@ -55,6 +55,11 @@ struct Args {
 // tile of its own and both use every tile. Head sizes above 128 have room for
 // one stream only.
 //
+// 8 sequences of 64 nodes, 64/8 heads of 128, contexts to 32768, bf16: 347 us, 0.98 PFLOP/s, with
+// the tensor pipe active 40 % of the time and the issue slots 37 %: the chain of product,
+// softmax and product bounds it. One thread a row: 381 us. 64 sequences of 9 nodes, 32/8 heads,
+// to 8192, bf16: 208 us, 5.8 TB/s.
+//
 // Work: the tiles of all (sequence, key/value head) items, with a few units for the item
 // itself before them, form one line, cut into equal ranges, one for each group of CTAs (the CTAs of a group take the item's
 // Q tiles, in step, so that a tile is read from HBM once). The cuts follow the
@@ -1175,6 +1180,10 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
 // O for each piece: off by at most 2^-12 of itself or, for small weights, 2^-22 of the
 // reference weight. A bf16 cache uses bf16 operands, P rounded once (2^-8).
 //
+// 64 sequences of 9 nodes, 32/8 heads of 128, contexts to 8192, e4m3: 206 us, 3.1 TB/s, with
+// 54 % of the issue slots active, the tensor pipe 13 % and the memory 41 %: the latency of
+// the softmax's dependent steps. One token over 32768 keys: 30 us.
+//
 // Streams, ranges and parts are those of the kernel above; the next tile's
 // S^T is issued before this tile's O^T, so neither waits for the other. The softmax
 // warps meet at hardware barriers, so none of them leaves early: once a wait
@@ -1193,8 +1202,8 @@ struct FewCfg {
   static constexpr int kSlot = KT * (F8 ? 128 : 256);
   static constexpr int kTailBytes = 12 * 1024;
   static constexpr int kFit = (226 * 1024 - kTailBytes - kQBytes - 4 * kPBytes) / kSlot;
-  // More than 96 KB in flight on each SM only lengthens the queue at the memory: an
-  // e4m3 cache's batch took 219 us with ten slots, 214 with seven, 210 with five.
+  // More in flight on each SM only lengthens the queue at the memory: an e4m3 cache's
+  // batch took 217 us with every slot that fitted (at most eight), 214 with seven, 210 with five.
   static constexpr int kSlots = kFit < 6 ? kFit : 6;
   static constexpr int kSoft = 16;                                 // softmax warps
   static constexpr int kThreads = 32 * (kSoft + 2);
@@ -1945,7 +1954,7 @@ __global__ void clear_kernel(unsigned* p, int n) {
 //
 // One warp a query row, one key at a time, running maximum and sum in fp32.
 // Takes every head size and page size; bound by the latency of a key's
-// reduction over the lanes.
+// reduction over the lanes: 8 sequences of 4 nodes, 32 heads of 100, 2000 keys, e4m3: 2.7 ms.
 
 constexpr int kAnyThreads = 128;
 constexpr int kAnyPerLane = kHeadDimMax / 32;

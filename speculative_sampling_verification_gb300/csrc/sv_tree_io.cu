@@ -246,51 +246,57 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(NormRopeArgs a) {
 
 // Any even R <= D, any D, any strides: one warp a row, element loads. The row
 // is read again for the rotation (from L1) after the sum of squares; a pair's
-// two elements belong to one lane, so in-place calls are sound.
+// two elements belong to one lane, so in-place calls are sound. A block takes up to
+// kAnyHeads heads of one token and computes its angles once: with fractions of a turn (fp64,
+// at 1/64 of the rate) for each row, 16383 tokens of 40 heads of 100 in bf16 took 763 us, so 226 (1.2 TB/s).
+constexpr int kAnyHeads = 16;
 template <int DT>
 __global__ void __launch_bounds__(kThreads) norm_rope_any_kernel(NormRopeArgs a) {
+  extern __shared__ float2 turns[];  // [R/2]
   const int lane = threadIdx.x & 31;
-  const int H = a.Hq + a.Hkv;
-  const long long row = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-  if (row >= (long long)a.N * H) return;
-  const int n = (int)(row / H), h = (int)(row % H);
-  const bool isq = h < a.Hq;
-  const void* src = isq ? a.q : a.k;
-  void* dst = isq ? a.qo : a.ko;
-  const void* w = isq ? a.qw : a.kw;
-  const long long at = isq ? n * a.q_sn + h * a.q_sh : n * a.k_sn + (h - a.Hq) * a.k_sh;
-  const long long to = isq ? n * a.qo_sn + h * a.qo_sh : n * a.ko_sn + (h - a.Hq) * a.ko_sh;
+  const int H = a.Hq + a.Hkv, groups = (H + kAnyHeads - 1) / kAnyHeads;
+  const int n = (int)(blockIdx.x / (unsigned)groups), h0 = (int)(blockIdx.x % (unsigned)groups) * kAnyHeads;
   const int half = a.R / 2;
-  float ss = 0.0f, v[1];
-  for (int e = lane; e < a.D; e += 32) {
-    load_vec<DT, 1>(src, at + e, v);
-    ss = fmaf(v[0], v[0], ss);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  const float r = 1.0f / sqrtf(fmaf(ss, 1.0f / (float)a.D, a.eps));
   const int pos = a.positions[n];
-  for (int i = lane; i < half; i += 32) {
-    const int i0 = a.interleaved ? 2 * i : i, i1 = a.interleaved ? 2 * i + 1 : i + half;
-    float x0[1], x1[1], w0[1] = {1.0f}, w1[1] = {1.0f};
-    load_vec<DT, 1>(src, at + i0, x0);
-    load_vec<DT, 1>(src, at + i1, x1);
-    if (w) {
-      load_vec<DT, 1>(w, i0, w0);
-      load_vec<DT, 1>(w, i1, w1);
+  for (int i = threadIdx.x; i < half; i += kThreads) turns[i] = turn_cos_sin(pos, turn_fraction(a.inv_freq[i]));
+  __syncthreads();
+  for (int h = h0 + (int)(threadIdx.x >> 5); h < min(H, h0 + kAnyHeads); h += kThreads / 32) {
+    const bool isq = h < a.Hq;
+    const void* src = isq ? a.q : a.k;
+    void* dst = isq ? a.qo : a.ko;
+    const void* w = isq ? a.qw : a.kw;
+    const long long at = isq ? n * a.q_sn + h * a.q_sh : n * a.k_sn + (h - a.Hq) * a.k_sh;
+    const long long to = isq ? n * a.qo_sn + h * a.qo_sh : n * a.ko_sn + (h - a.Hq) * a.ko_sh;
+    float ss = 0.0f, v[1];
+    for (int e = lane; e < a.D; e += 32) {
+      load_vec<DT, 1>(src, at + e, v);
+      ss = fmaf(v[0], v[0], ss);
     }
-    const float2 c = turn_cos_sin(pos, turn_fraction(a.inv_freq[i]));
-    const float p = x0[0] * (r * w0[0]), s = x1[0] * (r * w1[0]);
-    const float y0[1] = {p * c.x - s * c.y}, y1[1] = {s * c.x + p * c.y};
-    store_vec<DT, 1>(dst, to + i0, y0);
-    store_vec<DT, 1>(dst, to + i1, y1);
-  }
-  for (int e = a.R + lane; e < a.D; e += 32) {
-    float x[1], ww[1] = {1.0f};
-    load_vec<DT, 1>(src, at + e, x);
-    if (w) load_vec<DT, 1>(w, e, ww);
-    const float y[1] = {x[0] * (r * ww[0])};
-    store_vec<DT, 1>(dst, to + e, y);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    const float r = 1.0f / sqrtf(fmaf(ss, 1.0f / (float)a.D, a.eps));
+    for (int i = lane; i < half; i += 32) {
+      const int i0 = a.interleaved ? 2 * i : i, i1 = a.interleaved ? 2 * i + 1 : i + half;
+      float x0[1], x1[1], w0[1] = {1.0f}, w1[1] = {1.0f};
+      load_vec<DT, 1>(src, at + i0, x0);
+      load_vec<DT, 1>(src, at + i1, x1);
+      if (w) {
+        load_vec<DT, 1>(w, i0, w0);
+        load_vec<DT, 1>(w, i1, w1);
+      }
+      const float2 c = turns[i];
+      const float p = x0[0] * (r * w0[0]), s = x1[0] * (r * w1[0]);
+      const float y0[1] = {p * c.x - s * c.y}, y1[1] = {s * c.x + p * c.y};
+      store_vec<DT, 1>(dst, to + i0, y0);
+      store_vec<DT, 1>(dst, to + i1, y1);
+    }
+    for (int e = a.R + lane; e < a.D; e += 32) {
+      float x[1], ww[1] = {1.0f};
+      load_vec<DT, 1>(src, at + e, x);
+      if (w) load_vec<DT, 1>(w, e, ww);
+      const float y[1] = {x[0] * (r * ww[0])};
+      store_vec<DT, 1>(dst, to + e, y);
+    }
   }
 }
 
@@ -346,7 +352,8 @@ SV_DEVINL bool slot_ok(const CacheArgs& a, long long slot) {
 // lane: one slot leads to 2 HB rows whose loads are in flight together. A row's scale
 // is its largest magnitude over 448, the largest e4m3 value, so that no code saturates
 // but by rounding. A row with NaN or infinity gets a NaN scale and codes of zero: it
-// reads back as NaN everywhere.
+// reads back as NaN everywhere. Bound by memory: 32767 tokens of 8 heads of 128, bf16 to
+// e4m3, take 33 us, 5.8 TB/s. Heads a group, in blocks of 256: one 37 us, two 34, four 40.
 template <int DT, int CDT, int L, int HB>
 __global__ void __launch_bounds__(kThreads) cache_write_kernel(CacheArgs a) {
   constexpr int VEC = DT == SV_BF16 ? 8 : 4;
@@ -423,6 +430,8 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(CacheArgs a) {
   }
 }
 
+// The same division; 100003 tokens of 8 heads of 128, e4m3 to bf16, take 101 us, 6.1 TB/s.
+// Heads a group, in blocks of 256: one 105 us, two 102, four 106.
 template <int DT, int CDT, int L, int HB>
 __global__ void __launch_bounds__(kThreads) cache_read_kernel(CacheArgs a) {
   constexpr int VEC = DT == SV_BF16 ? 8 : 4;
@@ -493,7 +502,8 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(CacheArgs a) {
   }
 }
 
-// Any D, any alignment: one warp a row, element accesses.
+// Any D, any alignment: one warp a row, element accesses. 16383 tokens of 8 heads of 100, bf16
+// and e4m3: written in 92 us, read in 68 (0.9 and 1.2 TB/s).
 template <int DT, int CDT>
 __global__ void __launch_bounds__(kThreads) cache_write_any_kernel(CacheArgs a) {
   const int lane = threadIdx.x & 31;
@@ -586,7 +596,8 @@ cudaError_t norm_rope(NormRopeArgs a, bool vec, cudaStream_t st) {
   constexpr int VEC = DT == SV_BF16 ? 8 : 4;
   const int H = a.Hq + a.Hkv;
   if (!vec) {
-    norm_rope_any_kernel<DT><<<blocks_for((long long)a.N * H, kThreads / 32), kThreads, 0, st>>>(a);
+    norm_rope_any_kernel<DT><<<blocks_for((long long)a.N * ((H + kAnyHeads - 1) / kAnyHeads), 1), kThreads,
+                               a.R / 2 * sizeof(float2), st>>>(a);
     return cudaGetLastError();
   }
   const int L = lanes_for(a.D / (2 * VEC));

