@@ -1218,6 +1218,7 @@ template <int RP>
 struct FewTail {
   TcTail t;
   unsigned long long anc[2][2][64];  // [item parity][stream][node]: ancestors and itself
+  unsigned long long o_read;         // every softmax warp has read the item's O
   // Arrays that are read four values at a time lie on 16-byte boundaries.
   alignas(16) float mref[2][RP];     // [stream] references, powers of two
   alignas(16) float fac[2][RP];      // [stream] factors of a rescaling
@@ -1327,6 +1328,7 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
       mbar_init(smem_u32(&t.p_ready[i]), kSoft / 2);
       mbar_init(smem_u32(&t.pv_done[i]), 1);
     }
+    mbar_init(smem_u32(&f.o_read), kSoft);
     t.abort = 0;
     t.bad[0] = t.bad[1] = t.badv[0] = t.badv[1] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -1442,6 +1444,9 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
       for (int i = 0; i < n && ok; ++i) {
         const int s = i & 1;
         ok = ok && warp_wait(smem_u32(&t.p_ready[s]), pcount[s] & 1, abort, a.status);
+        // The warps of both streams read both streams' O of the last item; the first P comes
+        // from the warps of one.
+        if (i == 0 && item > 0) ok = ok && warp_wait(smem_u32(&f.o_read), (item - 1) & 1, abort, a.status);
         if (!ok) break;
         fence_after();
         ++pcount[s];
@@ -1928,6 +1933,9 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
           if (wt == 0) x.part_ml[slot * nrows + r] = make_float2(fin.z, fin.w);
         }
       }
+      fence_before();
+      __syncwarp();
+      if (lane == 0) bar_arrive(smem_u32(&f.o_read));
       if (!whole)
         join_parts(x, t, w, 0, nrows, nrows, 32 * kSoft);
       w = nx;
