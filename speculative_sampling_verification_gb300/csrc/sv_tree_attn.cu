@@ -1024,12 +1024,15 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
       // ---- the item's end: the streams' results joined, written or stored as a part
       if (any) wait(&t.pv_done[s], (scount - 1) & 1);
       wide.ml[s][hf][wt] = make_float2(any ? m : -INFINITY, any ? sum : 0.0f);
+      // The next item's flags are cleared here: it sets them after the barrier, and the last
+      // item's, in the same place, have been read (this item's first S, for which thread 0
+      // has waited, came after every warp's arrival at q_ready).
+      if (threadIdx.x == 0) t.bad[(item + 1) & 1] = t.badv[(item + 1) & 1] = 0;
       fence_before();
       named_sync(3, 32 * kSoft);
       fence_after();
       const bool bad = t.bad[item & 1] != 0;
       const bool badv = t.badv[item & 1] != 0;
-      if (threadIdx.x == 0) t.bad[(item + 1) & 1] = t.badv[(item + 1) & 1] = 0;
       float f0 = 1.0f, f1 = 0.0f;
       sum = wide.ml[s][0][wt].y + wide.ml[s][1][wt].y;
       if (ALT) {
@@ -1862,6 +1865,9 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
       }
       halve<false, HR, 16>(l, lane, 0, HR, f.wsum[s][q] + row0);
       named_sync(3, 32 * kSoft);
+      // The next item's flags are cleared between the two barriers: the last item's, in the
+      // same place, were read before its second one, and the next sets them after this one's.
+      if (threadIdx.x == 0) t.bad[(item + 1) & 1] = t.badv[(item + 1) & 1] = 0;
       // Both streams have read their last S: the next item's Q may go in.
       if (nx.more()) {
         put_q((item + 1) & 1);
@@ -1889,7 +1895,6 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
       fence_before();
       named_sync(3, 32 * kSoft);
       fence_after();
-      if (threadIdx.x == 0) t.bad[(item + 1) & 1] = t.badv[(item + 1) & 1] = 0;
       const bool whole = w.t0 == 0 && w.t1 == w.n;
       const long long slot = (long long)group * 2 + (w.t0 == 0 ? 1 : 0);
       // A row a group of four warps and step (a short loop: it runs once an item).

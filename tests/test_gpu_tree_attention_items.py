@@ -127,3 +127,32 @@ def test_nan_values_of_nodes_among_several_items(T, Hq, Hkv, D, cdt):
             assert bool(out[hit][..., 4:].isfinite().all()) and bool(out[hit][..., :3].isfinite().all())
         assert clean2 is None or torch.equal(out.view(torch.int16), clean2.view(torch.int16))
         clean2 = out
+
+
+@pytest.mark.parametrize("T,Hq,Hkv,D", SHAPES)
+@pytest.mark.parametrize("cdt", [BF, F8])
+def test_faults_among_several_items(T, Hq, Hkv, D, cdt):
+    """Bad pages and malformed trees in some sequences: those read NaN in every
+    row, and the others' rows do not change."""
+    args = batch(T, Hq, Hkv, D, cdt, T + D + 2)
+    clean, status = base.run(args, 0.09)
+    assert status == 0
+    q, cache, table, lens, par = (t.clone() if isinstance(t, torch.Tensor) else t for t in args)
+    bits, faulty = 0, []
+    for b in range(3, 64, 4):
+        if b % 8 == 3 and int(lens[b]) > 0:  # a context's page
+            table[b, int(lens[b]) // 32] = -1 if b % 16 == 3 else cache.num_pages
+            bits |= 1024
+        elif b % 8 == 7:
+            par[b, 0] = 0
+            bits |= 2048
+        else:
+            continue
+        faulty.append(b)
+    good = [b for b in range(64) if b not in faulty]
+    assert len(faulty) > 10 and bits == 3072
+    for _ in range(3):
+        out, status = base.run((q, cache, table, lens, par), 0.09)
+        assert status == bits
+        assert bool(out[faulty].isnan().all())
+        assert torch.equal(out[good], clean[good])
