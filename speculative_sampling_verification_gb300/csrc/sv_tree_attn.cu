@@ -1023,7 +1023,9 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
 
       // ---- the item's end: the streams' results joined, written or stored as a part
       if (any) wait(&t.pv_done[s], (scount - 1) & 1);
-      wide.ml[s][hf][wt] = make_float2(any ? m : -INFINITY, any ? sum : 0.0f);
+      // (A stream without tiles waits for none, so that the last item's figures may still be read:
+      // it writes nothing, and nobody reads its place.)
+      if (any) wide.ml[s][hf][wt] = make_float2(m, sum);
       // The next item's flags are cleared here: it sets them after the barrier, and the last
       // item's, in the same place, have been read (this item's first S, for which thread 0
       // has waited, came after every warp's arrival at q_ready).
@@ -1034,13 +1036,16 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
       const bool bad = t.bad[item & 1] != 0;
       const bool badv = t.badv[item & 1] != 0;
       float f0 = 1.0f, f1 = 0.0f;
-      sum = wide.ml[s][0][wt].y + wide.ml[s][1][wt].y;
       if (ALT) {
-        const float m0 = wide.ml[0][0][wt].x, m1 = wide.ml[1][0][wt].x;
+        const bool two = n > 1;
+        const float m0 = wide.ml[0][0][wt].x, m1 = two ? wide.ml[1][0][wt].x : -INFINITY;
         m = fmaxf(m0, m1);
         f0 = m0 == -INFINITY ? 0.0f : ex2_fast((m0 - m) * c);
         f1 = m1 == -INFINITY ? 0.0f : ex2_fast((m1 - m) * c);
-        sum = (wide.ml[0][0][wt].y + wide.ml[0][1][wt].y) * f0 + (wide.ml[1][0][wt].y + wide.ml[1][1][wt].y) * f1;
+        sum = (wide.ml[0][0][wt].y + wide.ml[0][1][wt].y) * f0;
+        if (two) sum += (wide.ml[1][0][wt].y + wide.ml[1][1][wt].y) * f1;
+      } else {
+        sum = wide.ml[s][0][wt].y + wide.ml[s][1][wt].y;
       }
       if (bad) m = __int_as_float(0x7fc00000);
       const bool whole = w.t0 == 0 && w.t1 == w.n;

@@ -156,3 +156,18 @@ def test_faults_among_several_items(T, Hq, Hkv, D, cdt):
         assert status == bits
         assert bool(out[faulty].isnan().all())
         assert torch.equal(out[good], clean[good])
+
+
+@pytest.mark.parametrize("T,Hq,Hkv,D", SHAPES)
+@pytest.mark.parametrize("cdt", [BF, F8])
+def test_items_of_one_tile(T, Hq, Hkv, D, cdt):
+    """Every item lies in one tile, so that only the first of two streams has work, item after item."""
+    rng = np.random.default_rng(T)
+    most = max(0, (64 if D > 128 else 128) - T)
+    lens = [int(n) for n in rng.integers(0, most + 1, 96)]
+    args = base.make(96, T, Hq, Hkv, D, 32, lens, cdt, T + D + 3)
+    out, status = base.run(args, D ** -0.5)
+    assert status == 0
+    check(args, D ** -0.5, out)
+    for _ in range(3):
+        assert torch.equal(base.run(args, D ** -0.5)[0], out)
