@@ -2014,7 +2014,7 @@ __global__ void __launch_bounds__(kAnyThreads) tree_attn_any_kernel(Args a) {
   const int32_t* table = a.page_table + (long long)b * a.max_pages;
   bool bad_page = ctx < 0 || (long long)ctx + live > (long long)a.max_pages * a.P;
   if (!bad_page && !bad_tree) {
-    const int need = (ctx + live + a.P - 1) / a.P;
+    const int need = (int)(((long long)ctx + live + a.P - 1) / a.P);
     for (int i = lane; i < need; i += 32) {
       bool used = i * (long long)a.P < ctx;
       for (int j = max(0, i * a.P - ctx); j < live && !used && j < (i + 1) * a.P - ctx; ++j)

@@ -299,3 +299,17 @@ def test_python_refusals():
         sv.tree_attention(q[:, :, :3], cache, table, lens, par)
     with pytest.raises(sv.StatusError):
         sv.tree_attention(q, cache, table, lens, par, scale=float("inf"))
+
+
+def test_pages_of_more_than_2_30_tokens_are_checked():
+    """The number of needed pages is counted in 64 bits: a context and a page of more than
+    2^30 tokens each add up to more than an int holds. No key of the bad page is read."""
+    P = (1 << 30) + 4096
+    cache = sv.PagedCache(*(torch.empty(1, 1, P, 1, dtype=torch.bfloat16, device=DEV) for _ in range(2)))
+    q = torch.zeros(1, 3, 1, 1, dtype=torch.bfloat16, device=DEV)
+    lens = torch.tensor([(1 << 30) + 1000], dtype=torch.int32, device=DEV)
+    for page in (-1, 1):
+        table = torch.full((1, 1), page, dtype=torch.int32, device=DEV)
+        out, status = run((q, cache, table, lens, None), 1.0)
+        assert status == 1024
+        assert bool(out.isnan().all())
