@@ -611,10 +611,17 @@ def _raw_stream(device, stream):
     return torch._C._cuda_getCurrentRawStream(device.index)  # 2 us less than through a Stream object
 
 
-def _rows(name, t, shape, dtype):
-    """Checks an operand on the GPU whose rows are consecutive."""
+def _gpu(name, t):
+    """The GPU that a call runs on: its first operand's."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+def _rows(name, t, shape, dtype, device):
+    """Checks an operand on the call's GPU whose rows are consecutive."""
+    if t.device != device:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}")
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if t.dtype is not dtype:
@@ -625,11 +632,31 @@ def _rows(name, t, shape, dtype):
     return strides
 
 
-def _vector(name, t, shape, dtype):
-    if not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+def _vector(name, t, shape, dtype, device):
+    if t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor on {device}")
     if t.shape != shape or t.dtype is not dtype:
         raise ValueError(f"{name} must be {list(shape)} {dtype}")
+
+
+def _scratch(t, device):
+    """Address and bytes of a call's workspace."""
+    if t.device != device or not t.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous CUDA tensor on {device}")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _status_word(t, device):
+    if t is None:
+        return None
+    if t.device != device or t.dtype is not torch.int32 or t.numel() < 1:
+        raise ValueError(f"status must be an int32 CUDA tensor on {device}")
+    return t.data_ptr()
+
+
+def _cache_device(cache, device):
+    if cache.device != device:
+        raise ValueError(f"the cache is on {cache.device}, the other operands on {device}")
 
 
 def sv_qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved, q_out, k_out,
@@ -639,22 +666,23 @@ def sv_qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions, eps, interlea
     None, inv_freq [R/2] f32, positions [N] int32; returns the host status code."""
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q must be [N, Hq, D] and k [N, Hkv, D]")
+    dev = _gpu("q", q)
     N, Hq, D = q.shape
     Hkv, dtype, code = k.shape[1], q.dtype, _dtype_code(q)
-    qs, qos = _rows("q", q, (N, Hq, D), dtype), _rows("q_out", q_out, (N, Hq, D), dtype)
-    ks, kos = _rows("k", k, (N, Hkv, D), dtype), _rows("k_out", k_out, (N, Hkv, D), dtype)
+    qs, qos = _rows("q", q, (N, Hq, D), dtype, dev), _rows("q_out", q_out, (N, Hq, D), dtype, dev)
+    ks, kos = _rows("k", k, (N, Hkv, D), dtype, dev), _rows("k_out", k_out, (N, Hkv, D), dtype, dev)
     for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
         if w is not None:
-            _vector(name, w, (D,), dtype)
+            _vector(name, w, (D,), dtype, dev)
     if inv_freq.dim() != 1:
         raise ValueError("inv_freq must be [R/2]")
     half = inv_freq.shape[0]
-    _vector("inv_freq", inv_freq, (half,), torch.float32)
-    _vector("positions", positions, (N,), torch.int32)
+    _vector("inv_freq", inv_freq, (half,), torch.float32, dev)
+    _vector("positions", positions, (N,), torch.int32, dev)
     return load_library().sv_qk_norm_rope(
         q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1], _address(q_weight), _address(k_weight),
         inv_freq.data_ptr(), positions.data_ptr(), N, Hq, Hkv, D, 2 * half, code, eps, 1 if interleaved else 0,
-        q_out.data_ptr(), qos[0], qos[1], k_out.data_ptr(), kos[0], kos[1], _raw_stream(q.device, stream))
+        q_out.data_ptr(), qos[0], qos[1], k_out.data_ptr(), kos[0], kos[1], _raw_stream(dev, stream))
 
 
 def qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions, *, eps=1e-6, interleaved=False, q_out=None,
@@ -680,13 +708,14 @@ def sv_cache_write(k, v, slots, cache, status=None, stream=None) -> int:
     returns the host status code."""
     N = slots.shape[0]
     shape = (N, cache.heads, cache.head_dim)
-    code = _dtype_code(k)
-    ks, vs = _rows("k", k, shape, k.dtype), _rows("v", v, shape, k.dtype)
-    _vector("slots", slots, (N,), torch.int64)
+    dev, code = _gpu("k", k), _dtype_code(k)
+    ks, vs = _rows("k", k, shape, k.dtype, dev), _rows("v", v, shape, k.dtype, dev)
+    _vector("slots", slots, (N,), torch.int64, dev)
+    _cache_device(cache, dev)
     return load_library().sv_cache_write(
         k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], slots.data_ptr(), N, cache.heads, cache.head_dim,
-        code, *cache.addresses, cache.num_pages, cache.page_size, cache.code, _address(status),
-        _raw_stream(k.device, stream))
+        code, *cache.addresses, cache.num_pages, cache.page_size, cache.code, _status_word(status, dev),
+        _raw_stream(dev, stream))
 
 
 def cache_write(k, v, slots, cache, *, status=None, stream=None):
@@ -703,13 +732,14 @@ def sv_cache_read(cache, slots, k_out, v_out, status=None, stream=None) -> int:
     f32 (any token and head strides); returns the host status code."""
     N = slots.shape[0]
     shape = (N, cache.heads, cache.head_dim)
-    code = _dtype_code(k_out)
-    ks, vs = _rows("k_out", k_out, shape, k_out.dtype), _rows("v_out", v_out, shape, k_out.dtype)
-    _vector("slots", slots, (N,), torch.int64)
+    dev, code = _gpu("k_out", k_out), _dtype_code(k_out)
+    ks, vs = _rows("k_out", k_out, shape, k_out.dtype, dev), _rows("v_out", v_out, shape, k_out.dtype, dev)
+    _vector("slots", slots, (N,), torch.int64, dev)
+    _cache_device(cache, dev)
     return load_library().sv_cache_read(
         *cache.addresses, cache.num_pages, cache.page_size, cache.code, slots.data_ptr(), N, cache.heads,
-        cache.head_dim, code, k_out.data_ptr(), ks[0], ks[1], v_out.data_ptr(), vs[0], vs[1], _address(status),
-        _raw_stream(k_out.device, stream))
+        cache.head_dim, code, k_out.data_ptr(), ks[0], ks[1], v_out.data_ptr(), vs[0], vs[1],
+        _status_word(status, dev), _raw_stream(dev, stream))
 
 
 def cache_read(cache, slots, *, dtype=torch.bfloat16, k_out=None, v_out=None, status=None, stream=None):
@@ -739,20 +769,21 @@ def sv_tree_attention(q, cache, page_table, ctx_lens, parents, scale, out, works
     if q.dim() != 4:
         raise ValueError("q must be [B, T, Hq, D]")
     B, T, Hq, D = q.shape
-    qs = _rows("q", q, (B, T, Hq, cache.head_dim), torch.bfloat16)
+    dev = _gpu("q", q)
+    qs = _rows("q", q, (B, T, Hq, cache.head_dim), torch.bfloat16, dev)
+    _cache_device(cache, dev)
     if page_table.dim() != 2:
         raise ValueError("page_table must be [B, max_pages]")
     width = page_table.shape[1]
-    _vector("page_table", page_table, (B, width), torch.int32)
-    _vector("ctx_lens", ctx_lens, (B,), torch.int32)
+    _vector("page_table", page_table, (B, width), torch.int32, dev)
+    _vector("ctx_lens", ctx_lens, (B,), torch.int32, dev)
     if parents is not None:
-        _vector("parents", parents, (B, T), torch.int32)
-    _vector("out", out, (B, T, Hq, D), torch.bfloat16)
+        _vector("parents", parents, (B, T), torch.int32, dev)
+    _vector("out", out, (B, T, Hq, D), torch.bfloat16, dev)
     return load_library().sv_tree_attention(
         q.data_ptr(), qs[0], qs[1], qs[2], *cache.addresses, cache.num_pages, cache.page_size, cache.code,
         page_table.data_ptr(), ctx_lens.data_ptr(), _address(parents), B, T, Hq, cache.heads, D, width, scale,
-        out.data_ptr(), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _raw_stream(q.device, stream))
+        out.data_ptr(), *_scratch(workspace, dev), _raw_stream(dev, stream))
 
 
 def tree_attention(q, cache, page_table, ctx_lens, parents=None, *, scale=None, out=None, workspace=None,
@@ -789,19 +820,19 @@ def spec_verify_tree(target, draft, draft_index, tokens, parents, uniforms, temp
     B, T, V = target.shape
     if draft.dtype != target.dtype:
         raise TypeError("draft must have the target's dtype")
+    dev = _gpu("target", target)
     for name, t in (("target", target), ("draft", draft)):
-        if not t.is_cuda or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous CUDA tensor")
+        if t.device != dev or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous CUDA tensor on {dev}")
     for name, t in (("draft_index", draft_index), ("tokens", tokens), ("parents", parents),
                     ("out_tokens", out_tokens), ("out_nodes", out_nodes)):
-        _vector(name, t, (B, T), torch.int32)
-    _vector("uniforms", uniforms, (B, T), torch.float32)
-    _vector("n_accepted", n_accepted, (B,), torch.int32)
+        _vector(name, t, (B, T), torch.int32, dev)
+    _vector("uniforms", uniforms, (B, T), torch.float32, dev)
+    _vector("n_accepted", n_accepted, (B,), torch.int32, dev)
     return load_library().spec_verify_tree(
         target.data_ptr(), draft.data_ptr(), draft_index.data_ptr(), tokens.data_ptr(), parents.data_ptr(),
         uniforms.data_ptr(), B, T, V, draft.shape[0], _dtype_code(target), temperature, out_tokens.data_ptr(),
-        out_nodes.data_ptr(), n_accepted.data_ptr(), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _raw_stream(target.device, stream))
+        out_nodes.data_ptr(), n_accepted.data_ptr(), *_scratch(workspace, dev), _raw_stream(dev, stream))
 
 
 def verify_tree(target, draft, draft_index, tokens, parents, uniforms, temperature, *, workspace=None, outs=None,
