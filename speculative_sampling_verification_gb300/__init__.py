@@ -559,7 +559,8 @@ def lmhead_stats(hidden, weight, tokens, temperature, *, workspace=None, stream=
 class PagedCache:
     """A paged key/value cache: k and v [num_pages, Hkv, page_size, D], bfloat16
     or float8_e4m3fn, the latter with fp32 scales [num_pages, Hkv, page_size].
-    Holds the tensors it is given; checks them once."""
+    Holds the tensors it is given; checks them once, so that they cannot be
+    exchanged for others (their contents may change)."""
 
     __slots__ = ("k", "v", "k_scale", "v_scale", "num_pages", "heads", "page_size", "head_dim", "code",
                  "device", "addresses")
@@ -568,11 +569,11 @@ class PagedCache:
         if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype:
             raise ValueError("k and v must be [num_pages, Hkv, page_size, D] of one type")
         if k.dtype == torch.bfloat16:
-            self.code = SV_BF16
+            code = SV_BF16
             if k_scale is not None or v_scale is not None:
                 raise ValueError("a bfloat16 cache has no scales")
         elif k.dtype == torch.float8_e4m3fn:
-            self.code = SV_E4M3
+            code = SV_E4M3
             for t in (k_scale, v_scale):
                 if t is None or t.shape != k.shape[:3] or t.dtype != torch.float32:
                     raise ValueError("a float8_e4m3fn cache needs fp32 scales [num_pages, Hkv, page_size]")
@@ -585,10 +586,18 @@ class PagedCache:
                 raise ValueError("a cache's tensors must be on one CUDA device")
             if not t.is_contiguous():
                 raise ValueError("a cache's tensors must be contiguous")
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.num_pages, self.heads, self.page_size, self.head_dim = k.shape
-        self.device = k.device
-        self.addresses = (k.data_ptr(), v.data_ptr(), _address(k_scale), _address(v_scale))
+        pages, heads, page_size, head_dim = k.shape
+        for name, value in (("k", k), ("v", v), ("k_scale", k_scale), ("v_scale", v_scale), ("num_pages", pages),
+                            ("heads", heads), ("page_size", page_size), ("head_dim", head_dim), ("code", code),
+                            ("device", k.device),
+                            ("addresses", (k.data_ptr(), v.data_ptr(), _address(k_scale), _address(v_scale)))):
+            object.__setattr__(self, name, value)
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"a PagedCache's {name} is fixed: make another PagedCache")
+
+    def __delattr__(self, name):
+        raise AttributeError(f"a PagedCache's {name} is fixed")
 
 
 def new_cache(num_pages, heads, page_size, head_dim, dtype=torch.bfloat16, device="cuda") -> PagedCache:

@@ -119,3 +119,14 @@ def test_a_workspace_with_gaps_is_refused(op, calls):
     with pytest.raises(ValueError, match="workspace"):
         call(fn, positional, {**keyword, "workspace": torch.zeros(1 << 17, dtype=torch.uint8)[::2]})
     assert not calls
+
+
+def test_a_caches_tensors_cannot_be_exchanged():
+    c = cache(F8)
+    for name in ("k", "v", "k_scale", "v_scale", "page_size", "addresses"):
+        before = getattr(c, name)
+        with pytest.raises(AttributeError):
+            setattr(c, name, before)
+        with pytest.raises(AttributeError):
+            delattr(c, name)
+        assert getattr(c, name) is before
