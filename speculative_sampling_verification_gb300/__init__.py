@@ -13,6 +13,7 @@ paper card, §4.2 and Algorithm 2).
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -620,6 +621,25 @@ def _raw_stream(device, stream):
     return torch._C._cuda_getCurrentRawStream(device.index)  # 2 us less than through a Stream object
 
 
+_CURRENT = contextlib.nullcontext()
+
+
+def _owned(stream):
+    """Memory that a call on `stream` allocates belongs to that stream: freed, it goes back to the
+    stream that may still use it, and what an earlier owner left pending there comes before."""
+    return _CURRENT if stream is None else torch.cuda.stream(stream)
+
+
+def _shared(stream, *outputs):
+    """Outputs that a call on `stream` allocated are for the current stream's use too: freed, they
+    wait for what it has queued."""
+    if stream is not None:
+        current = torch.cuda.current_stream(stream.device)
+        if current != stream:
+            for t in outputs:
+                t.record_stream(current)
+
+
 def _gpu(name, t):
     """The GPU that a call runs on: its first operand's."""
     if not t.is_cuda:
@@ -699,10 +719,15 @@ def qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions, *, eps=1e-6, int
     """Norms per head and rotation by position in one pass; allocates the
     outputs that are not given (pass q and k themselves to work in place) and
     returns (q_out, k_out)."""
-    if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    if k_out is None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    made = []
+    with _owned(stream):
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            made.append(q_out)
+        if k_out is None:
+            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+            made.append(k_out)
+    _shared(stream, *made)
     rc = sv_qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved, q_out, k_out,
                          stream=stream)
     if rc != SV_OK:
@@ -755,10 +780,15 @@ def cache_read(cache, slots, *, dtype=torch.bfloat16, k_out=None, v_out=None, st
     """The keys and values in `slots` (zeros for -1), as `dtype` where the
     outputs are not given; returns (k_out, v_out)."""
     shape = (slots.shape[0], cache.heads, cache.head_dim)
-    if k_out is None:
-        k_out = torch.empty(shape, dtype=dtype if v_out is None else v_out.dtype, device=cache.device)
-    if v_out is None:
-        v_out = torch.empty(shape, dtype=k_out.dtype, device=cache.device)
+    made = []
+    with _owned(stream):
+        if k_out is None:
+            k_out = torch.empty(shape, dtype=dtype if v_out is None else v_out.dtype, device=cache.device)
+            made.append(k_out)
+        if v_out is None:
+            v_out = torch.empty(shape, dtype=k_out.dtype, device=cache.device)
+            made.append(v_out)
+    _shared(stream, *made)
     rc = sv_cache_read(cache, slots, k_out, v_out, status, stream=stream)
     if rc != SV_OK:
         raise StatusError(rc, "sv_cache_read")
@@ -803,11 +833,15 @@ def tree_attention(q, cache, page_table, ctx_lens, parents=None, *, scale=None, 
     if q.dim() != 4:
         raise ValueError("q must be [B, T, Hq, D]")
     B, T, Hq, D = q.shape
-    if out is None:
-        out = torch.empty((B, T, Hq, D), dtype=torch.bfloat16, device=q.device)
-    if workspace is None:
-        n = sv_tree_attention_workspace_size(B, T, Hq, cache.heads, D, page_table.shape[-1], cache.page_size)
-        workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=q.device)
+    made = []
+    with _owned(stream):
+        if out is None:
+            out = torch.empty((B, T, Hq, D), dtype=torch.bfloat16, device=q.device)
+            made.append(out)
+        if workspace is None:
+            n = sv_tree_attention_workspace_size(B, T, Hq, cache.heads, D, page_table.shape[-1], cache.page_size)
+            workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=q.device)
+    _shared(stream, *made)
     rc = sv_tree_attention(q, cache, page_table, ctx_lens, parents, D ** -0.5 if scale is None else scale, out,
                            workspace, stream=stream)
     if rc != SV_OK:
@@ -853,12 +887,16 @@ def verify_tree(target, draft, draft_index, tokens, parents, uniforms, temperatu
         raise ValueError("target must be [B, T, V]")
     B, T, V = target.shape
     dev = target.device
-    if outs is None:
-        outs = (torch.empty(B, T, dtype=torch.int32, device=dev), torch.empty(B, T, dtype=torch.int32, device=dev),
-                torch.empty(B, dtype=torch.int32, device=dev))
-    if workspace is None:
-        n = sv_tree_workspace_size(B, T, V, _dtype_code(target))
-        workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
+    made = ()
+    with _owned(stream):
+        if outs is None:
+            outs = made = (torch.empty(B, T, dtype=torch.int32, device=dev),
+                           torch.empty(B, T, dtype=torch.int32, device=dev),
+                           torch.empty(B, dtype=torch.int32, device=dev))
+        if workspace is None:
+            n = sv_tree_workspace_size(B, T, V, _dtype_code(target))
+            workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
+    _shared(stream, *made)
     rc = spec_verify_tree(target, draft, draft_index, tokens, parents, uniforms, temperature, *outs, workspace,
                           stream=stream)
     if rc != SV_OK:

@@ -2,6 +2,8 @@
 word that the GPU cannot reach is refused before the library is called. Tensors here are
 CPU tensors that claim to lie on a GPU."""
 
+import contextlib
+
 import pytest
 import torch
 
@@ -130,3 +132,55 @@ def test_a_caches_tensors_cannot_be_exchanged():
         with pytest.raises(AttributeError):
             delattr(c, name)
         assert getattr(c, name) is before
+
+
+@pytest.mark.parametrize("op", OPS[:1] + OPS[2:])
+@pytest.mark.parametrize("own_stream", [False, True])
+def test_memory_made_for_another_stream_belongs_to_it(op, own_stream, calls, monkeypatch):
+    """A workspace that a call makes is freed when it returns, with the kernels still to run on `stream`:
+    from the current stream's memory, the next tensor made there could lie on it. Outputs are in use on
+    the current stream as well."""
+    class Stream:
+        device = torch.device("cuda:0")
+
+    current, other = Stream(), Stream()
+    active, made = [current], []
+
+    @contextlib.contextmanager
+    def on(stream):
+        active.append(stream)
+        yield
+        active.pop()
+
+    class Made(OnGpu):
+        def record_stream(self, stream):
+            self.users.append(stream)
+
+    empty = torch.empty
+
+    def allocate(*shape, device=None, **kw):
+        t = Made(empty(*shape, **kw))
+        t.owner, t.users = active[-1], []
+        made.append(t)
+        return t
+
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: active[-1])
+    monkeypatch.setattr(torch, "empty", allocate)
+    monkeypatch.setattr(sv, "sv_tree_attention_workspace_size", lambda *a: 4096)
+    monkeypatch.setattr(sv, "sv_tree_workspace_size", lambda *a: 4096)
+    fn, positional, _ = operands(op)
+    put = [OnGpu(t) for t in positional.values()]
+    stream = other if own_stream else None
+    kw = {"stream": stream}
+    if op == "verify":
+        out = sv.verify_tree(*put[:6], 1.0, **kw)
+    else:
+        out = fn(*put, **kw)
+    out = out if isinstance(out, tuple) else (out,)
+    assert len(calls) == 1 and made
+    for t in made:
+        assert t.owner is (other if own_stream else current)
+        is_output = any(t is o for o in out)
+        assert t.users == ([current] if own_stream and is_output else [])
+    assert len(made) == {"norm_rope": 2, "read": 2, "attention": 2, "verify": 4}[op]
