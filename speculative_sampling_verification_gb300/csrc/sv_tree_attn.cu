@@ -1221,6 +1221,9 @@ struct FewCfg {
 };
 
 constexpr float kNoScore = -1e30f;  // reference of a row that has seen no key
+// The least reference of the values' scales (2^-119). Never 0: a NaN scale raises no reference, and
+// what it put into O must outlast the reference's product at the item's end.
+constexpr unsigned kLeastExponent = 8;
 
 template <int RP>
 struct FewTail {
@@ -1601,7 +1604,7 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
       const float* qc = f.qc[item & 1] + row0;
       const float* mref = f.mref[s] + row0;
       if (st < RP) f.mref[s][st] = st < nrows ? kNoScore : 0.0f;
-      if (st == 0) f.vref[s] = 0.0f;
+      if (st == 0) f.vref[s] = __int_as_float(kLeastExponent << 23);
       unsigned bad = seq_ok ? 0u : (unsigned)SV_DEV_PAGE_RANGE;
       if (tail && st < a.T) par[st] = a.parents ? a.parents[(long long)w.b * a.T + st] : st - 1;
       // The next item's first needs on their way to L2 while this one is worked on.
@@ -1727,8 +1730,8 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
 #pragma unroll
             for (int k = 0; k < 4; ++k) vtop = fmaxf(vtop, fmaxf(f.wvs[s][0][k], f.wvs[s][1][k]));
             const unsigned ex = (__float_as_uint(vtop) + 0x7fffffu) >> 23;  // power of two not below it
-            vnew = fmaxf(vold, vtop > 0.0f ? __int_as_float(max(8u, min(250u, ex)) << 23) : 0.0f);
-            if (vnew > vold) g = vold / vnew;
+            vnew = fmaxf(vold, __int_as_float(max(kLeastExponent, min(250u, ex)) << 23));
+            g = vold / vnew;
           }
           if (st < RP) {
             const float top = fmaxf(fmaxf(f.wmax[s][0][st], f.wmax[s][1][st]),
@@ -1767,10 +1770,7 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
         }
         // Weights, their sums, and P^T: the half's part of this key's 128 bytes.
         float vs = 1.0f;
-        if (F8) {
-          const float vr = f.vref[s];
-          vs = vr > 0.0f ? vs_now * (C::kLift * __fdividef(1.0f, vr)) : isnan(vs_now) ? vs_now : 0.0f;
-        }
+        if (F8) vs = vs_now * (C::kLift * __fdividef(1.0f, f.vref[s]));
         constexpr int kWords = C::HN / (F8 ? 4 : 2);
         uint32_t words[kWords];
 #pragma unroll
@@ -1918,9 +1918,8 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
         } else {
           tmem_ld_1x2(col, 128, &o0, &o1);
         }
-        // A stream that had no tile, or a row that it gave nothing, has factor 0.
-        float v = fin.x == 0.0f ? 0.0f : o0 * fin.x;
-        if (fin.y != 0.0f) v = __fmaf_rn(o1, fin.y, v);
+        float v = o0 * fin.x;
+        if (n > 1) v = __fmaf_rn(o1, fin.y, v);  // (else the second stream had no tile)
         if (wt >= a.D) continue;
         if (badv) {  // NaN and infinities of the nodes the row attends
           for (int k = 0; k < a.T; ++k) {
