@@ -487,8 +487,8 @@ __device__ __noinline__ void join_parts(const TcArgs& x, TcTail& t, const Walk<K
       top = nt;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        if (ml[k].x == -INFINITY) continue;
-        const float f = ex2_fast((ml[k].x - top) * x.join_c);
+        // (A part of NaN scores alone has the maximum -inf too: its sum, NaN, still counts.)
+        const float f = ml[k].x == -INFINITY ? 0.0f : ex2_fast((ml[k].x - top) * x.join_c);
         l = fmaf(ml[k].y, f, l);
         acc.x = fmaf(o[k].x, f, acc.x);
         acc.y = fmaf(o[k].y, f, acc.y);
@@ -1069,7 +1069,7 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
             tmem_ld8(tmem + lanes + C::kO1 + col, u);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-              v[j] = (f0 > 0.0f || isnan(f0) ? v[j] * f0 : 0.0f) + (f1 > 0.0f || isnan(f1) ? u[j] * f1 : 0.0f);
+              v[j] = v[j] * f0 + (n > 1 ? u[j] * f1 : 0.0f);
           }
           if (badv && have) {  // NaN and infinities of the nodes this row attends
 #pragma unroll 1

@@ -47,3 +47,22 @@ def test_a_nan_value_alone_in_its_tile(G, D, cdt, bad, ctx):
     else:  # only the value's own channel
         assert bool(out[0][..., 4:].isfinite().all()) and bool(out[0][..., :3].isfinite().all())
     assert torch.equal(out[1], clean[1])
+
+
+@pytest.mark.parametrize("G,D", KINDS)
+@pytest.mark.parametrize("cdt", [BF, F8])
+@pytest.mark.parametrize("ctx", [0, 64, 128, 384])
+def test_a_nan_key_alone_in_its_tile(G, D, cdt, ctx):
+    """The same with the new token's key: its stream or part has NaN scores only, and no maximum."""
+    P, Hkv = 16, 2
+    args = base.make(2, 1, Hkv * G, Hkv, D, P, [ctx, 200], cdt, 8 + ctx + G)
+    q, cache, table, lens, par = args
+    clean, _ = base.run(args, 0.09)
+    x = torch.ones(1, Hkv, D, device=DEV)
+    x[:, :, 3] = float("nan")
+    slot = table[0, ctx // P].long().view(1) * P + ctx % P
+    sv.cache_write(x, torch.ones(1, Hkv, D, device=DEV), slot, cache)
+    out, status = base.run(args, 0.09)
+    assert status == 0
+    assert bool(out[0].isnan().all())
+    assert torch.equal(out[1], clean[1])
