@@ -1229,6 +1229,7 @@ template <int RP>
 struct FewTail {
   TcTail t;
   unsigned long long anc[2][2][64];  // [item parity][stream][node]: ancestors and itself
+  unsigned long long o_done;         // the item's products are complete
   unsigned long long o_read;         // every softmax warp has read the item's O
   // Arrays that are read four values at a time lie on 16-byte boundaries.
   alignas(16) float mref[2][RP];     // [stream] references, powers of two
@@ -1339,6 +1340,7 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
       mbar_init(smem_u32(&t.p_ready[i]), kSoft / 2);
       mbar_init(smem_u32(&t.pv_done[i]), 1);
     }
+    mbar_init(smem_u32(&f.o_done), 1);
     mbar_init(smem_u32(&f.o_read), kSoft);
     t.abort = 0;
     t.bad[0] = t.bad[1] = t.badv[0] = t.badv[1] = 0;
@@ -1478,6 +1480,7 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
         commit(lead, smem_u32(&t.pv_done[s]));
         commit(lead, smem_u32(&t.empty[e % C::kSlots]));
       }
+      if (ok) commit(lead, smem_u32(&f.o_done));
       entry0 += 2u * n;
     }
   } else if (warp < kSoft) {
@@ -1896,7 +1899,9 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
         f.fin[r] = make_float4((F8 ? g0 * (f.vref[0] / C::kLift) : g0), (F8 ? g1 * (f.vref[1] / C::kLift) : g1),
                                whole ? inv : at_fault ? __int_as_float(0x7fc00000) : m, sum);
       }
-      if (any) wait(&t.pv_done[s], (scount - 1) & 1);
+      // (pv_done's parity would not do here: a tile's S^T is issued before the product of the
+      // stream's tile before it, so that two of them may be outstanding.)
+      wait(&f.o_done, item & 1);
       fence_before();
       named_sync(3, 32 * kSoft);
       fence_after();

@@ -171,3 +171,18 @@ def test_items_of_one_tile(T, Hq, Hkv, D, cdt):
     check(args, D ** -0.5, out)
     for _ in range(3):
         assert torch.equal(base.run(args, D ** -0.5)[0], out)
+
+
+@pytest.mark.parametrize("T,Hq,D", [(1, 8, 128), (4, 8, 128), (16, 2, 128), (9, 8, 128), (20, 8, 128), (70, 8, 128),
+                                    (9, 8, 64), (9, 8, 256)])
+@pytest.mark.parametrize("cdt", [BF, F8])
+@pytest.mark.parametrize("ctx", [20000, 32700, 32768, 100001])
+def test_one_sequence_of_many_tiles_a_range(T, Hq, D, cdt, ctx):
+    """Two heads of one long sequence: ranges of three tiles and more, whose values arrive late,
+    and nothing but full tiles in most of them."""
+    args = base.make(1, T, Hq, 2, D, 64, [ctx], cdt, T + D + 4)
+    out, status = base.run(args, D ** -0.5)
+    assert status == 0
+    check(args, D ** -0.5, out)
+    for _ in range(10):
+        assert torch.equal(base.run(args, D ** -0.5)[0], out)
