@@ -497,9 +497,11 @@ size_t sv_tree_attention_workspace_size(int B, int T, int Hq, int Hkv, int D, in
  *   workspace   device, sv_tree_attention_workspace_size() bytes, 256-byte aligned;
  *               its first 4 bytes are the device status word
  * T = 1 is the ordinary decoding step. Sums, maxima and the running output are
- * fp32. For their product with the values the weights are rounded to bf16; with an
- * e4m3 cache and few rows (T * Hq/Hkv <= 40, D <= 128) q enters as two e4m3 pieces and
- * the weights as three. Codes are expected finite, as sv_cache_write stores them. A
+ * fp32. For their product with the values the weights are rounded to bf16 (2^-8 of
+ * each). With an e4m3 cache and few rows (T * Hq/Hkv <= 40, D <= 128) q enters as two e4m3
+ * pieces (off by 2^-19 of a row's largest value at most), and a weight times its value's
+ * scale as three: off by 2^-11 of itself, or by 2^-24 of the row's largest such
+ * product. Codes and scales are expected as sv_cache_write stores them (finite codes, scales up to 2^100). A
  * sequence with a malformed tree (SV_DEV_TREE), or whose context or
  * needed pages lie outside the table or the cache (SV_DEV_PAGE_RANGE), gets NaN
  * outputs; the others are unaffected. What masked positions hold, NaN included,

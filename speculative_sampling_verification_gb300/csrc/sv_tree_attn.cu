@@ -1174,19 +1174,24 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
 // rule): the operands change places. S^T = K Q^T has the tile's 128 keys as the M of the product and the
 // rows as its N, so the tensor cores and the softmax work on the rows that exist.
 // One thread a key holds that key's scores of all rows, its scales and its
-// mask; the maximum of a row is not needed, only a reference m that no score
-// exceeds by more than 2^8 (e4m3: 2^4): a vote of the warpgroup finds the rare tile that
-// does, and only then are maxima taken across the threads and O rescaled. P^T goes to
-// shared memory as the other operand of O^T = V^T P^T (M = 128 channels of the
-// head). A row's sum is kept by each thread for its keys and joined at the item's end.
+// mask; the maximum of a row is not needed, only a reference m that no score (e4m3: no
+// score with its value's scale, s + log2 v) exceeds by more than 2^8 (e4m3: 2^4): a vote of the
+// stream's threads finds the rare tile that does, and only then are maxima taken across the
+// threads and O rescaled. P^T goes to shared memory as the other operand of O^T = V^T P^T
+// (M = 128 channels of the head). A row's sum is kept by each thread for its keys and joined at the item's end.
 //
 // An e4m3 cache feeds the tensor cores as it is (kind::f8f6f4), with no pass to
 // convert it: Q and P enter as sums of e4m3 pieces. Q, scaled by a power of two to
 // (224, 448], is hi + lo, exact for elements above 2^-10 of the row's largest and off by
-// 2^-19 of that at most below; both multiply into the same columns. P, times 2^4 and the value's
-// scale over a power of two not below any scale seen, is p1 + p2/16 + p3/256 with columns of
-// O for each piece: off by at most 2^-12 of itself or, for small weights, 2^-22 of the
-// reference weight. A bf16 cache uses bf16 operands, P rounded once (2^-8).
+// 2^-19 of that at most below; both multiply into the same columns. A key's part of O is its
+// weight times its value's scale; P is that, relative to the reference, times 2^4, as
+// p1 + p2/32 + p3/1024 with columns of O for each piece: off by at most 2^-11 of itself (a
+// half's rounding) or, for small parts, 2^-24 of the reference. The reference is the row's largest
+// part, not its largest weight: with a reference for the weights and one for the scales,
+// one row of large values that weighed nothing drove every other part below what three
+// pieces hold. The sums are relative to the same reference: 2^(s - m) stays in range for
+// scales of 2^-108 (the least that sv_cache_write stores) to 2^100. A bf16 cache uses bf16
+// operands, P rounded once (2^-8).
 //
 // 64 sequences of 9 nodes, 32/8 heads of 128, contexts to 8192, e4m3: 206 us, 3.1 TB/s, with
 // 54 % of the issue slots active, the tensor pipe 13 % and the memory 41 %: the latency of
@@ -1221,9 +1226,9 @@ struct FewCfg {
 };
 
 constexpr float kNoScore = -1e30f;  // reference of a row that has seen no key
-// The least reference of the values' scales (2^-119). Never 0: a NaN scale raises no reference, and
-// what it put into O must outlast the reference's product at the item's end.
-constexpr unsigned kLeastExponent = 8;
+// Values' scales below 2^-100 (an unwritten slot's 0, NaN) count as this in the references, so
+// that the sums of weights stay finite.
+constexpr float kLeastScale = 7.888609052210118e-31f;
 
 template <int RP>
 struct FewTail {
@@ -1236,8 +1241,7 @@ struct FewTail {
   alignas(16) float fac[2][RP];      // [stream] factors of a rescaling
   alignas(16) float qc[2][RP];       // [item parity] c over the row's scale of Q
   float4 fin[RP];
-  float wmax[2][4][RP], wsum[2][4][RP], wvs[2][2][4];
-  float vref[2];
+  float wmax[2][4][RP], wsum[2][4][RP];
   int row_out[RP];                   // a row's place in a token block of the output: node Hq + head of the group
 };
 
@@ -1247,13 +1251,6 @@ constexpr int few_smem() {
   static_assert(sizeof(FewTail<RP>) <= C::kTailBytes, "tail");
   static_assert(C::HR % 4 == 0 && C::kQBytes % 2048 == 0, "rows of four values, blocks of 1024 bytes");
   return 1024 + C::kQBytes + 4 * C::kPBytes + C::kSlots * C::kSlot + (int)sizeof(FewTail<RP>);
-}
-
-SV_DEVINL float redux_max(float v) {
-  // Order-preserving integers: the warp's integer maximum.
-  const int b = __float_as_int(v);
-  const int m = __reduce_max_sync(0xffffffffu, b ^ ((b >> 31) & 0x7fffffff));
-  return __int_as_float(m ^ ((m >> 31) & 0x7fffffff));
 }
 
 SV_DEVINL uint32_t half2_bits(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
@@ -1606,8 +1603,7 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
       unsigned long long* anc = f.anc[item & 1][s];
       const float* qc = f.qc[item & 1] + row0;
       const float* mref = f.mref[s] + row0;
-      if (st < RP) f.mref[s][st] = st < nrows ? kNoScore : 0.0f;
-      if (st == 0) f.vref[s] = __int_as_float(kLeastExponent << 23);
+      if (st < RP) f.mref[s][st] = st < nrows ? kNoScore : -kNoScore;  // (no score of 0 exceeds that)
       unsigned bad = seq_ok ? 0u : (unsigned)SV_DEV_PAGE_RANGE;
       if (tail && st < a.T) par[st] = a.parents ? a.parents[(long long)w.b * a.T + st] : st - 1;
       // The next item's first needs on their way to L2 while this one is worked on.
@@ -1661,7 +1657,8 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
         if (seq_ok && (nd < 0 || (nd < a.T && par[nd] != -2)) && (id < 0 || id >= a.num_pages))
           bad |= SV_DEV_PAGE_RANGE;
         const float kc = F8 ? ksc : 1.0f;
-        const float vs_now = see != 0 ? vsc : 0.0f;  // masked places may hold anything
+        const float vs = F8 ? vsc * C::kLift : 1.0f;
+        const float lv = F8 ? __log2f(fmaxf(vsc, kLeastScale)) : 0.0f;
         id = id1;
         if (F8) {
           ksc = ksc1;
@@ -1703,8 +1700,7 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
         float over[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int r = 0; r < HR; ++r) over[r & 3] = fmaxf(over[r & 3], y[r]);
-        bool up = fmaxf(fmaxf(over[0], over[1]), fmaxf(over[2], over[3])) > C::kGrow;
-        if (F8) up = up || vs_now > f.vref[s];
+        const bool up = fmaxf(fmaxf(over[0], over[1]), fmaxf(over[2], over[3])) > C::kGrow - lv;
         const bool raise = named_any(1 + s, 256, up);
         // (This tile's P buffer is free: its S^T was issued, and announced, after the
         // product that read the buffer four tiles ago.)
@@ -1718,24 +1714,10 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
           {
             float v[HR];
 #pragma unroll
-            for (int r = 0; r < HR; ++r) v[r] = y[r];
+            for (int r = 0; r < HR; ++r) v[r] = y[r] + lv;
             halve<true, HR, 16>(v, lane, 0, HR, f.wmax[s][q] + row0);
           }
-          if (F8) {  // (both halves have the same scales but where a mask parts them)
-            const float v = redux_max(vs_now > 0.0f ? vs_now : 0.0f);
-            if (lane == 0) f.wvs[s][h][q] = v;
-          }
           named_sync(1 + s, 256);
-          float g = 1.0f, vnew = 0.0f;
-          if (F8) {
-            const float vold = f.vref[s];
-            float vtop = 0.0f;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) vtop = fmaxf(vtop, fmaxf(f.wvs[s][0][k], f.wvs[s][1][k]));
-            const unsigned ex = (__float_as_uint(vtop) + 0x7fffffu) >> 23;  // power of two not below it
-            vnew = fmaxf(vold, __int_as_float(max(kLeastExponent, min(250u, ex)) << 23));
-            g = vold / vnew;
-          }
           if (st < RP) {
             const float top = fmaxf(fmaxf(f.wmax[s][0][st], f.wmax[s][1][st]),
                                     fmaxf(f.wmax[s][2][st], f.wmax[s][3][st]));
@@ -1748,7 +1730,6 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
             f.fac[s][st] = fr;
           }
           named_sync(1 + s, 256);
-          if (st == 0 && F8) f.vref[s] = vnew;
           const float* fac = f.fac[s] + row0;
 #pragma unroll
           for (int r = 0; r < HR; ++r) {
@@ -1763,17 +1744,14 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
               for (int pc = 0; pc < (F8 ? 3 : 1); ++pc) {
                 float v[4];
                 tmem_ld4(obase + pc * HR + r, v);
-                tmem_st4(obase + pc * HR + r, v[0] * (f4.x * g), v[1] * (f4.y * g), v[2] * (f4.z * g),
-                         v[3] * (f4.w * g));
+                tmem_st4(obase + pc * HR + r, v[0] * f4.x, v[1] * f4.y, v[2] * f4.z, v[3] * f4.w);
               }
             }
             tmem_wait_st();
           }
-          named_sync(1 + s, 256);  // fac and vref have been read and written
+          named_sync(1 + s, 256);  // fac has been read
         }
         // Weights, their sums, and P^T: the half's part of this key's 128 bytes.
-        float vs = 1.0f;
-        if (F8) vs = vs_now * (C::kLift * __fdividef(1.0f, f.vref[s]));
         constexpr int kWords = C::HN / (F8 ? 4 : 2);
         uint32_t words[kWords];
 #pragma unroll
@@ -1796,15 +1774,15 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
 #pragma unroll
               for (int j = 0; j < 4; ++j) p[j] = see >> (r + j) & 1u ? p[j] : 0.0f;
             }
-            const __half2 sixteen = __half2half2(__ushort_as_half(0x4c00));
+            const __half2 step = __half2half2(__ushort_as_half(0x5000));  // 32
             uint32_t c[3][2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               const __half2 w0 = __floats2half2_rn(p[2 * j], p[2 * j + 1]);
               c[0][j] = half2_to_e4m3(w0);
-              const __half2 r1 = __hmul2(__hsub2(w0, e4m3_to_half2(c[0][j])), sixteen);
+              const __half2 r1 = __hmul2(__hsub2(w0, e4m3_to_half2(c[0][j])), step);
               c[1][j] = half2_to_e4m3(r1);
-              const __half2 r2 = __hmul2(__hsub2(r1, e4m3_to_half2(c[1][j])), sixteen);
+              const __half2 r2 = __hmul2(__hsub2(r1, e4m3_to_half2(c[1][j])), step);
               c[2][j] = half2_to_e4m3(r2);
             }
             words[r / 4] = __byte_perm(c[0][0], c[0][1], 0x5410);
@@ -1896,7 +1874,7 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
         // Factors of the streams' O: for a whole item with the division by the sum.
         float inv = 1.0f;
         if (whole) inv = at_fault ? __int_as_float(0x7fc00000) : sum == 0.0f ? 0.0f : 1.0f / sum;
-        f.fin[r] = make_float4((F8 ? g0 * (f.vref[0] / C::kLift) : g0), (F8 ? g1 * (f.vref[1] / C::kLift) : g1),
+        f.fin[r] = make_float4(g0 / C::kLift, g1 / C::kLift,
                                whole ? inv : at_fault ? __int_as_float(0x7fc00000) : m, sum);
       }
       // (pv_done's parity would not do here: a tile's S^T is issued before the product of the
@@ -1918,8 +1896,8 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
         if (F8) {
           float u[6];
           tmem_ld_3x2(col, HR, 128, u);
-          o0 = __fmaf_rn(__fmaf_rn(u[2], 0.0625f, u[1]), 0.0625f, u[0]);
-          o1 = __fmaf_rn(__fmaf_rn(u[5], 0.0625f, u[4]), 0.0625f, u[3]);
+          o0 = __fmaf_rn(__fmaf_rn(u[2], 0.03125f, u[1]), 0.03125f, u[0]);
+          o1 = __fmaf_rn(__fmaf_rn(u[5], 0.03125f, u[4]), 0.03125f, u[3]);
         } else {
           tmem_ld_1x2(col, 128, &o0, &o1);
         }
