@@ -36,6 +36,7 @@
 // slots are active on average, 74 % on the busiest SM. 512 threads a CTA, two an SM: 162.
 // CTAs of 256 an SM, before the rows' statistics took one pass: three 193, four 164, five 169. One tree of nine nodes over 32000 tokens: 34 us.
 #include <cfloat>
+#include <climits>
 #include <cmath>
 #include <cstdint>
 #include <algorithm>
@@ -361,7 +362,10 @@ SV_DEVINL double token_ratio(float lq, float lp, ff c, const Args& a, const floa
 }
 
 // The token at which the running sum of the region's weights passes `target`,
-// or the region's last token of positive weight.
+// or the region's last token of positive weight. The lanes' running sums are of
+// one order each, so that rounding alone may lift a lane without weight over a target at
+// the border before it: then the token before the border is drawn, the one after where
+// the region has none before.
 template <int DT, bool VEC>
 SV_DEVINL int region_draw(const Mix& x, int begin, int end, ff target, int lane, const Args& a,
                           const float2* tab, const float2* tab1k) {
@@ -370,6 +374,7 @@ SV_DEVINL int region_draw(const Mix& x, int begin, int end, ff target, int lane,
 #pragma unroll 1
   for (int e0 = begin; e0 < end; e0 += kStep) {
     const int e = e0 + lane * 8;
+    const int earlier = last;
     ff2 w[4];
     mix8<DT, VEC>(x, e, end, a, tab, tab1k, w);
     ff mine = {0.0f, 0.0f};
@@ -389,19 +394,21 @@ SV_DEVINL int region_draw(const Mix& x, int begin, int end, ff target, int lane,
     const unsigned hit = __ballot_sync(0xffffffffu, ff_gt(ff_add(before, incl), target));
     if (hit) {
       const int owner = __ffs(hit) - 1;
-      int token = e;
-      if (lane == owner) {
-        ff run = ff_add(before, ff_sub(incl, mine));
-        token = -1;
+      int token = -1, first = INT_MAX;
+      ff run = ff_add(before, ff_sub(incl, mine));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const ff v = i & 1 ? ff{w[i >> 1].hi.y, w[i >> 1].lo.y} : ff{w[i >> 1].hi.x, w[i >> 1].lo.x};
-          run = ff_add(run, v);
-          if (token < 0 && v.hi > 0.0f && ff_gt(run, target)) token = e + i;
-        }
-        if (token < 0) token = last;  // the sums' rounding hid the step
+      for (int i = 0; i < 8; ++i) {
+        const ff v = i & 1 ? ff{w[i >> 1].hi.y, w[i >> 1].lo.y} : ff{w[i >> 1].hi.x, w[i >> 1].lo.x};
+        run = ff_add(run, v);
+        if (v.hi > 0.0f) first = min(first, e + i);
+        if (token < 0 && v.hi > 0.0f && ff_gt(run, target)) token = e + i;
       }
-      return __shfl_sync(0xffffffffu, token, owner);
+      token = __shfl_sync(0xffffffffu, token, owner);
+      if (token >= 0) return token;
+      token = __reduce_max_sync(0xffffffffu, lane <= owner ? last : earlier);
+      if (token >= 0) return token;
+      first = __reduce_min_sync(0xffffffffu, lane > owner ? first : INT_MAX);
+      if (first < INT_MAX) return first;
     }
     before = ff_add(before, {__shfl_sync(0xffffffffu, incl.hi, 31), __shfl_sync(0xffffffffu, incl.lo, 31)});
   }
