@@ -431,6 +431,7 @@ int sv_lmhead_stats(const void* hidden, const void* weight, const int32_t* token
  *   q_weight, k_weight  device, [D] dtype, or NULL for ones
  *   inv_freq      device, [R/2] fp32
  *   positions     device, [N] int32
+ *   N             N * ceil((Hq + Hkv) / 16) < 2^31
  *   D, R          1 <= D <= 1024, 0 <= R <= D, R even
  *   q_out, k_out  device, written; strides as above; may be q and k themselves
  *                 (same pointer and strides), must not overlap them otherwise
@@ -452,6 +453,7 @@ int sv_qk_norm_rope(const void* q, int64_t q_stride_n, int64_t q_stride_h, const
  *
  * Writes N tokens' keys and values into their slots:
  *   k, v     device, [N, Hkv, D], dtype (SV_BF16 or SV_F32), strides in elements
+ *   N        N * Hkv < 2^32
  *   slots    device, [N] int64; -1 writes nothing. No slot may occur twice.
  *   status   device word, may be NULL: SV_DEV_SLOT_RANGE is OR-ed into it when a
  *            slot lies outside the cache (that token is not written). The

@@ -670,7 +670,7 @@ int run_cache(CacheArgs a, long long num_pages, int dtype, int cache_dtype, void
   if (a.N < 0 || a.H < 1 || a.H > 1024 || a.D < 1 || a.D > kHeadDimMax || a.P < 1 || num_pages < 1)
     return SV_ERR_SHAPE;
   // N * H rows fill at most 2^31 - 1 blocks; the cache stays below 2^62 elements.
-  if ((long long)a.N * a.H > (1ll << 32) || num_pages > (1ll << 31) || a.P > (1 << 20)) return SV_ERR_SHAPE;
+  if ((long long)a.N * a.H >= (1ll << 32) || num_pages > (1ll << 31) || a.P > (1 << 20)) return SV_ERR_SHAPE;
   if (a.N == 0) return SV_OK;
   const void* rows_k = READ ? a.ko : a.k;
   const void* rows_v = READ ? a.vo : a.v;
@@ -714,6 +714,8 @@ int sv_qk_norm_rope(const void* q, int64_t q_stride_n, int64_t q_stride_h, const
   if (N < 0 || Hq < 0 || Hkv < 0 || Hq + Hkv < 1 || Hq > 1024 || Hkv > 1024 || D < 1 ||
       D > sv::kHeadDimMax || R < 0 || R > D || R % 2 != 0 || !(eps >= 0.0f) || std::isinf(eps))
     return SV_ERR_SHAPE;
+  // At most 2^31 - 1 blocks: odd sizes take kAnyHeads heads of a token a block, the others no fewer rows.
+  if ((long long)N * ((Hq + Hkv + kAnyHeads - 1) / kAnyHeads) >= (1ll << 31)) return SV_ERR_SHAPE;
   if (N == 0) return SV_OK;
   if ((Hq && (!q || !q_out)) || (Hkv && (!k || !k_out)) || (R && !inv_freq) || !positions)
     return SV_ERR_NULL;

@@ -8,6 +8,7 @@ import pytest
 import torch
 
 import speculative_sampling_verification_gb300 as sv
+from speculative_sampling_verification_gb300._build import build_library
 
 F8 = torch.float8_e4m3fn
 
@@ -184,3 +185,20 @@ def test_memory_made_for_another_stream_belongs_to_it(op, own_stream, calls, mon
         is_output = any(t is o for o in out)
         assert t.users == ([current] if own_stream and is_output else [])
     assert len(made) == {"norm_rope": 2, "read": 2, "attention": 2, "verify": 4}[op]
+
+
+def test_calls_of_more_blocks_than_a_grid_has_are_refused():
+    """Norm: one block for 16 heads of a token; the count wrapped round in 32 bits before, so that
+    2^26 + 1 tokens of 1024 heads launched 64 blocks. No pointer here is followed."""
+    lib, P = sv.load_library(build_library()), 1 << 20
+
+    def norm(N, Hq, Hkv):
+        return lib.sv_qk_norm_rope(P, 1, 1, P, 1, 1, None, None, P, P, N, Hq, Hkv, 1, 0, sv.SV_BF16, 1e-6, 0, P, 1, 1,
+                                   P, 1, 1, None)
+
+    def write(N, H):
+        return lib.sv_cache_write(P, 1, 1, P, 1, 1, P, N, H, 1, sv.SV_BF16, P, P, None, None, 4, 16, sv.SV_BF16, None,
+                                  None)
+
+    assert norm((1 << 26) + 1, 1000, 24) == 2 and norm(1 << 30, 16, 1) == 2
+    assert write(1 << 22, 1024) == 2 and write((1 << 31) - 1, 3) == 2
