@@ -154,6 +154,25 @@ def load_library(path: str | None = None, build: bool = False) -> ctypes.CDLL:
     return lib
 
 
+_CURRENT = contextlib.nullcontext()
+
+
+def _owned(stream):
+    """Memory that a call on `stream` allocates belongs to that stream: freed, it goes back to the
+    stream that may still use it, and what an earlier owner left pending there comes before."""
+    return _CURRENT if stream is None else torch.cuda.stream(stream)
+
+
+def _shared(stream, *outputs):
+    """Outputs that a call on `stream` allocated are for the current stream's use too: freed, they
+    wait for what it has queued."""
+    if stream is not None:
+        current = torch.cuda.current_stream(stream.device)
+        if current != stream:
+            for t in outputs:
+                t.record_stream(current)
+
+
 def _dtype_code(t: torch.Tensor) -> int:
     if t.dtype == torch.bfloat16:
         return SV_BF16
@@ -323,19 +342,23 @@ def verify(target, draft, tokens, uniforms, temperature, *, workspace=None, debu
     """Allocate outputs (and a workspace if none is given) with torch, run one
     verification step, and return (out_tokens [B,K+1] int32, n_accepted [B]
     int32), plus a dict of intermediate values when `debug` is set."""
-    if tokens.dtype == torch.int64:
-        tokens = tokens.to(torch.int32)
-    B, K, V, dt = _check(target, draft, tokens, uniforms)
-    dev = target.device
-    out = torch.empty(B, K + 1, dtype=torch.int32, device=dev)
-    nacc = torch.empty(B, dtype=torch.int32, device=dev)
-    ws = workspace if workspace is not None else new_workspace(B, K, V, dt, dev)
+    with _owned(stream):
+        if tokens.dtype == torch.int64:
+            tokens = tokens.to(torch.int32)
+        B, K, V, dt = _check(target, draft, tokens, uniforms)
+        dev = target.device
+        out = torch.empty(B, K + 1, dtype=torch.int32, device=dev)
+        nacc = torch.empty(B, dtype=torch.int32, device=dev)
+        ws = workspace if workspace is not None else new_workspace(B, K, V, dt, dev)
+        if debug:
+            lse = torch.empty(B, 2 * K + 1, dtype=torch.float64, device=dev)
+            thr = torch.empty(B, K, dtype=torch.float64, device=dev)
+            prob = torch.empty(B, dtype=torch.float64, device=dev)
+            rmax = torch.empty(B, 2 * K + 1, dtype=torch.float64, device=dev)
+            ratio = torch.empty(B, K, dtype=torch.float64, device=dev)
+    _shared(stream, out, nacc)
     if debug:
-        lse = torch.empty(B, 2 * K + 1, dtype=torch.float64, device=dev)
-        thr = torch.empty(B, K, dtype=torch.float64, device=dev)
-        prob = torch.empty(B, dtype=torch.float64, device=dev)
-        rmax = torch.empty(B, 2 * K + 1, dtype=torch.float64, device=dev)
-        ratio = torch.empty(B, K, dtype=torch.float64, device=dev)
+        _shared(stream, lse, thr, prob, rmax, ratio, ws)
         rc = spec_verify_debug(target, draft, tokens, uniforms, temperature, out, nacc, ws,
                                lse, thr, prob, rmax, ratio, stream=stream)
     else:
@@ -368,16 +391,18 @@ def verify_topk(target, draft, tokens, uniforms, temperature, top_k, *, workspac
                 stream=None):
     """Allocate outputs (and a workspace if none is given) and run top-k
     filtered verification; returns (out_tokens [B, K+1] int32, n_accepted [B] int32)."""
-    if tokens.dtype == torch.int64:
-        tokens = tokens.to(torch.int32)
-    B, K, V, dt = _check(target, draft, tokens, uniforms)
-    dev = target.device
-    out = torch.empty(B, K + 1, dtype=torch.int32, device=dev)
-    nacc = torch.empty(B, dtype=torch.int32, device=dev)
-    ws = workspace
-    if ws is None:
-        n = sv_topk_workspace_size(B, K, V, dt, int(top_k))
-        ws = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
+    with _owned(stream):
+        if tokens.dtype == torch.int64:
+            tokens = tokens.to(torch.int32)
+        B, K, V, dt = _check(target, draft, tokens, uniforms)
+        dev = target.device
+        out = torch.empty(B, K + 1, dtype=torch.int32, device=dev)
+        nacc = torch.empty(B, dtype=torch.int32, device=dev)
+        ws = workspace
+        if ws is None:
+            n = sv_topk_workspace_size(B, K, V, dt, int(top_k))
+            ws = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
+    _shared(stream, out, nacc)
     rc = spec_verify_topk(target, draft, tokens, uniforms, temperature, top_k, out, nacc, ws,
                           stream=stream)
     if rc != SV_OK:
@@ -405,17 +430,19 @@ def verify_topp(target, draft, tokens, uniforms, temperature, top_p, *, workspac
     """Allocate outputs (and a workspace if none is given) and run nucleus
     filtered verification; returns (out_tokens [B, K+1] int32, n_accepted [B]
     int32, kept_counts [B, 2K+1] int32)."""
-    if tokens.dtype == torch.int64:
-        tokens = tokens.to(torch.int32)
-    B, K, V, dt = _check(target, draft, tokens, uniforms)
-    dev = target.device
-    out = torch.empty(B, K + 1, dtype=torch.int32, device=dev)
-    nacc = torch.empty(B, dtype=torch.int32, device=dev)
-    kept = torch.empty(B, 2 * K + 1, dtype=torch.int32, device=dev)
-    ws = workspace
-    if ws is None:
-        n = sv_topp_workspace_size(B, K, V, dt)
-        ws = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
+    with _owned(stream):
+        if tokens.dtype == torch.int64:
+            tokens = tokens.to(torch.int32)
+        B, K, V, dt = _check(target, draft, tokens, uniforms)
+        dev = target.device
+        out = torch.empty(B, K + 1, dtype=torch.int32, device=dev)
+        nacc = torch.empty(B, dtype=torch.int32, device=dev)
+        kept = torch.empty(B, 2 * K + 1, dtype=torch.int32, device=dev)
+        ws = workspace
+        if ws is None:
+            n = sv_topp_workspace_size(B, K, V, dt)
+            ws = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
+    _shared(stream, out, nacc, kept)
     rc = spec_verify_topp(target, draft, tokens, uniforms, temperature, top_p, out, nacc, ws,
                           kept, stream=stream)
     if rc != SV_OK:
@@ -453,12 +480,14 @@ def draft_sample(logits, uniforms, temperature, *, workspace=None, with_prob=Fal
     drawn tokens' probabilities [N] fp64 when `with_prob`)."""
     N, V = logits.shape
     dev = logits.device
-    out = torch.empty(N, dtype=torch.int32, device=dev)
-    prob = torch.empty(N, dtype=torch.float64, device=dev) if with_prob else None
-    ws = workspace
-    if ws is None:
-        n = sv_sample_workspace_size(N, V, _dtype_code(logits))
-        ws = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
+    with _owned(stream):
+        out = torch.empty(N, dtype=torch.int32, device=dev)
+        prob = torch.empty(N, dtype=torch.float64, device=dev) if with_prob else None
+        ws = workspace
+        if ws is None:
+            n = sv_sample_workspace_size(N, V, _dtype_code(logits))
+            ws = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
+    _shared(stream, *((out, prob) if with_prob else (out,)))
     rc = spec_draft_sample(logits, uniforms, temperature, out, ws, prob, stream=stream)
     if rc != SV_OK:
         raise StatusError(rc, "spec_draft_sample")
@@ -491,16 +520,18 @@ def spec_verify_greedy(target, tokens, out_tokens, n_accepted, workspace, stream
 def verify_greedy(target, tokens, *, workspace=None, stream=None):
     """Allocate outputs (and a workspace if none is given) and run greedy
     verification; returns (out_tokens [B, K+1] int32, n_accepted [B] int32)."""
-    if tokens.dtype == torch.int64:
-        tokens = tokens.to(torch.int32)
     B, K1, V = target.shape
     dev = target.device
-    out = torch.empty(B, K1, dtype=torch.int32, device=dev)
-    nacc = torch.empty(B, dtype=torch.int32, device=dev)
-    ws = workspace
-    if ws is None:
-        n = sv_greedy_workspace_size(B, K1 - 1, V, _dtype_code(target))
-        ws = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
+    with _owned(stream):
+        if tokens.dtype == torch.int64:
+            tokens = tokens.to(torch.int32)
+        out = torch.empty(B, K1, dtype=torch.int32, device=dev)
+        nacc = torch.empty(B, dtype=torch.int32, device=dev)
+        ws = workspace
+        if ws is None:
+            n = sv_greedy_workspace_size(B, K1 - 1, V, _dtype_code(target))
+            ws = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
+    _shared(stream, out, nacc)
     rc = spec_verify_greedy(target, tokens, out, nacc, ws, stream=stream)
     if rc != SV_OK:
         raise StatusError(rc, "spec_verify_greedy")
@@ -537,18 +568,20 @@ def sv_lmhead_stats(hidden, weight, tokens, temperature, row_max, lse, at, works
 def lmhead_stats(hidden, weight, tokens, temperature, *, workspace=None, stream=None):
     """Allocate the outputs (and a workspace if none is given) with torch and
     run the fused projection + statistics; returns (row_max, lse, at)."""
-    if tokens.dtype == torch.int64:
-        tokens = tokens.to(torch.int32)
     N, D = hidden.shape
     V = weight.shape[0]
     dev = hidden.device
     n = sv_lmhead_workspace_size(N, D, V)
     if n == 0:
         raise StatusError(2, "sv_lmhead_workspace_size")
-    ws = workspace if workspace is not None else torch.empty(n, dtype=torch.uint8, device=dev)
-    row_max = torch.empty(N, dtype=torch.float64, device=dev)
-    lse = torch.empty(N, dtype=torch.float64, device=dev)
-    at = torch.empty(N, dtype=torch.float32, device=dev)
+    with _owned(stream):
+        if tokens.dtype == torch.int64:
+            tokens = tokens.to(torch.int32)
+        ws = workspace if workspace is not None else torch.empty(n, dtype=torch.uint8, device=dev)
+        row_max = torch.empty(N, dtype=torch.float64, device=dev)
+        lse = torch.empty(N, dtype=torch.float64, device=dev)
+        at = torch.empty(N, dtype=torch.float32, device=dev)
+    _shared(stream, row_max, lse, at)
     rc = sv_lmhead_stats(hidden, weight, tokens, temperature, row_max, lse, at, ws, stream=stream)
     if rc != SV_OK:
         raise StatusError(rc, "sv_lmhead_stats")
@@ -619,25 +652,6 @@ def _raw_stream(device, stream):
     if stream is not None:
         return stream.cuda_stream
     return torch._C._cuda_getCurrentRawStream(device.index)  # 2 us less than through a Stream object
-
-
-_CURRENT = contextlib.nullcontext()
-
-
-def _owned(stream):
-    """Memory that a call on `stream` allocates belongs to that stream: freed, it goes back to the
-    stream that may still use it, and what an earlier owner left pending there comes before."""
-    return _CURRENT if stream is None else torch.cuda.stream(stream)
-
-
-def _shared(stream, *outputs):
-    """Outputs that a call on `stream` allocated are for the current stream's use too: freed, they
-    wait for what it has queued."""
-    if stream is not None:
-        current = torch.cuda.current_stream(stream.device)
-        if current != stream:
-            for t in outputs:
-                t.record_stream(current)
 
 
 def _gpu(name, t):
