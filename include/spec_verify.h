@@ -492,7 +492,7 @@ size_t sv_tree_attention_workspace_size(int B, int T, int Hq, int Hkv, int D, in
  *   q           device, [B, T, Hq, D] bf16, strides in elements
  *   k_cache, v_cache, k_scale, v_scale, num_pages, page_size, cache_dtype  the cache
  *   page_table  device, [B, max_pages] int32; entries past a sequence's last node
- *               are not read
+ *               are not used
  *   ctx_lens    device, [B] int32, 0 or more
  *   parents     device, [B, T] int32, or NULL for chains (node i's parent is i - 1)
  *   out         device, [B, T, Hq, D] bf16, contiguous (written); 0 for padding
@@ -530,7 +530,9 @@ size_t sv_tree_workspace_size(int B, int T, int V, int dtype);
  * becomes the current node; a rejection turns r into max(0, r - p) over its sum (a
  * sum below 2^-40, which is r = p but for rounding, leaves r). When no child is left, one token is drawn
  * from r. With each node's children drawn independently from p, the emitted
- * tokens follow the target's distribution. A chain gives spec_verify's results.
+ * tokens follow the target's distribution. The tests' row sums are fp32 (about 1e-6 of a
+ * ratio; spec_verify's are float-floats): a chain gives spec_verify's results but where a uniform lies within that of
+ * its ratio. Draws use float-floats.
  *   target_logits  device, [B, T, V] dtype: row i is the target's at node i
  *   draft_logits   device, [R, V] dtype: the draft's rows
  *   draft_index    device, [B, T] int32: node i's row of draft_logits; read for

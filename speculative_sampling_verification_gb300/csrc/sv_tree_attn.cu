@@ -330,9 +330,9 @@ SV_DEVINL uint32_t pack_bf16(float a, float b) {
 }
 SV_DEVINL void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// Hardware barrier of `threads` threads, and the OR of their predicates.
 // The kernel launched before this one (which cleared the counters) is complete.
 SV_DEVINL void wait_for_clear() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Hardware barrier of `threads` threads, and the OR of their predicates.
 SV_DEVINL void named_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
@@ -2097,7 +2097,7 @@ bool tc_shape(int D, int page_size) {
 // How the rows of an item are cut: up to 128 in one Q tile; more in pairs of equal
 // tiles (D above 128: single tiles), a CTA each.
 struct Plan {
-  int rows, rpt, parts, groups, cta_rows, pad;
+  int rows, rpt, parts, groups, cta_rows;
   bool shared;
   size_t off_counters, off_ml, off_o, total;
 };

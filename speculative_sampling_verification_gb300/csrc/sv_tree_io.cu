@@ -6,7 +6,6 @@
 #include <cmath>
 #include <cstdint>
 #include <algorithm>
-#include <mutex>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
