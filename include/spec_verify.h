@@ -528,8 +528,8 @@ size_t sv_tree_workspace_size(int B, int T, int V, int dtype);
  * draft row's softmax(l / T), the children are tried in index order against the residual
  * r, q at first: child c of token x is accepted while u < min(1, r(x)/p(x)), and
  * becomes the current node; a rejection turns r into max(0, r - p) over its sum (a
- * sum below 2^-40, which is r = p but for rounding, leaves r). When no child is left, one token is drawn
- * from r. With each node's children drawn independently from p, the emitted
+ * sum below 2^-30, which is r = p but for rounding, leaves r). When no child is left,
+ * one token is drawn from r. With each node's children drawn independently from p, the emitted
  * tokens follow the target's distribution. The tests' row sums are fp32 (about 1e-6 of a
  * ratio; spec_verify's are float-floats): a chain gives spec_verify's results but where a uniform lies within that of
  * its ratio. Draws use float-floats.

@@ -12,9 +12,11 @@
 // with two scalars: max(0, max(0, A q - B p) - p) = max(0, A q - (B + 1) p),
 // because where the inner maximum is 0 the outer one is too. So a rejection
 // costs one pass over two rows for Z = sum max(0, A q - (B + 1) p), then
-// (A, B) <- (A, B + 1) / Z, and no residual is ever stored. A sum below 2^-40 (r
+// (A, B) <- (A, B + 1) / Z, and no residual is ever stored. A sum below 2^-30 (r
 // equals p but for rounding: such a rejection has that probability) leaves r
-// as it was.
+// as it was. Where q and p are equal but not their logits, A q - B p is what the
+// exponentials' errors leave, up to 1.5e-10 (2^-32.6) with the short ones: at 2^-40 that was
+// taken for a residual, and the next child's ratio was noise.
 //
 // One thread-block cluster a sequence; the vocabulary is cut into one region
 // per warp of the cluster. Only the rows of visited nodes are read: from HBM
@@ -55,7 +57,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;  // the portable cluster size
 constexpr int kTreeMax = 128;
-constexpr double kResidualMin = 9.094947017729282e-13;  // 2^-40
+constexpr double kResidualMin = 9.313225746154785e-10;  // 2^-30
 constexpr int kStep = 256;      // elements a warp takes at once: eight a lane
 
 struct Args {
