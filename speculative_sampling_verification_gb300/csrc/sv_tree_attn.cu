@@ -55,10 +55,11 @@ struct Args {
 // tile of its own and both use every tile. Head sizes above 128 have room for
 // one stream only.
 //
-// 8 sequences of 64 nodes, 64/8 heads of 128, contexts to 32768, bf16: 347 us, 0.98 PFLOP/s, with
-// the tensor pipe active 40 % of the time and the issue slots 37 %: the chain of product,
+// 8 sequences of 64 nodes, 64/8 heads of 128, contexts to 32768, bf16: 341 us, 1.00 PFLOP/s, with
+// the tensor pipe active 41 % of the time and the issue slots 38 %: the chain of product,
 // softmax and product bounds it. One thread a row: 381 us. 64 sequences of 9 nodes, 32/8 heads,
-// to 8192, bf16: 208 us, 5.8 TB/s.
+// to 8192, bf16: 208 us, 5.8 TB/s. From an e4m3 cache four warps convert every code, which
+// bounds it whatever the rows: 11 nodes (44 rows) 411 us, 32 nodes 437 us.
 //
 // Work: the tiles of all (sequence, key/value head) items, with a few units for the item
 // itself before them, form one line, cut into equal ranges, one for each group of CTAs (the CTAs of a group take the item's
@@ -1193,9 +1194,10 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
 // scales of 2^-108 (the least that sv_cache_write stores) to 2^100. A bf16 cache uses bf16
 // operands, P rounded once (2^-8).
 //
-// 64 sequences of 9 nodes, 32/8 heads of 128, contexts to 8192, e4m3: 206 us, 3.1 TB/s, with
-// 54 % of the issue slots active, the tensor pipe 13 % and the memory 41 %: the latency of
-// the softmax's dependent steps. One token over 32768 keys: 30 us.
+// 64 sequences of 9 nodes, 32/8 heads of 128, contexts to 8192, e4m3: 205 us, 3.1 TB/s, with
+// 54 % of the issue slots active, the tensor pipe 13 % and the memory 40 %. With one node (4
+// rows) it is 159 us: a tile's chain of product, vote, weights and product; the other 32
+// rows' weights and pieces take the rest. One token over 32768 keys: 30 us, bf16 37 us.
 //
 // Streams, ranges and parts are those of the kernel above; the next tile's
 // S^T is issued before this tile's O^T, so neither waits for the other. The softmax
@@ -2223,10 +2225,10 @@ int launch_few(const TcArgs& x, cudaStream_t st) {
 }
 
 // Whether keys, not rows, are the M of the products. Measured, keys / rows as M in us:
-// e4m3, 64 sequences to 8192, D 128: 156 / 403 (4 rows), 206 / 409 (36), since only the
+// e4m3, 64 sequences to 8192, D 128: 159 / 403 (4 rows), 205 / 409 (36), since only the
 // first takes the codes as they are; it loses only for contexts of a few tiles (53 / 48
-// at 300 keys, 36 rows, D 64). bf16, D 128: one sequence of 32768 39 / 42 (4 rows) and 52 / 54
-// (36); 64 to 8192 206 / 202 and 222 / 209; 160 to 1024 111 / 122 and 148 / 139. bf16, D 64,
+// at 300 keys, 36 rows, D 64). bf16, D 128: one sequence of 32768 37 / 42 (4 rows) and 52 / 54
+// (36); 64 to 8192 205 / 202 and 222 / 209; 160 to 1024 111 / 122 and 148 / 139. bf16, D 64,
 // one sequence of 32768 31 / 28 and 41 / 35; 64 to 8192 175 / 131 and 200 / 136.
 bool keys_as_m(int rows, int D, bool f8) {
   return f8 ? D <= 128 && rows <= kFewRows : D > 64 && D <= 128 && rows <= 16;

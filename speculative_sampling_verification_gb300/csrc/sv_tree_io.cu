@@ -133,8 +133,9 @@ SV_DEVINL uint4 raw_vec(const void* base, long long at) {
 // rotates together, so nothing crosses lanes); interleaved, or past R, two vectors that
 // each stand alone. The angles are computed once and serve the group's heads: with one
 // head a group their cosines and sines bound the kernel (137 us for 16383 tokens of
-// 40 heads of 128 in bf16); so it takes 67 us, 5.0 TB/s. Blocks of 128 threads: 77 us
-// with 256, whose last blocks are fewer and longer.
+// 40 heads of 128 in bf16); so it takes 67 us, 5.0 TB/s, with 72 % of the issue slots active and
+// the memory 54 %: its instructions bound it now. fp32: 121 us, 5.6 TB/s.
+// Blocks of 128 threads: 77 us with 256, whose last blocks are fewer and longer.
 template <int DT, int L, bool INTER>
 __global__ void __launch_bounds__(kThreads) norm_rope_kernel(NormRopeArgs a) {
   constexpr int VEC = DT == SV_BF16 ? 8 : 4;
@@ -352,7 +353,7 @@ SV_DEVINL bool slot_ok(const CacheArgs& a, long long slot) {
 // is its largest magnitude over 448, the largest e4m3 value, so that no code saturates
 // but by rounding. A row with NaN or infinity gets a NaN scale and codes of zero: it
 // reads back as NaN everywhere. Bound by memory: 32767 tokens of 8 heads of 128, bf16 to
-// e4m3, take 33 us, 5.8 TB/s. Heads a group, in blocks of 256: one 37 us, two 34, four 40.
+// e4m3, take 33 us, 5.8 TB/s; bf16 to bf16 42 us, fp32 to e4m3 54 us. Heads a group, in blocks of 256: one 37 us, two 34, four 40.
 template <int DT, int CDT, int L, int HB>
 __global__ void __launch_bounds__(kThreads) cache_write_kernel(CacheArgs a) {
   constexpr int VEC = DT == SV_BF16 ? 8 : 4;
@@ -429,7 +430,8 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(CacheArgs a) {
   }
 }
 
-// The same division; 100003 tokens of 8 heads of 128, e4m3 to bf16, take 101 us, 6.1 TB/s.
+// The same division; 100003 tokens of 8 heads of 128, e4m3 to bf16, take 101 us, 6.1 TB/s; bf16 to
+// bf16 125 us, e4m3 to fp32 231 us (4.5 TB/s).
 // Heads a group, in blocks of 256: one 105 us, two 102, four 106.
 template <int DT, int CDT, int L, int HB>
 __global__ void __launch_bounds__(kThreads) cache_read_kernel(CacheArgs a) {

@@ -36,7 +36,8 @@
 // 64 trees of 16 nodes over 128256 tokens, bf16: 148 us, where reading the rows once takes 10. The
 // dependent passes of a path bound it and sequences differ in length: 44 % of the issue
 // slots are active on average, 74 % on the busiest SM. 512 threads a CTA, two an SM: 162.
-// CTAs of 256 an SM, before the rows' statistics took one pass: three 193, four 164, five 169. One tree of nine nodes over 32000 tokens: 34 us.
+// CTAs of 256 an SM, before the rows' statistics took one pass: three 193, four 164, five 169. One tree of nine nodes over 32000 tokens: 34 to 36 us.
+// 64 trees over 50257 tokens (rows off 16 bytes, element loads): 111 us, over 50256 88 us.
 #include <cfloat>
 #include <climits>
 #include <cmath>
