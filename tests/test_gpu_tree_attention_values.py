@@ -148,3 +148,25 @@ def test_rows_of_zeros(G, D, cdt, kept):
     out, status = base.run(args, D ** -0.5)
     assert status == 0
     base.check(*args, D ** -0.5, out)
+
+
+@pytest.mark.parametrize("G,D", KINDS)
+@pytest.mark.parametrize("cdt", [BF, F8])
+@pytest.mark.parametrize("written", [0, 5, 2000])
+def test_slots_never_written(G, D, cdt, written):
+    """A new cache is zeroed, e4m3 scales too: a context whose slots were never written has scores of 0 and
+    values of 0, beside the `written` ones."""
+    P, Hkv, ctx = 64, 2, 3000
+    cache = sv.new_cache(60, Hkv, P, D, cdt, DEV)
+    g = torch.Generator().manual_seed(G)
+    table = torch.randperm(60, generator=g)[:48].to(torch.int32).view(1, 48)
+    pos = torch.randperm(ctx + 1, generator=g)[:written]
+    slots = table[0].long()[pos // P] * P + pos % P
+    k, v = (torch.randn(written, Hkv, D, generator=g).to(BF).to(DEV) for _ in range(2))
+    sv.cache_write(k, v, slots.to(DEV), cache)
+    q = torch.randn(1, 1, Hkv * G, D, generator=g).to(BF).to(DEV)
+    args = (q, cache, table.to(DEV), torch.tensor([ctx], dtype=torch.int32, device=DEV),
+            torch.tensor([[-1]], dtype=torch.int32, device=DEV))
+    out, status = base.run(args, D ** -0.5)
+    assert status == 0
+    base.check(*args, D ** -0.5, out)
