@@ -86,6 +86,8 @@ enum {
   SV_DEV_TIMEOUT = 256,      /* a bounded wait in a kernel ran out (results invalid) */
   SV_DEV_SLOT_RANGE = 512,   /* a cache slot outside the cache, other than -1 */
   SV_DEV_PAGE_RANGE = 1024,  /* a needed page outside the cache, or a context outside its page table */
+  SV_DEV_NO_PAGES = 4096,    /* a request was refused: the ring has too few free pages */
+  SV_DEV_SETTING = 8192,     /* a row's sampling settings are out of range */
   SV_DEV_TREE = 2048         /* a malformed tree: a parent that is not an earlier node, or a node
                                 with children whose draft row lies outside the draft logits */
 };
@@ -553,6 +555,131 @@ int spec_verify_tree(const void* target_logits, const void* draft_logits, const 
                      int V, int R, int dtype, float temperature, int32_t* out_tokens,
                      int32_t* out_nodes, int32_t* n_accepted, void* workspace, size_t workspace_bytes,
                      void* stream);
+
+/* ---------------------------------------------------------------- drafting over a long cache
+ *
+ * What a draft step needs around the verification when the draft is the model itself
+ * reading a part of its cache: the step's pages and slots (sv_page_plan), bounds of the
+ * keys of each page (sv_page_bounds, after sv_cache_write), attention over the pages that the
+ * bounds select (sv_sparse_attention), and tokens from the transformed distribution
+ * (spec_filtered_sample; spec_verify_topk and spec_verify_topp verify tokens drawn with their
+ * filter). Lengths stay on the device, so that a captured graph follows them. */
+
+/* Bytes of device workspace sv_page_plan needs; 0 for B < 0. Pure host function. */
+size_t sv_page_plan_workspace_size(int B);
+
+/* The pages and slots of one step of B requests. Request b holds held[b] pages (the first
+ * entries of its row of page_table) and ctx_lens[b] tokens, and new_lens[b] >= 0 tokens
+ * come in behind them; new_lens[b] = -1 says that it has ended. Free pages wait in a ring:
+ * state is (head, count), the pages are ring[(head + i) % capacity], i < count.
+ *   - A request needs max(0, ceil((ctx + new) / page_size) - held) pages more. It is granted if
+ *     it needs none, or if its need and those of the valid requests before it come to at most `count`,
+ *     and if its tokens end within max_tokens; it then takes its pages from the ring in
+ *     order. Nothing is taken for a request that is not granted (granted[b] = 0).
+ *   - The pages of requests that have ended go behind the ring's tail, in order, and can be taken from
+ *     the next call on; held_out is then 0 and granted -1. The table's entries stay as they were.
+ *   - Tokens are packed by request: those of request b begin behind the sum of the max(new_lens, 0)
+ *     before it, granted or not.
+ *   ring         device, [capacity] int32, in and out
+ *   state        device, [2] int32; state_out may be the same
+ *   page_table   device, [B, max_pages] int32, in and out: only the new entries are written
+ *   held         device, [B] int32; held_out may be the same
+ *   slots        device, [max_tokens] int64 (written): page * page_size + offset, as
+ *                sv_cache_write takes them; -1 for tokens that are not granted or not there
+ *   positions, seqs  device, [max_tokens] int32 (written): the token's position and request, or -1
+ *   granted      device, [B] int32 (written): new_lens, or 0
+ *   workspace    device, sv_page_plan_workspace_size() bytes, 256-byte aligned
+ *   status       device word, may be NULL; bits are OR-ed into it: SV_DEV_NO_PAGES and
+ *                SV_DEV_SLOT_RANGE (past max_tokens) for requests that are refused, SV_DEV_PAGE_RANGE
+ *                for a negative length, held outside [0, max_pages], a need outside the table, or a
+ *                ring whose state is out of range or has no room for the pages that come back
+ *                (none come back then)
+ * Returns SV_OK once enqueued. */
+int sv_page_plan(int32_t* ring, int64_t capacity, const int32_t* state, int32_t* page_table, const int32_t* held,
+                 const int32_t* ctx_lens, const int32_t* new_lens, int B, int max_pages, int page_size, int max_tokens,
+                 int64_t* slots, int32_t* positions, int32_t* seqs, int32_t* granted, int32_t* held_out,
+                 int32_t* state_out, void* workspace, size_t workspace_bytes, uint32_t* status, void* stream);
+
+/* Bounds of the keys of every page that holds one of the positions
+ * ctx_lens[b] .. ctx_lens[b] + new_lens[b] - 1 (none for new_lens[b] <= 0), over all keys of the
+ * page up to the last of those positions:
+ *   codes   device, [num_pages, Hkv, 2, D] int8: the channels' minima, then their maxima
+ *   scale   device, [num_pages, Hkv] fp32
+ * With a = max(max |k|, 1e-30) over the page's keys of the head and up = 127 / a (rounded to fp32),
+ * a minimum's code is floor(min * up), a maximum's ceil(max * up), within -127 .. 127, and
+ * the scale a / 127. A page that holds NaN or infinity gets codes of 0 and the scale +inf. An
+ * e4m3 key counts as code * scale rounded to fp32. No page may belong to two sequences.
+ * `status` may be NULL: SV_DEV_PAGE_RANGE is OR-ed into it for lengths outside the page table (no
+ * bounds are written for that sequence) and pages outside the cache. 1 <= D <= 1024. Returns
+ * SV_OK once enqueued; B == 0 returns SV_OK at once. */
+int sv_page_bounds(const void* k_cache, const float* k_scale, int64_t num_pages, int page_size, int cache_dtype,
+                   const int32_t* page_table, const int32_t* ctx_lens, const int32_t* new_lens, int B, int Hkv,
+                   int D, int max_pages, int8_t* codes, float* scale, uint32_t* status, void* stream);
+
+/* Bytes of device workspace sv_sparse_attention needs; 0 for invalid sizes. Pure host function. */
+size_t sv_sparse_attention_workspace_size(int N, int Hq, int Hkv, int D, int max_pages, int page_size, int budget);
+
+/* Attention of N query rows over selected pages of their sequences. Row n stands at
+ * positions[n] of sequence seqs[n] (n itself if seqs is NULL) and sees the keys up to and with its
+ * own, in ceil((positions[n] + 1) / page_size) pages. For each key/value head it attends `budget` of
+ * them, or all if there are no more: the first `sink`, the last `recent`, and those of the highest
+ * scores, equal scores in page order. A head's queries q_g become codes
+ * c = rint(q * (127 / a)), within -127 .. 127, and the scale s_g = a / 127, a = max(max |q_g|, 1e-30),
+ * quotients and products rounded to fp32 (a head that holds NaN or infinity gets codes and a scale of
+ * 0); then, in fp32 and rounded at each product,
+ *   score(page) = max_g (s_g * sum_d max(c_d min_d, c_d max_d)) * scale(page)
+ * with the page's codes min_d and max_d; +inf where the page's scale is. It bounds the scores of the
+ * page's keys from above, to the codes' resolution, and is the same on any hardware.
+ *   q            device, [N, Hq, D] bf16, strides in elements
+ *   k_cache .. cache_dtype    the cache
+ *   codes, bound_scale        sv_page_bounds' outputs, up to date for every page that a row sees
+ *   page_table   device, [B, max_pages] int32, max_pages <= 49152
+ *   positions    device, [N] int32; -1: the row is empty
+ *   seqs         device, [N] int32 or NULL (then N <= B); -1: the row is empty
+ *   budget, sink, recent      sink >= 0, recent >= 1, sink + recent <= budget
+ *   scale        of the attention's scores, finite and > 0
+ *   out          device, [N, Hq, D] bf16, contiguous (written); 0 for an empty row
+ *   selected     device, [N, Hkv, budget] int32, may be NULL (written): the chosen pages' places in
+ *                their sequence, ascending, then -1
+ *   workspace    device, sv_sparse_attention_workspace_size() bytes, 256-byte aligned; its first
+ *                4 bytes are the device status word
+ * A row whose position or sequence is out of range, or one of whose pages lies outside the cache, gets NaN
+ * outputs, no selected pages and SV_DEV_PAGE_RANGE; the others are unaffected. Precision and the
+ * shapes of the tensor-core kernels as for sv_tree_attention. Returns SV_OK once enqueued; N == 0
+ * returns SV_OK at once. */
+int sv_sparse_attention(const void* q, int64_t q_stride_n, int64_t q_stride_h, const void* k_cache,
+                        const void* v_cache, const float* k_scale, const float* v_scale, int64_t num_pages,
+                        int page_size, int cache_dtype, const int8_t* codes, const float* bound_scale,
+                        const int32_t* page_table, const int32_t* positions, const int32_t* seqs, int N, int B,
+                        int Hq, int Hkv, int D, int max_pages, int budget, int sink, int recent, float scale,
+                        void* out, int32_t* selected, void* workspace, size_t workspace_bytes, void* stream);
+
+/* One token a row from the softmax of the entries that the row's settings keep, by the
+ * inverse-CDF convention above. With the entries ordered by logit (larger first, ties to the
+ * smaller id, -0 equal to +0) and w_i = exp((l_i - max l) / T):
+ *   - top_k keeps the first top_k entries (all for top_k <= 0 or >= V);
+ *   - top_p keeps the shortest prefix of those whose weight reaches top_p times theirs (all for
+ *     top_p >= 1);
+ *   - min_p keeps the entries of w_i >= min_p (all for min_p <= 0), the first entry always.
+ * T = 0 takes the first entry, whatever the other settings.
+ *   logits       device, [N, V] dtype, rows row_stride elements apart (>= V)
+ *   uniforms     device, [N] fp32
+ *   temperatures, top_ks, top_ps, min_ps   device, [N], a setting a row; where one is NULL the
+ *                value next to it holds for all rows
+ *   out_tokens   device, [N] int32 (written), -1 for a failed row
+ *   out_probs    device, [N] fp32, may be NULL (written): the token's probability among the kept
+ *                entries, NaN for a failed row
+ *   status       device word, may be NULL; bits are OR-ed into it
+ * Weights are float-float exponentials (5e-11) as whole numbers of 2^-44 of the row's largest (V above
+ * 2^17: 2^(61 - ceil(log2 V))), so that no result depends on the order of a sum; smaller weights count as 0.
+ * A row fails on NaN or +inf (SV_DEV_NONFINITE), with no finite entry (SV_DEV_EMPTY_ROW), on a
+ * uniform outside [0, 1] (SV_DEV_UNIFORM_RANGE), and on T negative or not finite, top_p NaN or <= 0, or min_p
+ * NaN or > 1 (SV_DEV_SETTING; host errors where the value holds for all rows). No workspace.
+ * 1 <= V <= 2^30. Returns SV_OK once enqueued; N == 0 returns SV_OK at once. */
+int spec_filtered_sample(const void* logits, int64_t row_stride, const float* uniforms, int N, int V,
+                         int dtype, const float* temperatures, float temperature, const int32_t* top_ks,
+                         int top_k, const float* top_ps, float top_p, const float* min_ps, float min_p,
+                         int32_t* out_tokens, float* out_probs, uint32_t* status, void* stream);
 
 #ifdef __cplusplus
 }

@@ -34,7 +34,10 @@ __all__ = [
     "sv_lmhead_workspace_size", "sv_lmhead_stats", "lmhead_stats",
     "SV_E4M3", "PagedCache", "new_cache", "sv_qk_norm_rope", "qk_norm_rope", "sv_cache_write", "cache_write",
     "sv_cache_read", "cache_read", "sv_tree_attention_workspace_size", "sv_tree_attention",
-    "tree_attention", "sv_tree_workspace_size", "spec_verify_tree", "verify_tree", "EXPORTED_SYMBOLS",
+    "tree_attention", "sv_tree_workspace_size", "spec_verify_tree", "verify_tree", "PagePool", "new_page_pool",
+    "sv_page_plan_workspace_size", "sv_page_plan", "page_plan", "PageBounds", "new_page_bounds", "sv_page_bounds",
+    "page_bounds", "sv_sparse_attention_workspace_size", "sv_sparse_attention", "sparse_attention",
+    "spec_filtered_sample", "filtered_sample", "EXPORTED_SYMBOLS",
 ]
 
 SV_BF16 = 0
@@ -42,7 +45,8 @@ SV_F32 = 1
 SV_E4M3 = 2
 SV_OK = 0
 DEVICE_BITS = {16: "token_range", 32: "nonfinite", 64: "empty_row", 128: "uniform_range",
-               256: "timeout", 512: "slot_range", 1024: "page_range", 2048: "tree"}
+               256: "timeout", 512: "slot_range", 1024: "page_range", 2048: "tree", 4096: "no_pages",
+               8192: "setting"}
 
 EXPORTED_SYMBOLS = (
     "sv_workspace_size", "spec_verify", "spec_verify_debug", "spec_verify_profiled",
@@ -54,7 +58,8 @@ EXPORTED_SYMBOLS = (
     "spec_verify_host_async", "sv_lmhead_workspace_size", "sv_lmhead_stats",
     "sv_topp_kernels_per_call", "sv_qk_norm_rope", "sv_cache_write", "sv_cache_read",
     "sv_tree_attention_workspace_size", "sv_tree_attention", "sv_tree_workspace_size",
-    "spec_verify_tree",
+    "spec_verify_tree", "sv_page_plan_workspace_size", "sv_page_plan", "sv_page_bounds",
+    "sv_sparse_attention_workspace_size", "sv_sparse_attention", "spec_filtered_sample",
 )
 
 _lib = None
@@ -149,6 +154,21 @@ def load_library(path: str | None = None, build: bool = False) -> ctypes.CDLL:
     lib.spec_verify_tree.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, f32, vp, vp, vp, vp, sz,
                                      vp]
     lib.spec_verify_tree.restype = i32
+    lib.sv_page_plan_workspace_size.argtypes = [i32]
+    lib.sv_page_plan_workspace_size.restype = sz
+    lib.sv_page_plan.argtypes = [vp, i64, vp, vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, sz,
+                                 vp, vp]
+    lib.sv_page_plan.restype = i32
+    lib.sv_page_bounds.argtypes = [vp, vp, i64, i32, i32, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp]
+    lib.sv_page_bounds.restype = i32
+    lib.sv_sparse_attention_workspace_size.argtypes = [i32] * 7
+    lib.sv_sparse_attention_workspace_size.restype = sz
+    lib.sv_sparse_attention.argtypes = [vp, i64, i64, vp, vp, vp, vp, i64, i32, i32, vp, vp, vp, vp, vp, i32, i32,
+                                        i32, i32, i32, i32, i32, i32, i32, f32, vp, vp, vp, sz, vp]
+    lib.sv_sparse_attention.restype = i32
+    lib.spec_filtered_sample.argtypes = [vp, i64, vp, i32, i32, i32, vp, f32, vp, i32, vp, f32, vp, f32, vp, vp, vp,
+                                         vp]
+    lib.spec_filtered_sample.restype = i32
     if path is None:
         _lib = lib
     return lib
@@ -916,3 +936,271 @@ def verify_tree(target, draft, draft_index, tokens, parents, uniforms, temperatu
     if rc != SV_OK:
         raise StatusError(rc, "spec_verify_tree")
     return tuple(outs)
+
+
+# ---------------------------------------------------------------- drafting over a long cache
+
+class _Fixed:
+    """Holds tensors that are checked once: they cannot be exchanged for others (their contents may change)."""
+
+    __slots__ = ()
+
+    def _keep(self, **values):
+        for name, value in values.items():
+            object.__setattr__(self, name, value)
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"a {type(self).__name__}'s {name} is fixed: make another {type(self).__name__}")
+
+    def __delattr__(self, name):
+        raise AttributeError(f"a {type(self).__name__}'s {name} is fixed")
+
+
+class PagePool(_Fixed):
+    """The free pages of a cache: a ring of page numbers (int32 [capacity]) and
+    its state (int32 [2]: head and count)."""
+
+    __slots__ = ("pages", "state", "capacity", "device", "addresses")
+
+    def __init__(self, pages, state):
+        if pages.dim() != 1 or pages.shape[0] < 1:
+            raise ValueError("pages must be [capacity]")
+        device = _gpu("pages", pages)
+        _vector("pages", pages, (pages.shape[0],), torch.int32, device)
+        _vector("state", state, (2,), torch.int32, device)
+        self._keep(pages=pages, state=state, capacity=pages.shape[0], device=device,
+                   addresses=(pages.data_ptr(), state.data_ptr()))
+
+
+def new_page_pool(num_pages, device="cuda") -> PagePool:
+    """A pool in which pages 0 .. num_pages - 1 are all free."""
+    return PagePool(torch.arange(num_pages, dtype=torch.int32, device=device),
+                    torch.tensor([0, num_pages], dtype=torch.int32, device=device))
+
+
+def sv_page_plan_workspace_size(B: int) -> int:
+    return int(load_library().sv_page_plan_workspace_size(B))
+
+
+def sv_page_plan(pool, page_table, held, ctx_lens, new_lens, page_size, slots, positions, seqs, granted, held_out,
+                 state_out, workspace, status=None, stream=None) -> int:
+    """Direct binding of the page plan: page_table [B, max_pages], held,
+    ctx_lens, new_lens, granted, held_out [B], positions and seqs [max_tokens],
+    state_out [2] int32, slots [max_tokens] int64; returns the host status code."""
+    dev = pool.device
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, max_pages]")
+    B, width = page_table.shape
+    n = slots.shape[0]
+    _vector("page_table", page_table, (B, width), torch.int32, dev)
+    for name, t in (("held", held), ("ctx_lens", ctx_lens), ("new_lens", new_lens), ("granted", granted),
+                    ("held_out", held_out)):
+        _vector(name, t, (B,), torch.int32, dev)
+    _vector("slots", slots, (n,), torch.int64, dev)
+    _vector("positions", positions, (n,), torch.int32, dev)
+    _vector("seqs", seqs, (n,), torch.int32, dev)
+    _vector("state_out", state_out, (2,), torch.int32, dev)
+    return load_library().sv_page_plan(
+        pool.addresses[0], pool.capacity, pool.addresses[1], page_table.data_ptr(), held.data_ptr(),
+        ctx_lens.data_ptr(), new_lens.data_ptr(), B, width, page_size, n, slots.data_ptr(), positions.data_ptr(),
+        seqs.data_ptr(), granted.data_ptr(), held_out.data_ptr(), state_out.data_ptr(), *_scratch(workspace, dev),
+        _status_word(status, dev), _raw_stream(dev, stream))
+
+
+def page_plan(pool, page_table, held, ctx_lens, new_lens, page_size, *, max_tokens=None, outs=None, held_out=None,
+              state_out=None, workspace=None, status=None, stream=None):
+    """The pages and slots of one step: requests take pages from the pool for
+    new_lens tokens behind their ctx_lens, or (new_lens = -1) give all of theirs
+    back. `held` and the pool's state are updated in place unless held_out and
+    state_out are given; `outs` holds the four results, or `max_tokens` says how
+    many tokens to allocate them for. Returns (slots, positions, seqs, granted)."""
+    dev = pool.device
+    made = ()
+    with _owned(stream):
+        if outs is None:
+            if max_tokens is None:
+                raise ValueError("page_plan needs max_tokens, or outs")
+            outs = made = (torch.empty(max_tokens, dtype=torch.int64, device=dev),
+                           torch.empty(max_tokens, dtype=torch.int32, device=dev),
+                           torch.empty(max_tokens, dtype=torch.int32, device=dev),
+                           torch.empty(ctx_lens.shape[0], dtype=torch.int32, device=dev))
+        if workspace is None:
+            workspace = torch.empty(sv_page_plan_workspace_size(ctx_lens.shape[0]), dtype=torch.uint8, device=dev)
+    _shared(stream, *made)
+    rc = sv_page_plan(pool, page_table, held, ctx_lens, new_lens, page_size, *outs,
+                      held if held_out is None else held_out, pool.state if state_out is None else state_out,
+                      workspace, status, stream=stream)
+    if rc != SV_OK:
+        raise StatusError(rc, "sv_page_plan")
+    return tuple(outs)
+
+
+class PageBounds(_Fixed):
+    """Bounds of the keys of a cache's pages: codes int8 [num_pages, Hkv, 2, D]
+    (minima, then maxima) and one fp32 scale [num_pages, Hkv]."""
+
+    __slots__ = ("codes", "scale", "shape", "device", "addresses")
+
+    def __init__(self, codes, scale):
+        if codes.dim() != 4 or codes.shape[2] != 2:
+            raise ValueError("codes must be [num_pages, Hkv, 2, D]")
+        device = _gpu("codes", codes)
+        _vector("codes", codes, codes.shape, torch.int8, device)
+        _vector("scale", scale, codes.shape[:2], torch.float32, device)
+        self._keep(codes=codes, scale=scale, shape=(codes.shape[0], codes.shape[1], codes.shape[3]), device=device,
+                   addresses=(codes.data_ptr(), scale.data_ptr()))
+
+
+def new_page_bounds(cache) -> PageBounds:
+    """Bounds for a cache's pages, all zero."""
+    return PageBounds(torch.zeros(cache.num_pages, cache.heads, 2, cache.head_dim, dtype=torch.int8,
+                                  device=cache.device),
+                      torch.zeros(cache.num_pages, cache.heads, dtype=torch.float32, device=cache.device))
+
+
+def _bounds_of(cache, bounds):
+    if bounds.shape != (cache.num_pages, cache.heads, cache.head_dim) or bounds.device != cache.device:
+        raise ValueError(f"the bounds are for {bounds.shape} on {bounds.device}, the cache is "
+                         f"{(cache.num_pages, cache.heads, cache.head_dim)} on {cache.device}")
+
+
+def sv_page_bounds(cache, bounds, page_table, ctx_lens, new_lens, status=None, stream=None) -> int:
+    """Direct binding of the page bounds: page_table [B, max_pages], ctx_lens
+    and new_lens [B] int32; returns the host status code."""
+    dev = cache.device
+    _bounds_of(cache, bounds)
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, max_pages]")
+    B, width = page_table.shape
+    _vector("page_table", page_table, (B, width), torch.int32, dev)
+    _vector("ctx_lens", ctx_lens, (B,), torch.int32, dev)
+    _vector("new_lens", new_lens, (B,), torch.int32, dev)
+    return load_library().sv_page_bounds(
+        cache.addresses[0], cache.addresses[2], cache.num_pages, cache.page_size, cache.code, page_table.data_ptr(),
+        ctx_lens.data_ptr(), new_lens.data_ptr(), B, cache.heads, cache.head_dim, width, *bounds.addresses,
+        _status_word(status, dev), _raw_stream(dev, stream))
+
+
+def page_bounds(cache, bounds, page_table, ctx_lens, new_lens, *, status=None, stream=None):
+    """Brings the bounds of the pages that got new_lens tokens behind ctx_lens
+    up to date (after cache_write); returns the bounds."""
+    rc = sv_page_bounds(cache, bounds, page_table, ctx_lens, new_lens, status, stream=stream)
+    if rc != SV_OK:
+        raise StatusError(rc, "sv_page_bounds")
+    return bounds
+
+
+def sv_sparse_attention_workspace_size(N: int, Hq: int, Hkv: int, D: int, max_pages: int, page_size: int,
+                                       budget: int) -> int:
+    return int(load_library().sv_sparse_attention_workspace_size(N, Hq, Hkv, D, max_pages, page_size, budget))
+
+
+def sv_sparse_attention(q, cache, bounds, page_table, positions, seqs, budget, sink, recent, scale, out, selected,
+                        workspace, stream=None) -> int:
+    """Direct binding of the sparse attention: q [N, Hq, D] bf16 (any strides
+    but the last), page_table [B, max_pages], positions [N] and seqs [N] (or
+    None: row n is sequence n) int32, out [N, Hq, D] bf16 contiguous, selected
+    [N, Hkv, budget] int32 or None; returns the host status code."""
+    if q.dim() != 3:
+        raise ValueError("q must be [N, Hq, D]")
+    N, Hq, D = q.shape
+    dev = _gpu("q", q)
+    qs = _rows("q", q, (N, Hq, cache.head_dim), torch.bfloat16, dev)
+    _cache_device(cache, dev)
+    _bounds_of(cache, bounds)
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, max_pages]")
+    B, width = page_table.shape
+    _vector("page_table", page_table, (B, width), torch.int32, dev)
+    _vector("positions", positions, (N,), torch.int32, dev)
+    if seqs is not None:
+        _vector("seqs", seqs, (N,), torch.int32, dev)
+    _vector("out", out, (N, Hq, D), torch.bfloat16, dev)
+    if selected is not None:
+        _vector("selected", selected, (N, cache.heads, budget), torch.int32, dev)
+    return load_library().sv_sparse_attention(
+        q.data_ptr(), qs[0], qs[1], *cache.addresses, cache.num_pages, cache.page_size, cache.code,
+        *bounds.addresses, page_table.data_ptr(), positions.data_ptr(), _address(seqs), N, B, Hq, cache.heads, D,
+        width, budget, sink, recent, scale, out.data_ptr(), _address(selected), *_scratch(workspace, dev),
+        _raw_stream(dev, stream))
+
+
+def sparse_attention(q, cache, bounds, page_table, positions, budget, *, seqs=None, sink=1, recent=1, scale=None,
+                     out=None, selected=None, workspace=None, stream=None):
+    """Attention of query rows at `positions` over at most `budget` pages each
+    (the first `sink`, the last `recent`, and those of the highest scores by the
+    pages' bounds; `scale` defaults to D ** -0.5); allocates the output and a
+    workspace if none is given, and returns out [N, Hq, D] bf16."""
+    if q.dim() != 3:
+        raise ValueError("q must be [N, Hq, D]")
+    N, Hq, D = q.shape
+    made = []
+    with _owned(stream):
+        if out is None:
+            out = torch.empty((N, Hq, D), dtype=torch.bfloat16, device=q.device)
+            made.append(out)
+        if workspace is None:
+            n = sv_sparse_attention_workspace_size(N, Hq, cache.heads, D, page_table.shape[-1], cache.page_size,
+                                                   budget)
+            workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=q.device)
+    _shared(stream, *made)
+    rc = sv_sparse_attention(q, cache, bounds, page_table, positions, seqs, budget, sink, recent,
+                             D ** -0.5 if scale is None else scale, out, selected, workspace, stream=stream)
+    if rc != SV_OK:
+        raise StatusError(rc, "sv_sparse_attention")
+    return out
+
+
+def _setting(name, value, off, N, dtype, device):
+    """A setting of all rows or of each: (address or None, value)."""
+    if value is None:
+        return None, off
+    if isinstance(value, torch.Tensor):
+        _vector(name, value, (N,), dtype, device)
+        return value.data_ptr(), off
+    return None, value
+
+
+def spec_filtered_sample(logits, uniforms, temperature, top_k, top_p, min_p, out, prob=None, status=None,
+                         stream=None) -> int:
+    """Direct binding of the filtered sampler: logits [N, V] bf16/f32 (any row
+    stride), uniforms [N] f32, temperature, top_p, min_p numbers or [N] f32,
+    top_k a number or [N] int32 (None: off), out [N] int32, prob [N] f32 or
+    None; returns the host status code."""
+    if logits.dim() != 2:
+        raise ValueError("logits must be [N, V]")
+    N, V = logits.shape
+    dev = _gpu("logits", logits)
+    stride = _rows("logits", logits, (N, V), logits.dtype, dev)[0]
+    _vector("uniforms", uniforms, (N,), torch.float32, dev)
+    _vector("out", out, (N,), torch.int32, dev)
+    if prob is not None:
+        _vector("prob", prob, (N,), torch.float32, dev)
+    return load_library().spec_filtered_sample(
+        logits.data_ptr(), stride, uniforms.data_ptr(), N, V, _dtype_code(logits),
+        *_setting("temperature", temperature, 1.0, N, torch.float32, dev),
+        *_setting("top_k", top_k, 0, N, torch.int32, dev), *_setting("top_p", top_p, 1.0, N, torch.float32, dev),
+        *_setting("min_p", min_p, 0.0, N, torch.float32, dev), out.data_ptr(), _address(prob),
+        _status_word(status, dev), _raw_stream(dev, stream))
+
+
+def filtered_sample(logits, uniforms, temperature=1.0, *, top_k=None, top_p=None, min_p=None, with_prob=False,
+                    out=None, prob=None, status=None, stream=None):
+    """One token a row after temperature, top-k, top-p and min-p, each a number
+    or a tensor with a setting a row; allocates the outputs that are not given
+    and returns tokens [N] int32 (with the tokens' probabilities among the kept
+    entries [N] f32 when `with_prob` or `prob` is given)."""
+    N = logits.shape[0]
+    made = []
+    with _owned(stream):
+        if out is None:
+            out = torch.empty(N, dtype=torch.int32, device=logits.device)
+            made.append(out)
+        if prob is None and with_prob:
+            prob = torch.empty(N, dtype=torch.float32, device=logits.device)
+            made.append(prob)
+    _shared(stream, *made)
+    rc = spec_filtered_sample(logits, uniforms, temperature, top_k, top_p, min_p, out, prob, status, stream=stream)
+    if rc != SV_OK:
+        raise StatusError(rc, "spec_filtered_sample")
+    return out if prob is None else (out, prob)

@@ -17,7 +17,8 @@ INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libspecverify.so")
 SOURCES = ["sv_kernels.cu", "sv_api.cu", "sv_static_scratch.cu", "sv_lmhead.cu",
-           "sv_tree_io.cu", "sv_tree_attn.cu", "sv_tree_verify.cu"]
+           "sv_tree_io.cu", "sv_tree_attn.cu", "sv_tree_verify.cu", "sv_page_plan.cu", "sv_sparse_attn.cu",
+           "sv_filtered_sample.cu"]
 # Translation units: (source, extra nvcc flags, object). sv_kernels.cu is
 # compiled three times, each unit holding one group of its kernels (SV_TU).
 UNITS = [("sv_kernels.cu", ["-DSV_TU=1"], "sv_kernels_verify.o"),
@@ -28,8 +29,11 @@ UNITS = [("sv_kernels.cu", ["-DSV_TU=1"], "sv_kernels_verify.o"),
          ("sv_lmhead.cu", [], "sv_lmhead.o"),
          ("sv_tree_io.cu", [], "sv_tree_io.o"),
          ("sv_tree_attn.cu", [], "sv_tree_attn.o"),
-         ("sv_tree_verify.cu", [], "sv_tree_verify.o")]
-HEADERS = ["sv_device.cuh", "sv_internal.h", "sv_exp_table.h"]
+         ("sv_tree_verify.cu", [], "sv_tree_verify.o"),
+         ("sv_page_plan.cu", [], "sv_page_plan.o"),
+         ("sv_sparse_attn.cu", [], "sv_sparse_attn.o"),
+         ("sv_filtered_sample.cu", [], "sv_filtered_sample.o")]
+HEADERS = ["sv_device.cuh", "sv_internal.h", "sv_exp_table.h", "sv_tree_attn.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2", "-diag-suppress=177",
          "--expt-relaxed-constexpr"]

@@ -486,7 +486,7 @@ const char* sv_status_string(int status) {
     case SV_OK: return "ok";
     case SV_ERR_NULL: return "a required pointer is NULL";
     case SV_ERR_SHAPE: return "invalid shape (B < 0, K outside [1,64], V < 1, or too large)";
-    case SV_ERR_TEMPERATURE: return "temperature must be finite and > 0";
+    case SV_ERR_TEMPERATURE: return "temperature must be finite and > 0 (spec_filtered_sample: or 0)";
     case SV_ERR_DTYPE: return "dtype must be SV_BF16 or SV_F32 (a cache's: SV_BF16 or SV_E4M3)";
     case SV_ERR_ALIGN: return "pointer misaligned (elements, or 256 bytes for workspace/staging)";
     case SV_ERR_WORKSPACE: return "workspace or staging buffer too small";
@@ -501,7 +501,9 @@ const char* sv_status_string(int status) {
   if (status & SV_DEV_UNIFORM_RANGE) return "device: a uniform is NaN or outside [0, 1]";
   if (status & SV_DEV_TREE) return "device: a malformed tree (a parent or a draft row out of range)";
   if (status & SV_DEV_PAGE_RANGE) return "device: a context or a needed page lies outside the table or the cache";
-  if (status & SV_DEV_SLOT_RANGE) return "device: a slot lies outside the cache";
+  if (status & SV_DEV_SLOT_RANGE) return "device: a slot lies outside the cache, or a token outside the step's slots";
+  if (status & SV_DEV_NO_PAGES) return "device: too few free pages for a request";
+  if (status & SV_DEV_SETTING) return "device: a row's temperature, top_p or min_p is out of range";
   return "unknown status";
 }
 

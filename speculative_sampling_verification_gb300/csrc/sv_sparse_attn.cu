@@ -1,0 +1,766 @@
+// Attention over the pages that a cheap score selects for each query
+// (sv_sparse_attention), and the bounds of a page's keys that the score is made
+// of (sv_page_bounds).
+#include <cfloat>
+#include <cmath>
+#include <cstdint>
+#include <algorithm>
+#include <mutex>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include "../../include/spec_verify.h"
+#include "sv_device.cuh"
+#include "sv_internal.h"
+#include "sv_tree_attn.h"
+
+namespace sv {
+namespace sparse {
+
+constexpr float kAmaxMin = 1e-30f;
+constexpr float kCodeMax = 127.0f;
+
+// ---------------------------------------------------------------- bounds of a page's keys
+//
+// For every channel the least and the largest value of a page's keys, as int8 codes
+// of one scale for the page and head, rounded outwards: code_min scale <= k_d <=
+// code_max scale (to the fp32 rounding of the product that makes the code). A page
+// that holds NaN or infinity gets the scale +inf, which selects it before others.
+//
+// One block a (sequence, head) and a share of the pages that got tokens. A group of
+// lanes takes a key (16 bytes a lane), the groups take the keys in turn, and the
+// groups' minima and maxima meet in shared memory.
+
+constexpr int kBoundThreads = 128;
+
+struct BoundArgs {
+  const void* kc;
+  const float* ks;
+  long long num_pages;
+  int Hkv, D, P, max_pages, B;
+  const int32_t *page_table, *ctx_lens, *new_lens;
+  int8_t* codes;
+  float* scale;
+  unsigned* status;
+  int chunks;
+};
+
+SV_DEVINL float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+SV_DEVINL float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+SV_DEVINL uint32_t min2_nan(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+SV_DEVINL uint32_t max2_nan(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Four e4m3 codes as floats.
+SV_DEVINL void e4m3x4(uint32_t w, float (&v)[4]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> (16 * i)), __NV_E4M3);
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
+}
+
+template <bool F8, bool VEC>
+__global__ void __launch_bounds__(kBoundThreads) page_bounds_kernel(const __grid_constant__ BoundArgs a) {
+  extern __shared__ float part[];  // [groups][2][D]
+  __shared__ float red[kBoundThreads / 32];
+  constexpr int PER = F8 ? 16 : 8;  // values of 16 bytes
+  const int chunk = blockIdx.x % a.chunks, hk = blockIdx.x / a.chunks % a.Hkv, b = blockIdx.x / a.chunks / a.Hkv;
+  const int tid = threadIdx.x;
+  const long long ctx = a.ctx_lens[b], add = a.new_lens[b];
+  if (add <= 0) return;
+  const long long end = ctx + add;
+  if (ctx < 0 || end > (long long)a.max_pages * a.P) {
+    if (tid == 0 && a.status) atomicOr(a.status, (unsigned)SV_DEV_PAGE_RANGE);
+    return;
+  }
+  const int p1 = (int)((end + a.P - 1) / a.P);
+  const int lanes = VEC ? a.D / PER : 1, groups = VEC ? kBoundThreads / lanes : 1;
+  const int g = VEC ? tid / lanes : 0, col = VEC ? (tid - g * lanes) * PER : 0;
+  for (int p = (int)(ctx / a.P) + chunk; p < p1; p += a.chunks) {
+    const int id = a.page_table[(long long)b * a.max_pages + p];
+    if (id < 0 || id >= a.num_pages) {
+      if (tid == 0 && a.status) atomicOr(a.status, (unsigned)SV_DEV_PAGE_RANGE);
+      continue;
+    }
+    const int count = (int)min((long long)a.P, end - (long long)p * a.P);
+    const long long row0 = ((long long)id * a.Hkv + hk) * a.P;
+    if constexpr (VEC) {
+      if (g < groups) {
+        float lo[PER], hi[PER];
+        if constexpr (!F8) {
+          uint32_t l[4], h[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) l[i] = 0x7f807f80u, h[i] = 0xff80ff80u;
+#pragma unroll 4
+          for (int r = g; r < count; r += groups) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.kc) +
+                                                                 (row0 + r) * a.D + col));
+            l[0] = min2_nan(l[0], v.x), h[0] = max2_nan(h[0], v.x);
+            l[1] = min2_nan(l[1], v.y), h[1] = max2_nan(h[1], v.y);
+            l[2] = min2_nan(l[2], v.z), h[2] = max2_nan(h[2], v.z);
+            l[3] = min2_nan(l[3], v.w), h[3] = max2_nan(h[3], v.w);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            lo[2 * i] = bf16_lo(l[i]), lo[2 * i + 1] = bf16_hi(l[i]);
+            hi[2 * i] = bf16_lo(h[i]), hi[2 * i + 1] = bf16_hi(h[i]);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < PER; ++i) lo[i] = INFINITY, hi[i] = -INFINITY;
+#pragma unroll 2
+          for (int r = g; r < count; r += groups) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(a.kc) +
+                                                                 (row0 + r) * a.D + col));
+            const float s = __ldg(a.ks + row0 + r);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              float x[4];
+              e4m3x4(w[q], x);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float y = __fmul_rn(x[i], s);
+                lo[4 * q + i] = min_nan(lo[4 * q + i], y);
+                hi[4 * q + i] = max_nan(hi[4 * q + i], y);
+              }
+            }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          part[(2 * g) * a.D + col + i] = lo[i];
+          part[(2 * g + 1) * a.D + col + i] = hi[i];
+        }
+      }
+    } else {
+      for (int d = tid; d < a.D; d += kBoundThreads) {
+        float lo = INFINITY, hi = -INFINITY;
+        for (int r = 0; r < count; ++r) {
+          const long long at = (row0 + r) * a.D + d;
+          float y;
+          if constexpr (F8) {
+            const __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<const unsigned char*>(a.kc)[at], __NV_E4M3);
+            y = __fmul_rn(__half2float(*reinterpret_cast<const __half*>(&h)), a.ks[row0 + r]);
+          } else {
+            y = __bfloat162float(static_cast<const __nv_bfloat16*>(a.kc)[at]);
+          }
+          lo = min_nan(lo, y);
+          hi = max_nan(hi, y);
+        }
+        part[d] = lo;
+        part[a.D + d] = hi;
+      }
+    }
+    __syncthreads();
+    // The groups' bounds of each channel, and the largest magnitude of all.
+    float amax = 0.0f;
+    for (int d = tid; d < a.D; d += kBoundThreads) {
+      float lo = part[d], hi = part[a.D + d];
+#pragma unroll 4
+      for (int k = 1; k < groups; ++k) {
+        lo = min_nan(lo, part[2 * k * a.D + d]);
+        hi = max_nan(hi, part[(2 * k + 1) * a.D + d]);
+      }
+      part[d] = lo;
+      part[a.D + d] = hi;
+      amax = max_nan(amax, max_nan(fabsf(lo), fabsf(hi)));  // |NaN| is NaN
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    if ((tid & 31) == 0) red[tid >> 5] = amax;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kBoundThreads / 32; ++i) amax = max_nan(amax, red[i]);
+    const bool fine = amax <= FLT_MAX;
+    const float top = fmaxf(amax, kAmaxMin), up = __fdiv_rn(kCodeMax, top);
+    const long long at = ((long long)id * a.Hkv + hk) * 2 * a.D;
+    for (int d = tid; d < a.D; d += kBoundThreads) {
+      const float lo = floorf(__fmul_rn(part[d], up)), hi = ceilf(__fmul_rn(part[a.D + d], up));
+      a.codes[at + d] = fine ? (int8_t)(int)fminf(fmaxf(lo, -kCodeMax), kCodeMax) : (int8_t)0;
+      a.codes[at + a.D + d] = fine ? (int8_t)(int)fminf(fmaxf(hi, -kCodeMax), kCodeMax) : (int8_t)0;
+    }
+    if (tid == 0) a.scale[(long long)id * a.Hkv + hk] = fine ? __fdiv_rn(top, kCodeMax) : INFINITY;
+    __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------- selection
+//
+// A query row and key/value head are an item, worked on by a cluster of CTAs that
+// share its pages. The group's queries become int8 codes (one scale a head), so that
+// a page's score is a whole number times two scales: the same whatever the order of
+// the sum, and four channels an instruction. sum_d max(q_d min_d, q_d max_d) splits by
+// the sign of q: the lanes that hold a page's minima use the negative codes, those that
+// hold its maxima the positive ones, and a page is one dot product of 2 D values. The scores go
+// as ordered 32-bit keys to the first CTA, which finds the budget-th largest by
+// halving the range of keys, bit by bit, and writes the chosen pages in their order.
+
+constexpr int kSelThreads = 256;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kSelPagesMax = 49152;  // keys of a row in shared memory
+constexpr unsigned kForced = 0xffffffffu;
+
+struct SelArgs {
+  const __nv_bfloat16* q;
+  long long q_sn, q_sh;
+  const int8_t* codes;
+  const float* scale;
+  const int32_t *page_table, *positions, *seqs;
+  int32_t *selected, *table, *ctx, *parent;
+  unsigned* clear;
+  int clear_words;
+  long long num_pages;
+  int N, B, Hq, Hkv, D, P, max_pages, budget, sink, recent, nc, ids_cap;
+};
+
+SV_DEVINL unsigned ordered(float f) {
+  const unsigned b = __float_as_uint(f + 0.0f);  // -0 is 0
+  return b ^ ((unsigned)((int)b >> 31) | 0x80000000u);
+}
+
+SV_DEVINL void dsmem_st_u32(unsigned a, unsigned v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+
+SV_DEVINL void store_key(unsigned keys0, int p, unsigned key, bool cluster) {
+  if (cluster)
+    dsmem_st_u32(keys0 + p * 4, key);
+  else
+    asm volatile("st.shared::cta.u32 [%0], %1;" ::"r"(keys0 + p * 4), "r"(key) : "memory");
+}
+
+// The head whose sum page_score leaves in lane li of a page's LP lanes.
+template <int LP, int HC>
+SV_DEVINL int lane_head(int li) {
+  int head = 0, step = LP / 2;
+#pragma unroll
+  for (int n = HC; n > 1; n >>= 1, step >>= 1)
+    if (li & step) head += n / 2;
+  return head;
+}
+
+// Sum over the LP lanes of a page of HC heads' products, times the heads' scales (`qs`: that
+// of lane_head), and the largest over the heads, the same in all LP lanes. The first steps hand half
+// of the heads over, so that a value takes about one exchange.
+template <int LP, int HC>
+SV_DEVINL float page_score(int (&v)[HC], float qs, int li) {
+  int step = LP / 2;
+#pragma unroll
+  for (int n = HC; n > 1; n >>= 1, step >>= 1) {
+    const bool up = li & step;
+#pragma unroll
+    for (int i = 0; i < n / 2; ++i) {
+      const int give = up ? v[i] : v[i + n / 2];
+      const int keep = up ? v[i + n / 2] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, step);
+    }
+  }
+#pragma unroll
+  for (int o = LP / 2 / HC; o > 0; o >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+  float s = __fmul_rn((float)v[0], qs);
+#pragma unroll
+  for (int o = LP / 2; o >= LP / HC; o >>= 1) s = fmaxf(s, __shfl_xor_sync(0xffffffffu, s, o));
+  return s;
+}
+
+// LP lanes hold the 2 D codes of a page, 16 each (LP = 0: any D, a warp a page); HC heads at a time.
+template <int LP, int HC>
+__global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_constant__ SelArgs a) {
+  extern __shared__ __align__(16) unsigned char dyn[];
+  unsigned* keys = reinterpret_cast<unsigned*>(dyn);               // [max_pages] (first CTA)
+  int* ids = reinterpret_cast<int*>(dyn + (size_t)a.max_pages * 4);  // [ids_cap] this CTA's pages
+  signed char* qcode = reinterpret_cast<signed char*>(ids + a.ids_cap);  // [HC][Dp]
+  __shared__ float qscale[8];
+  __shared__ unsigned faults[16];
+  __shared__ int wsum[kSelWarps], wsum2[kSelWarps];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const unsigned rank = a.nc > 1 ? cluster_ctarank() : 0;
+  if (a.nc > 1) cluster_arrive_relaxed();
+  const long long item = blockIdx.x / a.nc;
+  const int h = (int)(item % a.Hkv);
+  const long long n = item / a.Hkv;
+  const int G = a.Hq / a.Hkv;
+  if (blockIdx.x == 0)
+    for (int i = tid; i < a.clear_words; i += kSelThreads) a.clear[i] = 0;
+
+  const int pos = a.positions[n], seq = a.seqs ? a.seqs[n] : (int)n;
+  const bool empty = pos == -1 || seq == -1;
+  bool fault = !empty && (pos < 0 || (long long)pos >= (long long)a.max_pages * a.P || seq < 0 || seq >= a.B);
+  const int np = empty || fault ? 0 : pos / a.P + 1;
+  const int K = min(a.budget, np);
+  const int32_t* table = a.page_table + (long long)(np ? seq : 0) * a.max_pages;
+
+  // This CTA's pages.
+  const int share = (np + a.nc - 1) / a.nc;
+  const int first = min(np, (int)rank * share), mine = min(np, first + share) - first;
+  bool bad = false;
+  for (int i = tid; i < mine; i += kSelThreads) {
+    const int id = table[first + i];
+    const bool out = id < 0 || id >= a.num_pages;
+    bad |= out;
+    ids[i] = out ? 0 : id;
+  }
+  bad = __syncthreads_or(bad);
+  const bool rank_pages = np > a.budget;  // else all are chosen
+  if (a.nc > 1) cluster_wait();
+  const unsigned keys0 = a.nc > 1 ? dsmem_map(smem_u32(keys), 0) : smem_u32(keys);
+  if (tid == 0) {
+    if (a.nc > 1)
+      dsmem_st_u32(dsmem_map(smem_u32(&faults[rank]), 0), bad);
+    else
+      faults[0] = bad;
+  }
+
+  // The key of page p, this CTA's page i. With more than HC heads the largest so far stays here
+  // (rank 0: in its place; there i is p) and goes to the first CTA after the last heads.
+  auto put_key = [&](int h0, int i, int p, float best, float ps) {
+    const float s = isinf(ps) ? INFINITY : __fmul_rn(best, ps);
+    unsigned key = p < a.sink || p >= np - a.recent ? kForced : ordered(s);
+    if (h0 > 0) key = max(key, keys[i]);
+    if (h0 + HC < G)
+      keys[i] = key;
+    else
+      store_key(keys0, p, key, a.nc > 1);
+  };
+
+  if (rank_pages) {
+    const int Dp = (a.D + 15) & ~15;
+#pragma unroll 1
+    for (int h0 = 0; h0 < G; h0 += HC) {
+      if (h0) __syncthreads();
+      // A warp a head: its largest magnitude, then its codes.
+      for (int j = warp; j < HC; j += kSelWarps) {
+        float top = 0.0f;
+        bool fin = true;
+        const __nv_bfloat16* qr = a.q + n * a.q_sn + (long long)(h * G + h0 + j) * a.q_sh;
+        const bool on = h0 + j < G;
+        for (int d = lane; on && d < a.D; d += 32) {
+          const float x = fabsf(__bfloat162float(qr[d]));
+          fin = fin && x <= FLT_MAX;
+          top = fmaxf(top, x);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        fin = __all_sync(0xffffffffu, fin) && on;
+        top = fmaxf(top, kAmaxMin);
+        const float up = __fdiv_rn(kCodeMax, top);
+        for (int d = lane; d < Dp; d += 32) {
+          const float x = fin && d < a.D ? rintf(__fmul_rn(__bfloat162float(qr[d]), up)) : 0.0f;
+          qcode[j * Dp + d] = (signed char)(int)fminf(fmaxf(x, -kCodeMax), kCodeMax);
+        }
+        if (lane == 0) qscale[j] = fin ? __fdiv_rn(top, kCodeMax) : 0.0f;
+      }
+      __syncthreads();
+      if constexpr (LP > 0) {
+        constexpr int PPW = 32 / LP, U = 4;
+        const int li = lane % LP, sub = lane / LP, half = a.D / 16;
+        const bool used = li < 2 * half, upper = li >= half;
+        const int off = (upper ? li - half : li) * 16;
+        int qv[HC][4];
+#pragma unroll
+        for (int j = 0; j < HC; ++j)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const unsigned w = used ? *reinterpret_cast<const unsigned*>(qcode + j * Dp + off + 4 * k) : 0u;
+            const unsigned neg = __vcmpgtu4(w & 0x80808080u, 0u);  // bytes below zero
+            qv[j][k] = (int)(upper ? w & ~neg : w & neg);
+          }
+        const float my_qs = qscale[lane_head<LP, HC>(li)];
+#pragma unroll 1
+        for (int i0 = warp * PPW * U; i0 < mine; i0 += kSelWarps * PPW * U) {
+          uint4 c[U];
+          float ps[U];
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const int i = min(i0 + u * PPW + sub, mine - 1);
+            const long long at = (long long)ids[i] * a.Hkv + h;
+            c[u] = used ? __ldg(reinterpret_cast<const uint4*>(a.codes + at * 2 * a.D) + li) : make_uint4(0, 0, 0, 0);
+            ps[u] = __ldg(a.scale + at);
+          }
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            int v[HC];
+#pragma unroll
+            for (int j = 0; j < HC; ++j) {
+              int s = __dp4a((int)c[u].x, qv[j][0], 0);
+              s = __dp4a((int)c[u].y, qv[j][1], s);
+              s = __dp4a((int)c[u].z, qv[j][2], s);
+              v[j] = __dp4a((int)c[u].w, qv[j][3], s);
+            }
+            float best;
+            if (h0 + HC <= G) {
+              best = page_score<LP, HC>(v, my_qs, li);
+            } else {
+              best = -INFINITY;
+#pragma unroll
+              for (int j = 0; j < HC; ++j) {
+                int s = v[j];
+#pragma unroll
+                for (int o = LP / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+                if (h0 + j < G) best = fmaxf(best, __fmul_rn((float)s, qscale[j]));
+              }
+            }
+            const int i = i0 + u * PPW + sub, p = first + i;
+            if (li == 0 && i < mine) {
+              put_key(h0, i, p, best, ps[u]);
+            }
+          }
+        }
+      } else {
+        for (int i = warp; i < mine; i += kSelWarps) {
+          const int p = first + i;
+          const long long at = (long long)ids[i] * a.Hkv + h;
+          float best = -INFINITY;
+          for (int j = 0; j < HC && h0 + j < G; ++j) {
+            int s = 0;
+            for (int d = lane; d < a.D; d += 32) {
+              const int x = qcode[j * Dp + d];
+              s += x * (int)a.codes[at * 2 * a.D + (x > 0 ? a.D : 0) + d];
+            }
+            s = __reduce_add_sync(0xffffffffu, s);
+            best = fmaxf(best, __fmul_rn((float)s, qscale[j]));
+          }
+          if (lane == 0) {
+            put_key(h0, i, p, best, a.scale[at]);
+          }
+        }
+      }
+    }
+  }
+  if (a.nc > 1) cluster_sync();
+  if (rank != 0) return;
+  __syncthreads();
+  for (int i = 0; i < a.nc; ++i) fault = fault || faults[i] != 0;
+
+  int32_t* sel = a.selected ? a.selected + item * a.budget : nullptr;
+  int32_t* out = a.table + item * a.budget;
+  const int take = fault ? 0 : K;
+  if (h == 0 && tid == 0) {
+    // The chosen pages' keys as a context of their own: the last page is always
+    // chosen and ends with the query's own key.
+    a.ctx[n] = fault ? -1 : empty ? 0 : (K - 1) * a.P + pos % a.P;
+    a.parent[n] = empty ? -2 : -1;
+  }
+  for (int i = take + tid; i < a.budget; i += kSelThreads) {
+    if (sel) sel[i] = -1;
+    out[i] = -1;
+  }
+  if (take == 0) return;
+  if (!rank_pages) {
+    for (int i = tid; i < take; i += kSelThreads) {
+      if (sel) sel[i] = i;
+      out[i] = table[i];
+    }
+    return;
+  }
+  // The largest key that at least K keys reach.
+  unsigned cut = 0;
+  int at_least = np;
+#pragma unroll 1
+  for (int bit = 31; bit >= 0 && at_least != K; --bit) {
+    const unsigned tried = cut | (1u << bit);
+    int c = 0;
+    for (int i = tid; i < np; i += kSelThreads) c += keys[i] >= tried;
+    c = __reduce_add_sync(0xffffffffu, c);
+    if (lane == 0) (bit & 1 ? wsum : wsum2)[warp] = c;
+    __syncthreads();
+    c = 0;
+#pragma unroll
+    for (int i = 0; i < kSelWarps; ++i) c += (bit & 1 ? wsum : wsum2)[i];
+    if (c >= K) {
+      cut = tried;
+      at_least = c;
+    }
+  }
+  // Keys above the cut, and the first of those equal to it. A warp takes a run of pages.
+  const int run = (np + kSelWarps - 1) / kSelWarps;
+  const int r0 = min(np, warp * run), r1 = min(np, r0 + run);
+  int above = 0, equal = 0;
+  for (int i = r0 + lane; i < r1; i += 32) {
+    above += keys[i] > cut;
+    equal += keys[i] == cut;
+  }
+  above = __reduce_add_sync(0xffffffffu, above);
+  equal = __reduce_add_sync(0xffffffffu, equal);
+  __syncthreads();
+  if (lane == 0) {
+    wsum[warp] = above;
+    wsum2[warp] = equal;
+  }
+  __syncthreads();
+  int all_above = 0, above0 = 0, equal0 = 0;
+#pragma unroll
+  for (int i = 0; i < kSelWarps; ++i) {
+    if (i < warp) {
+      above0 += wsum[i];
+      equal0 += wsum2[i];
+    }
+    all_above += wsum[i];
+  }
+  const int ties = K - all_above;
+  for (int i0 = r0; i0 < r1; i0 += 32) {
+    const int i = i0 + lane;
+    const unsigned key = i < r1 ? keys[i] : 0u;
+    const bool gt = i < r1 && key > cut, eq = i < r1 && key == cut;
+    const unsigned bg = __ballot_sync(0xffffffffu, gt), be = __ballot_sync(0xffffffffu, eq);
+    const unsigned below = (1u << lane) - 1;
+    const int ng = above0 + __popc(bg & below), ne = equal0 + __popc(be & below);
+    if (gt || (eq && ne < ties)) {
+      const int to = ng + min(ne, ties);
+      if (sel) sel[to] = i;
+      out[to] = table[i];
+    }
+    above0 += __popc(bg);
+    equal0 += __popc(be);
+  }
+}
+
+// ---------------------------------------------------------------- host side
+
+bool misaligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
+
+struct Layout {
+  size_t off_table, off_ctx, off_parent, total;
+};
+
+bool sizes_ok(int N, int Hq, int Hkv, int D, int max_pages, int page_size, int budget) {
+  // The chosen pages are a page table of `budget` entries a head to the attention.
+  return tat::sizes_ok(N, 1, Hq, Hkv, D, max_pages, page_size) && max_pages <= kSelPagesMax && budget >= 1 &&
+         tat::sizes_ok(N, 1, Hq, Hkv, D, budget, page_size) && (long long)N * Hkv < (1ll << 27);
+}
+
+Layout make_layout(int N, int Hq, int Hkv, int D, int page_size, int budget) {
+  Layout L{};
+  size_t off = align_up(sv_tree_attention_workspace_size(N, 1, Hq, Hkv, D, budget, page_size), 256);
+  L.off_table = off;
+  off = align_up(off + (size_t)N * Hkv * budget * 4, 256);
+  L.off_ctx = off;
+  off = align_up(off + (size_t)N * 4, 256);
+  L.off_parent = off;
+  off = align_up(off + (size_t)N * 4, 256);
+  L.total = off;
+  return L;
+}
+
+template <int LP, int HC>
+int launch_select(const SelArgs& a, size_t smem, cudaStream_t st) {
+  static std::mutex mu;
+  static bool set[64] = {};
+  int device = 0;
+  if (cudaGetDevice(&device) != cudaSuccess || device < 0 || device >= 64) return SV_ERR_CUDA;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!set[device]) {
+      if (cudaFuncSetAttribute(select_kernel<LP, HC>, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024) !=
+          cudaSuccess)
+        return SV_ERR_CUDA;
+      set[device] = true;
+    }
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((long long)a.N * a.Hkv * a.nc));
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)a.nc;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, select_kernel<LP, HC>, a) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+}
+
+int launch_select_any(SelArgs& a, cudaStream_t st) {
+  // CTAs of an item: as many as keep all SMs busy with few items, and no fewer than 128 pages each.
+  const long long items = (long long)a.N * a.Hkv;
+  a.nc = 1;
+  while (a.nc < 8 && items * a.nc * 2 <= 1216 && a.max_pages >= 256 * a.nc) a.nc *= 2;
+  a.ids_cap = ((a.max_pages + a.nc - 1) / a.nc + 3) & ~3;
+  const int G = a.Hq / a.Hkv, hc = G <= 4 ? 4 : 8;
+  const size_t smem = (size_t)((a.max_pages + 3) & ~3) * 4 + (size_t)a.ids_cap * 4 + (size_t)hc * ((a.D + 15) & ~15);
+  if (smem > 220 * 1024) return SV_ERR_SHAPE;
+  const int lp = a.D % 16 || a.D > 256 || misaligned(a.codes, 16) ? 0 : a.D <= 64 ? 8 : a.D <= 128 ? 16 : 32;
+  if (hc == 4) {
+    switch (lp) {
+      case 8: return launch_select<8, 4>(a, smem, st);
+      case 16: return launch_select<16, 4>(a, smem, st);
+      case 32: return launch_select<32, 4>(a, smem, st);
+      default: return launch_select<0, 4>(a, smem, st);
+    }
+  }
+  switch (lp) {
+    case 8: return launch_select<8, 8>(a, smem, st);
+    case 16: return launch_select<16, 8>(a, smem, st);
+    case 32: return launch_select<32, 8>(a, smem, st);
+    default: return launch_select<0, 8>(a, smem, st);
+  }
+}
+
+}  // namespace sparse
+}  // namespace sv
+
+using namespace sv::sparse;
+
+extern "C" {
+
+int sv_page_bounds(const void* k_cache, const float* k_scale, int64_t num_pages, int page_size, int cache_dtype,
+                   const int32_t* page_table, const int32_t* ctx_lens, const int32_t* new_lens, int B, int Hkv,
+                   int D, int max_pages, int8_t* codes, float* scale, uint32_t* status, void* stream) {
+  if (cache_dtype != SV_BF16 && cache_dtype != SV_E4M3) return SV_ERR_DTYPE;
+  if (B < 0 || Hkv < 1 || D < 1 || D > sv::kHeadDimMax || max_pages < 1 || page_size < 1 || num_pages < 1 ||
+      num_pages > (1ll << 31) || (long long)max_pages * page_size >= (1ll << 31) || (long long)B * Hkv >= (1ll << 27))
+    return SV_ERR_SHAPE;
+  if (B == 0) return SV_OK;
+  if (!k_cache || !page_table || !ctx_lens || !new_lens || !codes || !scale) return SV_ERR_NULL;
+  if (cache_dtype == SV_E4M3 && !k_scale) return SV_ERR_NULL;
+  if (misaligned(k_cache, cache_dtype == SV_BF16 ? 2 : 1) || misaligned(page_table, 4) || misaligned(ctx_lens, 4) ||
+      misaligned(new_lens, 4) || misaligned(scale, 4) || misaligned(status, 4) ||
+      (cache_dtype == SV_E4M3 && misaligned(k_scale, 4)))
+    return SV_ERR_ALIGN;
+  BoundArgs a{};
+  a.kc = k_cache;
+  a.ks = k_scale;
+  a.num_pages = num_pages;
+  a.Hkv = Hkv;
+  a.D = D;
+  a.P = page_size;
+  a.max_pages = max_pages;
+  a.B = B;
+  a.page_table = page_table;
+  a.ctx_lens = ctx_lens;
+  a.new_lens = new_lens;
+  a.codes = codes;
+  a.scale = scale;
+  a.status = status;
+  // Blocks for eight a SM: the pages of a (sequence, head) are shared among them.
+  const long long items = (long long)B * Hkv;
+  a.chunks = (int)std::max(1ll, std::min((long long)max_pages, 1216 / items));
+  const bool f8 = cache_dtype == SV_E4M3;
+  const int per = f8 ? 16 : 8;
+  const bool vec = D % per == 0 && !misaligned(k_cache, 16);
+  const int groups = vec ? kBoundThreads / (D / per) : 1;
+  const size_t smem = (size_t)groups * 2 * D * 4;
+  const unsigned grid = (unsigned)(items * a.chunks);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (f8 && vec)
+    page_bounds_kernel<true, true><<<grid, kBoundThreads, smem, st>>>(a);
+  else if (f8)
+    page_bounds_kernel<true, false><<<grid, kBoundThreads, smem, st>>>(a);
+  else if (vec)
+    page_bounds_kernel<false, true><<<grid, kBoundThreads, smem, st>>>(a);
+  else
+    page_bounds_kernel<false, false><<<grid, kBoundThreads, smem, st>>>(a);
+  return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+}
+
+size_t sv_sparse_attention_workspace_size(int N, int Hq, int Hkv, int D, int max_pages, int page_size, int budget) {
+  if (!sizes_ok(N, Hq, Hkv, D, max_pages, page_size, budget)) return 0;
+  return make_layout(N, Hq, Hkv, D, page_size, budget).total;
+}
+
+int sv_sparse_attention(const void* q, int64_t q_stride_n, int64_t q_stride_h, const void* k_cache,
+                        const void* v_cache, const float* k_scale, const float* v_scale, int64_t num_pages,
+                        int page_size, int cache_dtype, const int8_t* codes, const float* bound_scale,
+                        const int32_t* page_table, const int32_t* positions, const int32_t* seqs, int N, int B,
+                        int Hq, int Hkv, int D, int max_pages, int budget, int sink, int recent, float scale,
+                        void* out, int32_t* selected, void* workspace, size_t workspace_bytes, void* stream) {
+  if (cache_dtype != SV_BF16 && cache_dtype != SV_E4M3) return SV_ERR_DTYPE;
+  if (!sizes_ok(N, Hq, Hkv, D, max_pages, page_size, budget) || B < 0 || num_pages < 1 || num_pages > (1ll << 31) ||
+      sink < 0 || recent < 1 || (long long)sink + recent > budget || !std::isfinite(scale) || !(scale > 0.0f))
+    return SV_ERR_SHAPE;
+  if (N == 0) return SV_OK;
+  if (!seqs && N > B) return SV_ERR_SHAPE;
+  if (!q || !k_cache || !v_cache || !codes || !bound_scale || !page_table || !positions || !out || !workspace)
+    return SV_ERR_NULL;
+  if (cache_dtype == SV_E4M3 && (!k_scale || !v_scale)) return SV_ERR_NULL;
+  const size_t ces = cache_dtype == SV_BF16 ? 2 : 1;
+  if (misaligned(q, 2) || misaligned(out, 2) || misaligned(k_cache, ces) || misaligned(v_cache, ces) ||
+      misaligned(bound_scale, 4) || misaligned(page_table, 4) || misaligned(positions, 4) || misaligned(seqs, 4) ||
+      misaligned(selected, 4) || misaligned(workspace, 256) ||
+      (cache_dtype == SV_E4M3 && (misaligned(k_scale, 4) || misaligned(v_scale, 4))))
+    return SV_ERR_ALIGN;
+  const Layout L = make_layout(N, Hq, Hkv, D, page_size, budget);
+  if (workspace_bytes < L.total) return SV_ERR_WORKSPACE;
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  SelArgs s{};
+  s.q = static_cast<const __nv_bfloat16*>(q);
+  s.q_sn = q_stride_n;
+  s.q_sh = q_stride_h;
+  s.codes = codes;
+  s.scale = bound_scale;
+  s.page_table = page_table;
+  s.positions = positions;
+  s.seqs = seqs;
+  s.selected = selected;
+  s.table = reinterpret_cast<int32_t*>(ws + L.off_table);
+  s.ctx = reinterpret_cast<int32_t*>(ws + L.off_ctx);
+  s.parent = reinterpret_cast<int32_t*>(ws + L.off_parent);
+  s.clear = reinterpret_cast<unsigned*>(ws);
+  s.clear_words = (int)sv::tat::cleared_words(1, Hq, Hkv, D, page_size);
+  s.num_pages = num_pages;
+  s.N = N;
+  s.B = B;
+  s.Hq = Hq;
+  s.Hkv = Hkv;
+  s.D = D;
+  s.P = page_size;
+  s.max_pages = max_pages;
+  s.budget = budget;
+  s.sink = sink;
+  s.recent = recent;
+  const int rc = launch_select_any(s, st);
+  if (rc != SV_OK) return rc;
+  sv::tat::Args a{};
+  a.q = s.q;
+  a.q_sb = q_stride_n;
+  a.q_st = 0;
+  a.q_sh = q_stride_h;
+  a.kc = k_cache;
+  a.vc = v_cache;
+  a.ks = k_scale;
+  a.vs = v_scale;
+  a.page_table = s.table;
+  a.ctx_lens = s.ctx;
+  a.parents = s.parent;
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.status = static_cast<unsigned*>(workspace);
+  a.num_pages = num_pages;
+  a.B = N;
+  a.T = 1;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.D = D;
+  a.P = page_size;
+  a.max_pages = budget;
+  a.table_heads = Hkv;
+  a.chained = 1;
+  a.scale = scale;
+  return sv::tat::launch_attention(a, cache_dtype, workspace, st);
+}
+
+}  // extern "C"

@@ -17,24 +17,10 @@
 #include "../../include/spec_verify.h"
 #include "sv_device.cuh"
 #include "sv_internal.h"
+#include "sv_tree_attn.h"
 
 namespace sv {
 namespace tat {
-
-constexpr int kTreeMax = 128;
-
-struct Args {
-  const __nv_bfloat16* q;
-  long long q_sb, q_st, q_sh;
-  const void *kc, *vc;
-  const float *ks, *vs;
-  const int32_t *page_table, *ctx_lens, *parents;
-  __nv_bfloat16* out;
-  unsigned* status;
-  long long num_pages;
-  int B, T, Hq, Hkv, D, P, max_pages;
-  float scale;
-};
 
 // ---------------------------------------------------------------- tensor cores
 //
@@ -549,6 +535,7 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
   const int group = blockIdx.x / x.parts_per_item, part = blockIdx.x % x.parts_per_item;
   constexpr int kSoft = NS * 8;  // softmax warps at work
 
+  if (a.chained) wait_for_clear();
   if (warp == 0) {
     find_range<KT>(x, t, group, lane);
   } else if (warp == kProducer && lane == 0) {
@@ -618,7 +605,7 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
         const int pos = tile * KT + lane * x.box;
         int page = -1;
         if (seq_ok && lane < boxes && pos < w.ctx + live && (pos >> x.lp) < a.max_pages)
-          page = a.page_table[(long long)w.b * a.max_pages + (pos >> x.lp)];
+          page = a.page_table[table_row(a, w.b, w.hk) + (pos >> x.lp)];
         if (page < 0 || page >= a.num_pages) page = -1;
         const unsigned hit = __ballot_sync(0xffffffffu, page >= 0);
         const int y = pos & (a.P - 1);
@@ -865,7 +852,7 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
               for (int j = max(0, p * a.P - w.ctx); j < j1 && !used; ++j) used = par[j] != -2;
             }
             if (!used) continue;
-            const int id = p < a.max_pages ? a.page_table[(long long)w.b * a.max_pages + p] : -1;
+            const int id = p < a.max_pages ? a.page_table[table_row(a, w.b, w.hk) + p] : -1;
             if (id < 0 || id >= a.num_pages) bad |= SV_DEV_PAGE_RANGE;
           }
         }
@@ -1082,7 +1069,7 @@ __global__ void __launch_bounds__(Cfg<DP, F8, SHARED>::kThreads, 1)
               for (int k = 1; k < 4; ++k)
                 if (k == nd >> 5) word = anc[k];
               if (!(word >> (nd & 31) & 1u) || (pos >> x.lp) >= a.max_pages) continue;
-              const int id = a.page_table[(long long)w.b * a.max_pages + (pos >> x.lp)];
+              const int id = a.page_table[table_row(a, w.b, w.hk) + (pos >> x.lp)];
               if (id < 0 || id >= a.num_pages) continue;
               const __nv_bfloat16* vr = static_cast<const __nv_bfloat16*>(a.vc) +
                                         (((long long)id * a.Hkv + w.hk) * a.P + (pos & (a.P - 1))) * a.D + col;
@@ -1326,6 +1313,7 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int group = blockIdx.x;
 
+  if (a.chained) wait_for_clear();
   if (warp == 0) {
     find_range<KT>(x, t, group, lane);
   } else if (warp == kProducer && lane == 0) {
@@ -1382,7 +1370,7 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
         const int pos = tile * KT + lane * x.box;
         int page = -1;
         if (seq_ok && lane < KT / x.box && pos < w.ctx + live && (pos >> x.lp) < a.max_pages)
-          page = a.page_table[(long long)w.b * a.max_pages + (pos >> x.lp)];
+          page = a.page_table[table_row(a, w.b, w.hk) + (pos >> x.lp)];
         if (page < 0 || page >= a.num_pages) page = -1;
         const unsigned hit = __ballot_sync(0xffffffffu, page >= 0);
         const int s = (int)(entry % C::kSlots);
@@ -1572,7 +1560,7 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
       if (!ctx_ok(a, it.ctx) || it.t0 + i >= it.t1 || pos >= (long long)it.ctx + a.T ||
           (pos >> x.lp) >= a.max_pages)
         return -1;
-      return a.page_table[(long long)it.b * a.max_pages + (pos >> x.lp)];
+      return a.page_table[table_row(a, it.b, it.hk) + (pos >> x.lp)];
     };
     auto scales_of = [&](const Walk<KT>& it, int i, int id, float* k, float* v) {
       *k = *v = 0.0f;
@@ -1910,7 +1898,7 @@ __global__ void __launch_bounds__(FewCfg<RP, F8>::kThreads, 1)
           for (int k = 0; k < a.T; ++k) {
             const long long pos = (long long)w.ctx + k;
             if (pos < (long long)w.t0 * KT || pos >= (long long)w.t1 * KT || (pos >> x.lp) >= a.max_pages) continue;
-            const int pg = a.page_table[(long long)w.b * a.max_pages + (pos >> x.lp)];
+            const int pg = a.page_table[table_row(a, w.b, w.hk) + (pos >> x.lp)];
             if (pg < 0 || pg >= a.num_pages || !(anc[r / G] >> k & 1ull)) continue;
             const long long at = (((long long)pg * a.Hkv + w.hk) * a.P + (pos & (a.P - 1))) * a.D + wt;
             const float z = F8 ? ((static_cast<const unsigned char*>(a.vc)[at] & 0x7f) == 0x7f
@@ -1995,7 +1983,7 @@ __global__ void __launch_bounds__(kAnyThreads) tree_attn_any_kernel(Args a) {
   bad_tree = __any_sync(0xffffffffu, bad_tree);
   live = __reduce_max_sync(0xffffffffu, live);
   const int ctx = a.ctx_lens[b];
-  const int32_t* table = a.page_table + (long long)b * a.max_pages;
+  const int32_t* table = a.page_table + table_row(a, b, hk);
   bool bad_page = ctx < 0 || (long long)ctx + live > (long long)a.max_pages * a.P;
   if (!bad_page && !bad_tree) {
     const int need = (int)(((long long)ctx + live + a.P - 1) / a.P);
@@ -2250,6 +2238,47 @@ int launch_tc_any(TcArgs& x, const Plan& p, cudaStream_t st) {
   return p.shared ? launch_tc<64, F8, true>(x, st) : launch_tc<64, F8, false>(x, st);
 }
 
+size_t cleared_words(int T, int Hq, int Hkv, int D, int page_size) {
+  return tc_shape(D, page_size) ? make_plan(T, Hq, Hkv, D).off_ml / 4 : 1;
+}
+
+int launch_attention(const Args& a, int cache_dtype, void* workspace, cudaStream_t st) {
+  // 16-byte aligned rows for the tensor-core kernel; scales are copied in 16 bytes too.
+  const bool tc = tc_shape(a.D, a.P) && !misaligned(a.q, 16) && !misaligned(a.out, 16) && !misaligned(a.kc, 16) &&
+                  !misaligned(a.vc, 16) && !misaligned(a.ks, 16) && !misaligned(a.vs, 16) && a.q_sb % 8 == 0 &&
+                  a.q_st % 8 == 0 && a.q_sh % 8 == 0;
+  if (tc) {
+    const Plan p = make_plan(a.T, a.Hq, a.Hkv, a.D);
+    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    TcArgs x{};
+    x.a = a;
+    x.rows = p.rows;
+    x.rpt = p.rpt;
+    x.parts_per_item = p.parts;
+    x.groups = p.groups;
+    x.c = a.scale == 0.0f ? 1.0f : std::fabs(a.scale) * 1.4426950408889634f;
+    x.join_c = keys_as_m(p.rows, a.D, cache_dtype == SV_E4M3) ? 1.0f : x.c;
+    x.qflip = a.scale < 0.0f ? 0x80008000u : 0u;
+    x.qzero = a.scale == 0.0f;
+    x.counters = reinterpret_cast<unsigned*>(ws + p.off_counters);
+    x.part_ml = reinterpret_cast<float2*>(ws + p.off_ml);
+    x.part_o = reinterpret_cast<float*>(ws + p.off_o);
+    if (!a.chained) {
+      clear_kernel<<<1, 256, 0, st>>>(static_cast<unsigned*>(workspace), (int)(p.off_ml / 4));
+      if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
+    }
+    return cache_dtype == SV_E4M3 ? launch_tc_any<true>(x, p, st) : launch_tc_any<false>(x, p, st);
+  }
+  if (!a.chained && cudaMemsetAsync(workspace, 0, 4, st) != cudaSuccess) return SV_ERR_CUDA;
+  const long long rows = (long long)a.B * a.T * a.Hq;
+  const unsigned grid = (unsigned)((rows + kAnyThreads / 32 - 1) / (kAnyThreads / 32));
+  if (cache_dtype == SV_E4M3)
+    tree_attn_any_kernel<SV_E4M3><<<grid, kAnyThreads, 0, st>>>(a);
+  else
+    tree_attn_any_kernel<SV_BF16><<<grid, kAnyThreads, 0, st>>>(a);
+  return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+}
+
 }  // namespace tat
 }  // namespace sv
 
@@ -2307,39 +2336,8 @@ int sv_tree_attention(const void* q, int64_t q_stride_b, int64_t q_stride_t, int
   a.P = page_size;
   a.max_pages = max_pages;
   a.scale = scale;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  // 16-byte aligned rows for the tensor-core kernel; scales are copied in 16 bytes too.
-  const bool tc = tc_shape(D, page_size) && !misaligned(q, 16) && !misaligned(out, 16) &&
-                  !misaligned(k_cache, 16) && !misaligned(v_cache, 16) && !misaligned(k_scale, 16) &&
-                  !misaligned(v_scale, 16) && q_stride_b % 8 == 0 && q_stride_t % 8 == 0 && q_stride_h % 8 == 0;
-  if (tc) {
-    const Plan p = make_plan(T, Hq, Hkv, D);
-    unsigned char* ws = static_cast<unsigned char*>(workspace);
-    TcArgs x{};
-    x.a = a;
-    x.rows = p.rows;
-    x.rpt = p.rpt;
-    x.parts_per_item = p.parts;
-    x.groups = p.groups;
-    x.c = scale == 0.0f ? 1.0f : std::fabs(scale) * 1.4426950408889634f;
-    x.join_c = keys_as_m(p.rows, D, cache_dtype == SV_E4M3) ? 1.0f : x.c;
-    x.qflip = scale < 0.0f ? 0x80008000u : 0u;
-    x.qzero = scale == 0.0f;
-    x.counters = reinterpret_cast<unsigned*>(ws + p.off_counters);
-    x.part_ml = reinterpret_cast<float2*>(ws + p.off_ml);
-    x.part_o = reinterpret_cast<float*>(ws + p.off_o);
-    clear_kernel<<<1, 256, 0, st>>>(static_cast<unsigned*>(workspace), (int)(p.off_ml / 4));
-    if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
-    return cache_dtype == SV_E4M3 ? launch_tc_any<true>(x, p, st) : launch_tc_any<false>(x, p, st);
-  }
-  if (cudaMemsetAsync(workspace, 0, 4, st) != cudaSuccess) return SV_ERR_CUDA;
-  const long long rows = (long long)B * T * Hq;
-  const unsigned grid = (unsigned)((rows + kAnyThreads / 32 - 1) / (kAnyThreads / 32));
-  if (cache_dtype == SV_E4M3)
-    tree_attn_any_kernel<SV_E4M3><<<grid, kAnyThreads, 0, st>>>(a);
-  else
-    tree_attn_any_kernel<SV_BF16><<<grid, kAnyThreads, 0, st>>>(a);
-  return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+  a.table_heads = 1;
+  return launch_attention(a, cache_dtype, workspace, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"
