@@ -5,6 +5,7 @@
 #include <cmath>
 #include <cstdint>
 #include <algorithm>
+#include <mutex>
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -19,31 +20,33 @@ namespace fs {
 typedef unsigned long long u64;
 
 // The kept entries are a prefix of the row in the order of logits, so that a row needs its
-// cut: the last entry that is kept. A cluster of CTAs shares a row and passes over it, the first time
-// from memory and then from L2:
-//   1. the maximum;
-//   2. a sample of the tiles, as counts by distance from the maximum, which gives a value that the
-//      cut is expected to lie above (a window), with room to spare;
-//   3. the entries of the window go to lists in shared memory, 32 at a time to be weighed by full
-//      warps; the weights below it, wanted for the mass that top_p is a part of, are summed in
-//      fp32. A histogram of the listed entries (counts and masses) gives the cut's bin, the first CTA
-//      orders that bin's entries and finds the cut among them;
-//   4. the kept entries' masses by chunk of ids, the chunk that the uniform falls in, and its token.
-// All decisions are made on whole-number masses (2^-44 of the largest weight). Where the fp32 sum below
-// the window could change the cut, that sum is made again with the exact weights; where
-// the window turns out too small, it is widened; a row that still has no cut, or too many entries
-// in the cut's bin (ties), is halved bit by bit over the keys, with a pass for every bit.
+// cut, the last entry that is kept. A cluster of CTAs shares a row and passes over it twice, the first time
+// from memory and then, as a rule, from L2:
+//   1. the maximum, and for top_p the sum of all weights in fp32;
+//   2. a sample of the tiles, as counts by distance from the maximum, gives a window of values that
+//      the cut is expected in, a few standard deviations of the sample wide;
+//   3. the entries of the window and above go to lists in shared memory, to be taken by full
+//      warps: those above are weighed and summed, those within are set aside;
+//   4. a histogram of the entries set aside gives the cut's bin, whose entries the first CTA
+//      puts in order; the kept ones' weights join the sums;
+//   5. the sums are kept by ranges of ids (records: what a warp has summed up between two turns of its
+//      list), so that the uniform's range is known, and its token is found there.
+// All decisions are made on whole-number masses (2^-44 of the largest weight), where sums do not depend
+// on their order. Where the fp32 sum could change the cut, the mass below the window is
+// summed exactly. A window that misses the cut is widened; a row that still has none, or more
+// entries in its window than there is room for (ties), is halved bit by bit over the keys, a pass for every bit.
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kTile = 256;       // elements of a warp's step: 8 a lane
-constexpr int kChunks = 1024;    // most chunks (of one or more tiles) of a CTA's share
+constexpr int kTile = 256;        // elements of a warp's step: 8 a lane
 constexpr int kMaxCluster = 8;
-constexpr int kBins = 512;       // bins of the window
-constexpr int kSampleBins = 256; // bins of the sample, 1/8 of a power of two each
-constexpr int kList = 256;       // listed entries of a warp
-constexpr int kCand = 1024;      // entries of the cut's bin
-constexpr int kSampled = 16384;  // elements of a row's sample
+constexpr int kBins = 512;        // bins of the window
+constexpr int kSampleBins = 512;  // bins of the sample, 1/16 of a power of two each
+constexpr int kList = 288;        // listed entries of a warp: a tile's, and fewer than 32 left over
+constexpr int kAside = 2048;      // entries of a CTA set aside
+constexpr int kCand = 1024;       // entries of the cut's bin
+constexpr int kFew = 256;         // entries set aside (by all CTAs) that are put in order without a histogram
+constexpr int kRecords = 64;      // ranges of ids of a warp
 
 struct Args {
   const void* logits;
@@ -53,51 +56,57 @@ struct Args {
   const int32_t* top_k;
   float temp1, top_p1, min_p1;
   int top_k1;
-  int N, V, nc, share, shift, scale_bits;
+  int N, V, nc, share, step, scale_bits;
   int32_t* out;
   float* prob;
   unsigned* status;
 };
 
-struct Cut {
-  unsigned key;  // entries of a larger key are kept, and those of this key up to `id`
-  int id;
-  u64 mass;      // of the kept entries
-  int found;
-};
-
 // What a row's weights are made of: w(l) = exp((l - m)/T) times a power of two, as a whole
-// number of 2^-scale_bits (so that sums do not depend on their order).
+// number of 2^-scale_bits.
 struct Weigh {
   bool fast;
   int qb;
   DrawConst dc;
-  float ih, il, m, lmin, low;
-  float scale;
+  float il, m, lmin, low, scale;
+};
+
+struct Entry {
+  float l;
+  int id;
 };
 
 struct Shared {
   float2 tab[1024];
-  float lv[kWarps][kList];
-  int li[kWarps][kList];
   union {
-    u64 cand[kCand];                                  // key, then ~id: entries of the cut's bin
-    struct { unsigned lo[kChunks], hi[kChunks]; } ch; // kept mass by chunk
-    unsigned eq[kChunks];                             // ties by chunk
+    Entry list[kWarps][kList];
+    struct {
+      u64 cand[kCand];  // key, then ~id: entries of the cut's bin (first CTA)
+      unsigned hlo[kBins], hhi[kBins], hcnt[kBins];
+    };
   };
-  unsigned hlo[kBins], hhi[kBins], hcnt[kBins];
-  unsigned sample[kSampleBins];
+  union {
+    Entry aside[kAside];
+    unsigned sample[kSampleBins];
+  };
+  unsigned rec_lo[kWarps][kRecords], rec_hi[kWarps][kRecords];
+  int rec_end[kWarps][kRecords];  // the id behind the record's last one
+  int recs[kWarps];
   u64 wsum[2][kWarps];
-  unsigned wcnt[2][kWarps];
+  unsigned wcnt[2][kWarps], wmore[2][kWarps];
   u64 inbox[2][kMaxCluster];
-  unsigned inbox_c[2][kMaxCluster];
-  float wmax[kWarps];
-  unsigned ncand[2];
-  unsigned listed[kWarps];
-  int over, bin;
+  unsigned inbox_c[2][kMaxCluster], inbox_d[2][kMaxCluster];
+  u64 tile_sum[kWarps];
+  float fmass[kWarps], fvar[kWarps], wmax[kWarps];
+  unsigned n_aside, n_cand[4];
+  int edge[6], bin;  // edges: of each attempt the window's upper and lower one
   u64 bin_mass;
   unsigned bin_count;
-  Cut cut;
+  // The cut: entries of a larger key are kept, and those of this key up to `cut_id`; their mass.
+  unsigned cut_key;
+  int cut_id, cut_found;
+  u64 cut_mass;
+  float log_hi, log_lo;  // T ln(min_p)
   Weigh w;
 };
 
@@ -119,9 +128,9 @@ __device__ __noinline__ u64 weight_far(float l, float m, float ih, float il, flo
   return (u64)((long long)__float2ll_rn(e.hi * scale) + __float2ll_rn(e.lo * scale));
 }
 
-SV_DEVINL u64 weight(float l, const Weigh& w, const Shared& s) {
-  if (!w.fast) return weight_far(l, w.m, w.ih, w.il, w.low, w.scale);
-  const ff e = exp_draw(fmaxf(l, w.lmin), w.qb, w.dc, s.tab);
+SV_DEVINL u64 weight(float l, const Weigh& w, const float2* tab) {
+  if (!w.fast) return weight_far(l, w.m, w.dc.ih, w.il, w.low, w.scale);
+  const ff e = exp_draw(fmaxf(l, w.lmin), w.qb, w.dc, tab);
   return (u64)((long long)__float2ll_rn(e.hi * w.scale) + __float2ll_rn(e.lo * w.scale));
 }
 
@@ -221,167 +230,12 @@ SV_DEVINL unsigned scan_up(unsigned x, int lane) {
   return x;
 }
 
-template <bool F32, bool VEC>
-struct Row {
-  const Args& a;
-  Shared& s;
-  const void* row;
-  int begin, end, tiles, chunks;
-  unsigned rank, turn;
-  Weigh w;
-
-  SV_DEVINL int lane() const { return threadIdx.x & 31; }
-  SV_DEVINL int warp() const { return __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0); }
-  SV_DEVINL void sync() {
-    if (a.nc > 1)
-      cluster_sync();
-    else
-      __syncthreads();
-  }
-  SV_DEVINL unsigned remote(const void* p, unsigned r) const {
-    return a.nc > 1 ? dsmem_map(smem_u32(p), r) : smem_u32(p);
-  }
-
-  // Sums over the row's CTAs, the same in every thread; `before`: over the CTAs of lower rank, `mine`: this one's.
-  SV_DEVINL void sum(u64& x, unsigned& c, u64* before = nullptr, u64* mine = nullptr, unsigned* c_before = nullptr) {
-    const int t = turn & 1;
-    ++turn;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    c = __reduce_add_sync(0xffffffffu, c);
-    if (lane() == 0) s.wsum[t][threadIdx.x >> 5] = x, s.wcnt[t][threadIdx.x >> 5] = c;
-    __syncthreads();
-    x = 0, c = 0;
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) x += s.wsum[t][i], c += s.wcnt[t][i];
-    if (before) *before = 0, *mine = x;
-    if (c_before) *c_before = 0;
-    if (a.nc == 1) return;
-    if ((int)threadIdx.x < a.nc) {
-      dsmem_st_u64(remote(&s.inbox[t][rank], threadIdx.x), x);
-      dsmem_st_u32(remote(&s.inbox_c[t][rank], threadIdx.x), c);
-    }
-    cluster_sync();
-    x = 0, c = 0;
-    for (int i = 0; i < a.nc; ++i) {
-      if (i == (int)rank) {
-        if (before) *before = x;
-        if (c_before) *c_before = c;
-      }
-      x += s.inbox[t][i], c += s.inbox_c[t][i];
-    }
-  }
-
-  // f(chunk, first id, words) for the tiles of this CTA's share, U at a time loaded ahead; a warp takes whole chunks.
-  template <int U, typename F>
-  SV_DEVINL void tiles_by_chunk(F f) {
-    const int per = 1 << a.shift, wp = warp();
-    // The warp's tiles as one sequence: i -> chunk wp + (i / per) * kWarps.
-    const int n_chunks = chunks > wp ? (chunks - wp + kWarps - 1) / kWarps : 0, n = n_chunks << a.shift;
-#pragma unroll 1
-    for (int i0 = 0; i0 < n; i0 += U) {
-      uint32_t x[U][F32 ? 8 : 4];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int i = i0 + u, t = ((wp + (i >> a.shift) * kWarps) << a.shift) + (i & (per - 1));
-        load_tile<F32, VEC>(row, begin + t * kTile, i < n && t < tiles ? end : 0, lane(), x[u]);
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int i = i0 + u, c = wp + (i >> a.shift) * kWarps, t = (c << a.shift) + (i & (per - 1));
-        if (i < n && t < tiles) f(c, begin + t * kTile, x[u]);
-      }
-    }
-  }
-  // The same in any order of tiles.
-  template <int U, typename F>
-  SV_DEVINL void any_tiles(F f, int first = 0, int step = 1) {
-    const int stride = kWarps * step;
-#pragma unroll 1
-    for (int t0 = first + warp() * step; t0 < tiles; t0 += stride * U) {
-      uint32_t x[U][F32 ? 8 : 4];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int t = t0 + u * stride;
-        load_tile<F32, VEC>(row, begin + t * kTile, t < tiles ? end : 0, lane(), x[u]);
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (t0 + u * stride < tiles) f(begin + (t0 + u * stride) * kTile, x[u]);
-    }
-  }
-
-  // Largest element of a lane's eight (no NaN among them).
-  SV_DEVINL float top_of(const uint32_t (&x)[F32 ? 8 : 4]) {
-    if constexpr (F32) {
-      float r = __uint_as_float(x[0]);
-#pragma unroll
-      for (int i = 1; i < 8; ++i) r = fmaxf(r, __uint_as_float(x[i]));
-      return r;
-    } else {
-      const uint32_t r = bf16x2_max(bf16x2_max(x[0], x[1]), bf16x2_max(x[2], x[3]));
-      return fmaxf(bf16_lo(r), bf16_hi(r));
-    }
-  }
-
-  // The entries l >= lo of this CTA's share, each once, to f(l, id), by full warps; the lists
-  // keep them all unless s.over is set. `tile(words)` sees every tile first.
-  template <typename G, typename F>
-  SV_DEVINL void scan_above(float lo, G tile, F f) {
-    const int ln = lane(), wp = warp();
-    float* lv = s.lv[wp];
-    int* li = s.li[wp];
-    int n = 0;
-    bool full = false;
-    any_tiles<F32 ? 2 : 4>([&](int base, const uint32_t (&x)[F32 ? 8 : 4]) {
-      tile(x);
-      if (!__any_sync(0xffffffffu, top_of(x) >= lo)) return;
-      unsigned mask = 0;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) mask |= element<F32>(x, e) >= lo ? 1u << e : 0u;
-      const unsigned c = __popc(mask), incl = scan_up(c, ln), all = __shfl_sync(0xffffffffu, incl, 31);
-      if (n + (int)all > kList) {
-        full = true;
-        __syncwarp();
-        for (int i = ln; i < n; i += 32) f(lv[i], li[i]);
-        n = 0;
-        __syncwarp();
-      }
-      int at = n + (int)(incl - c);
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (mask >> e & 1u) {
-          lv[at] = element<F32>(x, e);
-          li[at] = base + tile_id<F32>(ln, e);
-          ++at;
-        }
-      n += (int)all;
-    });
-    __syncwarp();
-    for (int i = ln; i < n; i += 32) f(lv[i], li[i]);
-    if (ln == 0) {
-      s.listed[wp] = n;
-      if (full) s.over = 1;
-    }
-  }
-  // The listed entries again, or those l >= lo by another pass.
-  template <typename F>
-  SV_DEVINL void again(float lo, F f) {
-    if (s.over) {
-      scan_above(lo, [](const uint32_t (&)[F32 ? 8 : 4]) {}, f);
-    } else {
-      const int wp = warp();
-      for (int i = lane(); i < (int)s.listed[wp]; i += 32) f(s.lv[wp][i], s.li[wp][i]);
-    }
-  }
-};
-
 // Among the n candidates of the cut's bin (first CTA), the one at which the running count reaches
 // `want_count`, or the running mass `want` (and does so for every mass from want_lo to want).
 // s.bin_mass and s.bin_count are what lies above the bin.
 __device__ __noinline__ void order_candidates(Shared& s, int n, bool by_count, u64 want_lo, u64 want) {
   const int tid = threadIdx.x;
-  if (tid == 0) s.cut.found = 0;
+  if (tid == 0) s.cut_found = 0;
   int size = 32;
   while (size < n) size <<= 1;
   for (int i = n + tid; i < size; i += kThreads) s.cand[i] = 0;
@@ -403,18 +257,368 @@ __device__ __noinline__ void order_candidates(Shared& s, int n, bool by_count, u
   const unsigned above_count = s.bin_count;
   for (int i0 = 0; i0 < n; i0 += 32) {
     const u64 c = i0 + tid < n ? s.cand[i0 + tid] : 0;
-    const u64 x = i0 + tid < n ? weight(unordered((unsigned)(c >> 32)), s.w, s) : 0;
+    const u64 x = i0 + tid < n ? weight(unordered((unsigned)(c >> 32)), s.w, s.tab) : 0;
     const u64 incl = scan_up(x, tid);
     const bool hit = i0 + tid < n &&
                      (by_count ? above_count + i0 + tid + 1 == want : mass + incl >= want && mass + incl - x < want);
     if (hit) {
-      s.cut.key = (unsigned)(c >> 32);
-      s.cut.id = (int)~(unsigned)c;
-      s.cut.mass = mass + incl;
-      s.cut.found = by_count || mass + incl - x < want_lo ? 1 : 2;
+      s.cut_key = (unsigned)(c >> 32);
+      s.cut_id = (int)~(unsigned)c;
+      s.cut_mass = mass + incl;
+      s.cut_found = by_count || mass + incl - x < want_lo ? 1 : 2;
     }
     mass += __shfl_sync(0xffffffffu, incl, 31);
   }
+}
+
+
+SV_DEVINL float next_down(float x) { return x * (1.0f - 0x1p-23f); }  // x > 0: below x by one or two steps
+
+// x 2^64, 0 <= x < 1, rounded down.
+SV_DEVINL u64 fraction(float x) {
+  const unsigned b = __float_as_uint(x);
+  const int e = (int)(b >> 23) - 86;  // x = mantissa 2^(e + 86 - 150)
+  const u64 mant = (b & 0x7fffffu) | (b >> 23 ? 0x800000u : 0u);
+  return e >= 0 ? mant << e : e > -24 ? mant >> -e : 0;
+}
+
+// x / y for 0 < x <= y, to fp32's last place.
+SV_DEVINL float ratio(u64 x, u64 y) {
+  const float xh = __ull2float_rn(x), yh = __ull2float_rn(y);
+  const float xl = __ll2float_rn((long long)(x - __float2ull_rn(xh))), yl = __ll2float_rn((long long)(y - __float2ull_rn(yh)));
+  const float q = __fdiv_rn(xh, yh);
+  return q + __fdiv_rn(__fmaf_rn(-q, yh, xh) + (xl - q * yl), yh);
+}
+
+template <bool F32, bool VEC>
+struct Row {
+  static constexpr int WORDS = F32 ? 8 : 4;
+  const Args& a;
+  Shared& s;
+  const void* row;
+  int begin, end, tiles, seg;  // this CTA's ids; tiles in all and of a warp (its segment is contiguous)
+  unsigned rank, turn;
+  Weigh w;
+
+  SV_DEVINL int lane() const { return threadIdx.x & 31; }
+  SV_DEVINL int warp() const { return __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0); }
+  SV_DEVINL void sync() {
+    if (a.nc > 1)
+      cluster_sync();
+    else
+      __syncthreads();
+  }
+  SV_DEVINL unsigned remote(const void* p, unsigned r) const {
+    return a.nc > 1 ? dsmem_map(smem_u32(p), r) : smem_u32(p);
+  }
+  SV_DEVINL u64 weigh(float l) const { return weight(l, w, s.tab); }
+
+  // Sums over the row's CTAs, the same in every thread; `before`: over the CTAs of lower rank, `mine`: this one's.
+  SV_DEVINL void sum(u64& x, unsigned& c, unsigned& d, u64* before = nullptr, u64* mine = nullptr,
+                     unsigned* c_before = nullptr) {
+    const int t = turn & 1;
+    ++turn;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    c = __reduce_add_sync(0xffffffffu, c);
+    d = __reduce_add_sync(0xffffffffu, d);
+    if (lane() == 0) {
+      const int wp = threadIdx.x >> 5;
+      s.wsum[t][wp] = x, s.wcnt[t][wp] = c, s.wmore[t][wp] = d;
+    }
+    __syncthreads();
+    x = 0, c = 0, d = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) x += s.wsum[t][i], c += s.wcnt[t][i], d += s.wmore[t][i];
+    if (before) *before = 0, *mine = x;
+    if (c_before) *c_before = 0;
+    if (a.nc == 1) return;
+    if ((int)threadIdx.x < a.nc) {
+      dsmem_st_u64(remote(&s.inbox[t][rank], threadIdx.x), x);
+      dsmem_st_u32(remote(&s.inbox_c[t][rank], threadIdx.x), c);
+      dsmem_st_u32(remote(&s.inbox_d[t][rank], threadIdx.x), d);
+    }
+    cluster_sync();
+    x = 0, c = 0, d = 0;
+    for (int i = 0; i < a.nc; ++i) {
+      if (i == (int)rank) {
+        if (before) *before = x;
+        if (c_before) *c_before = c;
+      }
+      x += s.inbox[t][i], c += s.inbox_c[t][i], d += s.inbox_d[t][i];
+    }
+  }
+  SV_DEVINL void sum(u64& x, unsigned& c) {
+    unsigned d = 0;
+    sum(x, c, d);
+  }
+
+  // f(first id, words) for tiles first, first + step, ... before `last`, U loaded ahead.
+  template <int U, typename F>
+  SV_DEVINL void some_tiles(int first, int last, int step, F f) {
+#pragma unroll 1
+    for (int t0 = first; t0 < last; t0 += U * step) {
+      uint32_t x[U][WORDS];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int t = t0 + u * step;
+        load_tile<F32, VEC>(row, begin + t * kTile, t < last ? end : 0, lane(), x[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (t0 + u * step < last) f(begin + (t0 + u * step) * kTile, x[u]);
+    }
+  }
+  template <int U, typename F>
+  SV_DEVINL void all_tiles(F f) {
+    some_tiles<U>(warp(), tiles, kWarps, f);
+  }
+
+  // Largest element of a lane's eight (no NaN among them).
+  SV_DEVINL float top_of(const uint32_t (&x)[WORDS]) {
+    if constexpr (F32) {
+      float r = __uint_as_float(x[0]);
+#pragma unroll
+      for (int i = 1; i < 8; ++i) r = fmaxf(r, __uint_as_float(x[i]));
+      return r;
+    } else {
+      const uint32_t r = bf16x2_max(bf16x2_max(x[0], x[1]), bf16x2_max(x[2], x[3]));
+      return fmaxf(bf16_lo(r), bf16_hi(r));
+    }
+  }
+
+  // A record of the ids before `stop` that have none yet: the warp's sum of x. A full table is
+  // halved first.
+  SV_DEVINL void record(int& n, u64 x, int stop) {
+    const int ln = lane(), wp = warp();
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    if (n == kRecords) {
+      const u64 p = ((u64)s.rec_hi[wp][2 * ln] << 32 | s.rec_lo[wp][2 * ln]) +
+                    ((u64)s.rec_hi[wp][2 * ln + 1] << 32 | s.rec_lo[wp][2 * ln + 1]);
+      const int e = s.rec_end[wp][2 * ln + 1];
+      __syncwarp();
+      s.rec_lo[wp][ln] = (unsigned)p, s.rec_hi[wp][ln] = (unsigned)(p >> 32);
+      s.rec_end[wp][ln] = e;
+      n = kRecords / 2;
+      __syncwarp();
+    }
+    if (ln == 0) {
+      s.rec_lo[wp][n] = (unsigned)x, s.rec_hi[wp][n] = (unsigned)(x >> 32);
+      s.rec_end[wp][n] = stop;
+    }
+    ++n;
+  }
+
+  // The entries l >= lo of this CTA's share (`all`: every entry): those above hi (and, with a cut, those that it keeps)
+  // are summed into records, the others set aside as far as there is room. Returns a thread's part of the sum.
+  SV_DEVINL u64 pass(float lo, float hi, bool cut, bool all, unsigned& count) {
+    const int ln = lane(), wp = warp();
+    Entry* list = s.list[wp];
+    const int first = min(tiles, wp * seg), last = min(tiles, first + seg), stop = min(end, begin + last * kTile);
+    u64 total = 0;
+    int recs = 0;
+    count = 0;
+    if (all) {
+      const int every = (seg + kRecords - 1) / kRecords;
+      u64 acc = 0;
+      int done = 0;
+      some_tiles<2>(first, last, 1, [&](int base, const uint32_t (&x)[WORDS]) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float l = element<F32>(x, e);
+          acc += l > neg_inf() ? weigh(l) : 0;
+        }
+        if (++done == every) {
+          total += acc;
+          record(recs, acc, base + kTile);
+          acc = 0;
+          done = 0;
+        }
+      });
+      total += acc;
+      record(recs, acc, stop);
+    } else {
+      const unsigned key = s.cut_key;
+      const int cut_id = s.cut_id;
+      int n = 0;
+      u64 acc = 0;
+      auto take = [&](int from, bool on) {  // 32 entries of the list
+        const Entry e = list[from + ln];
+        bool sure = e.l > hi;
+        if (cut && !sure) {
+          const unsigned k = ordered(e.l);
+          sure = k > key || (k == key && e.id <= cut_id);
+        }
+        if (on && sure) {
+          acc += weigh(e.l);
+          ++count;
+        }
+        const bool put = on && !sure && !cut;
+        const unsigned b = __ballot_sync(0xffffffffu, put);
+        if (b) {
+          unsigned at = 0;
+          if (ln == 0) at = atomicAdd(&s.n_aside, (unsigned)__popc(b));
+          at = __shfl_sync(0xffffffffu, at, 0) + __popc(b & ((1u << ln) - 1));
+          if (put && at < (unsigned)kAside) s.aside[at] = e;
+        }
+      };
+      some_tiles<F32 ? 2 : 4>(first, last, 1, [&](int base, const uint32_t (&x)[WORDS]) {
+        if (!__any_sync(0xffffffffu, top_of(x) >= lo)) return;
+        // In the order of ids: fp32's two halves of a tile one behind the other.
+        unsigned mask = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) mask |= element<F32>(x, e) >= lo ? 1u << e : 0u;
+        const unsigned c = F32 ? __popc(mask & 15u) | __popc(mask >> 4) << 16 : __popc(mask);
+        const unsigned incl = scan_up(c, ln), sum = __shfl_sync(0xffffffffu, incl, 31);
+        const int head = (int)(sum & 0xffffu), both = head + (int)(sum >> 16);
+        if (n + both > kList) {
+          __syncwarp();
+          const int full = n & ~31;
+          for (int i = 0; i < full; i += 32) take(i, true);
+          const int stop_at = list[min(full, kList - 1)].id;
+          const Entry left = list[min(full + ln, kList - 1)];
+          total += acc;
+          record(recs, acc, full < n ? stop_at : base);
+          acc = 0;
+          __syncwarp();
+          n -= full;
+          if (ln < n) list[ln] = left;
+        }
+        int at = n + (int)((incl - c) & 0xffffu), at2 = n + head + (int)((incl - c) >> 16);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (mask >> e & 1u) list[F32 && e >= 4 ? at2++ : at++] = Entry{element<F32>(x, e), base + tile_id<F32>(ln, e)};
+        n += both;
+      });
+      __syncwarp();
+      for (int i = 0; i < n; i += 32) take(i, i + ln < n);
+      total += acc;
+      record(recs, acc, stop);
+    }
+    if (ln == 0) s.recs[wp] = recs;
+    return total;
+  }
+
+  // The mass of the entries l < lo, exactly (a thread's part).
+  SV_DEVINL u64 below(float lo) {
+    u64 x = 0;
+    all_tiles<1>([&](int, const uint32_t (&v)[WORDS]) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float l = element<F32>(v, e);
+        if (l < lo && l > neg_inf()) x += weigh(l);
+      }
+    });
+    return x;
+  }
+};
+
+// The cut of a row by halving: the largest key that the wanted count (K, or 0) or mass reaches, then the last of its
+// ties that is kept; into s.cut_key and s.cut_id.
+template <bool F32, bool VEC>
+SV_DEVINL void cut_by_bits(Row<F32, VEC>& r, unsigned K, bool by_p, u64 part) {
+  constexpr int WORDS = F32 ? 8 : 4;
+  Shared& s = r.s;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  auto reach = [&](unsigned key, u64& mass, unsigned& count) {  // entries of this key or more
+    u64 x = 0;
+    unsigned c = 0;
+    r.template all_tiles<1>([&](int, const uint32_t (&v)[WORDS]) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float l = element<F32>(v, e);
+        if (l > neg_inf() && ordered(l) >= key) {
+          ++c;
+          x += r.weigh(l);
+        }
+      }
+    });
+    r.sum(x, c);
+    mass = x;
+    count = c;
+  };
+  // Two searches, one after the other, by the same loop: for the count, then for the mass.
+  u64 mass = 0, total = 0, want = 0;
+  unsigned count = 0, ties = 0xffffffffu, key = 0;
+#pragma unroll 1
+  for (int by = K ? 0 : 1; by < (by_p ? 2 : 1); ++by) {
+    if (by == 1) {
+      if (!K) {
+        reach(0, mass, count);
+        total = mass;
+      }
+      want = max(__umul64hi(total, part) + (total * part != 0 ? 1u : 0u), (u64)1);
+    }
+    unsigned found = 0;
+#pragma unroll 1
+    for (int bit = 31; bit >= 0; --bit) {
+      const unsigned tried = found | 1u << bit;
+      if (by == 1 && tried <= key) {
+        found = tried;  // the k kept entries reach all of their mass
+        continue;
+      }
+      reach(tried, mass, count);
+      if (by == 0 ? count >= K : mass >= want) found = tried;
+    }
+    reach(found + 1, mass, count);
+    const u64 one = found ? r.weigh(unordered(found)) : 0;
+    if (by == 0) {
+      ties = K - count;
+      total = mass + ties * one;
+    } else {
+      const u64 need = one ? (want - mass + one - 1) / one : 1;
+      ties = found > key ? (unsigned)need : (unsigned)min((u64)ties, need);
+    }
+    key = found;
+  }
+  // The id of the last tie that is kept. A warp's segment is contiguous, and so are the CTAs' shares.
+  const int first = min(r.tiles, warp * r.seg), last = min(r.tiles, first + r.seg);
+  auto equal = [&](const uint32_t (&v)[WORDS]) {
+    unsigned e = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e += ordered(element<F32>(v, i)) == key;
+    return e;
+  };
+  unsigned mine = 0;
+  r.template some_tiles<1>(first, last, 1, [&](int, const uint32_t (&v)[WORDS]) { mine += equal(v); });
+  unsigned before = 0, all = mine;
+  u64 z = 0;
+  const int t = r.turn & 1;
+  unsigned none = 0;
+  r.sum(z, all, none, nullptr, nullptr, &before);
+  for (int i = 0; i < warp; ++i) before += s.wcnt[t][i];
+  const unsigned here = s.wcnt[t][warp];
+  if (tid == 0) s.cut_id = 0x7fffffff;
+  __syncthreads();
+  if (all > ties && before < ties && before + here >= ties) {
+    unsigned seen = before;
+    r.template some_tiles<1>(first, last, 1, [&](int base, const uint32_t (&v)[WORDS]) {
+#pragma unroll
+      for (int g = 0; g < (F32 ? 2 : 1); ++g) {
+        constexpr int PER = F32 ? 4 : 8;
+        unsigned e = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) e += ordered(element<F32>(v, g * PER + i)) == key;
+        const unsigned inc = scan_up(e, lane);
+        unsigned at = seen + inc - e;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+          if (ordered(element<F32>(v, g * PER + i)) == key && ++at == ties)
+            s.cut_id = base + tile_id<F32>(lane, g * PER + i);
+        seen += __shfl_sync(0xffffffffu, inc, 31);
+      }
+    });
+  }
+  __syncthreads();
+  u64 id = tid == 0 && s.cut_id != 0x7fffffff ? (u64)(unsigned)s.cut_id : 0;  // one CTA at most has it
+  unsigned any = tid == 0 && s.cut_id != 0x7fffffff;
+  r.sum(id, any);
+  if (tid == 0) {
+    s.cut_key = key;
+    s.cut_id = any ? (int)id : 0x7fffffff;
+  }
+  __syncthreads();
 }
 
 template <bool F32, bool VEC>
@@ -429,17 +633,46 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
   const float T = a.temp ? a.temp[n] : a.temp1, u = a.uniforms[n];
   const float top_p = a.top_p ? a.top_p[n] : a.top_p1, min_p = a.min_p ? a.min_p[n] : a.min_p1;
   const int top_k = a.top_k ? a.top_k[n] : a.top_k1;
+  const unsigned K = T == 0.0f ? 1u : top_k > 0 && top_k < a.V ? (unsigned)top_k : 0u;
+  const bool by_p = top_p < 1.0f && T > 0.0f, by_m = min_p > 0.0f && T > 0.0f;
   const int begin = min(a.V, (int)rank * a.share), end = min(a.V, begin + a.share);
   const int tiles = (end - begin + kTile - 1) / kTile;
   Row<F32, VEC> r{a, s, static_cast<const unsigned char*>(a.logits) + (long long)n * a.stride * (F32 ? 4 : 2),
-                  begin, end, tiles, (tiles + (1 << a.shift) - 1) >> a.shift, rank, 0};
+                  begin, end, tiles, (tiles + kWarps - 1) / kWarps, rank, 0};
   Weigh& w = r.w;
 
-  // Maximum (NaN if there is one).
-  float m = neg_inf();
+  // Constants of T, in float-floats (fp64 takes longer here than the row).
+  float c_hi, c_lo;  // log2(e) / T; c_hi is rounded down and c_lo above 0, so that -inf stays -inf
   {
+    const float Tf = T > 0.0f ? T : 1.0f, ih = __fdiv_rn(1.0f, Tf);
+    w.dc.ih = ih;
+    w.il = __fmaf_rn(-ih, Tf, 1.0f) * ih;
+    const ff C = ff_mul_f(ff{0x1.62e43p-11f, -0x1.05c61p-39f}, Tf);  // T ln2/1024
+    w.dc.ch = C.hi;
+    w.dc.cli = C.lo * ih;
+    w.dc.inv = __fdiv_rn(1.0f, C.hi);
+    w.lmin = -2048.0f * Tf;
+    w.low = -88.0f * Tf;
+    w.scale = __int_as_float((127 + a.scale_bits) << 23);
+    const ff c = ff_mul(ff{0x1.715476p+0f, 0x1.4ae0c0p-26f}, ff{ih, w.il});
+    c_hi = next_down(c.hi);
+    c_lo = fmaxf((c.hi - c_hi) + c.lo, 1e-37f);
+  }
+  if (by_m && warp == kWarps - 1) {  // one warp, since it is fp64
+    const double x = (double)T * log((double)min_p);
+    if (lane == 0) {
+      s.log_hi = (float)x;
+      s.log_lo = (float)(x - (double)(float)x);
+    }
+  }
+
+  // The maximum (NaN if there is one), and for top_p alone the sum of all weights.
+  float m = neg_inf();
+  const bool summed = by_p && !K;
+  float run = 0.0f, far = 0.0f;  // weights relative to 2^far
+  if (!summed) {
     uint32_t m2 = 0xff80ff80u;
-    r.template any_tiles<F32 ? 4 : 8>([&](int, const uint32_t (&x)[WORDS]) {
+    r.template all_tiles<F32 ? 4 : 8>([&](int, const uint32_t (&x)[WORDS]) {
       if constexpr (F32) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) m = max_nan(m, __uint_as_float(x[i]));
@@ -448,12 +681,48 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
       }
     });
     if constexpr (!F32) m = max_nan(bf16_lo(m2), bf16_hi(m2));
+  } else {
+    bool nan = false;
+    r.template all_tiles<F32 ? 4 : 8>([&](int, const uint32_t (&x)[WORDS]) {
+      float top;
+      if constexpr (F32) {
+        top = __uint_as_float(x[0]);
+#pragma unroll
+        for (int i = 1; i < 8; ++i) top = max_nan(top, __uint_as_float(x[i]));
+      } else {
+        const uint32_t t2 = max2_nan(max2_nan(x[0], x[1]), max2_nan(x[2], x[3]));
+        top = max_nan(bf16_lo(t2), bf16_hi(t2));
+      }
+      if (!(top <= m)) {  // a new maximum (or NaN)
+        const float to = top * c_hi;
+        run = run > 0.0f ? run * ex2_fast(far - to) : 0.0f;
+        far = to;
+        nan |= isnan(top);
+        m = top;
+      }
+      if (m > neg_inf()) {
+        float2 t2 = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+          const float2 l = make_float2(element<F32>(x, e), element<F32>(x, e + 1));
+          const float2 y = f2_fma(l, f2(c_lo), f2_fma(l, f2(c_hi), f2(-far)));
+          t2 = f2_add(t2, make_float2(ex2_fast(y.x), ex2_fast(y.y)));
+        }
+        run += t2.x + t2.y;
+      }
+    });
+    if (nan) m = __int_as_float(0x7fc00000);
   }
   for (int i = tid; i < 1024; i += kThreads) s.tab[i] = kSvExp2Table1024[i];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
   if (lane == 0) s.wmax[warp] = m;
   for (int i = tid; i < kSampleBins; i += kThreads) s.sample[i] = 0;
+  if (tid < 6) s.edge[tid] = -1;
+  if (tid == 0) {
+    s.cut_key = 0;
+    s.cut_id = 0x7fffffff;
+  }
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < kWarps; ++i) m = max_nan(m, s.wmax[i]);
@@ -480,474 +749,437 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
     return;
   }
 
-  float c_hi, c_lo, far, tail_unit;  // a weight is about tail_unit 2^(l (c_hi + c_lo) - far)
+  w.m = m;
   {
-    const double Td = T > 0.0f ? (double)T : 1.0, inv = 1.0 / Td, C = Td * 0.69314718055994530942 / 1024.0;
-    w.ih = (float)inv;
-    w.il = (float)(inv - (double)w.ih);
-    w.dc.ch = (float)C;
-    w.dc.cli = (float)((C - (double)w.dc.ch) * inv);
-    w.dc.inv = (float)(1.0 / C);
-    w.dc.ih = w.ih;
-    w.m = m;
-    const double top = (double)m * inv;
-    w.fast = fabs(top) < 1386.0;
-    w.qb = 127 - ((int)floor((w.fast ? top : 0.0) * 1.4426950408889634074) + 1);
-    w.lmin = (float)(-2048.0 * Td);
-    w.low = (float)(-88.0 * Td);
-    w.scale = __int_as_float((127 + a.scale_bits) << 23);
-    // c_hi is c rounded down and c_lo above 0, so that -inf stays -inf.
-    const double c = 1.4426950408889634074 * inv;
-    c_hi = __double2float_rd(c);
-    c_lo = fmaxf((float)(c - (double)c_hi), 1e-37f);
-    far = (float)((double)m * c);
+    const float top = m * w.dc.ih;
+    w.fast = fabsf(top) < 1386.0f;
+    w.qb = 127 - ((int)floorf((w.fast ? top : 0.0f) * 1.44269504f) + 1);
     if (tid == 0) s.w = w;
-    tail_unit = (float)((double)weight(m, w, s) * exp2((double)far - (double)m * c));
   }
-  const float floor_l = min_p > 0.0f && T > 0.0f
-                            ? fminf(__double2float_ru((double)m + (double)T * log((double)min_p)), m)
-                            : -FLT_MAX;
-  const unsigned K = T == 0.0f ? 1u : top_k > 0 && top_k < a.V ? (unsigned)top_k : 0u;
-  const bool by_p = top_p < 1.0f && T > 0.0f;
-  const u64 part = (u64)((double)(by_p ? top_p : 0.0f) * 18446744073709551616.0);
+  // The least logit that min_p keeps: m + T ln(min_p), rounded up.
+  float floor_l = -FLT_MAX;
+  if (by_m) {
+    const ff x = two_sum(m, s.log_hi);
+    const ff y = fast_two_sum(x.hi, x.lo + s.log_lo);
+    floor_l = y.hi;
+    if (y.lo > 0.0f) floor_l = __uint_as_float(__float_as_uint(y.hi) + (y.hi >= 0.0f ? 1 : -1));
+    if (y.hi == 0.0f && y.lo > 0.0f) floor_l = y.lo;
+    floor_l = fmaxf(fminf(floor_l, m), -FLT_MAX);
+  }
+  const u64 part = by_p ? fraction(top_p) : 0;
   // The least whole mass that is top_p of `total` or more.
   auto part_of = [&](u64 total) { return max(__umul64hi(total, part) + (total * part != 0 ? 1u : 0u), (u64)1); };
 
-  Cut cut{0, 0x7fffffff, 0, 1};  // everything
-  float lo = floor_l;            // the lists hold the entries l >= lo
-  bool lists = false;
+  u64 sum = 0;       // a thread's part of the kept mass in the records
+  unsigned sure = 0; // entries in them
+  bool cut = false;  // s.cut_key and s.cut_id say what is kept of the entries set aside
+  float lo = floor_l, hi = floor_l > -FLT_MAX ? unordered(ordered(floor_l) - 1u) : -FLT_MAX;
 
-  if (K || by_p) {
+  if (!K && !by_p) {
+    sum = r.pass(lo, hi, false, !by_m, sure);
+  } else {
     bool found = false;
-    const float unit = 8.0f * c_hi;  // sample bins per unit of logit
+    u64 mass_all = 0, slack = 0;  // of the row, and what it may be off by
+    const float unit = 16.0f * c_hi;
+    if (summed && w.fast) {
+      // A thread's sum is relative to 2^far, where its maximum was.
+      unsigned z = 0;
+      mass_all = run > 0.0f ? __float2ull_rn(run * ex2_fast(__fmaf_rn(-m, c_hi, far) - m * c_lo) *
+                                             __ull2float_rn(r.weigh(m)))
+                            : 0;
+      r.sum(mass_all, z);
+      slack = mass_all >> 21;
+    }
     if (K != 1 && w.fast) {
-      const int step = max(1, a.V / kSampled);
-      r.template any_tiles<2>(
-          [&](int, const uint32_t (&x)[WORDS]) {
+      r.template some_tiles<2>(warp * a.step, tiles, kWarps * a.step, [&](int, const uint32_t (&x)[WORDS]) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float d = (m - element<F32>(x, e)) * unit;
-              if (d < (float)kSampleBins) atomicAdd(&s.sample[(int)d], 1u);
-            }
-          },
-          0, step);
+        for (int e = 0; e < 8; ++e) {
+          const float d = (m - element<F32>(x, e)) * unit;
+          if (d < (float)kSampleBins) atomicAdd(&s.sample[(int)d], 1u);
+        }
+      });
+      int sampled = 0;
+      for (int i = 0; i < a.nc; ++i) {
+        const int len = min(a.share, max(0, a.V - i * a.share)), n_tiles = (len + kTile - 1) / kTile;
+        const int k = (n_tiles + a.step - 1) / a.step;
+        sampled += k == 0 ? 0 : (n_tiles - 1) % a.step == 0 ? (k - 1) * kTile + len - (n_tiles - 1) * kTile : k * kTile;
+      }
       r.sync();
-      unsigned c = 0;
-      for (int i = 0; i < a.nc; ++i) c += dsmem_ld_u32(r.remote(&s.sample[tid], i));
-      // Running count and mass from the top, a bin a thread.
-      const float mass1 = (float)c * ex2_fast(-0.125f * ((float)tid + 0.5f));
-      unsigned cc = scan_up(c, lane);
-      float cm = mass1;
+      // Two bins a thread, the deepest first: the sample's mass below, its variance, and the count above.
+      const int b = kSampleBins - 2 - 2 * tid;
+      unsigned c0 = 0, c1 = 0;
+      for (int i = 0; i < a.nc; ++i) {
+        c0 += dsmem_ld_u32(r.remote(&s.sample[b], i));
+        c1 += dsmem_ld_u32(r.remote(&s.sample[b + 1], i));
+      }
+      const float w0 = ex2_fast(-0.0625f * ((float)b + 0.5f)), w1 = ex2_fast(-0.0625f * ((float)b + 1.5f));
+      const float m0 = (float)c0 * w0, m1 = (float)c1 * w1, v0 = m0 * w0, v1 = m1 * w1;
+      unsigned cc = scan_up(c0 + c1, lane);
+      float cm = m0 + m1, cv = v0 + v1;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const float y = __shfl_up_sync(0xffffffffu, cm, o);
-        if (lane >= o) cm += y;
+        const float y = __shfl_up_sync(0xffffffffu, cm, o), q = __shfl_up_sync(0xffffffffu, cv, o);
+        if (lane >= o) cm += y, cv += q;
       }
-      if (lane == 31) s.wcnt[0][warp] = cc, s.wmax[warp] = cm;
       __syncthreads();
-      float all = 0.0f;
+      if (lane == 31) s.wcnt[0][warp] = cc, s.fmass[warp] = cm, s.fvar[warp] = cv;
+      __syncthreads();
+      unsigned all_c = 0;
+      float below_m = 0.0f, below_v = 0.0f;
 #pragma unroll
       for (int i = 0; i < kWarps; ++i) {
-        if (i < warp) cc += s.wcnt[0][i], cm += s.wmax[i];
-        all += s.wmax[i];
+        if (i < warp) cc += s.wcnt[0][i], below_m += s.fmass[i], below_v += s.fvar[i];
+        all_c += s.wcnt[0][i];
       }
-      // Kept for the attempts below: counts as they are, masses as parts of the sample's.
-      s.hcnt[tid] = cc;
-      s.hlo[tid] = __float_as_uint(all - cm + 1e-6f * all);  // mass below the bin
-      s.hhi[tid] = __float_as_uint(all);
-      r.sync();
-    }
-    int edge_k = 0, edge_p = 0;
-    // The window's lower end, from the sample; -FLT_MAX where it does not reach far enough.
-    if (K == 1) {
-      lo = m;
-    } else if (!w.fast) {
-      lo = -FLT_MAX;
+      cm += below_m, cv += below_v;
+      const float scale = (float)a.V / (float)max(sampled, 1);
+      const float want_below = K ? 0.0f : (1.0f - top_p) * __ull2float_rn(mass_all) / __ull2float_rn(r.weigh(m)) / scale;
+#pragma unroll
+      for (int t = 0; t < 3; ++t) {
+        const float z = t == 0 ? 3.5f : t == 1 ? 8.0f : 20.0f, rel = t == 0 ? 0.03f : t == 1 ? 0.15f : 0.5f;
+        int up = -1, down = -1;  // the deepest bin edge that is surely above the cut; that is not surely below it
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int edge = b + j;
+          if (K) {
+            const float above = (float)(all_c - cc + (j ? c0 : 0u)), dev = z * sqrtf(above + 1.0f) + 2.0f;
+            if (!by_p && (above + dev) * scale <= (float)K) up = edge;
+            if ((above - dev) * scale < (float)K) down = edge;
+          } else {
+            const float mass = j ? cm - m0 : cm, dev = z * sqrtf(j ? fmaxf(cv - v0, 0.0f) : cv) + rel * mass;
+            if (mass - dev >= want_below) up = edge;
+            if (mass + dev > want_below) down = edge;
+          }
+        }
+        up = __reduce_max_sync(0xffffffffu, up);
+        down = __reduce_max_sync(0xffffffffu, down);
+        if (lane == 0) {
+          atomicMax(&s.edge[2 * t], up);
+          atomicMax(&s.edge[2 * t + 1], down);
+        }
+      }
+      __syncthreads();
     }
 #pragma unroll 1
-    for (int attempt = 0; attempt < 3 && !found; ++attempt) {
-      if (K != 1 && w.fast) {
-        if (attempt == 0) {
-          // Bins that hold enough of the sample: searched by all threads at once.
-          const int step = max(1, a.V / kSampled);
-          const float need = K ? (1.25f * (float)K + 12.0f * sqrtf((float)K) + 40.0f) / (float)step : 0.0f;
-          const float all = __uint_as_float(s.hhi[tid]);
-          const float spare = 0.5f * (1.0f - top_p) * all;
-          const bool short_k = K && (float)s.hcnt[tid] < need;
-          const bool short_p = !K && by_p && __uint_as_float(s.hlo[tid]) > spare;
-          edge_k = __syncthreads_count(short_k);
-          edge_p = __syncthreads_count(short_p);
-        } else {
-          edge_k += 16 * attempt * attempt;
-          edge_p += 12 * attempt * attempt;
-        }
-        const int edge = max(edge_k, edge_p) + 1;
-        lo = edge >= kSampleBins ? -FLT_MAX : fmaxf(m - (float)edge / unit, -FLT_MAX);
+    for (int attempt = 0; attempt < 3 && !found && w.fast; ++attempt) {
+      if (K == 1) {
+        lo = m;
+        hi = FLT_MAX;
+      } else {
+        const int up = s.edge[2 * attempt], down = s.edge[2 * attempt + 1];
+        hi = up > 0 ? m - (float)up / unit : FLT_MAX;
+        lo = down + 1 >= kSampleBins ? -FLT_MAX : fmaxf(m - (float)(down + 1) / unit, -FLT_MAX);
       }
       const bool floored = !(K && by_p) && floor_l >= lo;  // min_p cuts above the window's end
-      if (floored) lo = floor_l;
-      if (attempt > 0)
-        r.sync();  // the last attempt's bins have been read
-      else
-        __syncthreads();
-      for (int i = tid; i < kBins; i += kThreads) s.hlo[i] = s.hhi[i] = s.hcnt[i] = 0;
-      if (tid < 2) s.ncand[tid] = 0;
-      if (tid == 0) s.over = 0;
+      if (floored) {
+        lo = floor_l;
+        hi = fmaxf(hi, unordered(ordered(floor_l) - 1u));
+      }
+      if (attempt > 0) r.sync();  // (what the last attempt left has been read)
       __syncthreads();
-      const float width = fminf(m - lo, 256.0f / unit);  // (32 powers of two; further down is the last bin's)
+      if (tid == 0) s.n_aside = 0;
+      if (tid < 4) s.n_cand[tid] = 0;
+      __syncthreads();
+      sum = r.pass(lo, hi, false, false, sure);
+      __syncthreads();
+      u64 above = sum;
+      unsigned above_c = sure, aside = tid == 0 ? min(s.n_aside, 0x10000u) : 0u;
+      if (tid == 0 && s.n_aside > (unsigned)kAside) aside = 1u << 24;  // no room
+      r.sum(above, above_c, aside);
+      if (aside >= 1u << 24) break;
+      const int here = (int)min(s.n_aside, (unsigned)kAside);
+      const bool few = aside <= (unsigned)kFew;
+      // Masses and counts of the window's bins over all CTAs, two a thread, above what the thread's bins hold.
+      const float top_l = hi == FLT_MAX ? m : hi, width = fminf(top_l - lo, (float)kSampleBins / unit);
       const float per = width > 0.0f ? (float)kBins / width : 0.0f;
-      auto bin_of = [&](float l) { return min(kBins - 1, (int)fminf((m - l) * per, (float)kBins)); };
-      // Masses below the window: fp32, eight at a time, then lane by lane as whole numbers.
-      const bool tail = by_p && !K;
-      u64 tail_mass = 0;
-      auto into_bins = [&](float l, int) {
-        const int b = bin_of(l);
-        add64(&s.hlo[b], &s.hhi[b], weight(l, w, s));
-        atomicAdd(&s.hcnt[b], 1u);
-      };
-      if (tail) {
-        float run = 0.0f;
-        r.scan_above(
-            lo,
-            [&](const uint32_t (&x)[WORDS]) {
-              float t8 = 0.0f;
+      auto bin_of = [&](float l) { return min(kBins - 1, (int)fminf((top_l - l) * per, (float)kBins)); };
+      u64 hm0 = 0, hm1 = 0, im = 0, all_m = 0;
+      unsigned hc0 = 0, hc1 = 0, ic = 0;
+      if (!few) {
+        for (int i = tid; i < kBins; i += kThreads) s.hlo[i] = s.hhi[i] = s.hcnt[i] = 0;
+        __syncthreads();
+        for (int i = tid; i < here; i += kThreads) {
+          const int b = bin_of(s.aside[i].l);
+          add64(&s.hlo[b], &s.hhi[b], r.weigh(s.aside[i].l));
+          atomicAdd(&s.hcnt[b], 1u);
+        }
+        r.sync();
+        for (int i = 0; i < a.nc; ++i) {
+          hm0 += (u64)dsmem_ld_u32(r.remote(&s.hhi[2 * tid], i)) << 32;
+          hm0 += dsmem_ld_u32(r.remote(&s.hlo[2 * tid], i));
+          hc0 += dsmem_ld_u32(r.remote(&s.hcnt[2 * tid], i));
+          hm1 += (u64)dsmem_ld_u32(r.remote(&s.hhi[2 * tid + 1], i)) << 32;
+          hm1 += dsmem_ld_u32(r.remote(&s.hlo[2 * tid + 1], i));
+          hc1 += dsmem_ld_u32(r.remote(&s.hcnt[2 * tid + 1], i));
+        }
+        im = scan_up(hm0 + hm1, lane);
+        ic = scan_up(hc0 + hc1, lane);
+        const int t = r.turn & 1;
+        ++r.turn;
+        if (lane == 31) s.wsum[t][warp] = im, s.wcnt[t][warp] = ic;
+        __syncthreads();
 #pragma unroll
-              for (int e = 0; e < 8; e += 2) {
-                const float2 l = make_float2(element<F32>(x, e), element<F32>(x, e + 1));
-                const float2 y = f2_fma(l, f2(c_lo), f2_fma(l, f2(c_hi), f2(-far)));
-                const float p = l.x >= lo ? 0.0f : ex2_fast(y.x), q = l.y >= lo ? 0.0f : ex2_fast(y.y);
-                t8 += p + q;
-              }
-              run += t8;
-            },
-            into_bins);
-        tail_mass = (u64)((double)run * (double)tail_unit);
+        for (int i = 0; i < kWarps; ++i) {
+          if (i < warp) im += s.wsum[t][i], ic += s.wcnt[t][i];
+          all_m += s.wsum[t][i];
+        }
+        im += above - (hm0 + hm1);
+        ic += above_c - (hc0 + hc1);
       } else {
-        r.scan_above(lo, [](const uint32_t (&)[WORDS]) {}, into_bins);
-      }
-      lists = true;
-      unsigned z = 0;
-      r.sum(tail_mass, z);  // (its barrier completes the bins)
-      __syncthreads();
-      // All CTAs' bins, two a thread, and what lies above each.
-      u64 hm[2] = {0, 0};
-      unsigned hc[2] = {0, 0};
-      for (int i = 0; i < a.nc; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int b = 2 * tid + j;
-          hm[j] += (u64)dsmem_ld_u32(r.remote(&s.hhi[b], i)) << 32 | 0;
-          hm[j] += dsmem_ld_u32(r.remote(&s.hlo[b], i));
-          hc[j] += dsmem_ld_u32(r.remote(&s.hcnt[b], i));
+        // So few that the first CTA orders them all.
+        u64 x = 0;
+        for (int i = tid; i < here; i += kThreads) {
+          const Entry e = s.aside[i];
+          x += r.weigh(e.l);
+          const unsigned at = dsmem_add_u32(r.remote(&s.n_cand[0], 0), 1u);
+          dsmem_st_u64(r.remote(&s.cand[at], 0), (u64)ordered(e.l) << 32 | (unsigned)~e.id);
         }
-      u64 im = scan_up(hm[0] + hm[1], lane);
-      unsigned ic = scan_up(hc[0] + hc[1], lane);
-      const int t = r.turn & 1;
-      ++r.turn;
-      if (lane == 31) s.wsum[t][warp] = im, s.wcnt[t][warp] = ic;
-      __syncthreads();
-      u64 all_m = 0;
-      unsigned all_c = 0;
-#pragma unroll
-      for (int i = 0; i < kWarps; ++i) {
-        if (i < warp) im += s.wsum[t][i], ic += s.wcnt[t][i];
-        all_m += s.wsum[t][i], all_c += s.wcnt[t][i];
+        unsigned z = 0;
+        r.sum(x, z);
+        all_m = x;
       }
-      im -= hm[0] + hm[1];  // above this thread's two bins
-      ic -= hc[0] + hc[1];
-      u64 total = all_m + tail_mass;
-      u64 slack = tail_mass >> 20;  // what the fp32 sum may be off by
-      bool again_exact = false;
+      all_m += above;
+      const unsigned all_c = above_c + aside;
+      int turn = 1;
+      bool exact = K != 0;
+      u64 total = mass_all;
 #pragma unroll 1
-      for (int round = K ? 0 : 1; round < (by_p ? 2 : 1); ++round) {
-        const bool count = round == 0;
-        if (count && all_c < K) {
-          // Fewer entries than k: with the floor inside the window it cuts; else the window is too small.
-          if (floored || lo == -FLT_MAX) found = true;
-          break;
-        }
-        if (!count && K) total = cut.mass, slack = 0;
-        const u64 want = count ? (u64)K : part_of(total + slack);
-        const u64 want_lo = count ? (u64)K : part_of(total - slack);
-        if (!count && all_m < want) {
-          if (floored && all_m < want_lo) {
-            found = true;  // the floor cuts first
-            cut = Cut{0, 0x7fffffff, 0, 1};
+      for (int round = K ? 0 : 1; round < 2; ++round) {
+        u64 want = K, want_lo = K;
+        if (round == 0) {
+          if (above_c >= K) break;  // the window lies too deep
+          if (all_c < K) {
+            // Fewer than k: all of them are kept, if the window ends where the row or min_p does.
+            if (!floored && lo > -FLT_MAX) break;
+            total = all_m;
+            found = !by_p;
+            if (found) break;
+            continue;
+          }
+        } else {
+          want = part_of(total + slack);
+          want_lo = part_of(total - slack);
+          const bool in_sure = above >= want_lo, short_of = all_m < want;
+          if (in_sure || short_of) {
+            if (!exact && ((in_sure && above < want) || (floored && short_of && all_m >= want_lo))) {
+              // The fp32 sum decides nothing here.
+              u64 rest = r.below(lo);
+              unsigned z = 0;
+              r.sum(rest, z);
+              total = all_m + rest;
+              slack = 0;
+              exact = true;
+              --round;
+              continue;
+            }
+            found = !in_sure && floored;  // min_p cuts first: all entries of the window are kept
             break;
           }
-          if (!floored && lo > -FLT_MAX && !K) break;  // the window is too small
         }
-        // The bin in which the count or the mass is reached.
-        if (tid == 0) s.bin = -1;
-        __syncthreads();
+        if (!few) {
+          // The bin in which the count or the mass is reached.
+          if (tid == 0) s.bin = -1;
+          __syncthreads();
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const u64 m0 = im + (j ? hm[0] : 0), m1 = m0 + hm[j];
-          const unsigned c0 = ic + (j ? hc[0] : 0), c1 = c0 + hc[j];
-          if (count ? c0 < K && c1 >= K : m0 < want && m1 >= want) {
-            s.bin = 2 * tid + j;
-            s.bin_mass = m0;
-            s.bin_count = c0;
+          for (int j = 0; j < 2; ++j) {
+            const u64 from = j ? im + hm0 : im, to = from + (j ? hm1 : hm0);
+            const unsigned c_from = j ? ic + hc0 : ic, c_to = c_from + (j ? hc1 : hc0);
+            if (round == 0 ? c_from < K && c_to >= K : from < want && to >= want) {
+              s.bin = 2 * tid + j;
+              s.bin_mass = from;
+              s.bin_count = c_from;
+            }
           }
+          __syncthreads();
+          const int bin = s.bin;
+          if (bin < 0) break;
+          for (int i = tid; i < here; i += kThreads) {
+            const Entry e = s.aside[i];
+            if (bin_of(e.l) == bin) {
+              const unsigned at = dsmem_add_u32(r.remote(&s.n_cand[turn], 0), 1u);
+              if (at < (unsigned)kCand)
+                dsmem_st_u64(r.remote(&s.cand[at], 0), (u64)ordered(e.l) << 32 | (unsigned)~e.id);
+            }
+          }
+          r.sync();
+        } else if (tid == 0) {
+          s.bin_mass = above;
+          s.bin_count = above_c;
         }
-        __syncthreads();
-        const int bin = s.bin;
-        if (bin < 0) break;
-        r.again(lo, [&](float l, int id) {
-          if (bin_of(l) == bin) {
-            const unsigned at = dsmem_add_u32(r.remote(&s.ncand[round], 0), 1u);
-            if (at < (unsigned)kCand)
-              dsmem_st_u64(r.remote(&s.cand[at], 0), (u64)ordered(l) << 32 | (unsigned)~id);
-          }
-        });
-        r.sync();
         if (rank == 0) {
           __syncthreads();
-          const int nc = (int)s.ncand[round];
+          const int nc = (int)(few ? s.n_cand[0] : s.n_cand[turn]);
           if (nc <= kCand)
-            order_candidates(s, nc, count, want_lo, want);
+            order_candidates(s, nc, round == 0, want_lo, want);
           else if (tid == 0)
-            s.cut.found = 0;
+            s.cut_found = 0;
           __syncthreads();
         }
+        ++turn;
         r.sync();
-        cut.found = (int)dsmem_ld_u32(r.remote(&s.cut.found, 0));
-        cut.key = dsmem_ld_u32(r.remote(&s.cut.key, 0));
-        cut.id = (int)dsmem_ld_u32(r.remote(&s.cut.id, 0));
-        cut.mass = dsmem_ld_u64(r.remote(&s.cut.mass, 0));
-        if (cut.found == 2 && !again_exact) {
-          // The fp32 sum decides nothing here: the mass below the window once more, exactly.
-          u64 rest = 0;
-          r.template any_tiles<1>([&](int, const uint32_t (&x)[WORDS]) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float l = element<F32>(x, e);
-              if (l < lo && l > neg_inf()) rest += weight(l, w, s);
-            }
-          });
+        const int how = (int)dsmem_ld_u32(r.remote(&s.cut_found, 0));
+        const unsigned key = dsmem_ld_u32(r.remote(&s.cut_key, 0));
+        const int id = (int)dsmem_ld_u32(r.remote(&s.cut_id, 0));
+        const u64 mass = dsmem_ld_u64(r.remote(&s.cut_mass, 0));
+        r.sync();
+        if (how == 2 && !exact) {
+          u64 rest = r.below(lo);
+          unsigned z = 0;
           r.sum(rest, z);
           total = all_m + rest;
           slack = 0;
-          again_exact = true;
-          if (tid == 0) s.ncand[round] = 0;
-          r.sync();
+          exact = true;
           --round;
           continue;
         }
-        if (cut.found != 1) {
-          attempt = 3;  // ties: bit by bit
+        if (how != 1) {
+          attempt = 3;  // too many ties
           break;
         }
-        if (round == (by_p ? 1 : 0)) found = true;
+        cut = true;
+        if (tid == 0) {
+          s.cut_key = key;
+          s.cut_id = id;
+        }
+        __syncthreads();
+        total = mass;
+        if (round == 1 || !by_p) {
+          found = true;
+          break;
+        }
       }
     }
-    if (!found) {
-      // Bit by bit over the keys: the largest key that the wanted count or mass reaches, then the last of its
-      // ties that is kept.
-      auto reach = [&](unsigned key, u64& mass, unsigned& count) {  // entries of this key or more
-        u64 x = 0;
-        unsigned c = 0;
-        r.template any_tiles<2>([&](int, const uint32_t (&v)[WORDS]) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float l = element<F32>(v, e);
-            if (l > neg_inf() && ordered(l) >= key) {
-              ++c;
-              x += weight(l, w, s);
-            }
+    if (found) {
+      // What is kept of the entries set aside joins the records.
+      const int here = (int)min(s.n_aside, (unsigned)kAside);
+      const unsigned key = cut ? s.cut_key : 0u;
+      const int cut_id = cut ? s.cut_id : 0;
+      for (int i = tid; i < here; i += kThreads) {
+        const Entry e = s.aside[i];
+        const unsigned k = ordered(e.l);
+        if (e.l >= floor_l && (k > key || (k == key && e.id <= cut_id))) {
+          const u64 x = r.weigh(e.l);
+          const int wp = (e.id - begin) / kTile / r.seg;
+          int j = 0, left = s.recs[wp];  // the first record that ends behind the id
+          while (left > 1) {
+            const int half = left / 2;
+            if (s.rec_end[wp][j + half - 1] <= e.id)
+              j += half, left -= half;
+            else
+              left = half;
           }
-        });
-        r.sum(x, c);
-        mass = x;
-        count = c;
-      };
-      u64 mass = 0, total = 0;
-      unsigned count = 0, ties = 0xffffffffu, key = 0;
-      if (K) {
-        for (int bit = 31; bit >= 0; --bit) {
-          reach(key | 1u << bit, mass, count);
-          if (count >= K) key |= 1u << bit;
-        }
-        reach(key + 1, mass, count);
-        ties = K - count;
-        total = key ? mass + ties * weight(unordered(key), w, s) : mass;
-      }
-      if (by_p) {
-        if (!K) {
-          reach(0, mass, count);
-          total = mass;
-        }
-        const u64 want = part_of(total);
-        unsigned pkey = 0;
-        for (int bit = 31; bit >= 0; --bit) {
-          const unsigned tried = pkey | 1u << bit;
-          if (tried <= key) {
-            pkey = tried;  // the k kept entries reach all of their mass
-          } else {
-            reach(tried, mass, count);
-            if (mass >= want) pkey = tried;
-          }
-        }
-        reach(pkey + 1, mass, count);
-        const u64 one = weight(unordered(pkey), w, s);
-        const u64 need = one ? (want - mass + one - 1) / one : 1;
-        ties = pkey > key ? (unsigned)need : (unsigned)min((u64)ties, need);
-        key = pkey;
-      }
-      // The id of the last tie that is kept: ties by chunk, then within the chunk.
-      __syncthreads();
-      for (int i = tid; i < kChunks; i += kThreads) s.eq[i] = 0;
-      __syncthreads();
-      unsigned mine = 0, ties_before = 0;
-      r.template tiles_by_chunk<1>([&](int c, int, const uint32_t (&v)[WORDS]) {
-        unsigned e = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) e += ordered(element<F32>(v, i)) == key;
-        e = __reduce_add_sync(0xffffffffu, e);
-        if (lane == 0) {
-          s.eq[c] += e;
-          mine += e;
-        }
-      });
-      u64 z = 0;
-      unsigned all_eq = mine;
-      r.sum(z, all_eq, nullptr, nullptr, &ties_before);
-      __syncthreads();
-      cut = Cut{key, 0x7fffffff, 0, 1};
-      if (tid == 0) s.cut.id = 0x7fffffff;
-      __syncthreads();
-      if (all_eq > ties && warp == 0) {
-        // Does the tie number `ties` lie here?
-        unsigned run = ties_before;
-        for (int i0 = 0; i0 < r.chunks; i0 += 32) {
-          const unsigned x = i0 + lane < r.chunks ? s.eq[i0 + lane] : 0, incl = scan_up(x, lane);
-          const unsigned hit = __ballot_sync(0xffffffffu, run + incl >= ties && run + incl - x < ties);
-          if (hit) {
-            const int k = __ffs(hit) - 1, c = i0 + k;
-            unsigned seen = run + __shfl_sync(0xffffffffu, incl - x, k);
-            for (int tl = c << a.shift; tl < min(tiles, (c + 1) << a.shift); ++tl) {
-              uint32_t v[WORDS];
-              load_tile<F32, VEC>(r.row, begin + tl * kTile, end, lane, v);
-#pragma unroll
-              for (int g = 0; g < (F32 ? 2 : 1); ++g) {
-                constexpr int PER = F32 ? 4 : 8;
-                unsigned e = 0;
-#pragma unroll
-                for (int i = 0; i < PER; ++i) e += ordered(element<F32>(v, g * PER + i)) == key;
-                const unsigned inc = scan_up(e, lane);
-                unsigned at = seen + inc - e;
-#pragma unroll
-                for (int i = 0; i < PER; ++i)
-                  if (ordered(element<F32>(v, g * PER + i)) == key && ++at == ties)
-                    s.cut.id = begin + tl * kTile + tile_id<F32>(lane, g * PER + i);
-                seen += __shfl_sync(0xffffffffu, inc, 31);
-              }
-            }
-            break;
-          }
-          run += __shfl_sync(0xffffffffu, incl, 31);
+          add64(&s.rec_lo[wp][j], &s.rec_hi[wp][j], x);
+          sum += x;
         }
       }
+    } else {
       __syncthreads();
-      u64 id = (u64)(unsigned)(s.cut.id == 0x7fffffff ? 0 : s.cut.id + 1);  // one CTA at most has it
-      if (tid != 0) id = 0;
-      unsigned any = tid == 0 && s.cut.id != 0x7fffffff;
-      r.sum(id, any);
-      if (any) cut.id = (int)id - 1;
-      lo = fmaxf(floor_l, fmaxf(unordered(key), -FLT_MAX));
-      lists = false;
+      cut_by_bits(r, K, by_p, part);
+      cut = true;
+      sum = r.pass(fmaxf(floor_l, unordered(s.cut_key)), FLT_MAX, true, false, sure);
     }
   }
 
-  // Masses of the kept entries by chunk.
-  const bool all_kept = cut.key == 0 && floor_l == -FLT_MAX;
-  auto kept = [&](float l, int id) {
-    const unsigned k = ordered(l);
-    return l >= floor_l && (k > cut.key || (k == cut.key && id <= cut.id));
-  };
-  __syncthreads();
-  for (int i = tid; i < kChunks; i += kThreads) s.ch.lo[i] = s.ch.hi[i] = 0;
-  if (!lists && tid == 0) s.over = 1;
-  __syncthreads();
-  u64 sum = 0;
-  if (all_kept) {
-    r.template tiles_by_chunk<1>([&](int c, int, const uint32_t (&x)[WORDS]) {
-      u64 t8 = 0;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float l = element<F32>(x, e);
-        t8 += l > neg_inf() ? weight(l, w, s) : 0;
-      }
-      sum += t8;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) t8 += __shfl_xor_sync(0xffffffffu, t8, o);
-      if (lane == 0) add64(&s.ch.lo[c], &s.ch.hi[c], t8);
-    });
-  } else {
-    const float from = cut.key ? fmaxf(lo, fmaxf(floor_l, unordered(cut.key))) : fmaxf(lo, floor_l);
-    r.again(from, [&](float l, int id) {
-      if (kept(l, id)) {
-        const u64 x = weight(l, w, s);
-        const int c = (id - begin) / kTile >> a.shift;
-        add64(&s.ch.lo[c], &s.ch.hi[c], x);
-        sum += x;
-      }
-    });
-  }
-  u64 all = sum, before = 0, here = 0;
-  unsigned z = 0;
-  r.sum(all, z, &before, &here);
   // The smallest id whose cumulative weight exceeds u times the sum; for u = 1 the last one that is kept.
-  const u64 goal = u < 1.0f ? __umul64hi(all, (u64)((double)u * 18446744073709551616.0)) : all - 1;
-  if (goal < before || goal >= before + here) return;
+  u64 all = sum, before = 0, mine = 0;
+  unsigned z1 = 0, z2 = 0;
+  r.sum(all, z1, z2, &before, &mine);
+  const u64 goal = u < 1.0f ? __umul64hi(all, fraction(u)) : all - 1;
+  if (goal < before || goal >= before + mine) return;
   __syncthreads();
-  if (warp != 0) return;
-  u64 run = before;
-  int at = -1;
-  for (int i0 = 0; i0 < r.chunks && at < 0; i0 += 32) {
-    const u64 x = i0 + lane < r.chunks ? (u64)s.ch.hi[i0 + lane] << 32 | s.ch.lo[i0 + lane] : 0;
+  // The record, by every warp: 32 at a time, in the order of ids.
+  u64 start = before;
+  int from = begin, to = begin;
+  bool there = false;
+  for (int i = 0; i < kWarps * kRecords && !there; i += 32) {
+    const int wp = i / kRecords, j = i % kRecords + lane, recs = s.recs[wp];
+    if (i % kRecords >= recs) continue;
+    const u64 x = j < recs ? (u64)s.rec_hi[wp][j] << 32 | s.rec_lo[wp][j] : 0;
+    const int e = s.rec_end[wp][min(j, recs - 1)];
     const u64 incl = scan_up(x, lane);
-    const unsigned hit = __ballot_sync(0xffffffffu, run + incl > goal);
+    const unsigned hit = __ballot_sync(0xffffffffu, start + incl > goal);
     if (hit) {
       const int k = __ffs(hit) - 1;
-      at = i0 + k;
-      run += __shfl_sync(0xffffffffu, incl - x, k);
+      start += __shfl_sync(0xffffffffu, incl - x, k);
+      const int before_e = __shfl_sync(0xffffffffu, e, max(k - 1, 0));
+      from = k > 0 ? before_e : i % kRecords ? s.rec_end[wp][i % kRecords - 1] : begin + min(tiles, wp * r.seg) * kTile;
+      to = __shfl_sync(0xffffffffu, e, k);
+      there = true;
     } else {
-      run += __shfl_sync(0xffffffffu, incl, 31);
+      start += __shfl_sync(0xffffffffu, incl, 31);
     }
   }
-  if (at < 0) return;
-  for (int tl = at << a.shift; tl < min(tiles, (at + 1) << a.shift); ++tl) {
+  if (!there) return;
+  // Its tiles, one a warp, until the one that reaches the goal.
+  const unsigned key = cut ? s.cut_key : 0u;
+  const int cut_id = cut ? s.cut_id : 0;
+  auto kept = [&](float l, int id) {
+    const unsigned k = ordered(l);
+    return l > neg_inf() && l >= floor_l && id >= from && id < to && (k > key || (k == key && id <= cut_id));
+  };
+  const int t_end = (to - begin + kTile - 1) / kTile;
+#pragma unroll 1
+  for (int t0 = (from - begin) / kTile; t0 < t_end; t0 += kWarps) {
+    const int t = t0 + warp, base = begin + t * kTile;
     uint32_t v[WORDS];
-    load_tile<F32, VEC>(r.row, begin + tl * kTile, end, lane, v);
+    load_tile<F32, VEC>(r.row, base, t < t_end ? end : 0, lane, v);
+    u64 x = 0;
 #pragma unroll
-    for (int g = 0; g < (F32 ? 2 : 1); ++g) {
-      constexpr int PER = F32 ? 4 : 8;
-      u64 x[PER], part8 = 0;
-#pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const float l = element<F32>(v, g * PER + i);
-        x[i] = l > neg_inf() && kept(l, begin + tl * kTile + tile_id<F32>(lane, g * PER + i)) ? weight(l, w, s) : 0;
-        part8 += x[i];
-      }
-      const u64 incl = scan_up(part8, lane);
-      const unsigned hit = __ballot_sync(0xffffffffu, run + incl > goal);
-      if (hit) {
-        if (lane == __ffs(hit) - 1) {
-          u64 c = run + incl - part8;
-#pragma unroll
-          for (int i = 0; i < PER; ++i) {
-            if (c <= goal && c + x[i] > goal) {
-              a.out[n] = begin + tl * kTile + tile_id<F32>(lane, g * PER + i);
-              if (a.prob) a.prob[n] = T == 0.0f ? 1.0f : (float)((double)x[i] / (double)all);
-            }
-            c += x[i];
-          }
-        }
-        return;
-      }
-      run += __shfl_sync(0xffffffffu, incl, 31);
+    for (int e = 0; e < 8; ++e) {
+      const float l = element<F32>(v, e);
+      if (kept(l, base + tile_id<F32>(lane, e))) x += r.weigh(l);
     }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    if (lane == 0) s.tile_sum[warp] = x;
+    __syncthreads();
+    u64 run = start;
+    int hit = -1;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+      const u64 y = s.tile_sum[i];
+      if (hit < 0) {
+        if (run + y > goal)
+          hit = i;
+        else
+          run += y;
+      }
+    }
+    start = run;
+    if (hit == warp) {
+#pragma unroll
+      for (int g = 0; g < (F32 ? 2 : 1); ++g) {
+        constexpr int PER = F32 ? 4 : 8;
+        u64 mine8 = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          const float l = element<F32>(v, g * PER + i);
+          if (kept(l, base + tile_id<F32>(lane, g * PER + i))) mine8 += r.weigh(l);
+        }
+        const u64 incl = scan_up(mine8, lane);
+        const unsigned lanes = __ballot_sync(0xffffffffu, run + incl > goal);
+        if (lanes) {
+          if (lane == __ffs(lanes) - 1) {
+            u64 c = run + incl - mine8;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+              const float l = element<F32>(v, g * PER + i);
+              const int id = base + tile_id<F32>(lane, g * PER + i);
+              const u64 y = kept(l, id) ? r.weigh(l) : 0;
+              if (c <= goal && c + y > goal) {
+                a.out[n] = id;
+                if (a.prob) a.prob[n] = T == 0.0f ? 1.0f : ratio(y, all);
+              }
+              c += y;
+            }
+          }
+          break;
+        }
+        run += __shfl_sync(0xffffffffu, incl, 31);
+      }
+    }
+    if (hit >= 0) return;
+    __syncthreads();
   }
 }
 
@@ -958,10 +1190,21 @@ namespace {
 
 bool misaligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
 
-static_assert(sizeof(sv::fs::Shared) <= 48 * 1024, "shared memory");
-
-template <bool F32>
-int launch(const sv::fs::Args& a, bool vec, cudaStream_t st) {
+template <bool F32, bool VEC>
+int launch(const sv::fs::Args& a, cudaStream_t st) {
+  static std::mutex mu;
+  static bool set[64] = {};
+  int device = 0;
+  if (cudaGetDevice(&device) != cudaSuccess || device < 0 || device >= 64) return SV_ERR_CUDA;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!set[device]) {
+      if (cudaFuncSetAttribute(sv::fs::sample_kernel<F32, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)sizeof(sv::fs::Shared)) != cudaSuccess)
+        return SV_ERR_CUDA;
+      set[device] = true;
+    }
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.N * a.nc));
   cfg.blockDim = dim3(sv::fs::kThreads);
@@ -973,9 +1216,7 @@ int launch(const sv::fs::Args& a, bool vec, cudaStream_t st) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = vec ? cudaLaunchKernelEx(&cfg, sv::fs::sample_kernel<F32, true>, a)
-                            : cudaLaunchKernelEx(&cfg, sv::fs::sample_kernel<F32, false>, a);
-  return e == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, sv::fs::sample_kernel<F32, VEC>, a) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 
 }  // namespace
@@ -1013,14 +1254,15 @@ extern "C" int spec_filtered_sample(const void* logits, int64_t row_stride, cons
   a.prob = out_probs;
   a.status = status;
   a.nc = 1;
-  while (a.nc < sv::fs::kMaxCluster && (long long)N * a.nc * 2 <= 608 && V >= 8192 * a.nc) a.nc *= 2;
+  while (a.nc < sv::fs::kMaxCluster && V >= 8192 * a.nc && ((long long)N * a.nc * 2 <= 608 || V > 32768 * a.nc)) a.nc *= 2;
   const int tile = sv::fs::kTile;
   a.share = (int)(((long long)V + (long long)tile * a.nc - 1) / ((long long)tile * a.nc) * tile);
-  while ((long long)tile << a.shift < ((long long)a.share + sv::fs::kChunks - 1) / sv::fs::kChunks) ++a.shift;
+  a.step = std::max(1, V / (1 << 14) > 8 ? 8 : V / (1 << 14));
   int lg = 0;
   while ((1ll << lg) < V) ++lg;
   a.scale_bits = std::min(44, 61 - lg);
   const bool vec = !misaligned(logits, 16) && ((size_t)row_stride * es) % 16 == 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return dtype == SV_F32 ? launch<true>(a, vec, st) : launch<false>(a, vec, st);
+  if (dtype == SV_F32) return vec ? launch<true, true>(a, st) : launch<true, false>(a, st);
+  return vec ? launch<false, true>(a, st) : launch<false, false>(a, st);
 }
