@@ -96,7 +96,8 @@ struct Shared {
   unsigned wcnt[2][kWarps], wmore[2][kWarps];
   u64 inbox[2][kMaxCluster];
   unsigned inbox_c[2][kMaxCluster], inbox_d[2][kMaxCluster];
-  u64 tile_sum[kWarps];
+  u64 tile_sum[kWarps], hit_start;
+  int hit_from, hit_to;
   float fmass[kWarps], fvar[kWarps], wmax[kWarps];
   unsigned n_aside, n_cand[4];
   int edge[6], bin;  // edges: of each attempt the window's upper and lower one
@@ -231,23 +232,49 @@ SV_DEVINL unsigned scan_up(unsigned x, int lane) {
 }
 
 // Among the n candidates of the cut's bin (first CTA), the one at which the running count reaches
-// `want_count`, or the running mass `want` (and does so for every mass from want_lo to want).
+// `want`, or the running mass does (and does so for every mass from want_lo to want).
 // s.bin_mass and s.bin_count are what lies above the bin.
 __device__ __noinline__ void order_candidates(Shared& s, int n, bool by_count, u64 want_lo, u64 want) {
   const int tid = threadIdx.x;
   if (tid == 0) s.cut_found = 0;
-  int size = 32;
-  while (size < n) size <<= 1;
-  for (int i = n + tid; i < size; i += kThreads) s.cand[i] = 0;
+  u64 mine = 0, x = 0;
+  if (n <= kThreads) {
+    // A thread a candidate: what stands before it.
+    if (tid < n) {
+      mine = s.cand[tid];
+      x = weight(unordered((unsigned)(mine >> 32)), s.w, s.tab);
+      s.cand[kCand / 2 + tid] = x;
+    }
+    __syncthreads();
+    if (tid >= n) return;
+    u64 mass = s.bin_mass;
+    unsigned count = s.bin_count;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const bool before = s.cand[i] > mine;
+      mass += before ? s.cand[kCand / 2 + i] : 0;
+      count += before;
+    }
+    if (by_count ? count + 1 == want : mass < want && mass + x >= want) {
+      s.cut_key = (unsigned)(mine >> 32);
+      s.cut_id = (int)~(unsigned)mine;
+      s.cut_mass = mass + x;
+      s.cut_found = by_count || mass < want_lo ? 1 : 2;
+    }
+    return;
+  }
+  for (int i = n + tid; i < kCand; i += kThreads) s.cand[i] = 0;
   __syncthreads();
   // Largest first (bitonic).
-  for (int k = 2; k <= size; k <<= 1)
+#pragma unroll 1
+  for (int k = 2; k <= kCand; k <<= 1)
+#pragma unroll 1
     for (int j = k >> 1; j > 0; j >>= 1) {
-      for (int i = tid; i < size / 2; i += kThreads) {
-        const int p = (i / j) * 2 * j + i % j, q = p + j;
-        const u64 x = s.cand[p], y = s.cand[q];
-        const bool down = (p & k) == 0;
-        if (down ? x < y : x > y) s.cand[p] = y, s.cand[q] = x;
+#pragma unroll 1
+      for (int i = tid; i < kCand / 2; i += kThreads) {
+        const int p = 2 * i - (i & (j - 1)), q = p + j;
+        const u64 a = s.cand[p], b = s.cand[q];
+        if ((p & k) == 0 ? a < b : a > b) s.cand[p] = b, s.cand[q] = a;
       }
       __syncthreads();
     }
@@ -255,15 +282,15 @@ __device__ __noinline__ void order_candidates(Shared& s, int n, bool by_count, u
   if (tid >= 32) return;
   u64 mass = s.bin_mass;
   const unsigned above_count = s.bin_count;
+#pragma unroll 1
   for (int i0 = 0; i0 < n; i0 += 32) {
-    const u64 c = i0 + tid < n ? s.cand[i0 + tid] : 0;
-    const u64 x = i0 + tid < n ? weight(unordered((unsigned)(c >> 32)), s.w, s.tab) : 0;
+    mine = i0 + tid < n ? s.cand[i0 + tid] : 0;
+    x = i0 + tid < n ? weight(unordered((unsigned)(mine >> 32)), s.w, s.tab) : 0;
     const u64 incl = scan_up(x, tid);
-    const bool hit = i0 + tid < n &&
-                     (by_count ? above_count + i0 + tid + 1 == want : mass + incl >= want && mass + incl - x < want);
-    if (hit) {
-      s.cut_key = (unsigned)(c >> 32);
-      s.cut_id = (int)~(unsigned)c;
+    if (i0 + tid < n &&
+        (by_count ? above_count + i0 + tid + 1 == want : mass + incl >= want && mass + incl - x < want)) {
+      s.cut_key = (unsigned)(mine >> 32);
+      s.cut_id = (int)~(unsigned)mine;
       s.cut_mass = mass + incl;
       s.cut_found = by_count || mass + incl - x < want_lo ? 1 : 2;
     }
@@ -271,7 +298,11 @@ __device__ __noinline__ void order_candidates(Shared& s, int n, bool by_count, u
   }
 }
 
-
+SV_DEVINL float sqrt_fast(float x) {
+  float y;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 SV_DEVINL float next_down(float x) { return x * (1.0f - 0x1p-23f); }  // x > 0: below x by one or two steps
 
 // x 2^64, 0 <= x < 1, rounded down.
@@ -313,40 +344,33 @@ struct Row {
   }
   SV_DEVINL u64 weigh(float l) const { return weight(l, w, s.tab); }
 
-  // Sums over the row's CTAs, the same in every thread; `before`: over the CTAs of lower rank, `mine`: this one's.
-  SV_DEVINL void sum(u64& x, unsigned& c, unsigned& d, u64* before = nullptr, u64* mine = nullptr,
-                     unsigned* c_before = nullptr) {
-    const int t = turn & 1;
+  // Sums over the row's CTAs, the same in every thread. Each CTA's are left in the inboxes of `turn`.
+  SV_DEVINL void sum(u64& x, unsigned& c, unsigned& d) {
+    const int t = turn & 1, ln = lane(), wp = threadIdx.x >> 5;
     ++turn;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     c = __reduce_add_sync(0xffffffffu, c);
     d = __reduce_add_sync(0xffffffffu, d);
-    if (lane() == 0) {
-      const int wp = threadIdx.x >> 5;
-      s.wsum[t][wp] = x, s.wcnt[t][wp] = c, s.wmore[t][wp] = d;
-    }
+    if (ln == 0) s.wsum[t][wp] = x, s.wcnt[t][wp] = c, s.wmore[t][wp] = d;
     __syncthreads();
-    x = 0, c = 0, d = 0;
+    if (wp == 0) {
+      x = ln < kWarps ? s.wsum[t][ln] : 0;
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) x += s.wsum[t][i], c += s.wcnt[t][i], d += s.wmore[t][i];
-    if (before) *before = 0, *mine = x;
-    if (c_before) *c_before = 0;
-    if (a.nc == 1) return;
-    if ((int)threadIdx.x < a.nc) {
-      dsmem_st_u64(remote(&s.inbox[t][rank], threadIdx.x), x);
-      dsmem_st_u32(remote(&s.inbox_c[t][rank], threadIdx.x), c);
-      dsmem_st_u32(remote(&s.inbox_d[t][rank], threadIdx.x), d);
-    }
-    cluster_sync();
-    x = 0, c = 0, d = 0;
-    for (int i = 0; i < a.nc; ++i) {
-      if (i == (int)rank) {
-        if (before) *before = x;
-        if (c_before) *c_before = c;
+      for (int o = kWarps / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+      x = __shfl_sync(0xffffffffu, x, 0);
+      c = __reduce_add_sync(0xffffffffu, ln < kWarps ? s.wcnt[t][ln] : 0u);
+      d = __reduce_add_sync(0xffffffffu, ln < kWarps ? s.wmore[t][ln] : 0u);
+      if (ln < a.nc) {
+        dsmem_st_u64(remote(&s.inbox[t][rank], ln), x);
+        dsmem_st_u32(remote(&s.inbox_c[t][rank], ln), c);
+        dsmem_st_u32(remote(&s.inbox_d[t][rank], ln), d);
       }
-      x += s.inbox[t][i], c += s.inbox_c[t][i], d += s.inbox_d[t][i];
     }
+    sync();
+    x = 0, c = 0, d = 0;
+#pragma unroll 1
+    for (int i = 0; i < a.nc; ++i) x += s.inbox[t][i], c += s.inbox_c[t][i], d += s.inbox_d[t][i];
   }
   SV_DEVINL void sum(u64& x, unsigned& c) {
     unsigned d = 0;
@@ -585,8 +609,8 @@ SV_DEVINL void cut_by_bits(Row<F32, VEC>& r, unsigned K, bool by_p, u64 part) {
   unsigned before = 0, all = mine;
   u64 z = 0;
   const int t = r.turn & 1;
-  unsigned none = 0;
-  r.sum(z, all, none, nullptr, nullptr, &before);
+  r.sum(z, all);
+  for (int i = 0; i < (int)r.rank; ++i) before += s.inbox_c[t][i];
   for (int i = 0; i < warp; ++i) before += s.wcnt[t][i];
   const unsigned here = s.wcnt[t][warp];
   if (tid == 0) s.cut_id = 0x7fffffff;
@@ -713,6 +737,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
     });
     if (nan) m = __int_as_float(0x7fc00000);
   }
+  const float m_lane = m;
   for (int i = tid; i < 1024; i += kThreads) s.tab[i] = kSvExp2Table1024[i];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -780,25 +805,31 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
   } else {
     bool found = false;
     u64 mass_all = 0, slack = 0;  // of the row, and what it may be off by
-    const float unit = 16.0f * c_hi;
+    const float unit = 16.0f * c_hi, w_m = __ull2float_rn(r.weigh(m));
+    // For small k the threads' maxima will do as a sample: where k of them lie, at least k entries do.
+    const bool by_top = K > 1 && K <= 16u * (unsigned)a.nc;
     if (summed && w.fast) {
       // A thread's sum is relative to 2^far, where its maximum was.
       unsigned z = 0;
-      mass_all = run > 0.0f ? __float2ull_rn(run * ex2_fast(__fmaf_rn(-m, c_hi, far) - m * c_lo) *
-                                             __ull2float_rn(r.weigh(m)))
-                            : 0;
+      mass_all = run > 0.0f ? __float2ull_rn(run * ex2_fast(__fmaf_rn(-m, c_hi, far) - m * c_lo) * w_m) : 0;
       r.sum(mass_all, z);
       slack = mass_all >> 21;
     }
     if (K != 1 && w.fast) {
-      r.template some_tiles<2>(warp * a.step, tiles, kWarps * a.step, [&](int, const uint32_t (&x)[WORDS]) {
+      if (by_top) {
+        const float d = (m - m_lane) * unit;
+        if (d < (float)kSampleBins) atomicAdd(&s.sample[(int)d], 1u);
+      } else {
+        r.template some_tiles<2>(warp * a.step, tiles, kWarps * a.step, [&](int, const uint32_t (&x)[WORDS]) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float d = (m - element<F32>(x, e)) * unit;
-          if (d < (float)kSampleBins) atomicAdd(&s.sample[(int)d], 1u);
-        }
-      });
+          for (int e = 0; e < 8; ++e) {
+            const float d = (m - element<F32>(x, e)) * unit;
+            if (d < (float)kSampleBins) atomicAdd(&s.sample[(int)d], 1u);
+          }
+        });
+      }
       int sampled = 0;
+#pragma unroll 1
       for (int i = 0; i < a.nc; ++i) {
         const int len = min(a.share, max(0, a.V - i * a.share)), n_tiles = (len + kTile - 1) / kTile;
         const int k = (n_tiles + a.step - 1) / a.step;
@@ -832,9 +863,9 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
         all_c += s.wcnt[0][i];
       }
       cm += below_m, cv += below_v;
-      const float scale = (float)a.V / (float)max(sampled, 1);
-      const float want_below = K ? 0.0f : (1.0f - top_p) * __ull2float_rn(mass_all) / __ull2float_rn(r.weigh(m)) / scale;
-#pragma unroll
+      const float scale = by_top ? 1.0f : (float)a.V / (float)max(sampled, 1);
+      const float want_below = K ? 0.0f : (1.0f - top_p) * __ull2float_rn(mass_all) / (w_m * scale);
+#pragma unroll 1
       for (int t = 0; t < 3; ++t) {
         const float z = t == 0 ? 3.5f : t == 1 ? 8.0f : 20.0f, rel = t == 0 ? 0.03f : t == 1 ? 0.15f : 0.5f;
         int up = -1, down = -1;  // the deepest bin edge that is surely above the cut; that is not surely below it
@@ -842,11 +873,14 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
         for (int j = 0; j < 2; ++j) {
           const int edge = b + j;
           if (K) {
-            const float above = (float)(all_c - cc + (j ? c0 : 0u)), dev = z * sqrtf(above + 1.0f) + 2.0f;
-            if (!by_p && (above + dev) * scale <= (float)K) up = edge;
+            const float above = (float)(all_c - cc + (j ? c0 : 0u));
+            const float dev = by_top ? 0.0f : z * sqrt_fast(above + 1.0f) + 2.0f;
+            if (!by_p && !by_top && (above + dev) * scale <= (float)K) up = edge;
             if ((above - dev) * scale < (float)K) down = edge;
           } else {
-            const float mass = j ? cm - m0 : cm, dev = z * sqrtf(j ? fmaxf(cv - v0, 0.0f) : cv) + rel * mass;
+            // (An entry that the sample has missed may weigh as much as the edge's: one more in the variance.)
+            const float one = j ? w1 : w0, mass = j ? cm - m0 : cm;
+            const float dev = z * sqrt_fast((j ? fmaxf(cv - v0, 0.0f) : cv) + one * one) + rel * mass + 2.0f * one;
             if (mass - dev >= want_below) up = edge;
             if (mass + dev > want_below) down = edge;
           }
@@ -1081,41 +1115,60 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
   }
 
   // The smallest id whose cumulative weight exceeds u times the sum; for u = 1 the last one that is kept.
-  u64 all = sum, before = 0, mine = 0;
+  const int last_turn = r.turn & 1;
+  u64 all = sum;
   unsigned z1 = 0, z2 = 0;
-  r.sum(all, z1, z2, &before, &mine);
+  r.sum(all, z1, z2);
   const u64 goal = u < 1.0f ? __umul64hi(all, fraction(u)) : all - 1;
-  if (goal < before || goal >= before + mine) return;
-  __syncthreads();
-  // The record, by every warp: 32 at a time, in the order of ids.
-  u64 start = before;
-  int from = begin, to = begin;
-  bool there = false;
-  for (int i = 0; i < kWarps * kRecords && !there; i += 32) {
-    const int wp = i / kRecords, j = i % kRecords + lane, recs = s.recs[wp];
-    if (i % kRecords >= recs) continue;
-    const u64 x = j < recs ? (u64)s.rec_hi[wp][j] << 32 | s.rec_lo[wp][j] : 0;
-    const int e = s.rec_end[wp][min(j, recs - 1)];
-    const u64 incl = scan_up(x, lane);
-    const unsigned hit = __ballot_sync(0xffffffffu, start + incl > goal);
-    if (hit) {
-      const int k = __ffs(hit) - 1;
-      start += __shfl_sync(0xffffffffu, incl - x, k);
-      const int before_e = __shfl_sync(0xffffffffu, e, max(k - 1, 0));
-      from = k > 0 ? before_e : i % kRecords ? s.rec_end[wp][i % kRecords - 1] : begin + min(tiles, wp * r.seg) * kTile;
-      to = __shfl_sync(0xffffffffu, e, k);
-      there = true;
-    } else {
-      start += __shfl_sync(0xffffffffu, incl, 31);
+  u64 before = 0;
+#pragma unroll 1
+  for (int i = 0; i < (int)rank; ++i) before += s.inbox[last_turn][i];
+  if (goal < before || goal >= before + s.inbox[last_turn][rank]) return;
+  // Its record, 32 at a time in the order of ids.
+  if (warp == 0) {
+    int wp = 0;
+    u64 start = before;
+    int from = begin, to = begin;
+    bool there = false;
+#pragma unroll 1
+    for (int i = 0; i < kWarps * kRecords && !there; i += 32) {
+      wp = i / kRecords;
+      const int j = i % kRecords + lane, recs = s.recs[wp];
+      if (i % kRecords >= recs) continue;
+      const u64 x = j < recs ? (u64)s.rec_hi[wp][j] << 32 | s.rec_lo[wp][j] : 0;
+      const int e = s.rec_end[wp][min(j, recs - 1)];
+      const u64 incl = scan_up(x, lane);
+      const unsigned hit = __ballot_sync(0xffffffffu, start + incl > goal);
+      if (hit) {
+        const int k = __ffs(hit) - 1;
+        start += __shfl_sync(0xffffffffu, incl - x, k);
+        const int before_e = __shfl_sync(0xffffffffu, e, max(k - 1, 0));
+        from = k > 0           ? before_e
+               : i % kRecords ? s.rec_end[wp][i % kRecords - 1]
+                              : begin + min(tiles, wp * r.seg) * kTile;
+        to = __shfl_sync(0xffffffffu, e, k);
+        there = true;
+      } else {
+        start += __shfl_sync(0xffffffffu, incl, 31);
+      }
     }
+    if (lane == 0) s.hit_from = from, s.hit_to = to, s.hit_start = start;
   }
-  if (!there) return;
+  __syncthreads();
   // Its tiles, one a warp, until the one that reaches the goal.
+  const int from = s.hit_from, to = s.hit_to;
+  u64 start = s.hit_start;
   const unsigned key = cut ? s.cut_key : 0u;
   const int cut_id = cut ? s.cut_id : 0;
-  auto kept = [&](float l, int id) {
+  float* tile = reinterpret_cast<float*>(s.list[warp]);  // the warp's tile, in the order of ids
+  // The kept weight of element 32 i + lane of the tile that begins at `base`.
+  auto kept = [&](int i, int base) -> u64 {
+    const float l = tile[32 * i + lane];
+    const int id = base + 32 * i + lane;
     const unsigned k = ordered(l);
-    return l > neg_inf() && l >= floor_l && id >= from && id < to && (k > key || (k == key && id <= cut_id));
+    return l > neg_inf() && l >= floor_l && id >= from && id < to && (k > key || (k == key && id <= cut_id))
+               ? r.weigh(l)
+               : 0;
   };
   const int t_end = (to - begin + kTile - 1) / kTile;
 #pragma unroll 1
@@ -1123,62 +1176,50 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
     const int t = t0 + warp, base = begin + t * kTile;
     uint32_t v[WORDS];
     load_tile<F32, VEC>(r.row, base, t < t_end ? end : 0, lane, v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) tile[tile_id<F32>(lane, e)] = element<F32>(v, e);
+    __syncwarp();
     u64 x = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float l = element<F32>(v, e);
-      if (kept(l, base + tile_id<F32>(lane, e))) x += r.weigh(l);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    if (lane == 0) s.tile_sum[warp] = x;
-    __syncthreads();
-    u64 run = start;
+    // The first turn sums the warps' tiles; in the second the warp whose tile it is looks for the id.
+    u64 run = 0;
     int hit = -1;
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-      const u64 y = s.tile_sum[i];
-      if (hit < 0) {
-        if (run + y > goal)
-          hit = i;
-        else
-          run += y;
-      }
-    }
-    start = run;
-    if (hit == warp) {
-#pragma unroll
-      for (int g = 0; g < (F32 ? 2 : 1); ++g) {
-        constexpr int PER = F32 ? 4 : 8;
-        u64 mine8 = 0;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-          const float l = element<F32>(v, g * PER + i);
-          if (kept(l, base + tile_id<F32>(lane, g * PER + i))) mine8 += r.weigh(l);
+#pragma unroll 1
+    for (int turn = 0; turn < 2; ++turn) {
+#pragma unroll 1
+      for (int i = 0; i < 8; ++i) {
+        const u64 y = kept(i, base);
+        if (turn == 0) {
+          x += y;
+          continue;
         }
-        const u64 incl = scan_up(mine8, lane);
+        const u64 incl = scan_up(y, lane);
         const unsigned lanes = __ballot_sync(0xffffffffu, run + incl > goal);
         if (lanes) {
           if (lane == __ffs(lanes) - 1) {
-            u64 c = run + incl - mine8;
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-              const float l = element<F32>(v, g * PER + i);
-              const int id = base + tile_id<F32>(lane, g * PER + i);
-              const u64 y = kept(l, id) ? r.weigh(l) : 0;
-              if (c <= goal && c + y > goal) {
-                a.out[n] = id;
-                if (a.prob) a.prob[n] = T == 0.0f ? 1.0f : ratio(y, all);
-              }
-              c += y;
-            }
+            a.out[n] = base + 32 * i + lane;
+            if (a.prob) a.prob[n] = T == 0.0f ? 1.0f : ratio(y, all);
           }
-          break;
+          return;
         }
         run += __shfl_sync(0xffffffffu, incl, 31);
       }
+      if (turn == 1) return;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+      if (lane == 0) s.tile_sum[warp] = x;
+      __syncthreads();
+      run = start;
+#pragma unroll 1
+      for (int i = 0; i < kWarps && hit < 0; ++i) {
+        if (run + s.tile_sum[i] > goal)
+          hit = i;
+        else
+          run += s.tile_sum[i];
+      }
+      if (hit != warp) break;
     }
     if (hit >= 0) return;
+    start = run;
     __syncthreads();
   }
 }
