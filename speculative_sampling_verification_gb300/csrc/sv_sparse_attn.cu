@@ -30,9 +30,9 @@ constexpr float kCodeMax = 127.0f;
 // code_max scale (to the fp32 rounding of the product that makes the code). A page
 // that holds NaN or infinity gets the scale +inf, which selects it before others.
 //
-// One block a (sequence, head) and a share of the pages that got tokens. A group of
-// lanes takes a key (16 bytes a lane), the groups take the keys in turn, and the
-// groups' minima and maxima meet in shared memory.
+// A warp takes a page of a head by itself: its lanes hold a few channels each (the narrowest of 4, 8 or 16
+// bytes that lets 32 lanes hold a key) and go through the page's keys, several loads under way; no
+// barrier, and one exchange at the end. Rows that do not fit (odd or long ones) go channel by channel.
 
 constexpr int kBoundThreads = 128;
 
@@ -69,6 +69,10 @@ SV_DEVINL uint32_t max2_nan(uint32_t a, uint32_t b) {
   return r;
 }
 
+SV_DEVINL signed char bound_code(float x, bool fine) {
+  return fine ? (signed char)(int)fminf(fmaxf(x, -kCodeMax), kCodeMax) : (signed char)0;
+}
+
 // Four e4m3 codes as floats.
 SV_DEVINL void e4m3x4(uint32_t w, float (&v)[4]) {
 #pragma unroll
@@ -80,129 +84,172 @@ SV_DEVINL void e4m3x4(uint32_t w, float (&v)[4]) {
   }
 }
 
-template <bool F8, bool VEC>
+// The values in a lane's bytes of a key.
+template <bool F8, int BYTES>
+struct Piece {
+  static constexpr int N = F8 ? BYTES : BYTES / 2;
+  uint32_t w[BYTES / 4];
+  SV_DEVINL void load(const unsigned char* p) {
+    if constexpr (BYTES == 4) {
+      w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+    } else if constexpr (BYTES == 8) {
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+      w[0] = v.x, w[1] = v.y;
+    } else {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+      w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    }
+  }
+};
+
+// BYTES a lane (0: any row, channel by channel).
+template <bool F8, int BYTES>
 __global__ void __launch_bounds__(kBoundThreads) page_bounds_kernel(const __grid_constant__ BoundArgs a) {
-  extern __shared__ float part[];  // [groups][2][D]
-  __shared__ float red[kBoundThreads / 32];
-  constexpr int PER = F8 ? 16 : 8;  // values of 16 bytes
-  const int chunk = blockIdx.x % a.chunks, hk = blockIdx.x / a.chunks % a.Hkv, b = blockIdx.x / a.chunks / a.Hkv;
-  const int tid = threadIdx.x;
+  const int lane = threadIdx.x & 31;
+  const long long item = (long long)blockIdx.x * (kBoundThreads / 32) + (threadIdx.x >> 5);
+  const int hk = (int)(item % a.Hkv), chunk = (int)(item / a.Hkv % a.chunks);
+  const long long b = item / a.Hkv / a.chunks;
+  if (b >= a.B) return;
   const long long ctx = a.ctx_lens[b], add = a.new_lens[b];
   if (add <= 0) return;
   const long long end = ctx + add;
   if (ctx < 0 || end > (long long)a.max_pages * a.P) {
-    if (tid == 0 && a.status) atomicOr(a.status, (unsigned)SV_DEV_PAGE_RANGE);
+    if (lane == 0 && a.status) atomicOr(a.status, (unsigned)SV_DEV_PAGE_RANGE);
     return;
   }
   const int p1 = (int)((end + a.P - 1) / a.P);
-  const int lanes = VEC ? a.D / PER : 1, groups = VEC ? kBoundThreads / lanes : 1;
-  const int g = VEC ? tid / lanes : 0, col = VEC ? (tid - g * lanes) * PER : 0;
+#pragma unroll 1
   for (int p = (int)(ctx / a.P) + chunk; p < p1; p += a.chunks) {
-    const int id = a.page_table[(long long)b * a.max_pages + p];
+    const int id = a.page_table[b * a.max_pages + p];
     if (id < 0 || id >= a.num_pages) {
-      if (tid == 0 && a.status) atomicOr(a.status, (unsigned)SV_DEV_PAGE_RANGE);
+      if (lane == 0 && a.status) atomicOr(a.status, (unsigned)SV_DEV_PAGE_RANGE);
       continue;
     }
     const int count = (int)min((long long)a.P, end - (long long)p * a.P);
     const long long row0 = ((long long)id * a.Hkv + hk) * a.P;
-    if constexpr (VEC) {
-      if (g < groups) {
-        float lo[PER], hi[PER];
-        if constexpr (!F8) {
-          uint32_t l[4], h[4];
+    const long long at = ((long long)id * a.Hkv + hk) * 2 * a.D;
+    if constexpr (BYTES > 0) {
+      constexpr int N = Piece<F8, BYTES>::N, U = 8;
+      const int row_bytes = F8 ? a.D : 2 * a.D, lanes = row_bytes / BYTES;  // lanes of a key, at most 32
+      const int per = 32 / lanes, g = lane / lanes, col = lane - g * lanes;
+      const bool on = g < per;
+      const unsigned char* base = static_cast<const unsigned char*>(a.kc) + row0 * row_bytes + col * BYTES;
+      float lo[N], hi[N];
+      uint32_t l2[BYTES / 4], h2[BYTES / 4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) l[i] = 0x7f807f80u, h[i] = 0xff80ff80u;
-#pragma unroll 4
-          for (int r = g; r < count; r += groups) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.kc) +
-                                                                 (row0 + r) * a.D + col));
-            l[0] = min2_nan(l[0], v.x), h[0] = max2_nan(h[0], v.x);
-            l[1] = min2_nan(l[1], v.y), h[1] = max2_nan(h[1], v.y);
-            l[2] = min2_nan(l[2], v.z), h[2] = max2_nan(h[2], v.z);
-            l[3] = min2_nan(l[3], v.w), h[3] = max2_nan(h[3], v.w);
-          }
+      for (int i = 0; i < N; ++i) lo[i] = INFINITY, hi[i] = -INFINITY;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            lo[2 * i] = bf16_lo(l[i]), lo[2 * i + 1] = bf16_hi(l[i]);
-            hi[2 * i] = bf16_lo(h[i]), hi[2 * i + 1] = bf16_hi(h[i]);
-          }
-        } else {
+      for (int i = 0; i < BYTES / 4; ++i) l2[i] = 0x7f807f80u, h2[i] = 0xff80ff80u;
+#pragma unroll 1
+      for (int r0 = g; r0 < count; r0 += per * U) {
+        Piece<F8, BYTES> x[U];
+        float s[U];
 #pragma unroll
-          for (int i = 0; i < PER; ++i) lo[i] = INFINITY, hi[i] = -INFINITY;
-#pragma unroll 2
-          for (int r = g; r < count; r += groups) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(a.kc) +
-                                                                 (row0 + r) * a.D + col));
-            const float s = __ldg(a.ks + row0 + r);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        for (int u = 0; u < U; ++u) {
+          const int r = min(r0 + u * per, count - 1);  // (a key twice changes nothing)
+          if (on) x[u].load(base + (long long)r * row_bytes);
+          if constexpr (F8) s[u] = on ? __ldg(a.ks + row0 + r) : 0.0f;
+        }
+        if (!on) continue;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              float x[4];
-              e4m3x4(w[q], x);
+        for (int u = 0; u < U; ++u) {
+          if constexpr (F8) {
+#pragma unroll
+            for (int q = 0; q < BYTES / 4; ++q) {
+              float v[4];
+              e4m3x4(x[u].w[q], v);
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                const float y = __fmul_rn(x[i], s);
+                const float y = __fmul_rn(v[i], s[u]);
                 lo[4 * q + i] = min_nan(lo[4 * q + i], y);
                 hi[4 * q + i] = max_nan(hi[4 * q + i], y);
               }
             }
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-          part[(2 * g) * a.D + col + i] = lo[i];
-          part[(2 * g + 1) * a.D + col + i] = hi[i];
-        }
-      }
-    } else {
-      for (int d = tid; d < a.D; d += kBoundThreads) {
-        float lo = INFINITY, hi = -INFINITY;
-        for (int r = 0; r < count; ++r) {
-          const long long at = (row0 + r) * a.D + d;
-          float y;
-          if constexpr (F8) {
-            const __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<const unsigned char*>(a.kc)[at], __NV_E4M3);
-            y = __fmul_rn(__half2float(*reinterpret_cast<const __half*>(&h)), a.ks[row0 + r]);
           } else {
-            y = __bfloat162float(static_cast<const __nv_bfloat16*>(a.kc)[at]);
+#pragma unroll
+            for (int q = 0; q < BYTES / 4; ++q) {
+              l2[q] = min2_nan(l2[q], x[u].w[q]);
+              h2[q] = max2_nan(h2[q], x[u].w[q]);
+            }
           }
-          lo = min_nan(lo, y);
-          hi = max_nan(hi, y);
         }
-        part[d] = lo;
-        part[a.D + d] = hi;
       }
-    }
-    __syncthreads();
-    // The groups' bounds of each channel, and the largest magnitude of all.
-    float amax = 0.0f;
-    for (int d = tid; d < a.D; d += kBoundThreads) {
-      float lo = part[d], hi = part[a.D + d];
+      if constexpr (!F8) {
+#pragma unroll
+        for (int q = 0; q < BYTES / 4; ++q) {
+          lo[2 * q] = bf16_lo(l2[q]), lo[2 * q + 1] = bf16_hi(l2[q]);
+          hi[2 * q] = bf16_lo(h2[q]), hi[2 * q + 1] = bf16_hi(h2[q]);
+        }
+      }
+      // The groups of lanes that took different keys of the same channels.
+      float amax = 0.0f;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        for (int k = 1; k < per; ++k) {
+          const float y = __shfl_sync(0xffffffffu, lo[i], col + k * lanes), z = __shfl_sync(0xffffffffu, hi[i], col + k * lanes);
+          if (g == 0) lo[i] = min_nan(lo[i], y), hi[i] = max_nan(hi[i], z);
+        }
+        if (g == 0) amax = max_nan(amax, max_nan(fabsf(lo[i]), fabsf(hi[i])));  // |NaN| is NaN
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      const bool fine = amax <= FLT_MAX;
+      const float top = fmaxf(amax, kAmaxMin), up = __fdiv_rn(kCodeMax, top);
+      if (g == 0) {
+        signed char c[2][N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          c[0][i] = bound_code(floorf(__fmul_rn(lo[i], up)), fine);
+          c[1][i] = bound_code(ceilf(__fmul_rn(hi[i], up)), fine);
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          int8_t* to = a.codes + at + (long long)j * a.D + col * N;
+#pragma unroll
+          for (int i = 0; i < N; i += 2)
+            *reinterpret_cast<uint16_t*>(to + i) =
+                (uint16_t)((unsigned char)c[j][i] | (unsigned)(unsigned char)c[j][i + 1] << 8);
+        }
+      }
+      if (lane == 0) a.scale[(long long)id * a.Hkv + hk] = fine ? __fdiv_rn(top, kCodeMax) : INFINITY;
+    } else {
+      // Twice over the channels: the largest magnitude first.
+      float amax = 0.0f;
+#pragma unroll 1
+      for (int turn = 0; turn < 2; ++turn) {
+        const bool fine = amax <= FLT_MAX;
+        const float top = fmaxf(amax, kAmaxMin), up = __fdiv_rn(kCodeMax, top);
+#pragma unroll 1
+        for (int d = lane; d < a.D; d += 32) {
+          float lo = INFINITY, hi = -INFINITY;
 #pragma unroll 4
-      for (int k = 1; k < groups; ++k) {
-        lo = min_nan(lo, part[2 * k * a.D + d]);
-        hi = max_nan(hi, part[(2 * k + 1) * a.D + d]);
+          for (int r = 0; r < count; ++r) {
+            const long long e = (row0 + r) * a.D + d;
+            float y;
+            if constexpr (F8) {
+              const __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<const unsigned char*>(a.kc)[e], __NV_E4M3);
+              y = __fmul_rn(__half2float(*reinterpret_cast<const __half*>(&h)), a.ks[row0 + r]);
+            } else {
+              y = __bfloat162float(static_cast<const __nv_bfloat16*>(a.kc)[e]);
+            }
+            lo = min_nan(lo, y);
+            hi = max_nan(hi, y);
+          }
+          if (turn == 0) {
+            amax = max_nan(amax, max_nan(fabsf(lo), fabsf(hi)));
+          } else {
+            a.codes[at + d] = bound_code(floorf(__fmul_rn(lo, up)), fine);
+            a.codes[at + a.D + d] = bound_code(ceilf(__fmul_rn(hi, up)), fine);
+          }
+        }
+        if (turn == 0) {
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        } else if (lane == 0) {
+          a.scale[(long long)id * a.Hkv + hk] = fine ? __fdiv_rn(top, kCodeMax) : INFINITY;
+        }
       }
-      part[d] = lo;
-      part[a.D + d] = hi;
-      amax = max_nan(amax, max_nan(fabsf(lo), fabsf(hi)));  // |NaN| is NaN
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    if ((tid & 31) == 0) red[tid >> 5] = amax;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kBoundThreads / 32; ++i) amax = max_nan(amax, red[i]);
-    const bool fine = amax <= FLT_MAX;
-    const float top = fmaxf(amax, kAmaxMin), up = __fdiv_rn(kCodeMax, top);
-    const long long at = ((long long)id * a.Hkv + hk) * 2 * a.D;
-    for (int d = tid; d < a.D; d += kBoundThreads) {
-      const float lo = floorf(__fmul_rn(part[d], up)), hi = ceilf(__fmul_rn(part[a.D + d], up));
-      a.codes[at + d] = fine ? (int8_t)(int)fminf(fmaxf(lo, -kCodeMax), kCodeMax) : (int8_t)0;
-      a.codes[at + a.D + d] = fine ? (int8_t)(int)fminf(fmaxf(hi, -kCodeMax), kCodeMax) : (int8_t)0;
-    }
-    if (tid == 0) a.scale[(long long)id * a.Hkv + hk] = fine ? __fdiv_rn(top, kCodeMax) : INFINITY;
-    __syncthreads();
   }
 }
 
@@ -656,24 +703,28 @@ int sv_page_bounds(const void* k_cache, const float* k_scale, int64_t num_pages,
   a.codes = codes;
   a.scale = scale;
   a.status = status;
-  // Blocks for eight a SM: the pages of a (sequence, head) are shared among them.
+  // Warps for 48 a SM: the pages of a (sequence, head) are shared among them.
   const long long items = (long long)B * Hkv;
-  a.chunks = (int)std::max(1ll, std::min((long long)max_pages, 1216 / items));
+  a.chunks = (int)std::max(1ll, std::min((long long)max_pages, 7296 / items));
   const bool f8 = cache_dtype == SV_E4M3;
-  const int per = f8 ? 16 : 8;
-  const bool vec = D % per == 0 && !misaligned(k_cache, 16);
-  const int groups = vec ? kBoundThreads / (D / per) : 1;
-  const size_t smem = (size_t)groups * 2 * D * 4;
-  const unsigned grid = (unsigned)(items * a.chunks);
+  // The bytes of a lane: 32 lanes hold a row, whose pieces are aligned and even in number of codes.
+  const int row = f8 ? D : 2 * D;
+  int bytes = 0;
+  for (int w = 16; w >= 4; w /= 2)
+    if (row % w == 0 && row / w <= 32 && !misaligned(k_cache, w) && !misaligned(codes, 2) && D % 2 == 0) bytes = w;
+  const unsigned grid = (unsigned)((items * a.chunks + kBoundThreads / 32 - 1) / (kBoundThreads / 32));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (f8 && vec)
-    page_bounds_kernel<true, true><<<grid, kBoundThreads, smem, st>>>(a);
-  else if (f8)
-    page_bounds_kernel<true, false><<<grid, kBoundThreads, smem, st>>>(a);
-  else if (vec)
-    page_bounds_kernel<false, true><<<grid, kBoundThreads, smem, st>>>(a);
-  else
-    page_bounds_kernel<false, false><<<grid, kBoundThreads, smem, st>>>(a);
+  if (f8) {
+    if (bytes == 4) page_bounds_kernel<true, 4><<<grid, kBoundThreads, 0, st>>>(a);
+    else if (bytes == 8) page_bounds_kernel<true, 8><<<grid, kBoundThreads, 0, st>>>(a);
+    else if (bytes == 16) page_bounds_kernel<true, 16><<<grid, kBoundThreads, 0, st>>>(a);
+    else page_bounds_kernel<true, 0><<<grid, kBoundThreads, 0, st>>>(a);
+  } else {
+    if (bytes == 4) page_bounds_kernel<false, 4><<<grid, kBoundThreads, 0, st>>>(a);
+    else if (bytes == 8) page_bounds_kernel<false, 8><<<grid, kBoundThreads, 0, st>>>(a);
+    else if (bytes == 16) page_bounds_kernel<false, 16><<<grid, kBoundThreads, 0, st>>>(a);
+    else page_bounds_kernel<false, 0><<<grid, kBoundThreads, 0, st>>>(a);
+  }
   return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 
