@@ -262,12 +262,16 @@ __global__ void __launch_bounds__(kBoundThreads) page_bounds_kernel(const __grid
 // the sign of q: the lanes that hold a page's minima use the negative codes, those that
 // hold its maxima the positive ones, and a page is one dot product of 2 D values. The scores go
 // as ordered 32-bit keys to the first CTA, which finds the budget-th largest by
-// halving the range of keys, bit by bit, and writes the chosen pages in their order.
+// histograms over the keys' range (its least and largest key are known by then), finer until
+// the bin's keys are few enough to be ranked one by one, and writes the chosen pages in their order.
 
 constexpr int kSelThreads = 256;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelPagesMax = 49152;  // keys of a row in shared memory
+constexpr int kSelSmemMax = 212 * 1024;
 constexpr unsigned kForced = 0xffffffffu;
+constexpr int kKeyBins = 2048;
+constexpr int kSelClusterMax = 16;
 
 struct SelArgs {
   const __nv_bfloat16* q;
@@ -290,6 +294,12 @@ SV_DEVINL unsigned ordered(float f) {
 SV_DEVINL void dsmem_st_u32(unsigned a, unsigned v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
 }
+
+SV_DEVINL void dsmem_min_u32(unsigned a, unsigned v) {
+  asm volatile("red.shared::cluster.min.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+SV_DEVINL void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+SV_DEVINL void cluster_wait_acquire() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 SV_DEVINL void store_key(unsigned keys0, int p, unsigned key, bool cluster) {
   if (cluster)
@@ -334,18 +344,24 @@ SV_DEVINL float page_score(int (&v)[HC], float qs, int li) {
 
 // LP lanes hold the 2 D codes of a page, 16 each (LP = 0: any D, a warp a page); HC heads at a time.
 template <int LP, int HC>
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_constant__ SelArgs a) {
+__global__ void __launch_bounds__(kSelThreads, HC == 4 ? 4 : 3) select_kernel(const __grid_constant__ SelArgs a) {
   extern __shared__ __align__(16) unsigned char dyn[];
   unsigned* keys = reinterpret_cast<unsigned*>(dyn);               // [max_pages] (first CTA)
   int* ids = reinterpret_cast<int*>(dyn + (size_t)a.max_pages * 4);  // [ids_cap] this CTA's pages
   signed char* qcode = reinterpret_cast<signed char*>(ids + a.ids_cap);  // [HC][Dp]
   __shared__ float qscale[8];
-  __shared__ unsigned faults[16];
+  __shared__ unsigned faults[kSelClusterMax], key_range[2];  // least key, and the largest's complement
   __shared__ int wsum[kSelWarps], wsum2[kSelWarps];
+  __shared__ __align__(16) unsigned hist[kKeyBins];
+  __shared__ unsigned bin_keys[kSelThreads];
+  __shared__ int at_bin[3];  // bin, what is wanted of it, its keys
+  __shared__ unsigned n_bin, the_cut;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const unsigned rank = a.nc > 1 ? cluster_ctarank() : 0;
-  if (a.nc > 1) cluster_arrive_relaxed();
+  if (tid < 2) key_range[tid] = 0xffffffffu;
+  if (tid == 0) n_bin = 0;
+  if (a.nc > 1) cluster_arrive();
   const long long item = blockIdx.x / a.nc;
   const int h = (int)(item % a.Hkv);
   const long long n = item / a.Hkv;
@@ -370,16 +386,9 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
     bad |= out;
     ids[i] = out ? 0 : id;
   }
-  bad = __syncthreads_or(bad);
   const bool rank_pages = np > a.budget;  // else all are chosen
-  if (a.nc > 1) cluster_wait();
   const unsigned keys0 = a.nc > 1 ? dsmem_map(smem_u32(keys), 0) : smem_u32(keys);
-  if (tid == 0) {
-    if (a.nc > 1)
-      dsmem_st_u32(dsmem_map(smem_u32(&faults[rank]), 0), bad);
-    else
-      faults[0] = bad;
-  }
+  unsigned least = 0xffffffffu, most = 0;  // of this thread's keys, but for the forced pages'
 
   // The key of page p, this CTA's page i. With more than HC heads the largest so far stays here
   // (rank 0: in its place; there i is p) and goes to the first CTA after the last heads.
@@ -387,10 +396,19 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
     const float s = isinf(ps) ? INFINITY : __fmul_rn(best, ps);
     unsigned key = p < a.sink || p >= np - a.recent ? kForced : ordered(s);
     if (h0 > 0) key = max(key, keys[i]);
-    if (h0 + HC < G)
+    if (h0 + HC < G) {
       keys[i] = key;
-    else
-      store_key(keys0, p, key, a.nc > 1);
+      return;
+    }
+    store_key(keys0, p, key, a.nc > 1);
+    if (key != kForced) {
+      least = min(least, key);
+      most = max(most, key);
+    }
+  };
+  auto joined = [&] {  // this CTA's pages are known, and the first CTA is there
+    bad = __syncthreads_or(bad);
+    if (a.nc > 1) cluster_wait_acquire();
   };
 
   if (rank_pages) {
@@ -420,7 +438,10 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
         }
         if (lane == 0) qscale[j] = fin ? __fdiv_rn(top, kCodeMax) : 0.0f;
       }
-      __syncthreads();
+      if (h0 == 0)
+        joined();
+      else
+        __syncthreads();
       if constexpr (LP > 0) {
         constexpr int PPW = 32 / LP, U = 4;
         const int li = lane % LP, sub = lane / LP, half = a.D / 16;
@@ -497,6 +518,22 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
       }
     }
   }
+  if (rank_pages) {
+    least = __reduce_min_sync(0xffffffffu, least);
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0) {
+      dsmem_min_u32(a.nc > 1 ? dsmem_map(smem_u32(&key_range[0]), 0) : smem_u32(&key_range[0]), least);
+      dsmem_min_u32(a.nc > 1 ? dsmem_map(smem_u32(&key_range[1]), 0) : smem_u32(&key_range[1]), ~most);
+    }
+  } else {
+    joined();
+  }
+  if (tid == 0) {
+    if (a.nc > 1)
+      dsmem_st_u32(dsmem_map(smem_u32(&faults[rank]), 0), bad);
+    else
+      faults[0] = bad;
+  }
   if (a.nc > 1) cluster_sync();
   if (rank != 0) return;
   __syncthreads();
@@ -523,23 +560,75 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
     }
     return;
   }
-  // The largest key that at least K keys reach.
-  unsigned cut = 0;
-  int at_least = np;
+  // The K-th largest key.
+  unsigned cut = kForced, from = key_range[0], range = ~key_range[1] - from;
+  int need = K - a.sink - a.recent;  // of the keys from `from` to from + range; the forced ones are above
 #pragma unroll 1
-  for (int bit = 31; bit >= 0 && at_least != K; --bit) {
-    const unsigned tried = cut | (1u << bit);
-    int c = 0;
-    for (int i = tid; i < np; i += kSelThreads) c += keys[i] >= tried;
-    c = __reduce_add_sync(0xffffffffu, c);
-    if (lane == 0) (bit & 1 ? wsum : wsum2)[warp] = c;
+  while (need > 0) {
+    const int shift = max(0, 21 - __clz(range));  // fewer than 2048 bins
+    for (int i = tid; i < kKeyBins; i += kSelThreads) hist[i] = 0;
     __syncthreads();
-    c = 0;
+    for (int i = tid; i < np; i += kSelThreads) {
+      const unsigned k = keys[i];
+      if (k != kForced && k - from <= range) atomicAdd(&hist[(k - from) >> shift], 1u);
+    }
+    __syncthreads();
+    // Eight bins a thread, the largest keys first.
+    const int b0 = kKeyBins - 8 - 8 * tid;
+    const uint4 x = *reinterpret_cast<const uint4*>(&hist[b0]), y = *reinterpret_cast<const uint4*>(&hist[b0 + 4]);
+    const unsigned c[8] = {y.w, y.z, y.y, y.x, x.w, x.z, x.y, x.x};
+    int sum = 0;
 #pragma unroll
-    for (int i = 0; i < kSelWarps; ++i) c += (bit & 1 ? wsum : wsum2)[i];
-    if (c >= K) {
-      cut = tried;
-      at_least = c;
+    for (int i = 0; i < 8; ++i) sum += (int)c[i];
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int z = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += z;
+    }
+    if (lane == 31) wsum[warp] = incl;
+    __syncthreads();
+    for (int i = 0; i < warp; ++i) incl += wsum[i];
+    int above = incl - sum;
+    if (above < need && incl >= need) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (above < need && above + (int)c[i] >= need) {
+          at_bin[0] = b0 + 7 - i;
+          at_bin[1] = need - above;
+          at_bin[2] = (int)c[i];
+        }
+        above += (int)c[i];
+      }
+    }
+    __syncthreads();
+    const unsigned bin = (unsigned)at_bin[0];
+    need = at_bin[1];
+    const int few = at_bin[2];
+    if (shift == 0) {
+      cut = from + bin;
+      break;
+    }
+    from += bin << shift;
+    range = (1u << shift) - 1u;
+    if (few <= kSelThreads) {
+      for (int i = tid; i < np; i += kSelThreads) {
+        const unsigned k = keys[i];
+        if (k != kForced && k - from <= range) bin_keys[atomicAdd(&n_bin, 1u)] = k;
+      }
+      __syncthreads();
+      if (tid < few) {
+        const unsigned k = bin_keys[tid];
+        int gt = 0, ge = 0;
+        for (int i = 0; i < few; ++i) {
+          gt += bin_keys[i] > k;
+          ge += bin_keys[i] >= k;
+        }
+        if (gt < need && ge >= need) the_cut = k;
+      }
+      __syncthreads();
+      cut = the_cut;
+      break;
     }
   }
   // Keys above the cut, and the first of those equal to it. A warp takes a run of pages.
@@ -621,8 +710,9 @@ int launch_select(const SelArgs& a, size_t smem, cudaStream_t st) {
   {
     std::lock_guard<std::mutex> lock(mu);
     if (!set[device]) {
-      if (cudaFuncSetAttribute(select_kernel<LP, HC>, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024) !=
-          cudaSuccess)
+      if (cudaFuncSetAttribute(select_kernel<LP, HC>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelSmemMax) !=
+              cudaSuccess ||
+          cudaFuncSetAttribute(select_kernel<LP, HC>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
         return SV_ERR_CUDA;
       set[device] = true;
     }
@@ -642,14 +732,18 @@ int launch_select(const SelArgs& a, size_t smem, cudaStream_t st) {
 }
 
 int launch_select_any(SelArgs& a, cudaStream_t st) {
-  // CTAs of an item: as many as keep all SMs busy with few items, and no fewer than 128 pages each.
+  // CTAs of an item: as many as one wave holds with few items, and no fewer than 64 pages each.
   const long long items = (long long)a.N * a.Hkv;
   a.nc = 1;
-  while (a.nc < 8 && items * a.nc * 2 <= 1216 && a.max_pages >= 256 * a.nc) a.nc *= 2;
-  a.ids_cap = ((a.max_pages + a.nc - 1) / a.nc + 3) & ~3;
+  while (a.nc < kSelClusterMax && items * a.nc * 2 <= 608 && a.max_pages >= 128 * a.nc) a.nc *= 2;
   const int G = a.Hq / a.Hkv, hc = G <= 4 ? 4 : 8;
-  const size_t smem = (size_t)((a.max_pages + 3) & ~3) * 4 + (size_t)a.ids_cap * 4 + (size_t)hc * ((a.D + 15) & ~15);
-  if (smem > 220 * 1024) return SV_ERR_SHAPE;
+  size_t smem;
+  for (;; a.nc *= 2) {  // (tables so long that a CTA cannot hold an item's keys and pages are shared in any case)
+    a.ids_cap = ((a.max_pages + a.nc - 1) / a.nc + 3) & ~3;
+    smem = (size_t)((a.max_pages + 3) & ~3) * 4 + (size_t)a.ids_cap * 4 + (size_t)hc * ((a.D + 15) & ~15);
+    if (smem <= kSelSmemMax) break;
+    if (a.nc == kSelClusterMax) return SV_ERR_SHAPE;
+  }
   const int lp = a.D % 16 || a.D > 256 || misaligned(a.codes, 16) ? 0 : a.D <= 64 ? 8 : a.D <= 128 ? 16 : 32;
   if (hc == 4) {
     switch (lp) {
