@@ -18,7 +18,7 @@ LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libspecverify.so")
 SOURCES = ["sv_kernels.cu", "sv_api.cu", "sv_static_scratch.cu", "sv_lmhead.cu",
            "sv_tree_io.cu", "sv_tree_attn.cu", "sv_tree_verify.cu", "sv_page_plan.cu", "sv_sparse_attn.cu",
-           "sv_filtered_sample.cu"]
+           "sv_sparse_decode.cu", "sv_filtered_sample.cu"]
 # Translation units: (source, extra nvcc flags, object). sv_kernels.cu is
 # compiled three times, each unit holding one group of its kernels (SV_TU).
 UNITS = [("sv_kernels.cu", ["-DSV_TU=1"], "sv_kernels_verify.o"),
@@ -32,8 +32,9 @@ UNITS = [("sv_kernels.cu", ["-DSV_TU=1"], "sv_kernels_verify.o"),
          ("sv_tree_verify.cu", [], "sv_tree_verify.o"),
          ("sv_page_plan.cu", [], "sv_page_plan.o"),
          ("sv_sparse_attn.cu", [], "sv_sparse_attn.o"),
+         ("sv_sparse_decode.cu", [], "sv_sparse_decode.o"),
          ("sv_filtered_sample.cu", [], "sv_filtered_sample.o")]
-HEADERS = ["sv_device.cuh", "sv_internal.h", "sv_exp_table.h", "sv_tree_attn.h"]
+HEADERS = ["sv_device.cuh", "sv_internal.h", "sv_exp_table.h", "sv_tree_attn.h", "sv_sparse.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2", "-diag-suppress=177",
          "--expt-relaxed-constexpr"]

@@ -1,0 +1,48 @@
+// The sparse attention's kernel for few query heads a key/value head (sv_sparse_decode.cu).
+#pragma once
+
+#include <algorithm>
+#include <cstdint>
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+namespace sv {
+namespace sparse {
+namespace dec {
+
+struct Args {
+  const __nv_bfloat16* q;
+  long long q_sn, q_sh;
+  const void *kc, *vc;
+  const float *ks, *vs;
+  const int32_t *table, *ctx, *parent;  // of an item (row, key/value head): its pages; of a row: its last key, -1 at
+                                        // fault; -2 for an empty row
+  __nv_bfloat16* out;
+  unsigned *status, *counters;
+  float2* part_ml;  // [items splits][heads]: maximum and sum of a part
+  float* part_o;    // [items splits][heads][D]
+  long long num_pages;
+  int N, Hq, Hkv, D, P, budget, splits;
+  float scale;
+};
+
+// Shapes that the kernel takes: heads of a key/value head are the N of an 8-wide product, and a
+// block of 16 keys lies in one page.
+inline bool takes(int heads, int D, int page_size) {
+  return heads <= 8 && (D == 64 || D == 128) && page_size % 16 == 0;
+}
+
+// CTAs of an item: two waves in all, but no fewer than 128 keys a CTA.
+inline int splits_of(long long items, int budget, int page_size) {
+  const long long keys = (long long)budget * page_size;
+  const long long want = (912 + items - 1) / (items > 0 ? items : 1);
+  return (int)std::max(1ll, std::min({want, keys / 128, 64ll}));
+}
+
+// Enqueues the attention behind the selection, whose kernel clears the counters and the status word.
+int launch(const Args& a, int cache_dtype, cudaStream_t st);
+
+}  // namespace dec
+}  // namespace sparse
+}  // namespace sv

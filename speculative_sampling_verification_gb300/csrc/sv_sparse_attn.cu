@@ -15,6 +15,7 @@
 #include "../../include/spec_verify.h"
 #include "sv_device.cuh"
 #include "sv_internal.h"
+#include "sv_sparse.h"
 #include "sv_tree_attn.h"
 
 namespace sv {
@@ -265,13 +266,11 @@ __global__ void __launch_bounds__(kBoundThreads) page_bounds_kernel(const __grid
 // histograms over the keys' range (its least and largest key are known by then), finer until
 // the bin's keys are few enough to be ranked one by one, and writes the chosen pages in their order.
 
-constexpr int kSelThreads = 256;
-constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelPagesMax = 49152;  // keys of a row in shared memory
 constexpr int kSelSmemMax = 212 * 1024;
 constexpr unsigned kForced = 0xffffffffu;
 constexpr int kKeyBins = 2048;
-constexpr int kSelClusterMax = 16;
+constexpr int kSelClusterMax = 16;  // (8 unless the table is too long for it: clusters of 16 do not all fit at once)
 
 struct SelArgs {
   const __nv_bfloat16* q;
@@ -280,8 +279,8 @@ struct SelArgs {
   const float* scale;
   const int32_t *page_table, *positions, *seqs;
   int32_t *selected, *table, *ctx, *parent;
-  unsigned* clear;
-  int clear_words;
+  unsigned *clear, *clear2;  // words that the attention wants at 0
+  int clear_words, clear2_words;
   long long num_pages;
   int N, B, Hq, Hkv, D, P, max_pages, budget, sink, recent, nc, ids_cap;
 };
@@ -308,52 +307,37 @@ SV_DEVINL void store_key(unsigned keys0, int p, unsigned key, bool cluster) {
     asm volatile("st.shared::cta.u32 [%0], %1;" ::"r"(keys0 + p * 4), "r"(key) : "memory");
 }
 
-// The head whose sum page_score leaves in lane li of a page's LP lanes.
-template <int LP, int HC>
-SV_DEVINL int lane_head(int li) {
-  int head = 0, step = LP / 2;
-#pragma unroll
-  for (int n = HC; n > 1; n >>= 1, step >>= 1)
-    if (li & step) head += n / 2;
-  return head;
-}
-
-// Sum over the LP lanes of a page of HC heads' products, times the heads' scales (`qs`: that
-// of lane_head), and the largest over the heads, the same in all LP lanes. The first steps hand half
-// of the heads over, so that a value takes about one exchange.
-template <int LP, int HC>
-SV_DEVINL float page_score(int (&v)[HC], float qs, int li) {
+// Sums over the LP lanes of a page of 16 values a lane (16/HC pages of HC heads, in that order): each
+// step hands half of the values over to the lane that keeps them, so that a value takes about one exchange. Lane li
+// ends up with value li (LP = 16), values 2 li and 2 li + 1 (LP = 8), or value li / 2 (LP = 32).
+template <int LP>
+SV_DEVINL void sum_lanes(int (&v)[16], int li) {
   int step = LP / 2;
 #pragma unroll
-  for (int n = HC; n > 1; n >>= 1, step >>= 1) {
+  for (int n = 16; n > (LP == 8 ? 2 : 1); n >>= 1, step >>= 1) {
     const bool up = li & step;
 #pragma unroll
     for (int i = 0; i < n / 2; ++i) {
-      const int give = up ? v[i] : v[i + n / 2];
-      const int keep = up ? v[i + n / 2] : v[i];
+      const int give = up ? v[i] : v[i + n / 2], keep = up ? v[i + n / 2] : v[i];
       v[i] = keep + __shfl_xor_sync(0xffffffffu, give, step);
     }
   }
-#pragma unroll
-  for (int o = LP / 2 / HC; o > 0; o >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
-  float s = __fmul_rn((float)v[0], qs);
-#pragma unroll
-  for (int o = LP / 2; o >= LP / HC; o >>= 1) s = fmaxf(s, __shfl_xor_sync(0xffffffffu, s, o));
-  return s;
+  if (LP == 32) v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
 }
 
 // LP lanes hold the 2 D codes of a page, 16 each (LP = 0: any D, a warp a page); HC heads at a time.
-template <int LP, int HC>
-__global__ void __launch_bounds__(kSelThreads, HC == 4 ? 4 : 3) select_kernel(const __grid_constant__ SelArgs a) {
+template <int LP, int HC, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : HC == 4 ? 4 : 3) select_kernel(const __grid_constant__ SelArgs a) {
+  constexpr int WARPS = THREADS / 32;
   extern __shared__ __align__(16) unsigned char dyn[];
   unsigned* keys = reinterpret_cast<unsigned*>(dyn);               // [max_pages] (first CTA)
   int* ids = reinterpret_cast<int*>(dyn + (size_t)a.max_pages * 4);  // [ids_cap] this CTA's pages
   signed char* qcode = reinterpret_cast<signed char*>(ids + a.ids_cap);  // [HC][Dp]
   __shared__ float qscale[8];
   __shared__ unsigned faults[kSelClusterMax], key_range[2];  // least key, and the largest's complement
-  __shared__ int wsum[kSelWarps], wsum2[kSelWarps];
+  __shared__ int wsum[WARPS], wsum2[WARPS];
   __shared__ __align__(16) unsigned hist[kKeyBins];
-  __shared__ unsigned bin_keys[kSelThreads];
+  __shared__ unsigned bin_keys[THREADS];
   __shared__ int at_bin[3];  // bin, what is wanted of it, its keys
   __shared__ unsigned n_bin, the_cut;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -366,8 +350,10 @@ __global__ void __launch_bounds__(kSelThreads, HC == 4 ? 4 : 3) select_kernel(co
   const int h = (int)(item % a.Hkv);
   const long long n = item / a.Hkv;
   const int G = a.Hq / a.Hkv;
-  if (blockIdx.x == 0)
-    for (int i = tid; i < a.clear_words; i += kSelThreads) a.clear[i] = 0;
+  if (blockIdx.x == 0) {
+    for (int i = tid; i < a.clear_words; i += THREADS) a.clear[i] = 0;
+    for (int i = tid; i < a.clear2_words; i += THREADS) a.clear2[i] = 0;
+  }
 
   const int pos = a.positions[n], seq = a.seqs ? a.seqs[n] : (int)n;
   const bool empty = pos == -1 || seq == -1;
@@ -380,7 +366,7 @@ __global__ void __launch_bounds__(kSelThreads, HC == 4 ? 4 : 3) select_kernel(co
   const int share = (np + a.nc - 1) / a.nc;
   const int first = min(np, (int)rank * share), mine = min(np, first + share) - first;
   bool bad = false;
-  for (int i = tid; i < mine; i += kSelThreads) {
+  for (int i = tid; i < mine; i += THREADS) {
     const int id = table[first + i];
     const bool out = id < 0 || id >= a.num_pages;
     bad |= out;
@@ -417,7 +403,7 @@ __global__ void __launch_bounds__(kSelThreads, HC == 4 ? 4 : 3) select_kernel(co
     for (int h0 = 0; h0 < G; h0 += HC) {
       if (h0) __syncthreads();
       // A warp a head: its largest magnitude, then its codes.
-      for (int j = warp; j < HC; j += kSelWarps) {
+      for (int j = warp; j < HC; j += WARPS) {
         float top = 0.0f;
         bool fin = true;
         const __nv_bfloat16* qr = a.q + n * a.q_sn + (long long)(h * G + h0 + j) * a.q_sh;
@@ -443,7 +429,7 @@ __global__ void __launch_bounds__(kSelThreads, HC == 4 ? 4 : 3) select_kernel(co
       else
         __syncthreads();
       if constexpr (LP > 0) {
-        constexpr int PPW = 32 / LP, U = 4;
+        constexpr int PPW = 32 / LP, U = 16 / HC;  // pages of a load; loads of a turn
         const int li = lane % LP, sub = lane / LP, half = a.D / 16;
         const bool used = li < 2 * half, upper = li >= half;
         const int off = (upper ? li - half : li) * 16;
@@ -456,49 +442,43 @@ __global__ void __launch_bounds__(kSelThreads, HC == 4 ? 4 : 3) select_kernel(co
             const unsigned neg = __vcmpgtu4(w & 0x80808080u, 0u);  // bytes below zero
             qv[j][k] = (int)(upper ? w & ~neg : w & neg);
           }
-        const float my_qs = qscale[lane_head<LP, HC>(li)];
+        // The value that sum_lanes leaves in this lane: page my_u of the turn, head my_j (LP = 8: and the next).
+        const int value = LP == 8 ? 2 * li : LP == 16 ? li : li / 2, my_u = value / HC, my_j = value % HC;
+        const bool there = h0 + my_j < G, there1 = h0 + my_j + 1 < G;
+        const float qs0 = qscale[my_j], qs1 = LP == 8 ? qscale[my_j + 1] : 0.0f;
+        const int stride = a.Hkv * 2 * a.D;
+        const int8_t* base = a.codes + (long long)h * 2 * a.D + li * 16;
 #pragma unroll 1
-        for (int i0 = warp * PPW * U; i0 < mine; i0 += kSelWarps * PPW * U) {
+        for (int i0 = warp * PPW * U; i0 < mine; i0 += WARPS * PPW * U) {
           uint4 c[U];
-          float ps[U];
 #pragma unroll
           for (int u = 0; u < U; ++u) {
-            const int i = min(i0 + u * PPW + sub, mine - 1);
-            const long long at = (long long)ids[i] * a.Hkv + h;
-            c[u] = used ? __ldg(reinterpret_cast<const uint4*>(a.codes + at * 2 * a.D) + li) : make_uint4(0, 0, 0, 0);
-            ps[u] = __ldg(a.scale + at);
+            const int id = ids[min(i0 + u * PPW + sub, mine - 1)];
+            c[u] = used ? __ldg(reinterpret_cast<const uint4*>(base + (long long)id * stride)) : make_uint4(0, 0, 0, 0);
           }
+          const int i = i0 + my_u * PPW + sub;
+          const float ps = __ldg(a.scale + (long long)ids[min(i, mine - 1)] * a.Hkv + h);
+          int v[16];
 #pragma unroll
-          for (int u = 0; u < U; ++u) {
-            int v[HC];
+          for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int j = 0; j < HC; ++j) {
               int s = __dp4a((int)c[u].x, qv[j][0], 0);
               s = __dp4a((int)c[u].y, qv[j][1], s);
               s = __dp4a((int)c[u].z, qv[j][2], s);
-              v[j] = __dp4a((int)c[u].w, qv[j][3], s);
+              v[u * HC + j] = __dp4a((int)c[u].w, qv[j][3], s);
             }
-            float best;
-            if (h0 + HC <= G) {
-              best = page_score<LP, HC>(v, my_qs, li);
-            } else {
-              best = -INFINITY;
+          sum_lanes<LP>(v, li);
+          float best = there ? __fmul_rn((float)v[0], qs0) : -INFINITY;
+          if (LP == 8) best = fmaxf(best, there1 ? __fmul_rn((float)v[1], qs1) : -INFINITY);
+          // The other heads' lanes.
 #pragma unroll
-              for (int j = 0; j < HC; ++j) {
-                int s = v[j];
-#pragma unroll
-                for (int o = LP / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-                if (h0 + j < G) best = fmaxf(best, __fmul_rn((float)s, qscale[j]));
-              }
-            }
-            const int i = i0 + u * PPW + sub, p = first + i;
-            if (li == 0 && i < mine) {
-              put_key(h0, i, p, best, ps[u]);
-            }
-          }
+          for (int o = LP == 32 ? 2 : 1; o < (LP == 8 ? HC / 2 : LP == 16 ? HC : 2 * HC); o <<= 1)
+            best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
+          if (my_j == 0 && (LP != 32 || !(li & 1)) && i < mine) put_key(h0, i, first + i, best, ps);
         }
       } else {
-        for (int i = warp; i < mine; i += kSelWarps) {
+        for (int i = warp; i < mine; i += WARPS) {
           const int p = first + i;
           const long long at = (long long)ids[i] * a.Hkv + h;
           float best = -INFINITY;
@@ -548,13 +528,13 @@ __global__ void __launch_bounds__(kSelThreads, HC == 4 ? 4 : 3) select_kernel(co
     a.ctx[n] = fault ? -1 : empty ? 0 : (K - 1) * a.P + pos % a.P;
     a.parent[n] = empty ? -2 : -1;
   }
-  for (int i = take + tid; i < a.budget; i += kSelThreads) {
+  for (int i = take + tid; i < a.budget; i += THREADS) {
     if (sel) sel[i] = -1;
     out[i] = -1;
   }
   if (take == 0) return;
   if (!rank_pages) {
-    for (int i = tid; i < take; i += kSelThreads) {
+    for (int i = tid; i < take; i += THREADS) {
       if (sel) sel[i] = i;
       out[i] = table[i];
     }
@@ -566,20 +546,23 @@ __global__ void __launch_bounds__(kSelThreads, HC == 4 ? 4 : 3) select_kernel(co
 #pragma unroll 1
   while (need > 0) {
     const int shift = max(0, 21 - __clz(range));  // fewer than 2048 bins
-    for (int i = tid; i < kKeyBins; i += kSelThreads) hist[i] = 0;
+    for (int i = tid; i < kKeyBins; i += THREADS) hist[i] = 0;
     __syncthreads();
-    for (int i = tid; i < np; i += kSelThreads) {
+    for (int i = tid; i < np; i += THREADS) {
       const unsigned k = keys[i];
       if (k != kForced && k - from <= range) atomicAdd(&hist[(k - from) >> shift], 1u);
     }
     __syncthreads();
-    // Eight bins a thread, the largest keys first.
-    const int b0 = kKeyBins - 8 - 8 * tid;
-    const uint4 x = *reinterpret_cast<const uint4*>(&hist[b0]), y = *reinterpret_cast<const uint4*>(&hist[b0 + 4]);
-    const unsigned c[8] = {y.w, y.z, y.y, y.x, x.w, x.z, x.y, x.x};
+    // A few bins a thread, the largest keys first.
+    constexpr int BINS = kKeyBins / THREADS;
+    const int b0 = kKeyBins - BINS - BINS * tid;
+    unsigned c[BINS];
     int sum = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sum += (int)c[i];
+    for (int i = 0; i < BINS; ++i) {
+      c[i] = hist[b0 + BINS - 1 - i];
+      sum += (int)c[i];
+    }
     int incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -592,9 +575,9 @@ __global__ void __launch_bounds__(kSelThreads, HC == 4 ? 4 : 3) select_kernel(co
     int above = incl - sum;
     if (above < need && incl >= need) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < BINS; ++i) {
         if (above < need && above + (int)c[i] >= need) {
-          at_bin[0] = b0 + 7 - i;
+          at_bin[0] = b0 + BINS - 1 - i;
           at_bin[1] = need - above;
           at_bin[2] = (int)c[i];
         }
@@ -611,8 +594,8 @@ __global__ void __launch_bounds__(kSelThreads, HC == 4 ? 4 : 3) select_kernel(co
     }
     from += bin << shift;
     range = (1u << shift) - 1u;
-    if (few <= kSelThreads) {
-      for (int i = tid; i < np; i += kSelThreads) {
+    if (few <= THREADS) {
+      for (int i = tid; i < np; i += THREADS) {
         const unsigned k = keys[i];
         if (k != kForced && k - from <= range) bin_keys[atomicAdd(&n_bin, 1u)] = k;
       }
@@ -632,7 +615,7 @@ __global__ void __launch_bounds__(kSelThreads, HC == 4 ? 4 : 3) select_kernel(co
     }
   }
   // Keys above the cut, and the first of those equal to it. A warp takes a run of pages.
-  const int run = (np + kSelWarps - 1) / kSelWarps;
+  const int run = (np + WARPS - 1) / WARPS;
   const int r0 = min(np, warp * run), r1 = min(np, r0 + run);
   int above = 0, equal = 0;
   for (int i = r0 + lane; i < r1; i += 32) {
@@ -649,7 +632,7 @@ __global__ void __launch_bounds__(kSelThreads, HC == 4 ? 4 : 3) select_kernel(co
   __syncthreads();
   int all_above = 0, above0 = 0, equal0 = 0;
 #pragma unroll
-  for (int i = 0; i < kSelWarps; ++i) {
+  for (int i = 0; i < WARPS; ++i) {
     if (i < warp) {
       above0 += wsum[i];
       equal0 += wsum2[i];
@@ -679,7 +662,8 @@ __global__ void __launch_bounds__(kSelThreads, HC == 4 ? 4 : 3) select_kernel(co
 bool misaligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
 
 struct Layout {
-  size_t off_table, off_ctx, off_parent, total;
+  size_t off_table, off_ctx, off_parent, off_counters, off_ml, off_o, total;
+  int splits;
 };
 
 bool sizes_ok(int N, int Hq, int Hkv, int D, int max_pages, int page_size, int budget) {
@@ -697,12 +681,23 @@ Layout make_layout(int N, int Hq, int Hkv, int D, int page_size, int budget) {
   off = align_up(off + (size_t)N * 4, 256);
   L.off_parent = off;
   off = align_up(off + (size_t)N * 4, 256);
+  // For the few-rows kernel: parts of an item that have arrived, and their results.
+  if (dec::takes(Hq / Hkv, D, page_size)) {
+    L.splits = dec::splits_of((long long)N * Hkv, budget, page_size);
+    const size_t parts = (size_t)N * Hkv * L.splits * (Hq / Hkv);
+    L.off_counters = off;
+    off = align_up(off + (size_t)N * Hkv * 4, 256);
+    L.off_ml = off;
+    off = align_up(off + parts * 8, 256);
+    L.off_o = off;
+    off = align_up(off + parts * D * 4, 256);
+  }
   L.total = off;
   return L;
 }
 
-template <int LP, int HC>
-int launch_select(const SelArgs& a, size_t smem, cudaStream_t st) {
+template <int LP, int HC, int THREADS>
+int launch_select_of(const SelArgs& a, size_t smem, cudaStream_t st) {
   static std::mutex mu;
   static bool set[64] = {};
   int device = 0;
@@ -710,16 +705,16 @@ int launch_select(const SelArgs& a, size_t smem, cudaStream_t st) {
   {
     std::lock_guard<std::mutex> lock(mu);
     if (!set[device]) {
-      if (cudaFuncSetAttribute(select_kernel<LP, HC>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelSmemMax) !=
+      if (cudaFuncSetAttribute(select_kernel<LP, HC, THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelSmemMax) !=
               cudaSuccess ||
-          cudaFuncSetAttribute(select_kernel<LP, HC>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+          cudaFuncSetAttribute(select_kernel<LP, HC, THREADS>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
         return SV_ERR_CUDA;
       set[device] = true;
     }
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((long long)a.N * a.Hkv * a.nc));
-  cfg.blockDim = dim3(kSelThreads);
+  cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -728,14 +723,22 @@ int launch_select(const SelArgs& a, size_t smem, cudaStream_t st) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, select_kernel<LP, HC>, a) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, select_kernel<LP, HC, THREADS>, a) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+}
+
+// Large CTAs where there are too few to fill the SMs with small ones.
+template <int LP, int HC>
+int launch_select(const SelArgs& a, size_t smem, cudaStream_t st) {
+  constexpr int kLarge = HC == 4 ? 1024 : 512;
+  if ((long long)a.N * a.Hkv * a.nc <= 152 && a.max_pages >= 256 * a.nc) return launch_select_of<LP, HC, kLarge>(a, smem, st);
+  return launch_select_of<LP, HC, 256>(a, smem, st);
 }
 
 int launch_select_any(SelArgs& a, cudaStream_t st) {
   // CTAs of an item: as many as one wave holds with few items, and no fewer than 64 pages each.
   const long long items = (long long)a.N * a.Hkv;
   a.nc = 1;
-  while (a.nc < kSelClusterMax && items * a.nc * 2 <= 608 && a.max_pages >= 128 * a.nc) a.nc *= 2;
+  while (a.nc < 8 && items * a.nc * 2 <= 608 && a.max_pages >= 128 * a.nc) a.nc *= 2;
   const int G = a.Hq / a.Hkv, hc = G <= 4 ? 4 : 8;
   size_t smem;
   for (;; a.nc *= 2) {  // (tables so long that a CTA cannot hold an item's keys and pages are shared in any case)
@@ -866,7 +869,11 @@ int sv_sparse_attention(const void* q, int64_t q_stride_n, int64_t q_stride_h, c
   s.ctx = reinterpret_cast<int32_t*>(ws + L.off_ctx);
   s.parent = reinterpret_cast<int32_t*>(ws + L.off_parent);
   s.clear = reinterpret_cast<unsigned*>(ws);
-  s.clear_words = (int)sv::tat::cleared_words(1, Hq, Hkv, D, page_size);
+  const bool few = L.splits > 0 && !misaligned(q, 16) && !misaligned(k_cache, 16) && !misaligned(v_cache, 16) &&
+                   q_stride_n % 8 == 0 && q_stride_h % 8 == 0;
+  s.clear_words = few ? 1 : (int)sv::tat::cleared_words(1, Hq, Hkv, D, page_size);
+  s.clear2 = reinterpret_cast<unsigned*>(ws + L.off_counters);
+  s.clear2_words = few ? N * Hkv : 0;
   s.num_pages = num_pages;
   s.N = N;
   s.B = B;
@@ -880,6 +887,34 @@ int sv_sparse_attention(const void* q, int64_t q_stride_n, int64_t q_stride_h, c
   s.recent = recent;
   const int rc = launch_select_any(s, st);
   if (rc != SV_OK) return rc;
+  if (few) {
+    sv::sparse::dec::Args d{};
+    d.q = s.q;
+    d.q_sn = q_stride_n;
+    d.q_sh = q_stride_h;
+    d.kc = k_cache;
+    d.vc = v_cache;
+    d.ks = k_scale;
+    d.vs = v_scale;
+    d.table = s.table;
+    d.ctx = s.ctx;
+    d.parent = s.parent;
+    d.out = static_cast<__nv_bfloat16*>(out);
+    d.status = static_cast<unsigned*>(workspace);
+    d.counters = s.clear2;
+    d.part_ml = reinterpret_cast<float2*>(ws + L.off_ml);
+    d.part_o = reinterpret_cast<float*>(ws + L.off_o);
+    d.num_pages = num_pages;
+    d.N = N;
+    d.Hq = Hq;
+    d.Hkv = Hkv;
+    d.D = D;
+    d.P = page_size;
+    d.budget = budget;
+    d.splits = L.splits;
+    d.scale = scale;
+    return sv::sparse::dec::launch(d, cache_dtype, st);
+  }
   sv::tat::Args a{};
   a.q = s.q;
   a.q_sb = q_stride_n;

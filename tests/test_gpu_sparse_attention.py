@@ -86,7 +86,8 @@ SHAPES = [  # N, Hq, H, D, P, W, budget, sink, recent
     (4, 10, 2, 96, 16, 33, 33, 2, 3), (2, 8, 1, 256, 128, 6, 3, 0, 2), (2, 16, 1, 128, 16, 300, 20, 1, 1),
     (1, 40, 1, 64, 16, 50, 9, 1, 1), (2, 6, 3, 100, 24, 9, 4, 1, 1), (1, 3, 1, 17, 5, 40, 7, 2, 2),
     (1, 4, 2, 16, 16, 600, 64, 1, 1), (1, 8, 8, 128, 16, 2100, 128, 1, 2), (2, 9, 1, 48, 16, 31, 1, 0, 1),
-    (1, 20, 4, 512, 16, 12, 4, 1, 1), (1, 64, 2, 128, 16, 64, 10, 1, 1)]
+    (1, 20, 4, 512, 16, 12, 4, 1, 1), (1, 64, 2, 128, 16, 64, 10, 1, 1), (5, 7, 7, 64, 48, 21, 6, 1, 1),
+    (1, 8, 1, 128, 16, 900, 700, 1, 1), (40, 10, 2, 64, 128, 9, 5, 1, 2), (3, 6, 2, 128, 32, 64, 40, 0, 1)]
 
 
 @pytest.mark.parametrize("N,Hq,H,D,P,W,budget,sink,recent", SHAPES)
@@ -103,15 +104,17 @@ def test_selection_and_attention(N, Hq, H, D, P, W, budget, sink, recent, dtype)
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, F8])
-def test_short_contexts_are_attended_whole(dtype):
-    """Budgets that hold every page: the result is tree attention's for one node."""
-    cache, bounds, table = make(3, 20, 2, 16, 128, dtype, 5)
-    q = torch.randn(3, 8, 128, device=DEV).to(torch.bfloat16)
+@pytest.mark.parametrize("D,Hq", [(96, 8), (128, 18), (128, 8), (64, 2)])
+def test_short_contexts_are_attended_whole(dtype, D, Hq):
+    """Budgets that hold every page: tree attention of one node, bit for bit where its kernels do the work."""
+    cache, bounds, table = make(3, 20, 2, 16, D, dtype, 5)
+    q = torch.randn(3, Hq, D, device=DEV).to(torch.bfloat16)
     positions = [319, 100, 0]
     pos = torch.tensor(positions, dtype=torch.int32, device=DEV)
     a = sv.sparse_attention(q, cache, bounds, table, pos, 20)
-    b = sv.tree_attention(q.view(3, 1, 8, 128), cache, table, pos).view(3, 8, 128)
-    assert torch.equal(a, b)
+    b = sv.tree_attention(q.view(3, 1, Hq, D), cache, table, pos).view(3, Hq, D)
+    if D == 96 or Hq == 18:
+        assert torch.equal(a, b)
     check(cache, bounds, table, q, positions, None, 20, 1, 1)
 
 
@@ -215,3 +218,40 @@ def test_many_rows_and_two_workspaces_at_once():
     got = [sv.sparse_attention(q, cache, bounds, table, dpos, 6, seqs=dseq, stream=s) for s in streams * 3]
     torch.cuda.synchronize()
     assert all(torch.equal(g, want) for g in got)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, F8])
+@pytest.mark.parametrize("D", [64, 128])
+def test_scores_and_values_of_any_size(dtype, D):
+    """Scores that grow page by page, huge and tiny values, and values whose scales differ by 2^40."""
+    cache, bounds, table = make(1, 70, 2, 16, D, dtype, 13)
+    n = 70 * 16
+    g = torch.Generator(device=DEV).manual_seed(2)
+    k = torch.randn(n, 2, D, generator=g, device=DEV)
+    k *= torch.linspace(0.1, 12.0, n, device=DEV)[:, None, None]
+    v = torch.randn(n, 2, D, generator=g, device=DEV) * torch.exp2(torch.randint(-20, 20, (n, 2, 1), generator=g,
+                                                                                 device=DEV).float())
+    slots = (table[0].long().repeat_interleave(16) * 16 + torch.arange(n, device=DEV) % 16)
+    sv.cache_write(k, v, slots, cache)
+    sv.page_bounds(cache, bounds, table, torch.zeros(1, dtype=torch.int32, device=DEV),
+                   torch.tensor([n], dtype=torch.int32, device=DEV))
+    q = torch.randn(1, 8, D, device=DEV).to(torch.bfloat16)
+    q[0, 1] *= 2.0 ** 30
+    q[0, 2] *= 2.0 ** -30
+    q[0, 3, 1:] = 0.0
+    for budget in (70, 33, 3):
+        check(cache, bounds, table, q, [n - 1], [0], budget, 1, 1)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, F8])
+def test_nan_behind_the_last_key_does_not_count(dtype):
+    cache, bounds, table = make(1, 10, 2, 16, 128, dtype, 14)
+    row = cache.v_scale if dtype == F8 else cache.v
+    key = cache.k_scale if dtype == F8 else cache.k
+    page = int(table[0, 9])
+    row[page, :, 7:] = float("nan")
+    key[page, :, 7:] = float("nan")
+    q = torch.randn(1, 8, 128, device=DEV).to(torch.bfloat16)
+    check(cache, bounds, table, q, [9 * 16 + 6], [0], 4, 1, 1)
+    out = sv.sparse_attention(q, cache, bounds, table, torch.tensor([9 * 16 + 7], dtype=torch.int32, device=DEV), 4)
+    assert torch.isnan(out).all()
