@@ -327,7 +327,7 @@ SV_DEVINL void sum_lanes(int (&v)[16], int li) {
 
 // LP lanes hold the 2 D codes of a page, 16 each (LP = 0: any D, a warp a page); HC heads at a time.
 template <int LP, int HC, int THREADS>
-__global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : HC == 4 ? 4 : 3) select_kernel(const __grid_constant__ SelArgs a) {
+__global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : 4) select_kernel(const __grid_constant__ SelArgs a) {
   constexpr int WARPS = THREADS / 32;
   extern __shared__ __align__(16) unsigned char dyn[];
   unsigned* keys = reinterpret_cast<unsigned*>(dyn);               // [max_pages] (first CTA)
@@ -354,6 +354,33 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : HC == 4 ? 4 : 3) 
     for (int i = tid; i < a.clear_words; i += THREADS) a.clear[i] = 0;
     for (int i = tid; i < a.clear2_words; i += THREADS) a.clear2[i] = 0;
   }
+
+  const int Dp = (a.D + 15) & ~15;
+  auto codes_of = [&](int h0) {
+    // A warp a head: its largest magnitude, then its codes.
+    for (int j = warp; j < HC; j += WARPS) {
+      float top = 0.0f;
+      bool fin = true;
+      const __nv_bfloat16* qr = a.q + n * a.q_sn + (long long)(h * G + h0 + j) * a.q_sh;
+      const bool on = h0 + j < G;
+      for (int d = lane; on && d < a.D; d += 32) {
+        const float x = fabsf(__bfloat162float(qr[d]));
+        fin = fin && x <= FLT_MAX;
+        top = fmaxf(top, x);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      fin = __all_sync(0xffffffffu, fin) && on;
+      top = fmaxf(top, kAmaxMin);
+      const float up = __fdiv_rn(kCodeMax, top);
+      for (int d = lane; d < Dp; d += 32) {
+        const float x = fin && d < a.D ? rintf(__fmul_rn(__bfloat162float(qr[d]), up)) : 0.0f;
+        qcode[j * Dp + d] = (signed char)(int)fminf(fmaxf(x, -kCodeMax), kCodeMax);
+      }
+      if (lane == 0) qscale[j] = fin ? __fdiv_rn(top, kCodeMax) : 0.0f;
+    }
+  };
+  codes_of(0);  // (nothing it needs has to be looked up first)
 
   const int pos = a.positions[n], seq = a.seqs ? a.seqs[n] : (int)n;
   const bool empty = pos == -1 || seq == -1;
@@ -398,32 +425,10 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : HC == 4 ? 4 : 3) 
   };
 
   if (rank_pages) {
-    const int Dp = (a.D + 15) & ~15;
 #pragma unroll 1
     for (int h0 = 0; h0 < G; h0 += HC) {
       if (h0) __syncthreads();
-      // A warp a head: its largest magnitude, then its codes.
-      for (int j = warp; j < HC; j += WARPS) {
-        float top = 0.0f;
-        bool fin = true;
-        const __nv_bfloat16* qr = a.q + n * a.q_sn + (long long)(h * G + h0 + j) * a.q_sh;
-        const bool on = h0 + j < G;
-        for (int d = lane; on && d < a.D; d += 32) {
-          const float x = fabsf(__bfloat162float(qr[d]));
-          fin = fin && x <= FLT_MAX;
-          top = fmaxf(top, x);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        fin = __all_sync(0xffffffffu, fin) && on;
-        top = fmaxf(top, kAmaxMin);
-        const float up = __fdiv_rn(kCodeMax, top);
-        for (int d = lane; d < Dp; d += 32) {
-          const float x = fin && d < a.D ? rintf(__fmul_rn(__bfloat162float(qr[d]), up)) : 0.0f;
-          qcode[j * Dp + d] = (signed char)(int)fminf(fmaxf(x, -kCodeMax), kCodeMax);
-        }
-        if (lane == 0) qscale[j] = fin ? __fdiv_rn(top, kCodeMax) : 0.0f;
-      }
+      if (h0 > 0) codes_of(h0);
       if (h0 == 0)
         joined();
       else
@@ -448,16 +453,25 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : HC == 4 ? 4 : 3) 
         const float qs0 = qscale[my_j], qs1 = LP == 8 ? qscale[my_j + 1] : 0.0f;
         const int stride = a.Hkv * 2 * a.D;
         const int8_t* base = a.codes + (long long)h * 2 * a.D + li * 16;
-#pragma unroll 1
-        for (int i0 = warp * PPW * U; i0 < mine; i0 += WARPS * PPW * U) {
-          uint4 c[U];
+        auto fetch = [&](int i0, uint4 (&c)[U], float& ps) {
 #pragma unroll
           for (int u = 0; u < U; ++u) {
             const int id = ids[min(i0 + u * PPW + sub, mine - 1)];
             c[u] = used ? __ldg(reinterpret_cast<const uint4*>(base + (long long)id * stride)) : make_uint4(0, 0, 0, 0);
           }
+          ps = __ldg(a.scale + (long long)ids[min(i0 + my_u * PPW + sub, mine - 1)] * a.Hkv + h);
+        };
+        uint4 c[U], ahead[U];  // the next turn's pages are under way while one is worked on
+        float ps, ps_ahead = 0.0f;
+        int i0 = warp * PPW * U;
+        if (i0 < mine) fetch(i0, ahead, ps_ahead);
+#pragma unroll 1
+        for (; i0 < mine; i0 += WARPS * PPW * U) {
+#pragma unroll
+          for (int u = 0; u < U; ++u) c[u] = ahead[u];
+          ps = ps_ahead;
+          if (i0 + WARPS * PPW * U < mine) fetch(i0 + WARPS * PPW * U, ahead, ps_ahead);
           const int i = i0 + my_u * PPW + sub;
-          const float ps = __ldg(a.scale + (long long)ids[min(i, mine - 1)] * a.Hkv + h);
           int v[16];
 #pragma unroll
           for (int u = 0; u < U; ++u)

@@ -37,6 +37,7 @@ constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr float kNone = -1e38f;  // below any score
 constexpr float kLazy = 8.0f;
+constexpr float kTiny = 1e-36f;   // products below count as 0 (the scale of a row of zeros is above)
 constexpr float kRaise = 128.0f;  // products go up to 2^8 of their reference: raised to 2^15, below fp16's largest
 
 SV_DEVINL void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -129,7 +130,7 @@ SV_DEVINL void load_block(Block<D, F8>& x, const Args& a, long long row0, int le
 }
 
 template <int D, bool F8>
-__global__ void __launch_bounds__(kThreads, F8 ? 4 : 3) sparse_decode_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kThreads, 4) sparse_decode_kernel(const __grid_constant__ Args a) {
   using B = Block<D, F8>;
   constexpr int STEPS = D / 16, U = F8 ? 2 : 1;
   __shared__ float so[kWarps][8][D];
@@ -229,8 +230,14 @@ __global__ void __launch_bounds__(kThreads, F8 ? 4 : 3) sparse_decode_kernel(con
           for (int d = 4; d < 32; d <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, d));
           const float f = ex2_fast(m[i] - t);
           l[i] *= f;
+          if constexpr (F8) {
+            ref[i] *= f;  // O stays: its reference is what shrinks
+            if (ref[i] < kTiny) ref[i] = 0.0f;
+            inv[i] = ref[i] > 0.0f ? __fdiv_rn(kRaise, ref[i]) : 0.0f;
+          } else {
 #pragma unroll
-          for (int t2 = 0; t2 < D / 16; ++t2) o[t2][i] *= f, o[t2][i + 2] *= f;
+            for (int t2 = 0; t2 < D / 16; ++t2) o[t2][i] *= f, o[t2][i + 2] *= f;
+          }
           m[i] = t;
         }
       }
@@ -249,6 +256,7 @@ __global__ void __launch_bounds__(kThreads, F8 ? 4 : 3) sparse_decode_kernel(con
             float t = fmaxf(ref[i], fmaxf(p[i], p[i + 2]));
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, d));
+            if (t < kTiny) t = 0.0f;
             inv[i] = t > 0.0f ? __fdiv_rn(kRaise, t) : 0.0f;
             const float f = ref[i] * inv[i] * (1.0f / kRaise);
 #pragma unroll

@@ -222,11 +222,12 @@ def test_many_rows_and_two_workspaces_at_once():
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, F8])
 @pytest.mark.parametrize("D", [64, 128])
-def test_scores_and_values_of_any_size(dtype, D):
+@pytest.mark.parametrize("seed", range(6))
+def test_scores_and_values_of_any_size(dtype, D, seed):
     """Scores that grow page by page, huge and tiny values, and values whose scales differ by 2^40."""
     cache, bounds, table = make(1, 70, 2, 16, D, dtype, 13)
     n = 70 * 16
-    g = torch.Generator(device=DEV).manual_seed(2)
+    g = torch.Generator(device=DEV).manual_seed(seed)
     k = torch.randn(n, 2, D, generator=g, device=DEV)
     k *= torch.linspace(0.1, 12.0, n, device=DEV)[:, None, None]
     v = torch.randn(n, 2, D, generator=g, device=DEV) * torch.exp2(torch.randint(-20, 20, (n, 2, 1), generator=g,
@@ -235,7 +236,7 @@ def test_scores_and_values_of_any_size(dtype, D):
     sv.cache_write(k, v, slots, cache)
     sv.page_bounds(cache, bounds, table, torch.zeros(1, dtype=torch.int32, device=DEV),
                    torch.tensor([n], dtype=torch.int32, device=DEV))
-    q = torch.randn(1, 8, D, device=DEV).to(torch.bfloat16)
+    q = torch.randn(1, 8, D, generator=g, device=DEV).to(torch.bfloat16)
     q[0, 1] *= 2.0 ** 30
     q[0, 2] *= 2.0 ** -30
     q[0, 3, 1:] = 0.0
