@@ -22,30 +22,30 @@ typedef unsigned long long u64;
 // The kept entries are a prefix of the row in the order of logits, so that a row needs its
 // cut, the last entry that is kept. A cluster of CTAs shares a row and passes over it twice, the first time
 // from memory and then, as a rule, from L2:
-//   1. the maximum, and for top_p the sum of all weights in fp32;
-//   2. a sample of the tiles, as counts by distance from the maximum, gives a window of values that
-//      the cut is expected in, a few standard deviations of the sample wide;
-//   3. the entries of the window and above go to lists in shared memory, to be taken by full
-//      warps: those above are weighed and summed, those within are set aside;
-//   4. a histogram of the entries set aside gives the cut's bin, whose entries the first CTA
-//      puts in order; the kept ones' weights join the sums;
-//   5. the sums are kept by ranges of ids (records: what a warp has summed up between two turns of its
+//   1. the maximum, for top_p the sum of all weights in fp32, and counts of a sample of the tiles' entries by
+//      value; from them a window of values that the cut is expected in, a few standard deviations of the sample wide;
+//   2. the entries of the window and above go to lists in shared memory, to be taken by full
+//      warps: those above are weighed and summed, those within are set aside and counted into the bins of a histogram,
+//      by number and mass. The entries of the cut's bin go to every CTA, which puts them in order; the
+//      kept ones' weights join the sums;
+//   3. the sums are kept by ranges of ids (records: what a warp has summed up between two turns of its
 //      list), so that the uniform's range is known, and its token is found there.
-// All decisions are made on whole-number masses (2^-44 of the largest weight), where sums do not depend
-// on their order. Where the fp32 sum could change the cut, the mass below the window is
-// summed exactly. A window that misses the cut is widened; a row that still has none, or more
-// entries in its window than there is room for (ties), is halved bit by bit over the keys, a pass for every bit.
+// The CTAs wait for one another once after each of these steps, and once for the cut's bin. All decisions are made on
+// whole-number masses (2^-44 of the largest weight), where sums do not depend on their order. Where the fp32
+// sum could change the cut, the mass below the window is summed again, at last exactly. A window that misses the cut
+// is widened; a row that still has none, or more entries in its window than there is room for (ties), is
+// halved bit by bit over the keys, a pass for every bit.
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kTile = 256;        // elements of a warp's step: 8 a lane
 constexpr int kMaxCluster = 8;
 constexpr int kBins = 512;        // bins of the window
-constexpr int kSampleBins = 512;  // bins of the sample, 1/16 of a power of two each
+constexpr int kSampleBins = 512;  // bins of the sample below the maximum, 1/16 of a power of two each
+constexpr int kValueBins = 1024;  // bins by value, over and over again
 constexpr int kList = 288;        // listed entries of a warp: a tile's, and fewer than 32 left over
-constexpr int kAside = 2048;      // entries of a CTA set aside
+constexpr int kAside = 1792;      // entries of a CTA set aside
 constexpr int kCand = 1024;       // entries of the cut's bin
-constexpr int kFew = 256;         // entries set aside (by all CTAs) that are put in order without a histogram
 constexpr int kRecords = 64;      // ranges of ids of a warp
 
 struct Args {
@@ -80,15 +80,13 @@ struct Shared {
   float2 tab[1024];
   union {
     Entry list[kWarps][kList];
-    struct {
-      u64 cand[kCand];  // key, then ~id: entries of the cut's bin (first CTA)
-      unsigned hlo[kBins], hhi[kBins], hcnt[kBins];
-    };
+    u64 cand[kCand];  // key, then ~id: entries of the cut's bin
   };
   union {
     Entry aside[kAside];
-    unsigned sample[kSampleBins];
+    unsigned sample[kValueBins];
   };
+  unsigned hlo[kBins], hhi[kBins], hcnt[kBins];
   unsigned rec_lo[kWarps][kRecords], rec_hi[kWarps][kRecords];
   int rec_end[kWarps][kRecords];  // the id behind the record's last one
   int recs[kWarps];
@@ -99,6 +97,8 @@ struct Shared {
   u64 tile_sum[kWarps], hit_start;
   int hit_from, hit_to;
   float fmass[kWarps], fvar[kWarps], wmax[kWarps];
+  float cta_max[kMaxCluster], cta_sum[kMaxCluster], cta_far[kMaxCluster];
+  unsigned cta_sampled[kMaxCluster];
   unsigned n_aside, n_cand[4];
   int edge[6], bin;  // edges: of each attempt the window's upper and lower one
   u64 bin_mass;
@@ -231,7 +231,7 @@ SV_DEVINL unsigned scan_up(unsigned x, int lane) {
   return x;
 }
 
-// Among the n candidates of the cut's bin (first CTA), the one at which the running count reaches
+// Among the n candidates of the cut's bin, the one at which the running count reaches
 // `want`, or the running mass does (and does so for every mass from want_lo to want).
 // s.bin_mass and s.bin_count are what lies above the bin.
 __device__ __noinline__ void order_candidates(Shared& s, int n, bool by_count, u64 want_lo, u64 want) {
@@ -411,6 +411,10 @@ struct Row {
     }
   }
 
+  SV_DEVINL int bin_of(float l, float top, float per) const {
+    return min(kBins - 1, (int)fminf((top - l) * per, (float)kBins));
+  }
+
   // A record of the ids before `stop` that have none yet: the warp's sum of x. A full table is
   // halved first.
   SV_DEVINL void record(int& n, u64 x, int stop) {
@@ -436,7 +440,8 @@ struct Row {
 
   // The entries l >= lo of this CTA's share (`all`: every entry): those above hi (and, with a cut, those that it keeps)
   // are summed into records, the others set aside as far as there is room. Returns a thread's part of the sum.
-  SV_DEVINL u64 pass(float lo, float hi, bool cut, bool all, unsigned& count) {
+  // An entry set aside is counted into bin (top - l) per.
+  SV_DEVINL u64 pass(float lo, float hi, bool cut, bool all, float top, float per, unsigned& count) {
     const int ln = lane(), wp = warp();
     Entry* list = s.list[wp];
     const int first = min(tiles, wp * seg), last = min(tiles, first + seg), stop = min(end, begin + last * kTile);
@@ -484,7 +489,12 @@ struct Row {
           unsigned at = 0;
           if (ln == 0) at = atomicAdd(&s.n_aside, (unsigned)__popc(b));
           at = __shfl_sync(0xffffffffu, at, 0) + __popc(b & ((1u << ln) - 1));
-          if (put && at < (unsigned)kAside) s.aside[at] = e;
+          if (put && at < (unsigned)kAside) {
+            s.aside[at] = e;
+            const int bin = bin_of(e.l, top, per);
+            add64(&s.hlo[bin], &s.hhi[bin], weigh(e.l));
+            atomicAdd(&s.hcnt[bin], 1u);
+          }
         }
       };
       some_tiles<F32 ? 2 : 4>(first, last, 1, [&](int base, const uint32_t (&x)[WORDS]) {
@@ -522,6 +532,22 @@ struct Row {
     }
     if (ln == 0) s.recs[wp] = recs;
     return total;
+  }
+
+  // The mass of the entries l < lo relative to the maximum's, in fp32 (a thread's part).
+  SV_DEVINL float below_fast(float lo, float c_hi, float c_lo, float far) {
+    float x = 0.0f;
+    all_tiles<2>([&](int, const uint32_t (&v)[WORDS]) {
+      float2 t2 = make_float2(0.0f, 0.0f);
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+        const float2 l = make_float2(element<F32>(v, e), element<F32>(v, e + 1));
+        const float2 y = f2_fma(l, f2(c_lo), f2_fma(l, f2(c_hi), f2(-far)));
+        t2 = f2_add(t2, make_float2(l.x < lo ? ex2_fast(y.x) : 0.0f, l.y < lo ? ex2_fast(y.y) : 0.0f));
+      }
+      x += t2.x + t2.y;
+    });
+    return x;
   }
 
   // The mass of the entries l < lo, exactly (a thread's part).
@@ -690,24 +716,31 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
     }
   }
 
-  // The maximum (NaN if there is one), and for top_p alone the sum of all weights.
+  // The maximum (NaN if there is one); for top_p alone the sum of all weights, and a sample by value: entries
+  // of every step-th tile, or for small k the threads' maxima (where k of them lie, at least k entries do).
+  const bool summed = by_p && !K, by_top = K > 1 && K <= 16u * (unsigned)a.nc;
+  const float unit = 16.0f * c_hi;
   float m = neg_inf();
-  const bool summed = by_p && !K;
   float run = 0.0f, far = 0.0f;  // weights relative to 2^far
-  if (!summed) {
-    uint32_t m2 = 0xff80ff80u;
-    r.template all_tiles<F32 ? 4 : 8>([&](int, const uint32_t (&x)[WORDS]) {
-      if constexpr (F32) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m = max_nan(m, __uint_as_float(x[i]));
-      } else {
-        m2 = max2_nan(m2, max2_nan(max2_nan(x[0], x[1]), max2_nan(x[2], x[3])));
-      }
-    });
-    if constexpr (!F32) m = max_nan(bf16_lo(m2), bf16_hi(m2));
-  } else {
+  unsigned sampled = 0;
+  for (int i = tid; i < kValueBins; i += kThreads) s.sample[i] = 0;
+  for (int i = tid; i < 1024; i += kThreads) s.tab[i] = kSvExp2Table1024[i];
+  for (int i = tid; i < kBins; i += kThreads) s.hlo[i] = s.hhi[i] = s.hcnt[i] = 0;
+  if (tid < 6) s.edge[tid] = -1;
+  if (tid < 4) s.n_cand[tid] = 0;
+  if (tid == 0) {
+    s.n_aside = 0;
+    s.cut_key = 0;
+    s.cut_id = 0x7fffffff;
+  }
+  __syncthreads();
+  auto into_sample = [&](float l) {
+    // (further than the sample's bins from a maximum so far: far from the row's as well)
+    if ((m - l) * unit < (float)kSampleBins) atomicAdd(&s.sample[__float2int_rd(l * unit) & (kValueBins - 1)], 1u);
+  };
+  if (summed || (K > 1 && !by_top)) {
     bool nan = false;
-    r.template all_tiles<F32 ? 4 : 8>([&](int, const uint32_t (&x)[WORDS]) {
+    r.template all_tiles<F32 ? 4 : 8>([&](int base, const uint32_t (&x)[WORDS]) {
       float top;
       if constexpr (F32) {
         top = __uint_as_float(x[0]);
@@ -725,37 +758,72 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
         m = top;
       }
       if (m > neg_inf()) {
-        float2 t2 = make_float2(0.0f, 0.0f);
+        if (summed) {
+          float2 t2 = make_float2(0.0f, 0.0f);
 #pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-          const float2 l = make_float2(element<F32>(x, e), element<F32>(x, e + 1));
-          const float2 y = f2_fma(l, f2(c_lo), f2_fma(l, f2(c_hi), f2(-far)));
-          t2 = f2_add(t2, make_float2(ex2_fast(y.x), ex2_fast(y.y)));
+          for (int e = 0; e < 8; e += 2) {
+            const float2 l = make_float2(element<F32>(x, e), element<F32>(x, e + 1));
+            const float2 y = f2_fma(l, f2(c_lo), f2_fma(l, f2(c_hi), f2(-far)));
+            t2 = f2_add(t2, make_float2(ex2_fast(y.x), ex2_fast(y.y)));
+          }
+          run += t2.x + t2.y;
         }
-        run += t2.x + t2.y;
+      }
+      const int t = (base - begin) / kTile;
+      if ((t + (t >> 3)) % a.step == 0) {
+        sampled += (unsigned)min(kTile, end - base);
+        if (m > neg_inf()) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) into_sample(element<F32>(x, e));
+        }
       }
     });
     if (nan) m = __int_as_float(0x7fc00000);
-  }
-  const float m_lane = m;
-  for (int i = tid; i < 1024; i += kThreads) s.tab[i] = kSvExp2Table1024[i];
+  } else {
+    uint32_t m2 = 0xff80ff80u;
+    r.template all_tiles<F32 ? 4 : 8>([&](int, const uint32_t (&x)[WORDS]) {
+      if constexpr (F32) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (lane == 0) s.wmax[warp] = m;
-  for (int i = tid; i < kSampleBins; i += kThreads) s.sample[i] = 0;
-  if (tid < 6) s.edge[tid] = -1;
-  if (tid == 0) {
-    s.cut_key = 0;
-    s.cut_id = 0x7fffffff;
+        for (int i = 0; i < 8; ++i) m = max_nan(m, __uint_as_float(x[i]));
+      } else {
+        m2 = max2_nan(m2, max2_nan(max2_nan(x[0], x[1]), max2_nan(x[2], x[3])));
+      }
+    });
+    if constexpr (!F32) m = max_nan(bf16_lo(m2), bf16_hi(m2));
+    if (by_top && m > neg_inf()) into_sample(m);
   }
-  __syncthreads();
+  // The CTA's, then the row's. A sum is relative to 2^far of its CTA.
+  {
+    const float mine = m;
 #pragma unroll
-  for (int i = 0; i < kWarps; ++i) m = max_nan(m, s.wmax[i]);
-  if (a.nc > 1) {
-    cluster_wait();
-    if (tid < a.nc) dsmem_st_u32(r.remote(&s.inbox_c[1][rank], tid), __float_as_uint(m));
-    cluster_sync();
-    for (int i = 0; i < a.nc; ++i) m = max_nan(m, __uint_as_float(s.inbox_c[1][i]));
+    for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (lane == 0) s.wmax[warp] = m;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) m = max_nan(m, s.wmax[i]);
+    const float to = m * c_hi;
+    float sum = run > 0.0f && mine > neg_inf() ? run * ex2_fast(far - to) : 0.0f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) s.fmass[warp] = sum, s.wcnt[0][warp] = sampled;
+    __syncthreads();
+    if (warp == 0) {
+      if (a.nc > 1) cluster_wait();
+      sum = 0.0f, sampled = 0;
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) sum += s.fmass[i], sampled += s.wcnt[0][i];
+      if (lane < a.nc) {
+        dsmem_st_u32(r.remote(&s.cta_max[rank], lane), __float_as_uint(m));
+        dsmem_st_u32(r.remote(&s.cta_sum[rank], lane), __float_as_uint(sum));
+        dsmem_st_u32(r.remote(&s.cta_far[rank], lane), __float_as_uint(to));
+        dsmem_st_u32(r.remote(&s.cta_sampled[rank], lane), sampled);
+      }
+    } else if (a.nc > 1) {
+      cluster_wait();
+    }
+    r.sync();
+    m = s.cta_max[0];
+    for (int i = 1; i < a.nc; ++i) m = max_nan(m, s.cta_max[i]);
   }
 
   unsigned fault = 0;
@@ -801,49 +869,36 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
   float lo = floor_l, hi = floor_l > -FLT_MAX ? unordered(ordered(floor_l) - 1u) : -FLT_MAX;
 
   if (!K && !by_p) {
-    sum = r.pass(lo, hi, false, !by_m, sure);
+    sum = r.pass(lo, hi, false, !by_m, 0.0f, 0.0f, sure);
   } else {
     bool found = false;
-    u64 mass_all = 0, slack = 0;  // of the row, and what it may be off by
-    const float unit = 16.0f * c_hi, w_m = __ull2float_rn(r.weigh(m));
-    // For small k the threads' maxima will do as a sample: where k of them lie, at least k entries do.
-    const bool by_top = K > 1 && K <= 16u * (unsigned)a.nc;
+    const u64 w_max = r.weigh(m);
+    const float w_m = __ull2float_rn(w_max), top_c = m * c_hi;
+    u64 mass_all = 0;  // of the row
+    float mass_f = 0.0f;
     if (summed && w.fast) {
-      // A thread's sum is relative to 2^far, where its maximum was.
-      unsigned z = 0;
-      mass_all = run > 0.0f ? __float2ull_rn(run * ex2_fast(__fmaf_rn(-m, c_hi, far) - m * c_lo) * w_m) : 0;
-      r.sum(mass_all, z);
-      slack = mass_all >> 21;
+      for (int i = 0; i < a.nc; ++i) {
+        const float x = s.cta_sum[i];
+        if (x > 0.0f) mass_f += x * ex2_fast(__fmaf_rn(-m, c_hi, s.cta_far[i]) - m * c_lo);
+      }
+      mass_all = __float2ull_rn(mass_f * w_m);
     }
+    const int top_bin = __float2int_rd(m * unit);  // (w.fast: |m unit| < 2^15)
     if (K != 1 && w.fast) {
-      if (by_top) {
-        const float d = (m - m_lane) * unit;
-        if (d < (float)kSampleBins) atomicAdd(&s.sample[(int)d], 1u);
-      } else {
-        r.template some_tiles<2>(warp * a.step, tiles, kWarps * a.step, [&](int, const uint32_t (&x)[WORDS]) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float d = (m - element<F32>(x, e)) * unit;
-            if (d < (float)kSampleBins) atomicAdd(&s.sample[(int)d], 1u);
-          }
-        });
-      }
-      int sampled = 0;
-#pragma unroll 1
-      for (int i = 0; i < a.nc; ++i) {
-        const int len = min(a.share, max(0, a.V - i * a.share)), n_tiles = (len + kTile - 1) / kTile;
-        const int k = (n_tiles + a.step - 1) / a.step;
-        sampled += k == 0 ? 0 : (n_tiles - 1) % a.step == 0 ? (k - 1) * kTile + len - (n_tiles - 1) * kTile : k * kTile;
-      }
-      r.sync();
+      unsigned n_sampled = 0;
+      for (int i = 0; i < a.nc; ++i) n_sampled += s.cta_sampled[i];
       // Two bins a thread, the deepest first: the sample's mass below, its variance, and the count above.
-      const int b = kSampleBins - 2 - 2 * tid;
+      const int b = kSampleBins - 2 - 2 * tid, at0 = (top_bin - b) & (kValueBins - 1), at1 = (top_bin - b - 1) & (kValueBins - 1);
       unsigned c0 = 0, c1 = 0;
-      for (int i = 0; i < a.nc; ++i) {
-        c0 += dsmem_ld_u32(r.remote(&s.sample[b], i));
-        c1 += dsmem_ld_u32(r.remote(&s.sample[b + 1], i));
-      }
-      const float w0 = ex2_fast(-0.0625f * ((float)b + 0.5f)), w1 = ex2_fast(-0.0625f * ((float)b + 1.5f));
+#pragma unroll
+      for (int i = 0; i < kMaxCluster; ++i)
+        if (i < a.nc) {
+          c0 += dsmem_ld_u32(r.remote(&s.sample[at0], i));
+          c1 += dsmem_ld_u32(r.remote(&s.sample[at1], i));
+        }
+      // (a bin's middle is b + part - 1/2 sixteenths below the maximum, part = m unit - top_bin)
+      const float mid = (float)b + (m * unit - (float)top_bin) - 0.5f;
+      const float w0 = ex2_fast(-0.0625f * mid), w1 = ex2_fast(-0.0625f * (mid + 1.0f));
       const float m0 = (float)c0 * w0, m1 = (float)c1 * w1, v0 = m0 * w0, v1 = m1 * w1;
       unsigned cc = scan_up(c0 + c1, lane);
       float cm = m0 + m1, cv = v0 + v1;
@@ -852,19 +907,19 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
         const float y = __shfl_up_sync(0xffffffffu, cm, o), q = __shfl_up_sync(0xffffffffu, cv, o);
         if (lane >= o) cm += y, cv += q;
       }
+      if (lane == 31) s.wcnt[1][warp] = cc, s.fmass[warp] = cm, s.fvar[warp] = cv;
       __syncthreads();
-      if (lane == 31) s.wcnt[0][warp] = cc, s.fmass[warp] = cm, s.fvar[warp] = cv;
-      __syncthreads();
+      if (a.nc > 1) cluster_arrive_relaxed();  // the other CTAs' samples have been read
       unsigned all_c = 0;
       float below_m = 0.0f, below_v = 0.0f;
 #pragma unroll
       for (int i = 0; i < kWarps; ++i) {
-        if (i < warp) cc += s.wcnt[0][i], below_m += s.fmass[i], below_v += s.fvar[i];
-        all_c += s.wcnt[0][i];
+        if (i < warp) cc += s.wcnt[1][i], below_m += s.fmass[i], below_v += s.fvar[i];
+        all_c += s.wcnt[1][i];
       }
       cm += below_m, cv += below_v;
-      const float scale = by_top ? 1.0f : (float)a.V / (float)max(sampled, 1);
-      const float want_below = K ? 0.0f : (1.0f - top_p) * __ull2float_rn(mass_all) / (w_m * scale);
+      const float scale = by_top ? 1.0f : (float)a.V / (float)max(n_sampled, 1u);
+      const float want_below = K ? 0.0f : (1.0f - top_p) * mass_f / scale;
 #pragma unroll 1
       for (int t = 0; t < 3; ++t) {
         const float z = t == 0 ? 3.5f : t == 1 ? 8.0f : 20.0f, rel = t == 0 ? 0.03f : t == 1 ? 0.15f : 0.5f;
@@ -892,6 +947,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
           atomicMax(&s.edge[2 * t + 1], down);
         }
       }
+      if (a.nc > 1) cluster_wait();
       __syncthreads();
     }
 #pragma unroll 1
@@ -900,92 +956,74 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
         lo = m;
         hi = FLT_MAX;
       } else {
+        // Edge e is the value (top_bin - e + 1) / unit.
         const int up = s.edge[2 * attempt], down = s.edge[2 * attempt + 1];
-        hi = up > 0 ? m - (float)up / unit : FLT_MAX;
-        lo = down + 1 >= kSampleBins ? -FLT_MAX : fmaxf(m - (float)(down + 1) / unit, -FLT_MAX);
+        hi = up > 0 ? (float)(top_bin - up + 1) / unit : FLT_MAX;
+        lo = down + 1 >= kSampleBins ? -FLT_MAX : fmaxf((float)(top_bin - down) / unit, -FLT_MAX);
       }
       const bool floored = !(K && by_p) && floor_l >= lo;  // min_p cuts above the window's end
       if (floored) {
         lo = floor_l;
         hi = fmaxf(hi, unordered(ordered(floor_l) - 1u));
       }
-      if (attempt > 0) r.sync();  // (what the last attempt left has been read)
-      __syncthreads();
-      if (tid == 0) s.n_aside = 0;
-      if (tid < 4) s.n_cand[tid] = 0;
-      __syncthreads();
-      sum = r.pass(lo, hi, false, false, sure);
+      if (attempt > 0) {
+        r.sync();  // (what the last attempt left has been read)
+        for (int i = tid; i < kBins; i += kThreads) s.hlo[i] = s.hhi[i] = s.hcnt[i] = 0;
+        if (tid == 0) s.n_aside = 0;
+        if (tid < 4) s.n_cand[tid] = 0;
+        __syncthreads();
+      }
+      const float top_l = hi == FLT_MAX ? m : hi, width = fminf(top_l - lo, (float)kSampleBins / unit);
+      const float per = width > 0.0f ? (float)kBins / width : 0.0f;
+      sum = r.pass(lo, hi, false, false, top_l, per, sure);
       __syncthreads();
       u64 above = sum;
-      unsigned above_c = sure, aside = tid == 0 ? min(s.n_aside, 0x10000u) : 0u;
+      unsigned above_c = sure, aside = tid == 0 ? s.n_aside : 0u;
       if (tid == 0 && s.n_aside > (unsigned)kAside) aside = 1u << 24;  // no room
       r.sum(above, above_c, aside);
       if (aside >= 1u << 24) break;
-      const int here = (int)min(s.n_aside, (unsigned)kAside);
-      const bool few = aside <= (unsigned)kFew;
-      // Masses and counts of the window's bins over all CTAs, two a thread, above what the thread's bins hold.
-      const float top_l = hi == FLT_MAX ? m : hi, width = fminf(top_l - lo, (float)kSampleBins / unit);
-      const float per = width > 0.0f ? (float)kBins / width : 0.0f;
-      auto bin_of = [&](float l) { return min(kBins - 1, (int)fminf((top_l - l) * per, (float)kBins)); };
-      u64 hm0 = 0, hm1 = 0, im = 0, all_m = 0;
-      unsigned hc0 = 0, hc1 = 0, ic = 0;
-      if (!few) {
-        for (int i = tid; i < kBins; i += kThreads) s.hlo[i] = s.hhi[i] = s.hcnt[i] = 0;
-        __syncthreads();
-        for (int i = tid; i < here; i += kThreads) {
-          const int b = bin_of(s.aside[i].l);
-          add64(&s.hlo[b], &s.hhi[b], r.weigh(s.aside[i].l));
-          atomicAdd(&s.hcnt[b], 1u);
-        }
-        r.sync();
-        for (int i = 0; i < a.nc; ++i) {
-          hm0 += (u64)dsmem_ld_u32(r.remote(&s.hhi[2 * tid], i)) << 32;
-          hm0 += dsmem_ld_u32(r.remote(&s.hlo[2 * tid], i));
-          hc0 += dsmem_ld_u32(r.remote(&s.hcnt[2 * tid], i));
-          hm1 += (u64)dsmem_ld_u32(r.remote(&s.hhi[2 * tid + 1], i)) << 32;
-          hm1 += dsmem_ld_u32(r.remote(&s.hlo[2 * tid + 1], i));
-          hc1 += dsmem_ld_u32(r.remote(&s.hcnt[2 * tid + 1], i));
-        }
-        im = scan_up(hm0 + hm1, lane);
-        ic = scan_up(hc0 + hc1, lane);
-        const int t = r.turn & 1;
-        ++r.turn;
-        if (lane == 31) s.wsum[t][warp] = im, s.wcnt[t][warp] = ic;
-        __syncthreads();
+      const int here = (int)s.n_aside;
+      // Masses and counts of the window's bins over all CTAs, two a thread, and what lies above the thread's.
+      u64 hm0 = 0, hm1 = 0;
+      unsigned hc0 = 0, hc1 = 0;
 #pragma unroll
-        for (int i = 0; i < kWarps; ++i) {
-          if (i < warp) im += s.wsum[t][i], ic += s.wcnt[t][i];
-          all_m += s.wsum[t][i];
+      for (int i = 0; i < kMaxCluster; ++i)
+        if (i < a.nc) {
+          const u64 h = dsmem_ld_u64(r.remote(&s.hhi[2 * tid], i)), l = dsmem_ld_u64(r.remote(&s.hlo[2 * tid], i)),
+                    c = dsmem_ld_u64(r.remote(&s.hcnt[2 * tid], i));
+          hm0 += (h << 32) + (l & 0xffffffffu);
+          hm1 += (h >> 32 << 32) + (l >> 32);
+          hc0 += (unsigned)c;
+          hc1 += (unsigned)(c >> 32);
         }
-        im += above - (hm0 + hm1);
-        ic += above_c - (hc0 + hc1);
-      } else {
-        // So few that the first CTA orders them all.
-        u64 x = 0;
-        for (int i = tid; i < here; i += kThreads) {
-          const Entry e = s.aside[i];
-          x += r.weigh(e.l);
-          const unsigned at = dsmem_add_u32(r.remote(&s.n_cand[0], 0), 1u);
-          dsmem_st_u64(r.remote(&s.cand[at], 0), (u64)ordered(e.l) << 32 | (unsigned)~e.id);
-        }
-        unsigned z = 0;
-        r.sum(x, z);
-        all_m = x;
+      u64 im = scan_up(hm0 + hm1, lane), all_m = above;
+      unsigned ic = scan_up(hc0 + hc1, lane);
+      const int t = r.turn & 1;
+      ++r.turn;
+      if (lane == 31) s.wsum[t][warp] = im, s.wcnt[t][warp] = ic;
+      if (tid == 0) s.bin = -1;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) {
+        if (i < warp) im += s.wsum[t][i], ic += s.wcnt[t][i];
+        all_m += s.wsum[t][i];
       }
-      all_m += above;
+      im += above - (hm0 + hm1);
+      ic += above_c - (hc0 + hc1);
       const unsigned all_c = above_c + aside;
-      int turn = 1;
-      bool exact = K != 0;
-      u64 total = mass_all;
+      int turn = 0, tier = K ? 2 : 0;  // tier: how well the mass below the window is known (2: exactly)
+      u64 total = mass_all, slack = mass_all >> 21;
 #pragma unroll 1
       for (int round = K ? 0 : 1; round < 2; ++round) {
         u64 want = K, want_lo = K;
+        bool better = false;  // the mass below the window decides, and could be known better
         if (round == 0) {
           if (above_c >= K) break;  // the window lies too deep
           if (all_c < K) {
             // Fewer than k: all of them are kept, if the window ends where the row or min_p does.
             if (!floored && lo > -FLT_MAX) break;
             total = all_m;
+            slack = 0;
             found = !by_p;
             if (found) break;
             continue;
@@ -995,25 +1033,19 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
           want_lo = part_of(total - slack);
           const bool in_sure = above >= want_lo, short_of = all_m < want;
           if (in_sure || short_of) {
-            if (!exact && ((in_sure && above < want) || (floored && short_of && all_m >= want_lo))) {
-              // The fp32 sum decides nothing here.
-              u64 rest = r.below(lo);
-              unsigned z = 0;
-              r.sum(rest, z);
-              total = all_m + rest;
-              slack = 0;
-              exact = true;
-              --round;
-              continue;
+            better = tier < 2 && ((in_sure && above < want) || (floored && short_of && all_m >= want_lo));
+            if (!better) {
+              found = !in_sure && floored;  // min_p cuts first: all entries of the window are kept
+              break;
             }
-            found = !in_sure && floored;  // min_p cuts first: all entries of the window are kept
-            break;
           }
         }
-        if (!few) {
+        if (!better) {
           // The bin in which the count or the mass is reached.
-          if (tid == 0) s.bin = -1;
-          __syncthreads();
+          if (turn > 0) {
+            if (tid == 0) s.bin = -1;
+            r.sync();  // (the last candidates have been read)
+          }
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const u64 from = j ? im + hm0 : im, to = from + (j ? hm1 : hm0);
@@ -1026,61 +1058,53 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
           }
           __syncthreads();
           const int bin = s.bin;
-          if (bin < 0) break;
+          if (bin < 0 || turn > 3) break;
           for (int i = tid; i < here; i += kThreads) {
             const Entry e = s.aside[i];
-            if (bin_of(e.l) == bin) {
-              const unsigned at = dsmem_add_u32(r.remote(&s.n_cand[turn], 0), 1u);
-              if (at < (unsigned)kCand)
-                dsmem_st_u64(r.remote(&s.cand[at], 0), (u64)ordered(e.l) << 32 | (unsigned)~e.id);
+            if (r.bin_of(e.l, top_l, per) == bin) {
+              for (int k = 0; k < a.nc; ++k) {
+                const unsigned at = dsmem_add_u32(r.remote(&s.n_cand[turn], k), 1u);
+                if (at < (unsigned)kCand)
+                  dsmem_st_u64(r.remote(&s.cand[at], k), (u64)ordered(e.l) << 32 | (unsigned)~e.id);
+              }
             }
           }
           r.sync();
-        } else if (tid == 0) {
-          s.bin_mass = above;
-          s.bin_count = above_c;
-        }
-        if (rank == 0) {
+          const int n_cand = (int)s.n_cand[turn];
+          ++turn;
+          if (n_cand > kCand) {
+            attempt = 3;  // too many ties
+            break;
+          }
+          order_candidates(s, n_cand, round == 0, want_lo, want);
           __syncthreads();
-          const int nc = (int)(few ? s.n_cand[0] : s.n_cand[turn]);
-          if (nc <= kCand)
-            order_candidates(s, nc, round == 0, want_lo, want);
-          else if (tid == 0)
-            s.cut_found = 0;
-          __syncthreads();
+          const int how = s.cut_found;
+          if (how == 0) break;
+          better = how == 2 && tier < 2;
+          if (!better) {
+            cut = true;
+            total = s.cut_mass;
+            slack = 0;
+            if (round == 1 || !by_p) {
+              found = true;
+              break;
+            }
+            continue;
+          }
         }
-        ++turn;
-        r.sync();
-        const int how = (int)dsmem_ld_u32(r.remote(&s.cut_found, 0));
-        const unsigned key = dsmem_ld_u32(r.remote(&s.cut_key, 0));
-        const int id = (int)dsmem_ld_u32(r.remote(&s.cut_id, 0));
-        const u64 mass = dsmem_ld_u64(r.remote(&s.cut_mass, 0));
-        r.sync();
-        if (how == 2 && !exact) {
-          u64 rest = r.below(lo);
-          unsigned z = 0;
-          r.sum(rest, z);
-          total = all_m + rest;
-          slack = 0;
-          exact = true;
-          --round;
-          continue;
+        // The mass below the window again: in fp32 (off by 2^-20 of itself at most), then exactly.
+        u64 rest;
+        unsigned z = 0;
+        if (tier == 0) {
+          rest = __float2ull_rn(r.below_fast(lo, c_hi, c_lo, top_c) * ex2_fast(__fmaf_rn(-m, c_hi, top_c) - m * c_lo) * w_m);
+        } else {
+          rest = r.below(lo);
         }
-        if (how != 1) {
-          attempt = 3;  // too many ties
-          break;
-        }
-        cut = true;
-        if (tid == 0) {
-          s.cut_key = key;
-          s.cut_id = id;
-        }
-        __syncthreads();
-        total = mass;
-        if (round == 1 || !by_p) {
-          found = true;
-          break;
-        }
+        r.sum(rest, z);
+        total = all_m + rest;
+        slack = tier == 0 ? rest >> 20 : 0;
+        ++tier;
+        --round;
       }
     }
     if (found) {
@@ -1107,10 +1131,10 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
         }
       }
     } else {
-      __syncthreads();
+      r.sync();
       cut_by_bits(r, K, by_p, part);
       cut = true;
-      sum = r.pass(fmaxf(floor_l, unordered(s.cut_key)), FLT_MAX, true, false, sure);
+      sum = r.pass(fmaxf(floor_l, unordered(s.cut_key)), FLT_MAX, true, false, 0.0f, 0.0f, sure);
     }
   }
 
