@@ -44,7 +44,8 @@ constexpr int kBins = 512;        // bins of the window
 constexpr int kSampleBins = 512;  // bins of the sample below the maximum, 1/16 of a power of two each
 constexpr int kValueBins = 1024;  // bins by value, over and over again
 constexpr int kList = 288;        // listed entries of a warp: a tile's, and fewer than 32 left over
-constexpr int kAside = 1792;      // entries of a CTA set aside
+constexpr int kAsideBytes = 14336; // entries of a CTA set aside: 3584 short or 1792 long ones
+constexpr int kShortIds = 65536;  // ids of a CTA's share that a short entry can tell apart
 constexpr int kCand = 1024;       // entries of the cut's bin
 constexpr int kRecords = 64;      // ranges of ids of a warp
 
@@ -71,19 +72,30 @@ struct Weigh {
   float il, m, lmin, low, scale;
 };
 
+// A listed entry: value and place in the CTA's share; a bf16 value and 16 bits of place where those do.
+template <bool SHORT>
 struct Entry {
-  float l;
-  int id;
+  typedef u64 Word;
+  static SV_DEVINL u64 make(uint32_t value, int at) { return (u64)value << 32 | (unsigned)at; }
+  static SV_DEVINL float value(u64 w) { return __uint_as_float((unsigned)(w >> 32)); }
+  static SV_DEVINL int at(u64 w) { return (int)(unsigned)w; }
+};
+template <>
+struct Entry<true> {
+  typedef uint32_t Word;
+  static SV_DEVINL uint32_t make(uint32_t value, int at) { return value | (unsigned)at; }  // (value: the high half)
+  static SV_DEVINL float value(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+  static SV_DEVINL int at(uint32_t w) { return (int)(w & 0xffffu); }
 };
 
 struct Shared {
   float2 tab[1024];
   union {
-    Entry list[kWarps][kList];
-    u64 cand[kCand];  // key, then ~id: entries of the cut's bin
+    u64 list[kWarps][kList];  // of either kind of entry
+    u64 cand[kCand];          // key, then ~id: entries of the cut's bin
   };
   union {
-    Entry aside[kAside];
+    u64 aside[kAsideBytes / 8];  // of either kind
     unsigned sample[kValueBins];
   };
   unsigned hlo[kBins], hhi[kBins], hcnt[kBins];
@@ -100,7 +112,7 @@ struct Shared {
   float cta_max[kMaxCluster], cta_sum[kMaxCluster], cta_far[kMaxCluster];
   unsigned cta_sampled[kMaxCluster];
   unsigned n_aside, n_cand[4];
-  int edge[6], bin;  // edges: of each attempt the window's upper and lower one
+  int edge[2], bin;  // edges: the window's upper and lower one
   u64 bin_mass;
   unsigned bin_count;
   // The cut: entries of a larger key are kept, and those of this key up to `cut_id`; their mass.
@@ -205,6 +217,11 @@ SV_DEVINL unsigned dsmem_add_u32(unsigned a, unsigned v) {
   unsigned r;
   asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(r) : "r"(a), "r"(v) : "memory");
   return r;
+}
+
+// All ones in the halves where a >= b.
+SV_DEVINL uint32_t ge2(uint32_t a, uint32_t b) {
+  return __hge2_mask(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
 }
 
 // A 64-bit sum in two words of shared memory.
@@ -321,9 +338,12 @@ SV_DEVINL float ratio(u64 x, u64 y) {
   return q + __fdiv_rn(__fmaf_rn(-q, yh, xh) + (xl - q * yl), yh);
 }
 
-template <bool F32, bool VEC>
+template <bool F32, bool VEC, bool SHORT>
 struct Row {
   static constexpr int WORDS = F32 ? 8 : 4;
+  typedef Entry<SHORT> E;
+  typedef typename E::Word Word;
+  static constexpr unsigned kAside = kAsideBytes / sizeof(Word);
   const Args& a;
   Shared& s;
   const void* row;
@@ -443,7 +463,8 @@ struct Row {
   // An entry set aside is counted into bin (top - l) per.
   SV_DEVINL u64 pass(float lo, float hi, bool cut, bool all, float top, float per, unsigned& count) {
     const int ln = lane(), wp = warp();
-    Entry* list = s.list[wp];
+    Word* list = reinterpret_cast<Word*>(s.list[wp]);
+    Word* aside = reinterpret_cast<Word*>(s.aside);
     const int first = min(tiles, wp * seg), last = min(tiles, first + seg), stop = min(end, begin + last * kTile);
     u64 total = 0;
     int recs = 0;
@@ -473,14 +494,16 @@ struct Row {
       int n = 0;
       u64 acc = 0;
       auto take = [&](int from, bool on) {  // 32 entries of the list
-        const Entry e = list[from + ln];
-        bool sure = e.l > hi;
+        const Word e = list[from + ln];
+        const float l = E::value(e);
+        bool sure = l > hi;
         if (cut && !sure) {
-          const unsigned k = ordered(e.l);
-          sure = k > key || (k == key && e.id <= cut_id);
+          const unsigned k = ordered(l);
+          sure = k > key || (k == key && begin + E::at(e) <= cut_id);
         }
+        const u64 x = on && (sure || !cut) ? weigh(l) : 0;
         if (on && sure) {
-          acc += weigh(e.l);
+          acc += x;
           ++count;
         }
         const bool put = on && !sure && !cut;
@@ -489,20 +512,31 @@ struct Row {
           unsigned at = 0;
           if (ln == 0) at = atomicAdd(&s.n_aside, (unsigned)__popc(b));
           at = __shfl_sync(0xffffffffu, at, 0) + __popc(b & ((1u << ln) - 1));
-          if (put && at < (unsigned)kAside) {
-            s.aside[at] = e;
-            const int bin = bin_of(e.l, top, per);
-            add64(&s.hlo[bin], &s.hhi[bin], weigh(e.l));
+          if (put && at < kAside) {
+            aside[at] = e;
+            const int bin = bin_of(l, top, per);
+            add64(&s.hlo[bin], &s.hhi[bin], x);
             atomicAdd(&s.hcnt[bin], 1u);
           }
         }
       };
+      uint32_t lo2 = 0;  // the least bf16 at or above lo, twice
+      if constexpr (!F32) {
+        const unsigned b = __bfloat16_as_ushort(__float2bfloat16_ru(lo));
+        lo2 = b | b << 16;
+      }
       some_tiles<F32 ? 2 : 4>(first, last, 1, [&](int base, const uint32_t (&x)[WORDS]) {
         if (!__any_sync(0xffffffffu, top_of(x) >= lo)) return;
         // In the order of ids: fp32's two halves of a tile one behind the other.
         unsigned mask = 0;
+        if constexpr (F32) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) mask |= element<F32>(x, e) >= lo ? 1u << e : 0u;
+          for (int e = 0; e < 8; ++e) mask |= element<F32>(x, e) >= lo ? 1u << e : 0u;
+        } else {
+          mask = (ge2(x[0], lo2) & 0x00020001u) | (ge2(x[1], lo2) & 0x00080004u) | (ge2(x[2], lo2) & 0x00200010u) |
+                 (ge2(x[3], lo2) & 0x00800040u);
+          mask = (mask | mask >> 16) & 0xffu;
+        }
         const unsigned c = F32 ? __popc(mask & 15u) | __popc(mask >> 4) << 16 : __popc(mask);
         const unsigned incl = scan_up(c, ln), sum = __shfl_sync(0xffffffffu, incl, 31);
         const int head = (int)(sum & 0xffffu), both = head + (int)(sum >> 16);
@@ -510,8 +544,8 @@ struct Row {
           __syncwarp();
           const int full = n & ~31;
           for (int i = 0; i < full; i += 32) take(i, true);
-          const int stop_at = list[min(full, kList - 1)].id;
-          const Entry left = list[min(full + ln, kList - 1)];
+          const int stop_at = begin + E::at(list[min(full, kList - 1)]);
+          const Word left = list[min(full + ln, kList - 1)];
           total += acc;
           record(recs, acc, full < n ? stop_at : base);
           acc = 0;
@@ -522,7 +556,8 @@ struct Row {
         int at = n + (int)((incl - c) & 0xffffu), at2 = n + head + (int)((incl - c) >> 16);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          if (mask >> e & 1u) list[F32 && e >= 4 ? at2++ : at++] = Entry{element<F32>(x, e), base + tile_id<F32>(ln, e)};
+          if (mask >> e & 1u)
+            list[F32 && e >= 4 ? at2++ : at++] = E::make(__float_as_uint(element<F32>(x, e)), base - begin + tile_id<F32>(ln, e));
         n += both;
       });
       __syncwarp();
@@ -566,8 +601,8 @@ struct Row {
 
 // The cut of a row by halving: the largest key that the wanted count (K, or 0) or mass reaches, then the last of its
 // ties that is kept; into s.cut_key and s.cut_id.
-template <bool F32, bool VEC>
-SV_DEVINL void cut_by_bits(Row<F32, VEC>& r, unsigned K, bool by_p, u64 part) {
+template <bool F32, bool VEC, bool SHORT>
+SV_DEVINL void cut_by_bits(Row<F32, VEC, SHORT>& r, unsigned K, bool by_p, u64 part) {
   constexpr int WORDS = F32 ? 8 : 4;
   Shared& s = r.s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -671,7 +706,7 @@ SV_DEVINL void cut_by_bits(Row<F32, VEC>& r, unsigned K, bool by_p, u64 part) {
   __syncthreads();
 }
 
-template <bool F32, bool VEC>
+template <bool F32, bool VEC, bool SHORT>
 __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_constant__ Args a) {
   extern __shared__ __align__(16) unsigned char dyn[];
   Shared& s = *reinterpret_cast<Shared*>(dyn);
@@ -687,7 +722,9 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
   const bool by_p = top_p < 1.0f && T > 0.0f, by_m = min_p > 0.0f && T > 0.0f;
   const int begin = min(a.V, (int)rank * a.share), end = min(a.V, begin + a.share);
   const int tiles = (end - begin + kTile - 1) / kTile;
-  Row<F32, VEC> r{a, s, static_cast<const unsigned char*>(a.logits) + (long long)n * a.stride * (F32 ? 4 : 2),
+  typedef Entry<SHORT> E;
+  typedef typename E::Word Word;
+  Row<F32, VEC, SHORT> r{a, s, static_cast<const unsigned char*>(a.logits) + (long long)n * a.stride * (F32 ? 4 : 2),
                   begin, end, tiles, (tiles + kWarps - 1) / kWarps, rank, 0};
   Weigh& w = r.w;
 
@@ -723,10 +760,11 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
   float m = neg_inf();
   float run = 0.0f, far = 0.0f;  // weights relative to 2^far
   unsigned sampled = 0;
+  int to_sample = 1 + warp % a.step;  // tiles of this warp up to the next one that is sampled
   for (int i = tid; i < kValueBins; i += kThreads) s.sample[i] = 0;
   for (int i = tid; i < 1024; i += kThreads) s.tab[i] = kSvExp2Table1024[i];
   for (int i = tid; i < kBins; i += kThreads) s.hlo[i] = s.hhi[i] = s.hcnt[i] = 0;
-  if (tid < 6) s.edge[tid] = -1;
+  if (tid < 2) s.edge[tid] = -1;
   if (tid < 4) s.n_cand[tid] = 0;
   if (tid == 0) {
     s.n_aside = 0;
@@ -769,8 +807,8 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
           run += t2.x + t2.y;
         }
       }
-      const int t = (base - begin) / kTile;
-      if ((t + (t >> 3)) % a.step == 0) {
+      if (--to_sample == 0) {
+        to_sample = a.step;
         sampled += (unsigned)min(kTile, end - base);
         if (m > neg_inf()) {
 #pragma unroll
@@ -920,32 +958,28 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
       cm += below_m, cv += below_v;
       const float scale = by_top ? 1.0f : (float)a.V / (float)max(n_sampled, 1u);
       const float want_below = K ? 0.0f : (1.0f - top_p) * mass_f / scale;
-#pragma unroll 1
-      for (int t = 0; t < 3; ++t) {
-        const float z = t == 0 ? 3.5f : t == 1 ? 8.0f : 20.0f, rel = t == 0 ? 0.03f : t == 1 ? 0.15f : 0.5f;
-        int up = -1, down = -1;  // the deepest bin edge that is surely above the cut; that is not surely below it
+      int up = -1, down = -1;  // the deepest bin edge that is surely above the cut; that is not surely below it
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int edge = b + j;
-          if (K) {
-            const float above = (float)(all_c - cc + (j ? c0 : 0u));
-            const float dev = by_top ? 0.0f : z * sqrt_fast(above + 1.0f) + 2.0f;
-            if (!by_p && !by_top && (above + dev) * scale <= (float)K) up = edge;
-            if ((above - dev) * scale < (float)K) down = edge;
-          } else {
-            // (An entry that the sample has missed may weigh as much as the edge's: one more in the variance.)
-            const float one = j ? w1 : w0, mass = j ? cm - m0 : cm;
-            const float dev = z * sqrt_fast((j ? fmaxf(cv - v0, 0.0f) : cv) + one * one) + rel * mass + 2.0f * one;
-            if (mass - dev >= want_below) up = edge;
-            if (mass + dev > want_below) down = edge;
-          }
+      for (int j = 0; j < 2; ++j) {
+        const int edge = b + j;
+        if (K) {
+          const float above = (float)(all_c - cc + (j ? c0 : 0u));
+          const float dev = by_top ? 0.0f : 3.5f * sqrt_fast(above + 1.0f) + 2.0f;
+          if (!by_p && !by_top && (above + dev) * scale <= (float)K) up = edge;
+          if ((above - dev) * scale < (float)K) down = edge;
+        } else {
+          // (An entry that the sample has missed may weigh as much as the edge's: one more in the variance.)
+          const float one = j ? w1 : w0, mass = j ? cm - m0 : cm;
+          const float dev = 3.5f * sqrt_fast((j ? fmaxf(cv - v0, 0.0f) : cv) + one * one) + 0.03f * mass + 2.0f * one;
+          if (mass - dev >= want_below) up = edge;
+          if (mass + dev > want_below) down = edge;
         }
-        up = __reduce_max_sync(0xffffffffu, up);
-        down = __reduce_max_sync(0xffffffffu, down);
-        if (lane == 0) {
-          atomicMax(&s.edge[2 * t], up);
-          atomicMax(&s.edge[2 * t + 1], down);
-        }
+      }
+      up = __reduce_max_sync(0xffffffffu, up);
+      down = __reduce_max_sync(0xffffffffu, down);
+      if (lane == 0) {
+        atomicMax(&s.edge[0], up);
+        atomicMax(&s.edge[1], down);
       }
       if (a.nc > 1) cluster_wait();
       __syncthreads();
@@ -957,7 +991,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
         hi = FLT_MAX;
       } else {
         // Edge e is the value (top_bin - e + 1) / unit.
-        const int up = s.edge[2 * attempt], down = s.edge[2 * attempt + 1];
+        const int wider = 24 * attempt * attempt, up = s.edge[0] - wider, down = s.edge[1] + wider;
         hi = up > 0 ? (float)(top_bin - up + 1) / unit : FLT_MAX;
         lo = down + 1 >= kSampleBins ? -FLT_MAX : fmaxf((float)(top_bin - down) / unit, -FLT_MAX);
       }
@@ -979,7 +1013,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
       __syncthreads();
       u64 above = sum;
       unsigned above_c = sure, aside = tid == 0 ? s.n_aside : 0u;
-      if (tid == 0 && s.n_aside > (unsigned)kAside) aside = 1u << 24;  // no room
+      if (tid == 0 && s.n_aside > r.kAside) aside = 1u << 24;  // no room
       r.sum(above, above_c, aside);
       if (aside >= 1u << 24) break;
       const int here = (int)s.n_aside;
@@ -1060,12 +1094,14 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
           const int bin = s.bin;
           if (bin < 0 || turn > 3) break;
           for (int i = tid; i < here; i += kThreads) {
-            const Entry e = s.aside[i];
-            if (r.bin_of(e.l, top_l, per) == bin) {
+            const Word e = reinterpret_cast<const Word*>(s.aside)[i];
+            const float l = E::value(e);
+            if (r.bin_of(l, top_l, per) == bin) {
+#pragma unroll 1
               for (int k = 0; k < a.nc; ++k) {
                 const unsigned at = dsmem_add_u32(r.remote(&s.n_cand[turn], k), 1u);
                 if (at < (unsigned)kCand)
-                  dsmem_st_u64(r.remote(&s.cand[at], k), (u64)ordered(e.l) << 32 | (unsigned)~e.id);
+                  dsmem_st_u64(r.remote(&s.cand[at], k), (u64)ordered(l) << 32 | (unsigned)~(begin + E::at(e)));
               }
             }
           }
@@ -1109,19 +1145,21 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
     }
     if (found) {
       // What is kept of the entries set aside joins the records.
-      const int here = (int)min(s.n_aside, (unsigned)kAside);
+      const int here = (int)min(s.n_aside, r.kAside);
       const unsigned key = cut ? s.cut_key : 0u;
       const int cut_id = cut ? s.cut_id : 0;
       for (int i = tid; i < here; i += kThreads) {
-        const Entry e = s.aside[i];
-        const unsigned k = ordered(e.l);
-        if (e.l >= floor_l && (k > key || (k == key && e.id <= cut_id))) {
-          const u64 x = r.weigh(e.l);
-          const int wp = (e.id - begin) / kTile / r.seg;
+        const Word e = reinterpret_cast<const Word*>(s.aside)[i];
+        const float l = E::value(e);
+        const int id = begin + E::at(e);
+        const unsigned k = ordered(l);
+        if (l >= floor_l && (k > key || (k == key && id <= cut_id))) {
+          const u64 x = r.weigh(l);
+          const int wp = E::at(e) / kTile / r.seg;
           int j = 0, left = s.recs[wp];  // the first record that ends behind the id
           while (left > 1) {
             const int half = left / 2;
-            if (s.rec_end[wp][j + half - 1] <= e.id)
+            if (s.rec_end[wp][j + half - 1] <= id)
               j += half, left -= half;
             else
               left = half;
@@ -1255,7 +1293,7 @@ namespace {
 
 bool misaligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
 
-template <bool F32, bool VEC>
+template <bool F32, bool VEC, bool SHORT>
 int launch(const sv::fs::Args& a, cudaStream_t st) {
   static std::mutex mu;
   static bool set[64] = {};
@@ -1264,7 +1302,7 @@ int launch(const sv::fs::Args& a, cudaStream_t st) {
   {
     std::lock_guard<std::mutex> lock(mu);
     if (!set[device]) {
-      if (cudaFuncSetAttribute(sv::fs::sample_kernel<F32, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      if (cudaFuncSetAttribute(sv::fs::sample_kernel<F32, VEC, SHORT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                (int)sizeof(sv::fs::Shared)) != cudaSuccess)
         return SV_ERR_CUDA;
       set[device] = true;
@@ -1281,7 +1319,7 @@ int launch(const sv::fs::Args& a, cudaStream_t st) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, sv::fs::sample_kernel<F32, VEC>, a) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, sv::fs::sample_kernel<F32, VEC, SHORT>, a) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 
 }  // namespace
@@ -1319,7 +1357,8 @@ extern "C" int spec_filtered_sample(const void* logits, int64_t row_stride, cons
   a.prob = out_probs;
   a.status = status;
   a.nc = 1;
-  while (a.nc < sv::fs::kMaxCluster && V >= 8192 * a.nc && ((long long)N * a.nc * 2 <= 608 || V > 32768 * a.nc)) a.nc *= 2;
+  while (a.nc < sv::fs::kMaxCluster && V >= 8192 * a.nc && ((long long)N * a.nc * 2 <= 608 || V > (dtype == SV_F32 ? 32768 : 65536) * a.nc))
+    a.nc *= 2;
   const int tile = sv::fs::kTile;
   a.share = (int)(((long long)V + (long long)tile * a.nc - 1) / ((long long)tile * a.nc) * tile);
   a.step = std::max(1, V / (1 << 14) > 8 ? 8 : V / (1 << 14));
@@ -1328,6 +1367,8 @@ extern "C" int spec_filtered_sample(const void* logits, int64_t row_stride, cons
   a.scale_bits = std::min(44, 61 - lg);
   const bool vec = !misaligned(logits, 16) && ((size_t)row_stride * es) % 16 == 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (dtype == SV_F32) return vec ? launch<true, true>(a, st) : launch<true, false>(a, st);
-  return vec ? launch<false, true>(a, st) : launch<false, false>(a, st);
+  if (dtype == SV_F32) return vec ? launch<true, true, false>(a, st) : launch<true, false, false>(a, st);
+  // (more than 524288 ids: long entries, and element loads, since no such vocabulary is common)
+  if (a.share > sv::fs::kShortIds) return launch<false, false, false>(a, st);
+  return vec ? launch<false, true, true>(a, st) : launch<false, false, true>(a, st);
 }
