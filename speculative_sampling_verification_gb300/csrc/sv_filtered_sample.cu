@@ -67,7 +67,7 @@ struct Args {
 // number of 2^-scale_bits.
 struct Weigh {
   bool fast;
-  int qb;
+  int shift;  // of a weight's 45 bits at k >> 10 = 0
   DrawConst dc;
   float il, m, lmin, low, scale;
 };
@@ -143,8 +143,18 @@ __device__ __noinline__ u64 weight_far(float l, float m, float ih, float il, flo
 
 SV_DEVINL u64 weight(float l, const Weigh& w, const float2* tab) {
   if (!w.fast) return weight_far(l, w.m, w.dc.ih, w.il, w.low, w.scale);
-  const ff e = exp_draw(fmaxf(l, w.lmin), w.qb, w.dc, tab);
-  return (u64)((long long)__float2ll_rn(e.hi * w.scale) + __float2ll_rn(e.lo * w.scale));
+  // exp_draw's steps up to head + tail = T.x + lo in [1, 2) times 2^(k >> 10), then in whole numbers: the
+  // head's 24 bits and the tail's to 2^-40, twice 2^44 of them, shifted into place and rounded.
+  const float x = fmaxf(l, w.lmin);
+  const float ym = __fmaf_rn(x, -w.dc.inv, kRoundMagic), nkf = __fsub_rn(ym, kRoundMagic);
+  const float sv = __fmaf_rn(__fmaf_rn(nkf, w.dc.ch, x), w.dc.ih, __fmul_rn(nkf, w.dc.cli));
+  const float u = __fmaf_rn(sv, __fmul_rn(__fmaf_rn(sv, 1.0f / 6.0f, 0.5f), sv), sv);
+  const int k = __float_as_int(kRoundMagic) - __float_as_int(ym);
+  const float2 T = tab[k & 1023];
+  const int tail = __float2int_rn(__fmaf_rn(T.x, u, T.y) * 0x1p40f);  // below 2^31
+  const unsigned head = (__float_as_uint(T.x) & 0x7fffffu) | 0x800000u;
+  const u64 both = (u64)head * (1u << 22) + (u64)((long long)tail * 32);
+  return ((both >> min(w.shift - (k >> 10), 63)) + 1) >> 1;
 }
 
 // Eight elements a lane of the tile at `base` of a row, as they are stored (bf16 pairs in the first
@@ -884,7 +894,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
   {
     const float top = m * w.dc.ih;
     w.fast = fabsf(top) < 1386.0f;
-    w.qb = 127 - ((int)floorf((w.fast ? top : 0.0f) * 1.44269504f) + 1);
+    w.shift = 44 - a.scale_bits + (int)floorf((w.fast ? top : 0.0f) * 1.44269504f) + 1;
     if (tid == 0) s.w = w;
   }
   // The least logit that min_p keeps: m + T ln(min_p), rounded up.
