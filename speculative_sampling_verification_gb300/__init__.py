@@ -1155,7 +1155,7 @@ def _setting(name, value, off, N, dtype, device):
     """A setting of all rows or of each: (address or None, value)."""
     if value is None:
         return None, off
-    if isinstance(value, torch.Tensor):
+    if hasattr(value, "data_ptr"):
         _vector(name, value, (N,), dtype, device)
         return value.data_ptr(), off
     return None, value
