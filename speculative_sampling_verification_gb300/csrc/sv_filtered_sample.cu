@@ -41,7 +41,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kTile = 256;        // elements of a warp's step: 8 a lane
 constexpr int kMaxCluster = 8;
 constexpr int kBins = 512;        // bins of the window
-constexpr int kSampleBins = 512;  // bins of the sample below the maximum, 1/16 of a power of two each
+constexpr int kSampleBins = 512;  // bins of the sample below the maximum
 constexpr int kValueBins = 1024;  // bins by value, over and over again
 constexpr int kList = 288;        // listed entries of a warp: a tile's, and fewer than 32 left over
 constexpr int kAsideBytes = 14336; // entries of a CTA set aside: 3584 short or 1792 long ones
@@ -766,7 +766,26 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
   // The maximum (NaN if there is one); for top_p alone the sum of all weights, and a sample by value: entries
   // of every step-th tile, or for small k the threads' maxima (where k of them lie, at least k entries do).
   const bool summed = by_p && !K, by_top = K > 1 && K <= 16u * (unsigned)a.nc;
-  const float unit = 16.0f * c_hi;
+  // Bins of the sample per unit of logit: 16 a power of two of weight, or, where it is the count that matters, 128 for
+  // what the row's first 256 entries spread over.
+  float unit = 16.0f * c_hi;
+  if (K > 1) {
+    uint32_t x[WORDS];
+    load_tile<F32, VEC>(r.row, 0, a.V, lane, x);
+    float top = neg_inf(), low = INFINITY;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float l = element<F32>(x, e);
+      top = fmaxf(top, l);
+      if (l > neg_inf()) low = fminf(low, l);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
+    }
+    if (top > low && top - low <= FLT_MAX) unit = __fdiv_rn(128.0f, top - low);
+  }
   float m = neg_inf();
   float run = 0.0f, far = 0.0f;  // weights relative to 2^far
   unsigned sampled = 0;

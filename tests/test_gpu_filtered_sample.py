@@ -163,7 +163,7 @@ def test_uniforms_at_the_ends(dtype):
 
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_failed_rows(dtype):
-    logits = torch.randn(8, 3000).to(dtype)
+    logits = torch.randn(8, 3000, generator=torch.Generator().manual_seed(6)).to(dtype)
     logits[1, 2999], logits[2, 0], logits[3] = float("nan"), torch.inf, -torch.inf
     u = torch.full((8,), 0.5)
     u[4] = 1.5
@@ -184,14 +184,15 @@ def test_strides_and_alignment(dtype, pad, offset):
     N, V = 6, 4000
     store = torch.full((N * (V + pad) + offset,), float("nan"), dtype=dtype, device=DEV)
     logits = store[offset:].view(N, V + pad)[:, :V]
-    logits.copy_(3.0 * torch.randn(N, V))
-    check(logits, rng.random(N).astype(np.float32), *settings(N, "all", rng, V))
+    logits.copy_(3.0 * torch.randn(N, V, generator=torch.Generator().manual_seed(pad)))
+    # (two equal logits kept by top_k = 2 put a border at exactly top_p = 0.5: such rows are passed over)
+    check(logits, rng.random(N).astype(np.float32), *settings(N, "all", rng, V), most_near=2)
 
 
 def test_graph_and_other_stream():
     rng = np.random.default_rng(1)
     N, V = 9, 30001
-    logits = (3.0 * torch.randn(N, V)).to(torch.bfloat16).to(DEV)
+    logits = (3.0 * torch.randn(N, V, generator=torch.Generator().manual_seed(4))).to(torch.bfloat16).to(DEV)
     T, k, p, m = settings(N, "mixed", rng, V)
     u = rng.random(N).astype(np.float32)
     want = run(logits, u, T, k, p, m)
