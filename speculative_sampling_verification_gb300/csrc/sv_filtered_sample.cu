@@ -33,8 +33,8 @@ typedef unsigned long long u64;
 // The CTAs wait for one another once after each of these steps, and once for the cut's bin. All decisions are made on
 // whole-number masses (2^-44 of the largest weight), where sums do not depend on their order. Where the fp32
 // sum could change the cut, the mass below the window is summed again, at last exactly. A window that misses the cut
-// is widened; a row that still has none, or more entries in its window than there is room for (ties), is
-// halved bit by bit over the keys, a pass for every bit.
+// is widened, or begins above its old top where the cut turns out to lie there; a row that still has none, or more
+// entries in its window than there is room for (ties), is halved bit by bit over the keys, a pass for every bit.
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
@@ -784,7 +784,8 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
       low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
     }
-    if (top > low && top - low <= FLT_MAX) unit = __fdiv_rn(128.0f, top - low);
+    // (and so that the bins' edges are floats of their own)
+    if (top > low && top - low <= FLT_MAX) unit = fminf(__fdiv_rn(128.0f, top - low), __fdiv_rn(0x1p18f, fmaxf(top, -low)));
   }
   float m = neg_inf();
   float run = 0.0f, far = 0.0f;  // weights relative to 2^far
@@ -939,6 +940,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
     sum = r.pass(lo, hi, false, !by_m, 0.0f, 0.0f, sure);
   } else {
     bool found = false;
+    float raised = FLT_MAX;  // the cut is known to lie above this logit, and few entries do
     const u64 w_max = r.weigh(m);
     const float w_m = __ull2float_rn(w_max), top_c = m * c_hi;
     u64 mass_all = 0;  // of the row
@@ -950,7 +952,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
       }
       mass_all = __float2ull_rn(mass_f * w_m);
     }
-    const int top_bin = __float2int_rd(m * unit);  // (w.fast: |m unit| < 2^15)
+    const int top_bin = __float2int_rd(fminf(fmaxf(m * unit, -0x1p30f), 0x1p30f));
     if (K != 1 && w.fast) {
       unsigned n_sampled = 0;
       for (int i = 0; i < a.nc; ++i) n_sampled += s.cta_sampled[i];
@@ -1018,6 +1020,9 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
       if (K == 1) {
         lo = m;
         hi = FLT_MAX;
+      } else if (raised < FLT_MAX) {
+        lo = raised;
+        hi = FLT_MAX;
       } else {
         // Edge e is the value (top_bin - e + 1) / unit.
         const int wider = 24 * attempt * attempt, up = s.edge[0] - wider, down = s.edge[1] + wider;
@@ -1036,7 +1041,8 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
         if (tid < 4) s.n_cand[tid] = 0;
         __syncthreads();
       }
-      const float top_l = hi == FLT_MAX ? m : hi, width = fminf(top_l - lo, (float)kSampleBins / unit);
+      const float top_l = hi == FLT_MAX ? m : hi;
+      const float width = raised < FLT_MAX ? top_l - lo : fminf(top_l - lo, (float)kSampleBins / unit);
       const float per = width > 0.0f ? (float)kBins / width : 0.0f;
       sum = r.pass(lo, hi, false, false, top_l, per, sure);
       __syncthreads();
@@ -1081,7 +1087,10 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
         u64 want = K, want_lo = K;
         bool better = false;  // the mass below the window decides, and could be known better
         if (round == 0) {
-          if (above_c >= K) break;  // the window lies too deep
+          if (above_c >= K) {  // the window lies too deep
+            if (above_c <= r.kAside) raised = hi;
+            break;
+          }
           if (all_c < K) {
             // Fewer than k: all of them are kept, if the window ends where the row or min_p does.
             if (!floored && lo > -FLT_MAX) break;
@@ -1099,6 +1108,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
             better = tier < 2 && ((in_sure && above < want) || (floored && short_of && all_m >= want_lo));
             if (!better) {
               found = !in_sure && floored;  // min_p cuts first: all entries of the window are kept
+              if (in_sure && above_c <= r.kAside) raised = hi;
               break;
             }
           }

@@ -236,3 +236,21 @@ def test_large_and_many_rows():
         g = torch.Generator(device=DEV).manual_seed(V)
         logits = (2.5 * torch.randn(N, V, generator=g, device=DEV)).to(dtype)
         check(logits, rng.random(N).astype(np.float32), *settings(N, kind, rng, V), most_near=3)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("kind", ["k", "p", "kp", "pm"])
+@pytest.mark.parametrize("spread", [8.0, 20.0, 1e-3])
+def test_rows_that_their_sample_misjudges(dtype, kind, spread):
+    """Logits further apart than the sample tells apart, and a first part of the row that is unlike the rest."""
+    N, V = 33, 32000
+    rng = np.random.default_rng(int(spread) + len(kind))
+    g = torch.Generator().manual_seed(int(spread) * 3 + len(kind))
+    x = spread * torch.randn(N, V, generator=g)
+    x[::3, :256] *= 1e-4
+    x[1::3, :256] -= 40.0
+    x.scatter_add_(1, torch.randint(0, V, (N, 32), generator=g), torch.full((N, 32), 2.0 * spread))
+    x = x.to(dtype).to(DEV)
+    u = rng.random(N).astype(np.float32)
+    # (bf16 at 1e-3: few different values and so many equal weights; borders at round numbers of them)
+    check(x, u, *settings(N, kind, rng, V), most_near=3)
