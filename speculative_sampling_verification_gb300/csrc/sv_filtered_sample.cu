@@ -32,7 +32,7 @@ typedef unsigned long long u64;
 //      list), so that the uniform's range is known, and its token is found there.
 // The CTAs wait for one another once after each of these steps, and once for the cut's bin. All decisions are made on
 // whole-number masses (2^-44 of the largest weight), where sums do not depend on their order. Where the fp32
-// sum could change the cut, the mass below the window is summed again, at last exactly. A window that misses the cut
+// sum could change the cut, the mass below the window is summed again, exactly. A window that misses the cut
 // is widened, or begins above its old top where the cut turns out to lie there; a row that still has none, or more
 // entries in its window than there is room for (ties), is halved bit by bit over the keys, a pass for every bit.
 
@@ -109,7 +109,8 @@ struct Shared {
   u64 tile_sum[kWarps], hit_start;
   int hit_from, hit_to;
   float fmass[kWarps], fvar[kWarps], wmax[kWarps];
-  float cta_max[kMaxCluster], cta_sum[kMaxCluster], cta_far[kMaxCluster];
+  u64 cta_sum[kMaxCluster];
+  float cta_max[kMaxCluster];
   unsigned cta_sampled[kMaxCluster];
   unsigned n_aside, n_cand[4];
   int edge[2], bin;  // edges: the window's upper and lower one
@@ -338,6 +339,14 @@ SV_DEVINL u64 fraction(float x) {
   const int e = (int)(b >> 23) - 86;  // x = mantissa 2^(e + 86 - 150)
   const u64 mant = (b & 0x7fffffu) | (b >> 23 ? 0x800000u : 0u);
   return e >= 0 ? mant << e : e > -24 ? mant >> -e : 0;
+}
+
+// x 2^e, x >= 0, rounded.
+SV_DEVINL u64 whole(float x, int e) {
+  const unsigned b = __float_as_uint(x);
+  const int sh = (int)(b >> 23) - 150 + e;
+  const u64 mant = (b & 0x7fffffu) | 0x800000u;
+  return b < 0x800000u || sh < -25 ? 0 : sh >= 0 ? mant << min(sh, 39) : ((mant >> (-sh - 1)) + 1) >> 1;
 }
 
 // x / y for 0 < x <= y, to fp32's last place.
@@ -579,22 +588,6 @@ struct Row {
     return total;
   }
 
-  // The mass of the entries l < lo relative to the maximum's, in fp32 (a thread's part).
-  SV_DEVINL float below_fast(float lo, float c_hi, float c_lo, float far) {
-    float x = 0.0f;
-    all_tiles<2>([&](int, const uint32_t (&v)[WORDS]) {
-      float2 t2 = make_float2(0.0f, 0.0f);
-#pragma unroll
-      for (int e = 0; e < 8; e += 2) {
-        const float2 l = make_float2(element<F32>(v, e), element<F32>(v, e + 1));
-        const float2 y = f2_fma(l, f2(c_lo), f2_fma(l, f2(c_hi), f2(-far)));
-        t2 = f2_add(t2, make_float2(l.x < lo ? ex2_fast(y.x) : 0.0f, l.y < lo ? ex2_fast(y.y) : 0.0f));
-      }
-      x += t2.x + t2.y;
-    });
-    return x;
-  }
-
   // The mass of the entries l < lo, exactly (a thread's part).
   SV_DEVINL u64 below(float lo) {
     u64 x = 0;
@@ -788,7 +781,15 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
     if (top > low && top - low <= FLT_MAX) unit = fminf(__fdiv_rn(128.0f, top - low), __fdiv_rn(0x1p18f, fmaxf(top, -low)));
   }
   float m = neg_inf();
-  float run = 0.0f, far = 0.0f;  // weights relative to 2^far
+  // The sum: 2^(n + f - far) for l log2(e)/T = n + f with n whole and |f| <= 1/2, where ex2.approx is off by
+  // 1.46e-7 at most (every argument tried), and the roundings of f by 2.1e-8. Eight are added in three steps
+  // (2^-24 each) and then in float-floats: the sum is good to 3.5e-7, whatever the entries are (measured: 1.7e-7 at
+  // most, 1e-8 for normal logits). far is a thread's maximum so far; entries below lmin count as lmin (2^-101).
+  const float reach = -1480.0f * (T > 0.0f ? T : 1.0f);  // no entry as low as this counts in a row with `fast` weights
+  float ref = reach, lmin = 1.0475f * reach, far = rintf(reach * c_hi), magic = kRoundMagic - far;
+  uint32_t lmin2 = 0;  // the same, two bf16
+  if constexpr (!F32) lmin2 = __bfloat16_as_ushort(__float2bfloat16_ru(lmin)) * 0x10001u;
+  ff run{0.0f, 0.0f};
   unsigned sampled = 0;
   int to_sample = 1 + warp % a.step;  // tiles of this warp up to the next one that is sampled
   for (int i = tid; i < kValueBins; i += kThreads) s.sample[i] = 0;
@@ -807,7 +808,6 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
     if ((m - l) * unit < (float)kSampleBins) atomicAdd(&s.sample[__float2int_rd(l * unit) & (kValueBins - 1)], 1u);
   };
   if (summed || (K > 1 && !by_top)) {
-    bool nan = false;
     r.template all_tiles<F32 ? 4 : 8>([&](int base, const uint32_t (&x)[WORDS]) {
       float top;
       if constexpr (F32) {
@@ -818,24 +818,37 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
         const uint32_t t2 = max2_nan(max2_nan(x[0], x[1]), max2_nan(x[2], x[3]));
         top = max_nan(bf16_lo(t2), bf16_hi(t2));
       }
-      if (!(top <= m)) {  // a new maximum (or NaN)
-        const float to = top * c_hi;
-        run = run > 0.0f ? run * ex2_fast(far - to) : 0.0f;
-        far = to;
-        nan |= isnan(top);
-        m = top;
-      }
-      if (m > neg_inf()) {
-        if (summed) {
-          float2 t2 = make_float2(0.0f, 0.0f);
-#pragma unroll
-          for (int e = 0; e < 8; e += 2) {
-            const float2 l = make_float2(element<F32>(x, e), element<F32>(x, e + 1));
-            const float2 y = f2_fma(l, f2(c_lo), f2_fma(l, f2(c_hi), f2(-far)));
-            t2 = f2_add(t2, make_float2(ex2_fast(y.x), ex2_fast(y.y)));
-          }
-          run += t2.x + t2.y;
+      m = max_nan(m, top);
+      if (summed) {
+        if (top > ref) {
+          const float to = rintf(top * c_hi), down = __int_as_float(max(127 + __float2int_rn(far - to), 0) << 23);
+          run.hi *= down;
+          run.lo *= down;
+          far = to;
+          ref = top;
+          magic = kRoundMagic - far;
+          lmin = top + 0.0475f * reach;
+          if constexpr (!F32) lmin2 = __bfloat16_as_ushort(__float2bfloat16_ru(lmin)) * 0x10001u;
         }
+        float2 t2[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float2 l;
+          if constexpr (F32) {
+            l = make_float2(fmaxf(element<F32>(x, 2 * e), lmin), fmaxf(element<F32>(x, 2 * e + 1), lmin));
+          } else {
+            const uint32_t l2 = bf16x2_max(x[e], lmin2);
+            l = make_float2(bf16_lo(l2), bf16_hi(l2));
+          }
+          const float2 k = f2_fma(l, f2(c_hi), f2(magic)), n = f2_fma(k, f2(-1.0f), f2(magic));
+          const float2 y = f2_fma(l, f2(c_lo), f2_fma(l, f2(c_hi), n));
+          t2[e] = make_float2(__uint_as_float(__float_as_uint(ex2_fast(y.x)) + (__float_as_uint(k.x) << 23)),
+                              __uint_as_float(__float_as_uint(ex2_fast(y.y)) + (__float_as_uint(k.y) << 23)));
+        }
+        const float2 t = f2_add(f2_add(t2[0], t2[1]), f2_add(t2[2], t2[3]));
+        const ff to = two_sum(run.hi, t.x + t.y);
+        run.hi = to.hi;
+        run.lo += to.lo;
       }
       if (--to_sample == 0) {
         to_sample = a.step;
@@ -846,7 +859,6 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
         }
       }
     });
-    if (nan) m = __int_as_float(0x7fc00000);
   } else {
     uint32_t m2 = 0xff80ff80u;
     r.template all_tiles<F32 ? 4 : 8>([&](int, const uint32_t (&x)[WORDS]) {
@@ -860,30 +872,31 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
     if constexpr (!F32) m = max_nan(bf16_lo(m2), bf16_hi(m2));
     if (by_top && m > neg_inf()) into_sample(m);
   }
-  // The CTA's, then the row's. A sum is relative to 2^far of its CTA.
+  // The power of two above the weight of l.
+  auto exponent = [&](float l) { return max(__float2int_rd(l * w.dc.ih * 1.44269504f), -4000) + 1; };
+  // The CTA's, then the row's; the sum is in whole numbers, as the weights are.
   {
-    const float mine = m;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
     if (lane == 0) s.wmax[warp] = m;
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kWarps; ++i) m = max_nan(m, s.wmax[i]);
-    const float to = m * c_hi;
-    float sum = run > 0.0f && mine > neg_inf() ? run * ex2_fast(far - to) : 0.0f;
+    const int e = __float2int_rn(far) - exponent(m) + a.scale_bits;
+    u64 sum = summed ? whole(run.hi, e) : 0;
+    sum += run.lo < 0.0f ? 0 - whole(-run.lo, e) : whole(run.lo, e);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) s.fmass[warp] = sum, s.wcnt[0][warp] = sampled;
+    if (lane == 0) s.wsum[0][warp] = sum, s.wcnt[0][warp] = sampled;
     __syncthreads();
     if (warp == 0) {
       if (a.nc > 1) cluster_wait();
-      sum = 0.0f, sampled = 0;
+      sum = 0, sampled = 0;
 #pragma unroll
-      for (int i = 0; i < kWarps; ++i) sum += s.fmass[i], sampled += s.wcnt[0][i];
+      for (int i = 0; i < kWarps; ++i) sum += s.wsum[0][i], sampled += s.wcnt[0][i];
       if (lane < a.nc) {
         dsmem_st_u32(r.remote(&s.cta_max[rank], lane), __float_as_uint(m));
-        dsmem_st_u32(r.remote(&s.cta_sum[rank], lane), __float_as_uint(sum));
-        dsmem_st_u32(r.remote(&s.cta_far[rank], lane), __float_as_uint(to));
+        dsmem_st_u64(r.remote(&s.cta_sum[rank], lane), sum);
         dsmem_st_u32(r.remote(&s.cta_sampled[rank], lane), sampled);
       }
     } else if (a.nc > 1) {
@@ -913,8 +926,8 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
   w.m = m;
   {
     const float top = m * w.dc.ih;
-    w.fast = fabsf(top) < 1386.0f;
-    w.shift = 44 - a.scale_bits + (int)floorf((w.fast ? top : 0.0f) * 1.44269504f) + 1;
+    w.fast = fabsf(top) < 1386.0f && T < 1e30f;  // (T: so that T times anything here is a number)
+    w.shift = 44 - a.scale_bits + exponent(w.fast ? m : 0.0f);
     if (tid == 0) s.w = w;
   }
   // The least logit that min_p keeps: m + T ln(min_p), rounded up.
@@ -942,15 +955,11 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
     bool found = false;
     float raised = FLT_MAX;  // the cut is known to lie above this logit, and few entries do
     const u64 w_max = r.weigh(m);
-    const float w_m = __ull2float_rn(w_max), top_c = m * c_hi;
     u64 mass_all = 0;  // of the row
-    float mass_f = 0.0f;
+    float mass_f = 0.0f;  // the same, relative to the maximum's
     if (summed && w.fast) {
-      for (int i = 0; i < a.nc; ++i) {
-        const float x = s.cta_sum[i];
-        if (x > 0.0f) mass_f += x * ex2_fast(__fmaf_rn(-m, c_hi, s.cta_far[i]) - m * c_lo);
-      }
-      mass_all = __float2ull_rn(mass_f * w_m);
+      for (int i = 0; i < a.nc; ++i) mass_all += s.cta_sum[i] >> min(exponent(m) - exponent(s.cta_max[i]), 63);
+      mass_f = __fdiv_rn(__ull2float_rn(mass_all), __ull2float_rn(w_max));
     }
     const int top_bin = __float2int_rd(fminf(fmaxf(m * unit, -0x1p30f), 0x1p30f));
     if (K != 1 && w.fast) {
@@ -1080,8 +1089,9 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
       im += above - (hm0 + hm1);
       ic += above_c - (hc0 + hc1);
       const unsigned all_c = above_c + aside;
-      int turn = 0, tier = K ? 2 : 0;  // tier: how well the mass below the window is known (2: exactly)
-      u64 total = mass_all, slack = mass_all >> 21;
+      int turn = 0;
+      bool exact = K != 0;  // the total mass is known exactly
+      u64 total = mass_all, slack = (mass_all >> 22) + (mass_all >> 23) + (unsigned)a.V;  // (a unit a weight, for their rounding)
 #pragma unroll 1
       for (int round = K ? 0 : 1; round < 2; ++round) {
         u64 want = K, want_lo = K;
@@ -1102,10 +1112,10 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
           }
         } else {
           want = part_of(total + slack);
-          want_lo = part_of(total - slack);
+          want_lo = part_of(total - min(slack, total));
           const bool in_sure = above >= want_lo, short_of = all_m < want;
           if (in_sure || short_of) {
-            better = tier < 2 && ((in_sure && above < want) || (floored && short_of && all_m >= want_lo));
+            better = !exact && ((in_sure && above < want) || (floored && short_of && all_m >= want_lo));
             if (!better) {
               found = !in_sure && floored;  // min_p cuts first: all entries of the window are kept
               if (in_sure && above_c <= r.kAside) raised = hi;
@@ -1155,7 +1165,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
           __syncthreads();
           const int how = s.cut_found;
           if (how == 0) break;
-          better = how == 2 && tier < 2;
+          better = how == 2 && !exact;
           if (!better) {
             cut = true;
             total = s.cut_mass;
@@ -1167,18 +1177,13 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
             continue;
           }
         }
-        // The mass below the window again: in fp32 (off by 2^-20 of itself at most), then exactly.
-        u64 rest;
+        // The mass below the window, exactly.
+        u64 rest = r.below(lo);
         unsigned z = 0;
-        if (tier == 0) {
-          rest = __float2ull_rn(r.below_fast(lo, c_hi, c_lo, top_c) * ex2_fast(__fmaf_rn(-m, c_hi, top_c) - m * c_lo) * w_m);
-        } else {
-          rest = r.below(lo);
-        }
         r.sum(rest, z);
         total = all_m + rest;
-        slack = tier == 0 ? rest >> 20 : 0;
-        ++tier;
+        slack = 0;
+        exact = true;
         --round;
       }
     }

@@ -254,3 +254,28 @@ def test_rows_that_their_sample_misjudges(dtype, kind, spread):
     u = rng.random(N).astype(np.float32)
     # (bf16 at 1e-3: few different values and so many equal weights; borders at round numbers of them)
     check(x, u, *settings(N, kind, rng, V), most_near=3)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("V", [4000, 40000])
+def test_mass_in_one_value(dtype, V):
+    """Most of the mass in entries of one value below the cut, so that errors of their weights do not cancel, and a
+    top_p just above or below what the entries above them hold: 2^-24 of it, fp32's step, decides."""
+    N = 64
+    rng = np.random.default_rng(V)
+    g = torch.Generator().manual_seed(V)
+    x = torch.randn(N, 1, generator=g).expand(N, V).clone() - 6.0 - 4.0 * torch.rand(N, 1, generator=g)
+    x[:, 7:V:V // 9] = 4.0 + torch.rand(N, len(range(7, V, V // 9)), generator=g)
+    x = x.to(dtype)
+    T = np.float32(0.5) + rng.random(N).astype(np.float32)
+    w = torch.exp((x.double() - x.double().amax(1, keepdim=True)) / torch.from_numpy(T).double()[:, None])
+    top = w.sort(-1, descending=True).values.cumsum(-1)
+    at = torch.from_numpy(rng.integers(0, 5, N))
+    p = (top.gather(1, at[:, None])[:, 0] / top[:, -1]).float().numpy()
+    p[::2] = np.nextafter(p[::2], np.float32(2))
+    p[1::2] = np.nextafter(p[1::2], np.float32(0))
+    k, m = np.zeros(N, np.int32), np.zeros(N, np.float32)
+    u = rng.random(N).astype(np.float32)
+    u[:8] = np.nextafter(np.float32(1), np.float32(0))
+    # (a margin is below 1e-9 where fp32's neighbour of p comes that close: 2^-23 wide, one in a hundred)
+    check(x.to(DEV), u, T, k, p, m, most_near=6)
