@@ -544,7 +544,9 @@ struct Row {
         const unsigned b = __bfloat16_as_ushort(__float2bfloat16_ru(lo));
         lo2 = b | b << 16;
       }
-      some_tiles<F32 ? 2 : 4>(first, last, 1, [&](int base, const uint32_t (&x)[WORDS]) {
+      // (two tiles of bf16 ahead: 210 us for 512 x 128256 with top-p, 226 with four, whose code is fetched more slowly
+      // than it runs, and 216 with one)
+      some_tiles<F32 ? 1 : 2>(first, last, 1, [&](int base, const uint32_t (&x)[WORDS]) {
         if (!__any_sync(0xffffffffu, top_of(x) >= lo)) return;
         // In the order of ids: fp32's two halves of a tile one behind the other.
         unsigned mask = 0;
@@ -808,7 +810,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
     if ((m - l) * unit < (float)kSampleBins) atomicAdd(&s.sample[__float2int_rd(l * unit) & (kValueBins - 1)], 1u);
   };
   if (summed || (K > 1 && !by_top)) {
-    r.template all_tiles<F32 ? 4 : 8>([&](int base, const uint32_t (&x)[WORDS]) {
+    r.template all_tiles<F32 ? 2 : 4>([&](int base, const uint32_t (&x)[WORDS]) {
       float top;
       if constexpr (F32) {
         top = __uint_as_float(x[0]);
