@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(kThreads) plan_one_kernel(const __grid_constan
 __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ Args a) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   int* ends = a.B <= kThreads ? reinterpret_cast<int*>(a.tok_end) : nullptr;
-  sum_requests(a, ends, ends + a.B, a.pages, a.head);
+  sum_requests(a, ends, ends ? ends + a.B : nullptr, a.pages, a.head);
 }
 
 __global__ void __launch_bounds__(kThreads) fill_short_kernel(const __grid_constant__ Args a) {

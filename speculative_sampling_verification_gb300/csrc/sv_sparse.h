@@ -22,7 +22,6 @@ struct Args {
   unsigned *status, *counters;
   float2* part_ml;  // [items splits][heads]: maximum and sum of a part
   float* part_o;    // [items splits][heads][D]
-  long long num_pages;
   int N, Hq, Hkv, D, P, budget, splits;
   float scale;
 };

@@ -249,11 +249,11 @@ __global__ void __launch_bounds__(kThreads, 4) sparse_decode_kernel(const __grid
         if constexpr (F8) p[i] *= x[u].vs[i >> 1];
       }
       if constexpr (F8) {
-        const bool past = fmaxf(p[0], p[2]) > 256.0f * ref[0] || fmaxf(p[1], p[3]) > 256.0f * ref[1];
+        const bool past = fmaxf(fabsf(p[0]), fabsf(p[2])) > 256.0f * ref[0] || fmaxf(fabsf(p[1]), fabsf(p[3])) > 256.0f * ref[1];
         if (__any_sync(0xffffffffu, past)) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            float t = fmaxf(ref[i], fmaxf(p[i], p[i + 2]));
+            float t = fmaxf(ref[i], fmaxf(fabsf(p[i]), fabsf(p[i + 2])));
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, d));
             if (t < kTiny) t = 0.0f;

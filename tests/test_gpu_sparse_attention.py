@@ -150,6 +150,39 @@ def test_pages_with_nan_are_taken_first():
     assert torch.isnan(out).all()
 
 
+@pytest.mark.parametrize("D,P", [(64, 16), (72, 16), (128, 32)])
+@pytest.mark.parametrize("many", [1, 30])
+def test_scales_never_written_count_as_infinite(D, P, many):
+    cache, bounds, table = make(1, 40, 1, P, D, torch.bfloat16, 8)
+    q = torch.randn(1, 2, D, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).to(DEV)
+    at = table[0, 5:5 + many].long()
+    bounds.scale[at] = torch.inf
+    check(cache, bounds, table, q, [40 * P - 1], [0], 6, 1, 1)
+    pos = torch.tensor([40 * P - 1], dtype=torch.int32, device=DEV)
+    sel = [torch.empty(1, 1, 6, dtype=torch.int32, device=DEV) for _ in range(2)]
+    sv.sparse_attention(q, cache, bounds, table, pos, 6, selected=sel[0])
+    bounds.scale[at] = torch.nan
+    sv.sparse_attention(q, cache, bounds, table, pos, 6, selected=sel[1])
+    assert torch.equal(*sel)
+
+
+@pytest.mark.parametrize("width", [20000, 49152])
+def test_longest_tables(width):
+    """Tables that name pages over and over again: up to 49152 entries, in clusters of 8 and 16 blocks."""
+    cache, bounds, small = make(1, 500, 2, 16, 64, torch.bfloat16, 13)
+    g = torch.Generator().manual_seed(width)
+    table = small[0].cpu()[torch.randint(0, 500, (2, width), generator=g)].contiguous().to(DEV)
+    q = torch.randn(3, 4, 64, generator=g).to(torch.bfloat16).to(DEV)
+    check(cache, bounds, table, q, [16 * width - 1, 16 * width - 100, 5000], [0, 1, 1], 40, 2, 3)
+
+
+def test_negative_value_scales():
+    cache, bounds, table = make(2, 40, 2, 16, 64, F8, 14)
+    cache.v_scale[::2] *= -1
+    q = torch.randn(2, 8, 64, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16).to(DEV)
+    check(cache, bounds, table, q, [639, 300], [0, 1], 12, 1, 1)
+
+
 def test_queries_of_any_size():
     cache, bounds, table = make(1, 50, 2, 16, 64, torch.bfloat16, 9)
     q = torch.randn(1, 8, 64, device=DEV).to(torch.bfloat16)
