@@ -142,8 +142,8 @@ __device__ __noinline__ u64 weight_far(float l, float m, float ih, float il, flo
   return (u64)((long long)__float2ll_rn(e.hi * scale) + __float2ll_rn(e.lo * scale));
 }
 
-SV_DEVINL u64 weight(float l, const Weigh& w, const float2* tab) {
-  if (!w.fast) return weight_far(l, w.m, w.dc.ih, w.il, w.low, w.scale);
+// The weight where w.fast (-inf: 0).
+SV_DEVINL u64 weight_fast(float l, const Weigh& w, const float2* tab) {
   // exp_draw's steps up to head + tail = T.x + lo in [1, 2) times 2^(k >> 10), then in whole numbers: the
   // head's 24 bits and the tail's to 2^-40, twice 2^44 of them, shifted into place and rounded.
   const float x = fmaxf(l, w.lmin);
@@ -156,6 +156,10 @@ SV_DEVINL u64 weight(float l, const Weigh& w, const float2* tab) {
   const unsigned head = (__float_as_uint(T.x) & 0x7fffffu) | 0x800000u;
   const u64 both = (u64)head * (1u << 22) + (u64)((long long)tail * 32);
   return ((both >> min(w.shift - (k >> 10), 63)) + 1) >> 1;
+}
+
+SV_DEVINL u64 weight(float l, const Weigh& w, const float2* tab) {
+  return w.fast ? weight_fast(l, w, tab) : weight_far(l, w.m, w.dc.ih, w.il, w.low, w.scale);
 }
 
 // Eight elements a lane of the tile at `base` of a row, as they are stored (bf16 pairs in the first
@@ -493,10 +497,16 @@ struct Row {
       u64 acc = 0;
       int done = 0;
       some_tiles<2>(first, last, 1, [&](int base, const uint32_t (&x)[WORDS]) {
+        // (one branch for all eight, so that their chains overlap)
+        if (w.fast) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float l = element<F32>(x, e);
-          acc += l > neg_inf() ? weigh(l) : 0;
+          for (int e = 0; e < 8; ++e) acc += weight_fast(element<F32>(x, e), w, s.tab);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float l = element<F32>(x, e);
+            acc += l > neg_inf() ? weigh(l) : 0;
+          }
         }
         if (++done == every) {
           total += acc;
@@ -590,14 +600,15 @@ struct Row {
     return total;
   }
 
-  // The mass of the entries l < lo, exactly (a thread's part).
+  // The mass of the entries l < lo, exactly (a thread's part), where w.fast.
   SV_DEVINL u64 below(float lo) {
     u64 x = 0;
     all_tiles<1>([&](int, const uint32_t (&v)[WORDS]) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float l = element<F32>(v, e);
-        if (l < lo && l > neg_inf()) x += weigh(l);
+        const u64 y = weight_fast(l, w, s.tab);
+        x += l < lo ? y : 0;
       }
     });
     return x;
