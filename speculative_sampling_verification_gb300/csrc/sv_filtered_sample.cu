@@ -35,6 +35,14 @@ typedef unsigned long long u64;
 // sum could change the cut, the mass below the window is summed again, exactly. A window that misses the cut
 // is widened, or begins above its old top where the cut turns out to lie there; a row that still has none, or more
 // entries in its window than there is room for (ties), is halved bit by bit over the keys, a pass for every bit.
+//
+// Few rows are bound by the steps between the passes, each a chain of shared memory, barriers and code fetched for the
+// first time (1 x 32000 with top-k: 21 us, of them 8 for the passes); many rows by issue slots. 512 x 128256
+// bf16 of normal logits (sigma 3, T = 1), 131 MB, 19 us at the copy rate: min_p 0.1 70 us, top_k 50 103, top_p 0.5 (T =
+// 0.6) 107, top_p 0.9 200, no setting 136 (every entry weighed to 2^-44).
+// A row is shared by as many CTAs as one wave of four an SM holds, then by one for 65536 entries (32768 of fp32):
+// with twice as many 512 rows took 234 us against 224 and, with top-k, 126 against 109: what a CTA does between the
+// passes is the larger part.
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;

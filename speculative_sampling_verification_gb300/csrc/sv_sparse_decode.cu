@@ -32,6 +32,10 @@ namespace dec {
 // fp16 relative to its largest value (2^-25 of that at most), and a weight times its value's scale is fp16
 // raised so that the largest is near
 // fp16's largest (2^-11 of itself, or 2^-32 of the largest).
+// 32 rows of 32/8 heads of 128: 75 us alone for 393 MB of bf16 (5.2 TB/s, DRAM 66 % active), 57 us for 204 MB of e4m3
+// (3.6 TB/s; its conversions come between a warp's loads). On the kernel for trees of few rows, with 128-wide products of
+// which 4 columns are used, a whole call took 97 (bf16) and 94 us (e4m3), where it was 91 and 78 with this one; 36 rows
+// of 64/8 heads 84 and 75, one row of 131072 keys 41 and 32.
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
