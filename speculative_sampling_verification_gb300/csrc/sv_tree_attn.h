@@ -35,7 +35,7 @@ __device__ __forceinline__ long long table_row(const Args& a, int b, int hk) {
 
 bool sizes_ok(int B, int T, int Hq, int Hkv, int D, int max_pages, int page_size);
 
-// Workspace words that must be 0 when the kernels of these sizes start; 0 for sizes
+// Workspace words that must be 0 when the kernels of these sizes start; 1 for sizes
 // whose kernel needs the status word alone.
 size_t cleared_words(int T, int Hq, int Hkv, int D, int page_size);
 
