@@ -373,6 +373,7 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : 4) select_kernel(
   const int h = (int)(item % a.Hkv);
   const long long n = item / a.Hkv;
   const int G = a.Hq / a.Hkv;
+  const int pos = a.positions[n], seq = a.seqs ? a.seqs[n] : (int)n;  // (under way during the codes)
   if (blockIdx.x == 0) {
     for (int i = tid; i < a.clear_words; i += THREADS) a.clear[i] = 0;
     for (int i = tid; i < a.clear2_words; i += THREADS) a.clear2[i] = 0;
@@ -403,9 +404,8 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : 4) select_kernel(
       if (lane == 0) qscale[j] = fin ? __fdiv_rn(top, kCodeMax) : 0.0f;
     }
   };
-  codes_of(0);  // (nothing it needs has to be looked up first)
+  codes_of(0);  // (nothing else it needs has to be looked up)
 
-  const int pos = a.positions[n], seq = a.seqs ? a.seqs[n] : (int)n;
   const bool empty = pos == -1 || seq == -1;
   bool fault = !empty && (pos < 0 || (long long)pos >= (long long)a.max_pages * a.P || seq < 0 || seq >= a.B);
   const int np = empty || fault ? 0 : pos / a.P + 1;

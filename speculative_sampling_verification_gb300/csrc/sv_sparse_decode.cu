@@ -26,14 +26,14 @@ namespace dec {
 //     makes pairs of keys of them; the rows of a tile are whatever channels the lanes hold.
 //     P goes from S's layout to B's by an 8 x 8 transposition each.
 // There is little to compute for what is read (16 products a block of 16 keys), so that warps with all their loads
-// under way are what counts: 12 or more a SM, 8 KB each. A running maximum per head moves only when a score
+// under way are what counts: 12 or more a SM, 8 KB each (codes: 4). A running maximum per head moves only when a score
 // exceeds it by more than 2^8, so that most blocks need one vote; a row's sum stays per lane until
 // the end. bf16 caches: P is rounded to bf16 (2^-8 of each weight). e4m3 caches: codes become fp16 (exact), q is
 // fp16 relative to its largest value (2^-25 of that at most), and a weight times its value's scale is fp16
 // raised so that the largest is near
 // fp16's largest (2^-11 of itself, or 2^-32 of the largest).
-// 32 rows of 32/8 heads of 128: 75 us alone for 393 MB of bf16 (5.2 TB/s, DRAM 66 % active), 57 us for 204 MB of e4m3
-// (3.6 TB/s; its conversions come between a warp's loads). On the kernel for trees of few rows, with 128-wide products of
+// 32 rows of 32/8 heads of 128: 73 us alone for 393 MB of bf16 (5.4 TB/s, DRAM 68 % active), 50 us for 204 MB of e4m3
+// (4.1 TB/s; its conversions come between a warp's loads). On the kernel for trees of few rows, with 128-wide products of
 // which 4 columns are used, a whole call took 97 (bf16) and 94 us (e4m3), where it was 91 and 78 with this one; 36 rows
 // of 64/8 heads 84 and 75, one row of 131072 keys 41 and 32.
 
@@ -136,7 +136,7 @@ SV_DEVINL void load_block(Block<D, F8>& x, const Args& a, long long row0, int le
 template <int D, bool F8>
 __global__ void __launch_bounds__(kThreads, 4) sparse_decode_kernel(const __grid_constant__ Args a) {
   using B = Block<D, F8>;
-  constexpr int STEPS = D / 16, U = F8 ? 2 : 1;
+  constexpr int STEPS = D / 16;
   __shared__ float so[kWarps][8][D];
   __shared__ float sm[kWarps][8], smv[kWarps][8], sl[kWarps][8];
   __shared__ int last;
@@ -192,96 +192,92 @@ __global__ void __launch_bounds__(kThreads, 4) sparse_decode_kernel(const __grid
   float o[D / 16][4] = {};
   float m[2] = {kNone, kNone}, l[2] = {0.0f, 0.0f};    // heads 2c, 2c + 1
   float ref[2] = {0.0f, 0.0f}, inv[2] = {0.0f, 0.0f};  // what a weight times its scale is relative to (e4m3)
+  // The next block's page is looked up while one is worked on (32 rows of bf16 83 us with it, 86 without). One block at a
+  // time: with two of e4m3 32 rows took 76 us, against 70, since their registers spill; so they do with the next
+  // block's loads under way (74). Prefetching its lines to L2 was slower too (bf16 87, e4m3 73).
+  auto page_of = [&](int b) { return __ldcg(table + min(b, b1 - 1) / per_page); };
+  int id = page_of(b0 + warp);
 #pragma unroll 1
-  for (int bb = b0 + warp * U; bb < b1; bb += kWarps * U) {
-    B x[U];
+  for (int b = b0 + warp; b < b1; b += kWarps) {
+    const int left = keys - b * 16;
+    B x;
+    load_block<D, F8>(x, a, ((long long)id * a.Hkv + h) * a.P + (b % per_page) * 16, left, lane);
+    id = page_of(b + kWarps);
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int b = min(bb + u, b1 - 1);
-      const int id = __ldcg(table + b / per_page);
-      const long long row0 = ((long long)id * a.Hkv + h) * a.P + (b % per_page) * 16;
-      load_block<D, F8>(x[u], a, row0, bb + u < b1 ? keys - b * 16 : 0, lane);
+    for (int t = 0; t < STEPS; ++t) {
+      uint32_t f[4];
+      if constexpr (F8) {
+        // Step t: words t and half of a word each.
+        f[0] = codes_f16(x.k[0][t], 0), f[1] = codes_f16(x.k[1][t], 0);
+        f[2] = codes_f16(x.k[0][t], 1), f[3] = codes_f16(x.k[1][t], 1);
+      } else {
+        f[0] = x.k[0][2 * t], f[1] = x.k[1][2 * t], f[2] = x.k[0][2 * t + 1], f[3] = x.k[1][2 * t + 1];
+      }
+      mma<F8>(s, f, q[t][0], q[t][1]);
     }
+    // Scores in powers of two: s[0], s[1] of key g, s[2], s[3] of key g + 8.
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (U > 1 && bb + u >= b1) break;
-      const int left = keys - (bb + u) * 16;
-      float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i = 0; i < 4; ++i) {
+      s[i] *= F8 ? qscale[i & 1] * x.ks[i >> 1] : qscale[i & 1];
+      if (g + 8 * (i >> 1) >= left) s[i] = -INFINITY;
+    }
+    const bool grows = s[0] > m[0] + kLazy || s[2] > m[0] + kLazy || s[1] > m[1] + kLazy || s[3] > m[1] + kLazy;
+    if (__any_sync(0xffffffffu, grows)) {
 #pragma unroll
-      for (int t = 0; t < STEPS; ++t) {
-        uint32_t f[4];
+      for (int i = 0; i < 2; ++i) {
+        float t = fmaxf(m[i], fmaxf(s[i], s[i + 2]));
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, d));
+        const float f = ex2_fast(m[i] - t);
+        l[i] *= f;
         if constexpr (F8) {
-          // Step t: words t and half of a word each.
-          f[0] = codes_f16(x[u].k[0][t], 0), f[1] = codes_f16(x[u].k[1][t], 0);
-          f[2] = codes_f16(x[u].k[0][t], 1), f[3] = codes_f16(x[u].k[1][t], 1);
+          ref[i] *= f;  // O stays: its reference is what shrinks
+          if (ref[i] < kTiny) ref[i] = 0.0f;
+          inv[i] = ref[i] > 0.0f ? __fdiv_rn(kRaise, ref[i]) : 0.0f;
         } else {
-          f[0] = x[u].k[0][2 * t], f[1] = x[u].k[1][2 * t], f[2] = x[u].k[0][2 * t + 1], f[3] = x[u].k[1][2 * t + 1];
-        }
-        mma<F8>(s, f, q[t][0], q[t][1]);
-      }
-      // Scores in powers of two: s[0], s[1] of key g, s[2], s[3] of key g + 8.
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        s[i] *= F8 ? qscale[i & 1] * x[u].ks[i >> 1] : qscale[i & 1];
-        if (g + 8 * (i >> 1) >= left) s[i] = -INFINITY;
+          for (int t2 = 0; t2 < D / 16; ++t2) o[t2][i] *= f, o[t2][i + 2] *= f;
+        }
+        m[i] = t;
       }
-      const bool grows = s[0] > m[0] + kLazy || s[2] > m[0] + kLazy || s[1] > m[1] + kLazy || s[3] > m[1] + kLazy;
-      if (__any_sync(0xffffffffu, grows)) {
+    }
+    float p[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      p[i] = ex2_fast(s[i] - m[i & 1]);
+      l[i & 1] += p[i];
+      if constexpr (F8) p[i] *= x.vs[i >> 1];
+    }
+    if constexpr (F8) {
+      const bool past = fmaxf(fabsf(p[0]), fabsf(p[2])) > 256.0f * ref[0] || fmaxf(fabsf(p[1]), fabsf(p[3])) > 256.0f * ref[1];
+      if (__any_sync(0xffffffffu, past)) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          float t = fmaxf(m[i], fmaxf(s[i], s[i + 2]));
+          float t = fmaxf(ref[i], fmaxf(fabsf(p[i]), fabsf(p[i + 2])));
 #pragma unroll
           for (int d = 4; d < 32; d <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, d));
-          const float f = ex2_fast(m[i] - t);
-          l[i] *= f;
-          if constexpr (F8) {
-            ref[i] *= f;  // O stays: its reference is what shrinks
-            if (ref[i] < kTiny) ref[i] = 0.0f;
-            inv[i] = ref[i] > 0.0f ? __fdiv_rn(kRaise, ref[i]) : 0.0f;
-          } else {
+          if (t < kTiny) t = 0.0f;
+          inv[i] = t > 0.0f ? __fdiv_rn(kRaise, t) : 0.0f;
+          const float f = ref[i] * inv[i] * (1.0f / kRaise);
 #pragma unroll
-            for (int t2 = 0; t2 < D / 16; ++t2) o[t2][i] *= f, o[t2][i + 2] *= f;
-          }
-          m[i] = t;
+          for (int t2 = 0; t2 < D / 16; ++t2) o[t2][i] *= f, o[t2][i + 2] *= f;
+          ref[i] = t;
         }
       }
-      float p[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        p[i] = ex2_fast(s[i] - m[i & 1]);
-        l[i & 1] += p[i];
-        if constexpr (F8) p[i] *= x[u].vs[i >> 1];
-      }
-      if constexpr (F8) {
-        const bool past = fmaxf(fabsf(p[0]), fabsf(p[2])) > 256.0f * ref[0] || fmaxf(fabsf(p[1]), fabsf(p[3])) > 256.0f * ref[1];
-        if (__any_sync(0xffffffffu, past)) {
+      for (int i = 0; i < 4; ++i) p[i] *= inv[i & 1];
+    }
+    const uint32_t p0 = transpose8(F8 ? pack_f16(p[0], p[1]) : pack_bf16(p[0], p[1]));
+    const uint32_t p1 = transpose8(F8 ? pack_f16(p[2], p[3]) : pack_bf16(p[2], p[3]));
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float t = fmaxf(ref[i], fmaxf(fabsf(p[i]), fabsf(p[i + 2])));
+    for (int t = 0; t < D / 16; ++t) {
+      uint32_t w[4];
 #pragma unroll
-            for (int d = 4; d < 32; d <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, d));
-            if (t < kTiny) t = 0.0f;
-            inv[i] = t > 0.0f ? __fdiv_rn(kRaise, t) : 0.0f;
-            const float f = ref[i] * inv[i] * (1.0f / kRaise);
-#pragma unroll
-            for (int t2 = 0; t2 < D / 16; ++t2) o[t2][i] *= f, o[t2][i + 2] *= f;
-            ref[i] = t;
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) p[i] *= inv[i & 1];
-      }
-      const uint32_t p0 = transpose8(F8 ? pack_f16(p[0], p[1]) : pack_bf16(p[0], p[1]));
-      const uint32_t p1 = transpose8(F8 ? pack_f16(p[2], p[3]) : pack_bf16(p[2], p[3]));
-#pragma unroll
-      for (int t = 0; t < D / 16; ++t) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = F8 ? codes_f16(x[u].v[i][t / 2], t & 1) : x[u].v[i][t];
-        const uint32_t f[4] = {__byte_perm(w[0], w[1], 0x5410), __byte_perm(w[0], w[1], 0x7632),
-                               __byte_perm(w[2], w[3], 0x5410), __byte_perm(w[2], w[3], 0x7632)};
-        mma<F8>(o[t], f, p0, p1);
-      }
+      for (int i = 0; i < 4; ++i) w[i] = F8 ? codes_f16(x.v[i][t / 2], t & 1) : x.v[i][t];
+      const uint32_t f[4] = {__byte_perm(w[0], w[1], 0x5410), __byte_perm(w[0], w[1], 0x7632),
+                             __byte_perm(w[2], w[3], 0x5410), __byte_perm(w[2], w[3], 0x7632)};
+      mma<F8>(o[t], f, p0, p1);
     }
   }
 
