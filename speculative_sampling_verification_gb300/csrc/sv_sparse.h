@@ -33,7 +33,7 @@ inline bool takes(int heads, int D, int page_size) {
 }
 
 // CTAs of an item: one wave in all (four a SM), but no fewer than 128 keys a CTA. Measured, us of a call with 608 / 912 /
-// 1216 / 1824 CTAs wanted: 32 rows of 8 heads and 48 pages of 64, bf16 85 / 88 / 88 / 95, e4m3 75 / 78 / 77 / 86; 36 rows
+// 1216 / 1824 CTAs wanted (pages not yet looked up ahead): 32 rows of 8 heads and 48 pages of 64, bf16 85 / 88 / 88 / 95, e4m3 75 / 78 / 77 / 86; 36 rows
 // of 32 pages 66 / 73 / 73 / 86: what a CTA does before and after its keys costs more than uneven lengths.
 inline int splits_of(long long items, int budget, int page_size) {
   const long long keys = (long long)budget * page_size;
