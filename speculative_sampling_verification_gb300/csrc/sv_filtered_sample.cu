@@ -112,6 +112,8 @@ struct Shared {
   int recs[kWarps];
   u64 wsum[2][kWarps];
   unsigned wcnt[2][kWarps], wmore[2][kWarps];
+  u64 bins_sum[kWarps];  // the window's bins, a warp's
+  unsigned bins_cnt[kWarps];
   u64 inbox[2][kMaxCluster];
   unsigned inbox_c[2][kMaxCluster], inbox_d[2][kMaxCluster];
   u64 tile_sum[kWarps], hit_start;
@@ -395,7 +397,9 @@ struct Row {
   }
   SV_DEVINL u64 weigh(float l) const { return weight(l, w, s.tab); }
 
-  // Sums over the row's CTAs, the same in every thread. Each CTA's are left in the inboxes of `turn`.
+  // Sums over the row's CTAs, the same in every thread. Each CTA's are left in the inboxes of `turn`: another CTA
+  // writes them again two sums later, so that the barrier of the sum between says that they have been read.
+  // Nothing else may advance `turn`.
   SV_DEVINL void sum(u64& x, unsigned& c, unsigned& d) {
     const int t = turn & 1, ln = lane(), wp = threadIdx.x >> 5;
     ++turn;
@@ -1097,15 +1101,14 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
         }
       u64 im = scan_up(hm0 + hm1, lane), all_m = above;
       unsigned ic = scan_up(hc0 + hc1, lane);
-      const int t = r.turn & 1;
-      ++r.turn;
-      if (lane == 31) s.wsum[t][warp] = im, s.wcnt[t][warp] = ic;
+      // (in words of its own, beside the row's sums: those change inboxes, a barrier of all CTAs from one to the next)
+      if (lane == 31) s.bins_sum[warp] = im, s.bins_cnt[warp] = ic;
       if (tid == 0) s.bin = -1;
       __syncthreads();
 #pragma unroll
       for (int i = 0; i < kWarps; ++i) {
-        if (i < warp) im += s.wsum[t][i], ic += s.wcnt[t][i];
-        all_m += s.wsum[t][i];
+        if (i < warp) im += s.bins_sum[i], ic += s.bins_cnt[i];
+        all_m += s.bins_sum[i];
       }
       im += above - (hm0 + hm1);
       ic += above_c - (hc0 + hc1);
