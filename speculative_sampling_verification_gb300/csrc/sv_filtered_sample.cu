@@ -139,6 +139,8 @@ SV_DEVINL unsigned ordered(float f) {
   return b ^ ((unsigned)((int)b >> 31) | 0x80000000u);
 }
 SV_DEVINL float unordered(unsigned k) { return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k); }
+// The largest value that compares below x: for -FLT_MAX -inf, and for zeros (of either sign) the first below both.
+SV_DEVINL float just_below(float x) { return unordered(min(ordered(x) - 1u, x == 0.0f ? 0x7ffffffeu : 0xffffffffu)); }
 
 // The weight for rows whose maximum is too far from 0 for the short exponential.
 __device__ __noinline__ u64 weight_far(float l, float m, float ih, float il, float low, float scale) {
@@ -972,7 +974,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
   u64 sum = 0;       // a thread's part of the kept mass in the records
   unsigned sure = 0; // entries in them
   bool cut = false;  // s.cut_key and s.cut_id say what is kept of the entries set aside
-  float lo = floor_l, hi = floor_l > -FLT_MAX ? unordered(ordered(floor_l) - 1u) : -FLT_MAX;
+  float lo = floor_l, hi = just_below(floor_l);
 
   if (!K && !by_p) {
     sum = r.pass(lo, hi, false, !by_m, 0.0f, 0.0f, sure);
@@ -1066,7 +1068,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
       const bool floored = !(K && by_p) && floor_l >= lo;  // min_p cuts above the window's end
       if (floored) {
         lo = floor_l;
-        hi = fmaxf(hi, unordered(ordered(floor_l) - 1u));
+        hi = fmaxf(hi, just_below(floor_l));
       }
       if (attempt > 0) {
         r.sync();  // (what the last attempt left has been read)

@@ -44,3 +44,47 @@ def test_blocks_of_a_row_agree_without_candidates(dtype, how):
             for _ in range(200)]
     tokens, probs = torch.stack([o[0] for o in outs]).cpu().numpy(), torch.stack([o[1] for o in outs]).cpu().numpy()
     assert (tokens == first[0]).all() and (probs == first[1]).all()
+
+
+def sentinels(N):
+    return dict(out=torch.full((N,), -77, dtype=torch.int32, device=DEV), prob=torch.full((N,), -7.0, device=DEV),
+                status=torch.zeros(1, dtype=torch.int32, device=DEV))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("V", [1, 5, 1000, 70001])
+@pytest.mark.parametrize("row", ["zeros", "signed_zeros", "largest_is_0", "largest_is_-0", "lowest", "one_lowest"])
+@pytest.mark.parametrize("extra", ["", "top_p", "top_k"])
+def test_min_p_of_1_keeps_what_equals_the_largest(dtype, V, row, extra):
+    """Equal weights: the token is the kept entry floor(u n), its probability 1 / n. Largest logits of zero and of the
+    type's lowest value, for which nothing, or only -inf, lies below the least kept value."""
+    N = 4
+    lowest = torch.finfo(dtype).min
+    g = torch.Generator().manual_seed(V)
+    keep = torch.rand(V, generator=g) < 0.5
+    keep[V // 2] = True
+    if row == "zeros":
+        x, keep = torch.zeros(V), torch.ones(V, dtype=torch.bool)
+    elif row == "signed_zeros":
+        x, keep = torch.where(keep, 0.0, -0.0), torch.ones(V, dtype=torch.bool)
+    elif row in ("largest_is_0", "largest_is_-0"):
+        x = torch.where(keep, 0.0 if row == "largest_is_0" else -0.0, -torch.rand(V, generator=g) - 1e-3)
+    elif row == "lowest":
+        x, keep = torch.full((V,), lowest), torch.ones(V, dtype=torch.bool)
+    else:
+        x = torch.where(keep, lowest, -torch.inf)
+    ids = keep.nonzero()[:, 0].numpy()
+    n = len(ids)
+    # (uniforms that stay clear of the borders i / n)
+    want = [0, int(0.3 * n), int(0.87 * n), n - 1]
+    u = torch.tensor([0.0, *(((w + 0.5) / n) for w in want[1:3]), 1.0], device=DEV)
+    s = sentinels(N)
+    more = {"top_p": dict(top_p=0.9999), "top_k": dict(top_k=n)}.get(extra, {})
+    sv.filtered_sample(x.expand(N, V).to(dtype).to(DEV), u, 1.0, min_p=1.0, **s, **more)
+    tokens, probs = s["out"].tolist(), s["prob"].tolist()
+    if extra == "top_p" and n > 1000:
+        # (how many of the equal entries top_p takes of so many is its own affair)
+        assert tokens[0] == ids[0] and min(tokens) >= 0 and int(s["status"]) == 0
+        return
+    assert tokens == [int(ids[w]) for w in want]
+    assert all(abs(p - 1.0 / n) <= (2.0 ** -24 + 1e-10) / n for p in probs) and int(s["status"]) == 0
