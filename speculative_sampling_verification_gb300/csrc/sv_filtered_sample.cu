@@ -130,7 +130,7 @@ struct Shared {
   unsigned cut_key;
   int cut_id, cut_found;
   u64 cut_mass;
-  float log_hi, log_lo;  // T ln(min_p)
+  float log_hi, log_lo;  // T ln(min_p), times log_unit
   Weigh w;
 };
 
@@ -775,8 +775,10 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
     c_hi = next_down(c.hi);
     c_lo = fmaxf((c.hi - c_hi) + c.lo, 1e-37f);
   }
+  const bool hot = T > 0x1p100f;  // (T ln(min_p) can be 103 times fp32's largest: a 256th of it, then)
+  const float log_unit = hot ? 0x1p-8f : 1.0f;
   if (by_m && warp == kWarps - 1) {  // one warp, since it is fp64
-    const double x = (double)T * log((double)min_p);
+    const double x = (double)T * log((double)min_p) * log_unit;
     if (lane == 0) {
       s.log_hi = (float)x;
       s.log_lo = (float)(x - (double)(float)x);
@@ -960,12 +962,12 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
   // The least logit that min_p keeps: m + T ln(min_p), rounded up.
   float floor_l = -FLT_MAX;
   if (by_m) {
-    const ff x = two_sum(m, s.log_hi);
+    const ff x = two_sum(m * log_unit, s.log_hi);
     const ff y = fast_two_sum(x.hi, x.lo + s.log_lo);
     floor_l = y.hi;
     if (y.lo > 0.0f) floor_l = __uint_as_float(__float_as_uint(y.hi) + (y.hi >= 0.0f ? 1 : -1));
     if (y.hi == 0.0f && y.lo > 0.0f) floor_l = y.lo;
-    floor_l = fmaxf(fminf(floor_l, m), -FLT_MAX);
+    floor_l = fmaxf(fminf(hot ? floor_l * 0x1p8f : floor_l, m), -FLT_MAX);
   }
   const u64 part = by_p ? fraction(top_p) : 0;
   // The least whole mass that is top_p of `total` or more.

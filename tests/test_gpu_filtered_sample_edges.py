@@ -88,3 +88,26 @@ def test_min_p_of_1_keeps_what_equals_the_largest(dtype, V, row, extra):
         return
     assert tokens == [int(ids[w]) for w in want]
     assert all(abs(p - 1.0 / n) <= (2.0 ** -24 + 1e-10) / n for p in probs) and int(s["status"]) == 0
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T", [1e20, 1e31, 1e37, 1e38, 3.4e38])
+@pytest.mark.parametrize("min_p", [0.5, 1e-2, 1e-20, 1e-44])
+def test_min_p_at_high_temperatures(dtype, T, min_p):
+    """All weights are 1 but those of entries that are as far below as T is high: min_p keeps what reaches it, also where
+    T ln(min_p) is no fp32 number."""
+    N, V = 4, 3001
+    x = torch.randn(V, generator=torch.Generator().manual_seed(3))
+    low = torch.finfo(dtype).min
+    at = torch.arange(V) % 3 == 1
+    x[at] = low
+    f = np.float32
+    keep = ~at | bool(np.exp(low / float(f(T))) >= float(f(min_p)))  # (no weight comes near min_p)
+    w = np.where(at, np.exp(low / float(f(T))), 1.0) * keep.numpy()
+    cdf = np.cumsum(w)
+    want = [0, int(np.searchsorted(cdf, 0.4 * cdf[-1])), int(np.searchsorted(cdf, 0.9 * cdf[-1])), V - 1]
+    u = [0.0, (cdf[want[1]] - 0.5 * w[want[1]]) / cdf[-1], (cdf[want[2]] - 0.5 * w[want[2]]) / cdf[-1], 1.0]
+    s = sentinels(N)
+    u = torch.tensor(u, dtype=torch.float32, device=DEV)
+    sv.filtered_sample(x.expand(N, V).to(dtype).to(DEV), u, T, min_p=min_p, **s)
+    assert s["out"].tolist() == want and int(s["status"]) == 0
