@@ -616,7 +616,8 @@ int sv_page_bounds(const void* k_cache, const float* k_scale, int64_t num_pages,
                    const int32_t* page_table, const int32_t* ctx_lens, const int32_t* new_lens, int B, int Hkv,
                    int D, int max_pages, int8_t* codes, float* scale, uint32_t* status, void* stream);
 
-/* Bytes of device workspace sv_sparse_attention needs; 0 for invalid sizes. Pure host function. */
+/* Bytes of device workspace sv_sparse_attention needs; 0 for invalid sizes. No less for more rows, so that
+ * a workspace for a batch serves smaller ones. Pure host function. */
 size_t sv_sparse_attention_workspace_size(int N, int Hq, int Hkv, int D, int max_pages, int page_size, int budget);
 
 /* Attention of N query rows over selected pages of their sequences. Row n stands at

@@ -41,6 +41,13 @@ inline int splits_of(long long items, int budget, int page_size) {
   return (int)std::max(1ll, std::min({want, keys / 128, 64ll}));
 }
 
+// Room for parts (items times splits): the most that any number of items up to this one has, since fewer items are split
+// further. A workspace for a batch then serves every smaller one.
+inline long long most_parts(long long items, int budget, int page_size) {
+  const long long keys = (long long)budget * page_size;
+  return std::min(std::max(608ll, items), items * std::max(1ll, std::min(keys / 128, 64ll)));
+}
+
 // Enqueues the attention behind the selection, whose kernel clears the counters and the status word.
 int launch(const Args& a, int cache_dtype, cudaStream_t st);
 

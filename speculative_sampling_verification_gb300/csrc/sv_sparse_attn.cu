@@ -722,7 +722,7 @@ Layout make_layout(int N, int Hq, int Hkv, int D, int page_size, int budget) {
   // For the few-rows kernel: parts of an item that have arrived, and their results.
   if (dec::takes(Hq / Hkv, D, page_size)) {
     L.splits = dec::splits_of((long long)N * Hkv, budget, page_size);
-    const size_t parts = (size_t)N * Hkv * L.splits * (Hq / Hkv);
+    const size_t parts = (size_t)dec::most_parts((long long)N * Hkv, budget, page_size) * (Hq / Hkv);
     L.off_counters = off;
     off = align_up(off + (size_t)N * Hkv * 4, 256);
     L.off_ml = off;
