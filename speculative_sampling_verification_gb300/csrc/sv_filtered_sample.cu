@@ -71,13 +71,14 @@ struct Args {
   unsigned* status;
 };
 
-// What a row's weights are made of: w(l) = exp((l - m)/T) times a power of two, as a whole
-// number of 2^-scale_bits.
+// What a row's weights are made of: w(l) = exp((l - m)/T) times a power of two, as a whole number of
+// 2^-scale_bits. The exponential takes l `unit` + `off` as its argument, whose temperature T `unit` lies in [1, 4) (below only
+// where T is subnormal). off is 0 where |m/T| < 1386. Elsewhere it is -m unit: the entries that then weigh anything lie
+// within 88 T of m, hence within a factor of two of it, and l - m is exact.
 struct Weigh {
-  bool fast;
   int shift;  // of a weight's 45 bits at k >> 10 = 0
   DrawConst dc;
-  float il, m, lmin, low, scale;
+  float unit, off, lmin;
 };
 
 // A listed entry: value and place in the CTA's share; a bf16 value and 16 bits of place where those do.
@@ -142,23 +143,11 @@ SV_DEVINL float unordered(unsigned k) { return __uint_as_float(k & 0x80000000u ?
 // The largest value that compares below x: for -FLT_MAX -inf, and for zeros (of either sign) the first below both.
 SV_DEVINL float just_below(float x) { return unordered(min(ordered(x) - 1u, x == 0.0f ? 0x7ffffffeu : 0xffffffffu)); }
 
-// The weight for rows whose maximum is too far from 0 for the short exponential.
-__device__ __noinline__ u64 weight_far(float l, float m, float ih, float il, float low, float scale) {
-  const ff d = two_sum(l, -m);
-  ff e{1.0f, 0.0f};
-  if (d.hi != 0.0f) {
-    if (!(d.hi > low)) return 0;
-    const ff p = two_prod(d.hi, ih);
-    e = exp_ff(p.hi, __fmaf_rn(d.hi, il, __fmaf_rn(d.lo, ih, p.lo)), kSvExp2Table);
-  }
-  return (u64)((long long)__float2ll_rn(e.hi * scale) + __float2ll_rn(e.lo * scale));
-}
-
-// The weight where w.fast (-inf: 0).
-SV_DEVINL u64 weight_fast(float l, const Weigh& w, const float2* tab) {
+// The weight of l (-inf: 0).
+SV_DEVINL u64 weight(float l, const Weigh& w, const float2* tab) {
   // exp_draw's steps up to head + tail = T.x + lo in [1, 2) times 2^(k >> 10), then in whole numbers: the
   // head's 24 bits and the tail's to 2^-40, twice 2^44 of them, shifted into place and rounded.
-  const float x = fmaxf(l, w.lmin);
+  const float x = fmaxf(__fmaf_rn(l, w.unit, w.off), w.lmin);
   const float ym = __fmaf_rn(x, -w.dc.inv, kRoundMagic), nkf = __fsub_rn(ym, kRoundMagic);
   const float sv = __fmaf_rn(__fmaf_rn(nkf, w.dc.ch, x), w.dc.ih, __fmul_rn(nkf, w.dc.cli));
   const float u = __fmaf_rn(sv, __fmul_rn(__fmaf_rn(sv, 1.0f / 6.0f, 0.5f), sv), sv);
@@ -168,10 +157,6 @@ SV_DEVINL u64 weight_fast(float l, const Weigh& w, const float2* tab) {
   const unsigned head = (__float_as_uint(T.x) & 0x7fffffu) | 0x800000u;
   const u64 both = (u64)head * (1u << 22) + (u64)((long long)tail * 32);
   return ((both >> min(w.shift - (k >> 10), 63)) + 1) >> 1;
-}
-
-SV_DEVINL u64 weight(float l, const Weigh& w, const float2* tab) {
-  return w.fast ? weight_fast(l, w, tab) : weight_far(l, w.m, w.dc.ih, w.il, w.low, w.scale);
 }
 
 // Eight elements a lane of the tile at `base` of a row, as they are stored (bf16 pairs in the first
@@ -511,17 +496,8 @@ struct Row {
       u64 acc = 0;
       int done = 0;
       some_tiles<2>(first, last, 1, [&](int base, const uint32_t (&x)[WORDS]) {
-        // (one branch for all eight, so that their chains overlap)
-        if (w.fast) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) acc += weight_fast(element<F32>(x, e), w, s.tab);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float l = element<F32>(x, e);
-            acc += l > neg_inf() ? weigh(l) : 0;
-          }
-        }
+        for (int e = 0; e < 8; ++e) acc += weigh(element<F32>(x, e));
         if (++done == every) {
           total += acc;
           record(recs, acc, base + kTile);
@@ -614,14 +590,14 @@ struct Row {
     return total;
   }
 
-  // The mass of the entries l < lo, exactly (a thread's part), where w.fast.
+  // The mass of the entries l < lo, exactly (a thread's part).
   SV_DEVINL u64 below(float lo) {
     u64 x = 0;
     all_tiles<1>([&](int, const uint32_t (&v)[WORDS]) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float l = element<F32>(v, e);
-        const u64 y = weight_fast(l, w, s.tab);
+        const u64 y = weigh(l);
         x += l < lo ? y : 0;
       }
     });
@@ -760,20 +736,20 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
 
   // Constants of T, in float-floats (fp64 takes longer here than the row).
   float c_hi, c_lo;  // log2(e) / T; c_hi is rounded down and c_lo above 0, so that -inf stays -inf
+  const float Tf = T > 0.0f ? T : 1.0f;
   {
-    const float Tf = T > 0.0f ? T : 1.0f, ih = __fdiv_rn(1.0f, Tf);
+    w.unit = __int_as_float(max(254 - (__float_as_int(Tf) >> 23 & 0xff), 1) << 23);
+    const float Tu = Tf * w.unit, ih = __fdiv_rn(1.0f, Tu), il = __fmaf_rn(-ih, Tu, 1.0f) * ih;
     w.dc.ih = ih;
-    w.il = __fmaf_rn(-ih, Tf, 1.0f) * ih;
-    const ff C = ff_mul_f(ff{0x1.62e43p-11f, -0x1.05c61p-39f}, Tf);  // T ln2/1024
+    const ff C = ff_mul_f(ff{0x1.62e43p-11f, -0x1.05c61p-39f}, Tu);  // T ln2/1024
     w.dc.ch = C.hi;
     w.dc.cli = C.lo * ih;
     w.dc.inv = __fdiv_rn(1.0f, C.hi);
-    w.lmin = -2048.0f * Tf;
-    w.low = -88.0f * Tf;
-    w.scale = __int_as_float((127 + a.scale_bits) << 23);
-    const ff c = ff_mul(ff{0x1.715476p+0f, 0x1.4ae0c0p-26f}, ff{ih, w.il});
+    w.lmin = -2048.0f * Tu;
+    const ff c = ff_mul(ff{0x1.715476p+0f, 0x1.4ae0c0p-26f}, ff{ih, il});
     c_hi = next_down(c.hi);
-    c_lo = fmaxf((c.hi - c_hi) + c.lo, 1e-37f);
+    c_lo = fmaxf(((c.hi - c_hi) + c.lo) * w.unit, 1e-37f);
+    c_hi = fminf(c_hi * w.unit, 0x1p120f);
   }
   const bool hot = T > 0x1p100f;  // (T ln(min_p) can be 103 times fp32's largest: a 256th of it, then)
   const float log_unit = hot ? 0x1p-8f : 1.0f;
@@ -814,7 +790,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
   // 1.46e-7 at most (every argument tried), and the roundings of f by 2.1e-8. Eight are added in three steps
   // (2^-24 each) and then in float-floats: the sum is good to 3.5e-7, whatever the entries are (measured: 1.7e-7 at
   // most, 1e-8 for normal logits). far is a thread's maximum so far; entries below lmin count as lmin (2^-101).
-  const float reach = -1480.0f * (T > 0.0f ? T : 1.0f);  // no entry as low as this counts in a row with `fast` weights
+  const float reach = -1480.0f * Tf;  // no entry as low as this counts in a row whose sum is used
   float ref = reach, lmin = 1.0475f * reach, far = rintf(reach * c_hi), magic = kRoundMagic - far;
   uint32_t lmin2 = 0;  // the same, two bf16
   if constexpr (!F32) lmin2 = __bfloat16_as_ushort(__float2bfloat16_ru(lmin)) * 0x10001u;
@@ -902,7 +878,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
     if (by_top && m > neg_inf()) into_sample(m);
   }
   // The power of two above the weight of l.
-  auto exponent = [&](float l) { return max(__float2int_rd(l * w.dc.ih * 1.44269504f), -4000) + 1; };
+  auto exponent = [&](float l) { return __float2int_rd(fmaxf(fminf(l * w.unit * w.dc.ih * 1.44269504f, 4000.0f), -4000.0f)) + 1; };
   // The CTA's, then the row's; the sum is in whole numbers, as the weights are.
   {
 #pragma unroll
@@ -952,11 +928,13 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
     return;
   }
 
-  w.m = m;
+  const bool near = fabsf(m * w.unit) < 1386.0f * (Tf * w.unit);
+  const bool known = near && T > 1e-30f && T < 1e30f;  // the first pass' sum is good
   {
-    const float top = m * w.dc.ih;
-    w.fast = fabsf(top) < 1386.0f && T < 1e30f;  // (T: so that T times anything here is a number)
-    w.shift = 44 - a.scale_bits + exponent(w.fast ? m : 0.0f);
+    w.shift = 44 - a.scale_bits + exponent(near ? m : 0.0f);
+    // (so far from m / T that no entry but m counts: a smaller unit does too, and keeps m unit a number)
+    if (fabsf(m) * w.unit > 0x1p100f) w.unit = __int_as_float((354 - (__float_as_int(m) >> 23 & 0xff)) << 23);
+    w.off = near ? 0.0f : -m * w.unit;
     if (tid == 0) s.w = w;
   }
   // The least logit that min_p keeps: m + T ln(min_p), rounded up.
@@ -978,24 +956,34 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
   bool cut = false;  // s.cut_key and s.cut_id say what is kept of the entries set aside
   float lo = floor_l, hi = just_below(floor_l);
 
-  if (!K && !by_p) {
-    sum = r.pass(lo, hi, false, !by_m, 0.0f, 0.0f, sure);
-  } else {
+  const bool weigh_all = summed && !known;  // a pass of its own for the mass of all entries
+  if ((!K && !by_p) || weigh_all) sum = r.pass(lo, hi, false, weigh_all || !by_m, 0.0f, 0.0f, sure);
+  if (K || by_p) {
     bool found = false;
     float raised = FLT_MAX;  // the cut is known to lie above this logit, and few entries do
     const u64 w_max = r.weigh(m);
     u64 mass_all = 0;  // of the row
     float mass_f = 0.0f;  // the same, relative to the maximum's
-    if (summed && w.fast) {
-      for (int i = 0; i < a.nc; ++i) mass_all += s.cta_sum[i] >> min(exponent(m) - exponent(s.cta_max[i]), 63);
+    if (summed) {
+      if (weigh_all) {
+        unsigned z = 0;
+        mass_all = sum;
+        r.sum(mass_all, z);
+      } else {
+        for (int i = 0; i < a.nc; ++i) mass_all += s.cta_sum[i] >> min(exponent(m) - exponent(s.cta_max[i]), 63);
+      }
       mass_f = __fdiv_rn(__ull2float_rn(mass_all), __ull2float_rn(w_max));
     }
-    const int top_bin = __float2int_rd(fminf(fmaxf(m * unit, -0x1p30f), 0x1p30f));
-    if (K != 1 && w.fast) {
+    const int top_bin = __float2int_rd(m * unit);
+    // Edge e of the sample's bins is the value (top_bin - e + 1) / unit, or, where such values are too many for floats
+    // (T is small beside m), about the maximum less (e - 1) / unit.
+    const bool steep = !(fabsf(m * unit) < 0x1p22f);
+    auto edge_at = [&](int e) { return steep ? m - (float)(e - 1) / unit : (float)(top_bin - e + 1) / unit; };
+    if (K != 1) {
       unsigned n_sampled = 0;
       for (int i = 0; i < a.nc; ++i) n_sampled += s.cta_sampled[i];
       // Two bins a thread, the deepest first: the sample's mass below, its variance, and the count above.
-      const int b = kSampleBins - 2 - 2 * tid, at0 = (top_bin - b) & (kValueBins - 1), at1 = (top_bin - b - 1) & (kValueBins - 1);
+      const int b = kSampleBins - 2 - 2 * tid, at0 = (int)((unsigned)top_bin - b) & (kValueBins - 1), at1 = (at0 - 1) & (kValueBins - 1);
       unsigned c0 = 0, c1 = 0;
 #pragma unroll
       for (int i = 0; i < kMaxCluster; ++i)
@@ -1004,7 +992,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
           c1 += dsmem_ld_u32(r.remote(&s.sample[at1], i));
         }
       // (a bin's middle is b + part - 1/2 sixteenths below the maximum, part = m unit - top_bin)
-      const float mid = (float)b + (m * unit - (float)top_bin) - 0.5f;
+      const float mid = (float)b + (steep ? 0.5f : m * unit - (float)top_bin) - 0.5f;
       const float w0 = ex2_fast(-0.0625f * mid), w1 = ex2_fast(-0.0625f * (mid + 1.0f));
       const float m0 = (float)c0 * w0, m1 = (float)c1 * w1, v0 = m0 * w0, v1 = m1 * w1;
       unsigned cc = scan_up(c0 + c1, lane);
@@ -1054,7 +1042,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
       __syncthreads();
     }
 #pragma unroll 1
-    for (int attempt = 0; attempt < 3 && !found && w.fast; ++attempt) {
+    for (int attempt = 0; attempt < 3 && !found; ++attempt) {
       if (K == 1) {
         lo = m;
         hi = FLT_MAX;
@@ -1062,10 +1050,9 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
         lo = raised;
         hi = FLT_MAX;
       } else {
-        // Edge e is the value (top_bin - e + 1) / unit.
         const int wider = 24 * attempt * attempt, up = s.edge[0] - wider, down = s.edge[1] + wider;
-        hi = up > 0 ? (float)(top_bin - up + 1) / unit : FLT_MAX;
-        lo = down + 1 >= kSampleBins ? -FLT_MAX : fmaxf((float)(top_bin - down) / unit, -FLT_MAX);
+        hi = up > 0 ? edge_at(up) : FLT_MAX;
+        lo = down + 1 >= kSampleBins ? -FLT_MAX : fmaxf(edge_at(down + 1), -FLT_MAX);
       }
       const bool floored = !(K && by_p) && floor_l >= lo;  // min_p cuts above the window's end
       if (floored) {
@@ -1118,8 +1105,9 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
       ic += above_c - (hc0 + hc1);
       const unsigned all_c = above_c + aside;
       int turn = 0;
-      bool exact = K != 0;  // the total mass is known exactly
-      u64 total = mass_all, slack = (mass_all >> 22) + (mass_all >> 23) + (unsigned)a.V;  // (a unit a weight, for their rounding)
+      bool exact = K || weigh_all;  // the total mass is known exactly
+      u64 total = mass_all;
+      u64 slack = exact ? 0 : (mass_all >> 22) + (mass_all >> 23) + (unsigned)a.V;  // (a unit a weight, for their rounding)
 #pragma unroll 1
       for (int round = K ? 0 : 1; round < 2; ++round) {
         u64 want = K, want_lo = K;

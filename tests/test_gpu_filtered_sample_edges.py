@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import speculative_sampling_verification_gb300 as sv
-from tests.test_gpu_filtered_sample import DEV, DTYPES, check, run
+from tests.test_gpu_filtered_sample import DEV, DTYPES, check, run, settings
 
 pytestmark = pytest.mark.gpu
 
@@ -111,3 +111,73 @@ def test_min_p_at_high_temperatures(dtype, T, min_p):
     u = torch.tensor(u, dtype=torch.float32, device=DEV)
     sv.filtered_sample(x.expand(N, V).to(dtype).to(DEV), u, T, min_p=min_p, **s)
     assert s["out"].tolist() == want and int(s["status"]) == 0
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("kind", ["none", "k", "p", "m", "kp", "pm", "all"])
+@pytest.mark.parametrize("T", [1e-45, 1e-38, 1e-31, 1e-12, 1e-6, 1e-4, 0.003, 0.01])
+def test_low_temperatures(dtype, kind, T):
+    """Largest logits of up to 1e46 temperatures; a few entries lie so near the largest that they count."""
+    N, V = 10, 20011
+    rng = np.random.default_rng(len(kind) + int(-np.log10(T)))
+    x = 3.0 * torch.randn(N, V, generator=torch.Generator().manual_seed(len(kind)))
+    top = x.amax(1, keepdim=True)
+    near = torch.rand(N, V, generator=torch.Generator().manual_seed(1)) < 0.002
+    x = torch.where(near, top - torch.rand(N, V, generator=torch.Generator().manual_seed(2)) * 4.0 * T, x)
+    _, k, p, m = settings(N, kind, rng, V)
+    # (bf16, and fp32 where T is below its steps: rows of equal logits, with borders at round numbers of them)
+    check(x.to(dtype).to(DEV), rng.random(N).astype(np.float32), np.full(N, T, np.float32), k, p, m, most_near=5)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("kind", ["none", "k", "p", "m", "kp", "pm", "all"])
+@pytest.mark.parametrize("offset,T", [(1386.0, 1.0), (-1387.0, 1.0), (3000.0, 2.0), (-20000.0, 0.7), (1e5, 1.0), (3e6, 1.0)])
+def test_large_offsets(dtype, kind, offset, T):
+    """All logits far from zero: the weights are of the differences from the largest. (1386 temperatures is where the
+    kernel begins to subtract it.)"""
+    N, V = 10, 20011
+    rng = np.random.default_rng(len(kind) + int(abs(offset)))
+    x = 3.0 * torch.randn(N, V, generator=torch.Generator().manual_seed(len(kind))) + offset
+    _, k, p, m = settings(N, kind, rng, V)
+    check(x.to(dtype).to(DEV), rng.random(N).astype(np.float32), np.full(N, T, np.float32), k, p, m, most_near=5)
+
+
+@pytest.mark.parametrize("kind", ["none", "k", "p", "m", "kp", "pm", "all"])
+@pytest.mark.parametrize("scale", [1e-36, 1e-30, 1e-20, 1e20, 1e30, 1e36, 3e37])
+def test_logits_and_temperatures_of_any_size(kind, scale):
+    """Logits and temperature scaled alike leave the distribution as it is, up to fp32's ends."""
+    N, V = 10, 20011
+    rng = np.random.default_rng(len(kind) + int(abs(np.log10(scale))))
+    x = (2.0 * torch.randn(N, V, generator=torch.Generator().manual_seed(len(kind))).double() * scale).float()
+    x = x.clamp(-3e38, 3e38)
+    _, k, p, m = settings(N, kind, rng, V)
+    T = (rng.choice([0.7, 1.0, 2.5], N) * scale).astype(np.float32)
+    check(x.to(DEV), rng.random(N).astype(np.float32), T, k, p, m, most_near=5)
+
+
+def shortest(call, times=30):
+    best = []
+    for i in range(times + 3):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        call()
+        b.record()
+        b.synchronize()
+        best.append(a.elapsed_time(b))
+    return min(best[3:])
+
+
+@pytest.mark.parametrize("kw", [dict(top_k=50), dict(top_p=0.9), dict(top_k=50, top_p=0.9)])
+@pytest.mark.parametrize("row", ["cold", "offset"])
+def test_cold_and_offset_rows_take_no_search_by_bits(kw, row):
+    """Rows far from zero in units of their temperature find their cut in a window of values as others do: a search bit by
+    bit is 33 passes over a row, and four times an ordinary call and more."""
+    g = torch.Generator(device=DEV).manual_seed(1)
+    x = 3.0 * torch.randn(64, 128256, generator=g, device=DEV)
+    u = torch.rand(64, generator=g, device=DEV)
+    far, T = (x, 0.005) if row == "cold" else (x + 2000.0, 1.0)
+    usual = shortest(lambda: sv.filtered_sample(x, u, 1.0, **kw))
+    assert shortest(lambda: sv.filtered_sample(far, u, T, **kw)) < 3.0 * usual
+    if row == "offset":
+        usual = shortest(lambda: sv.filtered_sample(x, u, 0.0))
+        assert shortest(lambda: sv.filtered_sample(far, u, 0.0)) < 3.0 * usual
