@@ -131,7 +131,7 @@ struct Shared {
   unsigned cut_key;
   int cut_id, cut_found;
   u64 cut_mass;
-  float log_hi, log_lo;  // T ln(min_p), times log_unit
+  float log_hi, log_lo;  // T ln(min_p), times the weights' unit
   Weigh w;
 };
 
@@ -140,6 +140,10 @@ SV_DEVINL unsigned ordered(float f) {
   return b ^ ((unsigned)((int)b >> 31) | 0x80000000u);
 }
 SV_DEVINL float unordered(unsigned k) { return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k); }
+// The next value above x.
+SV_DEVINL float just_above(float x) {
+  return x == 0.0f ? __uint_as_float(1u) : __uint_as_float(__float_as_uint(x) + (x > 0.0f ? 1u : 0xffffffffu));
+}
 // The largest value that compares below x: for -FLT_MAX -inf, and for zeros (of either sign) the first below both.
 SV_DEVINL float just_below(float x) { return unordered(min(ordered(x) - 1u, x == 0.0f ? 0x7ffffffeu : 0xffffffffu)); }
 
@@ -751,10 +755,8 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
     c_lo = fmaxf(((c.hi - c_hi) + c.lo) * w.unit, 1e-37f);
     c_hi = fminf(c_hi * w.unit, 0x1p120f);
   }
-  const bool hot = T > 0x1p100f;  // (T ln(min_p) can be 103 times fp32's largest: a 256th of it, then)
-  const float log_unit = hot ? 0x1p-8f : 1.0f;
   if (by_m && warp == kWarps - 1) {  // one warp, since it is fp64
-    const double x = (double)T * log((double)min_p) * log_unit;
+    const double x = (double)(Tf * w.unit) * log((double)min_p);
     if (lane == 0) {
       s.log_hi = (float)x;
       s.log_lo = (float)(x - (double)(float)x);
@@ -930,22 +932,28 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
 
   const bool near = fabsf(m * w.unit) < 1386.0f * (Tf * w.unit);
   const bool known = near && T > 1e-30f && T < 1e30f;  // the first pass' sum is good
+  // The least logit that min_p keeps: m + T ln(min_p), rounded up; in the weights' unit, since T ln(min_p) may be no fp32
+  // number, or a subnormal one.
+  float floor_l = -FLT_MAX;
+  if (by_m) {
+    const float mu = m * w.unit;
+    if (fabsf(mu) > 0x1p100f) {
+      floor_l = m;  // (every other value is further below than any min_p reaches)
+    } else {
+      const ff x = two_sum(mu, s.log_hi);
+      const ff y = fast_two_sum(x.hi, x.lo + s.log_lo);
+      const float least = y.lo > 0.0f ? just_above(y.hi) : y.hi;
+      floor_l = __fdiv_rn(least, w.unit);
+      if (floor_l * w.unit < least) floor_l = just_above(floor_l);  // (a subnormal that was rounded down)
+      floor_l = fmaxf(fminf(floor_l, m), -FLT_MAX);
+    }
+  }
   {
     w.shift = 44 - a.scale_bits + exponent(near ? m : 0.0f);
     // (so far from m / T that no entry but m counts: a smaller unit does too, and keeps m unit a number)
     if (fabsf(m) * w.unit > 0x1p100f) w.unit = __int_as_float((354 - (__float_as_int(m) >> 23 & 0xff)) << 23);
     w.off = near ? 0.0f : -m * w.unit;
     if (tid == 0) s.w = w;
-  }
-  // The least logit that min_p keeps: m + T ln(min_p), rounded up.
-  float floor_l = -FLT_MAX;
-  if (by_m) {
-    const ff x = two_sum(m * log_unit, s.log_hi);
-    const ff y = fast_two_sum(x.hi, x.lo + s.log_lo);
-    floor_l = y.hi;
-    if (y.lo > 0.0f) floor_l = __uint_as_float(__float_as_uint(y.hi) + (y.hi >= 0.0f ? 1 : -1));
-    if (y.hi == 0.0f && y.lo > 0.0f) floor_l = y.lo;
-    floor_l = fmaxf(fminf(hot ? floor_l * 0x1p8f : floor_l, m), -FLT_MAX);
   }
   const u64 part = by_p ? fraction(top_p) : 0;
   // The least whole mass that is top_p of `total` or more.

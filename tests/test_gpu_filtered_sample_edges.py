@@ -143,7 +143,7 @@ def test_large_offsets(dtype, kind, offset, T):
 
 
 @pytest.mark.parametrize("kind", ["none", "k", "p", "m", "kp", "pm", "all"])
-@pytest.mark.parametrize("scale", [1e-36, 1e-30, 1e-20, 1e20, 1e30, 1e36, 3e37])
+@pytest.mark.parametrize("scale", [1e-42, 1e-36, 1e-30, 1e-20, 1e20, 1e30, 1e36, 3e37])
 def test_logits_and_temperatures_of_any_size(kind, scale):
     """Logits and temperature scaled alike leave the distribution as it is, up to fp32's ends."""
     N, V = 10, 20011
