@@ -39,7 +39,7 @@ namespace dec {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr float kNone = -1e38f;  // below any score
+constexpr float kNone = -FLT_MAX;  // no score is below (but for -inf)
 constexpr float kLazy = 8.0f;
 constexpr float kTiny = 1e-36f;   // products below count as 0 (the scale of a row of zeros is above)
 constexpr float kRaise = 128.0f;  // products go up to 2^8 of their reference: raised to 2^15, below fp16's largest

@@ -30,3 +30,28 @@ def test_a_workspace_for_a_batch_serves_smaller_ones(dtype, Hq, D):
         got = sv.sparse_attention(q[:n], cache, bounds, table, pos[:n], 48, seqs=seqs[:n], workspace=ws)
         want = sv.sparse_attention(q[:n], cache, bounds, table, pos[:n], 48, seqs=seqs[:n])
         assert torch.equal(got, want)
+
+
+def refill(cache, bounds, table, k, v):
+    """Other keys and values [n, H, D] for the one sequence of `table`."""
+    P, n = cache.page_size, len(k)
+    slots = table[0].long().repeat_interleave(P)[:n] * P + torch.arange(n, device=DEV) % P
+    sv.cache_write(k, v, slots, cache)
+    sv.page_bounds(cache, bounds, table, torch.zeros(1, dtype=torch.int32, device=DEV),
+                   torch.tensor([n], dtype=torch.int32, device=DEV))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, F8])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("budget", [40, 9])
+def test_scores_near_the_lowest_float(dtype, D, budget):
+    """Every score below -1e38: they are scores like others, and the largest of them have the weights."""
+    cache, bounds, table = make(1, 40, 1, 16, D, dtype, 22)
+    n = 40 * 16
+    g = torch.Generator(device=DEV).manual_seed(D)
+    k = torch.zeros(n, 1, D, device=DEV)
+    k[:, 0, 3] = torch.where(torch.rand(n, generator=g, device=DEV) < 0.5, -1.5e38, -2.2e38)
+    refill(cache, bounds, table, k, torch.randn(n, 1, D, generator=g, device=DEV))
+    q = torch.zeros(1, 4, D, device=DEV)
+    q[0, :, 3] = torch.tensor([1.0, 0.75, 1.0, 0.5], device=DEV)
+    check(cache, bounds, table, q.to(torch.bfloat16), [n - 1], [0], budget, 1, 1, scale=1.0)
