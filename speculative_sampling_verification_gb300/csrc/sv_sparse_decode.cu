@@ -163,9 +163,10 @@ __global__ void __launch_bounds__(kThreads, 4) sparse_decode_kernel(const __grid
     float top = fmaxf(bf16_lo(top2), bf16_hi(top2));
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    // A power of two at or below the largest (1 for rows of zeros, and for infinities, which stay).
-    const unsigned e = __float_as_uint(top) & 0x7f800000u;
-    const float unit = e == 0u || e == 0x7f800000u ? 1.0f : __uint_as_float(e), down = __fdiv_rn(1.0f, unit);
+    // A power of two at or below the largest (fp32's least normal one for subnormals, 2^7 of which are whole; 1 for
+    // infinities, which stay).
+    const unsigned e = max(__float_as_uint(top) & 0x7f800000u, 0x00800000u);
+    const float unit = e == 0x7f800000u ? 1.0f : __uint_as_float(e), down = __fdiv_rn(1.0f, unit);
 #pragma unroll
     for (int s = 0; s < STEPS; ++s)
 #pragma unroll

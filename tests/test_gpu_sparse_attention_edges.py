@@ -55,3 +55,17 @@ def test_scores_near_the_lowest_float(dtype, D, budget):
     q = torch.zeros(1, 4, D, device=DEV)
     q[0, :, 3] = torch.tensor([1.0, 0.75, 1.0, 0.5], device=DEV)
     check(cache, bounds, table, q.to(torch.bfloat16), [n - 1], [0], budget, 1, 1, scale=1.0)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, F8])
+@pytest.mark.parametrize("D", [64, 128])
+def test_subnormal_queries_against_keys_as_large(dtype, D):
+    """Queries of subnormal bf16 whose products with the keys are ordinary scores."""
+    cache, bounds, table = make(1, 12, 1, 16, D, dtype, 23)
+    n = 12 * 16
+    g = torch.Generator(device=DEV).manual_seed(D + 1)
+    k = (torch.randn(n, 1, D, generator=g, device=DEV) * 5e37).clamp(-2e38, 2e38)
+    refill(cache, bounds, table, k, torch.randn(n, 1, D, generator=g, device=DEV))
+    q = (torch.randn(1, 4, D, generator=g, device=DEV) * 4e-39).clamp(-1.1e-38, 1.1e-38).to(torch.bfloat16)
+    assert 0 < float(q.float().abs().max()) < 2.0 ** -126
+    check(cache, bounds, table, q, [n - 1], [0], 12, 1, 1, scale=1.0)
