@@ -114,6 +114,9 @@ SV_DEVINL unsigned dsmem_map(unsigned addr, unsigned rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
+SV_DEVINL void dsmem_st_u32(unsigned a, unsigned v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
 SV_DEVINL void dsmem_st_u64(unsigned a, unsigned long long v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
 }
@@ -134,6 +137,25 @@ SV_DEVINL uint32_t bf16x2_max(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
+}
+
+// The same, and of two floats, where a NaN operand yields NaN.
+SV_DEVINL uint32_t bf16x2_max_nan(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+SV_DEVINL float fmax_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+// Floats as unsigned numbers of the same order (-0 as +0).
+SV_DEVINL unsigned ordered(float f) {
+  const unsigned b = __float_as_uint(f + 0.0f);
+  return b ^ ((unsigned)((int)b >> 31) | 0x80000000u);
 }
 
 // Hardware 2^x (MUFU), flushes subnormal results to zero; 2^-inf = 0.

@@ -135,10 +135,6 @@ struct Shared {
   Weigh w;
 };
 
-SV_DEVINL unsigned ordered(float f) {
-  const unsigned b = __float_as_uint(f + 0.0f);  // -0 is 0
-  return b ^ ((unsigned)((int)b >> 31) | 0x80000000u);
-}
 SV_DEVINL float unordered(unsigned k) { return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k); }
 // The next value above x.
 SV_DEVINL float just_above(float x) {
@@ -206,16 +202,6 @@ SV_DEVINL float element(const uint32_t (&w)[F32 ? 8 : 4], int e) {
   return e & 1 ? bf16_hi(w[e / 2]) : bf16_lo(w[e / 2]);
 }
 
-SV_DEVINL uint32_t max2_nan(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-SV_DEVINL float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
 SV_DEVINL unsigned dsmem_ld_u32(unsigned a) {
   unsigned v;
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
@@ -225,9 +211,6 @@ SV_DEVINL u64 dsmem_ld_u64(unsigned a) {
   u64 v;
   asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
   return v;
-}
-SV_DEVINL void dsmem_st_u32(unsigned a, unsigned v) {
-  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
 }
 SV_DEVINL unsigned dsmem_add_u32(unsigned a, unsigned v) {
   unsigned r;
@@ -820,12 +803,12 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
       if constexpr (F32) {
         top = __uint_as_float(x[0]);
 #pragma unroll
-        for (int i = 1; i < 8; ++i) top = max_nan(top, __uint_as_float(x[i]));
+        for (int i = 1; i < 8; ++i) top = fmax_nan(top, __uint_as_float(x[i]));
       } else {
-        const uint32_t t2 = max2_nan(max2_nan(x[0], x[1]), max2_nan(x[2], x[3]));
-        top = max_nan(bf16_lo(t2), bf16_hi(t2));
+        const uint32_t t2 = bf16x2_max_nan(bf16x2_max_nan(x[0], x[1]), bf16x2_max_nan(x[2], x[3]));
+        top = fmax_nan(bf16_lo(t2), bf16_hi(t2));
       }
-      m = max_nan(m, top);
+      m = fmax_nan(m, top);
       if (summed) {
         if (top > ref) {
           const float to = rintf(top * c_hi), down = __int_as_float(max(127 + __float2int_rn(far - to), 0) << 23);
@@ -871,12 +854,12 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
     r.template all_tiles<F32 ? 4 : 8>([&](int, const uint32_t (&x)[WORDS]) {
       if constexpr (F32) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m = max_nan(m, __uint_as_float(x[i]));
+        for (int i = 0; i < 8; ++i) m = fmax_nan(m, __uint_as_float(x[i]));
       } else {
-        m2 = max2_nan(m2, max2_nan(max2_nan(x[0], x[1]), max2_nan(x[2], x[3])));
+        m2 = bf16x2_max_nan(m2, bf16x2_max_nan(bf16x2_max_nan(x[0], x[1]), bf16x2_max_nan(x[2], x[3])));
       }
     });
-    if constexpr (!F32) m = max_nan(bf16_lo(m2), bf16_hi(m2));
+    if constexpr (!F32) m = fmax_nan(bf16_lo(m2), bf16_hi(m2));
     if (by_top && m > neg_inf()) into_sample(m);
   }
   // The power of two above the weight of l.
@@ -884,11 +867,11 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
   // The CTA's, then the row's; the sum is in whole numbers, as the weights are.
   {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int o = 16; o > 0; o >>= 1) m = fmax_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
     if (lane == 0) s.wmax[warp] = m;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) m = max_nan(m, s.wmax[i]);
+    for (int i = 0; i < kWarps; ++i) m = fmax_nan(m, s.wmax[i]);
     const int e = __float2int_rn(far) - exponent(m) + a.scale_bits;
     u64 sum = summed ? whole(run.hi, e) : 0;
     sum += run.lo < 0.0f ? 0 - whole(-run.lo, e) : whole(run.lo, e);
@@ -911,7 +894,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
     }
     r.sync();
     m = s.cta_max[0];
-    for (int i = 1; i < a.nc; ++i) m = max_nan(m, s.cta_max[i]);
+    for (int i = 1; i < a.nc; ++i) m = fmax_nan(m, s.cta_max[i]);
   }
 
   unsigned fault = 0;
@@ -1359,8 +1342,6 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
 
 namespace {
 
-bool misaligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
-
 template <bool F32, bool VEC, bool SHORT>
 int launch(const sv::fs::Args& a, cudaStream_t st) {
   static std::mutex mu;
@@ -1391,6 +1372,8 @@ int launch(const sv::fs::Args& a, cudaStream_t st) {
 }
 
 }  // namespace
+
+using sv::misaligned;
 
 extern "C" int spec_filtered_sample(const void* logits, int64_t row_stride, const float* uniforms, int N, int V,
                                     int dtype, const float* temperatures, float temperature, const int32_t* top_ks,

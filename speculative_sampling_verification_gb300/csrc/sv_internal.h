@@ -55,6 +55,7 @@ struct Layout {
 };
 
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+inline bool misaligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
 
 // Pure host computation of the workspace layout for B sequences of
 // `rows_per_seq` rows of V elements; false for invalid sizes.

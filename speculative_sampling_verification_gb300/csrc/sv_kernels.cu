@@ -1607,18 +1607,6 @@ __global__ void __launch_bounds__(kThreads, 4) fused_kernel(Params P) {
 // A pair (v, i) holds the value and the first index of the maximum; v is NaN
 // when a NaN or +inf entry was seen (the sequence fails, U12).
 
-SV_DEVINL uint32_t bf16x2_max_nan(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-
-SV_DEVINL float fmax_nan(float a, float b) {
-  float d;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-  return d;
-}
-
 // Warp-wide (max, first index of the max) of one pair per lane; NaN wins.
 SV_DEVINL void warp_argmax(float& v, long long& i) {
 #pragma unroll

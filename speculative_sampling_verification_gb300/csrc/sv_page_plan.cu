@@ -323,12 +323,11 @@ __global__ void __launch_bounds__(kThreads) fill_kernel(const __grid_constant__ 
   fill(a, blockIdx.x, gridDim.x);
 }
 
-bool misaligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
-
 }  // namespace plan
 }  // namespace sv
 
 using namespace sv::plan;
+using sv::misaligned;
 
 extern "C" {
 

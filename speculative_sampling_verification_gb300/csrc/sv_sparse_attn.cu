@@ -54,11 +54,6 @@ SV_DEVINL float min_nan(float a, float b) {
   asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
-SV_DEVINL float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
 // Of three values in one instruction.
 SV_DEVINL float min3_nan(float a, float b, float c) {
   float r;
@@ -73,11 +68,6 @@ SV_DEVINL float max3_nan(float a, float b, float c) {
 SV_DEVINL uint32_t min2_nan(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-SV_DEVINL uint32_t max2_nan(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
 
@@ -189,7 +179,7 @@ __global__ void __launch_bounds__(kBoundThreads) page_bounds_kernel(const __grid
 #pragma unroll
             for (int q = 0; q < BYTES / 4; ++q) {
               l2[q] = min2_nan(min2_nan(l2[q], x[u].w[q]), x[u + 1].w[q]);
-              h2[q] = max2_nan(max2_nan(h2[q], x[u].w[q]), x[u + 1].w[q]);
+              h2[q] = bf16x2_max_nan(bf16x2_max_nan(h2[q], x[u].w[q]), x[u + 1].w[q]);
             }
           }
         }
@@ -207,12 +197,12 @@ __global__ void __launch_bounds__(kBoundThreads) page_bounds_kernel(const __grid
       for (int i = 0; i < N; ++i) {
         for (int k = 1; k < per; ++k) {
           const float y = __shfl_sync(0xffffffffu, lo[i], col + k * lanes), z = __shfl_sync(0xffffffffu, hi[i], col + k * lanes);
-          if (g == 0) lo[i] = min_nan(lo[i], y), hi[i] = max_nan(hi[i], z);
+          if (g == 0) lo[i] = min_nan(lo[i], y), hi[i] = fmax_nan(hi[i], z);
         }
-        if (g == 0) amax = max_nan(amax, max_nan(fabsf(lo[i]), fabsf(hi[i])));  // |NaN| is NaN
+        if (g == 0) amax = fmax_nan(amax, fmax_nan(fabsf(lo[i]), fabsf(hi[i])));  // |NaN| is NaN
       }
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      for (int o = 16; o > 0; o >>= 1) amax = fmax_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
       const bool fine = amax <= FLT_MAX;
       const float top = fmaxf(amax, kAmaxMin), up = __fdiv_rn(kCodeMax, top);
       if (g == 0) {
@@ -253,10 +243,10 @@ __global__ void __launch_bounds__(kBoundThreads) page_bounds_kernel(const __grid
               y = __bfloat162float(static_cast<const __nv_bfloat16*>(a.kc)[e]);
             }
             lo = min_nan(lo, y);
-            hi = max_nan(hi, y);
+            hi = fmax_nan(hi, y);
           }
           if (turn == 0) {
-            amax = max_nan(amax, max_nan(fabsf(lo), fabsf(hi)));
+            amax = fmax_nan(amax, fmax_nan(fabsf(lo), fabsf(hi)));
           } else {
             a.codes[at + d] = bound_code(floorf(__fmul_rn(lo, up)), fine);
             a.codes[at + a.D + d] = bound_code(ceilf(__fmul_rn(hi, up)), fine);
@@ -264,7 +254,7 @@ __global__ void __launch_bounds__(kBoundThreads) page_bounds_kernel(const __grid
         }
         if (turn == 0) {
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+          for (int o = 16; o > 0; o >>= 1) amax = fmax_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
         } else if (lane == 0) {
           a.scale[(long long)id * a.Hkv + hk] = fine ? __fdiv_rn(top, kCodeMax) : INFINITY;
         }
@@ -308,14 +298,7 @@ struct SelArgs {
   int N, B, Hq, Hkv, D, P, max_pages, budget, sink, recent, nc, ids_cap;
 };
 
-SV_DEVINL unsigned ordered(float f) {
-  const unsigned b = __float_as_uint(f + 0.0f);  // -0 is 0
-  return b ^ ((unsigned)((int)b >> 31) | 0x80000000u);
-}
 
-SV_DEVINL void dsmem_st_u32(unsigned a, unsigned v) {
-  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
-}
 
 SV_DEVINL void dsmem_min_u32(unsigned a, unsigned v) {
   asm volatile("red.shared::cluster.min.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
@@ -697,8 +680,6 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : 4) select_kernel(
 
 // ---------------------------------------------------------------- host side
 
-bool misaligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
-
 struct Layout {
   size_t off_table, off_ctx, off_parent, off_counters, off_ml, off_o, total;
   int splits;
@@ -806,6 +787,7 @@ int launch_select_any(SelArgs& a, cudaStream_t st) {
 }  // namespace sv
 
 using namespace sv::sparse;
+using sv::misaligned;
 
 extern "C" {
 
