@@ -33,8 +33,10 @@ typedef unsigned long long u64;
 // The CTAs wait for one another once after each of these steps, and once for the cut's bin. All decisions are made on
 // whole-number masses (2^-44 of the largest weight), where sums do not depend on their order. Where the fp32
 // sum could change the cut, the mass below the window is summed again, exactly. A window that misses the cut
-// is widened, or begins above its old top where the cut turns out to lie there; a row that still has none, or more
-// entries in its window than there is room for (ties), is halved bit by bit over the keys, a pass for every bit.
+// is widened, or begins above its old top where the cut turns out to lie there; one with more entries than there is room for
+// (flat rows) is followed by one of three of its bins. A row that still has none, whose cut lies among more
+// than a thousand equal entries, or whose top_k is larger than that room and followed by top_p, is halved bit by bit over
+// the keys, a pass for every bit.
 //
 // Few rows are bound by the steps between the passes, each a chain of shared memory, barriers and code fetched for the
 // first time (1 x 32000 with top-k: 21 us, of them 8 for the passes); many rows by issue slots. 512 x 128256
@@ -468,8 +470,8 @@ struct Row {
   }
 
   // The entries l >= lo of this CTA's share (`all`: every entry): those above hi (and, with a cut, those that it keeps)
-  // are summed into records, the others set aside as far as there is room. Returns a thread's part of the sum.
-  // An entry set aside is counted into bin (top - l) per.
+  // are summed into records, the others set aside as far as there is room, and all of those counted into bin
+  // (top - l) per. Returns a thread's part of the sum.
   SV_DEVINL u64 pass(float lo, float hi, bool cut, bool all, float top, float per, unsigned& count) {
     const int ln = lane(), wp = warp();
     Word* list = reinterpret_cast<Word*>(s.list[wp]);
@@ -518,8 +520,8 @@ struct Row {
           unsigned at = 0;
           if (ln == 0) at = atomicAdd(&s.n_aside, (unsigned)__popc(b));
           at = __shfl_sync(0xffffffffu, at, 0) + __popc(b & ((1u << ln) - 1));
-          if (put && at < kAside) {
-            aside[at] = e;
+          if (put) {
+            if (at < kAside) aside[at] = e;
             const int bin = bin_of(l, top, per);
             add64(&s.hlo[bin], &s.hhi[bin], x);
             atomicAdd(&s.hcnt[bin], 1u);
@@ -951,7 +953,8 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
   if ((!K && !by_p) || weigh_all) sum = r.pass(lo, hi, false, weigh_all || !by_m, 0.0f, 0.0f, sure);
   if (K || by_p) {
     bool found = false;
-    float raised = FLT_MAX;  // the cut is known to lie above this logit, and few entries do
+    bool given = false;  // the last attempt says where the cut lies: above next_lo, and not above next_hi
+    float next_lo = 0.0f, next_hi = 0.0f;
     const u64 w_max = r.weigh(m);
     u64 mass_all = 0;  // of the row
     float mass_f = 0.0f;  // the same, relative to the maximum's
@@ -1033,13 +1036,13 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
       __syncthreads();
     }
 #pragma unroll 1
-    for (int attempt = 0; attempt < 3 && !found; ++attempt) {
+    for (int attempt = 0; attempt < 4 && !found; ++attempt) {
       if (K == 1) {
         lo = m;
         hi = FLT_MAX;
-      } else if (raised < FLT_MAX) {
-        lo = raised;
-        hi = FLT_MAX;
+      } else if (given) {
+        lo = next_lo;
+        hi = next_hi;
       } else {
         const int wider = 24 * attempt * attempt, up = s.edge[0] - wider, down = s.edge[1] + wider;
         hi = up > 0 ? edge_at(up) : FLT_MAX;
@@ -1058,15 +1061,16 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
         __syncthreads();
       }
       const float top_l = hi == FLT_MAX ? m : hi;
-      const float width = raised < FLT_MAX ? top_l - lo : fminf(top_l - lo, (float)kSampleBins / unit);
+      const float width = given ? top_l - lo : fminf(top_l - lo, (float)kSampleBins / unit);
       const float per = width > 0.0f ? (float)kBins / width : 0.0f;
       sum = r.pass(lo, hi, false, false, top_l, per, sure);
       __syncthreads();
       u64 above = sum;
       unsigned above_c = sure, aside = tid == 0 ? s.n_aside : 0u;
-      if (tid == 0 && s.n_aside > r.kAside) aside = 1u << 24;  // no room
       r.sum(above, above_c, aside);
-      if (aside >= 1u << 24) break;
+      bool over = false;  // a CTA had no room for all of its window's entries
+      for (int i = 0; i < a.nc; ++i) over |= s.inbox_d[~r.turn & 1][i] > r.kAside;
+      if (over && (K == 1 || (K && by_p))) break;  // (ties; two cuts, which a narrow window need not both hold)
       const int here = (int)s.n_aside;
       // Masses and counts of the window's bins over all CTAs, two a thread, and what lies above the thread's.
       u64 hm0 = 0, hm1 = 0;
@@ -1105,7 +1109,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
         bool better = false;  // the mass below the window decides, and could be known better
         if (round == 0) {
           if (above_c >= K) {  // the window lies too deep
-            if (above_c <= r.kAside) raised = hi;
+            if (above_c <= r.kAside) given = true, next_lo = hi, next_hi = FLT_MAX;
             break;
           }
           if (all_c < K) {
@@ -1125,7 +1129,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
             better = !exact && ((in_sure && above < want) || (floored && short_of && all_m >= want_lo));
             if (!better) {
               found = !in_sure && floored;  // min_p cuts first: all entries of the window are kept
-              if (in_sure && above_c <= r.kAside) raised = hi;
+              if (in_sure && above_c <= r.kAside) given = true, next_lo = hi, next_hi = FLT_MAX;
               break;
             }
           }
@@ -1149,6 +1153,12 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
           __syncthreads();
           const int bin = s.bin;
           if (bin < 0 || turn > 3) break;
+          if (over) {  // the bin and its neighbours are the next window
+            given = true;
+            next_hi = bin > 0 ? top_l - (float)(bin - 1) / per : hi;
+            next_lo = bin < kBins - 1 ? fmaxf(top_l - (float)(bin + 2) / per, lo) : lo;
+            break;
+          }
           for (int i = tid; i < here; i += kThreads) {
             const Word e = reinterpret_cast<const Word*>(s.aside)[i];
             const float l = E::value(e);
@@ -1165,7 +1175,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
           const int n_cand = (int)s.n_cand[turn];
           ++turn;
           if (n_cand > kCand) {
-            attempt = 3;  // too many ties
+            attempt = 4;  // too many ties
             break;
           }
           order_candidates(s, n_cand, round == 0, want_lo, want);
@@ -1192,6 +1202,12 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
         slack = 0;
         exact = true;
         --round;
+      }
+      if (found && over) {  // all of the window is kept: the next one is empty, above where it ends
+        found = false;
+        given = true;
+        next_lo = lo;
+        next_hi = just_below(lo);
       }
     }
     if (found) {

@@ -181,3 +181,36 @@ def test_cold_and_offset_rows_take_no_search_by_bits(kw, row):
     if row == "offset":
         usual = shortest(lambda: sv.filtered_sample(x, u, 0.0))
         assert shortest(lambda: sv.filtered_sample(far, u, 0.0)) < 3.0 * usual
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("N,V", [(200, 20011), (6, 150001), (310, 7001)])
+@pytest.mark.parametrize("kind", ["k", "p", "m", "kp", "pm"])
+@pytest.mark.parametrize("flat", [5.0, 50.0, 1e4, 1e9])
+def test_flat_rows(dtype, N, V, kind, flat):
+    """Rows whose weights hardly differ: more entries lie where the cut is expected than a block has room for. With `k` as
+    many entries kept as would fill it several times."""
+    rng = np.random.default_rng(V + len(kind))
+    x = 3.0 * torch.randn(N, V, generator=torch.Generator().manual_seed(N))
+    T, k, p, m = settings(N, kind, rng, V)
+    T[:] = flat
+    if "k" in kind:
+        k = np.where(np.arange(N) % 3 == 0, rng.integers(1, V, N), k).astype(np.int32)
+    if "m" in kind:  # (the floor inside of the row's spread)
+        m = np.exp(-rng.uniform(0.0, 30.0, N) / flat).astype(np.float32)
+    u = rng.random(N).astype(np.float32)
+    rows = slice(None) if N < 50 else slice(0, None, 9)
+    out, prob, status = run(x.to(dtype).to(DEV), u, T, k, p, m)
+    # (weights so near one another that fp32's min_p, 2^-24 off, is one of them)
+    check(x[rows].to(dtype), u[rows], T[rows], k[rows], p[rows], m[rows], got=(out[rows], prob[rows], status),
+          most_near=len(u[rows]) if flat > 1e3 else 3)
+
+
+@pytest.mark.parametrize("kw", [dict(top_p=0.9), dict(top_p=0.5, min_p=0.05), dict(top_k=30000)])
+@pytest.mark.parametrize("T", [10.0, 100.0])
+def test_flat_rows_take_no_search_by_bits(kw, T):
+    g = torch.Generator(device=DEV).manual_seed(2)
+    x = (3.0 * torch.randn(512, 50264, generator=g, device=DEV)).to(torch.bfloat16)
+    u = torch.rand(512, generator=g, device=DEV)
+    usual = shortest(lambda: sv.filtered_sample(x, u, 1.0, top_p=0.9))
+    assert shortest(lambda: sv.filtered_sample(x, u, T, **kw)) < 5.0 * usual
