@@ -647,10 +647,11 @@ size_t sv_sparse_attention_workspace_size(int N, int Hq, int Hkv, int D, int max
  * A row whose position or sequence is out of range, or one of whose pages lies outside the cache, gets NaN
  * outputs, no selected pages and SV_DEV_PAGE_RANGE; the others are unaffected.
  * With D 64 or 128, at most 8 query heads a key/value head, page_size a multiple of 16 and q and the cache on 16 bytes
- * (q's strides too), a kernel of its own attends the pages: a bf16 cache's weights are rounded to bf16
- * (2^-8 of each); over an e4m3 cache q is fp16 relative to its head's largest value (off by 2^-25 of that at most), and a
- * weight times its value's scale fp16 (off by 2^-11 of itself, or by 2^-32 of the row's largest). Other shapes,
- * and their precision, are sv_tree_attention's. Returns SV_OK once enqueued; N == 0 returns SV_OK at once. */
+ * (q's strides too), a kernel of its own attends the pages: a bf16 cache's weights are off by 2^-16 of
+ * each; over an e4m3 cache q is fp16 relative to its head's largest value (off by 2^-25 of that at most), and a
+ * weight times its value's scale is off by 2^-22 of itself, or by 2^-40 of the row's largest. Other shapes,
+ * and their precision, are sv_tree_attention's. Codes and scales are expected as sv_cache_write stores them. Returns
+ * SV_OK once enqueued; N == 0 returns SV_OK at once. */
 int sv_sparse_attention(const void* q, int64_t q_stride_n, int64_t q_stride_h, const void* k_cache,
                         const void* v_cache, const float* k_scale, const float* v_scale, int64_t num_pages,
                         int page_size, int cache_dtype, const int8_t* codes, const float* bound_scale,
