@@ -127,6 +127,9 @@ struct Shared {
   unsigned cta_sampled[kMaxCluster];
   unsigned n_aside, n_cand[4];
   int edge[2], bin;  // edges: the window's upper and lower one
+  // What the last attempt says of the cut: it lies at or above next_lo, and not above next_hi.
+  bool given;
+  float next_lo, next_hi;
   u64 bin_mass;
   unsigned bin_count;
   // The cut: entries of a larger key are kept, and those of this key up to `cut_id`; their mass.
@@ -793,6 +796,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
     s.n_aside = 0;
     s.cut_key = 0;
     s.cut_id = 0x7fffffff;
+    s.given = false;
   }
   __syncthreads();
   auto into_sample = [&](float l) {
@@ -953,8 +957,6 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
   if ((!K && !by_p) || weigh_all) sum = r.pass(lo, hi, false, weigh_all || !by_m, 0.0f, 0.0f, sure);
   if (K || by_p) {
     bool found = false;
-    bool given = false;  // the last attempt says where the cut lies: above next_lo, and not above next_hi
-    float next_lo = 0.0f, next_hi = 0.0f;
     const u64 w_max = r.weigh(m);
     u64 mass_all = 0;  // of the row
     float mass_f = 0.0f;  // the same, relative to the maximum's
@@ -1035,14 +1037,24 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
       if (a.nc > 1) cluster_wait();
       __syncthreads();
     }
+    auto next = [&](float from, float to) {
+      if (tid == 0) s.given = true, s.next_lo = from, s.next_hi = to;
+    };
 #pragma unroll 1
     for (int attempt = 0; attempt < 4 && !found; ++attempt) {
+      if (attempt > 0) {
+        r.sync();  // (what the last attempt left has been read)
+        for (int i = tid; i < kBins; i += kThreads) s.hlo[i] = s.hhi[i] = s.hcnt[i] = 0;
+        if (tid == 0) s.n_aside = 0;
+        if (tid < 4) s.n_cand[tid] = 0;
+        __syncthreads();
+      }
       if (K == 1) {
         lo = m;
         hi = FLT_MAX;
-      } else if (given) {
-        lo = next_lo;
-        hi = next_hi;
+      } else if (s.given) {
+        lo = s.next_lo;
+        hi = s.next_hi;
       } else {
         const int wider = 24 * attempt * attempt, up = s.edge[0] - wider, down = s.edge[1] + wider;
         hi = up > 0 ? edge_at(up) : FLT_MAX;
@@ -1053,15 +1065,8 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
         lo = floor_l;
         hi = fmaxf(hi, just_below(floor_l));
       }
-      if (attempt > 0) {
-        r.sync();  // (what the last attempt left has been read)
-        for (int i = tid; i < kBins; i += kThreads) s.hlo[i] = s.hhi[i] = s.hcnt[i] = 0;
-        if (tid == 0) s.n_aside = 0;
-        if (tid < 4) s.n_cand[tid] = 0;
-        __syncthreads();
-      }
       const float top_l = hi == FLT_MAX ? m : hi;
-      const float width = given ? top_l - lo : fminf(top_l - lo, (float)kSampleBins / unit);
+      const float width = s.given ? top_l - lo : fminf(top_l - lo, (float)kSampleBins / unit);
       const float per = width > 0.0f ? (float)kBins / width : 0.0f;
       sum = r.pass(lo, hi, false, false, top_l, per, sure);
       __syncthreads();
@@ -1109,7 +1114,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
         bool better = false;  // the mass below the window decides, and could be known better
         if (round == 0) {
           if (above_c >= K) {  // the window lies too deep
-            if (above_c <= r.kAside) given = true, next_lo = hi, next_hi = FLT_MAX;
+            if (above_c <= r.kAside) next(hi, FLT_MAX);
             break;
           }
           if (all_c < K) {
@@ -1129,7 +1134,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
             better = !exact && ((in_sure && above < want) || (floored && short_of && all_m >= want_lo));
             if (!better) {
               found = !in_sure && floored;  // min_p cuts first: all entries of the window are kept
-              if (in_sure && above_c <= r.kAside) given = true, next_lo = hi, next_hi = FLT_MAX;
+              if (in_sure && above_c <= r.kAside) next(hi, FLT_MAX);
               break;
             }
           }
@@ -1154,9 +1159,8 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
           const int bin = s.bin;
           if (bin < 0 || turn > 3) break;
           if (over) {  // the bin and its neighbours are the next window
-            given = true;
-            next_hi = bin > 0 ? top_l - (float)(bin - 1) / per : hi;
-            next_lo = bin < kBins - 1 ? fmaxf(top_l - (float)(bin + 2) / per, lo) : lo;
+            next(bin < kBins - 1 ? fmaxf(top_l - (float)(bin + 2) / per, lo) : lo,
+                 bin > 0 ? top_l - (float)(bin - 1) / per : hi);
             break;
           }
           for (int i = tid; i < here; i += kThreads) {
@@ -1205,9 +1209,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
       }
       if (found && over) {  // all of the window is kept: the next one is empty, above where it ends
         found = false;
-        given = true;
-        next_lo = lo;
-        next_hi = just_below(lo);
+        next(lo, just_below(lo));
       }
     }
     if (found) {
