@@ -29,12 +29,13 @@ namespace dec {
 // under way are what counts: 12 or more a SM, 8 KB each (codes: 4). A running maximum per head moves only when a score
 // exceeds it by more than 2^8, so that most blocks need one vote; a row's sum stays per lane until
 // the end. P enters as two values of 16 bits, with a product each, so that outputs are off by no more than their own
-// rounding (one value alone: error against 64 bits 0.0019 for bf16, 0.0016 with both; 32 rows take as long in bf16, 71 us
-// in place of 70 in e4m3). bf16 caches: 2^-16 of each weight. e4m3 caches: codes become fp16 (exact), q is
+// rounding (one value alone: error against 64 bits 0.0019 for bf16, 0.0016 with both; 32 rows take as long in bf16, 72 us
+// in place of 71 in e4m3). bf16 caches: 2^-16 of each weight. e4m3 caches: codes become fp16 (exact), q is
 // fp16 relative to its largest value (2^-25 of that at most), and a weight times its value's scale is two fp16
 // raised so that the largest is near fp16's largest (2^-22 of itself, or 2^-40 of the largest).
-// 32 rows of 32/8 heads of 128: 73 us alone for 393 MB of bf16 (5.4 TB/s, DRAM 68 % active), 50 us for 204 MB of e4m3
-// (4.1 TB/s; its conversions come between a warp's loads). On the kernel for trees of few rows, with 128-wide products of
+// 32 rows of 32/8 heads of 128: 72 us alone for 393 MB of bf16 (5.5 TB/s, DRAM 69 % active), 52 us for 204 MB of e4m3
+// (3.9 TB/s, DRAM 50 % active, issue slots 36 %: of a warp's time 41 % waits for its loads, which are not under way while it
+// converts, and 22 % for results of its own instructions). On the kernel for trees of few rows, with 128-wide products of
 // which 4 columns are used, a whole call took 97 (bf16) and 94 us (e4m3), where it was 91 and 78 with this one; 36 rows
 // of 64/8 heads 84 and 75, one row of 131072 keys 41 and 32.
 
