@@ -39,8 +39,8 @@ typedef unsigned long long u64;
 // the keys, a pass for every bit.
 //
 // Few rows are bound by the steps between the passes, each a chain of shared memory, barriers and code fetched for the
-// first time (1 x 32000 with top-k: 20 us, of them 8 for the passes). Many rows fill neither issue slots (57 % of them for the
-// nucleus rows, 80 % on the busiest SM) nor memory: a warp's time goes to results of its own instructions (21 %), loads (16 %),
+// first time (1 x 32000 with top-k: 20 us, of them 8 for the passes). Many rows fill neither issue slots (58 % of them for the
+// nucleus rows, 80 to 94 % on the busiest SM) nor memory: a warp's time goes to results of its own instructions (21 %), loads (16 %),
 // barriers (11 %) and fetching code (9 %). 512 x 128256 bf16 of normal logits (sigma 3, T = 1), 131 MB, 19 us at the copy
 // rate: min_p 0.1 66 us, greedy 76, top_k 50 98, no setting 132 (every entry weighed to 2^-44), top_p 0.9 197, and 626 at T =
 // 10, where the window is narrowed. A search bit by bit takes 33 passes: 64 x 128256 bf16 with top_k 60000 and top_p 1165.
