@@ -1158,6 +1158,8 @@ def _setting(name, value, off, N, dtype, device):
     if hasattr(value, "data_ptr"):
         _vector(name, value, (N,), dtype, device)
         return value.data_ptr(), off
+    if dtype is torch.int32:  # (a C int would take 2 ** 32 + 5 for 5)
+        value = max(-1, min(value, (1 << 31) - 1))
     return None, value
 
 
